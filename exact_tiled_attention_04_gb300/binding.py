@@ -27,6 +27,7 @@ FA_ERR_UNSUPPORTED = 2
 FA_ERR_ALIGNMENT = 3
 FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
+FA_ERR_CAPACITY = 6
 FA_DTYPE_F32 = 0
 FA_DTYPE_BF16 = 1
 FA_DTYPE_F16 = 2
@@ -34,6 +35,12 @@ FA_FLAG_CAUSAL = 0x100
 
 _lock = threading.Lock()
 _lib = None
+
+
+class fa_kv4_cache_t(ctypes.Structure):
+    """The C struct of include/fa.h (device addresses and sizes)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales", "weight", "pos", "counts")] \
+        + [(n, ctypes.c_int64) for n in ("B", "H_kv", "capacity", "d")]
 
 
 class FAError(RuntimeError):
@@ -112,6 +119,18 @@ def load(path: str | None = None):
         lib.fa_bwd_host.argtypes = bwd_args + [vp]
         lib.fa_bwd_host_workspace_size.restype = sz
         lib.fa_bwd_host_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64]
+        cp = ctypes.POINTER(fa_kv4_cache_t)
+        for name, args in (("fa_kv4_append", [cp, vp, vp, i64, c_int, vp]),
+                           ("fa_kv4_read", [cp, vp, i64, vp, vp, c_int]),
+                           ("fa_kv4_fwd", [cp, vp, vp, vp, vp, i64, i64, f32, c_int, vp, sz]),
+                           ("fa_kv4_evict", [cp, i64, i64, i64, vp, cp, vp, vp]),
+                           ("fa_fwd_weights", [vp] * 5 + [i64] * 8 + [f32, c_int])):
+            getattr(lib, name).restype = c_int
+            getattr(lib, name).argtypes = args + [vp]
+            getattr(lib, name + "_validate").restype = c_int
+            getattr(lib, name + "_validate").argtypes = args
+        lib.fa_kv4_fwd_workspace_size.restype = sz
+        lib.fa_kv4_fwd_workspace_size.argtypes = [i64] * 6 + [c_int]
         _lib = lib
         return lib
 
@@ -217,6 +236,64 @@ def fa_bwd_host(q: int, k: int, v: int, o: int, dout: int, lse: int, dq: int, dk
 
 def fa_bwd_host_workspace_size(B: int, H: int, H_kv: int, N_q: int, N_kv: int, d: int) -> int:
     return load().fa_bwd_host_workspace_size(B, H, H_kv, N_q, N_kv, d)
+
+
+def fa_kv4_append(cache, k: int, v: int, n: int, dtype: int, counts_out: int, stream: int | None) -> int:
+    """`cache` here and below: an fa_kv4_cache_t (None for a NULL pointer)."""
+    return load().fa_kv4_append(cache, k, v, n, dtype, counts_out, stream or None)
+
+
+def fa_kv4_append_validate(cache, k: int, v: int, n: int, dtype: int, counts_out: int) -> int:
+    return load().fa_kv4_append_validate(cache, k, v, n, dtype, counts_out)
+
+
+def fa_kv4_read(cache, first: int | None, count: int, k: int | None, v: int | None, dtype: int,
+                stream: int | None) -> int:
+    return load().fa_kv4_read(cache, first or None, count, k or None, v or None, dtype, stream or None)
+
+
+def fa_kv4_read_validate(cache, first: int | None, count: int, k: int | None, v: int | None, dtype: int) -> int:
+    return load().fa_kv4_read_validate(cache, first or None, count, k or None, v or None, dtype)
+
+
+def fa_kv4_fwd(cache, q: int, o: int, lse: int | None, weight_out: int | None, H: int, N_q: int, scale: float,
+               dtype: int, workspace: int, workspace_bytes: int, stream: int | None) -> int:
+    return load().fa_kv4_fwd(cache, q, o, lse or None, weight_out or None, H, N_q, scale, dtype, workspace,
+                             workspace_bytes, stream or None)
+
+
+def fa_kv4_fwd_validate(cache, q: int, o: int, lse: int | None, weight_out: int | None, H: int, N_q: int,
+                        scale: float, dtype: int, workspace: int, workspace_bytes: int) -> int:
+    return load().fa_kv4_fwd_validate(cache, q, o, lse or None, weight_out or None, H, N_q, scale, dtype, workspace,
+                                      workspace_bytes)
+
+
+def fa_kv4_fwd_workspace_size(B: int, H: int, H_kv: int, N_q: int, capacity: int, d: int, with_weight: int) -> int:
+    return int(load().fa_kv4_fwd_workspace_size(B, H, H_kv, N_q, capacity, d, with_weight))
+
+
+def fa_kv4_evict(cache, keep: int, sinks: int, recent: int, rank_by: int | None, to, src: int, counts_out: int,
+                 stream: int | None) -> int:
+    return load().fa_kv4_evict(cache, keep, sinks, recent, rank_by or None, to, src, counts_out, stream or None)
+
+
+def fa_kv4_evict_validate(cache, keep: int, sinks: int, recent: int, rank_by: int | None, to, src: int,
+                          counts_out: int) -> int:
+    return load().fa_kv4_evict_validate(cache, keep, sinks, recent, rank_by or None, to, src, counts_out)
+
+
+def fa_fwd_weights(q: int, k: int, lse: int, weight_in: int | None, weight_out: int, weight_stride: int, B: int,
+                   H: int, H_kv: int, N_q: int, N_kv: int, d: int, first_query: int, scale: float, dtype: int,
+                   stream: int | None) -> int:
+    return load().fa_fwd_weights(q, k, lse, weight_in or None, weight_out, weight_stride, B, H, H_kv, N_q, N_kv, d,
+                                 first_query, scale, dtype, stream or None)
+
+
+def fa_fwd_weights_validate(q: int, k: int, lse: int, weight_in: int | None, weight_out: int, weight_stride: int,
+                            B: int, H: int, H_kv: int, N_q: int, N_kv: int, d: int, first_query: int, scale: float,
+                            dtype: int) -> int:
+    return load().fa_fwd_weights_validate(q, k, lse, weight_in or None, weight_out, weight_stride, B, H, H_kv, N_q,
+                                          N_kv, d, first_query, scale, dtype)
 
 
 def fa_device_status(stream: int | None) -> int:

@@ -194,6 +194,7 @@ const char* fa_status_string(int status) {
         case FA_ERR_ALIGNMENT: return "tensor base address not 16-byte aligned";
         case FA_ERR_CUDA: return "CUDA call failed";
         case FA_ERR_TIMEOUT: return "kernel timed out waiting on an internal barrier";
+        case FA_ERR_CAPACITY: return "4-bit cache full: appended rows were dropped";
         default: return "unknown status";
     }
 }
@@ -684,7 +685,8 @@ int fa_device_status(void* stream) {
         return FA_ERR_CUDA;
     }
     std::snprintf(g_last_error, sizeof(g_last_error), "device error word 0x%08x", st.word);
-    return (st.word & fa::kDevErrTimeout) ? FA_ERR_TIMEOUT : FA_ERR_CUDA;
+    if (st.word & fa::kDevErrTimeout) return FA_ERR_TIMEOUT;
+    return (st.word & fa::kDevErrCapacity) ? FA_ERR_CAPACITY : FA_ERR_CUDA;
 }
 
 int fa_selftest_barrier_timeout(void* stream) {

@@ -1,0 +1,96 @@
+// Declarations shared by the host entry points of the 4-bit key/value cache
+// (fa_kv4_api.cu) and its kernels.  Not part of the public C ABI.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// A cache as the kernels see it (fa_kv4_cache_t in 32-bit sizes).
+struct Kv4Cache {
+    uint8_t* codes[2];   // keys, values: [B * H_kv, capacity, d / 2]
+    uint8_t* scales[2];  // [B * H_kv, capacity, d / 16]
+    float* weight;       // [B * H_kv, capacity] or nullptr
+    int32_t* pos;        // [B * H_kv, capacity] or nullptr
+    int32_t* counts;     // [2, B]: length, tokens appended
+    int B, H_kv, capacity, d;
+};
+
+struct Kv4AppendParams {
+    Kv4Cache c;
+    const void* x[2];     // k, v: [B * H_kv, n, d]
+    int32_t* counts_out;  // [2, B]
+    DevStatus* status;
+    long long n;
+    int f16;
+};
+cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t stream);
+
+struct Kv4ReadParams {
+    Kv4Cache c;
+    const int32_t* first;  // [B] or nullptr
+    void* x[2];            // k, v: [B * H_kv, count, d] or nullptr
+    long long count;
+    int f16;
+};
+cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t stream);
+
+struct Kv4EvictParams {
+    Kv4Cache from, to;    // to.codes[0] == from.codes[0]: in place
+    const float* rank_by;
+    int32_t* src;         // [B * H_kv, keep]
+    int32_t* counts_out;  // [2, B]
+    int keep, sinks;
+    int recent;
+};
+constexpr int kKv4EvictMaxCapacity = 393216;
+// sms: SM count of the current device
+cudaError_t launch_kv4_evict(const Kv4EvictParams& p, int sms, cudaStream_t stream);
+
+// Attention over the cache.  Rows: the R = N_q * group query rows of a
+// key/value head, row r = g * N_q + i (query head g of the group, query i),
+// in blocks of `rows_per_block`.  A unit is one (sequence, key/value head,
+// row block); its keys are cut into slabs of 32, and the slabs of all units,
+// in order, into runs of equal length, one per CTA.
+struct Kv4FwdParams {
+    Kv4Cache c;
+    const void* q;        // [B, H, N_q, d]
+    void* o;              // [B, H, N_q, d]
+    float* lse;           // [B, H, N_q] or nullptr
+    const float* weight_in;
+    float* weight_out;    // or nullptr
+    DevStatus* status;
+    unsigned int gen;
+    int Nq, group, rows, row_blocks;
+    int causal, f16;
+    float scale_log2;
+    int ctas;             // CTAs of the main kernel
+    // workspace
+    float* row_lse2;      // [B * H_kv * rows]: base-2 lse of the rows of units that one CTA finished
+    float* part_ml;       // [ctas, 2, rows_per_block, 4]
+    float* part_o;        // [ctas, 2, rows_per_block, d]
+    float* logits;        // [B * H_kv, capacity, rows] scaled, base 2, or nullptr
+};
+int kv4_rows_per_block(int64_t rows);
+int kv4_max_ctas(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms);
+cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, cudaStream_t stream);
+
+struct WeightsParams {
+    const float* lse;        // [B, H, N_q]
+    const float* weight_in;  // or nullptr
+    float* weight_out;
+    long long weight_stride;
+    DevStatus* status;
+    unsigned int gen;
+    int Nq, Nkv, H, H_kv, group, first_query;
+    int causal, causal_offset;
+    float scale_log2;
+    int splits;              // CTAs (one cluster) that share the query rows of a key block
+};
+cudaError_t launch_weights(int d, bool f16, const CUtensorMap& q, const CUtensorMap& k, const WeightsParams& p,
+                           unsigned int grid, cudaStream_t stream);
+
+}  // namespace fa

@@ -33,7 +33,8 @@ typedef enum {
     FA_ERR_UNSUPPORTED = 2,  /* head dimension / dtype combination not built, size beyond TMA limits */
     FA_ERR_ALIGNMENT = 3,    /* a tensor base address is not 16-byte aligned */
     FA_ERR_CUDA = 4,         /* a CUDA runtime or driver call failed (see fa_last_error_message) */
-    FA_ERR_TIMEOUT = 5       /* a kernel gave up waiting on an internal barrier (device status) */
+    FA_ERR_TIMEOUT = 5,      /* a kernel gave up waiting on an internal barrier (device status) */
+    FA_ERR_CAPACITY = 6      /* rows appended to a full 4-bit cache were dropped (device status) */
 } fa_status_t;
 
 /* Element type of q, k, v and o (the low 8 bits of every `dtype` argument). */
@@ -326,10 +327,175 @@ size_t fa_bwd_host_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t N_
    8 * B * H * ceil(N_q / 128) * 128 (rounded up to 256) + 4 * B * H * N_q * d. */
 size_t fa_bwd_workspace_size(int64_t B, int64_t H, int64_t N_q, int64_t d);
 
+/* ------------------------------------------------------------------------
+ * The 4-bit key/value cache.
+ *
+ * Decode steps against a long cache are bound by reading it.  This cache
+ * holds keys and values in 4 bits and a scale per 16 channels (4.5 bits a
+ * value, 0.28 of a 16-bit cache).  fa_kv4_append stores rows, fa_kv4_read
+ * returns them, fa_kv4_fwd attends over them, fa_fwd_weights and fa_kv4_fwd
+ * accumulate the attention weight each entry receives, and fa_kv4_evict keeps
+ * the entries with the largest weight.  The pages have no counterpart of
+ * these entry points; the attention is the pages' (online softmax over key
+ * partitions, "FlashAttention dissected", sections "Algorithmic core in
+ * pseudocode" and "Interaction with the KV cache during inference").
+ *
+ * Format.  A row (one token of one key/value head) is cut into blocks of 16
+ * consecutive channels.  Per block
+ *     s = e4m3(max |x| / 6)       nearest, ties to even, at most 448
+ *     c = e2m1(x / s)             nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with
+ *                                 its sign, ties to the even code, at most 6
+ * and the stored value is c * s, which has at most 6 significant bits and
+ * lies in 2^-10 .. 2688: bf16 and fp16 both hold it exactly, and nothing
+ * below rounds it again.  s = 0: the block holds zeros (the sign of a zero is
+ * not defined).  A block with an infinity or a NaN gets the scale NaN and
+ * reads as NaN throughout.  Two codes share a byte, the even channel in the
+ * low half.
+ *
+ * Entries are slots 0 .. length - 1 of each key/value head; attention does
+ * not depend on their order.  The library never allocates: every array is
+ * the caller's, on the current device.
+ */
+typedef struct {
+    uint8_t* k_codes;   /* [B, H_kv, capacity, d / 2], 16-byte aligned */
+    uint8_t* k_scales;  /* [B, H_kv, capacity, d / 16] e4m3, 16-byte aligned */
+    uint8_t* v_codes;   /* as k_codes */
+    uint8_t* v_scales;  /* as k_scales */
+    float* weight;      /* [B, H_kv, capacity] accumulated attention weight, or NULL */
+    int32_t* pos;       /* [B, H_kv, capacity] position of the token in its sequence, or NULL */
+    int32_t* counts;    /* [2, B]: slots in use (the length), then tokens appended so far */
+    int64_t B, H_kv;
+    int64_t capacity;   /* slots per key/value head, a multiple of 128 */
+    int64_t d;          /* 64 or 128 */
+} fa_kv4_cache_t;
+
+/*
+ * fa_kv4_append — store n rows per sequence at slots length .. length + n - 1.
+ *
+ *   k, v       : [B, H_kv, n, d] bf16 or fp16 (`dtype`, no flags), contiguous,
+ *                16-byte aligned.
+ *   counts_out : int32 [2, B], receives length + n and appended + n; may be
+ *                the cache's own counts (advanced in place), which are left
+ *                alone otherwise.
+ * pos, where the cache has it, gets appended + i for row i, and weight 0.
+ * Rows that do not fit the capacity are dropped, the length stops at the
+ * capacity, and fa_device_status reports FA_ERR_CAPACITY.  One kernel, and a
+ * second when counts advance in place and more than 1024 blocks of 16
+ * channels are stored.
+ */
+int fa_kv4_append(const fa_kv4_cache_t* cache, const void* k, const void* v, int64_t n, int dtype,
+                  int32_t* counts_out, void* stream);
+
+/*
+ * fa_kv4_read — the stored values of `count` slots of every head as bf16 or
+ * fp16 rows k, v [B, H_kv, count, d] (exact; see the format), from slot
+ * first[b] on (int32 [B] on the device; NULL: from slot 0).  Slots outside
+ * 0 .. capacity - 1 read as zero; slots at or behind the length hold what was
+ * there.  k or v may be NULL.  With it a chunk of a long prompt attends over
+ * stored rows by fa_fwd_ex.
+ */
+int fa_kv4_read(const fa_kv4_cache_t* cache, const int32_t* first, int64_t count, void* k, void* v,
+                int dtype, void* stream);
+
+/*
+ * fa_kv4_fwd — attention of q [B, H, N_q, d] over the cache's entries:
+ *
+ *     O = softmax(scale q K^T) V,  lse = log sum exp(scale q K^T)
+ *
+ * over the first counts[b] slots of key/value head h / (H / H_kv).
+ *   o          : [B, H, N_q, d] of `dtype`;  lse: fp32 [B, H, N_q] or NULL.
+ *   weight_out : fp32 [B, H_kv, capacity] or NULL.  Entry j of a head gets
+ *                cache.weight (0 where that is NULL) plus the softmax weights
+ *                of slot j, summed over the head's H / H_kv query heads and
+ *                N_q rows; may be cache.weight itself.  Slots at or behind
+ *                the length are not written.
+ *   dtype      : FA_DTYPE_BF16 or FA_DTYPE_F16, optionally FA_FLAG_CAUSAL:
+ *                row i sees slots j < length - (N_q - 1 - i), as the last N_q
+ *                tokens do that were appended before the call.
+ *   N_q * H / H_kv <= 128 (decode steps and drafts; longer chunks read the
+ *   rows back with fa_kv4_read and use fa_fwd_ex): else FA_ERR_UNSUPPORTED.
+ *   workspace  : fa_kv4_fwd_workspace_size(...) bytes, 16-byte aligned;
+ *                nothing in it needs to be zeroed.
+ * A row that sees no slot gets O = 0 and lse = -inf and adds no weight.
+ * Lengths are read on the device (clamped to 0 .. capacity), so a captured
+ * call follows them.  Results do not depend on the order in which blocks run.
+ * Two kernels.
+ */
+int fa_kv4_fwd(const fa_kv4_cache_t* cache, const void* q, void* o, float* lse, float* weight_out,
+               int64_t H, int64_t N_q, float scale, int dtype, void* workspace, size_t workspace_bytes,
+               void* stream);
+
+/* Workspace bytes of fa_kv4_fwd on the current device (the SM count is the
+ * one CUDA query; 1024 SMs when no device answers); 0 for invalid sizes. */
+size_t fa_kv4_fwd_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t N_q, int64_t capacity, int64_t d,
+                                 int with_weight);
+
+/*
+ * fa_kv4_evict — keep the `keep` entries of each key/value head that carry
+ * the largest weight.
+ *
+ *   rank_by    : fp32 [B, H_kv, capacity], the weights to go by; NULL:
+ *                cache.weight.  A NaN counts as larger than any number.
+ *   sinks, recent : entries with pos < sinks or pos >= appended - recent are
+ *                kept before all others (pos is needed when either is > 0).
+ *                Ties, and any two of those, go to the lowest slot.
+ *   to         : NULL: in place.  Else a cache of the same B, H_kv and d with
+ *                capacity >= keep, sharing no memory with the first, which
+ *                gets the kept entries and leaves the first as it was.  It
+ *                gets pos and weight where both caches have them.
+ *   src        : int32 [B, H_kv, keep]: the slot each slot's entry came from,
+ *                -1 behind the last.
+ *   counts_out : int32 [2, B]: min(length, keep) and appended; may be either
+ *                cache's counts, which are left alone otherwise.
+ * Slot j < min(length, keep) keeps its entry where that is kept; the other
+ * slots there take, in order, the kept entries from behind them.  Slots at or
+ * behind the new length are left as they were.  keep >= 1; capacity up to
+ * 393216.  One kernel (two when counts_out is the first cache's counts).
+ */
+int fa_kv4_evict(const fa_kv4_cache_t* cache, int64_t keep, int64_t sinks, int64_t recent,
+                 const float* rank_by, const fa_kv4_cache_t* to, int32_t* src, int32_t* counts_out,
+                 void* stream);
+
+/*
+ * fa_fwd_weights — the attention weight that the keys of a prompt receive:
+ *
+ *     out[b, g, j] = in[b, g, j] + sum over the query heads h of group g and
+ *                    rows i >= first_query of exp(scale q_i . k_j - lse_i)
+ *
+ * where row i sees key j.  q [B, H, N_q, d] and k [B, H_kv, N_kv, d] bf16 or
+ * fp16, lse as fa_fwd / fa_fwd_ex returned it for the same scale and mask
+ * (dtype's FA_FLAG_CAUSAL); rows whose lse is -inf count nothing.
+ *   weight_in  : fp32, rows of N_kv values `weight_stride` apart (>= N_kv; a
+ *                cache's weight has stride capacity), or NULL for zeros.
+ *   weight_out : the same layout; may be weight_in.
+ * Each output is summed by one thread in a fixed order: results repeat bit
+ * for bit.  One kernel; no workspace.
+ */
+int fa_fwd_weights(const void* q, const void* k, const float* lse, const float* weight_in, float* weight_out,
+                   int64_t weight_stride, int64_t B, int64_t H, int64_t H_kv, int64_t N_q, int64_t N_kv,
+                   int64_t d, int64_t first_query, float scale, int dtype, void* stream);
+
+/* The host-side argument checks of the calls above, alone; no CUDA call but
+ * fa_kv4_fwd_workspace_size's query. */
+int fa_kv4_append_validate(const fa_kv4_cache_t* cache, const void* k, const void* v, int64_t n, int dtype,
+                           const int32_t* counts_out);
+int fa_kv4_read_validate(const fa_kv4_cache_t* cache, const int32_t* first, int64_t count, const void* k,
+                         const void* v, int dtype);
+int fa_kv4_fwd_validate(const fa_kv4_cache_t* cache, const void* q, const void* o, const float* lse,
+                        const float* weight_out, int64_t H, int64_t N_q, float scale, int dtype,
+                        const void* workspace, size_t workspace_bytes);
+int fa_kv4_evict_validate(const fa_kv4_cache_t* cache, int64_t keep, int64_t sinks, int64_t recent,
+                          const float* rank_by, const fa_kv4_cache_t* to, const int32_t* src,
+                          const int32_t* counts_out);
+int fa_fwd_weights_validate(const void* q, const void* k, const float* lse, const float* weight_in,
+                            const float* weight_out, int64_t weight_stride, int64_t B, int64_t H, int64_t H_kv,
+                            int64_t N_q, int64_t N_kv, int64_t d, int64_t first_query, float scale, int dtype);
+
 /*
  * fa_device_status — synchronise `stream`, then read and clear the device
- * error word the kernels set when a bounded wait gives up.  Returns FA_OK,
- * FA_ERR_TIMEOUT, or FA_ERR_CUDA if the synchronisation itself failed.
+ * error word the kernels set when a bounded wait gives up or a 4-bit cache
+ * overflows.  Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_CAPACITY, or FA_ERR_CUDA
+ * if the synchronisation itself failed.
  * A launch that timed out leaves its outputs incomplete (the CTAs of that
  * launch stop early); later launches run normally whether or not the word
  * has been read.
