@@ -1,0 +1,783 @@
+// Attention over the 4-bit key/value cache, sm_103a (include/fa.h,
+// fa_kv4_fwd): the online softmax of "FlashAttention dissected", section
+// "Algorithmic core in pseudocode", over key partitions (its section
+// "Interaction with the KV cache during inference").
+//
+// Mathematics.  Per key/value head, with the R = N_q * group query rows of
+// its query heads: S^T = K Q^T (keys x rows), P = 2^(c S - ref), O^T = V^T P^T.
+// Keys, not rows, take the 16-row side of the matrix instruction
+// (m16n8k16), so up to 8 rows cost one instruction per 16 keys x 16 channels.
+// A stored value is e2m1 x e4m3, exact in fp16, so both products run in fp16
+// whatever the type of q: a row of q is scaled by a power of two to
+// [2^14, 2^15), which is exact (values below 2^-28 of the row's largest lose
+// bits, less than the fp32 accumulation does), and the power goes into c.
+//
+// Layout.  A cache row is read straight in fragment order: the contraction
+// index of S and the rows of O^T are permuted so that lane (g, t) of a
+// quarter-warp reads consecutive bytes of a key's codes (channels
+// (d / 4) t ..) and of a value's (channels (d / 8) g ..).  Nibbles of two
+// values are interleaved in bits before they are widened, which pairs keys
+// as the second product's operand needs them.
+//
+// What bounds it: reading the cache.  Each warp has a ring of slabs (32 keys:
+// codes and scales of K and V, four bulk copies) of its own, so warps never
+// wait for one another inside a unit; 16 warps an SM keep 147 KB in flight.
+//
+// Work split.  The slabs of all units (sequence, key/value head, block of
+// rows), in order, are cut into equal runs, one per CTA, from the lengths on
+// the device: no CTA idles because a sequence is short, and a long one is
+// shared by many.  A CTA whose run holds a whole unit writes its output; of
+// a unit cut between CTAs each leaves a partial result (at most two per CTA:
+// the unit it starts inside and the one it ends inside), which the second
+// kernel adds up in order, so results do not depend on timing.
+//
+// Every wait is bounded as in the forward kernel; a warp that gives up skips
+// its remaining slabs but still reaches the block's barriers.
+#include <cmath>
+#include <cstdint>
+
+#include "fa_fwd_kernel.cuh"
+#include "fa_kv4.h"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads4 = kWarps * 32;
+constexpr int kSlab = 32;          // keys per slab
+constexpr float kRefShift = 7.0f;  // weights are 2^7 at the row's reference maximum: fp16 then
+                                   // holds weights down to 2^-31 of it
+constexpr float kGrow = 15.0f;     // and up to 2^8 times it before the reference moves
+
+template <int D, int NT>
+struct Kv4Cfg {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kStages = 2;
+    static constexpr int kCodeBytes = kSlab * D / 2;
+    static constexpr int kScaleBytes = kSlab * D / 16;
+    static constexpr int kSlabBytes = 2 * (kCodeBytes + kScaleBytes);
+    static constexpr int kMt = D / 16;                  // 16-row tiles of O^T
+    static constexpr int kRegs = kMt * NT * 4;          // accumulators of O^T per lane
+    static constexpr int kOffRing = 0;                  // [warps][stages][slab]
+    static constexpr int kOffO = kOffRing + kWarps * kStages * kSlabBytes;  // float [warps][kRegs][32]
+    static constexpr int kOffMl = kOffO + kWarps * kRegs * 32 * 4;          // float [warps][kRows][4]
+    static constexpr int kOffBar = kOffMl + kWarps * kRows * 4 * 4;
+    static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
+    static constexpr int kSmemBytes = kOffAbort + 16;
+    static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+    static_assert(kSmemBytes * kCtasPerSm <= 232448 - 1024 * kCtasPerSm, "shared memory budget exceeded");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                          uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+// The four f16x2 pairs of a word's eight e2m1 codes.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ T lds(const uint8_t* p) {
+    return *reinterpret_cast<const T*>(p);
+}
+
+__device__ __forceinline__ int kv4_length(const Kv4Cache& c, int b) {
+    return min(max(c.counts[b], 0), c.capacity);
+}
+__device__ __forceinline__ int slabs_of(int len) { return (len + kSlab - 1) / kSlab; }
+
+// Sum over sequences [0, stop) of their slabs x units, by a warp (every lane
+// gets it); *all gets the sum over all sequences.
+__device__ __forceinline__ long long slabs_before(const Kv4Cache& c, int units, int stop, long long* all) {
+    const int lane = threadIdx.x % 32;
+    long long before = 0, total = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+        const int b = b0 + lane;
+        const long long n = b < c.B ? static_cast<long long>(slabs_of(kv4_length(c, b))) * units : 0;
+        total += n;
+        if (b < stop) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    *all = total;
+    return before;
+}
+// Slabs per CTA: equal runs, at least one slab for every warp.
+__device__ __forceinline__ long long slabs_per_cta(long long total, int ctas) {
+    const long long per = (total + ctas - 1) / ctas;
+    return per < kWarps ? kWarps : per;
+}
+
+// Position in a CTA's run of slabs.
+struct Cursor {
+    long long pos, end;  // in slabs over all units
+    long long base;      // first slab of sequence b
+    int b, len, slabs;   // sequence, its length and the slabs of one of its units
+    int unit;            // unit of sequence b
+    int s0, s1;          // slabs of that unit in this run
+
+    __device__ __forceinline__ void locate(const Kv4Cache& c, int units) {
+        while (pos < end && pos >= base + static_cast<long long>(slabs) * units) {
+            base += static_cast<long long>(slabs) * units;
+            ++b;
+            len = kv4_length(c, b);
+            slabs = slabs_of(len);
+        }
+        if (pos < end) {
+            const long long off = pos - base;
+            unit = static_cast<int>(off / slabs);
+            s0 = static_cast<int>(off - static_cast<long long>(unit) * slabs);
+            s1 = static_cast<int>(min(static_cast<long long>(slabs), s0 + (end - pos)));
+        }
+    }
+    __device__ __forceinline__ bool valid() const { return pos < end; }
+    __device__ __forceinline__ void next(const Kv4Cache& c, int units) {
+        pos += s1 - s0;
+        locate(c, units);
+    }
+    __device__ __forceinline__ void start(const Kv4Cache& c, int units, int ctas, int cta) {
+        long long total;
+        slabs_before(c, units, 0, &total);
+        const long long per = slabs_per_cta(total, ctas);
+        pos = min(total, per * cta);
+        end = min(total, pos + per);
+        base = 0;
+        b = 0;
+        unit = s0 = s1 = 0;
+        // the sequence that holds `pos`, 32 sequences at a time
+        const int lane = threadIdx.x % 32;
+        for (int b0 = 0; pos < end && b0 < c.B; b0 += 32) {
+            const long long n =
+                b0 + lane < c.B ? static_cast<long long>(slabs_of(kv4_length(c, b0 + lane))) * units : 0;
+            long long incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, base + incl > pos);
+            if (past) {
+                const int who = __ffs(static_cast<int>(past)) - 1;
+                base += __shfl_sync(0xffffffffu, incl - n, who);
+                b = b0 + who;
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        len = kv4_length(c, b);
+        slabs = slabs_of(len);
+        locate(c, units);
+    }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_kernel(const Kv4FwdParams p) {
+    using C = Kv4Cfg<D, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = static_cast<int>(threadIdx.x) / 32, lane = static_cast<int>(threadIdx.x) % 32;
+    const int g = lane / 4, t = lane % 4;
+    const uint32_t sbase = smem_u32(smem);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
+    FwdParams wp;  // what a bounded wait reports to
+    wp.status = p.status;
+    wp.gen = p.gen;
+    auto bar = [&](int s) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(warp * C::kStages + s); };
+    uint8_t* ring = smem + C::kOffRing + warp * C::kStages * C::kSlabBytes;
+
+    if (lane == 0)
+        for (int s = 0; s < C::kStages; ++s) mbar_init(bar(s), 1);
+    if (threadIdx.x == 0) *abort_flag = 0u;
+    mbar_init_fence();
+    __syncthreads();
+
+    const int units = p.c.H_kv * p.row_blocks;
+    Cursor load;
+    load.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x));
+    Cursor cur = load;
+    const uint64_t once = policy_evict_first();  // every byte is read once per block of rows
+
+    // ---- producer side of this warp: slabs s0 + warp, + 8, .. of each unit
+    int load_slab = cur.s0 + warp;
+    int issued = 0;  // slabs asked for so far; slab i uses stage i % kStages
+    auto issue = [&]() {
+        while (load.valid() && load_slab >= load.s1) {
+            load.next(p.c, units);
+            load_slab = load.s0 + warp;
+        }
+        if (!load.valid()) return;
+        if (lane == 0) {
+            const int s = issued % C::kStages;
+            const long long row =
+                (static_cast<long long>(load.b) * p.c.H_kv + load.unit / p.row_blocks) * p.c.capacity +
+                static_cast<long long>(load_slab) * kSlab;
+            const uint32_t dst = sbase + C::kOffRing + (warp * C::kStages + s) * C::kSlabBytes;
+            mbar_arrive_expect_tx(bar(s), C::kSlabBytes);
+            bulk_load(dst, p.c.codes[0] + row * (D / 2), C::kCodeBytes, bar(s), once);
+            bulk_load(dst + C::kCodeBytes, p.c.codes[1] + row * (D / 2), C::kCodeBytes, bar(s), once);
+            bulk_load(dst + 2 * C::kCodeBytes, p.c.scales[0] + row * (D / 16), C::kScaleBytes, bar(s), once);
+            bulk_load(dst + 2 * C::kCodeBytes + C::kScaleBytes, p.c.scales[1] + row * (D / 16), C::kScaleBytes, bar(s),
+                      once);
+        }
+        ++issued;
+        load_slab += kWarps;
+    };
+    for (int s = 0; s < C::kStages; ++s) issue();
+
+    float* sm_o = reinterpret_cast<float*>(smem + C::kOffO);
+    float* sm_ml = reinterpret_cast<float*>(smem + C::kOffMl);
+    int used = 0;  // slabs consumed
+    bool ok = true;
+
+    for (; cur.valid(); cur.next(p.c, units)) {
+        const int kvh = cur.b * p.c.H_kv + cur.unit / p.row_blocks;
+        const int row0 = (cur.unit % p.row_blocks) * C::kRows;  // of the head's rows
+        // ---- q fragments: lane (g, t) holds channels (D / 4) t .. of rows g + 8 nt, scaled
+        uint32_t q[NT][D / 16][2];
+        float c[NT][2];  // score factor of rows 2t, 2t + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = row0 + 8 * nt + g;
+            uint4 raw[D / 32];
+            if (r < p.rows) {
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.q) + (static_cast<long long>(kvh) * p.rows + r) * D + t * (D / 4));
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(src + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                m = __vmaxu2(__vmaxu2(__vmaxu2(m, raw[i].x & 0x7FFF7FFFu), raw[i].y & 0x7FFF7FFFu),
+                             __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
+            m = max(m & 0xFFFFu, m >> 16);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint32_t mf = __float_as_uint(p.f16 ? widen_lo16<true>(m) : widen_lo16<false>(m));
+            // the row's largest magnitude is in [2^e, 2^(e+1)); zero, infinite or NaN rows stay as they are
+            int e = static_cast<int>(mf >> 23) - 127;
+            e = mf == 0u || e == 128 ? 14 : max(e, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float lo = p.f16 ? widen_lo16<true>(w[j]) : widen_lo16<false>(w[j]);
+                    const float hi = p.f16 ? widen_lo16<true>(w[j] >> 16) : widen_lo16<false>(w[j] >> 16);
+                    // word j of 16 bytes: channels 8 i + 2 j, + 1: step 2 i + j / 2, half j % 2
+                    q[nt][2 * i + j / 2][j & 1] = pack_f16x2(lo * up, hi * up);
+                }
+            }
+            const float f = p.scale_log2 * down;
+            c[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+            c[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+        }
+        float ref[NT][2], l[NT][2], lq[NT][4], o[NT][C::kMt][4];
+        int lim[NT][2];  // slots rows 2t, 2t + 1 see
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = row0 + 8 * nt + 2 * t + i;
+                ref[nt][i] = -INFINITY;
+                l[nt][i] = 0.0f;
+                lim[nt][i] = cur.len - (p.causal && r < p.rows ? p.Nq - 1 - r % p.Nq : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lq[nt][i] = 0.0f;
+#pragma unroll
+                for (int mt = 0; mt < C::kMt; ++mt) o[nt][mt][i] = 0.0f;
+            }
+        }
+        const int all_see = cur.len - (p.causal ? p.Nq - 1 : 0);  // slots every row sees
+        float* logits = p.logits == nullptr ? nullptr
+                                            : p.logits + static_cast<long long>(kvh) * p.c.capacity * p.rows + row0;
+
+        for (int slab = cur.s0 + warp; ok && slab < cur.s1; slab += kWarps) {
+            const int s = used % C::kStages;
+            ok = __all_sync(0xffffffffu, wait_phase(bar(s), (used / C::kStages) & 1, abort_flag, wp, 80));
+            if (!ok) break;
+            const uint8_t* kc = ring + s * C::kSlabBytes;
+            const uint8_t* vc = kc + C::kCodeBytes;
+            const uint8_t* ks = vc + C::kCodeBytes;
+            const uint8_t* vs = ks + C::kScaleBytes;
+            const int key0 = slab * kSlab;
+            const bool masked = key0 + kSlab > all_see;
+            const int kg = (g >> 1) + 4 * (g & 1);  // key of fragment row g (and 8 more of row g + 8)
+
+            // ---- S^T of both halves of 16 keys
+            float x[2][NT][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[h][nt][i] = 0.0f;
+                const int ka = 16 * h + kg, kb = ka + 8;
+                uint32_t wa[D / 32], wb[D / 32], sa[D / 64], sb[D / 64];
+                if constexpr (D == 128) {
+                    const uint4 a = lds<uint4>(kc + ka * 64 + t * 16), b = lds<uint4>(kc + kb * 64 + t * 16);
+                    wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
+                    wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
+                    const uint32_t s2a = e4m3x2_to_f16x2(lds<uint16_t>(ks + ka * 8 + t * 2));
+                    const uint32_t s2b = e4m3x2_to_f16x2(lds<uint16_t>(ks + kb * 8 + t * 2));
+                    sa[0] = __byte_perm(s2a, 0, 0x1010), sa[1] = __byte_perm(s2a, 0, 0x3232);
+                    sb[0] = __byte_perm(s2b, 0, 0x1010), sb[1] = __byte_perm(s2b, 0, 0x3232);
+                } else {
+                    const uint2 a = lds<uint2>(kc + ka * 32 + t * 8), b = lds<uint2>(kc + kb * 32 + t * 8);
+                    wa[0] = a.x, wa[1] = a.y;
+                    wb[0] = b.x, wb[1] = b.y;
+                    sa[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + ka * 4 + t) * 0x0101u);
+                    sb[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + kb * 4 + t) * 0x0101u);
+                }
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    uint32_t ha[4], hb[4];
+                    widen_codes(wa[w], ha);
+                    widen_codes(wb[w], hb);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ha[i] = mul16x2(ha[i], sa[w / 2]);
+                        hb[i] = mul16x2(hb[i], sb[w / 2]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(x[h][nt], ha[0], hb[0], ha[1], hb[1], q[nt][2 * w][0], q[nt][2 * w][1]);
+                        mma_f16(x[h][nt], ha[2], hb[2], ha[3], hb[3], q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+                    }
+                }
+            }
+            // ---- scaled scores (base 2); hidden slots are -inf whatever is stored there
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[h][nt][i] *= c[nt][i & 1];
+                        if (masked && key0 + 16 * h + kg + 8 * (i >> 1) >= lim[nt][i & 1]) x[h][nt][i] = -INFINITY;
+                    }
+            if (logits != nullptr) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        const int key = key0 + 16 * h + kg + 8 * i2;
+                        if (key < cur.len) {
+                            float* dst = logits + static_cast<long long>(key) * p.rows;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const int r = 8 * nt + 2 * t;
+                                if (row0 + r < p.rows) dst[r] = x[h][nt][2 * i2];
+                                if (row0 + r + 1 < p.rows) dst[r + 1] = x[h][nt][2 * i2 + 1];
+                            }
+                        }
+                    }
+            }
+            bool grow = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) grow |= x[h][nt][i] > ref[nt][i & 1] + kGrow;
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float m = fmaxf(fmaxf(x[0][nt][i], x[0][nt][i + 2]), fmaxf(x[1][nt][i], x[1][nt][i + 2]));
+#pragma unroll
+                        for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                        const float nr = fmaxf(ref[nt][i], m - kRefShift);
+                        // -inf: nothing seen yet (and nothing to rescale)
+                        const float alpha = nr == -INFINITY ? 1.0f : ex2(ref[nt][i] - nr);
+                        ref[nt][i] = nr;
+                        l[nt][i] *= alpha;
+                        lq[nt][i] *= alpha;
+#pragma unroll
+                        for (int mt = 0; mt < C::kMt; ++mt) {
+                            o[nt][mt][i] *= alpha;
+                            o[nt][mt][i + 2] *= alpha;
+                        }
+                    }
+            }
+            // ---- weights, O^T += V^T P^T
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // a row that has seen nothing has ref = -inf and x = -inf (or NaN): 2^(-inf - 0)
+                        const float r = ref[nt][i & 1] == -INFINITY ? 0.0f : ref[nt][i & 1];
+                        w[i] = ex2(x[h][nt][i] - r);
+                        l[nt][i & 1] += w[i];
+                    }
+                    pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+                    pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+                    mma_f16(lq[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nt][0], pb[nt][1]);
+                }
+                uint32_t sc[4], v[4][D / 64];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = 16 * h + 4 * i + t;
+                    if constexpr (D == 128) {
+                        const uint2 a = lds<uint2>(vc + key * 64 + g * 8);
+                        v[i][0] = a.x, v[i][1] = a.y;
+                        sc[i] = lds<uint8_t>(vs + key * 8 + g);
+                    } else {
+                        v[i][0] = lds<uint32_t>(vc + key * 32 + g * 4);
+                        sc[i] = lds<uint8_t>(vs + key * 4 + g / 2);
+                    }
+                }
+                if (masked) {
+                    // slots behind the length hold anything: values 0.  A NaN in a slot that only some
+                    // rows see must not reach the others (0 * NaN): it is taken out of the product and
+                    // set in the rows that see it.
+                    bool nan = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (key0 + 16 * h + 4 * i + t >= cur.len) sc[i] = 0u;
+                        nan |= (sc[i] & 0x7Fu) == 0x7Fu;
+                    }
+                    if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const uint32_t su = __shfl_sync(0xffffffffu, sc[i], (lane & ~3) | u);
+                                if ((su & 0x7Fu) == 0x7Fu) {
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                        for (int j = 0; j < 2; ++j)
+                                            if (key0 + 16 * h + 4 * i + u < lim[nt][j]) {
+#pragma unroll
+                                                for (int mt = 0; mt < C::kMt; ++mt)
+                                                    o[nt][mt][j] = o[nt][mt][j + 2] = __int_as_float(0x7FC00000);
+                                            }
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((sc[i] & 0x7Fu) == 0x7Fu) sc[i] = 0u;
+                    }
+                }
+                const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w) {
+                    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                    uint32_t a0[4], a1[4], a2[4], a3[4];
+                    widen_codes((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), a0);
+                    widen_codes(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), a1);
+                    widen_codes((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), a2);
+                    widen_codes(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), a3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        a0[i] = mul16x2(a0[i], s01);
+                        a1[i] = mul16x2(a1[i], s01);
+                        a2[i] = mul16x2(a2[i], s23);
+                        a3[i] = mul16x2(a3[i], s23);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(o[nt][4 * w + i], a0[i], a1[i], a2[i], a3[i], pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+            __syncwarp();  // the slab has been read by every lane
+            ++used;
+            issue();
+        }
+
+        // ---- the unit's result over the CTA's warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float s = l[nt][i];
+#pragma unroll
+                for (int off = 4; off < 32; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
+                if (g == 0)
+                    *reinterpret_cast<float4*>(sm_ml + (warp * C::kRows + 8 * nt + 2 * t + i) * 4) =
+                        make_float4(ref[nt][i], s, lq[nt][i], 0.0f);
+            }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sm_o[((warp * C::kMt + mt) * NT * 4 + nt * 4 + i) * 32 + lane] = o[nt][mt][i];
+        __syncthreads();
+        // rows 2t, 2t + 1 of each block of 8: reference, sums, and every warp's weight
+        const bool whole = cur.s0 == 0 && cur.s1 == cur.slabs;
+        const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (cur.s0 > 0 ? 0 : 1)) * C::kRows;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float wt[kWarps][2], M[2], L[2], LQ[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * nt + 2 * t + i;
+                M[i] = -INFINITY;
+                L[i] = LQ[i] = 0.0f;
+                for (int w = 0; w < kWarps; ++w) M[i] = fmaxf(M[i], sm_ml[(w * C::kRows + r) * 4]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 ml = *reinterpret_cast<const float4*>(sm_ml + (w * C::kRows + r) * 4);
+                    // a warp that saw nothing counts 0 (a NaN sum stays one)
+                    wt[w][i] = M[i] == -INFINITY ? 1.0f : ex2(ml.x - M[i]);
+                    L[i] += wt[w][i] * ml.y;
+                    LQ[i] += wt[w][i] * ml.z;
+                }
+            }
+            for (int mt = warp; mt < C::kMt; mt += kWarps) {
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[i] += wt[w][i & 1] * sm_o[((w * C::kMt + mt) * NT * 4 + nt * 4 + i) * 32 + lane];
+                const int ch = (D / 8) * g + 2 * mt;  // channels ch, ch + 1
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = row0 + 8 * nt + 2 * t + i;
+                    if (r >= p.rows) continue;
+                    if (whole) {
+                        const float inv = LQ[i] == 0.0f ? 0.0f : 1.0f / LQ[i];
+                        const float lo = acc[i] * inv, hi = acc[i + 2] * inv;
+                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) +
+                                                     (static_cast<long long>(kvh) * p.rows + r) * D + ch) =
+                            p.f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+                    } else {
+                        *reinterpret_cast<float2*>(p.part_o + (slot + 8 * nt + 2 * t + i) * D + ch) =
+                            make_float2(acc[i], acc[i + 2]);
+                    }
+                }
+            }
+            if (warp == 0 && g == 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = row0 + 8 * nt + 2 * t + i;
+                    if (r >= p.rows) continue;
+                    if (whole) {
+                        const long long row = static_cast<long long>(kvh) * p.rows + r;
+                        const float lse2 = L[i] == 0.0f ? -INFINITY : M[i] + log2f(L[i]);
+                        if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
+                        p.row_lse2[row] = lse2;
+                    } else {
+                        *reinterpret_cast<float4*>(p.part_ml + (slot + 8 * nt + 2 * t + i) * 4) =
+                            make_float4(M[i], L[i], LQ[i], 0.0f);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // a warp that gave up leaves no copy of its own in flight behind it
+    if (!ok)
+        for (; used < issued; ++used)
+            wait_phase(bar(used % C::kStages), (used / C::kStages) & 1, abort_flag, wp, 81, false);
+}
+
+// ------------------------------------------------------------ second kernel
+// Where a unit's partial results are: CTAs first .. last of the main kernel,
+// slot 1 of the first and slot 0 of the others.
+struct Parts {
+    int slabs;
+    long long first, last;
+};
+__device__ __forceinline__ Parts parts_of(const Kv4FwdParams& p, int b, int unit) {
+    const int units = p.c.H_kv * p.row_blocks;
+    long long total;
+    const long long base = slabs_before(p.c, units, b, &total);
+    const long long per = slabs_per_cta(total, p.ctas);
+    Parts r;
+    r.slabs = slabs_of(kv4_length(p.c, b));
+    const long long hs = base + static_cast<long long>(unit) * r.slabs;
+    r.first = hs / per;
+    r.last = r.slabs > 0 ? (hs + r.slabs - 1) / per : r.first;
+    return r;
+}
+__device__ __forceinline__ long long part_row(long long cta, long long first, int rows, int r) {
+    return (cta * 2 + (cta == first ? 1 : 0)) * rows + r;
+}
+// A row's reference, exact sum and rounded sum over its parts, by a warp.
+__device__ __forceinline__ void row_sums(const Kv4FwdParams& p, const Parts& u, int rows, int r, float& M, float& L,
+                                         float& LQ) {
+    const int lane = threadIdx.x % 32;
+    M = -INFINITY;
+    for (long long c = u.first + lane; c <= u.last; c += 32)
+        M = fmaxf(M, p.part_ml[part_row(c, u.first, rows, r) * 4]);
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    L = LQ = 0.0f;
+    for (long long c = u.first + lane; c <= u.last; c += 32) {
+        const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + part_row(c, u.first, rows, r) * 4);
+        const float w = M == -INFINITY ? 1.0f : ex2(ml.x - M);
+        L += w * ml.y;
+        LQ += w * ml.z;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) {
+        L += __shfl_xor_sync(0xffffffffu, L, o);
+        LQ += __shfl_xor_sync(0xffffffffu, LQ, o);
+    }
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinKeys = 1024;  // keys per block of the weights' part
+constexpr int kMaxRows = 128;
+
+// Blocks 0 .. join_blocks - 1: one warp per output row whose unit several
+// CTAs shared (or that has no slot at all).  The others: accumulated weight,
+// kJoinKeys slots of one key/value head each.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdParams p, int rows_per_block,
+                                                                 int join_blocks) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (static_cast<int>(blockIdx.x) < join_blocks) {
+        const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + warp;
+        if (row >= static_cast<long long>(p.c.B) * p.c.H_kv * p.rows) return;
+        const long long kvh = row / p.rows;
+        const int r = static_cast<int>(row - kvh * p.rows);
+        const int b = static_cast<int>(kvh / p.c.H_kv);
+        const int unit = static_cast<int>(kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block;
+        const Parts u = parts_of(p, b, unit);
+        if (u.slabs > 0 && u.first == u.last) return;  // the main kernel wrote it
+        constexpr int kPer = D / 32;
+        float acc[kPer] = {}, M = -INFINITY, L = 0.0f, LQ = 0.0f;
+        if (u.slabs > 0) {
+            const int rb = r % rows_per_block;
+            row_sums(p, u, rows_per_block, rb, M, L, LQ);
+            for (long long c = u.first; c <= u.last; ++c) {
+                const long long at = part_row(c, u.first, rows_per_block, rb);
+                const float w = M == -INFINITY ? 1.0f : ex2(p.part_ml[at * 4] - M);
+                const float* src = p.part_o + at * D + lane * kPer;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) acc[i] += w * src[i];
+            }
+        }
+        const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + lane * kPer);
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2)
+            dst[i / 2] = p.f16 ? pack_f16x2(acc[i] * inv, acc[i + 1] * inv) : pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+        if (lane == 0 && p.lse != nullptr)
+            p.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        return;
+    }
+    __shared__ float lse2[kMaxRows];
+    const int chunks = (p.c.capacity + kJoinKeys - 1) / kJoinKeys;
+    const int i = static_cast<int>(blockIdx.x) - join_blocks;
+    const int kvh = i / chunks, b = kvh / p.c.H_kv;
+    const int key0 = (i % chunks) * kJoinKeys, len = kv4_length(p.c, b);
+    if (key0 >= len) return;
+    for (int r = warp; r < p.rows; r += kJoinThreads / 32) {
+        const Parts u = parts_of(p, b, (kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block);
+        float v;
+        if (u.first == u.last) {
+            v = p.row_lse2[static_cast<long long>(kvh) * p.rows + r];
+        } else {
+            float M, L, LQ;
+            row_sums(p, u, rows_per_block, r % rows_per_block, M, L, LQ);
+            v = L == 0.0f ? -INFINITY : M + log2f(L);
+        }
+        if (lane == 0) lse2[r] = v == -INFINITY ? INFINITY : v;  // a row that sees nothing adds nothing
+    }
+    __syncthreads();
+    for (int key = key0 + threadIdx.x; key < min(key0 + kJoinKeys, len); key += kJoinThreads) {
+        const float* t = p.logits + (static_cast<long long>(kvh) * p.c.capacity + key) * p.rows;
+        float s = 0.0f;
+        for (int r = 0; r < p.rows; ++r) s += ex2(t[r] - lse2[r]);
+        const long long at = static_cast<long long>(kvh) * p.c.capacity + key;
+        p.weight_out[at] = (p.weight_in != nullptr ? p.weight_in[at] : 0.0f) + s;
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
+    using C = Kv4Cfg<D, NT>;
+    auto kern = kv4_fwd_kernel<D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(p.ctas), kThreads4, C::kSmemBytes, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
+    const int join = static_cast<int>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+    const long long keys = p.logits == nullptr ? 0
+                                               : static_cast<long long>(p.c.B) * p.c.H_kv *
+                                                     ((p.c.capacity + kJoinKeys - 1) / kJoinKeys);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(join + keys));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D>, p, C::kRows, join);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+int kv4_rows_per_block(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+int kv4_max_ctas(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms) {
+    const int64_t rpb = kv4_rows_per_block(rows);
+    const int64_t slabs = B * H_kv * ((rows + rpb - 1) / rpb) * (capacity / kSlab);
+    const int64_t most = static_cast<int64_t>(sms) * (rpb == 8 ? 2 : 1);
+    const int64_t want = (slabs + kWarps - 1) / kWarps;
+    return static_cast<int>(want < most ? want : most);
+}
+
+cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, cudaStream_t stream) {
+    if (kv4_rows_per_block(p.rows) == 8)
+        return p.c.d == 128 ? launch_variant<128, 1>(p, stream) : launch_variant<64, 1>(p, stream);
+    return p.c.d == 128 ? launch_variant<128, 2>(p, stream) : launch_variant<64, 2>(p, stream);
+}
+
+}  // namespace fa
