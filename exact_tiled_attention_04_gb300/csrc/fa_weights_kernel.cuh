@@ -1,0 +1,325 @@
+// Attention weight received by the keys of a prompt, sm_103a (include/fa.h,
+// fa_fwd_weights):
+//
+//   w[j] = sum over rows i of 2^(c s_ij - lse2_i),  s = q_i . k_j
+//
+// the column sums of the attention map that the forward pass (whose lse it
+// takes) never writes; the map is recomputed tile by tile as the backward
+// pass does ("FlashAttention dissected", section "Memory complexity: from
+// O(N^2) to O(N)").
+//
+// The keys sit on the 128 tensor-memory lanes (S^T = K Q^T), so a thread
+// owns a key and its sum runs along the thread's own columns: no reduction
+// across threads, no atomics, one fixed order of additions.  A step's 128
+// terms are added first and then added to the running sum, which keeps the
+// rounding of a sum over 10^5 rows near 2^-22 of it.
+//
+// One CTA owns 256 keys of one key/value head (two tiles of 128, resident in
+// shared memory, so a query tile that was loaded serves two products) and
+// sweeps the rows of the head's query heads, 128 a step:
+//   warps 0-15  four warpgroups: key tile w % 2, steps of parity w / 2; each
+//               owns one 128-column buffer of tensor memory
+//   warp 16     tensor-core issuer (one thread) and tensor-memory owner
+//   warp 17     TMA producer
+// Bound by the exponentials and the products alike: 128 x 128 scores take 512
+// clocks of each at d = 128 (32 exponentials a clock and SM), half of the
+// latter at d = 64.
+//
+// Causal: the rows below a tile's diagonal are swept from the first one that
+// sees any of its keys; only the first steps are masked.  When the key blocks
+// do not fill the GPU, the CTAs of one thread-block cluster share the steps
+// of a key block and add their sums in order through distributed shared
+// memory.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "fa_fwd_kernel.cuh"
+#include "fa_kv4.h"
+
+namespace fa {
+
+constexpr int kWtWarpgroups = 4;
+constexpr int kWtSoftmaxWarps = 4 * kWtWarpgroups;
+constexpr int kWtMmaWarp = kWtSoftmaxWarps;
+constexpr int kWtLoadWarp = kWtMmaWarp + 1;
+constexpr int kWtThreads = (kWtLoadWarp + 1) * 32;
+
+template <int D, bool F16>
+struct WtCfg {
+    static constexpr int kAtoms = D / 64;
+    static constexpr int kAtomBytes = 128 * 128;
+    static constexpr int kTileBytes = kAtoms * kAtomBytes;
+    static constexpr int kSteps = D / 16;
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr uint32_t kFmt = F16 ? 0u : 1u;
+    static constexpr uint32_t kIdesc = instr_desc(kFmt, false, false, 128, 128);
+    static constexpr int kOffK = 0;                                  // two tiles
+    static constexpr int kOffQ = kOffK + 2 * kTileBytes;             // [kStages]
+    static constexpr int kOffLse = kOffQ + kStages * kTileBytes;     // float [warpgroup][2][128]
+    static constexpr int kOffSum = kOffLse + kWtWarpgroups * 2 * 128 * 4;  // float [warpgroup][128]
+    static constexpr int kOffBar = kOffSum + kWtWarpgroups * 128 * 4;
+    static constexpr int kBarK = 0;
+    static constexpr int kBarFull = 1;                    // [kStages] a query tile landed
+    static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] its products are done
+    static constexpr int kBarS = kBarEmpty + kStages;     // [4] scores ready
+    static constexpr int kBarSFree = kBarS + 4;           // [4] scores read
+    static constexpr int kBarDrain = kBarSFree + 4;
+    static constexpr int kNumBars = kBarDrain + 1;
+    static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
+    static constexpr int kOffAbort = kOffTmemSlot + 4;
+    static constexpr size_t kSmemBytes = static_cast<size_t>(kOffAbort + 4) + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
+};
+
+// grid = B * H_kv * ceil(N_kv / 256) * p.splits, clusters of p.splits.
+template <int D, bool F16>
+__global__ void __launch_bounds__(kWtThreads, 1)
+    fa_weights_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const WeightsParams p) {
+    using C = WtCfg<D, F16>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_u32 & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw_u32 + pad;
+    const int warp = static_cast<int>(threadIdx.x) / 32, lane = static_cast<int>(threadIdx.x) % 32;
+
+    const int n_blocks = (p.Nkv + 255) / 256;
+    const unsigned int split = blockIdx.x % static_cast<unsigned>(p.splits);
+    const unsigned int item = blockIdx.x / static_cast<unsigned>(p.splits);
+    int kvh, block;  // causal: a head's first key block is its heaviest
+    if (p.causal) {
+        lpt_item(item, static_cast<int>(gridDim.x) / p.splits / n_blocks, n_blocks, kvh, block);
+    } else {
+        kvh = static_cast<int>(item / static_cast<unsigned>(n_blocks));
+        block = static_cast<int>(item % static_cast<unsigned>(n_blocks));
+    }
+    const int key0 = block * 256;
+    const int tiles = p.Nkv - key0 > 128 ? 2 : 1;
+    // rows first_row .. Nq - 1 of every query head, 128 a step
+    int first_row = p.first_query;
+    if (p.causal) first_row = max(first_row, min(key0 - p.causal_offset, p.Nq));
+    const int per_head = (p.Nq - first_row + 127) / 128;
+    const int all = per_head * p.group;
+    const int share = (all + p.splits - 1) / p.splits;
+    const int begin = min(static_cast<int>(split) * share, all);
+    const int T = min(share, all - begin);
+    const long long head0 = static_cast<long long>(kvh / p.H_kv) * p.H + static_cast<long long>(kvh % p.H_kv) * p.group;
+
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(i); };
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
+    FwdParams wp;  // what a bounded wait reports to
+    wp.status = p.status;
+    wp.gen = p.gen;
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(C::kBarK), 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar(C::kBarFull + s), 1);
+            mbar_init(bar(C::kBarEmpty + s), 1);
+        }
+        for (int b = 0; b < 4; ++b) {
+            mbar_init(bar(C::kBarS + b), 1);
+            mbar_init(bar(C::kBarSFree + b), 4);
+        }
+        mbar_init(bar(C::kBarDrain), 1);
+        *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
+        mbar_init_fence();
+    }
+    if (warp == kWtMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool skip = *abort_flag != 0u;
+
+    if (warp == kWtLoadWarp) {
+        if (lane == 0 && T > 0 && !skip) {
+            const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+            mbar_arrive_expect_tx(bar(C::kBarK), static_cast<uint32_t>(tiles) * C::kTileBytes);
+            for (int i = 0; i < tiles; ++i)
+                for (int a = 0; a < C::kAtoms; ++a)
+                    tma_load_3d(sbase + C::kOffK + i * C::kTileBytes + a * C::kAtomBytes, &map_k, bar(C::kBarK), a * 64,
+                                key0 + 128 * i, kvh, once);
+            int issued = 0;
+            for (int j = 0; j < T; ++j) {
+                const int s = j % C::kStages;
+                if (!wait_phase(bar(C::kBarEmpty + s), ((j / C::kStages) & 1) ^ 1, abort_flag, wp, 90)) break;
+                const int step = begin + j, h = step / per_head;
+                mbar_arrive_expect_tx(bar(C::kBarFull + s), C::kTileBytes);
+                for (int a = 0; a < C::kAtoms; ++a)
+                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q, bar(C::kBarFull + s),
+                                a * 64, first_row + 128 * (step - h * per_head), static_cast<int>(head0) + h, keep);
+                issued = j + 1;
+            }
+            wait_phase(bar(C::kBarK), 0, abort_flag, wp, 91, false);
+            for (int s = 0; s < C::kStages && s < issued; ++s) {
+                const int last = s + ((issued - 1 - s) / C::kStages) * C::kStages;
+                wait_phase(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, wp, 92, false);
+            }
+        }
+    } else if (warp == kWtMmaWarp) {
+        if (lane == 0 && T > 0 && !skip) {
+            bool ok = wait_phase(bar(C::kBarK), 0, abort_flag, wp, 93);
+            for (int j = 0; ok && j < T; ++j) {
+                const int s = j % C::kStages;
+                ok = wait_phase(bar(C::kBarFull + s), (j / C::kStages) & 1, abort_flag, wp, 94);
+                for (int i = 0; ok && i < tiles; ++i) {
+                    const int b = (j & 1) * 2 + i;
+                    ok = wait_phase(bar(C::kBarSFree + b), ((j >> 1) & 1) ^ 1, abort_flag, wp, 95);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < C::kSteps; ++kk) {
+                        const uint32_t off = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
+                        mma_ss<false>(tmem + 128u * b,
+                                      smem_desc_sw128(sbase + C::kOffK + i * C::kTileBytes + off, 16, 1024),
+                                      smem_desc_sw128(sbase + C::kOffQ + s * C::kTileBytes + off, 16, 1024), C::kIdesc,
+                                      kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(bar(C::kBarS + b));
+                }
+                if (ok) tc_commit(bar(C::kBarEmpty + s));
+            }
+            tc_commit(bar(C::kBarDrain));
+            wait_phase(bar(C::kBarDrain), 0, abort_flag, wp, 96, false);
+        }
+    } else {
+        const int wg = warp / 4, t = static_cast<int>(threadIdx.x) % 128;
+        const int tile = wg % 2, parity = wg / 2;
+        const int b = parity * 2 + tile;
+        const int key = key0 + 128 * tile + t;
+        const uint32_t tS = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 128u * b;
+        float* neg = reinterpret_cast<float*>(smem + C::kOffLse) + wg * 256;
+        float total = 0.0f;
+        if (tile < tiles && !skip) {
+            // -lse2 of row t of step j; -inf where the row counts nothing
+            auto row_neg = [&](int j) -> float {
+                if (j >= T) return 0.0f;
+                const int step = begin + j, h = step / per_head;
+                const int row = first_row + 128 * (step - h * per_head) + t;
+                if (row >= p.Nq) return -INFINITY;
+                const float v = __ldg(p.lse + (head0 + h) * p.Nq + row);
+                return v == -INFINITY ? -INFINITY : v * -1.4426950408889634f;
+            };
+            const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+            float next = row_neg(parity);
+            bool ok = true;
+            for (int j = parity; j < T; j += 2) {
+                float* buf = neg + ((j >> 1) & 1) * 128;
+                buf[t] = next;
+                next = row_neg(j + 2);
+                named_barrier_sync(1 + wg, 128);
+                ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarS + b), (j >> 1) & 1, abort_flag, wp, 97));
+                // a warp that gave up keeps meeting the barrier above
+                if (!ok) continue;
+                tc_fence_after();
+                int first_col = 0;  // first row of this step that sees the key
+                if (p.causal) {
+                    const int step = begin + j;
+                    first_col = key - p.causal_offset - first_row - 128 * (step - step / per_head * per_head);
+                }
+                const bool masked = __any_sync(0xffffffffu, first_col > 0);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t r[32];
+                    tmem_ld32(tS + 32u * q, r);
+                    tmem_ld_wait(r);
+                    if (q == 3) {  // the scores are in registers: the next product may start
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::kBarSFree + b));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 n4 = *reinterpret_cast<const float4*>(buf + 32 * q + i);
+                        float x[4];
+                        f2_unpack(f2_fma(f2_pack(u2f(r[i]), u2f(r[i + 1])), c2, f2_pack(n4.x, n4.y)), x[0], x[1]);
+                        f2_unpack(f2_fma(f2_pack(u2f(r[i + 2]), u2f(r[i + 3])), c2, f2_pack(n4.z, n4.w)), x[2], x[3]);
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (32 * q + i + e < first_col) x[e] = -INFINITY;
+                        }
+                        sum[0] = f2_add(sum[0], f2_pack(ex2(x[0]), ex2(x[1])));
+                        sum[1] = f2_add(sum[1], f2_pack(ex2(x[2]), ex2(x[3])));
+                    }
+                }
+                float a0, a1;
+                f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
+                total += a0 + a1;
+            }
+        }
+        reinterpret_cast<float*>(smem + C::kOffSum)[wg * 128 + t] = total;
+    }
+    tc_fence_before();
+    if (p.splits > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    // two warpgroups and every CTA of the cluster add up in order
+    if (split == 0 && threadIdx.x < 256) {
+        const int tile = static_cast<int>(threadIdx.x) / 128, t = static_cast<int>(threadIdx.x) % 128;
+        const int key = key0 + 128 * tile + t;
+        if (key < p.Nkv) {
+            const long long at = static_cast<long long>(kvh) * p.weight_stride + key;
+            float s = 0.0f;
+            for (int r = 0; r < p.splits; ++r)
+                for (int half = 0; half < 2; ++half) {
+                    const int i = (half * 2 + tile) * 128 + t;
+                    float v;
+                    if (p.splits > 1)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(v)
+                                     : "r"(mapa_shared(sbase + C::kOffSum + 4u * static_cast<uint32_t>(i),
+                                                       static_cast<uint32_t>(r)))
+                                     : "memory");
+                    else
+                        v = reinterpret_cast<float*>(smem + C::kOffSum)[i];
+                    s += v;
+                }
+            p.weight_out[at] = (p.weight_in != nullptr ? p.weight_in[at] : 0.0f) + s;
+        }
+    }
+    if (p.splits > 1)
+        cluster_sync_all();  // no CTA leaves while its sums may be read
+    else
+        __syncthreads();
+    if (warp == kWtMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool F16>
+cudaError_t launch_weights_variant(const CUtensorMap& q, const CUtensorMap& k, const WeightsParams& p,
+                                   unsigned int grid, cudaStream_t stream) {
+    using C = WtCfg<D, F16>;
+    auto kern = fa_weights_kernel<D, F16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(C::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kWtThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kern, q, k, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace fa
