@@ -164,7 +164,9 @@ bool fwd_layout(int64_t B, int64_t H, int64_t H_kv, int64_t N_q, int64_t capacit
     const int64_t rows = N_q * group, all = mul(mul(B, H_kv), rows);
     const int64_t logits = mul(mul(B, H_kv), mul(capacity, rows * 4));
     const int64_t chunks = mul(B * H_kv, (capacity + 1023) / 1024);
-    // the second kernel's grid: a warp per row, and a block per 1024 slots
+    // the slabs of 32 slots over all blocks of 8 rows; the second kernel's grid: a warp per row, a block per 1024 slots
+    const int64_t slabs = mul(mul(B * H_kv, (rows + 7) / 8), capacity / 32);
+    if (slabs < 0 || slabs > kInt32Max / 2) return false;
     if (all < 0 || all > kInt32Max || logits < 0 || chunks < 0 || chunks > kInt32Max / 2) return false;
     l->ctas = fa::kv4_max_ctas(B, H_kv, rows, capacity, sms > 0 ? sms : 1024);
     const size_t rpb = static_cast<size_t>(fa::kv4_rows_per_block(rows));

@@ -61,7 +61,9 @@ struct Kv4Cfg {
     static constexpr int kOffRing = 0;                  // [warps][stages][slab]
     static constexpr int kOffO = kOffRing + kWarps * kStages * kSlabBytes;  // float [warps][kRegs][32]
     static constexpr int kOffMl = kOffO + kWarps * kRegs * 32 * 4;          // float [warps][kRows][4]
-    static constexpr int kOffBar = kOffMl + kWarps * kRows * 4 * 4;
+    static constexpr int kOffQ = kOffMl + kWarps * kRows * 4 * 4;           // uint4 [NT][D / 32][32]
+    static constexpr int kOffC = kOffQ + NT * (D / 32) * 32 * 16;           // float [kRows]: score factors
+    static constexpr int kOffBar = kOffC + kRows * 4;
     static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
     static constexpr int kSmemBytes = kOffAbort + 16;
     static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
@@ -115,90 +117,74 @@ __device__ __forceinline__ int kv4_length(const Kv4Cache& c, int b) {
 }
 __device__ __forceinline__ int slabs_of(int len) { return (len + kSlab - 1) / kSlab; }
 
-// Sum over sequences [0, stop) of their slabs x units, by a warp (every lane
-// gets it); *all gets the sum over all sequences.
-__device__ __forceinline__ long long slabs_before(const Kv4Cache& c, int units, int stop, long long* all) {
-    const int lane = threadIdx.x % 32;
-    long long before = 0, total = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-        const int b = b0 + lane;
-        const long long n = b < c.B ? static_cast<long long>(slabs_of(kv4_length(c, b))) * units : 0;
-        total += n;
-        if (b < stop) before += n;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o /= 2) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    *all = total;
-    return before;
-}
+// The slabs of all units fit 31 bits (the host checks it), so positions in
+// them are ints.
+//
 // Slabs per CTA: equal runs, at least one slab for every warp.
-__device__ __forceinline__ long long slabs_per_cta(long long total, int ctas) {
-    const long long per = (total + ctas - 1) / ctas;
+__device__ __forceinline__ int slabs_per_cta(int total, int ctas) {
+    const int per = (total + ctas - 1) / ctas;
     return per < kWarps ? kWarps : per;
 }
 
 // Position in a CTA's run of slabs.
 struct Cursor {
-    long long pos, end;  // in slabs over all units
-    long long base;      // first slab of sequence b
-    int b, len, slabs;   // sequence, its length and the slabs of one of its units
-    int unit;            // unit of sequence b
-    int s0, s1;          // slabs of that unit in this run
+    int pos, end;       // in slabs over all units
+    int base;           // first slab of sequence b
+    int b, len, slabs;  // sequence, its length and the slabs of one of its units
+    int unit;           // unit of sequence b
+    int s0, s1;         // slabs of that unit in this run
 
-    __device__ __forceinline__ void locate(const Kv4Cache& c, int units) {
-        while (pos < end && pos >= base + static_cast<long long>(slabs) * units) {
-            base += static_cast<long long>(slabs) * units;
-            ++b;
-            len = kv4_length(c, b);
-            slabs = slabs_of(len);
-        }
-        if (pos < end) {
-            const long long off = pos - base;
-            unit = static_cast<int>(off / slabs);
-            s0 = static_cast<int>(off - static_cast<long long>(unit) * slabs);
-            s1 = static_cast<int>(min(static_cast<long long>(slabs), s0 + (end - pos)));
-        }
-    }
     __device__ __forceinline__ bool valid() const { return pos < end; }
     __device__ __forceinline__ void next(const Kv4Cache& c, int units) {
         pos += s1 - s0;
-        locate(c, units);
+        if (pos >= end) return;
+        s0 = 0;
+        if (++unit == units) {  // the next sequence that has any slab
+            unit = 0;
+            base += slabs * units;
+            do {
+                len = kv4_length(c, ++b);
+                slabs = slabs_of(len);
+            } while (slabs == 0);
+        }
+        s1 = min(slabs, end - pos);
     }
     __device__ __forceinline__ void start(const Kv4Cache& c, int units, int ctas, int cta) {
-        long long total;
-        slabs_before(c, units, 0, &total);
-        const long long per = slabs_per_cta(total, ctas);
-        pos = min(total, per * cta);
-        end = min(total, pos + per);
-        base = 0;
-        b = 0;
-        unit = s0 = s1 = 0;
-        // the sequence that holds `pos`, 32 sequences at a time
         const int lane = threadIdx.x % 32;
+        const int len0 = lane < c.B ? kv4_length(c, lane) : 0;  // the first 32 sequences: all, mostly
+        int total = slabs_of(len0) * units;
+        for (int x = 32 + lane; x < c.B; x += 32) total += slabs_of(kv4_length(c, x)) * units;
+        total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total)));
+        const int per = slabs_per_cta(total, ctas);
+        pos = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(per) * cta));
+        end = min(total - pos, per) + pos;
+        base = b = len = slabs = unit = s0 = s1 = 0;
+        // the sequence that holds `pos`, 32 sequences at a time
         for (int b0 = 0; pos < end && b0 < c.B; b0 += 32) {
-            const long long n =
-                b0 + lane < c.B ? static_cast<long long>(slabs_of(kv4_length(c, b0 + lane))) * units : 0;
-            long long incl = n;
+            const int mine = b0 == 0 ? len0 : b0 + lane < c.B ? kv4_length(c, b0 + lane) : 0;
+            const int n = slabs_of(mine) * units;
+            int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
             const uint32_t past = __ballot_sync(0xffffffffu, base + incl > pos);
             if (past) {
                 const int who = __ffs(static_cast<int>(past)) - 1;
                 base += __shfl_sync(0xffffffffu, incl - n, who);
+                len = __shfl_sync(0xffffffffu, mine, who);
+                slabs = slabs_of(len);
                 b = b0 + who;
                 break;
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
-        len = kv4_length(c, b);
-        slabs = slabs_of(len);
-        locate(c, units);
+        if (pos < end) {
+            unit = (pos - base) / slabs;
+            s0 = pos - base - unit * slabs;
+            s1 = min(slabs, s0 + (end - pos));
+        }
     }
 };
 
@@ -216,11 +202,15 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     auto bar = [&](int s) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(warp * C::kStages + s); };
     uint8_t* ring = smem + C::kOffRing + warp * C::kStages * C::kSlabBytes;
 
-    if (lane == 0)
+    if (lane == 0) {
         for (int s = 0; s < C::kStages; ++s) mbar_init(bar(s), 1);
+        mbar_init_fence();  // a warp's barriers are its own
+    }
     if (threadIdx.x == 0) *abort_flag = 0u;
-    mbar_init_fence();
-    __syncthreads();
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second kernel waits by itself
 
     const int units = p.c.H_kv * p.row_blocks;
     Cursor load;
@@ -228,28 +218,39 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     Cursor cur = load;
     const uint64_t once = policy_evict_first();  // every byte is read once per block of rows
 
-    // ---- producer side of this warp: slabs s0 + warp, + 8, .. of each unit
-    int load_slab = cur.s0 + warp;
+    // Slabs are dealt to the warps in turn over the CTA's whole run, so that a
+    // unit's end leaves no warp a slab behind the others.
+    const int run0 = cur.pos;
+    auto first_slab = [&](const Cursor& u) -> int {
+        return u.s0 + ((warp - (u.pos - run0)) & (kWarps - 1));
+    };
+    // ---- producer side of this warp: lanes 0 .. 3 copy one array each
     int issued = 0;  // slabs asked for so far; slab i uses stage i % kStages
+    int load_slab = 0, load_end = 0;
+    const uint8_t* load_from = nullptr;
+    const uint8_t* const load_base = lane == 0   ? p.c.codes[0]
+                                     : lane == 1 ? p.c.codes[1]
+                                     : lane == 2 ? p.c.scales[0]
+                                                 : p.c.scales[1];
+    const uint32_t load_bytes = lane < 2 ? C::kCodeBytes : C::kScaleBytes;
+    const uint32_t load_to = sbase + C::kOffRing + warp * C::kStages * C::kSlabBytes +
+                             (lane < 2 ? lane * C::kCodeBytes : 2 * C::kCodeBytes + (lane - 2) * C::kScaleBytes);
     auto issue = [&]() {
-        while (load.valid() && load_slab >= load.s1) {
-            load.next(p.c, units);
-            load_slab = load.s0 + warp;
-        }
-        if (!load.valid()) return;
-        if (lane == 0) {
-            const int s = issued % C::kStages;
+        while (load_slab >= load_end) {
+            if (!load.valid()) return;
+            load_slab = first_slab(load);
+            load_end = load.s1;
             const long long row =
                 (static_cast<long long>(load.b) * p.c.H_kv + load.unit / p.row_blocks) * p.c.capacity +
                 static_cast<long long>(load_slab) * kSlab;
-            const uint32_t dst = sbase + C::kOffRing + (warp * C::kStages + s) * C::kSlabBytes;
-            mbar_arrive_expect_tx(bar(s), C::kSlabBytes);
-            bulk_load(dst, p.c.codes[0] + row * (D / 2), C::kCodeBytes, bar(s), once);
-            bulk_load(dst + C::kCodeBytes, p.c.codes[1] + row * (D / 2), C::kCodeBytes, bar(s), once);
-            bulk_load(dst + 2 * C::kCodeBytes, p.c.scales[0] + row * (D / 16), C::kScaleBytes, bar(s), once);
-            bulk_load(dst + 2 * C::kCodeBytes + C::kScaleBytes, p.c.scales[1] + row * (D / 16), C::kScaleBytes, bar(s),
-                      once);
+            load_from = load_base + row * (lane < 2 ? D / 2 : D / 16);
+            load.next(p.c, units);
         }
+        const int s = issued % C::kStages;
+        if (lane == 0) mbar_arrive_expect_tx(bar(s), C::kSlabBytes);
+        __syncwarp();
+        if (lane < 4) bulk_load(load_to + s * C::kSlabBytes, load_from, load_bytes, bar(s), once);
+        load_from += kWarps * load_bytes;
         ++issued;
         load_slab += kWarps;
     };
@@ -263,21 +264,20 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     for (; cur.valid(); cur.next(p.c, units)) {
         const int kvh = cur.b * p.c.H_kv + cur.unit / p.row_blocks;
         const int row0 = (cur.unit % p.row_blocks) * C::kRows;  // of the head's rows
-        // ---- q fragments: lane (g, t) holds channels (D / 4) t .. of rows g + 8 nt, scaled
-        uint32_t q[NT][D / 16][2];
-        float c[NT][2];  // score factor of rows 2t, 2t + 1
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = row0 + 8 * nt + g;
+        // ---- q fragments: lane (g, t) holds channels (D / 4) t .. of rows g + 8 nt, scaled; warp nt
+        // prepares them for the block
+        uint4* sm_q = reinterpret_cast<uint4*>(smem + C::kOffQ);
+        float* sm_c = reinterpret_cast<float*>(smem + C::kOffC);
+        if (warp < NT) {
+            const int r = row0 + 8 * warp + g;
             uint4 raw[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
             if (r < p.rows) {
                 const uint4* src = reinterpret_cast<const uint4*>(
                     static_cast<const uint16_t*>(p.q) + (static_cast<long long>(kvh) * p.rows + r) * D + t * (D / 4));
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(src + i);
-            } else {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = 0; i < D / 32; ++i) raw[i] = src[i];
             }
             uint32_t m = 0u;
 #pragma unroll
@@ -296,29 +296,36 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float lo = p.f16 ? widen_lo16<true>(w[j]) : widen_lo16<false>(w[j]);
                     const float hi = p.f16 ? widen_lo16<true>(w[j] >> 16) : widen_lo16<false>(w[j] >> 16);
-                    // word j of 16 bytes: channels 8 i + 2 j, + 1: step 2 i + j / 2, half j % 2
-                    q[nt][2 * i + j / 2][j & 1] = pack_f16x2(lo * up, hi * up);
+                    h[j] = pack_f16x2(lo * up, hi * up);
                 }
+                // words 0, 1: the two halves of step 2 i; 2, 3: of step 2 i + 1
+                sm_q[(warp * (D / 32) + i) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
             }
-            const float f = p.scale_log2 * down;
-            c[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
-            c[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+            if (t == 0) sm_c[8 * warp + g] = p.scale_log2 * down;
         }
+        __syncthreads();
+        float c[NT][2];  // score factor of rows 2t, 2t + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            c[nt][0] = sm_c[8 * nt + 2 * t];
+            c[nt][1] = sm_c[8 * nt + 2 * t + 1];
+        }
+        // ref: the exponent's reference (base 2), set by the warp's first slab of the unit
         float ref[NT][2], l[NT][2], lq[NT][4], o[NT][C::kMt][4];
-        int lim[NT][2];  // slots rows 2t, 2t + 1 see
+        // slots that row 8 nt + 2 t + i sees
+        auto limit = [&](int nt, int i) -> int {
+            const int r = row0 + 8 * nt + 2 * t + i;
+            return cur.len - (p.causal && r < p.rows ? p.Nq - 1 - r % p.Nq : 0);
+        };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = row0 + 8 * nt + 2 * t + i;
-                ref[nt][i] = -INFINITY;
-                l[nt][i] = 0.0f;
-                lim[nt][i] = cur.len - (p.causal && r < p.rows ? p.Nq - 1 - r % p.Nq : 0);
-            }
+            for (int i = 0; i < 2; ++i) ref[nt][i] = l[nt][i] = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 lq[nt][i] = 0.0f;
@@ -328,9 +335,12 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
         }
         const int all_see = cur.len - (p.causal ? p.Nq - 1 : 0);  // slots every row sees
         float* logits = p.logits == nullptr ? nullptr
-                                            : p.logits + static_cast<long long>(kvh) * p.c.capacity * p.rows + row0;
+                                            : p.logits + static_cast<long long>(kvh) * p.c.capacity * p.rows + row0 + 2 * t;
+        // rows 2t, 2t + 1 as one store: both exist and every slot's rows start on an even one
+        const bool pairs = p.rows % 2 == 0;
 
-        for (int slab = cur.s0 + warp; ok && slab < cur.s1; slab += kWarps) {
+        const int slab0 = first_slab(cur);
+        for (int slab = slab0; ok && slab < cur.s1; slab += kWarps) {
             const int s = used % C::kStages;
             ok = __all_sync(0xffffffffu, wait_phase(bar(s), (used / C::kStages) & 1, abort_flag, wp, 80));
             if (!ok) break;
@@ -379,46 +389,40 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(x[h][nt], ha[0], hb[0], ha[1], hb[1], q[nt][2 * w][0], q[nt][2 * w][1]);
-                        mma_f16(x[h][nt], ha[2], hb[2], ha[3], hb[3], q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+                        const uint4 q = sm_q[(nt * (D / 32) + w) * 32 + lane];
+                        mma_f16(x[h][nt], ha[0], hb[0], ha[1], hb[1], q.x, q.y);
+                        mma_f16(x[h][nt], ha[2], hb[2], ha[3], hb[3], q.z, q.w);
                     }
                 }
             }
-            // ---- scaled scores (base 2); hidden slots are -inf whatever is stored there
+            // ---- exponents (base 2) against the reference; hidden slots are -inf whatever is stored there
+            float top = -INFINITY;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[h][nt][i] *= c[nt][i & 1];
-                        if (masked && key0 + 16 * h + kg + 8 * (i >> 1) >= lim[nt][i & 1]) x[h][nt][i] = -INFINITY;
-                    }
-            if (logits != nullptr) {
+                    for (int i = 0; i < 4; ++i) x[h][nt][i] = fmaf(x[h][nt][i], c[nt][i & 1], -ref[nt][i & 1]);
+            if (masked) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        const int key = key0 + 16 * h + kg + 8 * i2;
-                        if (key < cur.len) {
-                            float* dst = logits + static_cast<long long>(key) * p.rows;
+                    for (int i = 0; i < 2; ++i) {
+                        const int lim = limit(nt, i) - key0 - kg;
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const int r = 8 * nt + 2 * t;
-                                if (row0 + r < p.rows) dst[r] = x[h][nt][2 * i2];
-                                if (row0 + r + 1 < p.rows) dst[r + 1] = x[h][nt][2 * i2 + 1];
-                            }
+                        for (int h = 0; h < 2; ++h) {
+                            if (16 * h >= lim) x[h][nt][i] = -INFINITY;
+                            if (16 * h + 8 >= lim) x[h][nt][i + 2] = -INFINITY;
                         }
                     }
             }
-            bool grow = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) grow |= x[h][nt][i] > ref[nt][i & 1] + kGrow;
-            if (__any_sync(0xffffffffu, grow)) {
+                for (int i = 0; i < 4; ++i) top = fmax3(top, x[0][nt][i], x[1][nt][i]);
+            // the first slab sets the reference (nothing to rescale); later ones move it when a weight would
+            // pass fp16's range
+            if (slab == slab0 || __any_sync(0xffffffffu, top > kGrow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -426,17 +430,47 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
                         float m = fmaxf(fmaxf(x[0][nt][i], x[0][nt][i + 2]), fmaxf(x[1][nt][i], x[1][nt][i + 2]));
 #pragma unroll
                         for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                        const float nr = fmaxf(ref[nt][i], m - kRefShift);
-                        // -inf: nothing seen yet (and nothing to rescale)
-                        const float alpha = nr == -INFINITY ? 1.0f : ex2(ref[nt][i] - nr);
-                        ref[nt][i] = nr;
-                        l[nt][i] *= alpha;
-                        lq[nt][i] *= alpha;
+                        // a row that sees none of a first slab sees none of the warp's later ones either
+                        float shift = m == -INFINITY ? 0.0f : m - kRefShift;
+                        if (slab != slab0) {
+                            shift = fmaxf(shift, 0.0f);
+                            const float alpha = ex2(-shift);
+                            l[nt][i] *= alpha;
+                            lq[nt][i] *= alpha;
 #pragma unroll
-                        for (int mt = 0; mt < C::kMt; ++mt) {
-                            o[nt][mt][i] *= alpha;
-                            o[nt][mt][i + 2] *= alpha;
+                            for (int mt = 0; mt < C::kMt; ++mt) {
+                                o[nt][mt][i] *= alpha;
+                                o[nt][mt][i + 2] *= alpha;
+                            }
                         }
+                        ref[nt][i] += shift;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            x[h][nt][i] -= shift;
+                            x[h][nt][i + 2] -= shift;
+                        }
+                    }
+            }
+            if (logits != nullptr) {
+                float* dst = logits + static_cast<long long>(key0 + kg) * p.rows;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        if (!masked || key0 + kg + 16 * h + 8 * i2 < cur.len) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const int left = p.rows - row0 - 8 * nt - 2 * t;  // rows from 2t on
+                                const float y0 = x[h][nt][2 * i2] + ref[nt][0], y1 = x[h][nt][2 * i2 + 1] + ref[nt][1];
+                                if (pairs && left > 0) {
+                                    *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(y0, y1);
+                                } else {
+                                    if (left > 0) dst[8 * nt] = y0;
+                                    if (left > 1) dst[8 * nt + 1] = y1;
+                                }
+                            }
+                        }
+                        dst += 8 * p.rows;
                     }
             }
             // ---- weights, O^T += V^T P^T
@@ -448,9 +482,7 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
                     float w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // a row that has seen nothing has ref = -inf and x = -inf (or NaN): 2^(-inf - 0)
-                        const float r = ref[nt][i & 1] == -INFINITY ? 0.0f : ref[nt][i & 1];
-                        w[i] = ex2(x[h][nt][i] - r);
+                        w[i] = ex2(x[h][nt][i]);
                         l[nt][i & 1] += w[i];
                     }
                     pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
@@ -491,7 +523,7 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
                                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                         for (int j = 0; j < 2; ++j)
-                                            if (key0 + 16 * h + 4 * i + u < lim[nt][j]) {
+                                            if (key0 + 16 * h + 4 * i + u < limit(nt, j)) {
 #pragma unroll
                                                 for (int mt = 0; mt < C::kMt; ++mt)
                                                     o[nt][mt][j] = o[nt][mt][j + 2] = __int_as_float(0x7FC00000);
@@ -540,7 +572,7 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
                 for (int off = 4; off < 32; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
                 if (g == 0)
                     *reinterpret_cast<float4*>(sm_ml + (warp * C::kRows + 8 * nt + 2 * t + i) * 4) =
-                        make_float4(ref[nt][i], s, lq[nt][i], 0.0f);
+                        make_float4(s == 0.0f ? -INFINITY : ref[nt][i], s, lq[nt][i], 0.0f);
             }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -624,35 +656,48 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
 // Where a unit's partial results are: CTAs first .. last of the main kernel,
 // slot 1 of the first and slot 0 of the others.
 struct Parts {
-    int slabs;
-    long long first, last;
+    int slabs, first, last;
 };
-__device__ __forceinline__ Parts parts_of(const Kv4FwdParams& p, int b, int unit) {
-    const int units = p.c.H_kv * p.row_blocks;
-    long long total;
-    const long long base = slabs_before(p.c, units, b, &total);
-    const long long per = slabs_per_cta(total, p.ctas);
+// Slabs of the sequences before b, and of all, by a warp (every lane gets them).
+struct Spread {
+    int before, slabs, per;
+};
+__device__ __forceinline__ Spread spread_of(const Kv4FwdParams& p, int b) {
+    const int lane = threadIdx.x % 32, units = p.c.H_kv * p.row_blocks;
+    int before = 0, total = 0;
+    for (int x = lane; x < p.c.B; x += 32) {
+        const int n = slabs_of(kv4_length(p.c, x)) * units;
+        total += n;
+        if (x < b) before += n;
+    }
+    Spread s;
+    s.before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
+    s.per = slabs_per_cta(static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total))), p.ctas);
+    s.slabs = slabs_of(kv4_length(p.c, b));
+    return s;
+}
+__device__ __forceinline__ Parts parts_of(const Spread& s, int unit) {
     Parts r;
-    r.slabs = slabs_of(kv4_length(p.c, b));
-    const long long hs = base + static_cast<long long>(unit) * r.slabs;
-    r.first = hs / per;
-    r.last = r.slabs > 0 ? (hs + r.slabs - 1) / per : r.first;
+    r.slabs = s.slabs;
+    const int hs = s.before + unit * s.slabs;
+    r.first = hs / s.per;
+    r.last = s.slabs > 0 ? (hs + s.slabs - 1) / s.per : r.first;
     return r;
 }
-__device__ __forceinline__ long long part_row(long long cta, long long first, int rows, int r) {
-    return (cta * 2 + (cta == first ? 1 : 0)) * rows + r;
+__device__ __forceinline__ long long part_row(int cta, int first, int rows, int r) {
+    return (static_cast<long long>(cta) * 2 + (cta == first ? 1 : 0)) * rows + r;
 }
 // A row's reference, exact sum and rounded sum over its parts, by a warp.
 __device__ __forceinline__ void row_sums(const Kv4FwdParams& p, const Parts& u, int rows, int r, float& M, float& L,
                                          float& LQ) {
     const int lane = threadIdx.x % 32;
     M = -INFINITY;
-    for (long long c = u.first + lane; c <= u.last; c += 32)
+    for (int c = u.first + lane; c <= u.last; c += 32)
         M = fmaxf(M, p.part_ml[part_row(c, u.first, rows, r) * 4]);
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     L = LQ = 0.0f;
-    for (long long c = u.first + lane; c <= u.last; c += 32) {
+    for (int c = u.first + lane; c <= u.last; c += 32) {
         const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + part_row(c, u.first, rows, r) * 4);
         const float w = M == -INFINITY ? 1.0f : ex2(ml.x - M);
         L += w * ml.y;
@@ -675,28 +720,46 @@ constexpr int kMaxRows = 128;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdParams p, int rows_per_block,
                                                                  int join_blocks) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // started while the main kernel's last CTAs run: what that kernel does not
+    // write (it waited for what came before) is read ahead of the wait
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (static_cast<int>(blockIdx.x) < join_blocks) {
         const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + warp;
-        if (row >= static_cast<long long>(p.c.B) * p.c.H_kv * p.rows) return;
+        if (row >= static_cast<long long>(p.c.B) * p.c.H_kv * p.rows) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            return;
+        }
         const long long kvh = row / p.rows;
         const int r = static_cast<int>(row - kvh * p.rows);
         const int b = static_cast<int>(kvh / p.c.H_kv);
         const int unit = static_cast<int>(kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block;
-        const Parts u = parts_of(p, b, unit);
+        const Parts u = parts_of(spread_of(p, b), unit);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         if (u.slabs > 0 && u.first == u.last) return;  // the main kernel wrote it
         constexpr int kPer = D / 32;
         float acc[kPer] = {}, M = -INFINITY, L = 0.0f, LQ = 0.0f;
         if (u.slabs > 0) {
             const int rb = r % rows_per_block;
             row_sums(p, u, rows_per_block, rb, M, L, LQ);
-            for (long long c = u.first; c <= u.last; ++c) {
-                const long long at = part_row(c, u.first, rows_per_block, rb);
-                const float w = M == -INFINITY ? 1.0f : ex2(p.part_ml[at * 4] - M);
-                const float* src = p.part_o + at * D + lane * kPer;
+            // 32 parts' factors at a time, one per lane; four parts' rows in flight
+            for (int c0 = u.first; c0 <= u.last; c0 += 32) {
+                const int mine = c0 + lane;
+                float f = 0.0f;
+                if (mine <= u.last)
+                    f = M == -INFINITY ? 1.0f : ex2(p.part_ml[part_row(mine, u.first, rows_per_block, rb) * 4] - M);
+                const int n = min(32, u.last - c0 + 1);
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) {
+                    const float w = __shfl_sync(0xffffffffu, f, i);
+                    const float* src =
+                        p.part_o + part_row(c0 + i, u.first, rows_per_block, rb) * D + lane * kPer;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) acc[i] += w * src[i];
+                    for (int j = 0; j < kPer; j += 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(src + j);
+                        acc[j] += w * v.x;
+                        acc[j + 1] += w * v.y;
+                    }
+                }
             }
         }
         const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
@@ -709,13 +772,30 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
         return;
     }
     __shared__ float lse2[kMaxRows];
+    constexpr int kMine = kJoinKeys / kJoinThreads;  // keys per thread
     const int chunks = (p.c.capacity + kJoinKeys - 1) / kJoinKeys;
     const int i = static_cast<int>(blockIdx.x) - join_blocks;
     const int kvh = i / chunks, b = kvh / p.c.H_kv;
     const int key0 = (i % chunks) * kJoinKeys, len = kv4_length(p.c, b);
+    const Spread spread = spread_of(p, b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (key0 >= len) return;
+    const long long slot0 = static_cast<long long>(kvh) * p.c.capacity + key0 + threadIdx.x;
+    const int left = len - key0 - static_cast<int>(threadIdx.x);  // this thread's keys: 0, 256, .. below it
+    // four rows (a quarter of a 16-row block, the usual group) wait in registers for the rows' sums
+    float4 first4[kMine];
+    float old[kMine];
+    const bool four = p.rows % 4 == 0;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const long long at = slot0 + k * kJoinThreads;
+        const bool in = k * kJoinThreads < left;
+        old[k] = in && p.weight_in != nullptr ? p.weight_in[at] : 0.0f;
+        first4[k] = in && four ? *reinterpret_cast<const float4*>(p.logits + at * p.rows)
+                               : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
     for (int r = warp; r < p.rows; r += kJoinThreads / 32) {
-        const Parts u = parts_of(p, b, (kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block);
+        const Parts u = parts_of(spread, (kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block);
         float v;
         if (u.first == u.last) {
             v = p.row_lse2[static_cast<long long>(kvh) * p.rows + r];
@@ -727,12 +807,23 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
         if (lane == 0) lse2[r] = v == -INFINITY ? INFINITY : v;  // a row that sees nothing adds nothing
     }
     __syncthreads();
-    for (int key = key0 + threadIdx.x; key < min(key0 + kJoinKeys, len); key += kJoinThreads) {
-        const float* t = p.logits + (static_cast<long long>(kvh) * p.c.capacity + key) * p.rows;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        if (k * kJoinThreads >= left) break;
+        const long long at = slot0 + k * kJoinThreads;
+        const float* t = p.logits + at * p.rows;
         float s = 0.0f;
-        for (int r = 0; r < p.rows; ++r) s += ex2(t[r] - lse2[r]);
-        const long long at = static_cast<long long>(kvh) * p.c.capacity + key;
-        p.weight_out[at] = (p.weight_in != nullptr ? p.weight_in[at] : 0.0f) + s;
+        if (four) {
+            float4 y = first4[k];
+            for (int r = 0;;) {
+                s += (ex2(y.x - lse2[r]) + ex2(y.y - lse2[r + 1])) + (ex2(y.z - lse2[r + 2]) + ex2(y.w - lse2[r + 3]));
+                if ((r += 4) >= p.rows) break;
+                y = *reinterpret_cast<const float4*>(t + r);
+            }
+        } else {
+            for (int r = 0; r < p.rows; ++r) s += ex2(t[r] - lse2[r]);
+        }
+        p.weight_out[at] = old[k] + s;
     }
 }
 
@@ -742,22 +833,27 @@ cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
     auto kern = kv4_fwd_kernel<D, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(p.ctas), kThreads4, C::kSmemBytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // both kernels may be set up while the one before them in the stream runs; they wait for its end
+    // before they touch memory
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
+    cfg.blockDim = dim3(kThreads4);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
     const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
     const int join = static_cast<int>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
     const long long keys = p.logits == nullptr ? 0
                                                : static_cast<long long>(p.c.B) * p.c.H_kv *
                                                      ((p.c.capacity + kJoinKeys - 1) / kJoinKeys);
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(join + keys));
     cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D>, p, C::kRows, join);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
