@@ -70,7 +70,7 @@ struct Kv4FwdParams {
     int ctas;             // CTAs of the main kernel
     // workspace
     float* row_lse2;      // [B * H_kv * rows]: base-2 lse of the rows of units that one CTA finished
-    float* part_ml;       // [ctas, 2, rows_per_block, 4]
+    float4* part_ml;      // [ctas, 2, rows_per_block]: reference, exact sum, rounded sum
     float* part_o;        // [ctas, 2, rows_per_block, d]
     float* logits;        // [B * H_kv, capacity, rows] scaled, base 2, or nullptr
 };

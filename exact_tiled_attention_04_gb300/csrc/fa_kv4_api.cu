@@ -350,7 +350,7 @@ int fa_kv4_fwd(const fa_kv4_cache_t* cache, const void* q, void* o, float* lse, 
     p.ctas = l.ctas;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.row_lse2 = reinterpret_cast<float*>(ws);
-    p.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+    p.part_ml = reinterpret_cast<float4*>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float*>(ws + l.part_o);
     p.logits = weight_out != nullptr ? reinterpret_cast<float*>(ws + l.logits) : nullptr;
     return launched(fa::launch_kv4_fwd(p, static_cast<cudaStream_t>(stream)), "fa_kv4_fwd launch");

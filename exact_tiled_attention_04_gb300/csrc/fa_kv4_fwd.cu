@@ -29,7 +29,12 @@
 // shared by many.  A CTA whose run holds a whole unit writes its output; of
 // a unit cut between CTAs each leaves a partial result (at most two per CTA:
 // the unit it starts inside and the one it ends inside), which the second
-// kernel adds up in order, so results do not depend on timing.
+// kernel adds up in order, so results do not depend on timing.  (The last CTA
+// to arrive adding them up, counted by an atomic, took longer: 44.3 against
+// 40.6 us at B = 8, H = 32/8, 16384 slots, d = 128, and 69 against 54 us for
+// one sequence of 131071.)  The second kernel also forms the accumulated
+// weights from the scores, which the first leaves in the workspace (4 bytes a
+// score, against the 68 of reading a key again at d = 128).
 //
 // Every wait is bounded as in the forward kernel; a warp that gives up skips
 // its remaining slabs but still reaches the block's barriers.
@@ -59,8 +64,8 @@ struct Kv4Cfg {
     static constexpr int kMt = D / 16;                  // 16-row tiles of O^T
     static constexpr int kRegs = kMt * NT * 4;          // accumulators of O^T per lane
     static constexpr int kOffRing = 0;                  // [warps][stages][slab]
-    static constexpr int kOffO = kOffRing + kWarps * kStages * kSlabBytes;  // float [warps][kRegs][32]
-    static constexpr int kOffMl = kOffO + kWarps * kRegs * 32 * 4;          // float [warps][kRows][4]
+    static constexpr int kOffO = kOffRing + kWarps * kStages * kSlabBytes;  // float4 [warps][kMt][NT][32]
+    static constexpr int kOffMl = kOffO + kWarps * kRegs * 32 * 4;          // float4 [warps][kRows]
     static constexpr int kOffQ = kOffMl + kWarps * kRows * 4 * 4;           // uint4 [NT][D / 32][32]
     static constexpr int kOffC = kOffQ + NT * (D / 32) * 32 * 16;           // float [kRows]: score factors
     static constexpr int kOffBar = kOffC + kRows * 4;
@@ -189,7 +194,7 @@ struct Cursor {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_kernel(const Kv4FwdParams p) {
+__global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
     using C = Kv4Cfg<D, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = static_cast<int>(threadIdx.x) / 32, lane = static_cast<int>(threadIdx.x) % 32;
@@ -217,6 +222,55 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     load.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x));
     Cursor cur = load;
     const uint64_t once = policy_evict_first();  // every byte is read once per block of rows
+
+    // q fragments: lane (g, t) holds channels (D / 4) t .. of rows g + 8 nt; warp nt loads them a unit ahead and
+    // puts them, scaled, into shared memory
+    uint4* sm_q = reinterpret_cast<uint4*>(smem + C::kOffQ);
+    float* sm_c = reinterpret_cast<float*>(smem + C::kOffC);
+    auto load_q = [&](const Cursor& u, uint4 (&raw)[D / 32]) {
+        const int r = (u.unit % p.row_blocks) * C::kRows + 8 * warp + g;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (u.valid() && r < p.rows) {
+            const long long head = static_cast<long long>(u.b) * p.c.H_kv + u.unit / p.row_blocks;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                              (head * p.rows + r) * D + t * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) raw[i] = src[i];
+        }
+    };
+    auto put_q = [&](const uint4 (&raw)[D / 32]) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            m = __vmaxu2(__vmaxu2(__vmaxu2(m, raw[i].x & 0x7FFF7FFFu), raw[i].y & 0x7FFF7FFFu),
+                         __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
+        m = max(m & 0xFFFFu, m >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t mf = __float_as_uint(p.f16 ? widen_lo16<true>(m) : widen_lo16<false>(m));
+        // the row's largest magnitude is in [2^e, 2^(e+1)); zero, infinite or NaN rows stay as they are
+        int e = static_cast<int>(mf >> 23) - 127;
+        e = mf == 0u || e == 128 ? 14 : max(e, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float lo = p.f16 ? widen_lo16<true>(w[j]) : widen_lo16<false>(w[j]);
+                const float hi = p.f16 ? widen_lo16<true>(w[j] >> 16) : widen_lo16<false>(w[j] >> 16);
+                h[j] = pack_f16x2(lo * up, hi * up);
+            }
+            // words 0, 1: the two halves of step 2 i; 2, 3: of step 2 i + 1
+            sm_q[(warp * (D / 32) + i) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        if (t == 0) sm_c[8 * warp + g] = p.scale_log2 * down;
+    };
+    uint4 raw[D / 32];
+    if (warp < NT) load_q(cur, raw);  // ahead of the copies below, which it would queue behind
 
     // Slabs are dealt to the warps in turn over the CTA's whole run, so that a
     // unit's end leaves no warp a slab behind the others.
@@ -256,58 +310,16 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     };
     for (int s = 0; s < C::kStages; ++s) issue();
 
-    float* sm_o = reinterpret_cast<float*>(smem + C::kOffO);
-    float* sm_ml = reinterpret_cast<float*>(smem + C::kOffMl);
+    float4* sm_o = reinterpret_cast<float4*>(smem + C::kOffO);
+    float4* sm_ml = reinterpret_cast<float4*>(smem + C::kOffMl);
     int used = 0;  // slabs consumed
     bool ok = true;
 
-    for (; cur.valid(); cur.next(p.c, units)) {
+    while (cur.valid()) {
         const int kvh = cur.b * p.c.H_kv + cur.unit / p.row_blocks;
         const int row0 = (cur.unit % p.row_blocks) * C::kRows;  // of the head's rows
-        // ---- q fragments: lane (g, t) holds channels (D / 4) t .. of rows g + 8 nt, scaled; warp nt
-        // prepares them for the block
-        uint4* sm_q = reinterpret_cast<uint4*>(smem + C::kOffQ);
-        float* sm_c = reinterpret_cast<float*>(smem + C::kOffC);
-        if (warp < NT) {
-            const int r = row0 + 8 * warp + g;
-            uint4 raw[D / 32];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < p.rows) {
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.q) + (static_cast<long long>(kvh) * p.rows + r) * D + t * (D / 4));
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) raw[i] = src[i];
-            }
-            uint32_t m = 0u;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                m = __vmaxu2(__vmaxu2(__vmaxu2(m, raw[i].x & 0x7FFF7FFFu), raw[i].y & 0x7FFF7FFFu),
-                             __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
-            m = max(m & 0xFFFFu, m >> 16);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint32_t mf = __float_as_uint(p.f16 ? widen_lo16<true>(m) : widen_lo16<false>(m));
-            // the row's largest magnitude is in [2^e, 2^(e+1)); zero, infinite or NaN rows stay as they are
-            int e = static_cast<int>(mf >> 23) - 127;
-            e = mf == 0u || e == 128 ? 14 : max(e, -100);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 + e - 14) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float lo = p.f16 ? widen_lo16<true>(w[j]) : widen_lo16<false>(w[j]);
-                    const float hi = p.f16 ? widen_lo16<true>(w[j] >> 16) : widen_lo16<false>(w[j] >> 16);
-                    h[j] = pack_f16x2(lo * up, hi * up);
-                }
-                // words 0, 1: the two halves of step 2 i; 2, 3: of step 2 i + 1
-                sm_q[(warp * (D / 32) + i) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            if (t == 0) sm_c[8 * warp + g] = p.scale_log2 * down;
-        }
+        // ---- q fragments for the block, from the rows loaded ahead
+        if (warp < NT) put_q(raw);
         __syncthreads();
         float c[NT][2];  // score factor of rows 2t, 2t + 1
 #pragma unroll
@@ -563,6 +575,8 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
         }
 
         // ---- the unit's result over the CTA's warps
+        const Cursor done = cur;
+        cur.next(p.c, units);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -571,76 +585,74 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
 #pragma unroll
                 for (int off = 4; off < 32; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
                 if (g == 0)
-                    *reinterpret_cast<float4*>(sm_ml + (warp * C::kRows + 8 * nt + 2 * t + i) * 4) =
+                    sm_ml[warp * C::kRows + 8 * nt + 2 * t + i] =
                         make_float4(s == 0.0f ? -INFINITY : ref[nt][i], s, lq[nt][i], 0.0f);
             }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sm_o[((warp * C::kMt + mt) * NT * 4 + nt * 4 + i) * 32 + lane] = o[nt][mt][i];
         __syncthreads();
-        // rows 2t, 2t + 1 of each block of 8: reference, sums, and every warp's weight
-        const bool whole = cur.s0 == 0 && cur.s1 == cur.slabs;
-        const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (cur.s0 > 0 ? 0 : 1)) * C::kRows;
+        // lane (g, t): row g of each block of 8, warps t and t + 4; then the quad's M, L, LQ of that row
+        float M[NT], L[NT], LQ[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float wt[kWarps][2], M[2], L[2], LQ[2];
+            const float4 ma = sm_ml[t * C::kRows + 8 * nt + g], mb = sm_ml[(t + 4) * C::kRows + 8 * nt + g];
+            float m = fmaxf(ma.x, mb.x);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // a warp that saw nothing counts 0 (a NaN sum stays one)
+            const float fa = m == -INFINITY ? 1.0f : ex2(ma.x - m), fb = m == -INFINITY ? 1.0f : ex2(mb.x - m);
+            M[nt] = m;
+            L[nt] = fa * ma.y + fb * mb.y;
+            LQ[nt] = fa * ma.z + fb * mb.z;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * nt + 2 * t + i;
-                M[i] = -INFINITY;
-                L[i] = LQ[i] = 0.0f;
-                for (int w = 0; w < kWarps; ++w) M[i] = fmaxf(M[i], sm_ml[(w * C::kRows + r) * 4]);
+            for (int off = 1; off < 4; off *= 2) {
+                L[nt] += __shfl_xor_sync(0xffffffffu, L[nt], off);
+                LQ[nt] += __shfl_xor_sync(0xffffffffu, LQ[nt], off);
+            }
+            // this warp's weight in row g, then in rows 2t, 2t + 1
+            const float f = __shfl_sync(0xffffffffu, warp < 4 ? fa : fb, (lane & ~3) | (warp & 3));
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 ml = *reinterpret_cast<const float4*>(sm_ml + (w * C::kRows + r) * 4);
-                    // a warp that saw nothing counts 0 (a NaN sum stays one)
-                    wt[w][i] = M[i] == -INFINITY ? 1.0f : ex2(ml.x - M[i]);
-                    L[i] += wt[w][i] * ml.y;
-                    LQ[i] += wt[w][i] * ml.z;
+            for (int mt = 0; mt < C::kMt; ++mt)
+                sm_o[((warp * C::kMt + mt) * NT + nt) * 32 + lane] =
+                    make_float4(o[nt][mt][0] * f0, o[nt][mt][1] * f1, o[nt][mt][2] * f0, o[nt][mt][3] * f1);
+        }
+        if (warp < NT) load_q(cur, raw);
+        __syncthreads();
+        const bool whole = done.s0 == 0 && done.s1 == done.slabs;
+        const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (done.s0 > 0 ? 0 : 1)) * C::kRows;
+        const long long row_first = static_cast<long long>(kvh) * p.rows + row0;  // output row of row 0
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + 2 * t;
+            if (warp < C::kMt) {  // each of the first D / 16 warps adds up one 16-channel tile
+                float4 acc = sm_o[(warp * NT + nt) * 32 + lane];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 v = sm_o[((w * C::kMt + warp) * NT + nt) * 32 + lane];
+                    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+                }
+                const int ch = (D / 8) * g + 2 * warp;  // channels ch, ch + 1 of rows r (x, z) and r + 1 (y, w)
+                if (whole) {
+                    const float q0 = __shfl_sync(0xffffffffu, LQ[nt], 8 * t), q1 = __shfl_sync(0xffffffffu, LQ[nt], 8 * t + 4);
+                    const float i0 = q0 == 0.0f ? 0.0f : 1.0f / q0, i1 = q1 == 0.0f ? 0.0f : 1.0f / q1;
+                    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (row_first + r) * D + ch);
+                    if (row0 + r < p.rows)
+                        out[0] = p.f16 ? pack_f16x2(acc.x * i0, acc.z * i0) : pack_bf16x2(acc.x * i0, acc.z * i0);
+                    if (row0 + r + 1 < p.rows)
+                        out[D / 2] = p.f16 ? pack_f16x2(acc.y * i1, acc.w * i1) : pack_bf16x2(acc.y * i1, acc.w * i1);
+                } else {
+                    float* out = p.part_o + (slot + r) * D + ch;
+                    *reinterpret_cast<float2*>(out) = make_float2(acc.x, acc.z);
+                    *reinterpret_cast<float2*>(out + D) = make_float2(acc.y, acc.w);
                 }
             }
-            for (int mt = warp; mt < C::kMt; mt += kWarps) {
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[i] += wt[w][i & 1] * sm_o[((w * C::kMt + mt) * NT * 4 + nt * 4 + i) * 32 + lane];
-                const int ch = (D / 8) * g + 2 * mt;  // channels ch, ch + 1
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = row0 + 8 * nt + 2 * t + i;
-                    if (r >= p.rows) continue;
-                    if (whole) {
-                        const float inv = LQ[i] == 0.0f ? 0.0f : 1.0f / LQ[i];
-                        const float lo = acc[i] * inv, hi = acc[i + 2] * inv;
-                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) +
-                                                     (static_cast<long long>(kvh) * p.rows + r) * D + ch) =
-                            p.f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
-                    } else {
-                        *reinterpret_cast<float2*>(p.part_o + (slot + 8 * nt + 2 * t + i) * D + ch) =
-                            make_float2(acc[i], acc[i + 2]);
-                    }
-                }
-            }
-            if (warp == 0 && g == 0) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = row0 + 8 * nt + 2 * t + i;
-                    if (r >= p.rows) continue;
-                    if (whole) {
-                        const long long row = static_cast<long long>(kvh) * p.rows + r;
-                        const float lse2 = L[i] == 0.0f ? -INFINITY : M[i] + log2f(L[i]);
-                        if (p.lse != nullptr) p.lse[row] = lse2 * 0.69314718055994531f;
-                        p.row_lse2[row] = lse2;
-                    } else {
-                        *reinterpret_cast<float4*>(p.part_ml + (slot + 8 * nt + 2 * t + i) * 4) =
-                            make_float4(M[i], L[i], LQ[i], 0.0f);
-                    }
+            if (warp == 0 && t == 0) {
+                const int rg = 8 * nt + g;
+                if (!whole) {
+                    p.part_ml[slot + rg] = make_float4(M[nt], L[nt], LQ[nt], 0.0f);
+                } else if (row0 + rg < p.rows) {
+                    const float lse2 = L[nt] == 0.0f ? -INFINITY : M[nt] + log2f(L[nt]);
+                    if (p.lse != nullptr) p.lse[row_first + rg] = lse2 * 0.69314718055994531f;
+                    p.row_lse2[row_first + rg] = lse2;
                 }
             }
         }
@@ -693,12 +705,12 @@ __device__ __forceinline__ void row_sums(const Kv4FwdParams& p, const Parts& u, 
     const int lane = threadIdx.x % 32;
     M = -INFINITY;
     for (int c = u.first + lane; c <= u.last; c += 32)
-        M = fmaxf(M, p.part_ml[part_row(c, u.first, rows, r) * 4]);
+        M = fmaxf(M, p.part_ml[part_row(c, u.first, rows, r)].x);
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     L = LQ = 0.0f;
     for (int c = u.first + lane; c <= u.last; c += 32) {
-        const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + part_row(c, u.first, rows, r) * 4);
+        const float4 ml = p.part_ml[part_row(c, u.first, rows, r)];
         const float w = M == -INFINITY ? 1.0f : ex2(ml.x - M);
         L += w * ml.y;
         LQ += w * ml.z;
@@ -746,7 +758,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
                 const int mine = c0 + lane;
                 float f = 0.0f;
                 if (mine <= u.last)
-                    f = M == -INFINITY ? 1.0f : ex2(p.part_ml[part_row(mine, u.first, rows_per_block, rb) * 4] - M);
+                    f = M == -INFINITY ? 1.0f : ex2(p.part_ml[part_row(mine, u.first, rows_per_block, rb)].x - M);
                 const int n = min(32, u.last - c0 + 1);
 #pragma unroll 4
                 for (int i = 0; i < n; ++i) {
@@ -834,7 +846,7 @@ cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     // both kernels may be set up while the one before them in the stream runs; they wait for its end
-    // before they touch memory
+    // before they touch memory that it writes
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
