@@ -19,9 +19,10 @@
 // values are interleaved in bits before they are widened, which pairs keys
 // as the second product's operand needs them.
 //
-// What bounds it: reading the cache.  Each warp has a ring of slabs (32 keys:
-// codes and scales of K and V, four bulk copies) of its own, so warps never
-// wait for one another inside a unit; 16 warps an SM keep 147 KB in flight.
+// What bounds it: reading the cache.  Groups of eight slabs (32 keys each, one
+// per warp) arrive by four bulk copies (codes and scales of K and V) in a
+// ring that the warp that finishes a group last refills; two blocks an SM
+// keep 147 KB in flight.
 //
 // Work split.  The slabs of all units (sequence, key/value head, block of
 // rows), in order, are cut into equal runs, one per CTA, from the lengths on
@@ -60,17 +61,18 @@ struct Kv4Cfg {
     static constexpr int kStages = 2;
     static constexpr int kCodeBytes = kSlab * D / 2;
     static constexpr int kScaleBytes = kSlab * D / 16;
-    static constexpr int kSlabBytes = 2 * (kCodeBytes + kScaleBytes);
+    static constexpr int kStageBytes = 2 * kWarps * (kCodeBytes + kScaleBytes);  // a group: a slab per warp
     static constexpr int kMt = D / 16;                  // 16-row tiles of O^T
     static constexpr int kRegs = kMt * NT * 4;          // accumulators of O^T per lane
-    static constexpr int kOffRing = 0;                  // [warps][stages][slab]
-    static constexpr int kOffO = kOffRing + kWarps * kStages * kSlabBytes;  // float4 [warps][kMt][NT][32]
+    static constexpr int kOffRing = 0;  // [stages] K codes, V codes, K scales, V scales of kWarps slabs
+    static constexpr int kOffO = kOffRing + kStages * kStageBytes;  // float4 [warps][kMt][NT][32]
     static constexpr int kOffMl = kOffO + kWarps * kRegs * 32 * 4;          // float4 [warps][kRows]
     static constexpr int kOffQ = kOffMl + kWarps * kRows * 4 * 4;           // uint4 [NT][D / 32][32]
     static constexpr int kOffC = kOffQ + NT * (D / 32) * 32 * 16;           // float [kRows]: score factors
     static constexpr int kOffBar = kOffC + kRows * 4;
-    static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
-    static constexpr int kSmemBytes = kOffAbort + 16;
+    static constexpr int kOffCount = kOffBar + kStages * 8;  // [stages] warps done with the stage
+    static constexpr int kOffAbort = kOffCount + kStages * 4;
+    static constexpr int kSmemBytes = (kOffAbort + 4 + 15) / 16 * 16;
     static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
     static_assert(kSmemBytes * kCtasPerSm <= 232448 - 1024 * kCtasPerSm, "shared memory budget exceeded");
 };
@@ -112,6 +114,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
+// Adds 1 to a shared counter that wraps after kWarps; the value before.
+__device__ __forceinline__ uint32_t count_in(uint32_t addr) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(kWarps - 1) : "memory");
+    return old;
+}
 template <typename T>
 __device__ __forceinline__ T lds(const uint8_t* p) {
     return *reinterpret_cast<const T*>(p);
@@ -125,10 +133,9 @@ __device__ __forceinline__ int slabs_of(int len) { return (len + kSlab - 1) / kS
 // The slabs of all units fit 31 bits (the host checks it), so positions in
 // them are ints.
 //
-// Slabs per CTA: equal runs, at least one slab for every warp.
+// Slabs per CTA: equal runs of whole groups.
 __device__ __forceinline__ int slabs_per_cta(int total, int ctas) {
-    const int per = (total + ctas - 1) / ctas;
-    return per < kWarps ? kWarps : per;
+    return max(1, (total + ctas * kWarps - 1) / (ctas * kWarps)) * kWarps;
 }
 
 // Position in a CTA's run of slabs.
@@ -204,15 +211,16 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     FwdParams wp;  // what a bounded wait reports to
     wp.status = p.status;
     wp.gen = p.gen;
-    auto bar = [&](int s) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(warp * C::kStages + s); };
-    uint8_t* ring = smem + C::kOffRing + warp * C::kStages * C::kSlabBytes;
+    auto bar = [&](int s) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(s); };
 
-    if (lane == 0) {
-        for (int s = 0; s < C::kStages; ++s) mbar_init(bar(s), 1);
-        mbar_init_fence();  // a warp's barriers are its own
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar(s), 1);
+            *reinterpret_cast<uint32_t*>(smem + C::kOffCount + 4 * s) = 0u;
+        }
+        *abort_flag = 0u;
+        mbar_init_fence();
     }
-    if (threadIdx.x == 0) *abort_flag = 0u;
-    __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second kernel waits by itself
@@ -272,47 +280,40 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     uint4 raw[D / 32];
     if (warp < NT) load_q(cur, raw);  // ahead of the copies below, which it would queue behind
 
-    // Slabs are dealt to the warps in turn over the CTA's whole run, so that a
-    // unit's end leaves no warp a slab behind the others.
-    const int run0 = cur.pos;
-    auto first_slab = [&](const Cursor& u) -> int {
-        return u.s0 + ((warp - (u.pos - run0)) & (kWarps - 1));
-    };
-    // ---- producer side of this warp: lanes 0 .. 3 copy one array each
-    int issued = 0;  // slabs asked for so far; slab i uses stage i % kStages
-    int load_slab = 0, load_end = 0;
-    const uint8_t* load_from = nullptr;
-    const uint8_t* const load_base = lane == 0   ? p.c.codes[0]
-                                     : lane == 1 ? p.c.codes[1]
-                                     : lane == 2 ? p.c.scales[0]
-                                                 : p.c.scales[1];
-    const uint32_t load_bytes = lane < 2 ? C::kCodeBytes : C::kScaleBytes;
-    const uint32_t load_to = sbase + C::kOffRing + warp * C::kStages * C::kSlabBytes +
-                             (lane < 2 ? lane * C::kCodeBytes : 2 * C::kCodeBytes + (lane - 2) * C::kScaleBytes);
-    auto issue = [&]() {
-        while (load_slab >= load_end) {
-            if (!load.valid()) return;
-            load_slab = first_slab(load);
-            load_end = load.s1;
+    // A unit's slabs go in groups of one per warp.  Stage i % kStages of the ring holds group i; the last warp
+    // to finish a group refills its stage, so no warp waits for the others and none is set aside for loading.
+    // Every warp follows the loads' position.
+    int issued = 0;  // groups asked for
+    int load_s = load.s0;
+    auto issue = [&](bool mine) {
+        if (!load.valid()) return;
+        if (mine) {
+            const int st = issued % C::kStages;
+            const int n = min(kWarps, load.s1 - load_s);
             const long long row =
                 (static_cast<long long>(load.b) * p.c.H_kv + load.unit / p.row_blocks) * p.c.capacity +
-                static_cast<long long>(load_slab) * kSlab;
-            load_from = load_base + row * (lane < 2 ? D / 2 : D / 16);
-            load.next(p.c, units);
+                static_cast<long long>(load_s) * kSlab;
+            const uint32_t dst = sbase + C::kOffRing + st * C::kStageBytes;
+            const uint32_t code = n * C::kCodeBytes, scale = n * C::kScaleBytes;
+            mbar_arrive_expect_tx(bar(st), 2 * (code + scale));
+            bulk_load(dst, p.c.codes[0] + row * (D / 2), code, bar(st), once);
+            bulk_load(dst + kWarps * C::kCodeBytes, p.c.codes[1] + row * (D / 2), code, bar(st), once);
+            bulk_load(dst + 2 * kWarps * C::kCodeBytes, p.c.scales[0] + row * (D / 16), scale, bar(st), once);
+            bulk_load(dst + kWarps * (2 * C::kCodeBytes + C::kScaleBytes), p.c.scales[1] + row * (D / 16), scale, bar(st),
+                      once);
         }
-        const int s = issued % C::kStages;
-        if (lane == 0) mbar_arrive_expect_tx(bar(s), C::kSlabBytes);
-        __syncwarp();
-        if (lane < 4) bulk_load(load_to + s * C::kSlabBytes, load_from, load_bytes, bar(s), once);
-        load_from += kWarps * load_bytes;
         ++issued;
-        load_slab += kWarps;
+        load_s += kWarps;
+        if (load_s >= load.s1) {
+            load.next(p.c, units);
+            load_s = load.s0;
+        }
     };
-    for (int s = 0; s < C::kStages; ++s) issue();
+    for (int s = 0; s < C::kStages; ++s) issue(threadIdx.x == 0);
 
     float4* sm_o = reinterpret_cast<float4*>(smem + C::kOffO);
     float4* sm_ml = reinterpret_cast<float4*>(smem + C::kOffMl);
-    int used = 0;  // slabs consumed
+    int used = 0;  // groups consumed
     bool ok = true;
 
     while (cur.valid()) {
@@ -351,227 +352,232 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
         // rows 2t, 2t + 1 as one store: both exist and every slot's rows start on an even one
         const bool pairs = p.rows % 2 == 0;
 
-        const int slab0 = first_slab(cur);
-        for (int slab = slab0; ok && slab < cur.s1; slab += kWarps) {
+        const int slab0 = cur.s0 + warp;
+        for (int group = cur.s0; group < cur.s1; group += kWarps) {
             const int s = used % C::kStages;
-            ok = __all_sync(0xffffffffu, wait_phase(bar(s), (used / C::kStages) & 1, abort_flag, wp, 80));
-            if (!ok) break;
-            const uint8_t* kc = ring + s * C::kSlabBytes;
-            const uint8_t* vc = kc + C::kCodeBytes;
-            const uint8_t* ks = vc + C::kCodeBytes;
-            const uint8_t* vs = ks + C::kScaleBytes;
-            const int key0 = slab * kSlab;
-            const bool masked = key0 + kSlab > all_see;
-            const int kg = (g >> 1) + 4 * (g & 1);  // key of fragment row g (and 8 more of row g + 8)
+            const int slab = group + warp;
+            const bool mine = slab < cur.s1;
+            if (mine) ok = ok && __all_sync(0xffffffffu, wait_phase(bar(s), (used / C::kStages) & 1, abort_flag, wp, 80));
+            if (mine && ok) {
+                const uint8_t* kc = smem + C::kOffRing + s * C::kStageBytes + warp * C::kCodeBytes;
+                const uint8_t* vc = kc + kWarps * C::kCodeBytes;
+                const uint8_t* ks = smem + C::kOffRing + s * C::kStageBytes + 2 * kWarps * C::kCodeBytes + warp * C::kScaleBytes;
+                const uint8_t* vs = ks + kWarps * C::kScaleBytes;
+                const int key0 = slab * kSlab;
+                const bool masked = key0 + kSlab > all_see;
+                const int kg = (g >> 1) + 4 * (g & 1);  // key of fragment row g (and 8 more of row g + 8)
 
-            // ---- S^T of both halves of 16 keys
-            float x[2][NT][4];
+                // ---- S^T of both halves of 16 keys
+                float x[2][NT][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[h][nt][i] = 0.0f;
-                const int ka = 16 * h + kg, kb = ka + 8;
-                uint32_t wa[D / 32], wb[D / 32], sa[D / 64], sb[D / 64];
-                if constexpr (D == 128) {
-                    const uint4 a = lds<uint4>(kc + ka * 64 + t * 16), b = lds<uint4>(kc + kb * 64 + t * 16);
-                    wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
-                    wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
-                    const uint32_t s2a = e4m3x2_to_f16x2(lds<uint16_t>(ks + ka * 8 + t * 2));
-                    const uint32_t s2b = e4m3x2_to_f16x2(lds<uint16_t>(ks + kb * 8 + t * 2));
-                    sa[0] = __byte_perm(s2a, 0, 0x1010), sa[1] = __byte_perm(s2a, 0, 0x3232);
-                    sb[0] = __byte_perm(s2b, 0, 0x1010), sb[1] = __byte_perm(s2b, 0, 0x3232);
-                } else {
-                    const uint2 a = lds<uint2>(kc + ka * 32 + t * 8), b = lds<uint2>(kc + kb * 32 + t * 8);
-                    wa[0] = a.x, wa[1] = a.y;
-                    wb[0] = b.x, wb[1] = b.y;
-                    sa[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + ka * 4 + t) * 0x0101u);
-                    sb[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + kb * 4 + t) * 0x0101u);
+                        for (int i = 0; i < 4; ++i) x[h][nt][i] = 0.0f;
+                    const int ka = 16 * h + kg, kb = ka + 8;
+                    uint32_t wa[D / 32], wb[D / 32], sa[D / 64], sb[D / 64];
+                    if constexpr (D == 128) {
+                        const uint4 a = lds<uint4>(kc + ka * 64 + t * 16), b = lds<uint4>(kc + kb * 64 + t * 16);
+                        wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
+                        wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
+                        const uint32_t s2a = e4m3x2_to_f16x2(lds<uint16_t>(ks + ka * 8 + t * 2));
+                        const uint32_t s2b = e4m3x2_to_f16x2(lds<uint16_t>(ks + kb * 8 + t * 2));
+                        sa[0] = __byte_perm(s2a, 0, 0x1010), sa[1] = __byte_perm(s2a, 0, 0x3232);
+                        sb[0] = __byte_perm(s2b, 0, 0x1010), sb[1] = __byte_perm(s2b, 0, 0x3232);
+                    } else {
+                        const uint2 a = lds<uint2>(kc + ka * 32 + t * 8), b = lds<uint2>(kc + kb * 32 + t * 8);
+                        wa[0] = a.x, wa[1] = a.y;
+                        wb[0] = b.x, wb[1] = b.y;
+                        sa[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + ka * 4 + t) * 0x0101u);
+                        sb[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + kb * 4 + t) * 0x0101u);
+                    }
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) {
+                        uint32_t ha[4], hb[4];
+                        widen_codes(wa[w], ha);
+                        widen_codes(wb[w], hb);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            ha[i] = mul16x2(ha[i], sa[w / 2]);
+                            hb[i] = mul16x2(hb[i], sb[w / 2]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 q = sm_q[(nt * (D / 32) + w) * 32 + lane];
+                            mma_f16(x[h][nt], ha[0], hb[0], ha[1], hb[1], q.x, q.y);
+                            mma_f16(x[h][nt], ha[2], hb[2], ha[3], hb[3], q.z, q.w);
+                        }
+                    }
                 }
-#pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    uint32_t ha[4], hb[4];
-                    widen_codes(wa[w], ha);
-                    widen_codes(wb[w], hb);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ha[i] = mul16x2(ha[i], sa[w / 2]);
-                        hb[i] = mul16x2(hb[i], sb[w / 2]);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 q = sm_q[(nt * (D / 32) + w) * 32 + lane];
-                        mma_f16(x[h][nt], ha[0], hb[0], ha[1], hb[1], q.x, q.y);
-                        mma_f16(x[h][nt], ha[2], hb[2], ha[3], hb[3], q.z, q.w);
-                    }
-                }
-            }
-            // ---- exponents (base 2) against the reference; hidden slots are -inf whatever is stored there
-            float top = -INFINITY;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[h][nt][i] = fmaf(x[h][nt][i], c[nt][i & 1], -ref[nt][i & 1]);
-            if (masked) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int lim = limit(nt, i) - key0 - kg;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (16 * h >= lim) x[h][nt][i] = -INFINITY;
-                            if (16 * h + 8 >= lim) x[h][nt][i + 2] = -INFINITY;
-                        }
-                    }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmax3(top, x[0][nt][i], x[1][nt][i]);
-            // the first slab sets the reference (nothing to rescale); later ones move it when a weight would
-            // pass fp16's range
-            if (slab == slab0 || __any_sync(0xffffffffu, top > kGrow)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float m = fmaxf(fmaxf(x[0][nt][i], x[0][nt][i + 2]), fmaxf(x[1][nt][i], x[1][nt][i + 2]));
-#pragma unroll
-                        for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                        // a row that sees none of a first slab sees none of the warp's later ones either
-                        float shift = m == -INFINITY ? 0.0f : m - kRefShift;
-                        if (slab != slab0) {
-                            shift = fmaxf(shift, 0.0f);
-                            const float alpha = ex2(-shift);
-                            l[nt][i] *= alpha;
-                            lq[nt][i] *= alpha;
-#pragma unroll
-                            for (int mt = 0; mt < C::kMt; ++mt) {
-                                o[nt][mt][i] *= alpha;
-                                o[nt][mt][i + 2] *= alpha;
-                            }
-                        }
-                        ref[nt][i] += shift;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            x[h][nt][i] -= shift;
-                            x[h][nt][i + 2] -= shift;
-                        }
-                    }
-            }
-            if (logits != nullptr) {
-                float* dst = logits + static_cast<long long>(key0 + kg) * p.rows;
+                // ---- exponents (base 2) against the reference; hidden slots are -inf whatever is stored there
+                float top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        if (!masked || key0 + kg + 16 * h + 8 * i2 < cur.len) {
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const int left = p.rows - row0 - 8 * nt - 2 * t;  // rows from 2t on
-                                const float y0 = x[h][nt][2 * i2] + ref[nt][0], y1 = x[h][nt][2 * i2 + 1] + ref[nt][1];
-                                if (pairs && left > 0) {
-                                    *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(y0, y1);
-                                } else {
-                                    if (left > 0) dst[8 * nt] = y0;
-                                    if (left > 1) dst[8 * nt + 1] = y1;
-                                }
+                        for (int i = 0; i < 4; ++i) x[h][nt][i] = fmaf(x[h][nt][i], c[nt][i & 1], -ref[nt][i & 1]);
+                if (masked) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int lim = limit(nt, i) - key0 - kg;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (16 * h >= lim) x[h][nt][i] = -INFINITY;
+                                if (16 * h + 8 >= lim) x[h][nt][i + 2] = -INFINITY;
                             }
                         }
-                        dst += 8 * p.rows;
-                    }
-            }
-            // ---- weights, O^T += V^T P^T
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t pb[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = ex2(x[h][nt][i]);
-                        l[nt][i & 1] += w[i];
-                    }
-                    pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-                    pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-                    mma_f16(lq[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nt][0], pb[nt][1]);
                 }
-                uint32_t sc[4], v[4][D / 64];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = 16 * h + 4 * i + t;
-                    if constexpr (D == 128) {
-                        const uint2 a = lds<uint2>(vc + key * 64 + g * 8);
-                        v[i][0] = a.x, v[i][1] = a.y;
-                        sc[i] = lds<uint8_t>(vs + key * 8 + g);
-                    } else {
-                        v[i][0] = lds<uint32_t>(vc + key * 32 + g * 4);
-                        sc[i] = lds<uint8_t>(vs + key * 4 + g / 2);
-                    }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmax3(top, x[0][nt][i], x[1][nt][i]);
+                // the first slab sets the reference (nothing to rescale); later ones move it when a weight would
+                // pass fp16's range
+                if (slab == slab0 || __any_sync(0xffffffffu, top > kGrow)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float m = fmaxf(fmaxf(x[0][nt][i], x[0][nt][i + 2]), fmaxf(x[1][nt][i], x[1][nt][i + 2]));
+#pragma unroll
+                            for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                            // a row that sees none of a first slab sees none of the warp's later ones either
+                            float shift = m == -INFINITY ? 0.0f : m - kRefShift;
+                            if (slab != slab0) {
+                                shift = fmaxf(shift, 0.0f);
+                                const float alpha = ex2(-shift);
+                                l[nt][i] *= alpha;
+                                lq[nt][i] *= alpha;
+#pragma unroll
+                                for (int mt = 0; mt < C::kMt; ++mt) {
+                                    o[nt][mt][i] *= alpha;
+                                    o[nt][mt][i + 2] *= alpha;
+                                }
+                            }
+                            ref[nt][i] += shift;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                x[h][nt][i] -= shift;
+                                x[h][nt][i + 2] -= shift;
+                            }
+                        }
                 }
-                if (masked) {
-                    // slots behind the length hold anything: values 0.  A NaN in a slot that only some
-                    // rows see must not reach the others (0 * NaN): it is taken out of the product and
-                    // set in the rows that see it.
-                    bool nan = false;
+                if (logits != nullptr) {
+                    float* dst = logits + static_cast<long long>(key0 + kg) * p.rows;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (key0 + 16 * h + 4 * i + t >= cur.len) sc[i] = 0u;
-                        nan |= (sc[i] & 0x7Fu) == 0x7Fu;
-                    }
-                    if (__any_sync(0xffffffffu, nan)) {
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i2 = 0; i2 < 2; ++i2) {
+                            if (!masked || key0 + kg + 16 * h + 8 * i2 < cur.len) {
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const int left = p.rows - row0 - 8 * nt - 2 * t;  // rows from 2t on
+                                    const float y0 = x[h][nt][2 * i2] + ref[nt][0], y1 = x[h][nt][2 * i2 + 1] + ref[nt][1];
+                                    if (pairs && left > 0) {
+                                        *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(y0, y1);
+                                    } else {
+                                        if (left > 0) dst[8 * nt] = y0;
+                                        if (left > 1) dst[8 * nt + 1] = y1;
+                                    }
+                                }
+                            }
+                            dst += 8 * p.rows;
+                        }
+                }
+                // ---- weights, O^T += V^T P^T
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pb[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const uint32_t su = __shfl_sync(0xffffffffu, sc[i], (lane & ~3) | u);
-                                if ((su & 0x7Fu) == 0x7Fu) {
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                        for (int j = 0; j < 2; ++j)
-                                            if (key0 + 16 * h + 4 * i + u < limit(nt, j)) {
-#pragma unroll
-                                                for (int mt = 0; mt < C::kMt; ++mt)
-                                                    o[nt][mt][j] = o[nt][mt][j + 2] = __int_as_float(0x7FC00000);
-                                            }
-                                }
-                            }
+                            w[i] = ex2(x[h][nt][i]);
+                            l[nt][i & 1] += w[i];
                         }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if ((sc[i] & 0x7Fu) == 0x7Fu) sc[i] = 0u;
+                        pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+                        pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+                        mma_f16(lq[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nt][0], pb[nt][1]);
                     }
-                }
-                const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
-#pragma unroll
-                for (int w = 0; w < D / 64; ++w) {
-                    constexpr uint32_t kLow = 0x0F0F0F0Fu;
-                    uint32_t a0[4], a1[4], a2[4], a3[4];
-                    widen_codes((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), a0);
-                    widen_codes(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), a1);
-                    widen_codes((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), a2);
-                    widen_codes(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), a3);
+                    uint32_t sc[4], v[4][D / 64];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        a0[i] = mul16x2(a0[i], s01);
-                        a1[i] = mul16x2(a1[i], s01);
-                        a2[i] = mul16x2(a2[i], s23);
-                        a3[i] = mul16x2(a3[i], s23);
+                        const int key = 16 * h + 4 * i + t;
+                        if constexpr (D == 128) {
+                            const uint2 a = lds<uint2>(vc + key * 64 + g * 8);
+                            v[i][0] = a.x, v[i][1] = a.y;
+                            sc[i] = lds<uint8_t>(vs + key * 8 + g);
+                        } else {
+                            v[i][0] = lds<uint32_t>(vc + key * 32 + g * 4);
+                            sc[i] = lds<uint8_t>(vs + key * 4 + g / 2);
+                        }
+                    }
+                    if (masked) {
+                        // slots behind the length hold anything: values 0.  A NaN in a slot that only some
+                        // rows see must not reach the others (0 * NaN): it is taken out of the product and
+                        // set in the rows that see it.
+                        bool nan = false;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(o[nt][4 * w + i], a0[i], a1[i], a2[i], a3[i], pb[nt][0], pb[nt][1]);
+                        for (int i = 0; i < 4; ++i) {
+                            if (key0 + 16 * h + 4 * i + t >= cur.len) sc[i] = 0u;
+                            nan |= (sc[i] & 0x7Fu) == 0x7Fu;
+                        }
+                        if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    const uint32_t su = __shfl_sync(0xffffffffu, sc[i], (lane & ~3) | u);
+                                    if ((su & 0x7Fu) == 0x7Fu) {
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                            for (int j = 0; j < 2; ++j)
+                                                if (key0 + 16 * h + 4 * i + u < limit(nt, j)) {
+#pragma unroll
+                                                    for (int mt = 0; mt < C::kMt; ++mt)
+                                                        o[nt][mt][j] = o[nt][mt][j + 2] = __int_as_float(0x7FC00000);
+                                                }
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if ((sc[i] & 0x7Fu) == 0x7Fu) sc[i] = 0u;
+                        }
+                    }
+                    const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
+#pragma unroll
+                    for (int w = 0; w < D / 64; ++w) {
+                        constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                        uint32_t a0[4], a1[4], a2[4], a3[4];
+                        widen_codes((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), a0);
+                        widen_codes(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), a1);
+                        widen_codes((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), a2);
+                        widen_codes(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), a3);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            a0[i] = mul16x2(a0[i], s01);
+                            a1[i] = mul16x2(a1[i], s01);
+                            a2[i] = mul16x2(a2[i], s23);
+                            a3[i] = mul16x2(a3[i], s23);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(o[nt][4 * w + i], a0[i], a1[i], a2[i], a3[i], pb[nt][0], pb[nt][1]);
+                        }
                     }
                 }
             }
             __syncwarp();  // the slab has been read by every lane
+            bool refill = false;
+            if (lane == 0) refill = count_in(sbase + C::kOffCount + 4 * s) == kWarps - 1;
             ++used;
-            issue();
+            issue(refill);
         }
 
         // ---- the unit's result over the CTA's warps
@@ -658,10 +664,10 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
         }
         __syncthreads();
     }
-    // a warp that gave up leaves no copy of its own in flight behind it
+    // a warp that gave up leaves no copy in flight behind the block
     if (!ok)
-        for (; used < issued; ++used)
-            wait_phase(bar(used % C::kStages), (used / C::kStages) & 1, abort_flag, wp, 81, false);
+        for (int i = max(0, issued - C::kStages); i < issued; ++i)
+            wait_phase(bar(i % C::kStages), (i / C::kStages) & 1, abort_flag, wp, 81, false);
 }
 
 // ------------------------------------------------------------ second kernel
