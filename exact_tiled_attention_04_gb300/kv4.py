@@ -11,9 +11,18 @@ import math
 from . import binding as _b
 
 
+torch = None  # PyTorch, imported by the first call (importing the package does not need it)
+
+
+def _need_torch():
+    global torch
+    if torch is None:
+        import torch as module
+        torch = module
+
+
 @functools.lru_cache(maxsize=None)
 def _default_scale(d: int) -> float:
-    import torch
     return float(torch.tensor(1.0, dtype=torch.float32) / torch.sqrt(torch.tensor(float(d), dtype=torch.float32)))
 
 
@@ -25,56 +34,45 @@ def _scale(scale, d: int) -> float:
     return float(scale)
 
 
-class _On:
-    """The tensors' device as the current one, switched only when it is not."""
-
-    def __init__(self, device):
-        import torch
-        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _stream(stream, device, *made):
-    """The stream to launch on.  `made`: tensors allocated for this call, whose
-    memory the allocator must not hand out again before another stream is done."""
-    import torch
-    current = torch.cuda.current_stream(device)
-    if stream is None or stream == current:
-        return current.cuda_stream
-    for t in made:
-        t.record_stream(stream)
-    return stream.cuda_stream
+def _call(where: str, function, device, stream, made, *args):
+    """One C call on `stream` (default: the device's current one) with the
+    device made current where it is not.  `made`: tensors allocated for the
+    call, whose memory the allocator must not hand out again before another
+    stream than its own is done."""
+    current = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is not None and stream.cuda_stream != current:
+        for t in made:
+            t.record_stream(stream)
+        current = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = function(*args, current or None)
+    else:
+        with torch.cuda.device(device):
+            status = function(*args, current or None)
+    if status != _b.FA_OK:
+        raise _b.FAError(status, where)
 
 
 def _check(t, what: str, dtype, shape, device):
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA tensor on {device}")
+    raise ValueError(f"{what} must be a contiguous CUDA tensor on {device}")
 
 
-def _rows(t, what: str, device):
-    import torch
+def _rows(t, what: str, device) -> int:
+    """Check 16-bit rows [batch, heads, rows, d]; their dtype code."""
     if t.dim() != 4:
         raise ValueError(f"{what} must be [batch, heads, rows, d], got {tuple(t.shape)}")
-    if t.dtype not in (torch.bfloat16, torch.float16):
+    code = _b.FA_DTYPE_BF16 if t.dtype == torch.bfloat16 else _b.FA_DTYPE_F16 if t.dtype == torch.float16 else None
+    if code is None:
         raise TypeError(f"{what} must be bfloat16 or float16, got {t.dtype}")
-    if not t.is_cuda or (device is not None and t.device != device) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA tensor" + (f" on {device}" if device is not None else ""))
-
-
-def _done(status: int, where: str):
-    if status != _b.FA_OK:
-        raise _b.FAError(status, where)
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor on {device}")
+    return code
 
 
 class KV4Cache:
@@ -88,7 +86,7 @@ class KV4Cache:
     """
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, counts, pos=None, weight=None):
-        import torch
+        _need_torch()
         if k_codes.dim() != 4:
             raise ValueError(f"k_codes must be [B, H_kv, capacity, d // 2], got {tuple(k_codes.shape)}")
         B, H_kv, capacity, half = (int(x) for x in k_codes.shape)
@@ -117,7 +115,7 @@ class KV4Cache:
     @classmethod
     def empty(cls, B: int, H_kv: int, capacity: int, d: int, device="cuda", pos: bool = True, weight: bool = True):
         """An empty cache of at least `capacity` slots (rounded up to a multiple of 128)."""
-        import torch
+        _need_torch()
         cap = max(128, -(-capacity // 128) * 128)
         new = functools.partial(torch.zeros, device=device)
         return cls(new((B, H_kv, cap, d // 2), dtype=torch.uint8), new((B, H_kv, cap, d // 16), dtype=torch.uint8),
@@ -134,7 +132,7 @@ class KV4Cache:
         """Bytes kv4_attention needs for these sizes on the cache's device."""
         key = (H, N_q, bool(with_weight))
         if key not in self._need:
-            with _On(self.device):
+            with torch.cuda.device(self.device):
                 self._need[key] = _b.fa_kv4_fwd_workspace_size(self.B, H, self.H_kv, N_q, self.capacity, self.d,
                                                                int(with_weight))
         return self._need[key]
@@ -145,32 +143,33 @@ def kv4_append(cache: KV4Cache, k, v, counts_out=None, stream=None):
     entries; the counts advance in place, or go to `counts_out` (int32
     [2, B]).  Rows past the capacity are dropped and reported by
     fa_device_status (FA_ERR_CAPACITY).  Returns the advanced counts."""
-    import torch
-    _rows(k, "k", cache.device)
+    code = _rows(k, "k", cache.device)
     if v.dtype != k.dtype:
         raise TypeError("k and v must share a dtype")
     _check(v, "v", k.dtype, k.shape, cache.device)
-    if (k.shape[0], k.shape[1], k.shape[3]) != (cache.B, cache.H_kv, cache.d):
+    B, H_kv, n, d = k.shape
+    if B != cache.B or H_kv != cache.H_kv or d != cache.d:
         raise ValueError(f"k must be [{cache.B}, {cache.H_kv}, n, {cache.d}], got {tuple(k.shape)}")
-    counts = cache.counts
-    if counts_out is not None:
-        _check(counts_out, "counts_out", torch.int32, (2, cache.B), cache.device)
-        counts = counts_out
-    with _On(cache.device):
-        _done(_b.fa_kv4_append(cache._ref, k.data_ptr(), v.data_ptr(), k.shape[2], _b._dtype_code(k),
-                               counts.data_ptr(), _stream(stream, cache.device)), "fa_kv4_append")
-    return counts
+    if counts_out is None:
+        counts_out = cache.counts
+    else:
+        _check(counts_out, "counts_out", torch.int32, (2, B), cache.device)
+    _call("fa_kv4_append", _b.load().fa_kv4_append, cache.device, stream, (),
+          cache._ref, k.data_ptr(), v.data_ptr(), n, code, counts_out.data_ptr())
+    return counts_out
 
 
 def kv4_read(cache: KV4Cache, count: int, first=None, dtype=None, k=None, v=None, stream=None):
     """The values (k, v) [B, H_kv, count, d] of `count` slots from first[b] on
     (int32 [B]; default 0), exactly as attention sees them.  dtype: bfloat16
     (default) or float16."""
-    import torch
-    dtype = dtype or torch.bfloat16
-    if dtype not in (torch.bfloat16, torch.float16):
+    if dtype is None or dtype == torch.bfloat16:
+        dtype, code = torch.bfloat16, _b.FA_DTYPE_BF16
+    elif dtype == torch.float16:
+        code = _b.FA_DTYPE_F16
+    else:
         raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
-    shape = (cache.B, cache.H_kv, int(count), cache.d)
+    shape = (cache.B, cache.H_kv, count, cache.d)
     made = []
     if k is None:
         made.append(k := torch.empty(shape, dtype=dtype, device=cache.device))
@@ -182,9 +181,8 @@ def kv4_read(cache: KV4Cache, count: int, first=None, dtype=None, k=None, v=None
         _check(v, "v", dtype, shape, cache.device)
     if first is not None:
         _check(first, "first", torch.int32, (cache.B,), cache.device)
-    with _On(cache.device):
-        _done(_b.fa_kv4_read(cache._ref, first.data_ptr() if first is not None else None, int(count), k.data_ptr(),
-                             v.data_ptr(), _b._dtype_code(k), _stream(stream, cache.device, *made)), "fa_kv4_read")
+    _call("fa_kv4_read", _b.load().fa_kv4_read, cache.device, stream, made,
+          cache._ref, first.data_ptr() if first is not None else None, count, k.data_ptr(), v.data_ptr(), code)
     return k, v
 
 
@@ -198,8 +196,8 @@ def kv4_attention(q, cache: KV4Cache, scale: float | None = None, causal: bool =
     cache.weight (or 0) plus each entry's softmax weights (pass cache.weight
     to accumulate in place).  `workspace` (uint8, cache.workspace_size(...)
     bytes) is allocated when not given."""
-    import torch
-    _rows(q, "q", cache.device)
+    device = cache.device
+    code = _rows(q, "q", device)
     B, H, N_q, d = q.shape
     if B != cache.B or d != cache.d or H % cache.H_kv:
         raise ValueError(f"q must be [{cache.B}, a multiple of {cache.H_kv}, N_q, {cache.d}], got {tuple(q.shape)}")
@@ -207,24 +205,24 @@ def kv4_attention(q, cache: KV4Cache, scale: float | None = None, causal: bool =
     if out is None:
         made.append(out := torch.empty_like(q))
     else:
-        _check(out, "out", q.dtype, q.shape, cache.device)
+        _check(out, "out", q.dtype, q.shape, device)
     if lse is not None:
-        _check(lse, "lse", torch.float32, q.shape[:3], cache.device)
+        _check(lse, "lse", torch.float32, (B, H, N_q), device)
     elif with_lse:
-        made.append(lse := torch.empty((B, H, N_q), dtype=torch.float32, device=cache.device))
+        made.append(lse := torch.empty((B, H, N_q), dtype=torch.float32, device=device))
     if weight_out is not None:
-        _check(weight_out, "weight_out", torch.float32, (B, cache.H_kv, cache.capacity), cache.device)
+        _check(weight_out, "weight_out", torch.float32, (B, cache.H_kv, cache.capacity), device)
     if workspace is None:
-        need = cache.workspace_size(H, N_q, weight_out is not None)
-        made.append(workspace := torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device))
-    elif workspace.device != cache.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
-    with _On(cache.device):
-        _done(_b.fa_kv4_fwd(cache._ref, q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                            weight_out.data_ptr() if weight_out is not None else None, H, N_q, _scale(scale, d),
-                            _b._dtype_code(q) | (_b.FA_FLAG_CAUSAL if causal else 0), workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream(stream, cache.device, *made)),
-              "fa_kv4_fwd")
+        size = max(cache.workspace_size(H, N_q, weight_out is not None), 16)
+        made.append(workspace := torch.empty(size, dtype=torch.uint8, device=device))
+    else:
+        size = workspace.numel() * workspace.element_size()
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    _call("fa_kv4_fwd", _b.load().fa_kv4_fwd, device, stream, made,
+          cache._ref, q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+          weight_out.data_ptr() if weight_out is not None else None, H, N_q, _scale(scale, d),
+          code | _b.FA_FLAG_CAUSAL if causal else code, workspace.data_ptr(), size)
     return out, lse
 
 
@@ -236,7 +234,6 @@ def kv4_evict(cache: KV4Cache, keep: int, sinks: int = 0, recent: int = 0, weigh
     `out`; the new counts go to the cache that holds the result, or to
     `counts_out`.  Returns src int32 [B, H_kv, keep]: the slot each slot's
     entry came from, -1 behind the last."""
-    import torch
     if keep < 1:
         raise ValueError(f"keep must be at least 1, got {keep}")
     if weight is not None:
@@ -252,23 +249,22 @@ def kv4_evict(cache: KV4Cache, keep: int, sinks: int = 0, recent: int = 0, weigh
         _check(counts_out, "counts_out", torch.int32, (2, cache.B), cache.device)
     if out is not None and out.device != cache.device:
         raise ValueError(f"out must be on {cache.device}")
-    with _On(cache.device):
-        _done(_b.fa_kv4_evict(cache._ref, keep, sinks, recent, weight.data_ptr() if weight is not None else None,
-                              out._ref if out is not None else None, src.data_ptr(), counts_out.data_ptr(),
-                              _stream(stream, cache.device, *made)), "fa_kv4_evict")
+    _call("fa_kv4_evict", _b.load().fa_kv4_evict, cache.device, stream, made,
+          cache._ref, keep, sinks, recent, weight.data_ptr() if weight is not None else None,
+          out._ref if out is not None else None, src.data_ptr(), counts_out.data_ptr())
     return src
 
 
 def _weight_stride(t, what: str, shape, device) -> int:
     """Distance between the heads' rows of a [B, H_kv, N_kv] tensor whose
     rows are contiguous and equally far apart."""
-    import torch
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or t.device != device:
+    if t.dtype != torch.float32 or t.shape != shape or t.device != device:
         raise ValueError(f"{what} must be fp32 {shape} on {device}")
     B, H_kv, N_kv = shape
+    s0, s1, s2 = t.stride()
     # a dimension of size 1 has no stride of its own
-    row = t.stride(1) if H_kv > 1 else t.stride(0) if B > 1 else N_kv
-    if (N_kv > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != H_kv * row) or row < N_kv:
+    row = s1 if H_kv > 1 else s0 if B > 1 else N_kv
+    if (N_kv > 1 and s2 != 1) or (B > 1 and s0 != H_kv * row) or row < N_kv:
         raise ValueError(f"{what} must have contiguous rows, equally far apart")
     return row
 
@@ -281,26 +277,26 @@ def attention_weights(q, k, lse, scale: float | None = None, causal: bool = Fals
     k [B, H_kv, N_kv, d] (bf16 or fp16) and lse [B, H, N_q] as `attention`
     took and returned them.  `out` and `weight_in` may be the first N_kv
     columns of a cache's weight (same strides), and the same tensor."""
-    import torch
-    _rows(q, "q", None)
-    _rows(k, "k", q.device)
+    _need_torch()
+    device = q.device
+    code = _rows(q, "q", device)
+    _rows(k, "k", device)
     if k.dtype != q.dtype:
         raise TypeError("q and k must share a dtype")
     B, H, N_q, d = q.shape
-    if k.shape[0] != B or k.shape[3] != d or H % k.shape[1]:
+    _, H_kv, N_kv, _ = k.shape
+    if k.shape[0] != B or k.shape[3] != d or H_kv < 1 or H % H_kv:
         raise ValueError(f"incompatible q and k shapes: {tuple(q.shape)} {tuple(k.shape)}")
-    H_kv, N_kv = k.shape[1], k.shape[2]
-    _check(lse, "lse", torch.float32, (B, H, N_q), q.device)
+    _check(lse, "lse", torch.float32, (B, H, N_q), device)
+    shape = (B, H_kv, N_kv)
     made = []
     if out is None:
-        made.append(out := torch.empty((B, H_kv, N_kv), dtype=torch.float32, device=q.device))
-    stride = _weight_stride(out, "out", (B, H_kv, N_kv), q.device)
-    if weight_in is not None and _weight_stride(weight_in, "weight_in", (B, H_kv, N_kv), q.device) != stride:
+        made.append(out := torch.empty(shape, dtype=torch.float32, device=device))
+    stride = _weight_stride(out, "out", shape, device)
+    if weight_in is not None and _weight_stride(weight_in, "weight_in", shape, device) != stride:
         raise ValueError("weight_in and out must have the same strides")
-    with _On(q.device):
-        _done(_b.fa_fwd_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(),
-                                weight_in.data_ptr() if weight_in is not None else None, out.data_ptr(), stride, B, H,
-                                H_kv, N_q, N_kv, d, first_query, _scale(scale, d),
-                                _b._dtype_code(q) | (_b.FA_FLAG_CAUSAL if causal else 0),
-                                _stream(stream, q.device, *made)), "fa_fwd_weights")
+    _call("fa_fwd_weights", _b.load().fa_fwd_weights, device, stream, made,
+          q.data_ptr(), k.data_ptr(), lse.data_ptr(), weight_in.data_ptr() if weight_in is not None else None,
+          out.data_ptr(), stride, B, H, H_kv, N_q, N_kv, d, first_query, _scale(scale, d),
+          code | _b.FA_FLAG_CAUSAL if causal else code)
     return out
