@@ -47,8 +47,7 @@ struct Kv4EvictParams {
     int recent;
 };
 constexpr int kKv4EvictMaxCapacity = 393216;
-// sms: SM count of the current device
-cudaError_t launch_kv4_evict(const Kv4EvictParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream);
 
 // Attention over the cache.  Rows: the R = N_q * group query rows of a
 // key/value head, row r = g * N_q + i (query head g of the group, query i),

@@ -2,23 +2,27 @@
 // fa_kv4_evict): per key/value head, the `keep` entries of largest key, where
 // an entry's key orders (protected first, then weight; ties by slot).
 //
-// One block per head, or a cluster of them where heads are few or long, every
-// CTA holding a contiguous slice of the head's keys in shared memory:
+// One block per head, or a cluster of them where a head is long, every CTA
+// holding a contiguous slice of the head's keys in shared memory:
 //   1. radix selection, 8 bits at a time, gives the threshold T and how many
 //      entries equal to T are kept.  A histogram has 256 bins of 32 counters,
 //      one per lane, so that no two lanes of a warp meet in a bank or on a
 //      counter, however the weights are distributed (a layer's weights share a
 //      few exponents, all new entries share 0);
-//   2. the entries' flags, by ballots: kept = key > T, or key == T and its
-//      rank among those (in slot order) is below that count;
+//   2. a bit per entry: kept = key > T, or key == T and among the first of
+//      those in slot order;
 //   3. holes (slots below the new length whose entry leaves) and late entries
 //      (kept ones at or behind it) are as many as one another; hole r takes
-//      late entry r;
+//      late entry r.  Ranks come from a scan over the words of bits;
 //   4. the moved rows are copied, 32 a warp with all their loads in flight.
 //      Sources lie at or behind the new length and targets below it, so in
 //      place no copy reads what another writes.
+// A decode step that puts one entry too many into the cache needs no
+// threshold: up to kEvFew leaving entries of a head that one block holds are
+// found one by one as block-wide minima.
 // Short rows are bound by the latency of these steps, long ones that move
 // many entries by their copies.
+#include <cstddef>
 #include <cstdint>
 
 #include "fa_kv4.h"
@@ -32,16 +36,37 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvMaxCluster = 8;
 constexpr int kEvMaxSlice = kKv4EvictMaxCapacity / kEvMaxCluster;  // keys per CTA
 
+constexpr int kEvFew = 8;
+constexpr uint32_t kEvList = 256;  // open entries that are compared with one another
+constexpr int kEvMaxWords = (kEvMaxSlice + 31) / 32;
+
 // Shared memory: EvShared, then the slice's keys.
-struct EvShared {
-    uint32_t hist[256 * 32];   // [bin][lane]; after the selection a bit per key (kept)
+struct alignas(16) EvShared {  // the keys behind it are read 16 bytes at a time
+    union {
+        uint32_t hist[256 * 32];  // [bin][lane]
+        struct {                  // after the selection, a word per 32 entries
+            uint32_t kept[kEvMaxWords];   // bit i: entry stays
+            uint32_t equal[kEvMaxWords];  // bit i: key equals the threshold
+            uint32_t before[kEvMaxWords]; // holes (low half) and late entries (high half) of earlier words
+        };
+        struct {                  // few leaving entries
+            uint2 least[2][kEvWarps];  // a warp's least key and the highest slot that has it
+            int leaving[kEvFew], hole[kEvFew], late[kEvFew];
+        };
+    };
     uint32_t bins[256];        // this CTA's sums
-    uint32_t total[256];       // the cluster's
-    uint32_t warp_count[2][kEvWarps];
-    uint32_t count[4];         // this CTA's, read by the cluster
+    union {
+        uint32_t total[256];     // the cluster's
+        uint32_t list[kEvList];  // one CTA: the open entries
+    };
+    uint32_t warp_count[kEvWarps];
+    uint32_t pick[3];          // bin, entries above it, entries in it
+    uint32_t count[2];         // this CTA's, read by the cluster
+    uint32_t listed;           // open entries in the list
 };
 
-static_assert(kEvMaxSlice / 32 <= 256 * 32 && sizeof(EvShared) + kEvMaxSlice * 4 <= 232448,
+static_assert(sizeof(EvShared) % 16 == 0 && offsetof(EvShared, bins) % 16 == 0 && offsetof(EvShared, total) % 16 == 0, "16-byte reads");
+static_assert(sizeof(EvShared) + kEvMaxSlice * 4 <= 232448,
               "shared memory budget exceeded");
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank) {
@@ -116,6 +141,51 @@ __device__ __forceinline__ void copy_entries(const Kv4Cache& f, const Kv4Cache& 
     }
 }
 
+// One entry, by a warp.
+template <int D>
+__device__ __forceinline__ void copy_entry(const Kv4Cache& c, long long from, long long to) {
+    constexpr int kChunks = D / 32;
+    const int lane = threadIdx.x % 32;
+    if (lane < 2 * kChunks) {
+        uint8_t* codes = lane < kChunks ? c.codes[0] : c.codes[1];
+        reinterpret_cast<uint4*>(codes)[to * kChunks + lane % kChunks] =
+            reinterpret_cast<const uint4*>(codes)[from * kChunks + lane % kChunks];
+    } else if (lane < 10) {
+        uint8_t* scales = lane == 8 ? c.scales[0] : c.scales[1];
+        if (lane >= 8) {
+            if constexpr (D == 128)
+                reinterpret_cast<uint2*>(scales)[to] = reinterpret_cast<const uint2*>(scales)[from];
+            else
+                reinterpret_cast<uint32_t*>(scales)[to] = reinterpret_cast<const uint32_t*>(scales)[from];
+        }
+    } else if (lane == 10) {
+        if (c.pos != nullptr) c.pos[to] = c.pos[from];
+    } else if (lane == 11) {
+        if (c.weight != nullptr) c.weight[to] = c.weight[from];
+    }
+}
+
+// The bits below and above the new length nn of the word that starts at slot.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Exclusive prefix of v over the block's threads; *sum gets the total.
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t (&warp_count)[kEvWarps], uint32_t* sum) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_count[warp] = x;
+    __syncthreads();
+    const uint32_t w = warp_count[lane];
+    *sum = __reduce_add_sync(0xffffffffu, w);
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
+    __syncthreads();  // warp_count may be written again
+    return before + x - v;
+}
+
 // kOne: a block per head (no cluster).
 template <int D, bool kOne>
 __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_constant__ Kv4EvictParams p, int slice,
@@ -123,7 +193,6 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
     extern __shared__ __align__(16) uint8_t ev_smem[];
     EvShared& sh = *reinterpret_cast<EvShared*>(ev_smem);
     uint32_t* keys = reinterpret_cast<uint32_t*>(ev_smem + sizeof(EvShared));
-    uint32_t* kept = sh.hist;  // bit i % 32 of word i / 32: entry begin + i stays
     const uint32_t keys_addr = smem_u32(keys);
     const uint32_t cs = kOne ? 1u : static_cast<uint32_t>(gridDim.x) / static_cast<uint32_t>(p.from.B * p.from.H_kv);
     const uint32_t rank = kOne ? 0u : cluster_ctarank();
@@ -134,6 +203,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
     const int head = static_cast<int>(blockIdx.x / cs);
     const int b = head / p.from.H_kv;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) sh.listed = 0u;
     for (int i = threadIdx.x; i < 256 * 8; i += kEvThreads)
         reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -141,6 +211,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
     const int seen = p.from.counts[p.from.B + b];
     const int nn = min(n, p.keep);  // the new length
     const bool in_place = p.to.codes[0] == p.from.codes[0];
+    bool copied = false;
     int32_t* src = p.src + static_cast<long long>(head) * p.keep;
     const long long row0 = static_cast<long long>(head) * p.from.capacity;
     const long long to0 = static_cast<long long>(head) * p.to.capacity;
@@ -152,156 +223,268 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
         const int32_t* pos = p.from.pos + row0 + begin;
         const bool protect = p.sinks > 0 || p.recent > 0;
         const long long newest = static_cast<long long>(seen) - p.recent;
+        auto key_of = [&](float w, int at) -> uint32_t {
+            return rank_key(w, protect && (at < p.sinks || at >= newest));
+        };
+        if (((reinterpret_cast<uintptr_t>(rank_by) | (protect ? reinterpret_cast<uintptr_t>(pos) : 0u)) & 15u) == 0u) {
 #pragma unroll 4
-        for (int i = threadIdx.x; i < size; i += kEvThreads) {
-            const float w = rank_by[i];
-            const int at = protect ? pos[i] : 0;
-            keys[i] = rank_key(w, protect && (at < p.sinks || at >= newest));
-        }
-        // 1. threshold: the entries whose upper bits equal `prefix` are still open
-        uint32_t prefix = 0u;
-        uint32_t want = static_cast<uint32_t>(nn), open = 0u;  // entries to take among the open ones; those of the bin
-#pragma unroll 1
-        for (int down = 24; down >= 0; down -= 8) {
-            __syncthreads();  // keys and a zeroed histogram
-#pragma unroll 4
-            for (int i = threadIdx.x; i < size; i += kEvThreads) {
-                const uint32_t k = keys[i];
-                if (down == 24 || (k >> (down + 8)) == prefix)
-                    atomicAdd(&sh.hist[((k >> down) & 255u) * 32 + lane], 1u);
+            for (int i = 4 * threadIdx.x; i < size; i += 4 * kEvThreads) {  // a row has 128 slots or a multiple
+                const float4 w = *reinterpret_cast<const float4*>(rank_by + i);
+                const int4 at = protect ? *reinterpret_cast<const int4*>(pos + i) : make_int4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(keys + i) =
+                    make_uint4(key_of(w.x, at.x), key_of(w.y, at.y), key_of(w.z, at.z), key_of(w.w, at.w));
             }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 256 / kEvWarps; ++i) {
-                const int bin = warp * (256 / kEvWarps) + i;
-                const uint32_t s = __reduce_add_sync(0xffffffffu, sh.hist[bin * 32 + lane]);
-                sh.hist[bin * 32 + lane] = 0u;
-                if (lane == 0) sh.bins[bin] = s;
-            }
-            sync_all();
-            if constexpr (!kOne) {
-                if (threadIdx.x < 256) {
-                    uint32_t s = 0u;
-                    for (uint32_t r = 0; r < cs; ++r) s += ld_cluster_u32(smem_u32(&sh.bins[threadIdx.x]), r);
-                    sh.total[threadIdx.x] = s;
-                }
-                cluster_sync_all();  // and every CTA has read the others' sums
-            }
-            // from the top bin down: lane l holds bins 255 - 8 l .. 248 - 8 l; every warp finds the bin
-            const uint4* t4 = reinterpret_cast<const uint4*>(kOne ? sh.bins : sh.total) + (31 - lane) * 2;
-            const uint4 lo = t4[0], hi = t4[1];
-            const uint32_t c[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
-            const uint32_t sum = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
-            uint32_t above = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, above, o);
-                if (lane >= o) above += y;
-            }
-            above -= sum;
-            const uint32_t holder = __ballot_sync(0xffffffffu, above < want && want <= above + sum);
-            uint32_t bin = 0u, before = above, in_bin = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (in_bin == 0u && before + c[i] >= want) {
-                    bin = static_cast<uint32_t>(255 - 8 * lane - i);
-                    in_bin = c[i];
-                }
-                if (in_bin == 0u) before += c[i];
-            }
-            const int who = __ffs(static_cast<int>(holder)) - 1;
-            prefix = (prefix << 8) | __shfl_sync(0xffffffffu, bin, who);
-            want -= __shfl_sync(0xffffffffu, before, who);
-            open = __shfl_sync(0xffffffffu, in_bin, who);
-        }
-        // 2. kept flags; warps take contiguous runs of words, ranks follow slot order
-        const uint32_t T = prefix;  // `want` of the `open` entries equal to T are kept
-        const int words = (size + 31) / 32;
-        const int per_warp = (words + kEvWarps - 1) / kEvWarps;
-        const int w0 = min(warp * per_warp, words), w1 = min(w0 + per_warp, words);
-        uint32_t eq_before = 0u;
-        if (want < open) {  // not all of them: their ranks over the cluster
-            uint32_t eq = 0u;
-            for (int x = w0; x < w1; ++x)
-                eq += __popc(__ballot_sync(0xffffffffu, x * 32 + lane < size && keys[x * 32 + lane] == T));
-            if (lane == 0) sh.warp_count[0][warp] = eq;
-            __syncthreads();
-            const uint32_t mine = sh.warp_count[0][lane];
-            eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0u);
-            const uint32_t all = __reduce_add_sync(0xffffffffu, mine);
-            if (threadIdx.x == 0) sh.count[2] = all;
-            sync_all();
-            for (uint32_t r = 0; r < rank; ++r) eq_before += ld_cluster_u32(smem_u32(&sh.count[2]), r);
-        }
-        uint32_t holes = 0u, late = 0u;
-        for (int x = w0; x < w1; ++x) {
-            const int i = x * 32 + lane;
-            const bool in = i < size;
-            const uint32_t k = in ? keys[i] : 0u;
-            const uint32_t eqs = __ballot_sync(0xffffffffu, in && k == T);
-            const bool stay =
-                in && (k > T || (k == T && (want == open || eq_before + __popc(eqs & ((1u << lane) - 1u)) < want)));
-            eq_before += __popc(eqs);
-            const uint32_t bits = __ballot_sync(0xffffffffu, stay);
-            if (lane == 0) kept[x] = bits;
-            holes += __popc(__ballot_sync(0xffffffffu, in && !stay && begin + i < nn));
-            late += __popc(__ballot_sync(0xffffffffu, stay && begin + i >= nn));
-        }
-        // 3. ranks of holes and late entries over the cluster
-        __syncthreads();  // the counts of equal entries were read
-        if (lane == 0) {
-            sh.warp_count[0][warp] = holes;
-            sh.warp_count[1][warp] = late;
+        } else {
+            for (int i = threadIdx.x; i < size; i += kEvThreads) keys[i] = key_of(rank_by[i], protect ? pos[i] : 0);
         }
         __syncthreads();
-        const uint32_t hs = sh.warp_count[0][lane], ls = sh.warp_count[1][lane];
-        uint32_t h_rank = __reduce_add_sync(0xffffffffu, lane < warp ? hs : 0u);
-        uint32_t l_rank = __reduce_add_sync(0xffffffffu, lane < warp ? ls : 0u);
-        if constexpr (!kOne) {
-            const uint32_t h_all = __reduce_add_sync(0xffffffffu, hs), l_all = __reduce_add_sync(0xffffffffu, ls);
-            if (threadIdx.x == 0) {
-                sh.count[0] = h_all;
-                sh.count[1] = l_all;
+        if (kOne && n - nn <= kEvFew) {
+            // the entries in the order they leave: ascending key, descending slot
+            uint32_t last_key = 0u;
+            int last_slot = 0x7FFFFFFF;
+            for (int r = 0; r < n - nn; ++r) {
+                uint32_t key = 0xFFFFFFFFu;
+                int slot = -1;
+                for (int i = threadIdx.x; i < n; i += kEvThreads) {
+                    const uint32_t k = keys[i];
+                    if ((k > last_key || (k == last_key && i < last_slot)) && (k < key || (k == key && i > slot))) {
+                        key = k;
+                        slot = i;
+                    }
+                }
+                uint32_t least = __reduce_min_sync(0xffffffffu, key);
+                slot = __reduce_max_sync(0xffffffffu, key == least ? slot : -1);
+                if (lane == 0) sh.least[r & 1][warp] = make_uint2(least, static_cast<uint32_t>(slot));
+                __syncthreads();
+                const uint2 w = sh.least[r & 1][lane];
+                last_key = __reduce_min_sync(0xffffffffu, w.x);
+                last_slot = __reduce_max_sync(0xffffffffu, w.x == last_key ? static_cast<int>(w.y) : -1);
+                if (threadIdx.x == 0) sh.leaving[r] = last_slot;
             }
-            cluster_sync_all();  // also every key was read: the slices now hold the list of holes
-            for (uint32_t r = 0; r < rank; ++r) {
-                h_rank += ld_cluster_u32(smem_u32(&sh.count[0]), r);
-                l_rank += ld_cluster_u32(smem_u32(&sh.count[1]), r);
+            __syncthreads();
+            const int e = n - nn;
+            if (warp == 0) {
+                const int gone = lane < e ? sh.leaving[lane] : -1, end = nn + lane;
+                int hole_rank = 0, late_rank = 0;
+                bool leaves = false;
+                for (int i = 0; i < e; ++i) {
+                    const int o = sh.leaving[i];
+                    hole_rank += o < gone ? 1 : 0;
+                    late_rank += o >= nn && o < end ? 1 : 0;  // leaving ones among the slots before this one
+                    leaves |= o == end;
+                }
+                if (gone >= 0 && gone < nn) sh.hole[hole_rank] = gone;
+                if (lane < e && !leaves) sh.late[lane - late_rank] = end;
             }
-        }
-        for (int x = w0; x < w1; ++x) {
-            const int i = begin + x * 32 + lane;
-            const bool in = x * 32 + lane < size;
-            const bool stay = (kept[x] >> lane) & 1u;
-            const bool hole = in && !stay && i < nn;
-            const uint32_t bits = __ballot_sync(0xffffffffu, hole);
-            if (hole) {
-                const uint32_t r = h_rank + __popc(bits & ((1u << lane) - 1u));
-                if constexpr (kOne)
-                    keys[r] = static_cast<uint32_t>(i);
-                else
-                    st_cluster_u32(keys_addr + 4u * (r % static_cast<uint32_t>(slice)), r / static_cast<uint32_t>(slice),
-                                   static_cast<uint32_t>(i));
+            const int holes = __syncthreads_count(static_cast<int>(threadIdx.x) < e && sh.leaving[threadIdx.x] < nn);
+            for (int i = threadIdx.x; i < nn; i += kEvThreads) src[i] = i;
+            if (in_place && warp < holes) copy_entry<D>(p.from, row0 + sh.late[warp], row0 + sh.hole[warp]);
+            __syncthreads();
+            if (static_cast<int>(threadIdx.x) < holes) src[sh.hole[threadIdx.x]] = sh.late[threadIdx.x];
+            copied = true;
+        } else {
+            // 1. threshold: the entries whose upper bits equal `prefix` are still open
+            uint32_t prefix = 0u;
+            uint32_t want = static_cast<uint32_t>(nn), open = 0u;  // entries to take among the open ones; those of the bin
+#pragma unroll 1
+            for (int down = 24; down >= 0; down -= 8) {
+#pragma unroll 4
+                for (int i = 4 * threadIdx.x; i < size; i += 4 * kEvThreads) {
+                    const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
+                    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (i + j < size && (down == 24 || (k[j] >> (down + 8)) == prefix))
+                            atomicAdd(&sh.hist[((k[j] >> down) & 255u) * 32 + lane], 1u);
+                }
+                __syncthreads();
+                // four threads per bin, each eight of its counters, in an order that keeps the banks apart
+                const int bin = threadIdx.x / 4;
+                uint32_t sum = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t& h = sh.hist[bin * 32 + ((threadIdx.x % 4 * 8 + i + bin) & 31)];
+                    sum += h;
+                    h = 0u;
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (threadIdx.x % 4 == 0) sh.bins[bin] = sum;
+                sync_all();
+                if constexpr (!kOne) {
+                    if (threadIdx.x < 256) {
+                        uint32_t t = 0u;
+                        for (uint32_t r = 0; r < cs; ++r) t += ld_cluster_u32(smem_u32(&sh.bins[threadIdx.x]), r);
+                        sh.total[threadIdx.x] = t;
+                    }
+                    cluster_sync_all();  // and every CTA has read the others' sums
+                }
+                if (warp == 0) {
+                    // from the top bin down: lane l holds bins 255 - 8 l .. 248 - 8 l
+                    const uint4* t4 = reinterpret_cast<const uint4*>(kOne ? sh.bins : sh.total) + (31 - lane) * 2;
+                    const uint4 lo = t4[0], hi = t4[1];
+                    const uint32_t c[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+                    const uint32_t all = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
+                    uint32_t above = all;
+#pragma unroll
+                    for (int o = 1; o < 32; o *= 2) {
+                        const uint32_t y = __shfl_up_sync(0xffffffffu, above, o);
+                        if (lane >= o) above += y;
+                    }
+                    above -= all;
+                    if (above < want && want <= above + all) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (above < want && want <= above + c[i]) {
+                                sh.pick[0] = static_cast<uint32_t>(255 - 8 * lane - i);
+                                sh.pick[1] = above;
+                                sh.pick[2] = c[i];
+                            }
+                            above += c[i];
+                        }
+                    }
+                }
+                __syncthreads();
+                prefix = (prefix << 8) | sh.pick[0];
+                want -= sh.pick[1];
+                open = sh.pick[2];
+                if (kOne && down > 0 && open <= kEvList) {
+                    // few entries are open: each against all of them.  Those with fewer than `want` greater ones,
+                    // and at least that many greater or equal, equal the threshold
+#pragma unroll 4
+                    for (int i = 4 * threadIdx.x; i < size; i += 4 * kEvThreads) {
+                        const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
+                        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (i + j < size && (k[j] >> down) == prefix) sh.list[atomicAdd(&sh.listed, 1u)] = k[j];
+                    }
+                    __syncthreads();
+                    if (threadIdx.x < open) {
+                        const uint32_t k = sh.list[threadIdx.x];
+                        uint32_t more = 0u, equal = 0u;
+                        for (uint32_t i = 0; i < open; ++i) {
+                            const uint32_t o = sh.list[i];
+                            more += o > k ? 1u : 0u;
+                            equal += o == k ? 1u : 0u;
+                        }
+                        if (more < want && want <= more + equal) {  // every entry equal to the threshold writes the same
+                            sh.pick[0] = k;
+                            sh.pick[1] = more;
+                            sh.pick[2] = equal;
+                        }
+                    }
+                    __syncthreads();
+                    prefix = sh.pick[0];
+                    want -= sh.pick[1];
+                    open = sh.pick[2];
+                    break;
+                }
             }
-            h_rank += __popc(bits);
-            if (i < nn && stay) src[i] = i;
-        }
-        sync_all();
-        for (int x = w0; x < w1; ++x) {
-            const int i = begin + x * 32 + lane;
-            const bool mine = x * 32 + lane < size && ((kept[x] >> lane) & 1u) && i >= nn;
-            const uint32_t bits = __ballot_sync(0xffffffffu, mine);
-            if (mine) {
-                const uint32_t r = l_rank + __popc(bits & ((1u << lane) - 1u));
-                uint32_t hole;
-                if constexpr (kOne)
-                    hole = keys[r];
-                else
-                    hole = ld_cluster_u32(keys_addr + 4u * (r % static_cast<uint32_t>(slice)),
-                                          r / static_cast<uint32_t>(slice));
-                src[hole] = i;
+            // 2. a bit per entry, words in turn to the warps
+            const uint32_t T = prefix;  // `want` of the `open` entries equal to T are kept
+            const int words = (size + 31) / 32;
+#pragma unroll 4
+            for (int x = warp; x < words; x += kEvWarps) {
+                const int i = x * 32 + lane;
+                const uint32_t k = i < size ? keys[i] : 0u;
+                const uint32_t equal = __ballot_sync(0xffffffffu, i < size && k == T);
+                const uint32_t more = __ballot_sync(0xffffffffu, i < size && k > T);
+                if (lane == 0) {
+                    sh.kept[x] = more | (want == open ? equal : 0u);
+                    sh.equal[x] = equal;
+                }
             }
-            l_rank += __popc(bits);
+            __syncthreads();
+            const int x0 = 2 * static_cast<int>(threadIdx.x);  // this thread's words: x0, x0 + 1
+            if (want < open) {  // of the entries equal to T the first `want`, over the cluster
+                const uint32_t e0 = x0 < words ? sh.equal[x0] : 0u, e1 = x0 + 1 < words ? sh.equal[x0 + 1] : 0u;
+                uint32_t all;
+                uint32_t before = block_prefix(__popc(e0) + __popc(e1), sh.warp_count, &all);
+                if constexpr (!kOne) {
+                    if (threadIdx.x == 0) sh.count[0] = all;
+                    cluster_sync_all();
+                    for (uint32_t r = 0; r < rank; ++r) before += ld_cluster_u32(smem_u32(&sh.count[0]), r);
+                    cluster_sync_all();  // count is written again below
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t bits = i == 0 ? e0 : e1;
+                    const uint32_t n_bits = __popc(bits);
+                    const int take = static_cast<int>(want) - static_cast<int>(before);
+                    if (take < static_cast<int>(n_bits)) {
+                        uint32_t some = 0u;
+                        for (int j = 0; j < take; ++j) {  // the lowest `take` bits
+                            some |= bits & (0u - bits);
+                            bits &= bits - 1u;
+                        }
+                        bits = some;
+                    }
+                    if (x0 + i < words) sh.kept[x0 + i] |= bits;
+                    before += n_bits;
+                }
+            }
+            // 3. ranks of holes and late entries: prefixes by word
+            uint32_t n0 = 0u, n1 = 0u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (x0 + i < words) {
+                    const uint32_t stay = sh.kept[x0 + i], below = low_bits(nn - begin - (x0 + i) * 32);
+                    const uint32_t n_i = static_cast<uint32_t>(__popc(low_bits(size - (x0 + i) * 32) & below & ~stay)) |
+                                         static_cast<uint32_t>(__popc(stay & ~below)) << 16;
+                    if (i == 0) n0 = n_i;
+                    else n1 = n_i;
+                }
+            uint32_t all;
+            const uint32_t before = block_prefix(n0 + n1, sh.warp_count, &all);
+            if (x0 < words) sh.before[x0] = before;
+            if (x0 + 1 < words) sh.before[x0 + 1] = before + n0;
+            uint32_t h_first = 0u, l_first = 0u;  // of earlier CTAs
+            if constexpr (kOne) {
+                __syncthreads();
+            } else {
+                if (threadIdx.x == 0) {
+                    sh.count[0] = all & 0xFFFFu;
+                    sh.count[1] = all >> 16;
+                }
+                cluster_sync_all();  // also every key was read: the slices now hold the list of holes
+                for (uint32_t r = 0; r < rank; ++r) {
+                    h_first += ld_cluster_u32(smem_u32(&sh.count[0]), r);
+                    l_first += ld_cluster_u32(smem_u32(&sh.count[1]), r);
+                }
+            }
+            const int low_words = min(words, max(0, (nn - begin + 31) / 32));  // words with slots below nn
+#pragma unroll 2
+            for (int x = warp; x < low_words; x += kEvWarps) {
+                const int i = begin + x * 32 + lane;
+                const uint32_t stay = sh.kept[x];
+                const uint32_t holes = low_bits(size - x * 32) & low_bits(nn - begin - x * 32) & ~stay;
+                if ((holes >> lane) & 1u) {
+                    const uint32_t r = h_first + (sh.before[x] & 0xFFFFu) + __popc(holes & ((1u << lane) - 1u));
+                    if constexpr (kOne)
+                        keys[r] = static_cast<uint32_t>(i);
+                    else
+                        st_cluster_u32(keys_addr + 4u * (r % static_cast<uint32_t>(slice)),
+                                       r / static_cast<uint32_t>(slice), static_cast<uint32_t>(i));
+                } else if (i < nn && ((stay >> lane) & 1u)) {
+                    src[i] = i;
+                }
+            }
+            sync_all();
+#pragma unroll 2
+            for (int x = max(0, nn - begin) / 32 + warp; x < words; x += kEvWarps) {
+                const uint32_t late = sh.kept[x] & ~low_bits(nn - begin - x * 32);
+                if ((late >> lane) & 1u) {
+                    const uint32_t r = l_first + (sh.before[x] >> 16) + __popc(late & ((1u << lane) - 1u));
+                    uint32_t hole;
+                    if constexpr (kOne)
+                        hole = keys[r];
+                    else
+                        hole = ld_cluster_u32(keys_addr + 4u * (r % static_cast<uint32_t>(slice)),
+                                              r / static_cast<uint32_t>(slice));
+                    src[hole] = begin + x * 32 + lane;
+                }
+            }
         }
     } else {
         for (int i = static_cast<int>(rank) * kEvThreads + threadIdx.x; i < nn; i += static_cast<int>(cs) * kEvThreads)
@@ -310,19 +493,41 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
     for (long long i = nn + static_cast<long long>(rank) * kEvThreads + threadIdx.x; i < p.keep;
          i += static_cast<long long>(cs) * kEvThreads)
         src[i] = -1;
-    // 4. copies, 32 slots per warp and step (src was written by the whole cluster)
-    sync_all();
-    const int step = static_cast<int>(cs) * kEvWarps * 32;
-    for (int j0 = (static_cast<int>(rank) * kEvWarps + warp) * 32; j0 < nn; j0 += step) {
-        const int j = j0 + lane;
-        int from = j < nn ? __ldcg(src + j) : -1;
-        if (in_place && from == j) from = -1;
-        if (__any_sync(0xffffffffu, from >= 0)) copy_entries<D>(p.from, p.to, row0, from, to0 + j0);
+    // 4. copies in place, 32 slots per warp and step (src was written by the whole cluster); those into another
+    // cache move every entry and have a kernel of their own, on every SM
+    if (in_place && !copied) {
+        sync_all();
+        const int step = static_cast<int>(cs) * kEvWarps * 32;
+        for (int j0 = (static_cast<int>(rank) * kEvWarps + warp) * 32; j0 < nn; j0 += step) {
+            const int j = j0 + lane;
+            int from = j < nn ? __ldcg(src + j) : -1;
+            if (from == j) from = -1;
+            if (__any_sync(0xffffffffu, from >= 0)) copy_entries<D>(p.from, p.to, row0, from, to0 + j0);
+        }
+    } else if (!kOne) {
+        sync_all();  // no CTA leaves while its list is read
     }
     if (advance && head % p.from.H_kv == 0 && rank == 0 && threadIdx.x == 0) {
         p.counts_out[b] = nn;
         p.counts_out[p.from.B + b] = seen;
     }
+}
+
+// The entries named by src into another cache, 32 a warp; grid: heads x
+// blocks of kCopyRows slots.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyRows = kCopyThreads;
+template <int D>
+__global__ void __launch_bounds__(kCopyThreads) kv4_evict_copy_kernel(const __grid_constant__ Kv4EvictParams p, int blocks) {
+    const int head = static_cast<int>(blockIdx.x) / blocks;
+    const int j0 = (static_cast<int>(blockIdx.x) % blocks) * kCopyRows + static_cast<int>(threadIdx.x) / 32 * 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (j0 >= p.keep) return;
+    const int j = j0 + static_cast<int>(threadIdx.x) % 32;
+    const int from = j < p.keep ? p.src[static_cast<long long>(head) * p.keep + j] : -1;
+    if (__any_sync(0xffffffffu, from >= 0))
+        copy_entries<D>(p.from, p.to, static_cast<long long>(head) * p.from.capacity, from,
+                        static_cast<long long>(head) * p.to.capacity + j0);
 }
 
 // counts_out where it is the counts that the clusters of a sequence read.
@@ -332,14 +537,12 @@ __global__ void kv4_evict_counts_kernel(const Kv4EvictParams p) {
 }
 
 template <int D>
-cudaError_t launch_evict(const Kv4EvictParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_evict(const Kv4EvictParams& p, cudaStream_t stream) {
     const int heads = p.from.B * p.from.H_kv;
-    // as many CTAs per head as leave no SM idle while each has kEvShare keys to look at, and as its keys need
-    constexpr int kEvShare = 8192;
+    // one CTA per head unless its keys need more: at 16384 slots and 64 heads a cluster of two took 42000 cycles
+    // to the list of sources, one CTA 33000 (a cluster's barriers and remote reads, four times over)
     int cs = 1;
-    while (cs < kEvMaxCluster && ((p.from.capacity + cs - 1) / cs > kEvMaxSlice ||
-                                  (2 * cs * heads <= sms && p.from.capacity / cs > kEvShare)))
-        cs *= 2;
+    while (cs < kEvMaxCluster && (p.from.capacity + cs - 1) / cs > kEvMaxSlice) cs *= 2;
     const int slice = ((p.from.capacity + cs - 1) / cs + 31) / 32 * 32;
     const size_t smem = sizeof(EvShared) + static_cast<size_t>(slice) * 4;
     auto kern = cs == 1 ? kv4_evict_kernel<D, true> : kv4_evict_kernel<D, false>;
@@ -362,14 +565,23 @@ cudaError_t launch_evict(const Kv4EvictParams& p, int sms, cudaStream_t stream) 
     cfg.numAttrs = cs == 1 ? 1 : 2;
     e = cudaLaunchKernelEx(&cfg, kern, p, slice, advance);
     if (e != cudaSuccess) return e;
+    if (p.to.codes[0] != p.from.codes[0]) {
+        const int blocks = (p.keep + kCopyRows - 1) / kCopyRows;
+        cfg.gridDim = dim3(static_cast<unsigned>(heads) * static_cast<unsigned>(blocks));
+        cfg.blockDim = dim3(kCopyThreads);
+        cfg.dynamicSmemBytes = 0;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, kv4_evict_copy_kernel<D>, p, blocks);
+        if (e != cudaSuccess) return e;
+    }
     if (!advance) kv4_evict_counts_kernel<<<(p.from.B + 127) / 128, 128, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_evict(const Kv4EvictParams& p, int sms, cudaStream_t stream) {
-    return p.from.d == 128 ? launch_evict<128>(p, sms, stream) : launch_evict<64>(p, sms, stream);
+cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream) {
+    return p.from.d == 128 ? launch_evict<128>(p, stream) : launch_evict<64>(p, stream);
 }
 
 }  // namespace fa

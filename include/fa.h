@@ -450,7 +450,8 @@ size_t fa_kv4_fwd_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t N_q
  * Slot j < min(length, keep) keeps its entry where that is kept; the other
  * slots there take, in order, the kept entries from behind them.  Slots at or
  * behind the new length are left as they were.  keep >= 1; capacity up to
- * 393216.  One kernel (two when counts_out is the first cache's counts).
+ * 393216.  One kernel, another for copies into `to` and one to advance the
+ * first cache's own counts.
  */
 int fa_kv4_evict(const fa_kv4_cache_t* cache, int64_t keep, int64_t sinks, int64_t recent,
                  const float* rank_by, const fa_kv4_cache_t* to, int32_t* src, int32_t* counts_out,
