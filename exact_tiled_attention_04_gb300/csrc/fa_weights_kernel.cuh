@@ -14,16 +14,18 @@
 // terms are added first and then added to the running sum, which keeps the
 // rounding of a sum over 10^5 rows near 2^-22 of it.
 //
-// One CTA owns 256 keys of one key/value head (two tiles of 128, resident in
-// shared memory, so a query tile that was loaded serves two products) and
-// sweeps the rows of the head's query heads, 128 a step:
-//   warps 0-15  four warpgroups: key tile w % 2, steps of parity w / 2; each
-//               owns one 128-column buffer of tensor memory
+// One CTA owns 256 keys of one key/value head (two tiles of 128) and sweeps
+// the rows of the head's query heads, 128 a step.  The keys are copied into
+// tensor memory once, as the products' A operand: with both operands in
+// shared memory a 128 x 128 product reads 128 bytes of it a clock, all it
+// gives, where this way it reads 64.
+//   warps 0-15  four warpgroups; product n (step n / 2, key tile n % 2) goes
+//               to warpgroup n % 4 through buffer n % 3 (128 columns)
 //   warp 16     tensor-core issuer (one thread) and tensor-memory owner
 //   warp 17     TMA producer
-// Bound by the exponentials and the products alike: 128 x 128 scores take 512
-// clocks of each at d = 128 (32 exponentials a clock and SM), half of the
-// latter at d = 64.
+// Bound by the exponentials, the products and the issue slots alike: 128 x 128
+// scores take 512 clocks of the first two at d = 128 (32 exponentials a clock
+// and SM; the products half of that at d = 64) and about 530 issue slots.
 //
 // Causal: the rows below a tile's diagonal are swept from the first one that
 // sees any of its keys; only the first steps are masked.  When the key blocks
@@ -55,6 +57,9 @@ struct WtCfg {
     static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr uint32_t kFmt = F16 ? 0u : 1u;
     static constexpr uint32_t kIdesc = instr_desc(kFmt, false, false, 128, 128);
+    static constexpr int kBufs = 3;                                  // score buffers
+    static constexpr uint32_t kColK = 0;                             // keys: D / 2 columns a tile
+    static constexpr uint32_t kColS = 128;                           // [kBufs] x 128
     static constexpr int kOffK = 0;                                  // two tiles
     static constexpr int kOffQ = kOffK + 2 * kTileBytes;             // [kStages]
     static constexpr int kOffLse = kOffQ + kStages * kTileBytes;     // float [warpgroup][2][128]
@@ -63,9 +68,10 @@ struct WtCfg {
     static constexpr int kBarK = 0;
     static constexpr int kBarFull = 1;                    // [kStages] a query tile landed
     static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] its products are done
-    static constexpr int kBarS = kBarEmpty + kStages;     // [4] scores ready
-    static constexpr int kBarSFree = kBarS + 4;           // [4] scores read
-    static constexpr int kBarDrain = kBarSFree + 4;
+    static constexpr int kBarS = kBarEmpty + kStages;     // [warpgroups] its product is done
+    static constexpr int kBarSFree = kBarS + kWtWarpgroups;  // [kBufs] scores read
+    static constexpr int kBarKSet = kBarSFree + kBufs;    // keys are in tensor memory
+    static constexpr int kBarDrain = kBarKSet + 1;
     static constexpr int kNumBars = kBarDrain + 1;
     static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
@@ -121,10 +127,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             mbar_init(bar(C::kBarFull + s), 1);
             mbar_init(bar(C::kBarEmpty + s), 1);
         }
-        for (int b = 0; b < 4; ++b) {
-            mbar_init(bar(C::kBarS + b), 1);
-            mbar_init(bar(C::kBarSFree + b), 4);
-        }
+        for (int w = 0; w < kWtWarpgroups; ++w) mbar_init(bar(C::kBarS + w), 1);
+        for (int b = 0; b < C::kBufs; ++b) mbar_init(bar(C::kBarSFree + b), 4);
+        mbar_init(bar(C::kBarKSet), static_cast<uint32_t>(4 * tiles));
         mbar_init(bar(C::kBarDrain), 1);
         *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
         mbar_init_fence();
@@ -166,24 +171,25 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
     } else if (warp == kWtMmaWarp) {
         if (lane == 0 && T > 0 && !skip) {
-            bool ok = wait_phase(bar(C::kBarK), 0, abort_flag, wp, 93);
+            bool ok = wait_phase(bar(C::kBarKSet), 0, abort_flag, wp, 93);
+            tc_fence_after();
+            int n = 0;
             for (int j = 0; ok && j < T; ++j) {
                 const int s = j % C::kStages;
                 ok = wait_phase(bar(C::kBarFull + s), (j / C::kStages) & 1, abort_flag, wp, 94);
-                for (int i = 0; ok && i < tiles; ++i) {
-                    const int b = (j & 1) * 2 + i;
-                    ok = wait_phase(bar(C::kBarSFree + b), ((j >> 1) & 1) ^ 1, abort_flag, wp, 95);
+                for (int i = 0; ok && i < tiles; ++i, ++n) {
+                    const int b = n % C::kBufs;
+                    ok = wait_phase(bar(C::kBarSFree + b), ((n / C::kBufs) & 1) ^ 1, abort_flag, wp, 95);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < C::kSteps; ++kk) {
                         const uint32_t off = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
-                        mma_ss<false>(tmem + 128u * b,
-                                      smem_desc_sw128(sbase + C::kOffK + i * C::kTileBytes + off, 16, 1024),
+                        mma_ts<false>(tmem + C::kColS + 128u * b, tmem + C::kColK + (D / 2) * i + 8 * kk,
                                       smem_desc_sw128(sbase + C::kOffQ + s * C::kTileBytes + off, 16, 1024), C::kIdesc,
                                       kk > 0 ? 1u : 0u);
                     }
-                    tc_commit(bar(C::kBarS + b));
+                    tc_commit(bar(C::kBarS + n % kWtWarpgroups));
                 }
                 if (ok) tc_commit(bar(C::kBarEmpty + s));
             }
@@ -192,13 +198,36 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
     } else {
         const int wg = warp / 4, t = static_cast<int>(threadIdx.x) % 128;
-        const int tile = wg % 2, parity = wg / 2;
-        const int b = parity * 2 + tile;
+        const int tile = tiles == 2 ? wg % 2 : 0;
         const int key = key0 + 128 * tile + t;
-        const uint32_t tS = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 128u * b;
+        const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
         float* neg = reinterpret_cast<float*>(smem + C::kOffLse) + wg * 256;
         float total = 0.0f;
-        if (tile < tiles && !skip) {
+        bool ok = T > 0 && !skip;
+        if (ok && wg < tiles) {
+            // this thread's key into tensor memory: its 16-byte pieces lie permuted by row % 8
+            ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarK), 0, abort_flag, wp, 98));
+            if (ok) {
+#pragma unroll
+                for (int a = 0; a < C::kAtoms; ++a) {
+                    const uint8_t* row = smem + C::kOffK + wg * C::kTileBytes + a * C::kAtomBytes + t * 128;
+                    uint32_t r[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(row + ((c ^ (t & 7)) << 4));
+                        r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+                    }
+                    tmem_st32(tmem + lanes + C::kColK + (D / 2) * wg + 32 * a, r);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kBarKSet));
+            }
+        }
+        if (T > 0 && !skip) {
+            // products n = wg, wg + 4, .. of T * tiles
+            const int products = T * tiles;
             // -lse2 of row t of step j; -inf where the row counts nothing
             auto row_neg = [&](int j) -> float {
                 if (j >= T) return 0.0f;
@@ -209,14 +238,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 return v == -INFINITY ? -INFINITY : v * -1.4426950408889634f;
             };
             const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-            float next = row_neg(parity);
-            bool ok = true;
-            for (int j = parity; j < T; j += 2) {
-                float* buf = neg + ((j >> 1) & 1) * 128;
+            float next = row_neg(wg / tiles);
+            for (int n = wg; n < products; n += kWtWarpgroups) {
+                const int j = n / tiles, b = n % C::kBufs;
+                const uint32_t tS = tmem + lanes + C::kColS + 128u * b;
+                float* buf = neg + ((n / kWtWarpgroups) & 1) * 128;
                 buf[t] = next;
-                next = row_neg(j + 2);
+                next = row_neg((n + kWtWarpgroups) / tiles);
                 named_barrier_sync(1 + wg, 128);
-                ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarS + b), (j >> 1) & 1, abort_flag, wp, 97));
+                ok = ok && __all_sync(0xffffffffu, wait_phase(bar(C::kBarS + wg), (n / kWtWarpgroups) & 1, abort_flag, wp, 97));
                 // a warp that gave up keeps meeting the barrier above
                 if (!ok) continue;
                 tc_fence_after();
@@ -228,25 +258,28 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const bool masked = __any_sync(0xffffffffu, first_col > 0);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t r[32];
-                    tmem_ld32(tS + 32u * q, r);
-                    tmem_ld_wait(r);
-                    if (q == 3) {  // the scores are in registers: the next product may start
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t r[2][32];
+                    tmem_ld32(tS + 64u * q, r[0]);
+                    tmem_ld32(tS + 64u * q + 32u, r[1]);
+                    tmem_ld_wait(r[0]);
+                    tmem_ld_wait(r[1]);
+                    if (q == 1) {  // the scores are in registers: the buffer's next product may start
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::kBarSFree + b));
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 n4 = *reinterpret_cast<const float4*>(buf + 32 * q + i);
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 n4 = *reinterpret_cast<const float4*>(buf + 64 * q + i);
+                        const uint32_t* x4 = &r[i / 32][i % 32];
                         float x[4];
-                        f2_unpack(f2_fma(f2_pack(u2f(r[i]), u2f(r[i + 1])), c2, f2_pack(n4.x, n4.y)), x[0], x[1]);
-                        f2_unpack(f2_fma(f2_pack(u2f(r[i + 2]), u2f(r[i + 3])), c2, f2_pack(n4.z, n4.w)), x[2], x[3]);
+                        f2_unpack(f2_fma(f2_pack(u2f(x4[0]), u2f(x4[1])), c2, f2_pack(n4.x, n4.y)), x[0], x[1]);
+                        f2_unpack(f2_fma(f2_pack(u2f(x4[2]), u2f(x4[3])), c2, f2_pack(n4.z, n4.w)), x[2], x[3]);
                         if (masked) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (32 * q + i + e < first_col) x[e] = -INFINITY;
+                                if (64 * q + i + e < first_col) x[e] = -INFINITY;
                         }
                         sum[0] = f2_add(sum[0], f2_pack(ex2(x[0]), ex2(x[1])));
                         sum[1] = f2_add(sum[1], f2_pack(ex2(x[2]), ex2(x[3])));
@@ -264,16 +297,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         cluster_sync_all();
     else
         __syncthreads();
-    // two warpgroups and every CTA of the cluster add up in order
+    // the warpgroups and every CTA of the cluster add up in order
     if (split == 0 && threadIdx.x < 256) {
         const int tile = static_cast<int>(threadIdx.x) / 128, t = static_cast<int>(threadIdx.x) % 128;
         const int key = key0 + 128 * tile + t;
         if (key < p.Nkv) {
             const long long at = static_cast<long long>(kvh) * p.weight_stride + key;
             float s = 0.0f;
+            // one tile: the four warpgroups took its products in turn; two: those of its parity
             for (int r = 0; r < p.splits; ++r)
-                for (int half = 0; half < 2; ++half) {
-                    const int i = (half * 2 + tile) * 128 + t;
+                for (int w = tile; w < kWtWarpgroups; w += tiles) {
+                    const int i = w * 128 + t;
                     float v;
                     if (p.splits > 1)
                         asm volatile("ld.shared::cluster.f32 %0, [%1];"
