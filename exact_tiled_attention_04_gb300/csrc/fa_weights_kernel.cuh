@@ -14,18 +14,25 @@
 // terms are added first and then added to the running sum, which keeps the
 // rounding of a sum over 10^5 rows near 2^-22 of it.
 //
-// One CTA owns 256 keys of one key/value head (two tiles of 128) and sweeps
-// the rows of the head's query heads, 128 a step.  The keys are copied into
-// tensor memory once, as the products' A operand: with both operands in
-// shared memory a 128 x 128 product reads 128 bytes of it a clock, all it
-// gives, where this way it reads 64.
-//   warps 0-15  four warpgroups; product n (step n / 2, key tile n % 2) goes
-//               to warpgroup n % 4 through buffer n % 3 (128 columns)
-//   warp 16     tensor-core issuer (one thread) and tensor-memory owner
-//   warp 17     TMA producer
+// One CTA owns 256 keys of one key/value head (two tiles of 128, resident in
+// shared memory, so a query tile that was loaded serves two products) and
+// sweeps the rows of the head's query heads, 128 a step:
+//   warps 0-15   four warpgroups; product n (step n / 2, key tile n % 2) goes
+//                to warpgroup n % 4, which owns 128 columns of tensor memory
+//                and gives them back once its second 64 are in registers
+//   warps 16, 17 tensor-core issuers, one thread per key tile; 16 owns the
+//                tensor memory
+//   warp 18      TMA producer
 // Bound by the exponentials, the products and the issue slots alike: 128 x 128
 // scores take 512 clocks of the first two at d = 128 (32 exponentials a clock
 // and SM; the products half of that at d = 64) and about 530 issue slots.
+// Each issuer's barrier waits, about 180 clocks a product, and the commits, 35
+// each, come on top: two issuers hide one another's, and a query stage is
+// given back by the warps that read the scores instead of by a commit.
+// Measured at B = 2, H = 32/8, N = 8192, d = 128, causal: one issuer 588 us;
+// keys in tensor memory and three buffers 566; products of 64 rows, whose
+// columns are free sooner, 800 (an N = 64 product takes 48 clocks a step
+// instead of 32).
 //
 // Causal: the rows below a tile's diagonal are swept from the first one that
 // sees any of its keys; only the first steps are masked.  When the key blocks
@@ -44,8 +51,8 @@ namespace fa {
 
 constexpr int kWtWarpgroups = 4;
 constexpr int kWtSoftmaxWarps = 4 * kWtWarpgroups;
-constexpr int kWtMmaWarp = kWtSoftmaxWarps;
-constexpr int kWtLoadWarp = kWtMmaWarp + 1;
+constexpr int kWtMmaWarp = kWtSoftmaxWarps;  // and the next: one issuer per key tile
+constexpr int kWtLoadWarp = kWtMmaWarp + 2;
 constexpr int kWtThreads = (kWtLoadWarp + 1) * 32;
 
 template <int D, bool F16>
@@ -57,9 +64,6 @@ struct WtCfg {
     static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr uint32_t kFmt = F16 ? 0u : 1u;
     static constexpr uint32_t kIdesc = instr_desc(kFmt, false, false, 128, 128);
-    static constexpr int kBufs = 3;                                  // score buffers
-    static constexpr uint32_t kColK = 0;                             // keys: D / 2 columns a tile
-    static constexpr uint32_t kColS = 128;                           // [kBufs] x 128
     static constexpr int kOffK = 0;                                  // two tiles
     static constexpr int kOffQ = kOffK + 2 * kTileBytes;             // [kStages]
     static constexpr int kOffLse = kOffQ + kStages * kTileBytes;     // float [warpgroup][2][128]
@@ -67,12 +71,11 @@ struct WtCfg {
     static constexpr int kOffBar = kOffSum + kWtWarpgroups * 128 * 4;
     static constexpr int kBarK = 0;
     static constexpr int kBarFull = 1;                    // [kStages] a query tile landed
-    static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] its products are done
-    static constexpr int kBarS = kBarEmpty + kStages;     // [warpgroups] its product is done
-    static constexpr int kBarSFree = kBarS + kWtWarpgroups;  // [kBufs] scores read
-    static constexpr int kBarKSet = kBarSFree + kBufs;    // keys are in tensor memory
-    static constexpr int kBarDrain = kBarKSet + 1;
-    static constexpr int kNumBars = kBarDrain + 1;
+    static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] its scores were read
+    static constexpr int kBarS = kBarEmpty + kStages;     // [warpgroups] scores ready
+    static constexpr int kBarSFree = kBarS + kWtWarpgroups;  // [warpgroups] scores read
+    static constexpr int kBarDrain = kBarSFree + kWtWarpgroups;  // [2] an issuer's products are done
+    static constexpr int kNumBars = kBarDrain + 2;
     static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr size_t kSmemBytes = static_cast<size_t>(kOffAbort + 4) + 1024;
@@ -125,12 +128,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         mbar_init(bar(C::kBarK), 1);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(C::kBarFull + s), 1);
-            mbar_init(bar(C::kBarEmpty + s), 1);
+            mbar_init(bar(C::kBarEmpty + s), static_cast<uint32_t>(4 * tiles));
         }
-        for (int w = 0; w < kWtWarpgroups; ++w) mbar_init(bar(C::kBarS + w), 1);
-        for (int b = 0; b < C::kBufs; ++b) mbar_init(bar(C::kBarSFree + b), 4);
-        mbar_init(bar(C::kBarKSet), static_cast<uint32_t>(4 * tiles));
-        mbar_init(bar(C::kBarDrain), 1);
+        for (int w = 0; w < kWtWarpgroups; ++w) {
+            mbar_init(bar(C::kBarS + w), 1);
+            mbar_init(bar(C::kBarSFree + w), 4);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(bar(C::kBarDrain + i), 1);
         *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
         mbar_init_fence();
     }
@@ -169,93 +173,70 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 wait_phase(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, wp, 92, false);
             }
         }
-    } else if (warp == kWtMmaWarp) {
-        if (lane == 0 && T > 0 && !skip) {
-            bool ok = wait_phase(bar(C::kBarKSet), 0, abort_flag, wp, 93);
-            tc_fence_after();
-            int n = 0;
+    } else if (warp >= kWtMmaWarp) {
+        const int i = warp - kWtMmaWarp;  // key tile
+        if (lane == 0 && T > 0 && !skip && i < tiles) {
+            // a k-step's descriptor is the tile's plus a constant
+            const uint64_t dk0 = smem_desc_sw128(sbase + C::kOffK + i * C::kTileBytes, 16, 1024);
+            const uint64_t dq0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+            bool ok = wait_phase(bar(C::kBarK), 0, abort_flag, wp, 93);
             for (int j = 0; ok && j < T; ++j) {
-                const int s = j % C::kStages;
-                ok = wait_phase(bar(C::kBarFull + s), (j / C::kStages) & 1, abort_flag, wp, 94);
-                for (int i = 0; ok && i < tiles; ++i, ++n) {
-                    const int b = n % C::kBufs;
-                    ok = wait_phase(bar(C::kBarSFree + b), ((n / C::kBufs) & 1) ^ 1, abort_flag, wp, 95);
-                    if (!ok) break;
-                    tc_fence_after();
+                const int s = j % C::kStages, n = j * tiles + i, w = n % kWtWarpgroups;
+                ok = wait_phase(bar(C::kBarFull + s), (j / C::kStages) & 1, abort_flag, wp, 94) &&
+                     wait_phase(bar(C::kBarSFree + w), ((n / kWtWarpgroups) & 1) ^ 1, abort_flag, wp, 95);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dq = dq0 + static_cast<uint64_t>((s * C::kTileBytes) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < C::kSteps; ++kk) {
-                        const uint32_t off = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
-                        mma_ts<false>(tmem + C::kColS + 128u * b, tmem + C::kColK + (D / 2) * i + 8 * kk,
-                                      smem_desc_sw128(sbase + C::kOffQ + s * C::kTileBytes + off, 16, 1024), C::kIdesc,
-                                      kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit(bar(C::kBarS + n % kWtWarpgroups));
+                for (int kk = 0; kk < C::kSteps; ++kk) {
+                    constexpr uint32_t kAtom = C::kAtomBytes;
+                    const uint32_t off = ((kk * 32) / 128 * kAtom + (kk * 32) % 128) >> 4;
+                    mma_ss<false>(tmem + 128u * w, dk0 + off, dq + off, C::kIdesc, kk > 0 ? 1u : 0u);
                 }
-                if (ok) tc_commit(bar(C::kBarEmpty + s));
+                tc_commit(bar(C::kBarS + w));
             }
-            tc_commit(bar(C::kBarDrain));
-            wait_phase(bar(C::kBarDrain), 0, abort_flag, wp, 96, false);
+            tc_commit(bar(C::kBarDrain + i));
+            wait_phase(bar(C::kBarDrain + i), 0, abort_flag, wp, 96, false);
         }
     } else {
         const int wg = warp / 4, t = static_cast<int>(threadIdx.x) % 128;
         const int tile = tiles == 2 ? wg % 2 : 0;
         const int key = key0 + 128 * tile + t;
-        const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+        const uint32_t tS = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 128u * wg;
         float* neg = reinterpret_cast<float*>(smem + C::kOffLse) + wg * 256;
         float total = 0.0f;
-        bool ok = T > 0 && !skip;
-        if (ok && wg < tiles) {
-            // this thread's key into tensor memory: its 16-byte pieces lie permuted by row % 8
-            ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarK), 0, abort_flag, wp, 98));
-            if (ok) {
-#pragma unroll
-                for (int a = 0; a < C::kAtoms; ++a) {
-                    const uint8_t* row = smem + C::kOffK + wg * C::kTileBytes + a * C::kAtomBytes + t * 128;
-                    uint32_t r[32];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(row + ((c ^ (t & 7)) << 4));
-                        r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
-                    }
-                    tmem_st32(tmem + lanes + C::kColK + (D / 2) * wg + 32 * a, r);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::kBarKSet));
-            }
-        }
         if (T > 0 && !skip) {
-            // products n = wg, wg + 4, .. of T * tiles
-            const int products = T * tiles;
-            // -lse2 of row t of step j; -inf where the row counts nothing
-            auto row_neg = [&](int j) -> float {
-                if (j >= T) return 0.0f;
-                const int step = begin + j, h = step / per_head;
-                const int row = first_row + 128 * (step - h * per_head) + t;
-                if (row >= p.Nq) return -INFINITY;
-                const float v = __ldg(p.lse + (head0 + h) * p.Nq + row);
+            // products n = wg, wg + 4, .. of T * tiles; the step of the next one to load is row block
+            // `block_in_head` of query head `head`
+            const int products = T * tiles, ahead = kWtWarpgroups / tiles;
+            int next_step = wg / tiles, head = (begin + next_step) / per_head;
+            int block_in_head = begin + next_step - head * per_head;
+            // -lse2 of row t of that step; -inf where the row counts nothing
+            auto row_neg = [&]() -> float {
+                const int row = first_row + 128 * block_in_head + t;
+                if (next_step >= T || row >= p.Nq) return -INFINITY;
+                const float v = __ldg(p.lse + (head0 + head) * p.Nq + row);
                 return v == -INFINITY ? -INFINITY : v * -1.4426950408889634f;
             };
             const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-            float next = row_neg(wg / tiles);
-            for (int n = wg; n < products; n += kWtWarpgroups) {
-                const int j = n / tiles, b = n % C::kBufs;
-                const uint32_t tS = tmem + lanes + C::kColS + 128u * b;
-                float* buf = neg + ((n / kWtWarpgroups) & 1) * 128;
+            const int diagonal = p.causal ? key - p.causal_offset - first_row : -1;  // first row that sees the key
+            float next = row_neg();
+            uint32_t turn = 0;
+            bool ok = true;
+            for (int n = wg; n < products; n += kWtWarpgroups, ++turn) {
+                float* buf = neg + (turn & 1) * 128;
                 buf[t] = next;
-                next = row_neg((n + kWtWarpgroups) / tiles);
+                const int first_col = diagonal - 128 * block_in_head;  // of this step
+                next_step += ahead;
+                for (block_in_head += ahead; block_in_head >= per_head; ++head) block_in_head -= per_head;
+                next = row_neg();
+                const bool masked = __any_sync(0xffffffffu, first_col > 0);
                 named_barrier_sync(1 + wg, 128);
-                ok = ok && __all_sync(0xffffffffu, wait_phase(bar(C::kBarS + wg), (n / kWtWarpgroups) & 1, abort_flag, wp, 97));
+                const int stage = n / tiles % C::kStages;
+                ok = ok && __all_sync(0xffffffffu, wait_phase(bar(C::kBarS + wg), turn & 1, abort_flag, wp, 97));
                 // a warp that gave up keeps meeting the barrier above
                 if (!ok) continue;
                 tc_fence_after();
-                int first_col = 0;  // first row of this step that sees the key
-                if (p.causal) {
-                    const int step = begin + j;
-                    first_col = key - p.causal_offset - first_row - 128 * (step - step / per_head * per_head);
-                }
-                const bool masked = __any_sync(0xffffffffu, first_col > 0);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -264,10 +245,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     tmem_ld32(tS + 64u * q + 32u, r[1]);
                     tmem_ld_wait(r[0]);
                     tmem_ld_wait(r[1]);
-                    if (q == 1) {  // the scores are in registers: the buffer's next product may start
+                    if (q == 1) {  // the scores are in registers: the next product may start
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C::kBarSFree + b));
+                        if (lane == 0) {
+                            mbar_arrive(bar(C::kBarSFree + wg));
+                            mbar_arrive(bar(C::kBarEmpty + stage));
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 64; i += 4) {
