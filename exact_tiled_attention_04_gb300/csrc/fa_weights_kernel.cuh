@@ -25,7 +25,7 @@
 //   warp 18      TMA producer
 // Bound by the exponentials, the products and the issue slots alike: 128 x 128
 // scores take 512 clocks of the first two at d = 128 (32 exponentials a clock
-// and SM; the products half of that at d = 64) and about 530 issue slots.
+// and SM; the products half of that at d = 64) and about 350 issue slots.
 // Each issuer's barrier waits, about 180 clocks a product, and the commits, 35
 // each, come on top: two issuers hide one another's, and a query stage is
 // given back by the warps that read the scores instead of by a commit.
@@ -66,11 +66,11 @@ struct WtCfg {
     static constexpr uint32_t kIdesc = instr_desc(kFmt, false, false, 128, 128);
     static constexpr int kOffK = 0;                                  // two tiles
     static constexpr int kOffQ = kOffK + 2 * kTileBytes;             // [kStages]
-    static constexpr int kOffLse = kOffQ + kStages * kTileBytes;     // float [warpgroup][2][128]
-    static constexpr int kOffSum = kOffLse + kWtWarpgroups * 2 * 128 * 4;  // float [warpgroup][128]
+    static constexpr int kOffLse = kOffQ + kStages * kTileBytes;     // float [kStages][128]: -lse2 of the rows
+    static constexpr int kOffSum = kOffLse + kStages * 128 * 4;  // float [warpgroup][128]
     static constexpr int kOffBar = kOffSum + kWtWarpgroups * 128 * 4;
     static constexpr int kBarK = 0;
-    static constexpr int kBarFull = 1;                    // [kStages] a query tile landed
+    static constexpr int kBarFull = 1;                    // [kStages] a query tile and its lse landed
     static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] its scores were read
     static constexpr int kBarS = kBarEmpty + kStages;     // [warpgroups] scores ready
     static constexpr int kBarSFree = kBarS + kWtWarpgroups;  // [warpgroups] scores read
@@ -81,6 +81,28 @@ struct WtCfg {
     static constexpr size_t kSmemBytes = static_cast<size_t>(kOffAbort + 4) + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
 };
+
+// Adds 2^(c r_i + neg_i) for 64 rows to the two pairs of sums; rows before
+// first_col are hidden (kMasked), whatever their scores are.
+template <bool kMasked>
+__device__ __forceinline__ void add_weights(const uint32_t (&r)[2][32], const float* neg, uint64_t c2, int first_col,
+                                            uint64_t (&sum)[2]) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 4) {
+        const float4 n4 = *reinterpret_cast<const float4*>(neg + i);
+        const uint32_t* x4 = &r[i / 32][i % 32];
+        float x[4];
+        f2_unpack(f2_fma(f2_pack(u2f(x4[0]), u2f(x4[1])), c2, f2_pack(n4.x, n4.y)), x[0], x[1]);
+        f2_unpack(f2_fma(f2_pack(u2f(x4[2]), u2f(x4[3])), c2, f2_pack(n4.z, n4.w)), x[2], x[3]);
+        if constexpr (kMasked) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < first_col) x[e] = -INFINITY;
+        }
+        sum[0] = f2_add(sum[0], f2_pack(ex2(x[0]), ex2(x[1])));
+        sum[1] = f2_add(sum[1], f2_pack(ex2(x[2]), ex2(x[3])));
+    }
+}
 
 // grid = B * H_kv * ceil(N_kv / 256) * p.splits, clusters of p.splits.
 template <int D, bool F16>
@@ -127,7 +149,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(bar(C::kBarK), 1);
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bar(C::kBarFull + s), 1);
+            mbar_init(bar(C::kBarFull + s), 2);  // the query tile, and its rows' lse
             mbar_init(bar(C::kBarEmpty + s), static_cast<uint32_t>(4 * tiles));
         }
         for (int w = 0; w < kWtWarpgroups; ++w) {
@@ -149,28 +171,59 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const bool skip = *abort_flag != 0u;
 
     if (warp == kWtLoadWarp) {
-        if (lane == 0 && T > 0 && !skip) {
+        if (T > 0 && !skip) {
             const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-            mbar_arrive_expect_tx(bar(C::kBarK), static_cast<uint32_t>(tiles) * C::kTileBytes);
-            for (int i = 0; i < tiles; ++i)
-                for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffK + i * C::kTileBytes + a * C::kAtomBytes, &map_k, bar(C::kBarK), a * 64,
-                                key0 + 128 * i, kvh, once);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(C::kBarK), static_cast<uint32_t>(tiles) * C::kTileBytes);
+                for (int i = 0; i < tiles; ++i)
+                    for (int a = 0; a < C::kAtoms; ++a)
+                        tma_load_3d(sbase + C::kOffK + i * C::kTileBytes + a * C::kAtomBytes, &map_k, bar(C::kBarK),
+                                    a * 64, key0 + 128 * i, kvh, once);
+            }
+            int head = begin / per_head, block_in_head = begin - head * per_head;
+            // lse of rows lane + 32 i of a step, -inf behind the last; asked for a step ahead
+            float lse[4];
+            auto load_lse = [&] {
+                const float* src = p.lse + (head0 + head) * p.Nq;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = first_row + 128 * block_in_head + lane + 32 * i;
+                    lse[i] = head < p.group && row < p.Nq ? __ldg(src + row) : -INFINITY;
+                }
+            };
+            load_lse();
             int issued = 0;
             for (int j = 0; j < T; ++j) {
                 const int s = j % C::kStages;
-                if (!wait_phase(bar(C::kBarEmpty + s), ((j / C::kStages) & 1) ^ 1, abort_flag, wp, 90)) break;
-                const int step = begin + j, h = step / per_head;
-                mbar_arrive_expect_tx(bar(C::kBarFull + s), C::kTileBytes);
-                for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q, bar(C::kBarFull + s),
-                                a * 64, first_row + 128 * (step - h * per_head), static_cast<int>(head0) + h, keep);
+                if (!__all_sync(0xffffffffu,
+                                wait_phase(bar(C::kBarEmpty + s), ((j / C::kStages) & 1) ^ 1, abort_flag, wp, 90)))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(C::kBarFull + s), C::kTileBytes);
+                    for (int a = 0; a < C::kAtoms; ++a)
+                        tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q,
+                                    bar(C::kBarFull + s), a * 64, first_row + 128 * block_in_head,
+                                    static_cast<int>(head0) + head, keep);
+                }
+                float* neg = reinterpret_cast<float*>(smem + C::kOffLse) + s * 128;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // -lse2; -inf where a row counts nothing
+                    neg[lane + 32 * i] = lse[i] == -INFINITY ? -INFINITY : lse[i] * -1.4426950408889634f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kBarFull + s));
+                if (++block_in_head == per_head) {
+                    block_in_head = 0;
+                    ++head;
+                }
+                load_lse();
                 issued = j + 1;
             }
-            wait_phase(bar(C::kBarK), 0, abort_flag, wp, 91, false);
-            for (int s = 0; s < C::kStages && s < issued; ++s) {
-                const int last = s + ((issued - 1 - s) / C::kStages) * C::kStages;
-                wait_phase(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, wp, 92, false);
+            if (lane == 0) {
+                wait_phase(bar(C::kBarK), 0, abort_flag, wp, 91, false);
+                for (int s = 0; s < C::kStages && s < issued; ++s) {
+                    const int last = s + ((issued - 1 - s) / C::kStages) * C::kStages;
+                    wait_phase(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, wp, 92, false);
+                }
             }
         }
     } else if (warp >= kWtMmaWarp) {
@@ -203,39 +256,25 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const int tile = tiles == 2 ? wg % 2 : 0;
         const int key = key0 + 128 * tile + t;
         const uint32_t tS = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + 128u * wg;
-        float* neg = reinterpret_cast<float*>(smem + C::kOffLse) + wg * 256;
         float total = 0.0f;
         if (T > 0 && !skip) {
-            // products n = wg, wg + 4, .. of T * tiles; the step of the next one to load is row block
-            // `block_in_head` of query head `head`
+            // products n = wg, wg + 4, .. of T * tiles; their steps j = n / tiles are row blocks
+            // `block_in_head` of the query heads
             const int products = T * tiles, ahead = kWtWarpgroups / tiles;
-            int next_step = wg / tiles, head = (begin + next_step) / per_head;
-            int block_in_head = begin + next_step - head * per_head;
-            // -lse2 of row t of that step; -inf where the row counts nothing
-            auto row_neg = [&]() -> float {
-                const int row = first_row + 128 * block_in_head + t;
-                if (next_step >= T || row >= p.Nq) return -INFINITY;
-                const float v = __ldg(p.lse + (head0 + head) * p.Nq + row);
-                return v == -INFINITY ? -INFINITY : v * -1.4426950408889634f;
-            };
+            int block_in_head = (begin + wg / tiles) % per_head;
             const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
             const int diagonal = p.causal ? key - p.causal_offset - first_row : -1;  // first row that sees the key
-            float next = row_neg();
             uint32_t turn = 0;
-            bool ok = true;
             for (int n = wg; n < products; n += kWtWarpgroups, ++turn) {
-                float* buf = neg + (turn & 1) * 128;
-                buf[t] = next;
+                const int j = n / tiles, stage = j % C::kStages;
+                const float* neg = reinterpret_cast<const float*>(smem + C::kOffLse) + stage * 128;
                 const int first_col = diagonal - 128 * block_in_head;  // of this step
-                next_step += ahead;
-                for (block_in_head += ahead; block_in_head >= per_head; ++head) block_in_head -= per_head;
-                next = row_neg();
+                for (block_in_head += ahead; block_in_head >= per_head;) block_in_head -= per_head;
                 const bool masked = __any_sync(0xffffffffu, first_col > 0);
-                named_barrier_sync(1 + wg, 128);
-                const int stage = n / tiles % C::kStages;
-                ok = ok && __all_sync(0xffffffffu, wait_phase(bar(C::kBarS + wg), turn & 1, abort_flag, wp, 97));
-                // a warp that gave up keeps meeting the barrier above
-                if (!ok) continue;
+                if (!__all_sync(0xffffffffu,
+                                wait_phase(bar(C::kBarFull + stage), (j / C::kStages) & 1, abort_flag, wp, 98) &&
+                                    wait_phase(bar(C::kBarS + wg), turn & 1, abort_flag, wp, 97)))
+                    break;
                 tc_fence_after();
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
@@ -248,27 +287,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     if (q == 1) {  // the scores are in registers: the next product may start
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(bar(C::kBarSFree + wg));
-                            mbar_arrive(bar(C::kBarEmpty + stage));
-                        }
+                        if (lane == 0) mbar_arrive(bar(C::kBarSFree + wg));
                     }
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 n4 = *reinterpret_cast<const float4*>(buf + 64 * q + i);
-                        const uint32_t* x4 = &r[i / 32][i % 32];
-                        float x[4];
-                        f2_unpack(f2_fma(f2_pack(u2f(x4[0]), u2f(x4[1])), c2, f2_pack(n4.x, n4.y)), x[0], x[1]);
-                        f2_unpack(f2_fma(f2_pack(u2f(x4[2]), u2f(x4[3])), c2, f2_pack(n4.z, n4.w)), x[2], x[3]);
-                        if (masked) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (64 * q + i + e < first_col) x[e] = -INFINITY;
-                        }
-                        sum[0] = f2_add(sum[0], f2_pack(ex2(x[0]), ex2(x[1])));
-                        sum[1] = f2_add(sum[1], f2_pack(ex2(x[2]), ex2(x[3])));
-                    }
+                    if (masked)
+                        add_weights<true>(r, neg + 64 * q, c2, first_col - 64 * q, sum);
+                    else
+                        add_weights<false>(r, neg + 64 * q, c2, 0, sum);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kBarEmpty + stage));  // the rows' lse was read
                 float a0, a1;
                 f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
                 total += a0 + a1;
