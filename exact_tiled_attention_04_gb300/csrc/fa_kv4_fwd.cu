@@ -5,19 +5,13 @@
 //
 // Mathematics.  Per key/value head, with the R = N_q * group query rows of
 // its query heads: S^T = K Q^T (keys x rows), P = 2^(c S - ref), O^T = V^T P^T.
-// Keys, not rows, take the 16-row side of the matrix instruction
-// (m16n8k16), so up to 8 rows cost one instruction per 16 keys x 16 channels.
 // A stored value is e2m1 x e4m3, exact in fp16, so both products run in fp16
 // whatever the type of q: a row of q is scaled by a power of two to
 // [2^14, 2^15), which is exact (values below 2^-28 of the row's largest lose
 // bits, less than the fp32 accumulation does), and the power goes into c.
 //
-// Layout.  A cache row is read straight in fragment order: the contraction
-// index of S and the rows of O^T are permuted so that lane (g, t) of a
-// quarter-warp reads consecutive bytes of a key's codes (channels
-// (d / 4) t ..) and of a value's (channels (d / 8) g ..).  Nibbles of two
-// values are interleaved in bits before they are widened, which pairs keys
-// as the second product's operand needs them.
+// Layout.  fa_kv4_tiles.cuh: how a warp reads a slab of 32 slots and keeps a
+// block of up to 4, 8 or 16 rows.
 //
 // What bounds it: reading the cache.  Groups of eight slabs (32 keys each, one
 // per warp) arrive by four bulk copies (codes and scales of K and V) in a
@@ -41,39 +35,40 @@
 // its remaining slabs but still reaches the block's barriers.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_fwd_kernel.cuh"
 #include "fa_kv4.h"
+#include "fa_kv4_tiles.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads4 = kWarps * 32;
-constexpr int kSlab = 32;          // keys per slab
-constexpr float kRefShift = 7.0f;  // weights are 2^7 at the row's reference maximum: fp16 then
-                                   // holds weights down to 2^-31 of it
-constexpr float kGrow = 15.0f;     // and up to 2^8 times it before the reference moves
+using namespace kv4;
 
-template <int D, int NT>
+constexpr int kThreads4 = kWarps * 32;
+
+// R: query rows per block, 4 (layout Paired), 8 or 16 (layout Wide).
+template <int D, int R>
 struct Kv4Cfg {
-    static constexpr int kRows = 8 * NT;
+    static constexpr int kRows = R;
     static constexpr int kStages = 2;
     static constexpr int kCodeBytes = kSlab * D / 2;
     static constexpr int kScaleBytes = kSlab * D / 16;
     static constexpr int kStageBytes = 2 * kWarps * (kCodeBytes + kScaleBytes);  // a group: a slab per warp
-    static constexpr int kMt = D / 16;                  // 16-row tiles of O^T
-    static constexpr int kRegs = kMt * NT * 4;          // accumulators of O^T per lane
+    static constexpr int kQTiles = R <= 8 ? 1 : 2;           // 8-column tiles of Q^T
+    static constexpr int kSums = R * D / 128;                // float4 accumulators of O^T per lane
     static constexpr int kOffRing = 0;  // [stages] K codes, V codes, K scales, V scales of kWarps slabs
-    static constexpr int kOffO = kOffRing + kStages * kStageBytes;  // float4 [warps][kMt][NT][32]
-    static constexpr int kOffMl = kOffO + kWarps * kRegs * 32 * 4;          // float4 [warps][kRows]
-    static constexpr int kOffQ = kOffMl + kWarps * kRows * 4 * 4;           // uint4 [NT][D / 32][32]
-    static constexpr int kOffC = kOffQ + NT * (D / 32) * 32 * 16;           // float [kRows]: score factors
+    static constexpr int kOffO = kOffRing + kStages * kStageBytes;          // float4 [warps][kSums][32]
+    static constexpr int kOffMl = kOffO + kWarps * kSums * 32 * 16;         // float4 [warps][kRows]
+    static constexpr int kOffQ = kOffMl + kWarps * kRows * 16;              // uint4 [kQTiles][D / 32][32]
+    static constexpr int kOffC = kOffQ + kQTiles * (D / 32) * 32 * 16;      // float [kRows]: score factors
     static constexpr int kOffBar = kOffC + kRows * 4;
     static constexpr int kOffCount = kOffBar + kStages * 8;  // [stages] warps done with the stage
     static constexpr int kOffAbort = kOffCount + kStages * 4;
     static constexpr int kSmemBytes = (kOffAbort + 4 + 15) / 16 * 16;
-    static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
+    static constexpr int kCtasPerSm = R <= 8 ? 2 : 1;
+    static_assert(kOffQ % 16 == 0 && kOffBar % 8 == 0 && kOffO % 16 == 0, "alignment");
     static_assert(kSmemBytes * kCtasPerSm <= 232448 - 1024 * kCtasPerSm, "shared memory budget exceeded");
 };
 
@@ -85,46 +80,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
         : "memory");
 }
-// The four f16x2 pairs of a word's eight e2m1 codes.
-__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
 // Adds 1 to a shared counter that wraps after kWarps; the value before.
 __device__ __forceinline__ uint32_t count_in(uint32_t addr) {
     uint32_t old;
     asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(kWarps - 1) : "memory");
     return old;
 }
-template <typename T>
-__device__ __forceinline__ T lds(const uint8_t* p) {
-    return *reinterpret_cast<const T*>(p);
-}
-
 __device__ __forceinline__ int kv4_length(const Kv4Cache& c, int b) {
     return min(max(c.counts[b], 0), c.capacity);
 }
@@ -200,9 +161,10 @@ struct Cursor {
     }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
-    using C = Kv4Cfg<D, NT>;
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_kernel(const __grid_constant__ Kv4FwdParams p) {
+    using C = Kv4Cfg<D, R>;
+    using Tile = std::conditional_t<R == 4, Paired<D>, Wide<D, R>>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = static_cast<int>(threadIdx.x) / 32, lane = static_cast<int>(threadIdx.x) % 32;
     const int g = lane / 4, t = lane % 4;
@@ -231,12 +193,13 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
     Cursor cur = load;
     const uint64_t once = policy_evict_first();  // every byte is read once per block of rows
 
-    // q fragments: lane (g, t) holds channels (D / 4) t .. of rows g + 8 nt; warp nt loads them a unit ahead and
-    // puts them, scaled, into shared memory
+    // q fragments: lane (g, t) holds channels (D / 4) t .. of one row per tile of 8 columns; warp nt loads tile nt
+    // a unit ahead and puts it, scaled, into shared memory
+    const int q_row = Tile::q_row(warp, g);
     uint4* sm_q = reinterpret_cast<uint4*>(smem + C::kOffQ);
     float* sm_c = reinterpret_cast<float*>(smem + C::kOffC);
     auto load_q = [&](const Cursor& u, uint4 (&raw)[D / 32]) {
-        const int r = (u.unit % p.row_blocks) * C::kRows + 8 * warp + g;
+        const int r = (u.unit % p.row_blocks) * R + q_row;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
         if (u.valid() && r < p.rows) {
@@ -275,10 +238,10 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
             // words 0, 1: the two halves of step 2 i; 2, 3: of step 2 i + 1
             sm_q[(warp * (D / 32) + i) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        if (t == 0) sm_c[8 * warp + g] = p.scale_log2 * down;
+        if (t == 0) sm_c[q_row] = p.scale_log2 * down;
     };
     uint4 raw[D / 32];
-    if (warp < NT) load_q(cur, raw);  // ahead of the copies below, which it would queue behind
+    if (warp < C::kQTiles) load_q(cur, raw);  // ahead of the copies below, which it would queue behind
 
     // A unit's slabs go in groups of one per warp.  Stage i % kStages of the ring holds group i; the last warp
     // to finish a group refills its stage, so no warp waits for the others and none is set aside for loading.
@@ -320,258 +283,34 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
         const int kvh = cur.b * p.c.H_kv + cur.unit / p.row_blocks;
         const int row0 = (cur.unit % p.row_blocks) * C::kRows;  // of the head's rows
         // ---- q fragments for the block, from the rows loaded ahead
-        if (warp < NT) put_q(raw);
+        if (warp < C::kQTiles) put_q(raw);
         __syncthreads();
-        float c[NT][2];  // score factor of rows 2t, 2t + 1
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            c[nt][0] = sm_c[8 * nt + 2 * t];
-            c[nt][1] = sm_c[8 * nt + 2 * t + 1];
-        }
-        // ref: the exponent's reference (base 2), set by the warp's first slab of the unit
-        float ref[NT][2], l[NT][2], lq[NT][4], o[NT][C::kMt][4];
-        // slots that row 8 nt + 2 t + i sees
-        auto limit = [&](int nt, int i) -> int {
-            const int r = row0 + 8 * nt + 2 * t + i;
-            return cur.len - (p.causal && r < p.rows ? p.Nq - 1 - r % p.Nq : 0);
-        };
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) ref[nt][i] = l[nt][i] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lq[nt][i] = 0.0f;
-#pragma unroll
-                for (int mt = 0; mt < C::kMt; ++mt) o[nt][mt][i] = 0.0f;
-            }
-        }
+        Tile tile;
+        tile.start(sm_c, lane);
+        Slab u;
+        u.q = sm_q;
+        u.logits = p.logits == nullptr ? nullptr : p.logits + static_cast<long long>(kvh) * p.c.capacity * p.rows + row0;
+        u.len = cur.len;
+        u.rows = p.rows;
+        u.row0 = row0;
+        u.Nq = p.Nq;
+        u.causal = p.causal;
         const int all_see = cur.len - (p.causal ? p.Nq - 1 : 0);  // slots every row sees
-        float* logits = p.logits == nullptr ? nullptr
-                                            : p.logits + static_cast<long long>(kvh) * p.c.capacity * p.rows + row0 + 2 * t;
-        // rows 2t, 2t + 1 as one store: both exist and every slot's rows start on an even one
-        const bool pairs = p.rows % 2 == 0;
-
-        const int slab0 = cur.s0 + warp;
         for (int group = cur.s0; group < cur.s1; group += kWarps) {
             const int s = used % C::kStages;
             const int slab = group + warp;
             const bool mine = slab < cur.s1;
             if (mine) ok = ok && __all_sync(0xffffffffu, wait_phase(bar(s), (used / C::kStages) & 1, abort_flag, wp, 80));
             if (mine && ok) {
-                const uint8_t* kc = smem + C::kOffRing + s * C::kStageBytes + warp * C::kCodeBytes;
-                const uint8_t* vc = kc + kWarps * C::kCodeBytes;
-                const uint8_t* ks = smem + C::kOffRing + s * C::kStageBytes + 2 * kWarps * C::kCodeBytes + warp * C::kScaleBytes;
-                const uint8_t* vs = ks + kWarps * C::kScaleBytes;
-                const int key0 = slab * kSlab;
-                const bool masked = key0 + kSlab > all_see;
-                const int kg = (g >> 1) + 4 * (g & 1);  // key of fragment row g (and 8 more of row g + 8)
-
-                // ---- S^T of both halves of 16 keys
-                float x[2][NT][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[h][nt][i] = 0.0f;
-                    const int ka = 16 * h + kg, kb = ka + 8;
-                    uint32_t wa[D / 32], wb[D / 32], sa[D / 64], sb[D / 64];
-                    if constexpr (D == 128) {
-                        const uint4 a = lds<uint4>(kc + ka * 64 + t * 16), b = lds<uint4>(kc + kb * 64 + t * 16);
-                        wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
-                        wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
-                        const uint32_t s2a = e4m3x2_to_f16x2(lds<uint16_t>(ks + ka * 8 + t * 2));
-                        const uint32_t s2b = e4m3x2_to_f16x2(lds<uint16_t>(ks + kb * 8 + t * 2));
-                        sa[0] = __byte_perm(s2a, 0, 0x1010), sa[1] = __byte_perm(s2a, 0, 0x3232);
-                        sb[0] = __byte_perm(s2b, 0, 0x1010), sb[1] = __byte_perm(s2b, 0, 0x3232);
-                    } else {
-                        const uint2 a = lds<uint2>(kc + ka * 32 + t * 8), b = lds<uint2>(kc + kb * 32 + t * 8);
-                        wa[0] = a.x, wa[1] = a.y;
-                        wb[0] = b.x, wb[1] = b.y;
-                        sa[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + ka * 4 + t) * 0x0101u);
-                        sb[0] = e4m3x2_to_f16x2(lds<uint8_t>(ks + kb * 4 + t) * 0x0101u);
-                    }
-#pragma unroll
-                    for (int w = 0; w < D / 32; ++w) {
-                        uint32_t ha[4], hb[4];
-                        widen_codes(wa[w], ha);
-                        widen_codes(wb[w], hb);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            ha[i] = mul16x2(ha[i], sa[w / 2]);
-                            hb[i] = mul16x2(hb[i], sb[w / 2]);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint4 q = sm_q[(nt * (D / 32) + w) * 32 + lane];
-                            mma_f16(x[h][nt], ha[0], hb[0], ha[1], hb[1], q.x, q.y);
-                            mma_f16(x[h][nt], ha[2], hb[2], ha[3], hb[3], q.z, q.w);
-                        }
-                    }
-                }
-                // ---- exponents (base 2) against the reference; hidden slots are -inf whatever is stored there
-                float top = -INFINITY;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[h][nt][i] = fmaf(x[h][nt][i], c[nt][i & 1], -ref[nt][i & 1]);
-                if (masked) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int lim = limit(nt, i) - key0 - kg;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (16 * h >= lim) x[h][nt][i] = -INFINITY;
-                                if (16 * h + 8 >= lim) x[h][nt][i + 2] = -INFINITY;
-                            }
-                        }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmax3(top, x[0][nt][i], x[1][nt][i]);
-                // the first slab sets the reference (nothing to rescale); later ones move it when a weight would
-                // pass fp16's range
-                if (slab == slab0 || __any_sync(0xffffffffu, top > kGrow)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float m = fmaxf(fmaxf(x[0][nt][i], x[0][nt][i + 2]), fmaxf(x[1][nt][i], x[1][nt][i + 2]));
-#pragma unroll
-                            for (int off = 4; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                            // a row that sees none of a first slab sees none of the warp's later ones either
-                            float shift = m == -INFINITY ? 0.0f : m - kRefShift;
-                            if (slab != slab0) {
-                                shift = fmaxf(shift, 0.0f);
-                                const float alpha = ex2(-shift);
-                                l[nt][i] *= alpha;
-                                lq[nt][i] *= alpha;
-#pragma unroll
-                                for (int mt = 0; mt < C::kMt; ++mt) {
-                                    o[nt][mt][i] *= alpha;
-                                    o[nt][mt][i + 2] *= alpha;
-                                }
-                            }
-                            ref[nt][i] += shift;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                x[h][nt][i] -= shift;
-                                x[h][nt][i + 2] -= shift;
-                            }
-                        }
-                }
-                if (logits != nullptr) {
-                    float* dst = logits + static_cast<long long>(key0 + kg) * p.rows;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i2 = 0; i2 < 2; ++i2) {
-                            if (!masked || key0 + kg + 16 * h + 8 * i2 < cur.len) {
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    const int left = p.rows - row0 - 8 * nt - 2 * t;  // rows from 2t on
-                                    const float y0 = x[h][nt][2 * i2] + ref[nt][0], y1 = x[h][nt][2 * i2 + 1] + ref[nt][1];
-                                    if (pairs && left > 0) {
-                                        *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(y0, y1);
-                                    } else {
-                                        if (left > 0) dst[8 * nt] = y0;
-                                        if (left > 1) dst[8 * nt + 1] = y1;
-                                    }
-                                }
-                            }
-                            dst += 8 * p.rows;
-                        }
-                }
-                // ---- weights, O^T += V^T P^T
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pb[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            w[i] = ex2(x[h][nt][i]);
-                            l[nt][i & 1] += w[i];
-                        }
-                        pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-                        pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-                        mma_f16(lq[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nt][0], pb[nt][1]);
-                    }
-                    uint32_t sc[4], v[4][D / 64];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = 16 * h + 4 * i + t;
-                        if constexpr (D == 128) {
-                            const uint2 a = lds<uint2>(vc + key * 64 + g * 8);
-                            v[i][0] = a.x, v[i][1] = a.y;
-                            sc[i] = lds<uint8_t>(vs + key * 8 + g);
-                        } else {
-                            v[i][0] = lds<uint32_t>(vc + key * 32 + g * 4);
-                            sc[i] = lds<uint8_t>(vs + key * 4 + g / 2);
-                        }
-                    }
-                    if (masked) {
-                        // slots behind the length hold anything: values 0.  A NaN in a slot that only some
-                        // rows see must not reach the others (0 * NaN): it is taken out of the product and
-                        // set in the rows that see it.
-                        bool nan = false;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (key0 + 16 * h + 4 * i + t >= cur.len) sc[i] = 0u;
-                            nan |= (sc[i] & 0x7Fu) == 0x7Fu;
-                        }
-                        if (__any_sync(0xffffffffu, nan)) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const uint32_t su = __shfl_sync(0xffffffffu, sc[i], (lane & ~3) | u);
-                                    if ((su & 0x7Fu) == 0x7Fu) {
-#pragma unroll
-                                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                            for (int j = 0; j < 2; ++j)
-                                                if (key0 + 16 * h + 4 * i + u < limit(nt, j)) {
-#pragma unroll
-                                                    for (int mt = 0; mt < C::kMt; ++mt)
-                                                        o[nt][mt][j] = o[nt][mt][j + 2] = __int_as_float(0x7FC00000);
-                                                }
-                                    }
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if ((sc[i] & 0x7Fu) == 0x7Fu) sc[i] = 0u;
-                        }
-                    }
-                    const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
-#pragma unroll
-                    for (int w = 0; w < D / 64; ++w) {
-                        constexpr uint32_t kLow = 0x0F0F0F0Fu;
-                        uint32_t a0[4], a1[4], a2[4], a3[4];
-                        widen_codes((v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), a0);
-                        widen_codes(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), a1);
-                        widen_codes((v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), a2);
-                        widen_codes(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), a3);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            a0[i] = mul16x2(a0[i], s01);
-                            a1[i] = mul16x2(a1[i], s01);
-                            a2[i] = mul16x2(a2[i], s23);
-                            a3[i] = mul16x2(a3[i], s23);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(o[nt][4 * w + i], a0[i], a1[i], a2[i], a3[i], pb[nt][0], pb[nt][1]);
-                        }
-                    }
-                }
+                const uint8_t* stage = smem + C::kOffRing + s * C::kStageBytes;
+                u.kc = stage + warp * C::kCodeBytes;
+                u.vc = u.kc + kWarps * C::kCodeBytes;
+                u.ks = stage + 2 * kWarps * C::kCodeBytes + warp * C::kScaleBytes;
+                u.vs = u.ks + kWarps * C::kScaleBytes;
+                u.key0 = slab * kSlab;
+                u.masked = u.key0 + kSlab > all_see;
+                u.first = group == cur.s0;
+                tile.slab(u);
             }
             __syncwarp();  // the slab has been read by every lane
             bool refill = false;
@@ -581,87 +320,15 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, NT>::kCtasPerSm) kv4_fwd_
         }
 
         // ---- the unit's result over the CTA's warps
-        const Cursor done = cur;
+        Target to;
+        to.whole = cur.s0 == 0 && cur.s1 == cur.slabs;
+        to.slot = (static_cast<long long>(blockIdx.x) * 2 + (cur.s0 > 0 ? 0 : 1)) * R;
+        to.row0 = static_cast<long long>(kvh) * p.rows + row0;
+        to.left = p.rows - row0;
         cur.next(p.c, units);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float s = l[nt][i];
-#pragma unroll
-                for (int off = 4; off < 32; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
-                if (g == 0)
-                    sm_ml[warp * C::kRows + 8 * nt + 2 * t + i] =
-                        make_float4(s == 0.0f ? -INFINITY : ref[nt][i], s, lq[nt][i], 0.0f);
-            }
-        __syncthreads();
-        // lane (g, t): row g of each block of 8, warps t and t + 4; then the quad's M, L, LQ of that row
-        float M[NT], L[NT], LQ[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float4 ma = sm_ml[t * C::kRows + 8 * nt + g], mb = sm_ml[(t + 4) * C::kRows + 8 * nt + g];
-            float m = fmaxf(ma.x, mb.x);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // a warp that saw nothing counts 0 (a NaN sum stays one)
-            const float fa = m == -INFINITY ? 1.0f : ex2(ma.x - m), fb = m == -INFINITY ? 1.0f : ex2(mb.x - m);
-            M[nt] = m;
-            L[nt] = fa * ma.y + fb * mb.y;
-            LQ[nt] = fa * ma.z + fb * mb.z;
-#pragma unroll
-            for (int off = 1; off < 4; off *= 2) {
-                L[nt] += __shfl_xor_sync(0xffffffffu, L[nt], off);
-                LQ[nt] += __shfl_xor_sync(0xffffffffu, LQ[nt], off);
-            }
-            // this warp's weight in row g, then in rows 2t, 2t + 1
-            const float f = __shfl_sync(0xffffffffu, warp < 4 ? fa : fb, (lane & ~3) | (warp & 3));
-            const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-#pragma unroll
-            for (int mt = 0; mt < C::kMt; ++mt)
-                sm_o[((warp * C::kMt + mt) * NT + nt) * 32 + lane] =
-                    make_float4(o[nt][mt][0] * f0, o[nt][mt][1] * f1, o[nt][mt][2] * f0, o[nt][mt][3] * f1);
-        }
-        if (warp < NT) load_q(cur, raw);
-        __syncthreads();
-        const bool whole = done.s0 == 0 && done.s1 == done.slabs;
-        const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (done.s0 > 0 ? 0 : 1)) * C::kRows;
-        const long long row_first = static_cast<long long>(kvh) * p.rows + row0;  // output row of row 0
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = 8 * nt + 2 * t;
-            if (warp < C::kMt) {  // each of the first D / 16 warps adds up one 16-channel tile
-                float4 acc = sm_o[(warp * NT + nt) * 32 + lane];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) {
-                    const float4 v = sm_o[((w * C::kMt + warp) * NT + nt) * 32 + lane];
-                    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-                }
-                const int ch = (D / 8) * g + 2 * warp;  // channels ch, ch + 1 of rows r (x, z) and r + 1 (y, w)
-                if (whole) {
-                    const float q0 = __shfl_sync(0xffffffffu, LQ[nt], 8 * t), q1 = __shfl_sync(0xffffffffu, LQ[nt], 8 * t + 4);
-                    const float i0 = q0 == 0.0f ? 0.0f : 1.0f / q0, i1 = q1 == 0.0f ? 0.0f : 1.0f / q1;
-                    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (row_first + r) * D + ch);
-                    if (row0 + r < p.rows)
-                        out[0] = p.f16 ? pack_f16x2(acc.x * i0, acc.z * i0) : pack_bf16x2(acc.x * i0, acc.z * i0);
-                    if (row0 + r + 1 < p.rows)
-                        out[D / 2] = p.f16 ? pack_f16x2(acc.y * i1, acc.w * i1) : pack_bf16x2(acc.y * i1, acc.w * i1);
-                } else {
-                    float* out = p.part_o + (slot + r) * D + ch;
-                    *reinterpret_cast<float2*>(out) = make_float2(acc.x, acc.z);
-                    *reinterpret_cast<float2*>(out + D) = make_float2(acc.y, acc.w);
-                }
-            }
-            if (warp == 0 && t == 0) {
-                const int rg = 8 * nt + g;
-                if (!whole) {
-                    p.part_ml[slot + rg] = make_float4(M[nt], L[nt], LQ[nt], 0.0f);
-                } else if (row0 + rg < p.rows) {
-                    const float lse2 = L[nt] == 0.0f ? -INFINITY : M[nt] + log2f(L[nt]);
-                    if (p.lse != nullptr) p.lse[row_first + rg] = lse2 * 0.69314718055994531f;
-                    p.row_lse2[row_first + rg] = lse2;
-                }
-            }
-        }
+        tile.finish(p, to, sm_ml, sm_o, warp, [&] {
+            if (warp < C::kQTiles) load_q(cur, raw);
+        });
         __syncthreads();
     }
     // a warp that gave up leaves no copy in flight behind the block
@@ -845,10 +512,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
     }
 }
 
-template <int D, int NT>
+template <int D, int R>
 cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
-    using C = Kv4Cfg<D, NT>;
-    auto kern = kv4_fwd_kernel<D, NT>;
+    using C = Kv4Cfg<D, R>;
+    auto kern = kv4_fwd_kernel<D, R>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     // both kernels may be set up while the one before them in the stream runs; they wait for its end
@@ -878,20 +545,22 @@ cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int kv4_rows_per_block(int64_t rows) { return rows <= 8 ? 8 : 16; }
+int kv4_rows_per_block(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 
 int kv4_max_ctas(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms) {
     const int64_t rpb = kv4_rows_per_block(rows);
     const int64_t slabs = B * H_kv * ((rows + rpb - 1) / rpb) * (capacity / kSlab);
-    const int64_t most = static_cast<int64_t>(sms) * (rpb == 8 ? 2 : 1);
+    const int64_t most = static_cast<int64_t>(sms) * (rpb <= 8 ? 2 : 1);
     const int64_t want = (slabs + kWarps - 1) / kWarps;
     return static_cast<int>(want < most ? want : most);
 }
 
 cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, cudaStream_t stream) {
-    if (kv4_rows_per_block(p.rows) == 8)
-        return p.c.d == 128 ? launch_variant<128, 1>(p, stream) : launch_variant<64, 1>(p, stream);
-    return p.c.d == 128 ? launch_variant<128, 2>(p, stream) : launch_variant<64, 2>(p, stream);
+    switch (kv4_rows_per_block(p.rows)) {
+        case 4: return p.c.d == 128 ? launch_variant<128, 4>(p, stream) : launch_variant<64, 4>(p, stream);
+        case 8: return p.c.d == 128 ? launch_variant<128, 8>(p, stream) : launch_variant<64, 8>(p, stream);
+        default: return p.c.d == 128 ? launch_variant<128, 16>(p, stream) : launch_variant<64, 16>(p, stream);
+    }
 }
 
 }  // namespace fa
