@@ -19,6 +19,30 @@ struct Kv4Cache {
     int B, H_kv, capacity, d;
 };
 
+// The kernels of this file are launched with programmatic serialization: a
+// kernel is set up while the one before it in the stream runs, and waits for
+// that one's end (and through it for everything earlier) before it touches
+// memory that another kernel may have written.
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream be set up.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+template <class Kernel, class... Args>
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct Kv4AppendParams {
     Kv4Cache c;
     const void* x[2];     // k, v: [B * H_kv, n, d]

@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
     if (threadIdx.x == 0) sh.listed = 0u;
     for (int i = threadIdx.x; i < 256 * 8; i += kEvThreads)
         reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_release();
+    grid_wait();
     const int n = min(max(p.from.counts[b], 0), p.from.capacity);
     const int seen = p.from.counts[p.from.B + b];
     const int nn = min(n, p.keep);  // the new length
@@ -521,7 +522,8 @@ template <int D>
 __global__ void __launch_bounds__(kCopyThreads) kv4_evict_copy_kernel(const __grid_constant__ Kv4EvictParams p, int blocks) {
     const int head = static_cast<int>(blockIdx.x) / blocks;
     const int j0 = (static_cast<int>(blockIdx.x) % blocks) * kCopyRows + static_cast<int>(threadIdx.x) / 32 * 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_release();
+    grid_wait();
     if (j0 >= p.keep) return;
     const int j = j0 + static_cast<int>(threadIdx.x) % 32;
     const int from = j < p.keep ? p.src[static_cast<long long>(head) * p.keep + j] : -1;
@@ -533,6 +535,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_evict_copy_kernel(const __gr
 // counts_out where it is the counts that the clusters of a sequence read.
 __global__ void kv4_evict_counts_kernel(const Kv4EvictParams p) {
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    grid_release();
+    grid_wait();
     if (b < p.from.B) p.counts_out[b] = min(min(max(p.from.counts[b], 0), p.from.capacity), p.keep);
 }
 
@@ -567,14 +571,11 @@ cudaError_t launch_evict(const Kv4EvictParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (p.to.codes[0] != p.from.codes[0]) {
         const int blocks = (p.keep + kCopyRows - 1) / kCopyRows;
-        cfg.gridDim = dim3(static_cast<unsigned>(heads) * static_cast<unsigned>(blocks));
-        cfg.blockDim = dim3(kCopyThreads);
-        cfg.dynamicSmemBytes = 0;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kv4_evict_copy_kernel<D>, p, blocks);
+        e = launch_dependent(kv4_evict_copy_kernel<D>, dim3(static_cast<unsigned>(heads) * static_cast<unsigned>(blocks)),
+                             kCopyThreads, 0, stream, p, blocks);
         if (e != cudaSuccess) return e;
     }
-    if (!advance) kv4_evict_counts_kernel<<<(p.from.B + 127) / 128, 128, 0, stream>>>(p);
+    if (!advance) return launch_dependent(kv4_evict_counts_kernel, dim3((p.from.B + 127) / 128), 128, 0, stream, p);
     return cudaGetLastError();
 }
 

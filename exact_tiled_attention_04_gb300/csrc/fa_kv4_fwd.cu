@@ -15,8 +15,10 @@
 //
 // What bounds it: reading the cache.  Groups of eight slabs (32 keys each, one
 // per warp) arrive by four bulk copies (codes and scales of K and V) in a
-// ring that the warp that finishes a group last refills; two blocks an SM
-// keep 147 KB in flight.
+// ring that a ninth warp refills (a copy holds up the warp that asks for it;
+// by the warp that finished a group last, 65536 slots took 109 us, by the
+// ninth 104, at B = 8, H = 32/8, d = 128); two blocks an SM keep 147 KB in
+// flight.
 //
 // Work split.  The slabs of all units (sequence, key/value head, block of
 // rows), in order, are cut into equal runs, one per CTA, from the lengths on
@@ -46,7 +48,8 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kThreads4 = kWarps * 32;
+constexpr int kLoadWarp = kWarps;
+constexpr int kThreads4 = (kWarps + 1) * 32;
 
 // R: query rows per block, 4 (layout Paired), 8 or 16 (layout Wide).
 template <int D, int R>
@@ -64,8 +67,7 @@ struct Kv4Cfg {
     static constexpr int kOffQ = kOffMl + kWarps * kRows * 16;              // uint4 [kQTiles][D / 32][32]
     static constexpr int kOffC = kOffQ + kQTiles * (D / 32) * 32 * 16;      // float [kRows]: score factors
     static constexpr int kOffBar = kOffC + kRows * 4;
-    static constexpr int kOffCount = kOffBar + kStages * 8;  // [stages] warps done with the stage
-    static constexpr int kOffAbort = kOffCount + kStages * 4;
+    static constexpr int kOffAbort = kOffBar + 2 * kStages * 8;  // behind [stages] landed, [stages] read
     static constexpr int kSmemBytes = (kOffAbort + 4 + 15) / 16 * 16;
     static constexpr int kCtasPerSm = R <= 8 ? 2 : 1;
     static_assert(kOffQ % 16 == 0 && kOffBar % 8 == 0 && kOffO % 16 == 0, "alignment");
@@ -79,12 +81,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
             dst),
         "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
         : "memory");
-}
-// Adds 1 to a shared counter that wraps after kWarps; the value before.
-__device__ __forceinline__ uint32_t count_in(uint32_t addr) {
-    uint32_t old;
-    asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(kWarps - 1) : "memory");
-    return old;
 }
 __device__ __forceinline__ int kv4_length(const Kv4Cache& c, int b) {
     return min(max(c.counts[b], 0), c.capacity);
@@ -173,25 +169,55 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
     FwdParams wp;  // what a bounded wait reports to
     wp.status = p.status;
     wp.gen = p.gen;
-    auto bar = [&](int s) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(s); };
+    auto full = [&](int s) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(s); };
+    auto empty = [&](int s) -> uint32_t { return full(C::kStages + s); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bar(s), 1);
-            *reinterpret_cast<uint32_t*>(smem + C::kOffCount + 4 * s) = 0u;
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kWarps);
         }
         *abort_flag = 0u;
         mbar_init_fence();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second kernel waits by itself
+    __syncthreads();
+    grid_wait();
+    grid_release();
 
     const int units = p.c.H_kv * p.row_blocks;
-    Cursor load;
-    load.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x));
-    Cursor cur = load;
-    const uint64_t once = policy_evict_first();  // every byte is read once per block of rows
+    Cursor cur;
+    cur.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x));
+
+    // A unit's slabs go in groups of one per warp; stage i % kStages of the ring holds group i.
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            const uint64_t once = policy_evict_first();  // every byte is read once per block of rows
+            int i = 0;
+            for (; cur.valid(); cur.next(p.c, units)) {
+                const long long row0 =
+                    (static_cast<long long>(cur.b) * p.c.H_kv + cur.unit / p.row_blocks) * p.c.capacity;
+                for (int slab = cur.s0; slab < cur.s1; slab += kWarps, ++i) {
+                    const int s = i % C::kStages;
+                    if (!wait_phase(empty(s), ((i / C::kStages) & 1) ^ 1, abort_flag, wp, 81)) break;
+                    const int n = min(kWarps, cur.s1 - slab);
+                    const long long row = row0 + static_cast<long long>(slab) * kSlab;
+                    const uint32_t dst = sbase + C::kOffRing + s * C::kStageBytes;
+                    const uint32_t code = n * C::kCodeBytes, scale = n * C::kScaleBytes;
+                    mbar_arrive_expect_tx(full(s), 2 * (code + scale));
+                    bulk_load(dst, p.c.codes[0] + row * (D / 2), code, full(s), once);
+                    bulk_load(dst + 2 * kWarps * C::kCodeBytes, p.c.scales[0] + row * (D / 16), scale, full(s), once);
+                    bulk_load(dst + kWarps * C::kCodeBytes, p.c.codes[1] + row * (D / 2), code, full(s), once);
+                    bulk_load(dst + kWarps * (2 * C::kCodeBytes + C::kScaleBytes), p.c.scales[1] + row * (D / 16), scale,
+                              full(s), once);
+                }
+                if (*abort_flag) break;
+            }
+            // every copy has landed before the block may end
+            for (int k = max(0, i - C::kStages); k < i; ++k)
+                wait_phase(full(k % C::kStages), (k / C::kStages) & 1, abort_flag, wp, 82, false);
+        }
+        return;
+    }
 
     // q fragments: lane (g, t) holds channels (D / 4) t .. of one row per tile of 8 columns; warp nt loads tile nt
     // a unit ahead and puts it, scaled, into shared memory
@@ -241,38 +267,7 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
         if (t == 0) sm_c[q_row] = p.scale_log2 * down;
     };
     uint4 raw[D / 32];
-    if (warp < C::kQTiles) load_q(cur, raw);  // ahead of the copies below, which it would queue behind
-
-    // A unit's slabs go in groups of one per warp.  Stage i % kStages of the ring holds group i; the last warp
-    // to finish a group refills its stage, so no warp waits for the others and none is set aside for loading.
-    // Every warp follows the loads' position.
-    int issued = 0;  // groups asked for
-    int load_s = load.s0;
-    auto issue = [&](bool mine) {
-        if (!load.valid()) return;
-        if (mine) {
-            const int st = issued % C::kStages;
-            const int n = min(kWarps, load.s1 - load_s);
-            const long long row =
-                (static_cast<long long>(load.b) * p.c.H_kv + load.unit / p.row_blocks) * p.c.capacity +
-                static_cast<long long>(load_s) * kSlab;
-            const uint32_t dst = sbase + C::kOffRing + st * C::kStageBytes;
-            const uint32_t code = n * C::kCodeBytes, scale = n * C::kScaleBytes;
-            mbar_arrive_expect_tx(bar(st), 2 * (code + scale));
-            bulk_load(dst, p.c.codes[0] + row * (D / 2), code, bar(st), once);
-            bulk_load(dst + kWarps * C::kCodeBytes, p.c.codes[1] + row * (D / 2), code, bar(st), once);
-            bulk_load(dst + 2 * kWarps * C::kCodeBytes, p.c.scales[0] + row * (D / 16), scale, bar(st), once);
-            bulk_load(dst + kWarps * (2 * C::kCodeBytes + C::kScaleBytes), p.c.scales[1] + row * (D / 16), scale, bar(st),
-                      once);
-        }
-        ++issued;
-        load_s += kWarps;
-        if (load_s >= load.s1) {
-            load.next(p.c, units);
-            load_s = load.s0;
-        }
-    };
-    for (int s = 0; s < C::kStages; ++s) issue(threadIdx.x == 0);
+    if (warp < C::kQTiles) load_q(cur, raw);
 
     float4* sm_o = reinterpret_cast<float4*>(smem + C::kOffO);
     float4* sm_ml = reinterpret_cast<float4*>(smem + C::kOffMl);
@@ -284,7 +279,7 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
         const int row0 = (cur.unit % p.row_blocks) * C::kRows;  // of the head's rows
         // ---- q fragments for the block, from the rows loaded ahead
         if (warp < C::kQTiles) put_q(raw);
-        __syncthreads();
+        sync_rows();
         Tile tile;
         tile.start(sm_c, lane);
         Slab u;
@@ -300,7 +295,7 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
             const int s = used % C::kStages;
             const int slab = group + warp;
             const bool mine = slab < cur.s1;
-            if (mine) ok = ok && __all_sync(0xffffffffu, wait_phase(bar(s), (used / C::kStages) & 1, abort_flag, wp, 80));
+            if (mine) ok = ok && __all_sync(0xffffffffu, wait_phase(full(s), (used / C::kStages) & 1, abort_flag, wp, 80));
             if (mine && ok) {
                 const uint8_t* stage = smem + C::kOffRing + s * C::kStageBytes;
                 u.kc = stage + warp * C::kCodeBytes;
@@ -313,10 +308,8 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
                 tile.slab(u);
             }
             __syncwarp();  // the slab has been read by every lane
-            bool refill = false;
-            if (lane == 0) refill = count_in(sbase + C::kOffCount + 4 * s) == kWarps - 1;
+            if (lane == 0) mbar_arrive(empty(s));
             ++used;
-            issue(refill);
         }
 
         // ---- the unit's result over the CTA's warps
@@ -329,12 +322,8 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
         tile.finish(p, to, sm_ml, sm_o, warp, [&] {
             if (warp < C::kQTiles) load_q(cur, raw);
         });
-        __syncthreads();
+        sync_rows();
     }
-    // a warp that gave up leaves no copy in flight behind the block
-    if (!ok)
-        for (int i = max(0, issued - C::kStages); i < issued; ++i)
-            wait_phase(bar(i % C::kStages), (i / C::kStages) & 1, abort_flag, wp, 81, false);
 }
 
 // ------------------------------------------------------------ second kernel
@@ -407,11 +396,12 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
                                                                  int join_blocks) {
     // started while the main kernel's last CTAs run: what that kernel does not
     // write (it waited for what came before) is read ahead of the wait
+    grid_release();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (static_cast<int>(blockIdx.x) < join_blocks) {
         const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + warp;
         if (row >= static_cast<long long>(p.c.B) * p.c.H_kv * p.rows) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            grid_wait();
             return;
         }
         const long long kvh = row / p.rows;
@@ -419,7 +409,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
         const int b = static_cast<int>(kvh / p.c.H_kv);
         const int unit = static_cast<int>(kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block;
         const Parts u = parts_of(spread_of(p, b), unit);
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        grid_wait();
         if (u.slabs > 0 && u.first == u.last) return;  // the main kernel wrote it
         constexpr int kPer = D / 32;
         float acc[kPer] = {}, M = -INFINITY, L = 0.0f, LQ = 0.0f;
@@ -463,7 +453,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
     const int kvh = i / chunks, b = kvh / p.c.H_kv;
     const int key0 = (i % chunks) * kJoinKeys, len = kv4_length(p.c, b);
     const Spread spread = spread_of(p, b);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     if (key0 >= len) return;
     const long long slot0 = static_cast<long long>(kvh) * p.c.capacity + key0 + threadIdx.x;
     const int left = len - key0 - static_cast<int>(threadIdx.x);  // this thread's keys: 0, 256, .. below it
@@ -518,29 +508,15 @@ cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
     auto kern = kv4_fwd_kernel<D, R>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    // both kernels may be set up while the one before them in the stream runs; they wait for its end
-    // before they touch memory that it writes
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
-    cfg.blockDim = dim3(kThreads4);
-    cfg.dynamicSmemBytes = C::kSmemBytes;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), kThreads4, C::kSmemBytes, stream, p);
+    if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
     const int join = static_cast<int>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
     const long long keys = p.logits == nullptr ? 0
                                                : static_cast<long long>(p.c.B) * p.c.H_kv *
                                                      ((p.c.capacity + kJoinKeys - 1) / kJoinKeys);
-    cfg.gridDim = dim3(static_cast<unsigned>(join + keys));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<D>, p, C::kRows, join);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(kv4_join_kernel<D>, dim3(static_cast<unsigned>(join + keys)), kJoinThreads, 0, stream, p,
+                            C::kRows, join);
 }
 
 }  // namespace

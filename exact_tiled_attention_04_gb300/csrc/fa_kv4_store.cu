@@ -115,6 +115,8 @@ __device__ __forceinline__ void append_block(const Kv4AppendParams& p, long long
 template <bool F16>
 __global__ void kv4_append_kernel(const Kv4AppendParams p, long long total, int advance) {
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    grid_release();
+    grid_wait();
     if (i < total) append_block<F16>(p, i);
     if (advance && blockIdx.x == 0) {
         __syncthreads();
@@ -124,12 +126,16 @@ __global__ void kv4_append_kernel(const Kv4AppendParams p, long long total, int 
 
 __global__ void kv4_advance_kernel(const Kv4AppendParams p) {
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    grid_release();
+    grid_wait();
     if (b < p.c.B) advance_counts(p, b);
 }
 
 template <bool F16>
 __global__ void kv4_read_kernel(const Kv4ReadParams p, long long total) {
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    grid_release();
+    grid_wait();
     if (i >= total) return;
     const bool value = blockIdx.y != 0;
     void* x = value ? p.x[1] : p.x[0];
@@ -167,17 +173,15 @@ cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t stream) {
     const long long grid = (total + threads - 1) / threads;
     const int advance = (!in_place || grid == 1) ? 1 : 0;
     auto kern = p.f16 ? kv4_append_kernel<true> : kv4_append_kernel<false>;
-    kern<<<static_cast<unsigned>(grid), threads, 0, stream>>>(p, total, advance);
-    if (!advance) kv4_advance_kernel<<<(p.c.B + 127) / 128, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    const cudaError_t e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), threads, 0, stream, p, total, advance);
+    if (e != cudaSuccess || advance) return e;
+    return launch_dependent(kv4_advance_kernel, dim3((p.c.B + 127) / 128), 128, 0, stream, p);
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t stream) {
     const long long total = static_cast<long long>(p.c.B) * p.c.H_kv * p.count * (p.c.d / 16);
     const dim3 grid(static_cast<unsigned>((total + 255) / 256), 2);
-    auto kern = p.f16 ? kv4_read_kernel<true> : kv4_read_kernel<false>;
-    kern<<<grid, 256, 0, stream>>>(p, total);
-    return cudaGetLastError();
+    return launch_dependent(p.f16 ? kv4_read_kernel<true> : kv4_read_kernel<false>, grid, 256, 0, stream, p, total);
 }
 
 }  // namespace fa

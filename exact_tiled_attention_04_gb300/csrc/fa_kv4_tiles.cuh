@@ -73,6 +73,9 @@ __device__ __forceinline__ T lds(const uint8_t* p) {
 }
 
 
+// Barrier of the warps that hold rows.
+__device__ __forceinline__ void sync_rows() { named_barrier_sync(1, kWarps * 32); }
+
 // One slab and what is needed to work through it.
 struct Slab {
     const uint8_t *kc, *vc, *ks, *vs;  // its codes and scales in shared memory
@@ -363,7 +366,7 @@ struct Wide {
                     sm_ml[warp * R + 8 * nt + 2 * t + i] =
                         make_float4(s == 0.0f ? -INFINITY : ref[nt][i], s, lq[nt][i], 0.0f);
             }
-        __syncthreads();
+        sync_rows();
         // lane (g, t): row g of each block of 8, warps t and t + 4; then the quad's M, L, LQ of that row
         float M[NT], L[NT], LQ[NT];
 #pragma unroll
@@ -391,7 +394,7 @@ struct Wide {
                     make_float4(o[nt][mt][0] * f0, o[nt][mt][1] * f1, o[nt][mt][2] * f0, o[nt][mt][3] * f1);
         }
         ahead();
-        __syncthreads();
+        sync_rows();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = 8 * nt + 2 * t;
@@ -621,7 +624,7 @@ struct Paired {
 #pragma unroll
         for (int off = 4; off < 32; off *= 2) s += __shfl_xor_sync(0xffffffffu, s, off);
         if (g == 0) sm_ml[warp * 4 + t] = make_float4(s == 0.0f ? -INFINITY : ref, s, lq[0], 0.0f);
-        __syncthreads();
+        sync_rows();
         // lane (g, t): row t of warp g; then every lane has M, L, LQ of row t
         const float4 ml = sm_ml[g * 4 + t];
         float M = ml.x;
@@ -640,7 +643,7 @@ struct Paired {
             sm_o[(warp * kMt + mt) * 32 + lane] =
                 make_float4(o[mt][0] * mine, o[mt][1] * mine, o[mt][2] * mine, o[mt][3] * mine);
         ahead();
-        __syncthreads();
+        sync_rows();
         if (warp < kMt) {
             float4 acc = sm_o[warp * 32 + lane];
 #pragma unroll

@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const bool skip = *abort_flag != 0u;
+    grid_release();
+    grid_wait();
 
     if (warp == kWtLoadWarp) {
         if (T > 0 && !skip) {
@@ -356,13 +358,15 @@ cudaError_t launch_weights_variant(const CUtensorMap& q, const CUtensorMap& k, c
     cfg.blockDim = dim3(kWtThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, q, k, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
