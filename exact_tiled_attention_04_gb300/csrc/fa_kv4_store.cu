@@ -62,23 +62,24 @@ __device__ __forceinline__ void advance_counts(const Kv4AppendParams& p, int b) 
     p.counts_out[p.c.B + b] = static_cast<int32_t>(seen + p.n);
 }
 
-template <bool F16>
-__device__ __forceinline__ void append_block(const Kv4AppendParams& p, long long i) {
-    const int nblk = p.c.d / 16;
-    const int blk = static_cast<int>(i % nblk);
-    const long long t = i / nblk;
-    const long long row = t % p.n;
-    const long long rest = t / p.n;
+// Block i of 16 channels, in the order [head][key or value][row][block]; the
+// host keeps their number below 2^31, so 32-bit arithmetic finds it.
+template <int D, bool F16>
+__device__ __forceinline__ void append_block(const Kv4AppendParams& p, uint32_t i) {
+    constexpr uint32_t kBlocks = D / 16;
+    const uint32_t n = static_cast<uint32_t>(p.n);
+    const uint32_t blk = i % kBlocks, t = i / kBlocks;
+    const uint32_t rest = t / n, row = t - rest * n;
     const bool value = (rest & 1) != 0;
-    const long long head = rest >> 1;  // b * H_kv + key/value head
-    const int b = static_cast<int>(head / p.c.H_kv);
+    const uint32_t head = rest >> 1;  // b * H_kv + key/value head
+    const uint32_t b = head / static_cast<uint32_t>(p.c.H_kv);
     const long long slot = static_cast<long long>(max(p.c.counts[b], 0)) + row;
     if (slot >= p.c.capacity) {
-        if (row == p.n - 1 && blk == 0 && !value) atomicOr(&p.status->word, kDevErrCapacity);
+        if (row == n - 1 && blk == 0 && !value) atomicOr(&p.status->word, kDevErrCapacity);
         return;
     }
-    const uint4* x4 = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(value ? p.x[1] : p.x[0]) +
-                                                     (head * p.n + row) * p.c.d + blk * 16);
+    const uint4* x4 = reinterpret_cast<const uint4*>(value ? p.x[1] : p.x[0]) +
+                      ((static_cast<long long>(head) * n + row) * kBlocks + blk) * 2;
     const uint4 a = __ldg(x4), c = __ldg(x4 + 1);
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
     // magnitudes of bf16 and fp16 order as integers (NaN above infinity)
@@ -101,9 +102,9 @@ __device__ __forceinline__ void append_block(const Kv4AppendParams& p, long long
         lo = byte[0] | byte[1] << 8 | byte[2] << 16 | byte[3] << 24;
         hi = byte[4] | byte[5] << 8 | byte[6] << 16 | byte[7] << 24;
     }
-    const long long at = head * p.c.capacity + slot;
-    *reinterpret_cast<uint2*>((value ? p.c.codes[1] : p.c.codes[0]) + at * (p.c.d / 2) + blk * 8) = make_uint2(lo, hi);
-    (value ? p.c.scales[1] : p.c.scales[0])[at * nblk + blk] = static_cast<uint8_t>(sbyte);
+    const long long at = static_cast<long long>(head) * p.c.capacity + slot;
+    reinterpret_cast<uint2*>(value ? p.c.codes[1] : p.c.codes[0])[at * kBlocks + blk] = make_uint2(lo, hi);
+    (value ? p.c.scales[1] : p.c.scales[0])[at * kBlocks + blk] = static_cast<uint8_t>(sbyte);
     if (blk == 0 && !value) {
         if (p.c.pos != nullptr) p.c.pos[at] = static_cast<int32_t>(p.c.counts[p.c.B + b] + row);
         if (p.c.weight != nullptr) p.c.weight[at] = 0.0f;
@@ -112,12 +113,12 @@ __device__ __forceinline__ void append_block(const Kv4AppendParams& p, long long
 
 // advance: this launch also writes counts_out (a single CTA, or counts_out
 // is not the counts that other CTAs still read).
-template <bool F16>
-__global__ void kv4_append_kernel(const Kv4AppendParams p, long long total, int advance) {
-    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+template <int D, bool F16>
+__global__ void kv4_append_kernel(const Kv4AppendParams p, uint32_t total, int advance) {
+    const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
     grid_release();
     grid_wait();
-    if (i < total) append_block<F16>(p, i);
+    if (i < total) append_block<D, F16>(p, i);
     if (advance && blockIdx.x == 0) {
         __syncthreads();
         for (int b = threadIdx.x; b < p.c.B; b += blockDim.x) advance_counts(p, b);
@@ -131,37 +132,35 @@ __global__ void kv4_advance_kernel(const Kv4AppendParams p) {
     if (b < p.c.B) advance_counts(p, b);
 }
 
-template <bool F16>
-__global__ void kv4_read_kernel(const Kv4ReadParams p, long long total) {
-    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+template <int D, bool F16>
+__global__ void kv4_read_kernel(const Kv4ReadParams p, uint32_t total) {
+    constexpr uint32_t kBlocks = D / 16;
+    const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
     grid_release();
     grid_wait();
     if (i >= total) return;
     const bool value = blockIdx.y != 0;
-    void* x = value ? p.x[1] : p.x[0];
+    uint4* x = static_cast<uint4*>(value ? p.x[1] : p.x[0]);
     if (x == nullptr) return;
-    const int nblk = p.c.d / 16;
-    const int blk = static_cast<int>(i % nblk);
-    const long long t = i / nblk;
-    const long long row = t % p.count;
-    const long long head = t / p.count;
-    const int b = static_cast<int>(head / p.c.H_kv);
-    const long long slot = (p.first != nullptr ? p.first[b] : 0) + row;
+    const uint32_t count = static_cast<uint32_t>(p.count);
+    const uint32_t blk = i % kBlocks, t = i / kBlocks;
+    const uint32_t head = t / count, row = t - head * count;
+    const uint32_t b = head / static_cast<uint32_t>(p.c.H_kv);
+    const long long slot = static_cast<long long>(p.first != nullptr ? p.first[b] : 0) + row;
     uint32_t out[8] = {};
     if (slot >= 0 && slot < p.c.capacity) {
-        const long long at = head * p.c.capacity + slot;
-        const uint2 codes =
-            *reinterpret_cast<const uint2*>((value ? p.c.codes[1] : p.c.codes[0]) + at * (p.c.d / 2) + blk * 8);
-        const uint32_t s = e4m3_to_f16x2((value ? p.c.scales[1] : p.c.scales[0])[at * nblk + blk]);
+        const long long at = (static_cast<long long>(head) * p.c.capacity + slot) * kBlocks + blk;
+        const uint2 codes = reinterpret_cast<const uint2*>(value ? p.c.codes[1] : p.c.codes[0])[at];
+        const uint32_t s = e4m3_to_f16x2((value ? p.c.scales[1] : p.c.scales[0])[at]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t h = mul_f16x2(e2m1x2_to_f16x2(((j < 4 ? codes.x : codes.y) >> (8 * (j & 3))) & 0xFFu), s);
             out[j] = F16 ? h : pack_bf16x2(widen_lo16<true>(h), widen_lo16<true>(h >> 16));
         }
     }
-    uint4* x4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + i * 16);
-    x4[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    x4[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    x += static_cast<long long>(i) * 2;
+    x[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    x[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 }  // namespace
@@ -172,8 +171,10 @@ cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t stream) {
     const int threads = total <= kAppendOneCta ? static_cast<int>((total + 31) / 32 * 32) : kAppendThreads;
     const long long grid = (total + threads - 1) / threads;
     const int advance = (!in_place || grid == 1) ? 1 : 0;
-    auto kern = p.f16 ? kv4_append_kernel<true> : kv4_append_kernel<false>;
-    const cudaError_t e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), threads, 0, stream, p, total, advance);
+    auto kern = p.c.d == 128 ? (p.f16 ? kv4_append_kernel<128, true> : kv4_append_kernel<128, false>)
+                             : (p.f16 ? kv4_append_kernel<64, true> : kv4_append_kernel<64, false>);
+    const cudaError_t e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), threads, 0, stream, p,
+                                           static_cast<uint32_t>(total), advance);
     if (e != cudaSuccess || advance) return e;
     return launch_dependent(kv4_advance_kernel, dim3((p.c.B + 127) / 128), 128, 0, stream, p);
 }
@@ -181,7 +182,9 @@ cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t stream) {
 cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t stream) {
     const long long total = static_cast<long long>(p.c.B) * p.c.H_kv * p.count * (p.c.d / 16);
     const dim3 grid(static_cast<unsigned>((total + 255) / 256), 2);
-    return launch_dependent(p.f16 ? kv4_read_kernel<true> : kv4_read_kernel<false>, grid, 256, 0, stream, p, total);
+    auto kern = p.c.d == 128 ? (p.f16 ? kv4_read_kernel<128, true> : kv4_read_kernel<128, false>)
+                             : (p.f16 ? kv4_read_kernel<64, true> : kv4_read_kernel<64, false>);
+    return launch_dependent(kern, grid, 256, 0, stream, p, static_cast<uint32_t>(total));
 }
 
 }  // namespace fa
