@@ -91,6 +91,7 @@ struct Kv4FwdParams {
     int causal, f16;
     float scale_log2;
     int ctas;             // CTAs of the main kernel
+    int single;           // 1: one per unit
     // workspace
     float* row_lse2;      // [B * H_kv * rows]: base-2 lse of the rows of units that one CTA finished
     float4* part_ml;      // [ctas, 2, rows_per_block]: reference, exact sum, rounded sum
@@ -98,7 +99,11 @@ struct Kv4FwdParams {
     float* logits;        // [B * H_kv, capacity, rows] scaled, base 2, or nullptr
 };
 int kv4_rows_per_block(int64_t rows);
-int kv4_max_ctas(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms);
+struct Kv4Plan {
+    int ctas;
+    bool single;
+};
+Kv4Plan kv4_plan(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms);
 cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, cudaStream_t stream);
 
 struct WeightsParams {

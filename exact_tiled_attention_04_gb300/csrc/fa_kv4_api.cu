@@ -149,7 +149,7 @@ int validate_read(const fa_kv4_cache_t* c, const int32_t* first, int64_t count, 
 
 // ---------------------------------------------------------------- attention
 struct FwdLayout {
-    int ctas;
+    fa::Kv4Plan plan;
     size_t part_ml, part_o, logits, bytes;  // offsets (row_lse2 is first), total
 };
 
@@ -168,12 +168,13 @@ bool fwd_layout(int64_t B, int64_t H, int64_t H_kv, int64_t N_q, int64_t capacit
     const int64_t slabs = mul(mul(B * H_kv, (rows + 7) / 8), capacity / 32);
     if (slabs < 0 || slabs > kInt32Max / 2) return false;
     if (all < 0 || all > kInt32Max || logits < 0 || chunks < 0 || chunks > kInt32Max / 2) return false;
-    l->ctas = fa::kv4_max_ctas(B, H_kv, rows, capacity, sms > 0 ? sms : 1024);
-    const size_t rpb = static_cast<size_t>(fa::kv4_rows_per_block(rows));
+    l->plan = fa::kv4_plan(B, H_kv, rows, capacity, sms > 0 ? sms : 1024);
+    const size_t parts = l->plan.single ? 0 : static_cast<size_t>(l->plan.ctas) * 2 *
+                                                  static_cast<size_t>(fa::kv4_rows_per_block(rows));
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     l->part_ml = up(static_cast<size_t>(all) * 4);
-    l->part_o = l->part_ml + up(static_cast<size_t>(l->ctas) * 2 * rpb * 16);
-    l->logits = l->part_o + up(static_cast<size_t>(l->ctas) * 2 * rpb * static_cast<size_t>(d) * 4);
+    l->part_o = l->part_ml + up(parts * 16);
+    l->logits = l->part_o + up(parts * static_cast<size_t>(d) * 4);
     l->bytes = l->logits + (weight ? up(static_cast<size_t>(logits)) : 0);
     return true;
 }
@@ -347,7 +348,8 @@ int fa_kv4_fwd(const fa_kv4_cache_t* cache, const void* q, void* o, float* lse, 
     p.causal = (dtype & FA_FLAG_CAUSAL) != 0;
     p.f16 = (dtype & 0xFF) == FA_DTYPE_F16;
     p.scale_log2 = scale * kLog2e;
-    p.ctas = l.ctas;
+    p.ctas = l.plan.ctas;
+    p.single = l.plan.single ? 1 : 0;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.row_lse2 = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float4*>(ws + l.part_ml);

@@ -33,6 +33,9 @@
 // weights from the scores, which the first leaves in the workspace (4 bytes a
 // score, against the 68 of reading a key again at d = 128).
 //
+// A cache of at most kSingleSlots slots is not cut: a CTA per unit, four groups
+// of slabs at most, and no second kernel unless weights are asked for.
+//
 // Every wait is bounded as in the forward kernel; a warp that gives up skips
 // its remaining slabs but still reaches the block's barriers.
 #include <cmath>
@@ -49,6 +52,7 @@ namespace {
 using namespace kv4;
 
 constexpr int kLoadWarp = kWarps;
+constexpr int kSingleSlots = 4 * kWarps * kSlab;
 constexpr int kThreads4 = (kWarps + 1) * 32;
 
 // R: query rows per block, 4 (layout Paired), 8 or 16 (layout Wide).
@@ -105,7 +109,7 @@ struct Cursor {
 
     __device__ __forceinline__ bool valid() const { return pos < end; }
     __device__ __forceinline__ void next(const Kv4Cache& c, int units) {
-        pos += s1 - s0;
+        pos = s1 > s0 ? pos + (s1 - s0) : end;
         if (pos >= end) return;
         s0 = 0;
         if (++unit == units) {  // the next sequence that has any slab
@@ -117,6 +121,16 @@ struct Cursor {
             } while (slabs == 0);
         }
         s1 = min(slabs, end - pos);
+    }
+    // Unit `cta` whole, whatever its length (an empty one is visited, too).
+    __device__ __forceinline__ void start_single(const Kv4Cache& c, int units, int cta) {
+        b = cta / units;
+        unit = cta - b * units;
+        len = kv4_length(c, b);
+        slabs = slabs_of(len);
+        pos = base = s0 = 0;
+        s1 = slabs;
+        end = max(slabs, 1);
     }
     __device__ __forceinline__ void start(const Kv4Cache& c, int units, int ctas, int cta) {
         const int lane = threadIdx.x % 32;
@@ -186,7 +200,10 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
 
     const int units = p.c.H_kv * p.row_blocks;
     Cursor cur;
-    cur.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x));
+    if (p.single)
+        cur.start_single(p.c, units, static_cast<int>(blockIdx.x));
+    else
+        cur.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x));
 
     // A unit's slabs go in groups of one per warp; stage i % kStages of the ring holds group i.
     if (warp == kLoadWarp) {
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
     for (int r = warp; r < p.rows; r += kJoinThreads / 32) {
         const Parts u = parts_of(spread, (kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block);
         float v;
-        if (u.first == u.last) {
+        if (p.single || u.first == u.last) {
             v = p.row_lse2[static_cast<long long>(kvh) * p.rows + r];
         } else {
             float M, L, LQ;
@@ -510,8 +527,9 @@ cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), kThreads4, C::kSmemBytes, stream, p);
     if (e != cudaSuccess) return e;
-    const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
+    const long long rows = p.single ? 0 : static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
     const int join = static_cast<int>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+    if (p.single && p.logits == nullptr) return cudaSuccess;
     const long long keys = p.logits == nullptr ? 0
                                                : static_cast<long long>(p.c.B) * p.c.H_kv *
                                                      ((p.c.capacity + kJoinKeys - 1) / kJoinKeys);
@@ -523,12 +541,19 @@ cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
 
 int kv4_rows_per_block(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 
-int kv4_max_ctas(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms) {
+Kv4Plan kv4_plan(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms) {
     const int64_t rpb = kv4_rows_per_block(rows);
-    const int64_t slabs = B * H_kv * ((rows + rpb - 1) / rpb) * (capacity / kSlab);
-    const int64_t most = static_cast<int64_t>(sms) * (rpb <= 8 ? 2 : 1);
-    const int64_t want = (slabs + kWarps - 1) / kWarps;
-    return static_cast<int>(want < most ? want : most);
+    const int64_t units = B * H_kv * ((rows + rpb - 1) / rpb);
+    Kv4Plan plan;
+    plan.single = capacity <= kSingleSlots;
+    if (plan.single) {
+        plan.ctas = static_cast<int>(units);
+    } else {
+        const int64_t most = static_cast<int64_t>(sms) * (rpb <= 8 ? 2 : 1);
+        const int64_t want = (units * (capacity / kSlab) + kWarps - 1) / kWarps;
+        plan.ctas = static_cast<int>(want < most ? want : most);
+    }
+    return plan;
 }
 
 cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, cudaStream_t stream) {

@@ -419,7 +419,7 @@ int fa_kv4_read(const fa_kv4_cache_t* cache, const int32_t* first, int64_t count
  * A row that sees no slot gets O = 0 and lse = -inf and adds no weight.
  * Lengths are read on the device (clamped to 0 .. capacity), so a captured
  * call follows them.  Results do not depend on the order in which blocks run.
- * Two kernels.
+ * One or two kernels.
  */
 int fa_kv4_fwd(const fa_kv4_cache_t* cache, const void* q, void* o, float* lse, float* weight_out,
                int64_t H, int64_t N_q, float scale, int dtype, void* workspace, size_t workspace_bytes,

@@ -177,39 +177,48 @@ def check_attention(c, q, dtype, causal=False, scale=None, weight=True):
     return out, lse, w_out
 
 
+# Caches of up to 1024 slots get a block per head, longer ones are cut into runs that blocks share:
+# both, whatever the lengths in them.
+CAPACITY = pytest.mark.parametrize("capacity", [None, 2048], ids=["short", "cut"])
+
+
 # (N_q, group): rows 1, 3, 8 (one tile of 8), 9, 16 (two), 17, 40, 128 (blocks of 16)
 @pytest.mark.parametrize("N_q,G", [(1, 1), (1, 3), (2, 4), (1, 8), (3, 3), (4, 4), (17, 1), (5, 8), (16, 8)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_row_counts(N_q, G, d):
+@CAPACITY
+def test_row_counts(N_q, G, d, capacity):
     g = rng(200 + N_q * 10 + G)
-    c = filled(g, 2, 2, [333, 70], d)
+    c = filled(g, 2, 2, [333, 70], d, capacity)
     check_attention(c, rows(g, 2, 2 * G, N_q, d), "bf16")
     check_attention(c, rows(g, 2, 2 * G, N_q, d, dtype="f16"), "f16", causal=True)
 
 
 @pytest.mark.parametrize("lengths", [[1], [31, 32, 33], [0, 5, 0, 128], [127, 1, 129, 256, 0, 64, 1000], [2500], [0, 0]])
 @pytest.mark.parametrize("d", [64, 128])
-def test_lengths(lengths, d):
+@CAPACITY
+def test_lengths(lengths, d, capacity):
     g = rng(300 + sum(lengths))
-    c = filled(g, len(lengths), 3, lengths, d)
+    c = filled(g, len(lengths), 3, lengths, d, max(capacity or 0, max(lengths)))
     check_attention(c, rows(g, len(lengths), 6, 1, d), "bf16")
 
 
 @pytest.mark.parametrize("B", [33, 70])
-def test_many_sequences(B):
+@CAPACITY
+def test_many_sequences(B, capacity):
     """More sequences than the warp that looks for its first one holds."""
     g = rng(310 + B)
     lengths = [(37 * b) % 151 if b % 5 else 0 for b in range(B)]
-    c = filled(g, B, 1, lengths, 64)
+    c = filled(g, B, 1, lengths, 64, capacity)
     check_attention(c, rows(g, B, 2, 1, 64, dtype="f16"), "f16")
 
 
 @pytest.mark.parametrize("N_q,length", [(4, 2), (4, 4), (4, 5), (8, 1), (3, 0), (4, 100), (2, 33), (4, 640)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_causal_drafts(N_q, length, d):
+@CAPACITY
+def test_causal_drafts(N_q, length, d, capacity):
     """Rows that see fewer slots, or none (the draft is longer than the cache)."""
     g = rng(320 + N_q + length)
-    c = filled(g, 2, 2, [length, 200], d)
+    c = filled(g, 2, 2, [length, 200], d, capacity)
     check_attention(c, rows(g, 2, 4, N_q, d), "bf16", causal=True)
 
 
@@ -229,14 +238,16 @@ def test_query_magnitudes(dtype, gain):
     check_attention(c, q, dtype, scale=float(0.2 / gain), weight=False)
 
 
-def test_growing_scores():
+@pytest.mark.parametrize("G", [4, 8, 12])  # the three layouts
+@pytest.mark.parametrize("n", [900, 3000])
+def test_growing_scores(G, n):
     """Scores that keep rising along the cache: every warp moves its reference many times."""
     g = rng(350)
-    c = fa.KV4Cache.empty(1, 2, 3000, 128)
-    ramp = torch.linspace(0.1, 8.0, 3000, device="cuda")[None, None, :, None]
+    c = fa.KV4Cache.empty(1, 2, n, 128)
+    ramp = torch.linspace(0.1, 8.0, n, device="cuda")[None, None, :, None]
     u = torch.randn(1, 2, 1, 128, generator=g, device="cuda")
-    fa.kv4_append(c, (u * ramp).bfloat16(), rows(g, 1, 2, 3000, 128))
-    q = (u.repeat_interleave(4, 1) + 0.1 * torch.randn(1, 8, 1, 128, generator=g, device="cuda")).bfloat16()
+    fa.kv4_append(c, (u * ramp).bfloat16(), rows(g, 1, 2, n, 128))
+    q = (u.repeat_interleave(G, 1) + 0.1 * torch.randn(1, 2 * G, 1, 128, generator=g, device="cuda")).bfloat16()
     check_attention(c, q, "bf16")
 
 
@@ -255,11 +266,13 @@ def test_dominant_and_tiny_weights():
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_nan_behind_the_mask(d):
+@pytest.mark.parametrize("G", [1, 2, 4])  # 3, 6 and 12 rows: the three layouts
+@CAPACITY
+def test_nan_behind_the_mask(d, G, capacity):
     """A NaN entry that only the last row of a draft sees leaves the other rows as they were."""
     g = rng(360)
-    c = filled(g, 1, 1, [100], d)
-    q = rows(g, 1, 2, 3, d)
+    c = filled(g, 1, 1, [100], d, capacity)
+    q = rows(g, 1, G, 3, d)
     good, _ = fa.kv4_attention(q, c, causal=True)
     old = c.v_scales[0, 0, 99, 1].clone()
     c.v_scales[0, 0, 99, 1] = 0x7F
