@@ -378,17 +378,20 @@ __device__ __forceinline__ Parts parts_of(const Spread& s, int unit) {
 __device__ __forceinline__ long long part_row(int cta, int first, int rows, int r) {
     return (static_cast<long long>(cta) * 2 + (cta == first ? 1 : 0)) * rows + r;
 }
-// A row's reference, exact sum and rounded sum over its parts, by a warp.
+// A row's reference, exact sum and rounded sum over its parts, by a warp, and
+// the factor of the part first + lane (0 where there is none).
 __device__ __forceinline__ void row_sums(const Kv4FwdParams& p, const Parts& u, int rows, int r, float& M, float& L,
-                                         float& LQ) {
-    const int lane = threadIdx.x % 32;
-    M = -INFINITY;
-    for (int c = u.first + lane; c <= u.last; c += 32)
-        M = fmaxf(M, p.part_ml[part_row(c, u.first, rows, r)].x);
+                                         float& LQ, float& f) {
+    const int lane = threadIdx.x % 32, c0 = u.first + lane;
+    const float4 ml0 = c0 <= u.last ? p.part_ml[part_row(c0, u.first, rows, r)] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    M = ml0.x;
+    for (int c = c0 + 32; c <= u.last; c += 32) M = fmaxf(M, p.part_ml[part_row(c, u.first, rows, r)].x);
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    L = LQ = 0.0f;
-    for (int c = u.first + lane; c <= u.last; c += 32) {
+    f = c0 > u.last ? 0.0f : M == -INFINITY ? 1.0f : ex2(ml0.x - M);
+    L = f * ml0.y;
+    LQ = f * ml0.z;
+    for (int c = c0 + 32; c <= u.last; c += 32) {
         const float4 ml = p.part_ml[part_row(c, u.first, rows, r)];
         const float w = M == -INFINITY ? 1.0f : ex2(ml.x - M);
         L += w * ml.y;
@@ -404,6 +407,7 @@ __device__ __forceinline__ void row_sums(const Kv4FwdParams& p, const Parts& u, 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinKeys = 1024;  // keys per block of the weights' part
 constexpr int kMaxRows = 128;
+constexpr int kAhead = 8;  // parts' rows loaded ahead of the factors
 
 // Blocks 0 .. join_blocks - 1: one warp per output row whose unit several
 // CTAs shared (or that has no slot at all).  The others: accumulated weight,
@@ -431,26 +435,43 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
         constexpr int kPer = D / 32;
         float acc[kPer] = {}, M = -INFINITY, L = 0.0f, LQ = 0.0f;
         if (u.slabs > 0) {
-            const int rb = r % rows_per_block;
-            row_sums(p, u, rows_per_block, rb, M, L, LQ);
-            // 32 parts' factors at a time, one per lane; four parts' rows in flight
-            for (int c0 = u.first; c0 <= u.last; c0 += 32) {
-                const int mine = c0 + lane;
-                float f = 0.0f;
-                if (mine <= u.last)
-                    f = M == -INFINITY ? 1.0f : ex2(p.part_ml[part_row(mine, u.first, rows_per_block, rb)].x - M);
-                const int n = min(32, u.last - c0 + 1);
-#pragma unroll 4
-                for (int i = 0; i < n; ++i) {
-                    const float w = __shfl_sync(0xffffffffu, f, i);
-                    const float* src =
-                        p.part_o + part_row(c0 + i, u.first, rows_per_block, rb) * D + lane * kPer;
+            const int rb = r % rows_per_block, parts = u.last - u.first + 1;
+            const auto load = [&](int i, float (&v)[kPer]) {
+                const float* src = p.part_o + part_row(u.first + i, u.first, rows_per_block, rb) * D + lane * kPer;
 #pragma unroll
-                    for (int j = 0; j < kPer; j += 2) {
-                        const float2 v = *reinterpret_cast<const float2*>(src + j);
-                        acc[j] += w * v.x;
-                        acc[j + 1] += w * v.y;
-                    }
+                for (int j = 0; j < kPer; j += 2)
+                    *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(src + j);
+            };
+            // the first parts' rows are on their way while the factors are formed
+            float ahead[kAhead][kPer], f;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (i < parts) load(i, ahead[i]);
+            row_sums(p, u, rows_per_block, rb, M, L, LQ, f);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float w = __shfl_sync(0xffffffffu, f, i);
+                if (i < parts)
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) acc[j] += w * ahead[i][j];
+            }
+            // the others: 32 parts' factors at a time, one per lane; four parts' rows in flight
+            for (int i0 = kAhead; i0 < parts; i0 = (i0 / 32 + 1) * 32) {
+                if (i0 >= 32) {
+                    const int mine = u.first + i0 + lane;
+                    f = 0.0f;
+                    if (mine <= u.last)
+                        f = M == -INFINITY ? 1.0f
+                                           : ex2(p.part_ml[part_row(mine, u.first, rows_per_block, rb)].x - M);
+                }
+                const int n = min((i0 / 32 + 1) * 32, parts);
+#pragma unroll 4
+                for (int i = i0; i < n; ++i) {
+                    const float w = __shfl_sync(0xffffffffu, f, i % 32);
+                    float v[kPer];
+                    load(i, v);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) acc[j] += w * v[j];
                 }
             }
         }
@@ -492,8 +513,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
         if (p.single || u.first == u.last) {
             v = p.row_lse2[static_cast<long long>(kvh) * p.rows + r];
         } else {
-            float M, L, LQ;
-            row_sums(p, u, rows_per_block, r % rows_per_block, M, L, LQ);
+            float M, L, LQ, f;
+            row_sums(p, u, rows_per_block, r % rows_per_block, M, L, LQ, f);
             v = L == 0.0f ? -INFINITY : M + log2f(L);
         }
         if (lane == 0) lse2[r] = v == -INFINITY ? INFINITY : v;  // a row that sees nothing adds nothing
