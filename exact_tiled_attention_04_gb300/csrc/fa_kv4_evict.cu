@@ -5,25 +5,35 @@
 // One block per head, or a cluster of them where a head is long, every CTA
 // holding a contiguous slice of the head's keys in shared memory:
 //   1. radix selection, 8 bits at a time, gives the threshold T and how many
-//      entries equal to T are kept.  A histogram has 256 bins of 32 counters,
+//      entries equal to T are kept; the first histogram is counted as the keys
+//      arrive, and once at most 256 entries are open they are compared with
+//      one another.  A histogram has 256 bins of 32 counters,
 //      one per lane, so that no two lanes of a warp meet in a bank or on a
 //      counter, however the weights are distributed (a layer's weights share a
 //      few exponents, all new entries share 0);
 //   2. a bit per entry: kept = key > T, or key == T and among the first of
-//      those in slot order;
+//      those in slot order; a thread forms the word of 32 entries (a ballot
+//      per entry and warp took 3000 cycles instead of 2000 for 16384 keys);
 //   3. holes (slots below the new length whose entry leaves) and late entries
 //      (kept ones at or behind it) are as many as one another; hole r takes
-//      late entry r.  Ranks come from a scan over the words of bits;
+//      late entry r.  Ranks come from a scan over the words of bits, and the
+//      thread of a word walks its late entries (an entry per lane: 5300 cycles
+//      instead of 1500);
 //   4. the moved rows are copied, 32 a warp with all their loads in flight.
 //      Sources lie at or behind the new length and targets below it, so in
 //      place no copy reads what another writes.
 // A decode step that puts one entry too many into the cache needs no
 // threshold: up to kEvFew leaving entries of a head that one block holds are
 // found one by one as block-wide minima.
-// Short rows are bound by the latency of these steps, long ones that move
-// many entries by their copies.
+//
+// Short rows are bound by the latency of these steps (4097 slots to 4096, 64
+// heads, d = 64: 5.1 us); long ones by the selection, on an SM per head, and
+// then by reading scattered rows (up to 16384 slots to 2048, 64 heads,
+// d = 128: 25.3 us, of them 11 for the sources and 10.5 for the 40 MB copied,
+// whose 4-byte and 8-byte parts cost a 32-byte sector each).
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_kv4.h"
 #include "fa_ptx.cuh"
@@ -46,7 +56,6 @@ struct alignas(16) EvShared {  // the keys behind it are read 16 bytes at a time
         uint32_t hist[256 * 32];  // [bin][lane]
         struct {                  // after the selection, a word per 32 entries
             uint32_t kept[kEvMaxWords];   // bit i: entry stays
-            uint32_t equal[kEvMaxWords];  // bit i: key equals the threshold
             uint32_t before[kEvMaxWords]; // holes (low half) and late entries (high half) of earlier words
         };
         struct {                  // few leaving entries
@@ -204,6 +213,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
     const int b = head / p.from.H_kv;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (threadIdx.x == 0) sh.listed = 0u;
+    if (kOne && threadIdx.x < kEvList / 4)  // no key is 0
+        reinterpret_cast<uint4*>(sh.list)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = threadIdx.x; i < 256 * 8; i += kEvThreads)
         reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     grid_release();
@@ -227,19 +238,53 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
         auto key_of = [&](float w, int at) -> uint32_t {
             return rank_key(w, protect && (at < p.sinks || at >= newest));
         };
-        if (((reinterpret_cast<uintptr_t>(rank_by) | (protect ? reinterpret_cast<uintptr_t>(pos) : 0u)) & 15u) == 0u) {
-#pragma unroll 4
-            for (int i = 4 * threadIdx.x; i < size; i += 4 * kEvThreads) {  // a row has 128 slots or a multiple
-                const float4 w = *reinterpret_cast<const float4*>(rank_by + i);
-                const int4 at = protect ? *reinterpret_cast<const int4*>(pos + i) : make_int4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(keys + i) =
-                    make_uint4(key_of(w.x, at.x), key_of(w.y, at.y), key_of(w.z, at.z), key_of(w.w, at.w));
+        const bool few = kOne && n - nn <= kEvFew;  // no threshold
+        // the keys, `loads` 16-byte reads a thread in flight; where a threshold is wanted, also the histogram of
+        // their first 8 bits, while others are on their way
+        const bool wide =
+            ((reinterpret_cast<uintptr_t>(rank_by) | (protect ? reinterpret_cast<uintptr_t>(pos) : 0u)) & 15u) == 0u;
+        auto load_keys = [&](auto loads, auto counted) {
+            constexpr int kLoads = decltype(loads)::value;
+            auto count_key = [&](uint32_t k) {
+                if constexpr (decltype(counted)::value) atomicAdd(&sh.hist[(k >> 24) * 32 + lane], 1u);
+            };
+            if (!wide) {
+                for (int i = threadIdx.x; i < size; i += kEvThreads) {
+                    keys[i] = key_of(rank_by[i], protect ? pos[i] : 0);
+                    count_key(keys[i]);
+                }
+                return;
             }
-        } else {
-            for (int i = threadIdx.x; i < size; i += kEvThreads) keys[i] = key_of(rank_by[i], protect ? pos[i] : 0);
-        }
-        __syncthreads();
-        if (kOne && n - nn <= kEvFew) {
+            for (int i0 = 4 * threadIdx.x; i0 < size; i0 += kLoads * 4 * kEvThreads) {  // a row has 128 n slots
+                float4 w[kLoads];
+                int4 at[kLoads];
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int i = i0 + u * 4 * kEvThreads;
+                    w[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    at[u] = make_int4(0, 0, 0, 0);
+                    if (i < size) {
+                        w[u] = *reinterpret_cast<const float4*>(rank_by + i);
+                        if (protect) at[u] = *reinterpret_cast<const int4*>(pos + i);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int i = i0 + u * 4 * kEvThreads;
+                    if (i >= size) break;
+                    const uint4 k = make_uint4(key_of(w[u].x, at[u].x), key_of(w[u].y, at[u].y),
+                                               key_of(w[u].z, at[u].z), key_of(w[u].w, at[u].w));
+                    *reinterpret_cast<uint4*>(keys + i) = k;
+                    count_key(k.x);
+                    if (i + 1 < size) count_key(k.y);
+                    if (i + 2 < size) count_key(k.z);
+                    if (i + 3 < size) count_key(k.w);
+                }
+            }
+        };
+        if (few) {
+            load_keys(std::integral_constant<int, 1>{}, std::false_type{});
+            __syncthreads();
             // the entries in the order they leave: ascending key, descending slot
             uint32_t last_key = 0u;
             int last_slot = 0x7FFFFFFF;
@@ -284,21 +329,26 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
             if (static_cast<int>(threadIdx.x) < holes) src[sh.hole[threadIdx.x]] = sh.late[threadIdx.x];
             copied = true;
         } else {
+            __syncthreads();  // the histogram is clear
+            load_keys(std::integral_constant<int, 4>{}, std::true_type{});
+            __syncthreads();
             // 1. threshold: the entries whose upper bits equal `prefix` are still open
             uint32_t prefix = 0u;
             uint32_t want = static_cast<uint32_t>(nn), open = 0u;  // entries to take among the open ones; those of the bin
 #pragma unroll 1
             for (int down = 24; down >= 0; down -= 8) {
+                if (down < 24) {
 #pragma unroll 4
-                for (int i = 4 * threadIdx.x; i < size; i += 4 * kEvThreads) {
-                    const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
-                    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+                    for (int i = 4 * threadIdx.x; i < size; i += 4 * kEvThreads) {
+                        const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
+                        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (i + j < size && (down == 24 || (k[j] >> (down + 8)) == prefix))
-                            atomicAdd(&sh.hist[((k[j] >> down) & 255u) * 32 + lane], 1u);
+                        for (int j = 0; j < 4; ++j)
+                            if (i + j < size && (k[j] >> (down + 8)) == prefix)
+                                atomicAdd(&sh.hist[((k[j] >> down) & 255u) * 32 + lane], 1u);
+                    }
+                    __syncthreads();
                 }
-                __syncthreads();
                 // four threads per bin, each eight of its counters, in an order that keeps the banks apart
                 const int bin = threadIdx.x / 4;
                 uint32_t sum = 0u;
@@ -361,19 +411,24 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                             if (i + j < size && (k[j] >> down) == prefix) sh.list[atomicAdd(&sh.listed, 1u)] = k[j];
                     }
                     __syncthreads();
-                    if (threadIdx.x < open) {
-                        const uint32_t k = sh.list[threadIdx.x];
-                        uint32_t more = 0u, equal = 0u;
-                        for (uint32_t i = 0; i < open; ++i) {
-                            const uint32_t o = sh.list[i];
-                            more += o > k ? 1u : 0u;
-                            equal += o == k ? 1u : 0u;
-                        }
-                        if (more < want && want <= more + equal) {  // every entry equal to the threshold writes the same
-                            sh.pick[0] = k;
-                            sh.pick[1] = more;
-                            sh.pick[2] = equal;
-                        }
+                    // four threads per entry
+                    const uint32_t mine = threadIdx.x / 4;
+                    const uint32_t k = mine < open ? sh.list[mine] : 0u;
+                    uint32_t more = 0u, equal = 0u;
+                    for (uint32_t i = 4 * (threadIdx.x % 4); i < open; i += 16) {  // zeros behind the last
+                        const uint4 o = *reinterpret_cast<const uint4*>(&sh.list[i]);
+                        more += (o.x > k ? 1u : 0u) + (o.y > k ? 1u : 0u) + (o.z > k ? 1u : 0u) + (o.w > k ? 1u : 0u);
+                        equal += (o.x == k ? 1u : 0u) + (o.y == k ? 1u : 0u) + (o.z == k ? 1u : 0u) + (o.w == k ? 1u : 0u);
+                    }
+#pragma unroll
+                    for (int o = 1; o < 4; o *= 2) {
+                        more += __shfl_xor_sync(0xffffffffu, more, o);
+                        equal += __shfl_xor_sync(0xffffffffu, equal, o);
+                    }
+                    if (mine < open && more < want && want <= more + equal) {  // all that equal the threshold write the same
+                        sh.pick[0] = k;
+                        sh.pick[1] = more;
+                        sh.pick[2] = equal;
                     }
                     __syncthreads();
                     prefix = sh.pick[0];
@@ -382,26 +437,31 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                     break;
                 }
             }
-            // 2. a bit per entry, words in turn to the warps
+            // 2. a bit per entry: a word of 32 entries per thread (two in the longest slices), its eight
+            // 16-byte reads begun at another one by each lane, to keep the banks apart
             const uint32_t T = prefix;  // `want` of the `open` entries equal to T are kept
             const int words = (size + 31) / 32;
-#pragma unroll 4
-            for (int x = warp; x < words; x += kEvWarps) {
-                const int i = x * 32 + lane;
-                const uint32_t k = i < size ? keys[i] : 0u;
-                const uint32_t equal = __ballot_sync(0xffffffffu, i < size && k == T);
-                const uint32_t more = __ballot_sync(0xffffffffu, i < size && k > T);
-                if (lane == 0) {
-                    sh.kept[x] = more | (want == open ? equal : 0u);
-                    sh.equal[x] = equal;
+            const int per = words > kEvThreads ? 2 : 1;
+            const int x0 = per * static_cast<int>(threadIdx.x);
+            uint32_t stay[2] = {0u, 0u}, ties[2] = {0u, 0u};
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int x = x0 + w;
+                if (w >= per || x >= words) break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = (j + lane) & 7;
+                    const uint4 k = *reinterpret_cast<const uint4*>(keys + 32 * x + 4 * c);
+                    stay[w] |= ((k.x > T ? 1u : 0u) | (k.y > T ? 2u : 0u) | (k.z > T ? 4u : 0u) | (k.w > T ? 8u : 0u)) << (4 * c);
+                    ties[w] |= ((k.x == T ? 1u : 0u) | (k.y == T ? 2u : 0u) | (k.z == T ? 4u : 0u) | (k.w == T ? 8u : 0u)) << (4 * c);
                 }
+                const uint32_t valid = low_bits(size - 32 * x);
+                stay[w] &= valid;
+                ties[w] &= valid;
             }
-            __syncthreads();
-            const int x0 = 2 * static_cast<int>(threadIdx.x);  // this thread's words: x0, x0 + 1
             if (want < open) {  // of the entries equal to T the first `want`, over the cluster
-                const uint32_t e0 = x0 < words ? sh.equal[x0] : 0u, e1 = x0 + 1 < words ? sh.equal[x0 + 1] : 0u;
                 uint32_t all;
-                uint32_t before = block_prefix(__popc(e0) + __popc(e1), sh.warp_count, &all);
+                uint32_t before = block_prefix(__popc(ties[0]) + __popc(ties[1]), sh.warp_count, &all);
                 if constexpr (!kOne) {
                     if (threadIdx.x == 0) sh.count[0] = all;
                     cluster_sync_all();
@@ -409,8 +469,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                     cluster_sync_all();  // count is written again below
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t bits = i == 0 ? e0 : e1;
+                for (int w = 0; w < 2; ++w) {
+                    uint32_t bits = ties[w];
                     const uint32_t n_bits = __popc(bits);
                     const int take = static_cast<int>(want) - static_cast<int>(before);
                     if (take < static_cast<int>(n_bits)) {
@@ -421,25 +481,32 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                         }
                         bits = some;
                     }
-                    if (x0 + i < words) sh.kept[x0 + i] |= bits;
+                    stay[w] |= bits;
                     before += n_bits;
                 }
+            } else {
+                stay[0] |= ties[0];
+                stay[1] |= ties[1];
             }
             // 3. ranks of holes and late entries: prefixes by word
-            uint32_t n0 = 0u, n1 = 0u;
+            uint32_t before[2], both[2] = {0u, 0u};
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (x0 + i < words) {
-                    const uint32_t stay = sh.kept[x0 + i], below = low_bits(nn - begin - (x0 + i) * 32);
-                    const uint32_t n_i = static_cast<uint32_t>(__popc(low_bits(size - (x0 + i) * 32) & below & ~stay)) |
-                                         static_cast<uint32_t>(__popc(stay & ~below)) << 16;
-                    if (i == 0) n0 = n_i;
-                    else n1 = n_i;
-                }
+            for (int w = 0; w < 2; ++w) {
+                const int x = x0 + w;
+                if (w >= per || x >= words) break;
+                const uint32_t below = low_bits(nn - begin - 32 * x);
+                both[w] = static_cast<uint32_t>(__popc(low_bits(size - 32 * x) & below & ~stay[w])) |
+                          static_cast<uint32_t>(__popc(stay[w] & ~below)) << 16;
+            }
             uint32_t all;
-            const uint32_t before = block_prefix(n0 + n1, sh.warp_count, &all);
-            if (x0 < words) sh.before[x0] = before;
-            if (x0 + 1 < words) sh.before[x0 + 1] = before + n0;
+            before[0] = block_prefix(both[0] + both[1], sh.warp_count, &all);
+            before[1] = before[0] + both[0];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (w >= per || x0 + w >= words) break;
+                sh.kept[x0 + w] = stay[w];
+                sh.before[x0 + w] = before[w];
+            }
             uint32_t h_first = 0u, l_first = 0u;  // of earlier CTAs
             if constexpr (kOne) {
                 __syncthreads();
@@ -458,8 +525,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
 #pragma unroll 2
             for (int x = warp; x < low_words; x += kEvWarps) {
                 const int i = begin + x * 32 + lane;
-                const uint32_t stay = sh.kept[x];
-                const uint32_t holes = low_bits(size - x * 32) & low_bits(nn - begin - x * 32) & ~stay;
+                const uint32_t kept = sh.kept[x];
+                const uint32_t holes = low_bits(size - x * 32) & low_bits(nn - begin - x * 32) & ~kept;
                 if ((holes >> lane) & 1u) {
                     const uint32_t r = h_first + (sh.before[x] & 0xFFFFu) + __popc(holes & ((1u << lane) - 1u));
                     if constexpr (kOne)
@@ -467,23 +534,24 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                     else
                         st_cluster_u32(keys_addr + 4u * (r % static_cast<uint32_t>(slice)),
                                        r / static_cast<uint32_t>(slice), static_cast<uint32_t>(i));
-                } else if (i < nn && ((stay >> lane) & 1u)) {
+                } else if (i < nn && ((kept >> lane) & 1u)) {
                     src[i] = i;
                 }
             }
             sync_all();
-#pragma unroll 2
-            for (int x = max(0, nn - begin) / 32 + warp; x < words; x += kEvWarps) {
-                const uint32_t late = sh.kept[x] & ~low_bits(nn - begin - x * 32);
-                if ((late >> lane) & 1u) {
-                    const uint32_t r = l_first + (sh.before[x] >> 16) + __popc(late & ((1u << lane) - 1u));
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int x = x0 + w;
+                if (w >= per || x >= words) break;
+                uint32_t r = l_first + (before[w] >> 16);
+                for (uint32_t late = stay[w] & ~low_bits(nn - begin - 32 * x); late != 0u; late &= late - 1u, ++r) {
                     uint32_t hole;
                     if constexpr (kOne)
                         hole = keys[r];
                     else
                         hole = ld_cluster_u32(keys_addr + 4u * (r % static_cast<uint32_t>(slice)),
                                               r / static_cast<uint32_t>(slice));
-                    src[hole] = begin + x * 32 + lane;
+                    src[hole] = begin + 32 * x + __ffs(static_cast<int>(late)) - 1;
                 }
             }
         }
