@@ -27,9 +27,9 @@
 // found one by one as block-wide minima.
 //
 // Short rows are bound by the latency of these steps (4097 slots to 4096, 64
-// heads, d = 64: 5.1 us); long ones by the selection, on an SM per head, and
+// heads, d = 64: 4.8 us); long ones by the selection, on an SM per head, and
 // then by reading scattered rows (up to 16384 slots to 2048, 64 heads,
-// d = 128: 25.3 us, of them 11 for the sources and 10.5 for the 40 MB copied,
+// d = 128: 25.2 us, of them 11 for the sources and 10.5 for the 40 MB copied,
 // whose 4-byte and 8-byte parts cost a 32-byte sector each).
 #include <cstddef>
 #include <cstdint>
@@ -217,23 +217,27 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
         reinterpret_cast<uint4*>(sh.list)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = threadIdx.x; i < 256 * 8; i += kEvThreads)
         reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    // what comes from the arguments alone is formed ahead of the wait
     grid_release();
-    grid_wait();
-    const int n = min(max(p.from.counts[b], 0), p.from.capacity);
-    const int seen = p.from.counts[p.from.B + b];
-    const int nn = min(n, p.keep);  // the new length
     const bool in_place = p.to.codes[0] == p.from.codes[0];
-    bool copied = false;
-    int32_t* src = p.src + static_cast<long long>(head) * p.keep;
+    const bool protect = p.sinks > 0 || p.recent > 0;
     const long long row0 = static_cast<long long>(head) * p.from.capacity;
     const long long to0 = static_cast<long long>(head) * p.to.capacity;
+    const float* rank_by = p.rank_by + row0 + static_cast<long long>(rank) * slice;
+    const int32_t* pos = p.from.pos + row0 + static_cast<long long>(rank) * slice;
+    const bool wide =
+        ((reinterpret_cast<uintptr_t>(rank_by) | (protect ? reinterpret_cast<uintptr_t>(pos) : 0u)) & 15u) == 0u;
+    int32_t* src = p.src + static_cast<long long>(head) * p.keep;
+    const int32_t* counts = p.from.counts + b;
+    bool copied = false;
+    grid_wait();
+    const int n = min(max(counts[0], 0), p.from.capacity);
+    const int seen = counts[p.from.B];
+    const int nn = min(n, p.keep);  // the new length
     const int begin = static_cast<int>(min(static_cast<long long>(rank) * slice, static_cast<long long>(n)));
     const int size = min(slice, n - begin);  // this CTA's keys
 
     if (n > nn) {
-        const float* rank_by = p.rank_by + row0 + begin;
-        const int32_t* pos = p.from.pos + row0 + begin;
-        const bool protect = p.sinks > 0 || p.recent > 0;
         const long long newest = static_cast<long long>(seen) - p.recent;
         auto key_of = [&](float w, int at) -> uint32_t {
             return rank_key(w, protect && (at < p.sinks || at >= newest));
@@ -241,8 +245,6 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
         const bool few = kOne && n - nn <= kEvFew;  // no threshold
         // the keys, `loads` 16-byte reads a thread in flight; where a threshold is wanted, also the histogram of
         // their first 8 bits, while others are on their way
-        const bool wide =
-            ((reinterpret_cast<uintptr_t>(rank_by) | (protect ? reinterpret_cast<uintptr_t>(pos) : 0u)) & 15u) == 0u;
         auto load_keys = [&](auto loads, auto counted) {
             constexpr int kLoads = decltype(loads)::value;
             auto count_key = [&](uint32_t k) {
