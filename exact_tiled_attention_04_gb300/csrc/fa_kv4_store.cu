@@ -64,7 +64,7 @@ __device__ __forceinline__ void load_values(const uint4* x, bool wide, uint32_t 
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                      : "l"(x));
     } else {
-        const uint4 a = __ldg(x), c = __ldg(x + 1);
+        const uint4 a = x[0], c = x[1];
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
     }
 }

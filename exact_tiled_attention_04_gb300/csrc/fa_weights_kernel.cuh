@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = first_row + 128 * block_in_head + lane + 32 * i;
-                    lse[i] = head < p.group && row < p.Nq ? __ldg(src + row) : -INFINITY;
+                    lse[i] = head < p.group && row < p.Nq ? src[row] : -INFINITY;
                 }
             };
             load_lse();

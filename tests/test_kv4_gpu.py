@@ -655,3 +655,70 @@ def test_captured_steps_follow_the_counts():
         x, y = getattr(eager, a), getattr(graph, a)
         for b, n in enumerate(eager.lengths.tolist()):
             assert torch.equal(x[b, :, :n], y[b, :, :n]), a
+
+
+def test_captured_across_streams():
+    """A captured step whose row and query come from another captured stream, beside which the
+    append runs, and whose output a third kernel reads."""
+    g = rng(720)
+    B, H, H_kv, d = 2, 8, 2, 128
+    c = filled(g, B, H_kv, [1500, 1100], d, capacity=2048)
+    k, v, q = (rows(g, B, h, 1, d) for h in (H_kv, H_kv, H))
+    q2, out, twice = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty(c.workspace_size(H, 1, True), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.mul(q, 2, out=q2)
+        fa.kv4_append(c, k, v)
+        here.wait_stream(side)
+        fa.kv4_attention(q2, c, out=out, weight_out=c.weight, workspace=ws)
+        torch.mul(out, 2, out=twice)
+
+    state = [t.clone() for t in (c.counts, c.weight)]
+    step()
+    torch.cuda.synchronize()
+    want, weight = twice.clone(), c.weight.clone()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        step()
+    for _ in range(3):
+        c.counts.copy_(state[0]), c.weight.copy_(state[1])
+        for t in (q2, out, twice):
+            t.zero_()
+        gr.replay()
+        assert torch.equal(twice, want) and torch.equal(c.weight, weight)
+
+
+def test_prompt_into_cache_behind_the_forward_pass():
+    """The forward pass, the keys' weights from its lse, storing and attending follow one another
+    without a wait in between, and match the same calls made one at a time."""
+    g = rng(730)
+    B, H, H_kv, N, d = 1, 8, 2, 2500, 128  # a last wave that the forward pass splits
+    q, k, v = (rows(g, B, h, N, d) for h in (H, H_kv, H_kv))
+    want = None
+    for apart in (True, False, False):
+        def step():
+            if apart:
+                torch.cuda.synchronize()
+        c = fa.KV4Cache.empty(B, H_kv, N + 1, d)
+        c.weight.zero_()
+        x = (k * 1).contiguous()
+        step()
+        o, lse = fa.attention(q, x, v, causal=True)
+        step()
+        fa.kv4_append(c, x, v)
+        step()
+        fa.attention_weights(q, x, lse, causal=True, weight_in=c.weight[:, :, :N], out=c.weight[:, :, :N])
+        step()
+        w = c.weight[:, :, :N].clone()
+        step()
+        out, _ = fa.kv4_attention(q[:, :, -1:].contiguous(), c, weight_out=c.weight)
+        torch.cuda.synchronize()
+        got = [o, lse, w, out, c.weight[:, :, :N].clone()]
+        want = want or got
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
