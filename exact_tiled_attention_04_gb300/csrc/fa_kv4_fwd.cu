@@ -36,6 +36,12 @@
 // A cache of at most kSingleSlots slots is not cut: a CTA per unit, four groups
 // of slabs at most, and no second kernel unless weights are asked for.
 //
+// What is left (B = 8, H = 32/8, d = 128): 16384 slots take 34.9 us, 65536
+// 102.8 (5.9 TB/s); 49152 more cost what reading them does, so 12 us do not
+// depend on the length: 1.5 from the wait to the first copy, 1.7 until it is
+// there, up to 8 between the first and the last block's end (equal runs, but
+// an SM's share of the bandwidth is not), 1.7 for the second kernel.
+//
 // Every wait is bounded as in the forward kernel; a warp that gives up skips
 // its remaining slabs but still reaches the block's barriers.
 #include <cmath>
@@ -59,7 +65,8 @@ constexpr int kThreads4 = (kWarps + 1) * 32;
 template <int D, int R>
 struct Kv4Cfg {
     static constexpr int kRows = R;
-    static constexpr int kStages = 2;
+    static constexpr int kStages = D == 128 ? 2 : 4;  // the same bytes in flight (two at d = 64: 68.1, four 66.9 us
+                                                      // at B = 8, H = 32/8, 65536 slots)
     static constexpr int kCodeBytes = kSlab * D / 2;
     static constexpr int kScaleBytes = kSlab * D / 16;
     static constexpr int kStageBytes = 2 * kWarps * (kCodeBytes + kScaleBytes);  // a group: a slab per warp
