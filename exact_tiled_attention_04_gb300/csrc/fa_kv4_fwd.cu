@@ -33,8 +33,11 @@
 // weights from the scores, which the first leaves in the workspace (4 bytes a
 // score, against the 68 of reading a key again at d = 128).
 //
-// A cache of at most kSingleSlots slots is not cut: a CTA per unit, four groups
-// of slabs at most, and no second kernel unless weights are asked for.
+// A cache of at most kWholeSlots slots, or twice that where there are as many
+// units as SMs, is not cut: a CTA per unit, and no second kernel unless
+// weights are asked for.  Whole against cut, in us, d = 128 and H = 32/8:
+// 512 slots B = 1 5.5 / 6.3, B = 8 5.5 / 6.5, B = 256 45.8 / 45.5; 1024 slots
+// B = 1 7.6 / 6.4, B = 8 8.2 / 8.0, B = 24 12.0 / 14.7, B = 256 68.6 / 69.9.
 //
 // What is left (B = 8, H = 32/8, d = 128): 16384 slots take 34.9 us, 65536
 // 102.8 (5.9 TB/s); 49152 more cost what reading them does, so 12 us do not
@@ -58,7 +61,7 @@ namespace {
 using namespace kv4;
 
 constexpr int kLoadWarp = kWarps;
-constexpr int kSingleSlots = 4 * kWarps * kSlab;
+constexpr int kWholeSlots = 2 * kWarps * kSlab;
 constexpr int kThreads4 = (kWarps + 1) * 32;
 
 // R: query rows per block, 4 (layout Paired), 8 or 16 (layout Wide).
@@ -573,7 +576,7 @@ Kv4Plan kv4_plan(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sm
     const int64_t rpb = kv4_rows_per_block(rows);
     const int64_t units = B * H_kv * ((rows + rpb - 1) / rpb);
     Kv4Plan plan;
-    plan.single = capacity <= kSingleSlots;
+    plan.single = capacity <= (units >= sms ? 2 : 1) * kWholeSlots;
     if (plan.single) {
         plan.ctas = static_cast<int>(units);
     } else {

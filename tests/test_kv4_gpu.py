@@ -229,6 +229,15 @@ def test_many_sequences(B, capacity):
     check_attention(c, rows(g, B, 2, 1, 64, dtype="f16"), "f16")
 
 
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 8)])
+def test_as_many_heads_as_blocks(d, G):
+    """Caches of 513 to 1024 slots that one block reads whole."""
+    g = rng(315 + d)
+    lengths = [(331 * b) % 1025 for b in range(39)] + [1024]
+    c = filled(g, 40, 8, lengths, d, 1024)
+    check_attention(c, rows(g, 40, 8 * G, 1, d), "bf16")
+
+
 @pytest.mark.parametrize("N_q,length", [(4, 2), (4, 4), (4, 5), (8, 1), (3, 0), (4, 100), (2, 33), (4, 640)])
 @pytest.mark.parametrize("d", [64, 128])
 @CAPACITY
