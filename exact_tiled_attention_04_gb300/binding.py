@@ -60,6 +60,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load the CUDA library (once).  Raises if it was not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

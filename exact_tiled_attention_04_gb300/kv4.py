@@ -44,7 +44,7 @@ def _call(where: str, function, device, stream, made, *args):
         for t in made:
             t.record_stream(stream)
         current = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         status = function(*args, current or None)
     else:
         with torch.cuda.device(device):
@@ -54,9 +54,9 @@ def _call(where: str, function, device, stream, made, *args):
 
 
 def _check(t, what: str, dtype, shape, device):
-    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -67,10 +67,11 @@ def _rows(t, what: str, device) -> int:
     """Check 16-bit rows [batch, heads, rows, d]; their dtype code."""
     if t.dim() != 4:
         raise ValueError(f"{what} must be [batch, heads, rows, d], got {tuple(t.shape)}")
-    code = _b.FA_DTYPE_BF16 if t.dtype == torch.bfloat16 else _b.FA_DTYPE_F16 if t.dtype == torch.float16 else None
+    dtype = t.dtype
+    code = _b.FA_DTYPE_BF16 if dtype is torch.bfloat16 else _b.FA_DTYPE_F16 if dtype is torch.float16 else None
     if code is None:
-        raise TypeError(f"{what} must be bfloat16 or float16, got {t.dtype}")
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise TypeError(f"{what} must be bfloat16 or float16, got {dtype}")
+    if t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor on {device}")
     return code
 
@@ -102,6 +103,8 @@ class KV4Cache:
                                       (weight, "weight", torch.float32, (B, H_kv, capacity))):
             if t is not None:
                 _check(t, what, dtype, shape, dev)
+        if dev.type != "cuda":
+            raise ValueError(f"k_codes must be a contiguous CUDA tensor, is on {dev}")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.counts, self.pos, self.weight = counts, pos, weight
         self.B, self.H_kv, self.capacity, self.d, self.device = B, H_kv, capacity, d, dev
@@ -203,7 +206,7 @@ def kv4_attention(q, cache: KV4Cache, scale: float | None = None, causal: bool =
         raise ValueError(f"q must be [{cache.B}, a multiple of {cache.H_kv}, N_q, {cache.d}], got {tuple(q.shape)}")
     made = []
     if out is None:
-        made.append(out := torch.empty_like(q))
+        made.append(out := torch.empty((B, H, N_q, d), dtype=q.dtype, device=device))
     else:
         _check(out, "out", q.dtype, q.shape, device)
     if lse is not None:
@@ -279,6 +282,8 @@ def attention_weights(q, k, lse, scale: float | None = None, causal: bool = Fals
     columns of a cache's weight (same strides), and the same tensor."""
     _need_torch()
     device = q.device
+    if device.type != "cuda":
+        raise ValueError(f"q must be a contiguous CUDA tensor, is on {device}")
     code = _rows(q, "q", device)
     _rows(k, "k", device)
     if k.dtype != q.dtype:
