@@ -415,7 +415,8 @@ int fa_kv4_read(const fa_kv4_cache_t* cache, const int32_t* first, int64_t count
  *   N_q * H / H_kv <= 128 (decode steps and drafts; longer chunks read the
  *   rows back with fa_kv4_read and use fa_fwd_ex): else FA_ERR_UNSUPPORTED.
  *   workspace  : fa_kv4_fwd_workspace_size(...) bytes, 16-byte aligned;
- *                nothing in it needs to be zeroed.
+ *                nothing in it needs to be zeroed.  Calls (and replays of
+ *                captured ones) that may run at once need one each.
  * A row that sees no slot gets O = 0 and lse = -inf and adds no weight.
  * Lengths are read on the device (clamped to 0 .. capacity), so a captured
  * call follows them.  Results do not depend on the order in which blocks run.

@@ -194,7 +194,7 @@ def check_attention(c, q, dtype, causal=False, scale=None, weight=True):
     return out, lse, w_out
 
 
-# Caches of up to 1024 slots get a block per head, longer ones are cut into runs that blocks share:
+# Caches of up to 512 slots get a block per head, longer ones are cut into runs that blocks share:
 # both, whatever the lengths in them.
 CAPACITY = pytest.mark.parametrize("capacity", [None, 2048], ids=["short", "cut"])
 
