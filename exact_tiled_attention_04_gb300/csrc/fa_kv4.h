@@ -92,16 +92,19 @@ struct Kv4FwdParams {
     float scale_log2;
     int ctas;             // CTAs of the main kernel
     int single;           // 1: one per unit
+    int unit_cost;        // slabs counted for ending a unit
     // workspace
     float* row_lse2;      // [B * H_kv * rows]: base-2 lse of the rows of units that one CTA finished
     float4* part_ml;      // [ctas, 2, rows_per_block]: reference, exact sum, rounded sum
     float* part_o;        // [ctas, 2, rows_per_block, d]
     float* logits;        // [B * H_kv, capacity, rows] scaled, base 2, or nullptr
 };
+constexpr int kKv4UnitCost = 8;  // slabs that ending a unit costs
 int kv4_rows_per_block(int64_t rows);
 struct Kv4Plan {
-    int ctas;
-    bool single;
+    int ctas = 0;
+    bool single = false;
+    int unit_cost = 0;
 };
 Kv4Plan kv4_plan(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms);
 cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, cudaStream_t stream);

@@ -165,7 +165,7 @@ bool fwd_layout(int64_t B, int64_t H, int64_t H_kv, int64_t N_q, int64_t capacit
     const int64_t logits = mul(mul(B, H_kv), mul(capacity, rows * 4));
     const int64_t chunks = mul(B * H_kv, (capacity + 1023) / 1024);
     // the slabs of 32 slots over all blocks of 8 rows; the second kernel's grid: a warp per row, a block per 1024 slots
-    const int64_t slabs = mul(mul(B * H_kv, (rows + 7) / 8), capacity / 32);
+    const int64_t slabs = mul(mul(B * H_kv, (rows + 7) / 8), capacity / 32 + fa::kKv4UnitCost);
     if (slabs < 0 || slabs > kInt32Max / 2) return false;
     if (all < 0 || all > kInt32Max || logits < 0 || chunks < 0 || chunks > kInt32Max / 2) return false;
     l->plan = fa::kv4_plan(B, H_kv, rows, capacity, sms > 0 ? sms : 1024);
@@ -350,6 +350,7 @@ int fa_kv4_fwd(const fa_kv4_cache_t* cache, const void* q, void* o, float* lse, 
     p.scale_log2 = scale * kLog2e;
     p.ctas = l.plan.ctas;
     p.single = l.plan.single ? 1 : 0;
+    p.unit_cost = l.plan.unit_cost;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.row_lse2 = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float4*>(ws + l.part_ml);

@@ -23,7 +23,13 @@
 // Work split.  The slabs of all units (sequence, key/value head, block of
 // rows), in order, are cut into equal runs, one per CTA, from the lengths on
 // the device: no CTA idles because a sequence is short, and a long one is
-// shared by many.  A CTA whose run holds a whole unit writes its output; of
+// shared by many.  A run that ends one unit and begins another takes about as
+// long as one of a group more, so a unit counts a group more than it has;
+// where a CTA gets two groups or fewer of a full cache it does not, as runs
+// then often end with their unit.  (Counted against not, at d = 128: N = 2048
+// B = 8 10.8 / 9.8 us; N = 2560 11.6 / 13.3; N = 4096 B = 5 11.8 / 13.3, B = 8,
+// where every unit is cut into four equal runs, 13.4 / 13.4; N = 16384 33.7 /
+// 34.9; 16 sequences of up to 8192 with weights 26.0 / 28.1.)  A CTA whose run holds a whole unit writes its output; of
 // a unit cut between CTAs each leaves a partial result (at most two per CTA:
 // the unit it starts inside and the one it ends inside), which the second
 // kernel adds up in order, so results do not depend on timing.  (The last CTA
@@ -39,11 +45,11 @@
 // 512 slots B = 1 5.5 / 6.3, B = 8 5.5 / 6.5, B = 256 45.8 / 45.5; 1024 slots
 // B = 1 7.6 / 6.4, B = 8 8.2 / 8.0, B = 24 12.0 / 14.7, B = 256 68.6 / 69.9.
 //
-// What is left (B = 8, H = 32/8, d = 128): 16384 slots take 34.9 us, 65536
-// 102.8 (5.9 TB/s); 49152 more cost what reading them does, so 12 us do not
+// What is left (B = 8, H = 32/8, d = 128): 16384 slots take 33.7 us, 65536
+// 103.5 (5.8 TB/s); 49152 more cost what reading them does, so 11 us do not
 // depend on the length: 1.5 from the wait to the first copy, 1.7 until it is
-// there, up to 8 between the first and the last block's end (equal runs, but
-// an SM's share of the bandwidth is not), 1.7 for the second kernel.
+// there, up to 7 between the first and the last block's end, 1.7 for the
+// second kernel.
 //
 // Every wait is bounded as in the forward kernel; a warp that gives up skips
 // its remaining slabs but still reaches the block's barriers.
@@ -100,31 +106,35 @@ __device__ __forceinline__ int kv4_length(const Kv4Cache& c, int b) {
     return min(max(c.counts[b], 0), c.capacity);
 }
 __device__ __forceinline__ int slabs_of(int len) { return (len + kSlab - 1) / kSlab; }
+// What a unit counts for in the runs: its slabs and `cost`, the slabs' worth
+// of ending it.
+__device__ __forceinline__ int share_of(int slabs, int cost) { return slabs > 0 ? slabs + cost : 0; }
 
-// The slabs of all units fit 31 bits (the host checks it), so positions in
+// The shares of all units fit 31 bits (the host checks it), so positions in
 // them are ints.
 //
-// Slabs per CTA: equal runs of whole groups.
+// Share per CTA: equal runs of whole groups.
 __device__ __forceinline__ int slabs_per_cta(int total, int ctas) {
     return max(1, (total + ctas * kWarps - 1) / (ctas * kWarps)) * kWarps;
 }
 
-// Position in a CTA's run of slabs.
+// Position in a CTA's run.
 struct Cursor {
-    int pos, end;       // in slabs over all units
-    int base;           // first slab of sequence b
+    int pos, end;       // in shares over all units
+    int base;           // where sequence b begins
+    int cost;
     int b, len, slabs;  // sequence, its length and the slabs of one of its units
     int unit;           // unit of sequence b
     int s0, s1;         // slabs of that unit in this run
 
     __device__ __forceinline__ bool valid() const { return pos < end; }
     __device__ __forceinline__ void next(const Kv4Cache& c, int units) {
-        pos = s1 > s0 ? pos + (s1 - s0) : end;
+        pos = slabs > 0 && s1 == slabs ? min(end, pos + share_of(slabs, cost) - s0) : end;
         if (pos >= end) return;
         s0 = 0;
         if (++unit == units) {  // the next sequence that has any slab
             unit = 0;
-            base += slabs * units;
+            base += share_of(slabs, cost) * units;
             do {
                 len = kv4_length(c, ++b);
                 slabs = slabs_of(len);
@@ -141,12 +151,14 @@ struct Cursor {
         pos = base = s0 = 0;
         s1 = slabs;
         end = max(slabs, 1);
+        cost = 0;
     }
-    __device__ __forceinline__ void start(const Kv4Cache& c, int units, int ctas, int cta) {
+    __device__ __forceinline__ void start(const Kv4Cache& c, int units, int ctas, int cta, int unit_cost) {
+        cost = unit_cost;
         const int lane = threadIdx.x % 32;
         const int len0 = lane < c.B ? kv4_length(c, lane) : 0;  // the first 32 sequences: all, mostly
-        int total = slabs_of(len0) * units;
-        for (int x = 32 + lane; x < c.B; x += 32) total += slabs_of(kv4_length(c, x)) * units;
+        int total = share_of(slabs_of(len0), cost) * units;
+        for (int x = 32 + lane; x < c.B; x += 32) total += share_of(slabs_of(kv4_length(c, x)), cost) * units;
         total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total)));
         const int per = slabs_per_cta(total, ctas);
         pos = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(per) * cta));
@@ -155,7 +167,7 @@ struct Cursor {
         // the sequence that holds `pos`, 32 sequences at a time
         for (int b0 = 0; pos < end && b0 < c.B; b0 += 32) {
             const int mine = b0 == 0 ? len0 : b0 + lane < c.B ? kv4_length(c, b0 + lane) : 0;
-            const int n = slabs_of(mine) * units;
+            const int n = share_of(slabs_of(mine), cost) * units;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -174,9 +186,11 @@ struct Cursor {
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (pos < end) {
-            unit = (pos - base) / slabs;
-            s0 = pos - base - unit * slabs;
+            const int share = share_of(slabs, cost);
+            unit = (pos - base) / share;
+            s0 = pos - base - unit * share;
             s1 = min(slabs, s0 + (end - pos));
+            if (s0 >= slabs) next(c, units);  // the run starts behind the unit's last slab
         }
     }
 };
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
     if (p.single)
         cur.start_single(p.c, units, static_cast<int>(blockIdx.x));
     else
-        cur.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x));
+        cur.start(p.c, units, p.ctas, static_cast<int>(blockIdx.x), p.unit_cost);
 
     // A unit's slabs go in groups of one per warp; stage i % kStages of the ring holds group i.
     if (warp == kLoadWarp) {
@@ -359,15 +373,15 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
 struct Parts {
     int slabs, first, last;
 };
-// Slabs of the sequences before b, and of all, by a warp (every lane gets them).
+// Where sequence b begins, its slabs, a CTA's share, by a warp (every lane gets them).
 struct Spread {
-    int before, slabs, per;
+    int before, slabs, per, cost;
 };
 __device__ __forceinline__ Spread spread_of(const Kv4FwdParams& p, int b) {
     const int lane = threadIdx.x % 32, units = p.c.H_kv * p.row_blocks;
     int before = 0, total = 0;
     for (int x = lane; x < p.c.B; x += 32) {
-        const int n = slabs_of(kv4_length(p.c, x)) * units;
+        const int n = share_of(slabs_of(kv4_length(p.c, x)), p.unit_cost) * units;
         total += n;
         if (x < b) before += n;
     }
@@ -375,12 +389,13 @@ __device__ __forceinline__ Spread spread_of(const Kv4FwdParams& p, int b) {
     s.before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
     s.per = slabs_per_cta(static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total))), p.ctas);
     s.slabs = slabs_of(kv4_length(p.c, b));
+    s.cost = p.unit_cost;
     return s;
 }
 __device__ __forceinline__ Parts parts_of(const Spread& s, int unit) {
     Parts r;
     r.slabs = s.slabs;
-    const int hs = s.before + unit * s.slabs;
+    const int hs = s.before + unit * share_of(s.slabs, s.cost);
     r.first = hs / s.per;
     r.last = s.slabs > 0 ? (hs + s.slabs - 1) / s.per : r.first;
     return r;
@@ -583,6 +598,7 @@ Kv4Plan kv4_plan(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sm
         const int64_t most = static_cast<int64_t>(sms) * (rpb <= 8 ? 2 : 1);
         const int64_t want = (units * (capacity / kSlab) + kWarps - 1) / kWarps;
         plan.ctas = static_cast<int>(want < most ? want : most);
+        plan.unit_cost = want > 2 * most ? kKv4UnitCost : 0;
     }
     return plan;
 }

@@ -238,6 +238,16 @@ def test_as_many_heads_as_blocks(d, G):
     check_attention(c, rows(g, 40, 8 * G, 1, d), "bf16")
 
 
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 4), (128, 8), (128, 16)])
+def test_runs_that_count_the_ends_of_heads(d, G):
+    """More than two groups of slots per block: runs begin and end anywhere, behind a head's last slot, too."""
+    g = rng(317 + d + G)
+    c = filled(g, 6, 8, [6000, 1, 0, 4097, 33, 5999], d)
+    check_attention(c, rows(g, 6, 8 * G, 1, d), "bf16")
+    c = filled(g, 1, 1, [300], d, 200000)  # short, in a long cache
+    check_attention(c, rows(g, 1, G, 1, d), "bf16")
+
+
 @pytest.mark.parametrize("N_q,length", [(4, 2), (4, 4), (4, 5), (8, 1), (3, 0), (4, 100), (2, 33), (4, 640)])
 @pytest.mark.parametrize("d", [64, 128])
 @CAPACITY
