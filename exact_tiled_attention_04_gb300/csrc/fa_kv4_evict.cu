@@ -92,7 +92,7 @@ __device__ __forceinline__ uint32_t rank_key(float w, bool first) {
     if (first) return 0xFFFFFFFFu;
     if (w != w) return 0xFFFFFFFEu;
     const uint32_t u = __float_as_uint(w + 0.0f);
-    return (u >> 31) ? ~u : (u | 0x80000000u);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
 // Entries to .. to + 31 of a head (rows `row` of the targets): lane i's entry
@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
     const int size = min(slice, n - begin);  // this CTA's keys
 
     if (n > nn) {
-        const long long newest = static_cast<long long>(seen) - p.recent;
+        // positions are ints: one below the smallest protects nothing more
+        const int newest = static_cast<int>(max(static_cast<long long>(seen) - p.recent, -2147483648ll));
         auto key_of = [&](float w, int at) -> uint32_t {
             return rank_key(w, protect && (at < p.sinks || at >= newest));
         };
