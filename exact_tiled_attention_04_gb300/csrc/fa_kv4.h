@@ -93,6 +93,7 @@ struct Kv4FwdParams {
     int ctas;             // CTAs of the main kernel
     int single;           // 1: one per unit
     int unit_cost;        // slabs counted for ending a unit
+    int join_warps;       // of the second kernel, per row: one or a block
     // workspace
     float* row_lse2;      // [B * H_kv * rows]: base-2 lse of the rows of units that one CTA finished
     float4* part_ml;      // [ctas, 2, rows_per_block]: reference, exact sum, rounded sum
@@ -105,6 +106,7 @@ struct Kv4Plan {
     int ctas = 0;
     bool single = false;
     int unit_cost = 0;
+    int join_warps = 1;
 };
 Kv4Plan kv4_plan(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sms);
 cudaError_t launch_kv4_fwd(const Kv4FwdParams& p, cudaStream_t stream);

@@ -351,6 +351,7 @@ int fa_kv4_fwd(const fa_kv4_cache_t* cache, const void* q, void* o, float* lse, 
     p.ctas = l.plan.ctas;
     p.single = l.plan.single ? 1 : 0;
     p.unit_cost = l.plan.unit_cost;
+    p.join_warps = l.plan.join_warps;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.row_lse2 = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float4*>(ws + l.part_ml);

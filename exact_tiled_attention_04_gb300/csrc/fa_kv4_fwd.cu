@@ -434,10 +434,13 @@ constexpr int kJoinKeys = 1024;  // keys per block of the weights' part
 constexpr int kMaxRows = 128;
 constexpr int kAhead = 8;  // parts' rows loaded ahead of the factors
 
-// Blocks 0 .. join_blocks - 1: one warp per output row whose unit several
-// CTAs shared (or that has no slot at all).  The others: accumulated weight,
+// Blocks 0 .. join_blocks - 1: the output rows whose unit several CTAs shared
+// (or that has no slot at all), p.join_warps warps a row: one, or the whole
+// block where a row has 2 kAhead parts or more.  A warp against a block, in us:
+// d = 128, H = 32/8, 16384 slots, B = 1 (38 parts) 14.5 / 10.1, B = 2 (19)
+// 16.1 / 15.7; 8192 slots, B = 4 (10) 14.4 / 15.7.  The others: accumulated weight,
 // kJoinKeys slots of one key/value head each.
-template <int D>
+template <int D, int kWays>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdParams p, int rows_per_block,
                                                                  int join_blocks) {
     // started while the main kernel's last CTAs run: what that kernel does not
@@ -445,7 +448,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
     grid_release();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (static_cast<int>(blockIdx.x) < join_blocks) {
-        const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + warp;
+        const int way = warp % kWays;  // this warp adds parts way, way + kWays, ..
+        const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32 / kWays) + warp / kWays;
         if (row >= static_cast<long long>(p.c.B) * p.c.H_kv * p.rows) {
             grid_wait();
             return;
@@ -467,38 +471,50 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
                 for (int j = 0; j < kPer; j += 2)
                     *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(src + j);
             };
-            // the first parts' rows are on their way while the factors are formed
+            // the first parts' rows are on their way while the factors are formed, one per lane
+            const auto reference = [&](int i) {
+                return i < parts ? p.part_ml[part_row(u.first + i, u.first, rows_per_block, rb)].x : -INFINITY;
+            };
+            const auto factor = [&](int i, float x) { return i >= parts ? 0.0f : M == -INFINITY ? 1.0f : ex2(x - M); };
+            const float x = kWays > 1 ? reference(way + kWays * lane) : 0.0f;
             float ahead[kAhead][kPer], f;
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (i < parts) load(i, ahead[i]);
+            for (int k = 0; k < kAhead; ++k)
+                if (way + kWays * k < parts) load(way + kWays * k, ahead[k]);
             row_sums(p, u, rows_per_block, rb, M, L, LQ, f);
+            if constexpr (kWays > 1) f = factor(way + kWays * lane, x);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const float w = __shfl_sync(0xffffffffu, f, i);
-                if (i < parts)
+            for (int k = 0; k < kAhead; ++k) {
+                const float w = __shfl_sync(0xffffffffu, f, k);
+                if (way + kWays * k < parts)
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) acc[j] += w * ahead[i][j];
+                    for (int j = 0; j < kPer; ++j) acc[j] += w * ahead[k][j];
             }
-            // the others: 32 parts' factors at a time, one per lane; four parts' rows in flight
-            for (int i0 = kAhead; i0 < parts; i0 = (i0 / 32 + 1) * 32) {
-                if (i0 >= 32) {
-                    const int mine = u.first + i0 + lane;
-                    f = 0.0f;
-                    if (mine <= u.last)
-                        f = M == -INFINITY ? 1.0f
-                                           : ex2(p.part_ml[part_row(mine, u.first, rows_per_block, rb)].x - M);
-                }
-                const int n = min((i0 / 32 + 1) * 32, parts);
+            // the others: 32 factors at a time; four parts' rows in flight
+            const int mine = (parts - way + kWays - 1) / kWays;
+            for (int k0 = kAhead; k0 < mine; k0 = (k0 / 32 + 1) * 32) {
+                if (k0 >= 32) f = factor(way + kWays * (k0 + lane), reference(way + kWays * (k0 + lane)));
+                const int n = min((k0 / 32 + 1) * 32, mine);
 #pragma unroll 4
-                for (int i = i0; i < n; ++i) {
-                    const float w = __shfl_sync(0xffffffffu, f, i % 32);
+                for (int k = k0; k < n; ++k) {
+                    const float w = __shfl_sync(0xffffffffu, f, k % 32);
                     float v[kPer];
-                    load(i, v);
+                    load(way + kWays * k, v);
 #pragma unroll
                     for (int j = 0; j < kPer; ++j) acc[j] += w * v[j];
                 }
             }
+        }
+        if constexpr (kWays > 1) {  // a block per row: every warp is here
+            __shared__ float sums[kJoinThreads / 32][D];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) sums[warp][lane * kPer + j] = acc[j];
+            __syncthreads();
+            if (warp > 0) return;
+#pragma unroll
+            for (int w = 1; w < kJoinThreads / 32; ++w)
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) acc[j] += sums[w][lane * kPer + j];
         }
         const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
         uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + lane * kPer);
@@ -574,13 +590,14 @@ cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
     e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), kThreads4, C::kSmemBytes, stream, p);
     if (e != cudaSuccess) return e;
     const long long rows = p.single ? 0 : static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
-    const int join = static_cast<int>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+    const int per_block = kJoinThreads / 32 / p.join_warps;
+    const int join = static_cast<int>((rows + per_block - 1) / per_block);
     if (p.single && p.logits == nullptr) return cudaSuccess;
     const long long keys = p.logits == nullptr ? 0
                                                : static_cast<long long>(p.c.B) * p.c.H_kv *
                                                      ((p.c.capacity + kJoinKeys - 1) / kJoinKeys);
-    return launch_dependent(kv4_join_kernel<D>, dim3(static_cast<unsigned>(join + keys)), kJoinThreads, 0, stream, p,
-                            C::kRows, join);
+    auto second = p.join_warps > 1 ? kv4_join_kernel<D, kJoinThreads / 32> : kv4_join_kernel<D, 1>;
+    return launch_dependent(second, dim3(static_cast<unsigned>(join + keys)), kJoinThreads, 0, stream, p, C::kRows, join);
 }
 
 }  // namespace
@@ -599,6 +616,7 @@ Kv4Plan kv4_plan(int64_t B, int64_t H_kv, int64_t rows, int64_t capacity, int sm
         const int64_t want = (units * (capacity / kSlab) + kWarps - 1) / kWarps;
         plan.ctas = static_cast<int>(want < most ? want : most);
         plan.unit_cost = want > 2 * most ? kKv4UnitCost : 0;
+        if (plan.ctas >= 2 * kAhead * units) plan.join_warps = kJoinThreads / 32;
     }
     return plan;
 }

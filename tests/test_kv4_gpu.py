@@ -248,6 +248,14 @@ def test_runs_that_count_the_ends_of_heads(d, G):
     check_attention(c, rows(g, 1, G, 1, d), "bf16")
 
 
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 3), (128, 16)])
+@pytest.mark.parametrize("n", [5000, 20000, 77000])  # 20, 79 and 301 parts of each row at four rows a head
+def test_rows_of_many_parts(d, G, n):
+    g = rng(319 + d + G)
+    c = filled(g, 1, 1, [n], d)
+    check_attention(c, rows(g, 1, G, 1, d), "bf16")
+
+
 @pytest.mark.parametrize("N_q,length", [(4, 2), (4, 4), (4, 5), (8, 1), (3, 0), (4, 100), (2, 33), (4, 640)])
 @pytest.mark.parametrize("d", [64, 128])
 @CAPACITY
