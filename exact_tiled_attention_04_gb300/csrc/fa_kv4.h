@@ -2,6 +2,7 @@
 // (fa_kv4_api.cu) and its kernels.  Not part of the public C ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -28,6 +29,19 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // Lets the next kernel of the stream be set up.
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 #endif
+// Lets a kernel have `smem` bytes of dynamic shared memory, once per device
+// (`done`: a bit per device, the kernel's own).
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, int smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 template <class Kernel, class... Args>
 cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchAttribute attr[1];

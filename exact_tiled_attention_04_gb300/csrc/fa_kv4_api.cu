@@ -96,13 +96,17 @@ int check_dtype16(int dtype) {
 }
 
 int sm_count() {
+    static std::atomic<int> counts[64];  // 0: not asked yet
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return 0;
+    if (cudaGetDevice(&dev) == cudaSuccess) {
+        if (dev < 64 && (n = counts[dev].load(std::memory_order_relaxed)) > 0) return n;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) {
+            if (dev < 64) counts[dev].store(n, std::memory_order_relaxed);
+            return n;
+        }
     }
-    return n;
+    cudaGetLastError();
+    return 0;
 }
 
 int launched(cudaError_t e, const char* what) {

@@ -585,7 +585,8 @@ template <int D, int R>
 cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
     using C = Kv4Cfg<D, R>;
     auto kern = kv4_fwd_kernel<D, R>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(kern, C::kSmemBytes, allowed);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), kThreads4, C::kSmemBytes, stream, p);
     if (e != cudaSuccess) return e;
