@@ -29,15 +29,17 @@
 // then often end with their unit.  (Counted against not, at d = 128: N = 2048
 // B = 8 10.8 / 9.8 us; N = 2560 11.6 / 13.3; N = 4096 B = 5 11.8 / 13.3, B = 8,
 // where every unit is cut into four equal runs, 13.4 / 13.4; N = 16384 33.7 /
-// 34.9; 16 sequences of up to 8192 with weights 26.0 / 28.1.)  A CTA whose run holds a whole unit writes its output; of
-// a unit cut between CTAs each leaves a partial result (at most two per CTA:
-// the unit it starts inside and the one it ends inside), which the second
-// kernel adds up in order, so results do not depend on timing.  (The last CTA
-// to arrive adding them up, counted by an atomic, took longer: 44.3 against
-// 40.6 us at B = 8, H = 32/8, 16384 slots, d = 128, and 69 against 54 us for
-// one sequence of 131071.)  The second kernel also forms the accumulated
-// weights from the scores, which the first leaves in the workspace (4 bytes a
-// score, against the 68 of reading a key again at d = 128).
+// 34.9; 16 sequences of up to 8192 with weights 26.0 / 28.1.)
+//
+// A CTA whose run holds a whole unit writes its output; of a unit cut between
+// CTAs each leaves a partial result (at most two per CTA: the unit it starts
+// inside and the one it ends inside), which the second kernel adds up in
+// order, so results do not depend on timing.  (The last CTA to arrive adding
+// them up, counted by an atomic, took longer: 44.3 against 40.6 us at B = 8,
+// H = 32/8, 16384 slots, d = 128, and 69 against 54 us for one sequence of
+// 131071.)  The second kernel also forms the accumulated weights from the
+// scores, which the first leaves in the workspace (4 bytes a score, against
+// the 72 of reading a key again at d = 128).
 //
 // A cache of at most kWholeSlots slots, or twice that where there are as many
 // units as SMs, is not cut: a CTA per unit, and no second kernel unless

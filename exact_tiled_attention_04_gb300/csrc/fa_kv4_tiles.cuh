@@ -19,7 +19,9 @@
 // neighbours in the A operand as they are; the result's columns are (row,
 // parity) and P^T has zeros where the parities differ.  It takes as many
 // products as Wide, but no interleaving, half the exponentials (each row's
-// scores are spread over all lanes) and half the accumulators.
+// scores are spread over all lanes) and half the accumulators.  4 rows by
+// Paired instead of Wide<D, 8>: 36.3 against 39.7 us at B = 8, H = 32/8, 16384
+// slots, d = 128; 29.5 against 33.9 for 16 ragged sequences with weights.
 #pragma once
 
 #include <cmath>
