@@ -749,3 +749,39 @@ def test_prompt_into_cache_behind_the_forward_pass():
         want = want or got
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+
+
+def test_serving_loops_at_once():
+    """Loops on three streams, with the prompt's kernels between them, equal the same loops one after another."""
+    g = rng(740)
+    H, H_kv, d, steps, N = 8, 2, 64, 12, 1300
+    sizes = [(3, [1500, 20, 700], 1499), (1, [9000], 8900), (8, [600, 0, 31, 512, 511, 64, 1, 600], 600)]
+    token = [tuple(torch.stack([rows(g, B, h, 1, d) for _ in range(steps)]) for h in (H, H_kv, H_kv)) for B, _, _ in sizes]
+    pq, pk, pv = (rows(g, 1, h, N, d) for h in (H, H_kv, H_kv))
+
+    def caches():
+        return [filled(rng(741 + i), B, H_kv, lengths, d, max(lengths) + steps) for i, (B, lengths, _) in enumerate(sizes)]
+
+    def loop(c, size, t):
+        _, lse = fa.attention(pq, pk, pv, causal=True)
+        w = fa.attention_weights(pq, pk, lse, causal=True)
+        return [*serve(c, steps, size[2], *t), w, lse]
+
+    want = caches()
+    outs = [[x.clone() for x in loop(c, s, t)] for c, s, t in zip(want, sizes, token)]
+    for _ in range(3):
+        got = caches()
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in sizes]
+        res = []
+        for c, s, t, stream in zip(got, sizes, token, streams):
+            with torch.cuda.stream(stream):
+                res.append(loop(c, s, t))
+        torch.cuda.synchronize()
+        for a, b in zip(outs, res):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+        for x, y in zip(want, got):
+            assert torch.equal(x.counts, y.counts)
+            for name in ARRAYS:
+                for b, n in enumerate(x.lengths.tolist()):
+                    assert torch.equal(bits(x, name)[b, :, :n], bits(y, name)[b, :, :n]), name
