@@ -356,11 +356,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                 const int bin = threadIdx.x / 4;
                 uint32_t sum = 0u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t& h = sh.hist[bin * 32 + ((threadIdx.x % 4 * 8 + i + bin) & 31)];
-                    sum += h;
-                    h = 0u;
-                }
+                for (int i = 0; i < 8; ++i) sum += sh.hist[bin * 32 + ((threadIdx.x % 4 * 8 + i + bin) & 31)];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 if (threadIdx.x % 4 == 0) sh.bins[bin] = sum;
@@ -407,11 +403,11 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                     // and at least that many greater or equal, equal the threshold
 #pragma unroll 4
                     for (int i = 4 * threadIdx.x; i < size; i += 4 * kEvThreads) {
-                        const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
-                        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (i + j < size && (k[j] >> down) == prefix) sh.list[atomicAdd(&sh.listed, 1u)] = k[j];
+                        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+                        uint32_t match = ((k.x >> down) == prefix ? 1u : 0u) | ((k.y >> down) == prefix ? 2u : 0u) |
+                                         ((k.z >> down) == prefix ? 4u : 0u) | ((k.w >> down) == prefix ? 8u : 0u);
+                        for (match &= low_bits(size - i); match != 0u; match &= match - 1u)  // few have any
+                            sh.list[atomicAdd(&sh.listed, 1u)] = keys[i + __ffs(static_cast<int>(match)) - 1];
                     }
                     __syncthreads();
                     // four threads per entry
@@ -438,6 +434,11 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                     want -= sh.pick[1];
                     open = sh.pick[2];
                     break;
+                }
+                if (down > 0) {  // the histogram is read
+                    for (int i = threadIdx.x; i < 256 * 8; i += kEvThreads)
+                        reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+                    __syncthreads();
                 }
             }
             // 2. a bit per entry: a word of 32 entries per thread (two in the longest slices), its eight
