@@ -29,7 +29,7 @@
 // Short rows are bound by the latency of these steps (4097 slots to 4096, 64
 // heads, d = 64: 4.8 us); long ones by the selection, on an SM per head, and
 // then by reading scattered rows (up to 16384 slots to 2048, 64 heads,
-// d = 128: 25.2 us, of them 11 for the sources and 10.5 for the 40 MB copied,
+// d = 128: 24.7 us, of them 11 for the sources and 10.5 for the 40 MB copied,
 // whose 4-byte and 8-byte parts cost a 32-byte sector each).
 #include <cstddef>
 #include <cstdint>
