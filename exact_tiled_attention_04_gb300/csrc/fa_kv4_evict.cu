@@ -24,10 +24,14 @@
 //      place no copy reads what another writes.
 // A decode step that puts one entry too many into the cache needs no
 // threshold: up to kEvFew leaving entries of a head that one block holds are
-// found one by one as block-wide minima.
+// found one by one, by a warp with the least entry of every 32nd of the head in
+// a lane.  One by one against by a threshold, in us for 64 heads, d = 64: 1 entry
+// of 1025 3.1 / 7.7, of 4097 4.1 / 10.8, of 16385 5.7 / 19.0; 4 more than 4096
+// 5.1 / 10.8; 16 more than 4096 10.3 / 10.8, than 16384 18.0 / 19.0, than 40000
+// 32.7 / 34.3.
 //
 // Short rows are bound by the latency of these steps (4097 slots to 4096, 64
-// heads, d = 64: 4.8 us); long ones by the selection, on an SM per head, and
+// heads, d = 64: 4.5 us); long ones by the selection, on an SM per head, and
 // then by reading scattered rows (up to 16384 slots to 2048, 64 heads,
 // d = 128: 24.7 us, of them 11 for the sources and 10.5 for the 40 MB copied,
 // whose 4-byte and 8-byte parts cost a 32-byte sector each).
@@ -46,7 +50,7 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvMaxCluster = 8;
 constexpr int kEvMaxSlice = kKv4EvictMaxCapacity / kEvMaxCluster;  // keys per CTA
 
-constexpr int kEvFew = 8;
+constexpr int kEvFew = 16;
 constexpr uint32_t kEvList = 256;  // open entries that are compared with one another
 constexpr int kEvMaxWords = (kEvMaxSlice + 31) / 32;
 
@@ -59,7 +63,7 @@ struct alignas(16) EvShared {  // the keys behind it are read 16 bytes at a time
             uint32_t before[kEvMaxWords]; // holes (low half) and late entries (high half) of earlier words
         };
         struct {                  // few leaving entries
-            uint2 least[2][kEvWarps];  // a warp's least key and the highest slot that has it
+            uint2 least[kEvWarps];  // a warp's least key and the highest slot that has it
             int leaving[kEvFew], hole[kEvFew], late[kEvFew];
         };
     };
@@ -288,31 +292,54 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
         if (few) {
             load_keys(std::integral_constant<int, 1>{}, std::false_type{});
             __syncthreads();
-            // the entries in the order they leave: ascending key, descending slot
-            uint32_t last_key = 0u;
-            int last_slot = 0x7FFFFFFF;
-            for (int r = 0; r < n - nn; ++r) {
-                uint32_t key = 0xFFFFFFFFu;
-                int slot = -1;
-                for (int i = threadIdx.x; i < n; i += kEvThreads) {
-                    const uint32_t k = keys[i];
-                    if ((k > last_key || (k == last_key && i < last_slot)) && (k < key || (k == key && i > slot))) {
-                        key = k;
-                        slot = i;
+            // the entries in the order they leave: ascending key, descending slot.  Every warp finds the first of its
+            // own (slots 128 warp + 4096 i + 0 .. 127); then one warp, with a candidate per lane, takes the first of
+            // all and looks for the next one among the entries it came from, while the others begin the list
+            const int e = n - nn;
+            const auto earlier = [](uint32_t k, int i, uint32_t key, int slot) {
+                return k < key || (k == key && i > slot);
+            };
+            // the first entry of `share` behind (key, slot), over the warp
+            const auto first_of = [&](int share, uint32_t& key, int& slot) {
+                uint32_t first = 0xFFFFFFFFu;
+                int where = -1;
+                for (int i = 128 * share + 4 * lane; i < n; i += 4 * kEvThreads) {
+                    const uint4 k4 = *reinterpret_cast<const uint4*>(keys + i);
+                    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (i + j < n && earlier(key, slot, k[j], i + j) && earlier(k[j], i + j, first, where)) {
+                            first = k[j];
+                            where = i + j;
+                        }
+                }
+                key = __reduce_min_sync(0xffffffffu, first);
+                slot = __reduce_max_sync(0xffffffffu, first == key ? where : -1);
+            };
+            uint32_t key = 0u;  // no entry's
+            int slot = -1;
+            first_of(warp, key, slot);
+            if (lane == 0) sh.least[warp] = make_uint2(key, static_cast<uint32_t>(slot));
+            __syncthreads();
+            if (warp > 0)
+                for (int i = threadIdx.x - 32; i < nn; i += kEvThreads - 32) src[i] = i;
+            if (warp == 0) {
+                const uint2 w = sh.least[lane];
+                key = w.x;
+                slot = static_cast<int>(w.y);
+                for (int r = 0;; ++r) {
+                    uint32_t least = __reduce_min_sync(0xffffffffu, key);
+                    int out = __reduce_max_sync(0xffffffffu, key == least ? slot : -1);
+                    if (lane == 0) sh.leaving[r] = out;
+                    if (r + 1 == e) break;
+                    const int share = out / 128 % kEvWarps;
+                    first_of(share, least, out);
+                    if (lane == share) {
+                        key = least;
+                        slot = out;
                     }
                 }
-                uint32_t least = __reduce_min_sync(0xffffffffu, key);
-                slot = __reduce_max_sync(0xffffffffu, key == least ? slot : -1);
-                if (lane == 0) sh.least[r & 1][warp] = make_uint2(least, static_cast<uint32_t>(slot));
-                __syncthreads();
-                const uint2 w = sh.least[r & 1][lane];
-                last_key = __reduce_min_sync(0xffffffffu, w.x);
-                last_slot = __reduce_max_sync(0xffffffffu, w.x == last_key ? static_cast<int>(w.y) : -1);
-                if (threadIdx.x == 0) sh.leaving[r] = last_slot;
-            }
-            __syncthreads();
-            const int e = n - nn;
-            if (warp == 0) {
+                __syncwarp();
                 const int gone = lane < e ? sh.leaving[lane] : -1, end = nn + lane;
                 int hole_rank = 0, late_rank = 0;
                 bool leaves = false;
@@ -326,7 +353,6 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
                 if (lane < e && !leaves) sh.late[lane - late_rank] = end;
             }
             const int holes = __syncthreads_count(static_cast<int>(threadIdx.x) < e && sh.leaving[threadIdx.x] < nn);
-            for (int i = threadIdx.x; i < nn; i += kEvThreads) src[i] = i;
             if (in_place && warp < holes) copy_entry<D>(p.from, row0 + sh.late[warp], row0 + sh.hole[warp]);
             __syncthreads();
             if (static_cast<int>(threadIdx.x) < holes) src[sh.hole[threadIdx.x]] = sh.late[threadIdx.x];

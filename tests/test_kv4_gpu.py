@@ -538,6 +538,19 @@ def test_evict_into_another_cache(d, length, keep):
     check_evict(c, keep, 4, min(16, keep), out=to)
 
 
+@pytest.mark.parametrize("length", [17, 300, 4100, 40010])
+@pytest.mark.parametrize("e", [1, 2, 5, 15, 16, 17])
+def test_evict_a_few(length, e):
+    """As many as are found one by one, and one more; mostly ties; with protected ones among the last."""
+    if e >= length:
+        return
+    g = rng(625 + length + e)
+    c = filled(g, 1, 3, [length], 64)
+    c.weight[0, 1].copy_(torch.randint(0, 2, c.weight[0, 1].shape, generator=g, device="cuda").float())
+    c.weight[0, 2].zero_()
+    check_evict(c, length - e, 3, min(4, length - e))
+
+
 def test_evict_ties_and_odd_weights():
     """Ties by slot, signed zeros equal, infinities and NaN in order, over several warps' shares."""
     g = rng(630)
