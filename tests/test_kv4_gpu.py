@@ -798,3 +798,28 @@ def test_serving_loops_at_once():
             for name in ARRAYS:
                 for b, n in enumerate(x.lengths.tolist()):
                     assert torch.equal(bits(x, name)[b, :, :n], bits(y, name)[b, :, :n]), name
+
+
+def test_lengths_advanced_just_before_the_call():
+    """Appends whose blocks read the lengths on every SM and whose second kernel advances them, each
+    followed at once by attention with weights: the same as with a wait after every call."""
+    g = rng(750)
+    H, H_kv, d, n, steps = 32, 8, 128, 600, 3
+    k, v, q = (rows(g, 1, h, x, d) for h, x in ((H_kv, n), (H_kv, n), (H, 1)))
+    c = fa.KV4Cache.empty(1, H_kv, steps * n + 100, d)
+
+    def run(wait):
+        c.counts.zero_()
+        got = []
+        for i in range(1, steps + 1):
+            fa.kv4_append(c, k, v)
+            wait()
+            got += fa.kv4_attention(q, c, weight_out=c.weight)
+            wait()
+            got.append(c.weight[:, :, :i * n].clone())  # behind the length: what earlier rounds left
+        return got
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(20):
+        for a, b in zip(want, run(lambda: None)):
+            assert torch.equal(a, b)
