@@ -3,6 +3,8 @@ storing and reading back, attention (row counts, head layouts, lengths from
 none to many, masks, NaN behind the mask), accumulated weights of decode steps
 and of prompts, eviction in place and into another cache, and the calls
 together as a serving loop makes them, eager and captured."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -823,3 +825,29 @@ def test_lengths_advanced_just_before_the_call():
     for _ in range(20):
         for a, b in zip(want, run(lambda: None)):
             assert torch.equal(a, b)
+
+
+def test_evictions_of_several_host_threads():
+    """Threads that evict from caches of different sizes: none changes what the others may launch."""
+    sizes = (128, 40960) * 4
+    barrier = threading.Barrier(len(sizes))
+    status = []
+
+    def loop(capacity):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            c = filled(rng(760), 1, 2, [capacity], 64)
+            src = torch.empty(1, 2, capacity - 1, dtype=torch.int32, device="cuda")
+            counts = torch.empty_like(c.counts)
+        stream.synchronize()
+        call = (c._struct, capacity - 1, 0, 0, None, None, src.data_ptr(), counts.data_ptr(), stream.cuda_stream)
+        barrier.wait()
+        status.extend(fa.fa_kv4_evict(*call) for _ in range(2000))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=loop, args=(n,)) for n in sizes]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert status == [fa.FA_OK] * (2000 * len(sizes))
