@@ -319,6 +319,19 @@ def fa_version() -> int:
 
 
 # ------------------------------------------------------- PyTorch convenience
+def _empty_on(stream, shape, dtype, device, returned: bool = True):
+    """An uninitialised tensor for a call on `stream`, from that stream's
+    memory: kernels queued on the current stream may still use what was freed
+    on that one.  `returned`: the caller gets it, and may free it while the
+    current stream has work queued that reads it."""
+    import torch
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.bfloat16:

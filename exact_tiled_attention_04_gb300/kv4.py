@@ -1,6 +1,9 @@
 """PyTorch conveniences for the 4-bit key/value cache and for the attention
 weight of a prompt: tensor checks, allocation of outputs, and one call of the
 C entry point each (include/fa.h documents format, results and errors).
+
+Every call is enqueued on `stream` (default: the device's current stream), and
+what it allocates belongs to that stream.
 """
 from __future__ import annotations
 
@@ -34,16 +37,17 @@ def _scale(scale, d: int) -> float:
     return float(scale)
 
 
-def _call(where: str, function, device, stream, made, *args):
-    """One C call on `stream` (default: the device's current one) with the
-    device made current where it is not.  `made`: tensors allocated for the
-    call, whose memory the allocator must not hand out again before another
-    stream than its own is done."""
-    current = torch._C._cuda_getCurrentRawStream(device.index)
-    if stream is not None and stream.cuda_stream != current:
-        for t in made:
-            t.record_stream(stream)
-        current = stream.cuda_stream
+def _empty(shape, dtype, device, stream, returned: bool = True):
+    """Memory for a call on `stream` (None: the current one)."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _b._empty_on(stream, shape, dtype, device, returned)
+
+
+def _call(where: str, function, device, stream, *args):
+    """One C call on `stream` (None: the device's current one) with the
+    device made current where it is not."""
+    current = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == device.index:
         status = function(*args, current or None)
     else:
@@ -157,7 +161,7 @@ def kv4_append(cache: KV4Cache, k, v, counts_out=None, stream=None):
         counts_out = cache.counts
     else:
         _check(counts_out, "counts_out", torch.int32, (2, B), cache.device)
-    _call("fa_kv4_append", _b.load().fa_kv4_append, cache.device, stream, (),
+    _call("fa_kv4_append", _b.load().fa_kv4_append, cache.device, stream,
           cache._ref, k.data_ptr(), v.data_ptr(), n, code, counts_out.data_ptr())
     return counts_out
 
@@ -173,18 +177,17 @@ def kv4_read(cache: KV4Cache, count: int, first=None, dtype=None, k=None, v=None
     else:
         raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
     shape = (cache.B, cache.H_kv, count, cache.d)
-    made = []
     if k is None:
-        made.append(k := torch.empty(shape, dtype=dtype, device=cache.device))
+        k = _empty(shape, dtype, cache.device, stream)
     else:
         _check(k, "k", dtype, shape, cache.device)
     if v is None:
-        made.append(v := torch.empty(shape, dtype=dtype, device=cache.device))
+        v = _empty(shape, dtype, cache.device, stream)
     else:
         _check(v, "v", dtype, shape, cache.device)
     if first is not None:
         _check(first, "first", torch.int32, (cache.B,), cache.device)
-    _call("fa_kv4_read", _b.load().fa_kv4_read, cache.device, stream, made,
+    _call("fa_kv4_read", _b.load().fa_kv4_read, cache.device, stream,
           cache._ref, first.data_ptr() if first is not None else None, count, k.data_ptr(), v.data_ptr(), code)
     return k, v
 
@@ -204,25 +207,24 @@ def kv4_attention(q, cache: KV4Cache, scale: float | None = None, causal: bool =
     B, H, N_q, d = q.shape
     if B != cache.B or d != cache.d or H % cache.H_kv:
         raise ValueError(f"q must be [{cache.B}, a multiple of {cache.H_kv}, N_q, {cache.d}], got {tuple(q.shape)}")
-    made = []
     if out is None:
-        made.append(out := torch.empty((B, H, N_q, d), dtype=q.dtype, device=device))
+        out = _empty((B, H, N_q, d), q.dtype, device, stream)
     else:
         _check(out, "out", q.dtype, q.shape, device)
     if lse is not None:
         _check(lse, "lse", torch.float32, (B, H, N_q), device)
     elif with_lse:
-        made.append(lse := torch.empty((B, H, N_q), dtype=torch.float32, device=device))
+        lse = _empty((B, H, N_q), torch.float32, device, stream)
     if weight_out is not None:
         _check(weight_out, "weight_out", torch.float32, (B, cache.H_kv, cache.capacity), device)
     if workspace is None:
         size = max(cache.workspace_size(H, N_q, weight_out is not None), 16)
-        made.append(workspace := torch.empty(size, dtype=torch.uint8, device=device))
+        workspace = _empty(size, torch.uint8, device, stream, returned=False)
     else:
         size = workspace.numel() * workspace.element_size()
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    _call("fa_kv4_fwd", _b.load().fa_kv4_fwd, device, stream, made,
+    _call("fa_kv4_fwd", _b.load().fa_kv4_fwd, device, stream,
           cache._ref, q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None,
           weight_out.data_ptr() if weight_out is not None else None, H, N_q, _scale(scale, d),
           code | _b.FA_FLAG_CAUSAL if causal else code, workspace.data_ptr(), size)
@@ -241,9 +243,8 @@ def kv4_evict(cache: KV4Cache, keep: int, sinks: int = 0, recent: int = 0, weigh
         raise ValueError(f"keep must be at least 1, got {keep}")
     if weight is not None:
         _check(weight, "weight", torch.float32, (cache.B, cache.H_kv, cache.capacity), cache.device)
-    made = []
     if src is None:
-        made.append(src := torch.empty((cache.B, cache.H_kv, keep), dtype=torch.int32, device=cache.device))
+        src = _empty((cache.B, cache.H_kv, keep), torch.int32, cache.device, stream)
     else:
         _check(src, "src", torch.int32, (cache.B, cache.H_kv, keep), cache.device)
     if counts_out is None:
@@ -252,7 +253,7 @@ def kv4_evict(cache: KV4Cache, keep: int, sinks: int = 0, recent: int = 0, weigh
         _check(counts_out, "counts_out", torch.int32, (2, cache.B), cache.device)
     if out is not None and out.device != cache.device:
         raise ValueError(f"out must be on {cache.device}")
-    _call("fa_kv4_evict", _b.load().fa_kv4_evict, cache.device, stream, made,
+    _call("fa_kv4_evict", _b.load().fa_kv4_evict, cache.device, stream,
           cache._ref, keep, sinks, recent, weight.data_ptr() if weight is not None else None,
           out._ref if out is not None else None, src.data_ptr(), counts_out.data_ptr())
     return src
@@ -294,13 +295,12 @@ def attention_weights(q, k, lse, scale: float | None = None, causal: bool = Fals
         raise ValueError(f"incompatible q and k shapes: {tuple(q.shape)} {tuple(k.shape)}")
     _check(lse, "lse", torch.float32, (B, H, N_q), device)
     shape = (B, H_kv, N_kv)
-    made = []
     if out is None:
-        made.append(out := torch.empty(shape, dtype=torch.float32, device=device))
+        out = _empty(shape, torch.float32, device, stream)
     stride = _weight_stride(out, "out", shape, device)
     if weight_in is not None and _weight_stride(weight_in, "weight_in", shape, device) != stride:
         raise ValueError("weight_in and out must have the same strides")
-    _call("fa_fwd_weights", _b.load().fa_fwd_weights, device, stream, made,
+    _call("fa_fwd_weights", _b.load().fa_fwd_weights, device, stream,
           q.data_ptr(), k.data_ptr(), lse.data_ptr(), weight_in.data_ptr() if weight_in is not None else None,
           out.data_ptr(), stride, B, H, H_kv, N_q, N_kv, d, first_query, _scale(scale, d),
           code | _b.FA_FLAG_CAUSAL if causal else code)

@@ -419,6 +419,66 @@ def test_two_calls_at_once():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def calls_on_a_stream():
+    """Each call that allocates, with `stream` as its argument; and the bytes of its workspace."""
+    g = rng(420)
+    c = filled(g, 2, 2, [2000, 300], 64)
+    to = fa.KV4Cache.empty(2, 2, 256, 64)
+    q, pq, pk, pv = (rows(g, 2, h, n, 64) for h, n in ((8, 1), (4, 300), (2, 300), (2, 300)))
+    _, lse = fa.attention(pq, pk, pv, causal=True)
+    return {"attention": (lambda s: fa.kv4_attention(q, c, stream=s), c.workspace_size(8, 1, False)),
+            "read": (lambda s: fa.kv4_read(c, 300, stream=s), 0),
+            "evict": (lambda s: (fa.kv4_evict(c, 200, out=to, stream=s),), 0),
+            "weights": (lambda s: (fa.attention_weights(pq, pk, lse, causal=True, stream=s),), 0)}
+
+
+CALLS = pytest.mark.parametrize("name", ["attention", "read", "evict", "weights"])
+
+
+@CALLS
+def test_memory_of_a_call_on_another_stream(name):
+    """Nothing the call allocates was freed on the current stream, whose queued kernels still write it."""
+    call, bytes_ = calls_on_a_stream()[name]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)
+    freed = [torch.empty_like(t) for t in want] + [torch.empty(max(bytes_, 16), dtype=torch.uint8, device="cuda")]
+    for t in freed:
+        t.fill_(77)
+    at = {t.data_ptr() for t in freed}
+    del freed, t
+    got = call(s)
+    assert not at & {t.data_ptr() for t in got}
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()  # the fills are still to come
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@CALLS
+def test_freed_results_of_a_call_on_another_stream(name):
+    """A result that the caller frees while the current stream has its copy queued is not written again before that."""
+    call, _ = calls_on_a_stream()[name]
+    want = [t.clone() for t in call(None)]
+    copies = [torch.empty_like(t) for t in want]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = call(s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(100_000_000)
+    for a, b in zip(copies, got):
+        a.copy_(b)
+    at = {t.data_ptr() for t in got}
+    del got, b
+    with torch.cuda.stream(s):
+        again = [torch.full_like(t, 77) for t in want]
+    assert not at & {t.data_ptr() for t in again}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want))
+
+
 # ------------------------------------------------------------ prompt weights
 def check_weights(B, H, H_kv, N_q, N_kv, d, dtype, causal, first, seed, w_in=True):
     g = rng(seed)
