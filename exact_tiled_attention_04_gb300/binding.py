@@ -320,11 +320,13 @@ def fa_version() -> int:
 
 # ------------------------------------------------------- PyTorch convenience
 def _empty_on(stream, shape, dtype, device, returned: bool = True):
-    """An uninitialised tensor for a call on `stream`, from that stream's
-    memory: kernels queued on the current stream may still use what was freed
-    on that one.  `returned`: the caller gets it, and may free it while the
-    current stream has work queued that reads it."""
+    """An uninitialised tensor for a call on `stream` (None: the current one),
+    from that stream's memory: kernels queued on the current stream may still
+    use what was freed on that one.  `returned`: the caller gets it, and may
+    free it while the current stream has work queued that reads it."""
     import torch
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if returned:
@@ -380,11 +382,11 @@ def attention(q, k, v, scale: float | None = None, out=None, lse=None, with_lse:
     with torch.cuda.device(q.device):
         need = fa_fwd_ex_workspace_size(B, H, N_q, N_kv, d, num_splits)
     if need > 0 and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty_on(stream, need, torch.uint8, q.device, returned=False)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_on(stream, q.shape, q.dtype, q.device)
     if lse is None and with_lse:
-        lse = torch.empty((B, H, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty_on(stream, (B, H, N_q), torch.float32, q.device)
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
     with torch.cuda.device(q.device):
         st = fa_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -420,12 +422,11 @@ def attention_backward(q, k, v, o, lse, dout, scale: float | None = None, causal
     H_kv, N_kv = int(k.shape[1]), int(k.shape[2])
     if scale is None:
         scale = float(torch.tensor(1.0, dtype=torch.float32) / torch.sqrt(torch.tensor(float(d), dtype=torch.float32)))
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq, dk, dv = (_empty_on(stream, x.shape, x.dtype, x.device) if dx is None else dx
+                  for x, dx in ((q, dq), (k, dk), (v, dv)))
     need = fa_bwd_workspace_size(B, H, N_q, d)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty_on(stream, max(need, 16), torch.uint8, q.device, returned=False)
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
     with torch.cuda.device(q.device):
         st = fa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
