@@ -63,14 +63,13 @@ constexpr int kMaxDevices = 64;
 std::mutex g_err_mutex;
 std::atomic<unsigned int> g_generation{0};
 
-// Identity of the current CUDA context, unique over the process's life (the
-// driver's context id), or 0 when no context is current or the driver
-// entry points cannot be reached.  A device reset destroys the context and
-// the module's device symbols with it; the next context gets a new id.
 PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
 PFN_cuCtxGetId_v12000 g_ctx_id = nullptr;
 std::once_flag g_ctx_once;
 
+}  // namespace
+
+// The driver's context id.
 unsigned long long current_context_id() {
     std::call_once(g_ctx_once, [] {
         void* fn = nullptr;
@@ -90,8 +89,6 @@ unsigned long long current_context_id() {
     if (g_ctx_id(ctx, &id) != CUDA_SUCCESS) return 0;
     return id;
 }
-
-}  // namespace
 
 // Device address of a __device__ variable of this library on the current
 // device, looked up once per device and context (cudaGetSymbolAddress, with

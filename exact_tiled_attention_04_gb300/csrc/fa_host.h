@@ -23,6 +23,11 @@ unsigned int next_generation();
 // FA_OK or FA_ERR_CUDA (with the error message set).
 DevStatus* device_status_words(int* status);
 
+// Identity of the current CUDA context, unique over the process's life, or 0
+// when none is current or the driver cannot be asked.  A device reset
+// destroys the context and what the runtime held in it.
+unsigned long long current_context_id();
+
 // Per-device cache of one __device__ variable's address.  Entries are keyed
 // on the device's current CUDA context, so a device reset (which unloads the
 // module and may move the variable) is followed by a fresh lookup.

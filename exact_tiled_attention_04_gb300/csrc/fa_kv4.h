@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "fa_host.h"
 #include "fa_internal.h"
 
 namespace fa {
@@ -30,16 +31,21 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 #endif
 // Lets a kernel have `smem` bytes of dynamic shared memory, once per device
-// (`done`: a bit per device, the kernel's own).
-template <class Kernel>
-cudaError_t allow_smem(Kernel kernel, int smem, std::atomic<uint64_t>& done) {
+// and context (a device reset loses the limit).  `done`: per device the context
+// that has it; the kernel's own, as is its limit, which every call sets alike.
+struct SmemAllowed {
+    std::atomic<unsigned long long> ctx_id[host::kMaxCachedDevices] = {};
+};
+inline cudaError_t allow_smem(const void* kernel, int smem, SmemAllowed& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const bool cached = dev < host::kMaxCachedDevices;
+    const unsigned long long ctx = host::current_context_id();
+    if (cached && ctx != 0 && done.ctx_id[dev].load(std::memory_order_relaxed) == ctx) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    // the call made a context current if none was
+    if (e == cudaSuccess && cached) done.ctx_id[dev].store(host::current_context_id(), std::memory_order_relaxed);
     return e;
 }
 template <class Kernel, class... Args>

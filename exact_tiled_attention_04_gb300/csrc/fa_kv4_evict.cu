@@ -649,8 +649,9 @@ cudaError_t launch_evict(const Kv4EvictParams& p, cudaStream_t stream) {
     const size_t smem = sizeof(EvShared) + static_cast<size_t>(slice) * 4;
     auto kern = cs == 1 ? kv4_evict_kernel<D, true> : kv4_evict_kernel<D, false>;
     // the limit is the kernel's, not the call's: the same for all of them, whatever other threads evict meanwhile
-    static std::atomic<uint64_t> allowed[2];
-    cudaError_t e = allow_smem(kern, static_cast<int>(sizeof(EvShared)) + kEvMaxSlice * 4, allowed[cs == 1 ? 0 : 1]);
+    static SmemAllowed allowed[2];
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(sizeof(EvShared)) + kEvMaxSlice * 4,
+                               allowed[cs == 1 ? 0 : 1]);
     if (e != cudaSuccess) return e;
     const int advance = p.counts_out == p.from.counts ? 0 : 1;
     cudaLaunchConfig_t cfg = {};

@@ -600,8 +600,8 @@ template <int D, int R>
 cudaError_t launch_variant(const Kv4FwdParams& p, cudaStream_t stream) {
     using C = Kv4Cfg<D, R>;
     auto kern = kv4_fwd_kernel<D, R>;
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(kern, C::kSmemBytes, allowed);
+    static SmemAllowed allowed;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, allowed);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), kThreads4, C::kSmemBytes, stream, p);
     if (e != cudaSuccess) return e;

@@ -351,8 +351,8 @@ cudaError_t launch_weights_variant(const CUtensorMap& q, const CUtensorMap& k, c
                                    unsigned int grid, cudaStream_t stream) {
     using C = WtCfg<D, F16>;
     auto kern = fa_weights_kernel<D, F16>;
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(kern, static_cast<int>(C::kSmemBytes), allowed);
+    static SmemAllowed allowed;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes), allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);

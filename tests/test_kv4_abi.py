@@ -3,6 +3,8 @@ each call refuses, with which status, before any CUDA call; and of the Python
 handle."""
 import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -152,6 +154,48 @@ def test_prompt_weights_arguments():
                    (dict(w=A[0] + 64), 1), (dict(w=A[2]), 1), (dict(w_in=A[4] + 4), 1),
                    (dict(Nq=(1 << 31) - 1), 2), (dict(B=1 << 40, H=1 << 30), 1)):
         assert weights(**kw) == st, kw
+
+
+def run_host(tmp_path, source):
+    """Compile a C++ program against the library's internal headers, its CUDA calls the program's own; run it."""
+    from exact_tiled_attention_04_gb300 import build
+    (tmp_path / "t.cpp").write_text(source)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", build.CSRC, "-I", build.INCLUDE, "-isystem", cuda,
+                    "-o", str(tmp_path / "t"), str(tmp_path / "t.cpp")], check=True)
+    subprocess.run([str(tmp_path / "t")], check=True)
+
+
+def test_shared_memory_limit_is_set_once_per_context(tmp_path):
+    """A device reset loses a kernel's limit: the next context gets it again, a failed call is not remembered."""
+    run_host(tmp_path, r"""
+#include "fa_kv4.h"
+static int device = 0, calls = 0, limit = 0;
+static unsigned long long context = 7;
+static cudaError_t answer = cudaSuccess;
+extern "C" cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
+extern "C" cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int v) { ++calls; limit = v; return answer; }
+unsigned long long fa::host::current_context_id() { return context; }
+int main() {
+    static fa::SmemAllowed done;
+    int kernel = 0;
+    auto allow = [&] { return fa::allow_smem(&kernel, 100000, done); };
+    answer = cudaErrorInvalidValue;
+    if (allow() != cudaErrorInvalidValue || calls != 1) return 1;
+    answer = cudaSuccess;
+    if (allow() != cudaSuccess || calls != 2 || limit != 100000) return 2;
+    if (allow() != cudaSuccess || calls != 2) return 3;
+    device = 1, context = 8;  // another device has a context of its own
+    if (allow() != cudaSuccess || calls != 3) return 4;
+    device = 0, context = 9;  // the first device was reset
+    if (allow() != cudaSuccess || calls != 4 || allow() != cudaSuccess || calls != 4) return 5;
+    context = 0;  // none current
+    if (allow() != cudaSuccess || calls != 5) return 6;
+    device = 1000, context = 10;  // past the remembered devices
+    if (allow() != cudaSuccess || allow() != cudaSuccess || calls != 7) return 7;
+    return 0;
+}
+""")
 
 
 def test_handle_checks_its_tensors():
