@@ -91,6 +91,15 @@ struct Kv4EvictParams {
     int recent;
 };
 constexpr int kKv4EvictMaxCapacity = 393216;
+// Copies into another cache: blocks per head, of kKv4CopyRows slots each.  No
+// more entries are kept than the first cache has slots, however large `keep`.
+constexpr int kKv4CopyRows = 256;
+constexpr int kv4_kept_at_most(int64_t keep, int64_t capacity) {
+    return static_cast<int>(keep < capacity ? keep : capacity);
+}
+constexpr int kv4_copy_blocks(int64_t keep, int64_t capacity) {  // capacity <= kKv4EvictMaxCapacity
+    return (kv4_kept_at_most(keep, capacity) + kKv4CopyRows - 1) / kKv4CopyRows;
+}
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream);
 
 // Attention over the cache.  Rows: the R = N_q * group query rows of a

@@ -223,7 +223,7 @@ int validate_evict(const fa_kv4_cache_t* c, int64_t keep, int64_t sinks, int64_t
         return FA_ERR_UNSUPPORTED;
     const int64_t entries = mul(mul(c->B, c->H_kv), keep);
     if (mul(entries, 4) < 0) return FA_ERR_INVALID_ARG;
-    if (mul(c->B * c->H_kv, (keep + 255) / 256) > kInt32Max || c->B * c->H_kv > kInt32Max / 8) return FA_ERR_UNSUPPORTED;
+    if (mul(c->B * c->H_kv, fa::kv4_copy_blocks(keep, c->capacity)) > kInt32Max || c->B * c->H_kv > kInt32Max / 8) return FA_ERR_UNSUPPORTED;
     if (misaligned(rank_by, 4) || misaligned(src, 4) || misaligned(counts_out, 4)) return FA_ERR_ALIGNMENT;
     const Span rank{rank_by, static_cast<size_t>(c->B * c->H_kv * c->capacity) * 4};
     const Span list{src, static_cast<size_t>(entries) * 4}, co{counts_out, static_cast<size_t>(c->B) * 8};

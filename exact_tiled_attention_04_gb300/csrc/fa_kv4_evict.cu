@@ -613,18 +613,18 @@ __global__ void __launch_bounds__(kEvThreads, 1) kv4_evict_kernel(const __grid_c
 }
 
 // The entries named by src into another cache, 32 a warp; grid: heads x
-// blocks of kCopyRows slots.
-constexpr int kCopyThreads = 256;
-constexpr int kCopyRows = kCopyThreads;
+// blocks of kKv4CopyRows slots.
+constexpr int kCopyThreads = kKv4CopyRows;
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) kv4_evict_copy_kernel(const __grid_constant__ Kv4EvictParams p, int blocks) {
     const int head = static_cast<int>(blockIdx.x) / blocks;
-    const int j0 = (static_cast<int>(blockIdx.x) % blocks) * kCopyRows + static_cast<int>(threadIdx.x) / 32 * 32;
+    const int j0 = (static_cast<int>(blockIdx.x) % blocks) * kKv4CopyRows + static_cast<int>(threadIdx.x) / 32 * 32;
     grid_release();
     grid_wait();
-    if (j0 >= p.keep) return;
+    const int most = kv4_kept_at_most(p.keep, p.from.capacity);
+    if (j0 >= most) return;
     const int j = j0 + static_cast<int>(threadIdx.x) % 32;
-    const int from = j < p.keep ? p.src[static_cast<long long>(head) * p.keep + j] : -1;
+    const int from = j < most ? p.src[static_cast<long long>(head) * p.keep + j] : -1;
     if (__any_sync(0xffffffffu, from >= 0))
         copy_entries<D>(p.from, p.to, static_cast<long long>(head) * p.from.capacity, from,
                         static_cast<long long>(head) * p.to.capacity + j0);
@@ -671,7 +671,7 @@ cudaError_t launch_evict(const Kv4EvictParams& p, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, kern, p, slice, advance);
     if (e != cudaSuccess) return e;
     if (p.to.codes[0] != p.from.codes[0]) {
-        const int blocks = (p.keep + kCopyRows - 1) / kCopyRows;
+        const int blocks = kv4_copy_blocks(p.keep, p.from.capacity);
         e = launch_dependent(kv4_evict_copy_kernel<D>, dim3(static_cast<unsigned>(heads) * static_cast<unsigned>(blocks)),
                              kCopyThreads, 0, stream, p, blocks);
         if (e != cudaSuccess) return e;

@@ -198,6 +198,23 @@ int main() {
 """)
 
 
+def test_blocks_of_the_copy_into_another_cache(tmp_path):
+    """As many as hold the entries that can be kept, up to the largest `keep`."""
+    run_host(tmp_path, r"""
+#include "fa_kv4.h"
+int main() {
+    const int64_t capacities[] = {128, 256, 384, 40960, 393216}, keeps[] = {1, 255, 256, 257, 100000, 393216,
+        (int64_t{1} << 31) - 300, (int64_t{1} << 31) - 256, (int64_t{1} << 31) - 255, (int64_t{1} << 31) - 1};
+    for (int64_t c : capacities)
+        for (int64_t k : keeps) {
+            const int64_t n = k < c ? k : c, blocks = fa::kv4_copy_blocks(k, c);
+            if (fa::kv4_kept_at_most(k, c) != n || blocks * 256 < n || (blocks - 1) * 256 >= n) return 1;
+        }
+    return 0;
+}
+""")
+
+
 def test_handle_checks_its_tensors():
     torch = pytest.importorskip("torch")
     u8 = dict(dtype=torch.uint8)

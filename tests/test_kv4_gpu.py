@@ -600,6 +600,14 @@ def test_evict_into_another_cache(d, length, keep):
     check_evict(c, keep, 4, min(16, keep), out=to)
 
 
+@pytest.mark.parametrize("length,keep", [(300, 5000), (1, 129), (128, 100000)])
+def test_evict_into_a_larger_cache(length, keep):
+    """More than the first cache has slots may be asked for: all its entries are taken over."""
+    g = rng(622 + length)
+    c = filled(g, 2, 2, [length, 0], 64)
+    check_evict(c, keep, 4, 16, out=filled(g, 2, 2, [7, 8], 64, capacity=keep + 100))
+
+
 @pytest.mark.parametrize("length", [17, 300, 4100, 40010])
 @pytest.mark.parametrize("e", [1, 2, 5, 15, 16, 17])
 def test_evict_a_few(length, e):
