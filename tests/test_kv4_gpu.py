@@ -311,6 +311,28 @@ def test_dominant_and_tiny_weights():
     check_attention(c, q, "bf16", scale=float(24 * np.log(2) / 96))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("at", [7, 263])  # its warp's first slab, where the reference begins, and the second, which moves it
+@pytest.mark.parametrize("G", [4, 8, 12])  # the three layouts
+@pytest.mark.parametrize("d", [64, 128])
+def test_tiny_weights_beside_a_dominant_one(d, G, at, dtype):
+    """One key whose weight is 2^24 times the others' and whose value is 0: the output is the tiny
+    weights of the keys that its warp holds (slots 0 to 31 and 256 to 287 of a cache that one block
+    reads), and they are kept to fp16's 2^-25 below a weight of 2^7."""
+    n = 512
+    c = fa.KV4Cache.empty(1, 1, n, d)
+    k, v = (torch.zeros(1, 1, n, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[0, 0, at, :16] = 6.0
+    v[0, 0, :32] = v[0, 0, 256:288] = 1.0
+    v[0, 0, at] = 0.0
+    fa.kv4_append(c, k, v)
+    q = torch.zeros(1, G, 1, d, dtype=TORCH[dtype], device="cuda")
+    q[..., :16] = 1.0
+    out, _, _ = check_attention(c, q, dtype, scale=float(24 * np.log(2) / 96))
+    # 63 * 2^-24 / (1 + 511 * 2^-24); without the tiny weights it is 0, ten times what the check lets pass
+    assert (out.float() > 0.8 * 63 * 2.0 ** -24).all()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G", [1, 2, 4])  # 3, 6 and 12 rows: the three layouts
 @CAPACITY
@@ -356,6 +378,28 @@ def test_matches_the_16_bit_attention_on_the_stored_values():
     want, wl = fa.attention(q, k, v)
     got, gl = fa.kv4_attention(q, c)
     assert (got.float() - want.float()).abs().max() <= 2 * 1.5e-2 and (gl - wl).abs().max() <= 1e-3
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_is_as_near_the_16_bit_attention_as_roundings_allow(dtype):
+    """The two attentions on the same stored values differ by their own roundings only: this one's
+    (R.tol_out), and the other's weights (half a step of their type, in numerator and denominator),
+    scores and output."""
+    g = rng(381)
+    c = filled(g, 2, 2, [512, 512], 128)
+    q = rows(g, 2, 8, 1, 128, dtype=dtype)
+    k, v = fa.kv4_read(c, 512, dtype=TORCH[dtype])
+    want, wl = fa.attention(q, k, v)
+    got, gl = fa.kv4_attention(q, c)
+    hk, hv = held(c)
+    o, lse, _, av, big = R.attend(np64(q), hk, hv, [512, 512], float(np.float32(1 / np.sqrt(128))), False)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    mine = R.tol_out(o, av, big, 512, np.abs(hv).max(), 128, dtype)
+    rel = 2 * half + 2 * R.score_error(big, 128)[..., None] + 2.0 ** -20
+    other = half * np.abs(o) + (1 + half) * rel * (av + np.abs(o)) + 2.0 ** -24
+    err = np.abs(np64(got) - np64(want))
+    assert (err <= mine + other).all(), np.max(err / (mine + other))
+    assert (np.abs(np64(gl) - np64(wl)) <= 2 * R.tol_lse(lse, big, 128)).all()
 
 
 def test_long_cache_offsets_pass_32_bits():
