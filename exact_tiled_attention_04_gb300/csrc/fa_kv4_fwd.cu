@@ -375,6 +375,12 @@ __global__ void __launch_bounds__(kThreads4, Kv4Cfg<D, R>::kCtasPerSm) kv4_fwd_k
 struct Parts {
     int slabs, first, last;
 };
+// Lengths from the second-level cache: what a thread read of them ahead of its wait stays in no cache of the SM.
+__device__ __forceinline__ int length_of(const Kv4Cache& c, int b) { return min(max(__ldcg(c.counts + b), 0), c.capacity); }
+__device__ __forceinline__ int length_of_lane(const Kv4Cache& c) {
+    const int lane = threadIdx.x % 32;
+    return lane < c.B ? length_of(c, lane) : 0;
+}
 // Where sequence b begins, its length and slabs, a CTA's share, by a warp (every lane gets them); `mine`: the length
 // of sequence `lane`.
 struct Spread {
@@ -385,29 +391,16 @@ __device__ __forceinline__ Spread spread_of(const Kv4FwdParams& p, int b, int mi
     int total = share_of(slabs_of(mine), p.unit_cost) * units;
     int before = lane < b ? total : 0;
     for (int x = 32 + lane; x < p.c.B; x += 32) {
-        const int n = share_of(slabs_of(kv4_length(p.c, x)), p.unit_cost) * units;
+        const int n = share_of(slabs_of(length_of(p.c, x)), p.unit_cost) * units;
         total += n;
         if (x < b) before += n;
     }
     Spread s;
     s.before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
     s.per = slabs_per_cta(static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total))), p.ctas);
-    s.len = b < 32 ? __shfl_sync(0xffffffffu, mine, b) : kv4_length(p.c, b);
+    s.len = b < 32 ? __shfl_sync(0xffffffffu, mine, b) : length_of(p.c, b);
     s.slabs = slabs_of(s.len);
     s.cost = p.unit_cost;
-    return s;
-}
-// The same, behind the wait for the main kernel.  That kernel waited for whatever wrote the lengths, but only a
-// kernel's own wait makes them certain to it: what was formed ahead of the wait stands if they are the same behind it
-// (formed behind it alone: 16384 slots, B = 8, 35.3 us instead of 34.4).
-__device__ __forceinline__ Spread wait_and_spread(const Kv4FwdParams& p, int b) {
-    const int lane = threadIdx.x % 32;
-    const auto length = [&] { return lane < p.c.B ? min(max(__ldcg(p.c.counts + lane), 0), p.c.capacity) : 0; };
-    const int early = length();
-    Spread s = spread_of(p, b, early);
-    grid_wait();
-    const int mine = length();
-    if (p.c.B > 32 || __any_sync(0xffffffffu, mine != early)) s = spread_of(p, b, mine);
     return s;
 }
 __device__ __forceinline__ Parts parts_of(const Spread& s, int unit) {
@@ -421,12 +414,16 @@ __device__ __forceinline__ Parts parts_of(const Spread& s, int unit) {
 __device__ __forceinline__ long long part_row(int cta, int first, int rows, int r) {
     return (static_cast<long long>(cta) * 2 + (cta == first ? 1 : 0)) * rows + r;
 }
+// The sums of a row's part first + lane.
+__device__ __forceinline__ float4 first_sums(const Kv4FwdParams& p, const Parts& u, int rows, int r) {
+    const int c0 = u.first + static_cast<int>(threadIdx.x) % 32;
+    return c0 <= u.last ? p.part_ml[part_row(c0, u.first, rows, r)] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+}
 // A row's reference, exact sum and rounded sum over its parts, by a warp, and
-// the factor of the part first + lane (0 where there is none).
-__device__ __forceinline__ void row_sums(const Kv4FwdParams& p, const Parts& u, int rows, int r, float& M, float& L,
-                                         float& LQ, float& f) {
+// the factor of the part first + lane (0 where there is none); ml0: first_sums.
+__device__ __forceinline__ void row_sums(const Kv4FwdParams& p, const Parts& u, int rows, int r, const float4& ml0,
+                                         float& M, float& L, float& LQ, float& f) {
     const int lane = threadIdx.x % 32, c0 = u.first + lane;
-    const float4 ml0 = c0 <= u.last ? p.part_ml[part_row(c0, u.first, rows, r)] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
     M = ml0.x;
     for (int c = c0 + 32; c <= u.last; c += 32) M = fmaxf(M, p.part_ml[part_row(c, u.first, rows, r)].x);
 #pragma unroll
@@ -458,6 +455,13 @@ constexpr int kAhead = 8;  // parts' rows loaded ahead of the factors
 // d = 128, H = 32/8, 16384 slots, B = 1 (38 parts) 14.5 / 10.1, B = 2 (19)
 // 16.1 / 15.7; 8192 slots, B = 4 (10) 14.4 / 15.7.  The others: accumulated weight,
 // kJoinKeys slots of one key/value head each.
+//
+// The lengths are read ahead of the wait for the main kernel, and again behind
+// it: that kernel waited for whatever wrote them, but only a kernel's own wait
+// makes them certain to it.  What goes by the first reading, indices within the
+// workspace whatever was read and the first loads, is done again where the
+// second differs.  (All behind the wait: 16384 slots, B = 8, 35.3 us instead of
+// 33.9.)
 template <int D, int kWays>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdParams p, int rows_per_block,
                                                                  int join_blocks) {
@@ -474,29 +478,44 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
         const int r = static_cast<int>(row - kvh * p.rows);
         const int b = static_cast<int>(kvh / p.c.H_kv);
         const int unit = static_cast<int>(kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block;
-        const Parts u = parts_of(wait_and_spread(p, b), unit);
-        if (u.slabs > 0 && u.first == u.last) return;  // the main kernel wrote it
+        const int early = length_of_lane(p.c);
+        Parts u = parts_of(spread_of(p, b, early), unit);
+        grid_wait();
+        const int mine = length_of_lane(p.c);
         constexpr int kPer = D / 32;
+        const int rb = r % rows_per_block;
+        int parts = 0;
         float acc[kPer] = {}, M = -INFINITY, L = 0.0f, LQ = 0.0f;
-        if (u.slabs > 0) {
-            const int rb = r % rows_per_block, parts = u.last - u.first + 1;
-            const auto load = [&](int i, float (&v)[kPer]) {
-                const float* src = p.part_o + part_row(u.first + i, u.first, rows_per_block, rb) * D + lane * kPer;
+        float ahead[kAhead][kPer], x = 0.0f, f;
+        float4 ml0;
+        const auto load = [&](int i, float (&v)[kPer]) {
+            const float* src = p.part_o + part_row(u.first + i, u.first, rows_per_block, rb) * D + lane * kPer;
 #pragma unroll
-                for (int j = 0; j < kPer; j += 2)
-                    *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(src + j);
-            };
-            // the first parts' rows are on their way while the factors are formed, one per lane
-            const auto reference = [&](int i) {
-                return i < parts ? p.part_ml[part_row(u.first + i, u.first, rows_per_block, rb)].x : -INFINITY;
-            };
-            const auto factor = [&](int i, float x) { return i >= parts ? 0.0f : M == -INFINITY ? 1.0f : ex2(x - M); };
-            const float x = kWays > 1 ? reference(way + kWays * lane) : 0.0f;
-            float ahead[kAhead][kPer], f;
+            for (int j = 0; j < kPer; j += 2)
+                *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(src + j);
+        };
+        const auto reference = [&](int i) {
+            return i < parts ? p.part_ml[part_row(u.first + i, u.first, rows_per_block, rb)].x : -INFINITY;
+        };
+        // the first parts' rows are on their way while the factors are formed, one per lane
+        const auto begin = [&] {
+            parts = u.slabs > 0 ? u.last - u.first + 1 : 0;
+            if (parts == 0) return;
+            if constexpr (kWays > 1) x = reference(way + kWays * lane);
+            ml0 = first_sums(p, u, rows_per_block, rb);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (way + kWays * k < parts) load(way + kWays * k, ahead[k]);
-            row_sums(p, u, rows_per_block, rb, M, L, LQ, f);
+        };
+        if (p.c.B <= 32) begin();
+        if (p.c.B > 32 || __any_sync(0xffffffffu, mine != early)) {
+            u = parts_of(spread_of(p, b, mine), unit);
+            begin();
+        }
+        if (u.slabs > 0 && u.first == u.last) return;  // the main kernel wrote it
+        if (u.slabs > 0) {
+            const auto factor = [&](int i, float x) { return i >= parts ? 0.0f : M == -INFINITY ? 1.0f : ex2(x - M); };
+            row_sums(p, u, rows_per_block, rb, ml0, M, L, LQ, f);
             if constexpr (kWays > 1) f = factor(way + kWays * lane, x);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
@@ -506,10 +525,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
                     for (int j = 0; j < kPer; ++j) acc[j] += w * ahead[k][j];
             }
             // the others: 32 factors at a time; four parts' rows in flight
-            const int mine = (parts - way + kWays - 1) / kWays;
-            for (int k0 = kAhead; k0 < mine; k0 = (k0 / 32 + 1) * 32) {
+            const int of_way = (parts - way + kWays - 1) / kWays;
+            for (int k0 = kAhead; k0 < of_way; k0 = (k0 / 32 + 1) * 32) {
                 if (k0 >= 32) f = factor(way + kWays * (k0 + lane), reference(way + kWays * (k0 + lane)));
-                const int n = min((k0 / 32 + 1) * 32, mine);
+                const int n = min((k0 / 32 + 1) * 32, of_way);
 #pragma unroll 4
                 for (int k = k0; k < n; ++k) {
                     const float w = __shfl_sync(0xffffffffu, f, k % 32);
@@ -546,23 +565,33 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
     const int i = static_cast<int>(blockIdx.x) - join_blocks;
     const int kvh = i / chunks, b = kvh / p.c.H_kv;
     const int key0 = (i % chunks) * kJoinKeys;
-    const Spread spread = wait_and_spread(p, b);
-    const int len = spread.len;
-    if (key0 >= len) return;
+    const int early = length_of_lane(p.c);
+    Spread spread = spread_of(p, b, early);
+    grid_wait();
+    const int mine = length_of_lane(p.c);
     const long long slot0 = static_cast<long long>(kvh) * p.c.capacity + key0 + threadIdx.x;
-    const int left = len - key0 - static_cast<int>(threadIdx.x);  // this thread's keys: 0, 256, .. below it
+    int left = 0;  // this thread's keys: 0, 256, .. below it
     // four rows (a quarter of a 16-row block, the usual group) wait in registers for the rows' sums
     float4 first4[kMine];
     float old[kMine];
     const bool four = p.rows % 4 == 0;
+    const auto begin = [&] {
+        left = spread.len - key0 - static_cast<int>(threadIdx.x);
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-        const long long at = slot0 + k * kJoinThreads;
-        const bool in = k * kJoinThreads < left;
-        old[k] = in && p.weight_in != nullptr ? p.weight_in[at] : 0.0f;
-        first4[k] = in && four ? *reinterpret_cast<const float4*>(p.logits + at * p.rows)
-                               : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        for (int k = 0; k < kMine; ++k) {
+            const long long at = slot0 + k * kJoinThreads;
+            const bool in = k * kJoinThreads < left;
+            old[k] = in && p.weight_in != nullptr ? p.weight_in[at] : 0.0f;
+            first4[k] = in && four ? *reinterpret_cast<const float4*>(p.logits + at * p.rows)
+                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+    };
+    if (p.c.B <= 32) begin();
+    if (p.c.B > 32 || __any_sync(0xffffffffu, mine != early)) {
+        spread = spread_of(p, b, mine);
+        begin();
     }
+    if (key0 >= spread.len) return;
     for (int r = warp; r < p.rows; r += kJoinThreads / 32) {
         const Parts u = parts_of(spread, (kvh % p.c.H_kv) * p.row_blocks + r / rows_per_block);
         float v;
@@ -570,7 +599,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4FwdPara
             v = p.row_lse2[static_cast<long long>(kvh) * p.rows + r];
         } else {
             float M, L, LQ, f;
-            row_sums(p, u, rows_per_block, r % rows_per_block, M, L, LQ, f);
+            const float4 ml0 = first_sums(p, u, rows_per_block, r % rows_per_block);
+            row_sums(p, u, rows_per_block, r % rows_per_block, ml0, M, L, LQ, f);
             v = L == 0.0f ? -INFINITY : M + log2f(L);
         }
         if (lane == 0) lse2[r] = v == -INFINITY ? INFINITY : v;  // a row that sees nothing adds nothing
