@@ -26,10 +26,13 @@
 // shared by many.  A run that ends one unit and begins another takes about as
 // long as one of a group more, so a unit counts a group more than it has;
 // where a CTA gets two groups or fewer of a full cache it does not, as runs
-// then often end with their unit.  (Counted against not, at d = 128: N = 2048
-// B = 8 10.8 / 9.8 us; N = 2560 11.6 / 13.3; N = 4096 B = 5 11.8 / 13.3, B = 8,
-// where every unit is cut into four equal runs, 13.4 / 13.4; N = 16384 33.7 /
-// 34.9; 16 sequences of up to 8192 with weights 26.0 / 28.1.)
+// then often end with their unit.  (Counted against not, at d = 128, H = 32/8:
+// N = 2048 B = 8 10.7 / 10.0 us; N = 2560 13.2 / 14.7; N = 4096 B = 5 13.6 /
+// 14.7, B = 8, where every unit is cut into four equal runs, 15.3 / 15.3; N =
+// 16384 33.6 / 35.0; d = 64 alike.  With 8 rows a head, 2560 slots 15.6 / 17.8,
+// 16384 38.3 / 40.0, but B = 8 N = 4096 19.1 / 17.9; with 16, N = 4096 B = 5
+// 19.5 / 20.8, 8192 33.0 / 34.5, 16384 53.3 / 53.1, but 2048 17.1 / 15.4 and
+// 2560 19.6 / 17.5: there the rule counts where it had better not.)
 //
 // A CTA whose run holds a whole unit writes its output; of a unit cut between
 // CTAs each leaves a partial result (at most two per CTA: the unit it starts
@@ -44,14 +47,17 @@
 // A cache of at most kWholeSlots slots, or twice that where there are as many
 // units as SMs, is not cut: a CTA per unit, and no second kernel unless
 // weights are asked for.  Whole against cut, in us, d = 128 and H = 32/8:
-// 512 slots B = 1 5.5 / 6.3, B = 8 5.5 / 6.5, B = 256 45.8 / 45.5; 1024 slots
-// B = 1 7.6 / 6.4, B = 8 8.2 / 8.0, B = 24 12.0 / 14.7, B = 256 68.6 / 69.9.
+// 512 slots B = 1 5.5 / 6.9, B = 8 5.8 / 7.2, B = 64 16.1 / 18.6, B = 256 45.8 /
+// 45.5; 1024 slots B = 1 7.6 / 6.9, B = 24 12.0 / 15.4, B = 64 22.5 / 26.6, B =
+// 256 68.6 / 69.9; d = 64 and 8 or 16 rows a head alike.  64 units of 1024
+// slots, which the rule cuts, are 6 % sooner whole there (7.9 / 8.3), and up to
+// 24 % with 16 rows at d = 64 (7.9 / 9.8).
 //
-// What is left (B = 8, H = 32/8, d = 128): 16384 slots take 33.7 us, 65536
-// 103.5 (5.8 TB/s); 49152 more cost what reading them does, so 11 us do not
+// What is left (B = 8, H = 32/8, d = 128): 16384 slots take 33.8 us, 65536
+// 104 (5.8 TB/s); 49152 more cost what reading them does, so 11 us do not
 // depend on the length: 1.5 from the wait to the first copy, 1.7 until it is
-// there, up to 7 between the first and the last block's end, 1.7 for the
-// second kernel.
+// there, up to 7 between the first and the last block's end (about 3 between
+// their mean and the last), 1.7 for the second kernel.
 //
 // Every wait is bounded as in the forward kernel; a warp that gives up skips
 // its remaining slabs but still reaches the block's barriers.
@@ -452,8 +458,9 @@ constexpr int kAhead = 8;  // parts' rows loaded ahead of the factors
 // Blocks 0 .. join_blocks - 1: the output rows whose unit several CTAs shared
 // (or that has no slot at all), p.join_warps warps a row: one, or the whole
 // block where a row has 2 kAhead parts or more.  A warp against a block, in us:
-// d = 128, H = 32/8, 16384 slots, B = 1 (38 parts) 14.5 / 10.1, B = 2 (19)
-// 16.1 / 15.7; 8192 slots, B = 4 (10) 14.4 / 15.7.  The others: accumulated weight,
+// d = 128, H = 32/8, 16384 slots, B = 1 (38 parts) 14.9 / 10.4, B = 2 (19)
+// 17.5 / 16.5; 8192 slots, B = 4 (10) 15.7 / 16.1; d = 64 and 8 or 16 rows a
+// head alike (16384 slots, B = 1, 16 rows 19.2 / 17.1).  The others: accumulated weight,
 // kJoinKeys slots of one key/value head each.
 //
 // The lengths are read ahead of the wait for the main kernel, and again behind

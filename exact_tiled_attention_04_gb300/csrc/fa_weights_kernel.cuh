@@ -29,8 +29,9 @@
 // Each issuer's barrier waits, about 180 clocks a product, and the commits, 35
 // each, come on top: two issuers hide one another's, and a query stage is
 // given back by the warps that read the scores instead of by a commit.
-// Measured at B = 2, H = 32/8, N = 8192, d = 128, causal: 375 us, 1465 TFLOP/s
-// (tensor pipe and exponentials 67 % busy each); one issuer 588 us;
+// Measured at B = 2, H = 32/8, N = 8192, d = 128, causal: 375 to 408 us on
+// different boxes, 1465 to 1347 TFLOP/s (tensor pipe and exponentials 67 % busy
+// each); on the first, one issuer 588 us;
 // keys in tensor memory and three buffers 566; products of 64 rows, whose
 // columns are free sooner, 800 (an N = 64 product takes 48 clocks a step
 // instead of 32).

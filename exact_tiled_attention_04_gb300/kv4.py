@@ -88,6 +88,11 @@ class KV4Cache:
     appended); pos int32 and weight fp32 [B, H_kv, capacity], each optional.
     capacity is a multiple of 128, d is 64 or 128.  The tensors are checked
     here once; replace none of them afterwards.
+
+    Blocks of 16 channels below 0.006 in magnitude are stored as zeros, below
+    0.094 with fewer bits, above 2688 saturated: multiply keys or values out of
+    that range by a power of two before storing them, and `scale` or the output
+    by its inverse.
     """
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, counts, pos=None, weight=None):

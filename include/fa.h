@@ -349,7 +349,12 @@ size_t fa_bwd_workspace_size(int64_t B, int64_t H, int64_t N_q, int64_t d);
  * lies in 2^-10 .. 2688: bf16 and fp16 both hold it exactly, and nothing
  * below rounds it again.  s = 0: the block holds zeros (the sign of a zero is
  * not defined).  A block with an infinity or a NaN gets the scale NaN and
- * reads as NaN throughout.  Two codes share a byte, the even channel in the
+ * reads as NaN throughout.  There is no scale per head or tensor beside the
+ * blocks': a block whose largest magnitude is at most 6 * 2^-10 (0.0059) is
+ * stored as zeros, one below 6 * 2^-6 (0.094) has a scale of fewer bits, one
+ * above 2688 saturates, all without a report.  Keys or values outside that
+ * range are multiplied by a power of two before they are stored, and `scale`
+ * (keys) or the output (values) by its inverse.  Two codes share a byte, the even channel in the
  * low half.
  *
  * Entries are slots 0 .. length - 1 of each key/value head; attention does
@@ -418,6 +423,9 @@ int fa_kv4_read(const fa_kv4_cache_t* cache, const int32_t* first, int64_t count
  *                nothing in it needs to be zeroed.  Calls (and replays of
  *                captured ones) that may run at once need one each.
  * A row that sees no slot gets O = 0 and lse = -inf and adds no weight.
+ * Scores, sums, lse and the accumulated weights are held in 32 bits.  For the
+ * product with V the softmax weights are rounded to fp16, to 2^-11 of each and
+ * 2^-32 of the largest, and divided by the sum of the rounded ones.
  * Lengths are read on the device (clamped to 0 .. capacity), so a captured
  * call follows them.  Results do not depend on the order in which blocks run.
  * One or two kernels.
