@@ -484,9 +484,11 @@ def test_memory_of_a_call_on_another_stream(name):
     """Nothing the call allocates was freed on the current stream, whose queued kernels still write it."""
     call, bytes_ = calls_on_a_stream()[name]
     want = [t.clone() for t in call(None)]
+    for t in (*want, torch.empty(16, dtype=torch.uint8, device="cuda")):
+        torch.empty_like(t).fill_(77)  # loads the fills' kernels ahead of the pause
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    torch.cuda._sleep(100_000_000)
+    torch.cuda._sleep(400_000_000)  # 0.2 s
     freed = [torch.empty_like(t) for t in want] + [torch.empty(max(bytes_, 16), dtype=torch.uint8, device="cuda")]
     for t in freed:
         t.fill_(77)
@@ -511,7 +513,7 @@ def test_freed_results_of_a_call_on_another_stream(name):
     s = torch.cuda.Stream()
     got = call(s)
     torch.cuda.current_stream().wait_stream(s)
-    torch.cuda._sleep(100_000_000)
+    torch.cuda._sleep(400_000_000)
     for a, b in zip(copies, got):
         a.copy_(b)
     at = {t.data_ptr() for t in got}
