@@ -4,6 +4,8 @@ O = softmax(scale * Q K^T) V and the per-row log-sum-exp, computed by fused
 CUDA kernels that never write the N x N score matrix to HBM, and the
 gradients dQ, dK, dV recomputed from the saved log-sum-exp.  A key/value cache
 held in 4 bits, attention over it and eviction by accumulated weight: ``kv4``.
+Attention over packed sequences of different lengths and its gradients:
+``packed``.
 
 The C ABI (include/fa.h) is mirrored one to one by ``binding``; ``inputs``
 draws the seeded synthetic workloads.  Importing the package loads no CUDA
@@ -20,6 +22,8 @@ from .binding import (FA_DTYPE_BF16, FA_DTYPE_F16, FA_DTYPE_F32, FA_FLAG_CAUSAL,
                       fa_kv4_read_validate,
                       fa_fwd_ex_launches, fa_fwd_ex_splits, fa_fwd_ex_static, fa_fwd_ex_static_capacity, fa_fwd_ex_validate,
                       fa_fwd_ex_workspace_size, fa_fwd_host, fa_fwd_host_workspace_size, fa_fwd_validate,
-                      fa_last_error_message, fa_selftest_barrier_timeout, fa_status_string,
+                      fa_last_error_message, fa_packed_bwd, fa_packed_bwd_validate, fa_packed_bwd_workspace_size,
+                      fa_packed_fwd, fa_packed_fwd_validate, fa_rows_t, fa_selftest_barrier_timeout, fa_status_string,
                       fa_version)
 from .kv4 import KV4Cache, attention_weights, kv4_append, kv4_attention, kv4_evict, kv4_read  # noqa: F401
+from .packed import packed_attention, packed_attention_backward  # noqa: F401

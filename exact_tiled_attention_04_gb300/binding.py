@@ -43,6 +43,11 @@ class fa_kv4_cache_t(ctypes.Structure):
         + [(n, ctypes.c_int64) for n in ("B", "H_kv", "capacity", "d")]
 
 
+class fa_rows_t(ctypes.Structure):
+    """The C struct of include/fa.h: a view of [rows, heads, d] (address, strides in elements)."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 class FAError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -121,18 +126,22 @@ def load(path: str | None = None):
         lib.fa_bwd_host.argtypes = bwd_args + [vp]
         lib.fa_bwd_host_workspace_size.restype = sz
         lib.fa_bwd_host_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64]
-        cp = ctypes.POINTER(fa_kv4_cache_t)
+        cp, rp = ctypes.POINTER(fa_kv4_cache_t), ctypes.POINTER(fa_rows_t)
         for name, args in (("fa_kv4_append", [cp, vp, vp, i64, c_int, vp]),
                            ("fa_kv4_read", [cp, vp, i64, vp, vp, c_int]),
                            ("fa_kv4_fwd", [cp, vp, vp, vp, vp, i64, i64, f32, c_int, vp, sz]),
                            ("fa_kv4_evict", [cp, i64, i64, i64, vp, cp, vp, vp]),
-                           ("fa_fwd_weights", [vp] * 5 + [i64] * 8 + [f32, c_int])):
+                           ("fa_fwd_weights", [vp] * 5 + [i64] * 8 + [f32, c_int]),
+                           ("fa_packed_fwd", [rp] * 4 + [vp] * 3 + [i64] * 6 + [f32, c_int]),
+                           ("fa_packed_bwd", [rp] * 5 + [vp] + [rp] * 3 + [vp] * 2 + [i64] * 6 + [f32, c_int, vp, sz])):
             getattr(lib, name).restype = c_int
             getattr(lib, name).argtypes = args + [vp]
             getattr(lib, name + "_validate").restype = c_int
             getattr(lib, name + "_validate").argtypes = args
         lib.fa_kv4_fwd_workspace_size.restype = sz
         lib.fa_kv4_fwd_workspace_size.argtypes = [i64] * 6 + [c_int]
+        lib.fa_packed_bwd_workspace_size.restype = sz
+        lib.fa_packed_bwd_workspace_size.argtypes = [i64] * 4
         _lib = lib
         return lib
 
@@ -296,6 +305,36 @@ def fa_fwd_weights_validate(q: int, k: int, lse: int, weight_in: int | None, wei
                             dtype: int) -> int:
     return load().fa_fwd_weights_validate(q, k, lse, weight_in or None, weight_out, weight_stride, B, H, H_kv, N_q,
                                           N_kv, d, first_query, scale, dtype)
+
+
+def fa_packed_fwd(q, k, v, o, lse: int | None, cu_q: int, cu_k: int, B: int, T_q: int, T_k: int, H: int, H_kv: int,
+                  d: int, scale: float, dtype: int, stream: int | None) -> int:
+    """`q`, `k`, `v`, `o` here and below: an fa_rows_t (None for a NULL pointer)."""
+    return load().fa_packed_fwd(q, k, v, o, lse or None, cu_q, cu_k, B, T_q, T_k, H, H_kv, d, scale, dtype,
+                                stream or None)
+
+
+def fa_packed_fwd_validate(q, k, v, o, lse: int | None, cu_q: int, cu_k: int, B: int, T_q: int, T_k: int, H: int,
+                           H_kv: int, d: int, scale: float, dtype: int) -> int:
+    return load().fa_packed_fwd_validate(q, k, v, o, lse or None, cu_q, cu_k, B, T_q, T_k, H, H_kv, d, scale, dtype)
+
+
+def fa_packed_bwd(q, k, v, o, dout, lse: int, dq, dk, dv, cu_q: int, cu_k: int, B: int, T_q: int, T_k: int, H: int,
+                  H_kv: int, d: int, scale: float, dtype: int, workspace: int, workspace_bytes: int,
+                  stream: int | None) -> int:
+    return load().fa_packed_bwd(q, k, v, o, dout, lse, dq, dk, dv, cu_q, cu_k, B, T_q, T_k, H, H_kv, d, scale, dtype,
+                                workspace, workspace_bytes, stream or None)
+
+
+def fa_packed_bwd_validate(q, k, v, o, dout, lse: int, dq, dk, dv, cu_q: int, cu_k: int, B: int, T_q: int, T_k: int,
+                           H: int, H_kv: int, d: int, scale: float, dtype: int, workspace: int,
+                           workspace_bytes: int) -> int:
+    return load().fa_packed_bwd_validate(q, k, v, o, dout, lse, dq, dk, dv, cu_q, cu_k, B, T_q, T_k, H, H_kv, d, scale,
+                                         dtype, workspace, workspace_bytes)
+
+
+def fa_packed_bwd_workspace_size(B: int, T_q: int, H: int, d: int) -> int:
+    return int(load().fa_packed_bwd_workspace_size(B, T_q, H, d))
 
 
 def fa_device_status(stream: int | None) -> int:

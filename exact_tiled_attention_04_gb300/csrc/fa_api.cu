@@ -169,6 +169,33 @@ int encode_map(CUtensorMap* map, const void* base, int dtype, int64_t BH, int64_
     return FA_OK;
 }
 
+int encode_strided(CUtensorMap* map, const void* base, int dtype, int rank, const int64_t* dims, const int64_t* strides,
+                   const uint32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (enc == nullptr) {
+        set_error("cudaGetDriverEntryPointByVersion(cuTensorMapEncodeTiled)",
+                  static_cast<int>(g_encode_err), cudaGetErrorString(g_encode_err));
+        return FA_ERR_CUDA;
+    }
+    cuuint64_t n[5], bytes[4];
+    cuuint32_t b[5], step[5];
+    for (int i = 0; i < rank; ++i) {
+        n[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = i == 0 ? 64u : box[i];
+        step[i] = 1;
+        if (i > 0) bytes[i - 1] = static_cast<cuuint64_t>(strides[i]) * 2;
+    }
+    const CUresult r = enc(map, dtype == FA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           static_cast<cuuint32_t>(rank), const_cast<void*>(base), n, bytes, b, step,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled", static_cast<int>(r), "tensor map rejected");
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
 }  // namespace host
 }  // namespace fa
 

@@ -72,6 +72,8 @@
 #include <cstdint>
 
 #include "fa_bwd_internal.h"
+#include "fa_packed.cuh"
+#include "fa_packed.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -156,7 +158,7 @@ struct BwdCfg {
     static constexpr int kBarStagedDO = kBarStaged + kStages;  // [kStages] read-out layout: [d/2, d), in the dO tile (4)
     static constexpr int kNumBars = kBarStagedDO + kStages;
     // barriers, TMEM slot and abort flag
-    static constexpr int kCtrlBytes = kNumBars * 8 + 8;
+    static constexpr int kCtrlBytes = kNumBars * 8 + 8 + 32;  // (32: the SeqBlock of a packed launch)
     // The control block lives in whichever alignment gap holds it: below the
     // 1024-aligned base when the slack there is large enough, else after the
     // tiles, so the launch needs only the tiles plus 1 KB.
@@ -258,12 +260,20 @@ __device__ __forceinline__ void bwd_tmem_ld_wait16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-template <int D, bool F16, bool kCausal>
+// Orders what another kernel wrote to a tensor map in global memory ahead of
+// this thread's tensor copies by it.
+__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map))
+                 : "memory");
+}
+
+// kPacked: the key block is one of packed sequences (PackedBwdParams).
+template <int D, bool F16, bool kCausal, bool kPacked = false, class Params = BwdParams>
 __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>::kThreads), 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                   const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv,
-                  const __grid_constant__ CUtensorMap map_dq, const BwdParams p) {
+                  const __grid_constant__ CUtensorMap map_dq, const Params p) {
     constexpr bool kRead = bwd_read_layout<D, kCausal>();
     using C = BwdCfg<D, F16, kRead>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -282,26 +292,36 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
     // heaviest first, by groups of units; otherwise blockIdx.x = unit *
     // n_kv_blocks + kb.
     int kb, unit;
-    if (kCausal) {
+    if constexpr (kPacked) {
+        kb = unit = 0;  // found on the device, below
+    } else if (kCausal) {
         lpt_item(blockIdx.x, static_cast<int>(gridDim.x) / p.n_kv_blocks, p.n_kv_blocks, unit, kb);
     } else {
         kb = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.n_kv_blocks));
         unit = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.n_kv_blocks));
     }
-    const int b = unit / p.H_kv;
-    const int kvh = unit % p.H_kv;
+    int b = unit / p.H_kv;
+    int kvh = unit % p.H_kv;
+    int n_q_tiles = p.n_q_tiles, n_kv = p.Nkv, causal_offset = p.causal_offset;
+    // first tile of a query head's statistics and first row of its accumulator
+    [[maybe_unused]] int pad_tile = 0;
+    const CUtensorMap *pm_q = &map_q, *pm_k = &map_k, *pm_v = &map_v, *pm_do = &map_do, *pm_dk = &map_dk,
+                      *pm_dv = &map_dv;
     // Query tiles that see a key of this block: all, or under the causal mask
     // those holding a row i >= kb*128 - causal_offset (query i sees key j iff
     // j <= i + causal_offset).  The last query row sees every key, so at
     // least one tile remains.
-    int qt_begin = 0;
-    if (kCausal) {
-        const long long first_i = static_cast<long long>(kb) * 128 - p.causal_offset;
-        qt_begin = first_i <= 0 ? 0 : static_cast<int>(min(first_i / 128, static_cast<long long>(p.n_q_tiles)));
-    }
-    const int nqt = p.n_q_tiles - qt_begin;
-    const int T = p.group * nqt;  // (query head, query tile) pairs swept by this CTA
-    const bool has_work = T > 0;
+    int qt_begin, nqt, T;
+    auto plan = [&]() {
+        qt_begin = 0;
+        if (kCausal) {
+            const long long first_i = static_cast<long long>(kb) * 128 - causal_offset;
+            qt_begin = first_i <= 0 ? 0 : static_cast<int>(min(first_i / 128, static_cast<long long>(n_q_tiles)));
+        }
+        nqt = n_q_tiles - qt_begin;
+        T = p.group * nqt;  // (query head, query tile) pairs swept by this CTA
+    };
+    plan();
 
     auto bar = [&](int i) -> uint32_t { return ctrl_u32 + 8u * static_cast<uint32_t>(i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + C::kNumBars * 8);
@@ -334,21 +354,57 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         mbar_init_fence();
     }
     if (warp == kBwdLoadWarp && lane == 0) {
-        tma_prefetch_desc(&map_q);
-        tma_prefetch_desc(&map_k);
-        tma_prefetch_desc(&map_v);
-        tma_prefetch_desc(&map_do);
+        if constexpr (!kPacked) {
+            tma_prefetch_desc(&map_q);
+            tma_prefetch_desc(&map_k);
+            tma_prefetch_desc(&map_v);
+            tma_prefetch_desc(&map_do);
+        }
         tma_prefetch_desc(&map_dq);
     }
     if (warp == kBwdMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), kBwdTmemCols);
         tmem_relinquish();
     }
+    [[maybe_unused]] int* const block_info = reinterpret_cast<int*>(ctrl + C::kNumBars * 8 + 8);
+    if constexpr (kPacked) {
+        if (warp == kBwdReduceWarp) {
+            int head;
+            const SeqBlock blk = find_block<true>(p.seqs, 128, p.H_kv, blockIdx.x, head);
+            if (lane == 0) {
+                block_info[0] = blk.s;
+                block_info[1] = blk.r;
+                block_info[2] = blk.nq;
+                block_info[3] = blk.nk;
+                block_info[4] = blk.base;
+                block_info[5] = head;
+            }
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const bool skip = *abort_flag != 0u;
+    bool skip = *abort_flag != 0u;
+    if constexpr (kPacked) {
+        kb = block_info[1];
+        skip = skip || kb < 0;  // the grid is as large as any lengths need
+        n_q_tiles = (block_info[2] + 127) / 128;
+        n_kv = block_info[3];
+        causal_offset = n_kv - block_info[2];
+        pad_tile = block_info[4] / 128;
+        b = 0;
+        unit = kvh = block_info[5];
+        const CUtensorMap* maps = p.maps + (kb < 0 ? 0 : block_info[0]) * kPackedMaps;
+        pm_q = maps + kMapQ;
+        pm_k = maps + kMapK;
+        pm_v = maps + kMapV;
+        pm_do = maps + kMapDout;
+        pm_dk = maps + kMapDk;
+        pm_dv = maps + kMapDv;
+        plan();
+    }
+    const bool has_work = T > 0;
 
     if (skip) {
         // nothing issued: go straight to the teardown
@@ -409,11 +465,17 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         if (lane == 0) {
             const uint64_t keep = policy_evict_last();   // Q, dO, stats: read by every key block of the head
             const uint64_t once = policy_evict_first();  // K, V: read once
+            if constexpr (kPacked) {
+                acquire_map(pm_k);
+                acquire_map(pm_v);
+                acquire_map(pm_q);
+                acquire_map(pm_do);
+            }
             mbar_arrive_expect_tx(bar(C::kBarKV), 2u * C::kTileBytes);
             for (int a = 0; a < C::kAtoms; ++a) {
-                tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, &map_k, bar(C::kBarKV), a * C::kAtomElems,
+                tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, pm_k, bar(C::kBarKV), a * C::kAtomElems,
                             kb * 128, unit, once);
-                tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, &map_v, bar(C::kBarKV), a * C::kAtomElems,
+                tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, pm_v, bar(C::kBarKV), a * C::kAtomElems,
                             kb * 128, unit, once);
             }
             int issued_q = 0, issued_do = 0;
@@ -426,17 +488,17 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
                 if (!bwd_wait(bar(C::kBarEmpty + s), ph, abort_flag, p, 31)) break;
                 mbar_arrive_expect_tx(bar(C::kBarFull + s), C::kTileBytes + kBwdStatBytes);
                 for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q,
+                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, pm_q,
                                 bar(C::kBarFull + s), a * C::kAtomElems, qt * 128, bh, keep);
                 bulk_load(sbase + C::kOffStats + s * kBwdStatBytes,
-                          p.stats + (static_cast<size_t>(bh) * (p.Nq_pad / 128) + static_cast<size_t>(qt)) *
+                          p.stats + (static_cast<size_t>(bh) * (p.Nq_pad / 128) + static_cast<size_t>(pad_tile + qt)) *
                                         kStatFloatsPerTile,
                           kBwdStatBytes, bar(C::kBarFull + s), keep);
                 issued_q = it + 1;
                 if (!bwd_wait(bar(C::kBarEmptyDO + s), ph, abort_flag, p, 31)) break;
                 mbar_arrive_expect_tx(bar(C::kBarFullDO + s), C::kTileBytes);
                 for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, &map_do,
+                    tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, pm_do,
                                 bar(C::kBarFullDO + s), a * C::kAtomElems, qt * 128, bh, keep);
                 issued_do = it + 1;
             }
@@ -479,7 +541,8 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
                     const uint32_t stg = sbase + (w == 0 ? C::kOffQ : C::kOffDO) + s * C::kTileBytes;
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h)
-                        tma_reduce_add_3d(&map_dq, stg + h * C::kAtomBytes, w * (D / 2) + 32 * h, qt * 128, bh);
+                        tma_reduce_add_3d(&map_dq, stg + h * C::kAtomBytes, w * (D / 2) + 32 * h,
+                                          (pad_tile + qt) * 128, bh);
                     tma_store_commit();  // one group per half
                 }
                 if (!got) break;
@@ -623,7 +686,7 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         const uint32_t tDP = tmem + lane_off + C::kColDP + 64u * static_cast<uint32_t>(w);
         [[maybe_unused]] const uint32_t tDQ = tmem + lane_off + C::kColDQ + static_cast<uint32_t>(w * (D / 2));
         const long long key = static_cast<long long>(kb) * 128 + t;
-        const bool key_valid = key < p.Nkv;  // rows past Nkv were zero-filled: weight 0
+        const bool key_valid = key < n_kv;  // rows past Nkv were zero-filled: weight 0
         const float c = p.scale_log2;
         bool ok = true;
         uint32_t x[2][32];  // P^T of the current tile in fp32: this key, 64 query columns
@@ -647,7 +710,7 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
             // causal: query column q (index qt*128 + q) sees this key iff q >= thr
             int thr = 0;
             if (kCausal) {
-                const long long v = key - p.causal_offset - static_cast<long long>(qt) * 128;
+                const long long v = key - causal_offset - static_cast<long long>(qt) * 128;
                 thr = static_cast<int>(v < -1 ? -1 : (v > 129 ? 129 : v));
             }
             const uint64_t c2 = f2_pack(c, c);
@@ -807,7 +870,8 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         if (t == 0) {
             const bool all_in = bwd_wait(bar(C::kBarEpi + w), 0, abort_flag, p, 45);
             if (all_in && !*abort_flag) {
-                const CUtensorMap* map = (w == 0) ? &map_dv : &map_dk;
+                const CUtensorMap* map = (w == 0) ? pm_dv : pm_dk;
+                if constexpr (kPacked) acquire_map(map);
                 for (int a = 0; a < C::kAtoms; ++a)
                     tma_store_3d(map, smem_u32(stage + a * C::kAtomBytes), a * C::kAtomElems, kb * 128, unit);
                 tma_store_commit();
@@ -823,6 +887,22 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         tc_fence_after();
         tmem_dealloc(tmem, kBwdTmemCols);
     }
+}
+
+// Packed sequences: `grid` CTAs, enough for any lengths.  p.Nq_pad is 128 p.tiles.
+template <int D, bool F16, bool kCausal>
+cudaError_t launch_packed_bwd_variant(const CUtensorMap& dq, const PackedBwdParams& p, unsigned int grid,
+                                      cudaStream_t stream) {
+    using C = BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>;
+    auto kern = fa_bwd_kernel<D, F16, kCausal, true, PackedBwdParams>;
+    cudaFuncAttributes attr;  // see launch_bwd_variant
+    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != static_cast<int>(C::kLaunchRegs)) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(dq, dq, dq, dq, dq, dq, dq, p);
+    return cudaGetLastError();
 }
 
 template <int D, bool F16, bool kCausal>

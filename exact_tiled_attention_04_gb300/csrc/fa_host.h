@@ -49,5 +49,10 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb);
 int encode_map(CUtensorMap* map, const void* base, int dtype, int64_t BH, int64_t N, int64_t d,
                uint32_t box_rows = 128, uint32_t box_heads = 1);
 
+// The same with any strides: 16-bit elements, dims (d, ..), strides in elements
+// of every dimension but the first, boxes of 64 elements x box[1] x ..
+int encode_strided(CUtensorMap* map, const void* base, int dtype, int rank, const int64_t* dims, const int64_t* strides,
+                   const uint32_t* box);
+
 }  // namespace host
 }  // namespace fa

@@ -501,6 +501,85 @@ int fa_fwd_weights_validate(const void* q, const void* k, const float* lse, cons
                             const float* weight_out, int64_t weight_stride, int64_t B, int64_t H, int64_t H_kv,
                             int64_t N_q, int64_t N_kv, int64_t d, int64_t first_query, float scale, int dtype);
 
+/* ------------------------------------------------------------------------
+ * Attention over packed sequences.
+ *
+ * A batch of sequences of different lengths, their rows one behind the other
+ * without padding: sequence s has query rows cu_q[s] .. cu_q[s + 1] - 1 of a
+ * [T_q, H, d] tensor and key/value rows cu_k[s] .. cu_k[s + 1] - 1 of a
+ * [T_k, H_kv, d] one.  The attention and its gradients are those of fa_fwd_ex
+ * and fa_bwd within each sequence; the pages have no counterpart of the layout.
+ *
+ * A view of such a tensor: rows and heads may lie apart (q, k and v as slices
+ * of one projection's output), the d elements of a row are contiguous.
+ */
+typedef struct {
+    void* data;          /* row 0 of head 0, 16-byte aligned (NULL only where the view has no rows) */
+    int64_t row_stride;  /* elements from a row to the next one of its head, a multiple of 8 */
+    int64_t head_stride; /* elements from a head's row to the next head's, a multiple of 8 */
+} fa_rows_t;
+
+/*
+ * fa_packed_fwd — O = softmax(scale Q K^T) V and lse, sequence by sequence.
+ *
+ *   q, o       : views of T_q rows and H heads;  k, v: of T_k rows and H_kv
+ *                heads (H_kv divides H; query head h reads h / (H / H_kv)).
+ *                No two rows of a view overlap: either all heads of a row come
+ *                before the next row, or all rows of a head before the next.
+ *   lse        : fp32 [H, T_q], natural log, or NULL.
+ *   cu_q, cu_k : int32 [B + 1] on the device, read there: not decreasing, from 0
+ *                or above up to T_q (T_k) or below; cu_k may be cu_q.  (Other
+ *                values are clamped to that: no row outside the tensors is read
+ *                or written, but what is computed is not defined.)
+ *   B >= 1; T_q, T_k >= 0, T_q + 128 B and T_k + 128 B below 2^31.
+ *   dtype      : FA_DTYPE_BF16 or FA_DTYPE_F16, optionally FA_FLAG_CAUSAL: of a
+ *                sequence with n_q queries and n_k keys, query i sees keys
+ *                j <= i + n_k - n_q.  d: 64 or 128.
+ * A query that sees no key gets O = 0 and lse = -inf.  Rows of o and lse that
+ * belong to no sequence are left as they were, and whatever the rows of other
+ * sequences or of none hold (infinities, NaN) does not enter a sequence's
+ * results.  Within a sequence, an infinity or a NaN in a value row may reach
+ * queries up to 127 rows before it that do not see it.  o overlaps no input.
+ * Results do not depend on the order in which blocks run.  One kernel; no workspace.
+ */
+int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const fa_rows_t* o, float* lse,
+                  const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t T_q, int64_t T_k, int64_t H,
+                  int64_t H_kv, int64_t d, float scale, int dtype, void* stream);
+
+/*
+ * fa_packed_bwd — gradients of fa_packed_fwd: views dq of T_q rows and H heads,
+ * dk and dv of T_k rows and H_kv heads, from the forward's o and lse and the
+ * upstream gradient dout.  Arguments as in fa_packed_fwd; dk and dv sum over the
+ * query heads that share a key/value head.
+ *   workspace : fa_packed_bwd_workspace_size(...) bytes, 16-byte aligned;
+ *               nothing in it needs to be zeroed.  Calls (and replays of
+ *               captured ones) that may run at once need one each.
+ * Rows of dq, dk and dv that belong to no sequence are left as they were; keys
+ * that no query sees get zeros.  Non-finite rows of o, dout, q, k or v stay in
+ * their sequence, as above.  dq, dk, dv and the workspace overlap no input and
+ * not each other (slices of one tensor are fine).  dQ is summed over the key
+ * blocks in fp32 in an order that may change from call to call, as in fa_bwd;
+ * dk and dv repeat bit for bit.  Three kernels.
+ */
+int fa_packed_bwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const fa_rows_t* o,
+                  const fa_rows_t* dout, const float* lse, const fa_rows_t* dq, const fa_rows_t* dk,
+                  const fa_rows_t* dv, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t T_q,
+                  int64_t T_k, int64_t H, int64_t H_kv, int64_t d, float scale, int dtype, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Workspace bytes fa_packed_bwd needs (0 for invalid sizes). */
+size_t fa_packed_bwd_workspace_size(int64_t B, int64_t T_q, int64_t H, int64_t d);
+
+/* The host-side argument checks of the two calls, alone; no CUDA call. */
+int fa_packed_fwd_validate(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const fa_rows_t* o,
+                           const float* lse, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t T_q,
+                           int64_t T_k, int64_t H, int64_t H_kv, int64_t d, float scale, int dtype);
+int fa_packed_bwd_validate(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const fa_rows_t* o,
+                           const fa_rows_t* dout, const float* lse, const fa_rows_t* dq, const fa_rows_t* dk,
+                           const fa_rows_t* dv, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t T_q,
+                           int64_t T_k, int64_t H, int64_t H_kv, int64_t d, float scale, int dtype,
+                           const void* workspace, size_t workspace_bytes);
+
 /*
  * fa_device_status — synchronise `stream`, then read and clear the device
  * error word the kernels set when a bounded wait gives up or a 4-bit cache
