@@ -28,10 +28,12 @@ FA_ERR_ALIGNMENT = 3
 FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
 FA_ERR_CAPACITY = 6
+FA_ERR_RANGE = 7
 FA_DTYPE_F32 = 0
 FA_DTYPE_BF16 = 1
 FA_DTYPE_F16 = 2
 FA_FLAG_CAUSAL = 0x100
+FA_FLAG_INTERLEAVED = 0x200
 
 _lock = threading.Lock()
 _lib = None
@@ -46,6 +48,12 @@ class fa_kv4_cache_t(ctypes.Structure):
 class fa_rows_t(ctypes.Structure):
     """The C struct of include/fa.h: a view of [rows, heads, d] (address, strides in elements)."""
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class fa_paged_cache_t(ctypes.Structure):
+    """The C struct of include/fa.h (device addresses and sizes)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "block_table", "lengths")] \
+        + [(n, ctypes.c_int64) for n in ("num_pages", "page_size", "B", "max_pages", "H_kv", "d")]
 
 
 class FAError(RuntimeError):
@@ -126,13 +134,15 @@ def load(path: str | None = None):
         lib.fa_bwd_host.argtypes = bwd_args + [vp]
         lib.fa_bwd_host_workspace_size.restype = sz
         lib.fa_bwd_host_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64]
-        cp, rp = ctypes.POINTER(fa_kv4_cache_t), ctypes.POINTER(fa_rows_t)
+        cp, rp, gp = (ctypes.POINTER(t) for t in (fa_kv4_cache_t, fa_rows_t, fa_paged_cache_t))
         for name, args in (("fa_kv4_append", [cp, vp, vp, i64, c_int, vp]),
                            ("fa_kv4_read", [cp, vp, i64, vp, vp, c_int]),
                            ("fa_kv4_fwd", [cp, vp, vp, vp, vp, i64, i64, f32, c_int, vp, sz]),
                            ("fa_kv4_evict", [cp, i64, i64, i64, vp, cp, vp, vp]),
                            ("fa_fwd_weights", [vp] * 5 + [i64] * 8 + [f32, c_int]),
                            ("fa_packed_fwd", [rp] * 4 + [vp] * 3 + [i64] * 6 + [f32, c_int]),
+                           ("fa_paged_append", [gp, rp, rp, vp, i64, rp, rp, i64, rp, vp, i64, i64, vp, i64, vp, c_int]),
+                           ("fa_paged_fwd", [gp, vp, vp, vp, i64, i64, vp, i64, f32, c_int, vp, sz]),
                            ("fa_packed_bwd", [rp] * 5 + [vp] + [rp] * 3 + [vp] * 2 + [i64] * 6 + [f32, c_int, vp, sz])):
             getattr(lib, name).restype = c_int
             getattr(lib, name).argtypes = args + [vp]
@@ -140,6 +150,8 @@ def load(path: str | None = None):
             getattr(lib, name + "_validate").argtypes = args
         lib.fa_kv4_fwd_workspace_size.restype = sz
         lib.fa_kv4_fwd_workspace_size.argtypes = [i64] * 6 + [c_int]
+        lib.fa_paged_fwd_workspace_size.restype = sz
+        lib.fa_paged_fwd_workspace_size.argtypes = [i64] * 7
         lib.fa_packed_bwd_workspace_size.restype = sz
         lib.fa_packed_bwd_workspace_size.argtypes = [i64] * 4
         _lib = lib
@@ -335,6 +347,38 @@ def fa_packed_bwd_validate(q, k, v, o, dout, lse: int, dq, dk, dv, cu_q: int, cu
 
 def fa_packed_bwd_workspace_size(B: int, T_q: int, H: int, d: int) -> int:
     return int(load().fa_packed_bwd_workspace_size(B, T_q, H, d))
+
+
+def fa_paged_append(cache, k, v, cu: int | None, T: int, q, q_out, H: int, k_out, table: int | None, table_rows: int,
+                    rot: int, positions: int | None, first_position: int, lengths_out: int, dtype: int,
+                    stream: int | None) -> int:
+    """`cache` here and below: an fa_paged_cache_t (None for a NULL pointer)."""
+    return load().fa_paged_append(cache, k, v, cu or None, T, q, q_out, H, k_out, table or None, table_rows, rot,
+                                  positions or None, first_position, lengths_out, dtype, stream or None)
+
+
+def fa_paged_append_validate(cache, k, v, cu: int | None, T: int, q, q_out, H: int, k_out, table: int | None,
+                             table_rows: int, rot: int, positions: int | None, first_position: int, lengths_out: int,
+                             dtype: int) -> int:
+    return load().fa_paged_append_validate(cache, k, v, cu or None, T, q, q_out, H, k_out, table or None, table_rows,
+                                           rot, positions or None, first_position, lengths_out, dtype)
+
+
+def fa_paged_fwd(cache, q: int, o: int, lse: int | None, H: int, N_q: int, prefix_pages: int | None,
+                 prefix_length: int, scale: float, dtype: int, workspace: int, workspace_bytes: int,
+                 stream: int | None) -> int:
+    return load().fa_paged_fwd(cache, q, o, lse or None, H, N_q, prefix_pages or None, prefix_length, scale, dtype,
+                               workspace, workspace_bytes, stream or None)
+
+
+def fa_paged_fwd_validate(cache, q: int, o: int, lse: int | None, H: int, N_q: int, prefix_pages: int | None,
+                          prefix_length: int, scale: float, dtype: int, workspace: int, workspace_bytes: int) -> int:
+    return load().fa_paged_fwd_validate(cache, q, o, lse or None, H, N_q, prefix_pages or None, prefix_length, scale,
+                                        dtype, workspace, workspace_bytes)
+
+
+def fa_paged_fwd_workspace_size(B: int, H: int, H_kv: int, N_q: int, capacity: int, d: int, prefix_length: int) -> int:
+    return int(load().fa_paged_fwd_workspace_size(B, H, H_kv, N_q, capacity, d, prefix_length))
 
 
 def fa_device_status(stream: int | None) -> int:

@@ -28,7 +28,7 @@ SOURCES = ["fa_api.cu", "fa_fwd_bf16.cu", "fa_fwd_f16.cu", "fa_fwd_tf32.cu", "fa
            "fa_bwd_api.cu", "fa_bwd_bf16.cu", "fa_bwd_f16.cu", "fa_bwd_aux.cu", "fa_pipeline.cu",
            "fa_dec_bf16.cu", "fa_dec_f16.cu", "fa_kv4_api.cu", "fa_kv4_store.cu", "fa_kv4_fwd.cu",
            "fa_kv4_evict.cu", "fa_weights.cu", "fa_packed_api.cu", "fa_packed_aux.cu", "fa_packed_bf16.cu",
-           "fa_packed_f16.cu"]
+           "fa_packed_f16.cu", "fa_paged_api.cu", "fa_paged_store.cu", "fa_paged_bf16.cu", "fa_paged_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

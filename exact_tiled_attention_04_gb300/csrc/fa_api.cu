@@ -218,7 +218,8 @@ const char* fa_status_string(int status) {
         case FA_ERR_ALIGNMENT: return "tensor base address not 16-byte aligned";
         case FA_ERR_CUDA: return "CUDA call failed";
         case FA_ERR_TIMEOUT: return "kernel timed out waiting on an internal barrier";
-        case FA_ERR_CAPACITY: return "4-bit cache full: appended rows were dropped";
+        case FA_ERR_CAPACITY: return "key/value cache full: appended rows were dropped";
+        case FA_ERR_RANGE: return "page number or position outside its range";
         default: return "unknown status";
     }
 }
@@ -710,7 +711,8 @@ int fa_device_status(void* stream) {
     }
     std::snprintf(g_last_error, sizeof(g_last_error), "device error word 0x%08x", st.word);
     if (st.word & fa::kDevErrTimeout) return FA_ERR_TIMEOUT;
-    return (st.word & fa::kDevErrCapacity) ? FA_ERR_CAPACITY : FA_ERR_CUDA;
+    if (st.word & fa::kDevErrCapacity) return FA_ERR_CAPACITY;
+    return (st.word & fa::kDevErrRange) ? FA_ERR_RANGE : FA_ERR_CUDA;
 }
 
 int fa_selftest_barrier_timeout(void* stream) {

@@ -62,6 +62,7 @@
 #include "fa_internal.h"
 #include "fa_packed.cuh"
 #include "fa_packed.h"
+#include "fa_paged.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -69,7 +70,7 @@ namespace fa {
 // What a launch's query blocks are (kMode): blocks of a [B, H, N, d] tensor,
 // of packed sequences (PackedFwdParams), or the rows that several sequences
 // have for one key/value head, over the pages of a prefix (PrefixFwdParams).
-constexpr int kModeBatch = 0, kModePacked = 1;
+constexpr int kModeBatch = 0, kModePacked = 1, kModePrefix = 2;
 
 constexpr int kTileM = 128;  // query rows per softmax warpgroup = TMEM lanes
 constexpr int kTileN = 128;  // keys per K/V tile
@@ -802,6 +803,78 @@ __device__ __forceinline__ void produce_packed(const CUtensorMap& map_q, const C
     }
 }
 
+// Producer warp of a prefix launch: query rows of several sequences, keys and
+// values page by page (a box per lane).  Value rows behind the prefix's end, in
+// its last page or in pages that are not loaded, are zeroed as above.
+template <int D, bool F16, bool kOneTile>
+__device__ __forceinline__ void produce_prefix(const CUtensorMap& map_q, const CUtensorMap& map_k,
+                                               const CUtensorMap& map_v, const PrefixFwdParams& p, uint8_t* smem,
+                                               uint32_t sbase, int lane, int seq0, int kvh, int t_begin, int T,
+                                               volatile uint32_t* abort_flag) {
+    using C = FwdCfg<false, D, F16>;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(i); };
+    constexpr int kTiles = kOneTile ? 1 : 2;
+    const uint64_t keep = policy_evict_last();
+    const int end = p.Nkv - (t_begin + T - 1) * kTileN;  // keys of the last tile
+    const bool tail = end < kTileN;
+    const int per_tile = kTileN / p.page, mine = lane / C::kAtoms, atom = lane % C::kAtoms;
+    if (lane == 0) {
+        mbar_arrive_expect_tx(bar(C::kBarQFull), static_cast<uint32_t>(kTiles * C::kAtoms * p.rows * p.seqs * 128));
+        for (int w = 0; w < kTiles; ++w)
+            for (int a = 0; a < C::kAtoms; ++a)
+                tma_load_4d(sbase + C::kOffQ + w * C::kTileBytes + a * C::kAtomBytes, &map_q, bar(C::kBarQFull),
+                            a * C::kAtomElems, 0, kvh, seq0 + w * p.seqs, keep);
+    }
+    int nk = 0, nv = 0;  // K and V tiles whose loads were issued
+    for (int j = 0; j < T; ++j) {
+        const int page0 = (t_begin + j) * per_tile, have = min(per_tile, p.n_pages - page0);
+        const int id = mine < have ? p.pages[page0 + mine] : 0;
+        const uint32_t bytes = static_cast<uint32_t>(have * p.page * C::kAtoms * 128);
+        const int ks = j % C::kKStages, vs = j % C::kVStages;
+        if (!__all_sync(0xffffffffu, wait_phase(bar(C::kBarKEmpty + ks), ((j / C::kKStages) & 1) ^ 1, abort_flag, p, 1)))
+            break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarKFull + ks), bytes);
+        __syncwarp();
+        if (mine < have)
+            tma_load_4d(sbase + C::kOffK + ks * C::kTileBytes + atom * C::kAtomBytes + mine * p.page * 128, &map_k,
+                        bar(C::kBarKFull + ks), atom * C::kAtomElems, 0, kvh, id, keep);
+        nk = j + 1;
+        if (!__all_sync(0xffffffffu, wait_phase(bar(C::kBarVEmpty + vs), ((j / C::kVStages) & 1) ^ 1, abort_flag, p, 2)))
+            break;
+        const uint32_t vbar = tail && j + 1 == T ? bar(C::kBarVRaw) : bar(C::kBarVFull + vs);
+        if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
+        __syncwarp();
+        if (mine < have)
+            tma_load_4d(sbase + C::kOffV + vs * C::kTileBytes + atom * C::kAtomBytes + mine * p.page * 128, &map_v, vbar,
+                        atom * C::kAtomElems, 0, kvh, id, keep);
+        nv = j + 1;
+    }
+    __syncwarp();
+    if (tail && nv == T) {
+        const int vs = (T - 1) % C::kVStages;
+        if (__all_sync(0xffffffffu, wait_phase(bar(C::kBarVRaw), 0, abort_flag, p, 3, false))) {
+            for (int a = 0; a < C::kAtoms; ++a) {
+                uint4* rows = reinterpret_cast<uint4*>(smem + C::kOffV + vs * C::kTileBytes + a * C::kAtomBytes);
+                for (int i = end * 8 + lane; i < kTileN * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarVFull + vs));
+        }
+    }
+    if (lane == 0) {
+        wait_phase(bar(C::kBarQFull), 0, abort_flag, p, 3, false);
+        for (int s = 0; s < C::kKStages && s < nk; ++s) {
+            const int last = s + ((nk - 1 - s) / C::kKStages) * C::kKStages;
+            wait_phase(bar(C::kBarKFull + s), (last / C::kKStages) & 1, abort_flag, p, 3, false);
+        }
+        for (int s = 0; s < C::kVStages && s < nv; ++s) {
+            const int last = s + ((nv - 1 - s) / C::kVStages) * C::kVStages;
+            wait_phase(bar(C::kBarVFull + s), (last / C::kVStages) & 1, abort_flag, p, 3, false);
+        }
+    }
+}
+
 // kOneTile: a packed launch (p.pack = 1), where query tile 1 holds no row;
 // a template parameter so that unpacked launches carry none of its checks.
 template <bool TF32, int D, bool F16 = false, bool kCausal = false, bool kOneTile = false, int kMode = kModeBatch,
@@ -822,13 +895,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // blockIdx.x = cta * splits + split; cta = bh * n_q_blocks + qb, or
     // (causal) the heavy-first order of lpt_item over (bh, block)
     // grouped heads packed into query tile 0 (p.pack; always set when kOneTile)
-    const bool pack = kOneTile || p.pack != 0;
+    const bool pack = kMode == kModeBatch && (kOneTile || p.pack != 0);
     const unsigned int split = blockIdx.x % static_cast<unsigned>(p.splits);
     // (a tail launch starts at query block p.item_offset; unmasked launches only)
     const unsigned int cta = blockIdx.x / static_cast<unsigned>(p.splits) + static_cast<unsigned>(p.item_offset);
     int qb, bh;
     if constexpr (kMode == kModePacked) {
         qb = bh = 0;  // found on the device, below
+    } else if constexpr (kMode == kModePrefix) {
+        qb = static_cast<int>(cta % static_cast<unsigned>(p.blocks));  // of the sequences
+        bh = static_cast<int>(cta / static_cast<unsigned>(p.blocks));  // the key/value head
     } else if (kCausal) {
         // later query blocks see more keys: heaviest first, by groups of heads
         // (packed launches have one block per key/value head)
@@ -850,6 +926,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warpgroup sit out, and K/V stages are released by tile 0 alone
     constexpr bool one_tile = kOneTile;
     int row0 = qb * 2 * kTileM;
+    if constexpr (kMode == kModePrefix) {
+        kvh = bh;
+        row0 = 0;
+    }
+    // prefix launches: the first sequence of tile 0
+    [[maybe_unused]] int seq0 = 0;
+    if constexpr (kMode == kModePrefix) seq0 = qb * (kOneTile ? 1 : 2) * p.seqs;
     // key tiles this query block can see: all, or under the causal mask
     // those up to the last key its last row sees
     int n_tiles_block = p.n_kv_tiles;
@@ -972,7 +1055,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (the split last wave) may place its CTAs as this grid's leave the SMs
         if (lane == 0) asm volatile("griddepcontrol.launch_dependents;");
         if (!TF32 && pack) zero_unloaded_q<C::kTileBytes, C::kAtoms, C::kAtomBytes>(smem + C::kOffQ, pack_rows, lane);
-        if constexpr (kMode == kModePacked) {
+        if constexpr (kMode == kModePrefix) {
+            produce_prefix<D, F16, kOneTile>(map_q, map_k, map_v, p, smem, sbase, lane, seq0, kvh, t_begin, T, abort_flag);
+        } else if constexpr (kMode == kModePacked) {
             produce_packed<D, F16>(map_q, map_k, map_v, p, smem, sbase, lane, blk, row0, bh, kvh, T, abort_flag);
         } else if constexpr (TF32) {
             produce_tf32<D>(map_q, map_k, map_v, p, smem, sbase, lane, row0, bh, kvh, t_begin, T, abort_flag);
@@ -1172,6 +1257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = row0 + w * p.tile_step + t;  // (a sequence's rows fit an int, and so does 255 more)
             out_row = i < blk.nq ? blk.q0 + i : -1;
             row_limit = kCausal ? max(-1, min(blk.nk, i + 1 + blk.nk - blk.nq)) : blk.nk;
+        } else if constexpr (kMode == kModePrefix) {
+            const int b = seq0 + w * p.seqs + t / p.rows;
+            out_row = t < p.rows * p.seqs && b < p.B ? (static_cast<long long>(b) * p.H_kv + kvh) * p.rows + t % p.rows : -1;
         } else if (kCausal) {
             const long long lim = qi + p.causal_offset + 1;
             row_limit = static_cast<int>(max(-1ll, min(static_cast<long long>(p.Nkv), lim)));
@@ -1417,7 +1505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, got);
         }
         uint8_t* stage = smem + C::kOffQ + w * C::kTileBytes;  // Q_w is free after its last S MMA
-        const bool split_mode = p.splits > 1;
+        const bool split_mode = kMode == kModePrefix || p.splits > 1;
         if (ok && split_mode && active) {
             tc_fence_after();
             if (has_work) {
@@ -1566,6 +1654,29 @@ cudaError_t launch_packed_variant(const CUtensorMap& q, const CUtensorMap& k, co
     if (e != cudaSuccess) return e;
     kern<<<grid, kThreads, C::kSmemBytesPacked, stream>>>(q, k, v, q, p);
     return cudaGetLastError();
+}
+
+// Prefix launches.
+template <int D, bool F16, bool kOneTile>
+cudaError_t launch_prefix_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                  const PrefixFwdParams& p, cudaStream_t stream) {
+    using C = FwdCfg<false, D, F16>;
+    auto kern = fa_fwd_kernel<false, D, F16, false, kOneTile, kModePrefix, PrefixFwdParams>;
+    cudaFuncAttributes attr;  // see launch_fwd_variant
+    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    // (launched without overlap: the kernel behind it relies on this one having begun after all before it)
+    kern<<<static_cast<unsigned>(p.H_kv * p.blocks * p.splits), kThreads, C::kSmemBytes, stream>>>(q, k, v, q, p);
+    return cudaGetLastError();
+}
+template <int D, bool F16>
+cudaError_t launch_prefix(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PrefixFwdParams& p,
+                          cudaStream_t stream) {
+    return p.B <= p.seqs ? launch_prefix_variant<D, F16, true>(q, k, v, p, stream)
+                         : launch_prefix_variant<D, F16, false>(q, k, v, p, stream);
 }
 
 template <bool TF32, int D, bool F16, bool kCausal, bool kOneTile>

@@ -65,7 +65,8 @@ struct MergeParams {
 
 // Device error word bits.
 constexpr unsigned int kDevErrTimeout = 1u;
-constexpr unsigned int kDevErrCapacity = 2u;  // rows appended to a full 4-bit cache
+constexpr unsigned int kDevErrCapacity = 2u;  // rows appended to a full cache
+constexpr unsigned int kDevErrRange = 4u;     // a page number or a position outside its range
 
 // A one-CTA kernel that waits, with the forward kernel's bounded wait, on a
 // barrier phase nothing completes; it must give up and report a timeout.

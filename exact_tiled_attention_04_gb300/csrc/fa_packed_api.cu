@@ -8,57 +8,17 @@
 #include "fa_host.h"
 #include "fa_packed.cuh"
 #include "fa_packed.h"
+#include "fa_views.h"
 
 using namespace fa::host;
 
 namespace {
 
 constexpr int64_t kInt32Max = 2147483647;
-constexpr int64_t kMaxStride = int64_t{1} << 38;  // elements; a tensor map's strides are below 2^40 bytes
 
 struct Sizes {
     int64_t B, Tq, Tk, H, H_kv, d;
 };
-
-// A view with the strides that do not matter set to ones that do not disturb.
-struct View {
-    char* data;
-    int64_t row, head;  // strides in elements
-    int64_t rows, heads, d;
-    bool by_row;        // all heads of a row lie before the next row
-
-    size_t span() const { return rows == 0 ? 0 : static_cast<size_t>((rows - 1) * row + (heads - 1) * head + d) * 2; }
-};
-
-int make_view(const fa_rows_t* r, int64_t rows, int64_t heads, int64_t d, View* v) {
-    if (r == nullptr || (r->data == nullptr && rows > 0)) return FA_ERR_INVALID_ARG;
-    *v = View{static_cast<char*>(r->data), r->row_stride, r->head_stride, rows, heads, d, true};
-    if (rows <= 1) v->row = (heads - 1) * (heads > 1 ? v->head : 0) + d;
-    if (heads <= 1) v->head = d;
-    if (v->row < 1 || v->head < 1) return FA_ERR_INVALID_ARG;
-    if (v->row > kMaxStride || v->head > kMaxStride) return FA_ERR_UNSUPPORTED;
-    if (v->row % 8 != 0 || v->head % 8 != 0) return FA_ERR_ALIGNMENT;
-    if (reinterpret_cast<uintptr_t>(v->data) & 15u) return FA_ERR_ALIGNMENT;
-    // (strides below 2^38 and counts below 2^31 may exceed 2^63 together)
-    if ((rows > 1 && v->row > (int64_t{1} << 61) / rows) || (heads > 1 && v->head > (int64_t{1} << 61) / heads))
-        return FA_ERR_INVALID_ARG;
-    v->by_row = rows <= 1 || v->row >= (heads - 1) * v->head + d;
-    if (v->head < d || v->row < d) return FA_ERR_INVALID_ARG;
-    if (!v->by_row && heads > 1 && v->head < (rows - 1) * v->row + d) return FA_ERR_INVALID_ARG;
-    return FA_OK;
-}
-
-// Views with no element in common: their spans do not meet, or both have rows
-// equally far apart and their heads take different parts of a row's distance.
-bool disjoint(const View& a, const View& b) {
-    if (a.rows == 0 || b.rows == 0) return true;
-    if (!overlaps(a.data, a.span(), b.data, b.span())) return true;
-    if (!a.by_row || !b.by_row || a.row != b.row) return false;
-    const int64_t period = a.row * 2, wa = ((a.heads - 1) * a.head + a.d) * 2, wb = ((b.heads - 1) * b.head + b.d) * 2;
-    int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.data) - reinterpret_cast<uintptr_t>(a.data)) % period;
-    if (off < 0) off += period;
-    return off >= wa && off + wb <= period;
-}
 
 int check_sizes(const Sizes& z, float scale, int dtype_arg) {
     if (z.B < 1 || z.Tq < 0 || z.Tk < 0 || z.H < 1 || z.H_kv < 1 || z.d < 1 || z.H % z.H_kv != 0) return FA_ERR_INVALID_ARG;
@@ -66,7 +26,7 @@ int check_sizes(const Sizes& z, float scale, int dtype_arg) {
     const int dtype = dtype_arg & 0xFF;
     if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_F16) return FA_ERR_UNSUPPORTED;
     if (z.d != 64 && z.d != 128) return FA_ERR_UNSUPPORTED;
-    if (z.B > kInt32Max / 256 || z.Tq + 128 * z.B + 256 > kInt32Max || z.Tk + 128 * z.B + 256 > kInt32Max)
+    if (z.B > kInt32Max / 256 || z.Tq > kInt32Max || z.Tk > kInt32Max || z.Tq + 128 * z.B + 256 > kInt32Max || z.Tk + 128 * z.B + 256 > kInt32Max)
         return FA_ERR_UNSUPPORTED;
     // grids: a block of rows per head (blockIdx.y is a head in the backward's small kernels)
     if (z.H > 65535 || z.H * ((z.Tq + z.Tk) / 128 + z.B + 2) > kInt32Max) return FA_ERR_UNSUPPORTED;
@@ -78,10 +38,6 @@ int check_offsets(const int32_t* cu_q, const int32_t* cu_k, const float* lse, bo
     if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) | reinterpret_cast<uintptr_t>(lse)) & 3u)
         return FA_ERR_ALIGNMENT;
     return FA_OK;
-}
-
-bool meets(const View& v, const void* p, size_t n) {
-    return v.rows > 0 && p != nullptr && n > 0 && overlaps(v.data, v.span(), p, n);
 }
 
 // Views of a call: q, o, dout, dq by queries and k, v, dk, dv by keys.

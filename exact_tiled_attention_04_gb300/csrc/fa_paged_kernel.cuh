@@ -1,0 +1,658 @@
+// Attention of short query blocks (decode steps, drafts) over a paged
+// key/value cache, sm_103a: the online softmax of "FlashAttention dissected",
+// section "Algorithmic core in pseudocode", over key partitions (its section
+// "Interaction with the KV cache during inference").
+//
+// The products are those of the decode kernel (fa_decode_kernel.cuh), keys on
+// the tensor-memory lanes:  S^T = K_j Q^T (128 keys x NR rows), P^T = 2^(c S^T -
+// m), O^T += V_j^T P^T, with one reference maximum per row for the warpgroup.
+//
+// What bounds it: reading the cache.  Sequences have different lengths, known
+// on the device alone, so the tiles of all units are cut into equal runs, one
+// per CTA (one CTA an SM): none idles because a sequence is short, and a long
+// one is shared by many.  A CTA goes through the units of its run without a
+// pause: the loading warp is up to a ring ahead, in the next unit's keys while
+// the softmax still ends this one, and Q, S^T and O^T have two buffers each.
+// Of a unit cut between CTAs each leaves a partial result, at most two a CTA,
+// which a second kernel adds up in order, so results do not depend on timing.
+//
+// Pages.  A tile of 128 keys is 128 / page boxes of a tensor map over
+// [pages, H_kv, page, d], one or more per lane of the loading warp.  Pages behind the
+// last one in use are not loaded and a number outside the pool reads as
+// zeros.  Value rows behind a sequence's end hold anything; their weight is 0, but 0 x
+// infinity is not, so the softmax threads zero them in shared memory.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "fa_decode_kernel.cuh"
+#include "fa_paged.h"
+
+namespace fa {
+namespace paged {
+
+template <int D, bool F16, int NR>
+struct Cfg {
+    static constexpr int kAtomElems = 64;
+    static constexpr int kAtoms = D / kAtomElems;
+    static constexpr int kAtomBytes = 128 * 128;            // 128 keys x 128 bytes
+    static constexpr int kTileBytes = kAtoms * kAtomBytes;  // 128 keys x D
+    static constexpr int kRowAtomBytes = NR * 128;          // NR rows x 128 bytes
+    static constexpr int kQBytes = kAtoms * kRowAtomBytes;
+    static constexpr int kUmmaK = 16;
+    static constexpr int kQkSteps = D / kUmmaK;
+    static constexpr int kPvSteps = 128 / kUmmaK;
+    static constexpr int kStages = D == 128 ? 3 : 6;  // K+V stages
+    static constexpr uint32_t kFmt = F16 ? 0u : 1u;
+    static constexpr uint32_t kIdescQK = instr_desc(kFmt, false, false, 128, NR);
+    static constexpr uint32_t kIdescPV = instr_desc(kFmt, true, false, 128, NR);
+    // tensor memory
+    static constexpr uint32_t kColS = 0;       // [2] x NR
+    static constexpr uint32_t kColO = 2 * NR;  // [2] x NR
+    static constexpr uint32_t kTmemCols = 4 * NR;
+    static_assert(kTmemCols == 64 || kTmemCols == 128, "columns are allocated in powers of two");
+    // shared memory; V first: at d = 64 the padded half of V^T is read 16 KB
+    // past a V tile, which stays inside the V and K rings
+    static constexpr int kOffV = 0;                             // [kStages]
+    static constexpr int kOffK = kOffV + kStages * kTileBytes;  // [kStages]
+    static constexpr int kOffQ = kOffK + kStages * kTileBytes;  // [2] x kAtoms x NR rows
+    static constexpr int kOffP = kOffQ + 2 * kQBytes;           // [2] x 2 atoms x NR rows
+    static constexpr int kOffRed = kOffP + 2 * 2 * kRowAtomBytes;  // float [3][4 warps][NR]
+    static constexpr int kOffBar = kOffRed + 3 * 4 * NR * 4;
+    // barriers
+    static constexpr int kBarQFull = 0;                   // [2] a unit's Q landed
+    static constexpr int kBarQEmpty = kBarQFull + 2;      // [2] its last scores are computed
+    static constexpr int kBarFull = kBarQEmpty + 2;       // [kStages] K and V of a tile landed
+    static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] both consumed
+    static constexpr int kBarS = kBarEmpty + kStages;     // [2] S^T buffer ready
+    static constexpr int kBarP = kBarS + 2;               // [2] P^T buffer written (4 warps)
+    static constexpr int kBarPFree = kBarP + 2;           // [2] the product reading it is done
+    static constexpr int kBarO = kBarPFree + 2;           // [2] every product of a unit is done
+    static constexpr int kBarOFree = kBarO + 2;           // [2] its O^T was read (4 warps)
+    static constexpr int kBarDrain = kBarOFree + 2;
+    static constexpr int kNumBars = kBarDrain + 1;
+    static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
+    static constexpr int kOffAbort = kOffTmemSlot + 4;
+    static constexpr int kOffPlan = kOffAbort + 4;        // int [8]: the CTA's run
+    static constexpr int kSmemUsed = kOffPlan + 32;
+    static constexpr size_t kSmemBytes = static_cast<size_t>(kSmemUsed) + 1024;  // alignment slack
+    static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
+    static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "operand tiles must be 1024-byte aligned");
+};
+
+__device__ __forceinline__ int length_of(const PagedCache& c, int b) { return min(max(c.lengths[b], 0), c.capacity); }
+__device__ __forceinline__ int tiles_of(int len) { return (len + 127) / 128; }
+
+// Tiles of a run, all CTAs' alike (the tiles of all units number less than 2^31).
+__device__ __forceinline__ int run_of(int total, int ctas) { return max(1, (total + ctas - 1) / ctas); }
+
+// Tiles of one unit of each of the sequences before `b`, and of all, by one warp.
+struct Spread {
+    int before, total;  // in tiles of one unit each
+    int len;            // of sequence b
+};
+__device__ __forceinline__ Spread spread_of(const PagedCache& c, int b) {
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    int before = 0, total = 0, len = 0;
+    for (int s = lane; s < c.B; s += 32) {
+        const int l = length_of(c, s), n = tiles_of(l);
+        total += n;
+        if (s < b) before += n;
+        if (s == b) len = l;
+    }
+    return {static_cast<int>(__reduce_add_sync(0xffffffffu, before)), static_cast<int>(__reduce_add_sync(0xffffffffu, total)),
+            static_cast<int>(__reduce_max_sync(0xffffffffu, len))};
+}
+
+// Position in a CTA's run: tiles pos .. end - 1 of all units', unit u of
+// sequence b next, from its tile t on.
+struct Cursor {
+    int pos, end, b, u, t, len;
+
+    __device__ __forceinline__ bool valid() const { return pos < end; }
+    __device__ __forceinline__ int tiles() const { return tiles_of(len); }
+    __device__ __forceinline__ int last() const { return min(tiles(), t + end - pos); }  // behind the segment's last tile
+    __device__ __forceinline__ void next(const PagedCache& c, int units) {
+        const int n = last() - t;
+        const bool ended = t + n == tiles();
+        pos += n;
+        t = 0;
+        if (!ended || !valid()) return;
+        if (++u < units) return;
+        u = 0;
+        do len = length_of(c, ++b);
+        while (len == 0);  // (pos < end: a sequence with tiles follows)
+    }
+};
+
+// The run of CTA blockIdx.x, by one warp.
+__device__ __forceinline__ Cursor first_of(const PagedCache& c, int units, int ctas) {
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    const Spread all = spread_of(c, 0);
+    Cursor k{};
+    const int total = all.total * units, run = run_of(total, ctas);
+    const long long pos = static_cast<long long>(blockIdx.x) * run;
+    if (pos >= total) return k;  // pos = end = 0
+    k.pos = static_cast<int>(pos);
+    k.end = min(total - k.pos, run) + k.pos;
+    int left = k.pos;
+    for (int s0 = 0; s0 < c.B; s0 += 32) {
+        const int s = s0 + lane;
+        const int len = s < c.B ? length_of(c, s) : 0;
+        int sum = tiles_of(len) * units;
+        const int mine = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        const unsigned int hit = __ballot_sync(0xffffffffu, left < sum);
+        if (hit != 0u) {
+            const int src = __ffs(static_cast<int>(hit)) - 1;
+            const int in = __shfl_sync(0xffffffffu, left - (sum - mine), src);
+            k.b = s0 + src;
+            k.len = __shfl_sync(0xffffffffu, len, src);
+            k.u = in / tiles_of(k.len);
+            k.t = in % tiles_of(k.len);
+            return k;
+        }
+        left -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return k;
+}
+
+// One CTA per run.  map_q: [B * H_kv, R, d] (d first), boxes of NR rows.
+template <int D, bool F16, bool kCausal, int NR>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    fa_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v, const PagedFwdParams p) {
+    using C = Cfg<D, F16, NR>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_u32 & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw_u32 + pad;
+
+    const int warp = static_cast<int>(threadIdx.x) / 32;
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    const int units = p.c.H_kv * p.row_blocks;  // of a sequence
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(i); };
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
+    int* plan = reinterpret_cast<int*>(smem + C::kOffPlan);
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(C::kBarQFull + b), 1);
+            mbar_init(bar(C::kBarQEmpty + b), 1);
+            mbar_init(bar(C::kBarS + b), 1);
+            mbar_init(bar(C::kBarP + b), 4);
+            mbar_init(bar(C::kBarPFree + b), 1);
+            mbar_init(bar(C::kBarO + b), 1);
+            mbar_init(bar(C::kBarOFree + b), 4);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar(C::kBarFull + s), 1);
+            mbar_init(bar(C::kBarEmpty + s), 1);
+        }
+        mbar_init(bar(C::kBarDrain), 1);
+        *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
+        mbar_init_fence();
+    }
+    if (warp == kDecMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kDecLoadWarp) {
+        if (lane == 0) {
+            tma_prefetch_desc(&map_q);
+            tma_prefetch_desc(&map_k);
+            tma_prefetch_desc(&map_v);
+        }
+        // Lengths, pages and q may come from the kernel before.  Behind a
+        // prefix's kernel, which reads them too and so began after whatever
+        // wrote them, this one waits at its end, for the second kernel's sake.
+        if (!p.parts_always) grid_wait();
+        grid_release();
+        const Cursor k = first_of(p.c, units, p.ctas);
+        if (lane == 0) {
+            plan[0] = k.pos;
+            plan[1] = k.end;
+            plan[2] = k.b;
+            plan[3] = k.u;
+            plan[4] = k.t;
+            plan[5] = k.len;
+        }
+    } else if (!p.parts_always) {
+        grid_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool skip = *abort_flag != 0u;  // an earlier CTA of this launch gave up
+    const Cursor start{plan[0], plan[1], plan[2], plan[3], plan[4], plan[5]};
+
+    if (skip) {
+        // nothing (the device error word already reports the failure)
+    } else if (warp == kDecLoadWarp) {
+        // ---------------------------------------------------------- producer
+        const uint64_t once = policy_evict_first();  // every byte here is read once
+        const int pages = 128 / p.c.page;            // of a tile
+        // this lane's boxes of a tile: a part (K or V, 64 channels) of page `mine` and of every 32 / (2 kAtoms)-th one behind it
+        constexpr int kParts = 2 * C::kAtoms;
+        const int part = lane % kParts, mine = lane / kParts;
+        const bool value = part >= C::kAtoms;
+        const int atom = part % C::kAtoms;
+        const CUtensorMap* map = value ? &map_v : &map_k;
+        const uint32_t dst0 = sbase + (value ? C::kOffV : C::kOffK) + atom * C::kAtomBytes;
+        int it = 0, seg = 0;
+        bool ok = true;
+        for (Cursor k = start; ok && k.valid(); k.next(p.c, units), ++seg) {
+            const int kvh = k.u / p.row_blocks, rb = k.u % p.row_blocks;
+            const int32_t* table = p.c.table + static_cast<size_t>(k.b) * p.c.max_pages;
+            if (seg >= 2) ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarQEmpty + (seg & 1)), ((seg >> 1) & 1) ^ 1,
+                                                                  abort_flag, p, 70));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(C::kBarQFull + (seg & 1)), C::kQBytes);
+                for (int a = 0; a < C::kAtoms; ++a)
+                    tma_load_3d(sbase + C::kOffQ + (seg & 1) * C::kQBytes + a * C::kRowAtomBytes, &map_q,
+                                bar(C::kBarQFull + (seg & 1)), a * C::kAtomElems, rb * NR, k.b * p.c.H_kv + kvh, once);
+            }
+            for (int j = k.t; j < k.last(); ++j, ++it) {
+                const int s = it % C::kStages;
+                const int have = min(pages, (k.len - j * 128 + p.c.page - 1) / p.c.page);  // pages of the tile in use
+                int id = mine < have ? table[j * pages + mine] : 0;
+                ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarEmpty + s), ((it / C::kStages) & 1) ^ 1, abort_flag, p, 60));
+                if (!ok) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar(C::kBarFull + s),
+                                          static_cast<uint32_t>(have * p.c.page) * (kParts * 128u));
+                __syncwarp();
+                for (int g = mine; g < have; g += 32 / kParts) {
+                    if (g != mine) id = table[j * pages + g];
+                    tma_load_4d(dst0 + s * C::kTileBytes + g * p.c.page * 128, map, bar(C::kBarFull + s),
+                                atom * C::kAtomElems, 0, kvh, id, once);
+                }
+                __syncwarp();
+            }
+        }
+        // every issued load has landed before the CTA may exit
+        if (lane == 0) {
+            for (int s = 0; s < C::kStages && s < it; ++s) {
+                const int last = s + ((it - 1 - s) / C::kStages) * C::kStages;
+                wait_phase(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, p, 61, false);
+            }
+            for (int b = 0; b < 2 && b < seg; ++b) {
+                const int last = b + ((seg - 1 - b) / 2) * 2;
+                wait_phase(bar(C::kBarQFull + b), (last >> 1) & 1, abort_flag, p, 61, false);
+            }
+        }
+    } else if (warp == kDecMmaWarp) {
+        // ------------------------------------------------------------ issuer
+        if (lane == 0 && start.valid()) {
+            const int total = start.end - start.pos;
+            // S^T of the run's tiles goes two ahead of their products with V, so in
+            // the next unit, maybe, while this one's are issued: a cursor each
+            Cursor ks = start, kv = start;
+            int seg_s = 0, seg_v = 0, js = ks.t, jv = kv.t;
+            bool ok = true;
+            auto issue_s = [&](int it) {
+                if (js == ks.t) ok = wait_phase(bar(C::kBarQFull + (seg_s & 1)), (seg_s >> 1) & 1, abort_flag, p, 62);
+                if (ok) ok = wait_phase(bar(C::kBarFull + it % C::kStages), (it / C::kStages) & 1, abort_flag, p, 63);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t sK = sbase + C::kOffK + (it % C::kStages) * C::kTileBytes;
+                const uint32_t sQ = sbase + C::kOffQ + (seg_s & 1) * C::kQBytes;
+#pragma unroll
+                for (int kk = 0; kk < C::kQkSteps; ++kk) {
+                    const uint32_t koff = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
+                    const uint32_t qoff = (kk * 32) / 128 * C::kRowAtomBytes + (kk * 32) % 128;
+                    mma_ss<false>(tmem + C::kColS + NR * (it & 1), smem_desc_sw128(sK + koff, 16, 1024),
+                                  smem_desc_sw128(sQ + qoff, 16, 1024), C::kIdescQK, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(bar(C::kBarS + (it & 1)));
+                if (++js == ks.last()) {
+                    tc_commit(bar(C::kBarQEmpty + (seg_s & 1)));
+                    ks.next(p.c, units);
+                    js = ks.t;
+                    ++seg_s;
+                }
+            };
+            for (int it = 0; ok && it < 2 && it < total; ++it) issue_s(it);
+            for (int it = 0; ok && it < total; ++it) {
+                const int b = it & 1;
+                const bool first = jv == kv.t;
+                if (first && seg_v >= 2)  // O^T of the unit before the last one has been read
+                    ok = wait_phase(bar(C::kBarOFree + (seg_v & 1)), ((seg_v >> 1) & 1) ^ 1, abort_flag, p, 71);
+                if (ok) ok = wait_phase(bar(C::kBarP + b), (it >> 1) & 1, abort_flag, p, 64);
+                if (!ok) break;
+                tc_fence_after();
+                // O^T += V^T P^T: A = V read MN-major (d contiguous, its two
+                // 64-element blocks 16 KB apart), B = P^T K-major
+                const uint32_t sV = sbase + C::kOffV + (it % C::kStages) * C::kTileBytes;
+                const uint32_t sP = sbase + C::kOffP + b * 2 * C::kRowAtomBytes;
+#pragma unroll
+                for (int kk = 0; kk < C::kPvSteps; ++kk) {
+                    const uint32_t poff = (kk * 32) / 128 * C::kRowAtomBytes + (kk * 32) % 128;
+                    mma_ss<false>(tmem + C::kColO + NR * (seg_v & 1),
+                                  smem_desc_sw128(sV + kk * C::kUmmaK * 128, C::kAtomBytes, 1024),
+                                  smem_desc_sw128(sP + poff, 16, 1024), C::kIdescPV, (!first || kk > 0) ? 1u : 0u);
+                }
+                tc_commit(bar(C::kBarPFree + b));
+                tc_commit(bar(C::kBarEmpty + it % C::kStages));  // K and V are no longer read
+                if (++jv == kv.last()) {
+                    tc_commit(bar(C::kBarO + (seg_v & 1)));
+                    kv.next(p.c, units);
+                    jv = kv.t;
+                    ++seg_v;
+                }
+                if (it + 2 < total) issue_s(it + 2);  // buffer b: its S^T was read before this P^T was published
+            }
+            tc_commit(bar(C::kBarDrain));
+            wait_phase(bar(C::kBarDrain), 0, abort_flag, p, 65, false);
+        }
+    } else {
+        // ------------------------------------------------ softmax warpgroup
+        const int t = static_cast<int>(threadIdx.x);  // key t of each tile; lane t of O^T
+        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t tS = tmem + lane_base + C::kColS;
+        const float c = p.scale_log2;
+        float* red = reinterpret_cast<float*>(smem + C::kOffRed);  // [3][4 warps][NR]
+        constexpr int kLanesPerRow = 32 / NR;                      // after warp_reduce_rows
+        // key t's 16-bit slot in row n of a P^T buffer (see the decode kernel)
+        const int pch = (t % 64) / 8;
+        uint8_t* pkey = smem + C::kOffP + (t / 64) * C::kRowAtomBytes + (t % 8) * 2;
+        bool ok = true;
+        int it = 0, seg = 0;
+        for (Cursor k = start; ok && k.valid(); k.next(p.c, units), ++seg) {
+            const int row0 = (k.u % p.row_blocks) * NR;
+            const int rows = min(p.rows - row0, NR);
+            const uint32_t tO = tmem + lane_base + C::kColO + NR * (seg & 1);
+            float m[NR], l[NR], lq[NR];  // reference maxima (base 2, scaled), sums
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                m[n] = -INFINITY;
+                l[n] = 0.0f;
+                lq[n] = 0.0f;
+            }
+            // is key `key` visible to row n (rows past the last see every key)
+            auto visible = [&](int n, int key) -> bool {
+                if (key >= k.len) return false;
+                if (kCausal && n < rows) return key <= (row0 + n) % p.Nq + k.len - p.Nq;
+                return true;
+            };
+            const int first = k.t, last = k.last();
+            for (int j = first; j < last; ++j, ++it) {
+                const int b = it & 1, s_ = it % C::kStages;
+                const int key0 = j * 128;
+                const int key = key0 + t;
+                const bool masked = key0 + 128 > k.len || (kCausal && key0 + 127 > k.len - p.Nq);
+                uint32_t s[NR];
+                if (ok) ok = wait_phase(bar(C::kBarS + b), (it >> 1) & 1, abort_flag, p, 66);
+                ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-wide
+                if (ok) {
+                    tc_fence_after();
+                    tmem_ld_cols<NR>(tS + NR * b, s);
+                    tmem_ld_cols_wait<NR>(s);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) s[n] = 0u;
+                }
+                // x = t - m: the exponent of each weight against the current reference
+                float x[NR];
+                bool need = j == first || !ok;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    x[n] = fmaf(u2f(s[n]), c, -m[n]);
+                    if (masked && !visible(n, key)) x[n] = -INFINITY;
+                    need |= x[n] > kRescaleThreshold;
+                }
+                if (named_barrier_or(kDecNamedBar, 128, need)) {
+                    if (named_barrier_or(kDecNamedBar, 128, !ok)) {  // every thread leaves together
+                        ok = false;
+                        break;
+                    }
+                    // the tile's row maxima over its 128 keys
+                    float v[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) v[n] = (masked && !visible(n, key)) ? -INFINITY : u2f(s[n]) * c;
+                    const float r = warp_reduce_rows<NR, true>(v, lane);
+                    if (lane % kLanesPerRow == 0) red[warp * NR + lane / kLanesPerRow] = r;
+                    named_barrier_sync(kDecNamedBar, 128);
+                    float alpha[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const float tmax = fmaxf(fmaxf(red[n], red[NR + n]), fmaxf(red[2 * NR + n], red[3 * NR + n]));
+                        float mn = fmaxf(m[n], tmax);
+                        if (mn == -INFINITY) mn = 0.0f;  // no visible key yet: any finite reference
+                        alpha[n] = ex2(m[n] - mn);      // 0 while m was -inf
+                        l[n] *= alpha[n];
+                        lq[n] *= alpha[n];
+                        m[n] = mn;
+                        x[n] = (masked && !visible(n, key)) ? -INFINITY : fmaf(u2f(s[n]), c, -mn);
+                    }
+                    if (j > first) {  // O^T holds tiles < j: rescale it once the last product into it is done
+                        ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarPFree + (b ^ 1)), ((it - 1) >> 1) & 1,
+                                                                abort_flag, p, 67));
+                        if (ok) {
+                            tc_fence_after();
+                            uint32_t o[NR];
+                            tmem_ld_cols<NR>(tO, o);
+                            tmem_ld_cols_wait<NR>(o);
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) o[n] = f2u(u2f(o[n]) * alpha[n]);
+                            tmem_st_cols<NR>(tO, o);
+                            tmem_st_wait();
+                        }
+                    }
+                }
+                // P^T buffer b was last read by the product of tile it - 2
+                if (ok && it >= 2) ok = wait_phase(bar(C::kBarPFree + b), ((it - 2) >> 1) & 1, abort_flag, p, 68);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && key >= k.len) {  // value rows behind the sequence's end, and of pages not loaded
+                    ok = wait_phase(bar(C::kBarFull + s_), (it / C::kStages) & 1, abort_flag, p, 72);
+                    for (int a = 0; ok && a < C::kAtoms; ++a) {
+                        uint4* row = reinterpret_cast<uint4*>(smem + C::kOffV + s_ * C::kTileBytes + a * C::kAtomBytes + t * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    uint8_t* pbuf = pkey + b * 2 * C::kRowAtomBytes;
+#pragma unroll
+                    for (int n = 0; n < NR; n += 2) {
+                        const float p0 = ex2(x[n]), p1 = ex2(x[n + 1]);
+                        l[n] += p0;
+                        l[n + 1] += p1;
+                        const uint32_t w2 = pack_16x2<F16>(p0, p1);
+                        lq[n] += widen_lo16<F16>(w2);
+                        lq[n + 1] += widen_lo16<F16>(w2 >> 16);
+                        *reinterpret_cast<uint16_t*>(pbuf + n * 128 + ((pch ^ (n & 7)) << 4)) =
+                            static_cast<uint16_t>(w2 & 0xFFFFu);
+                        *reinterpret_cast<uint16_t*>(pbuf + (n + 1) * 128 + ((pch ^ ((n + 1) & 7)) << 4)) =
+                            static_cast<uint16_t>(w2 >> 16);
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::kBarP + b));
+                }
+            }
+
+            // --------------------------------------------- the unit's result
+            if (ok) ok = wait_phase(bar(C::kBarO + (seg & 1)), (seg >> 1) & 1, abort_flag, p, 69);
+            ok = __all_sync(0xffffffffu, ok);
+            if (named_barrier_or(kDecNamedBar, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t o[NR];
+            tmem_ld_cols<NR>(tO, o);
+            tmem_ld_cols_wait<NR>(o);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarOFree + (seg & 1)));
+            // l and lq over the 128 keys of the warpgroup
+            const float rl = warp_reduce_rows<NR, false>(l, lane);
+            const float rq = warp_reduce_rows<NR, false>(lq, lane);
+            if (lane % kLanesPerRow == 0) {
+                red[4 * NR + warp * NR + lane / kLanesPerRow] = rl;
+                red[8 * NR + warp * NR + lane / kLanesPerRow] = rq;
+            }
+            named_barrier_sync(kDecNamedBar, 128);
+            const bool whole = first == 0 && last == k.tiles();
+            const long long unit = static_cast<long long>(k.b) * units + k.u;
+            if (whole && !p.parts_always) {
+                uint16_t* out = static_cast<uint16_t*>(p.out);
+                const long long at = (static_cast<long long>(k.b) * p.c.H_kv + k.u / p.row_blocks) * p.rows + row0;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    if (n >= rows) break;
+                    const float* a = red + 4 * NR + n;
+                    const float* q = red + 8 * NR + n;
+                    const float LQ = (q[0] + q[NR]) + (q[2 * NR] + q[3 * NR]);
+                    const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
+                    if (t < D) out[(at + n) * D + t] = static_cast<uint16_t>(pack_16x2<F16>(u2f(o[n]) * inv, 0.0f) & 0xFFFFu);
+                    if (t == n && p.lse != nullptr) {
+                        const float L = (a[0] + a[NR]) + (a[2 * NR] + a[3 * NR]);
+                        p.lse[at + n] = L == 0.0f ? -INFINITY : (m[n] + log2f(L)) * 0.69314718055994531f;
+                    }
+                }
+            } else {
+                // a partial result; a row that sees no key here gets weight 0 (m = -inf)
+                const long long slot = whole ? 2ll * p.ctas + unit : 2ll * blockIdx.x + (seg == 0 ? 0 : 1);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    if (n >= rows) break;
+                    const float* a = red + 4 * NR + n;
+                    const float* q = red + 8 * NR + n;
+                    if (t < D) p.unit_o[(slot * NR + n) * D + t] = u2f(o[n]);
+                    if (t == n) {
+                        const float L = (a[0] + a[NR]) + (a[2 * NR] + a[3 * NR]);
+                        p.part_ml[slot * NR + n] = make_float4(L == 0.0f ? -INFINITY : m[n], L,
+                                                               (q[0] + q[NR]) + (q[2 * NR] + q[3 * NR]), 0.0f);
+                    }
+                }
+            }
+            // `red` is written again after the next unit's votes, which all threads reach
+        }
+    }
+
+    // --------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kDecMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+    if (p.parts_always) grid_wait();
+}
+
+constexpr int kJoinThreads = 256;
+
+// The second kernel: rows whose keys several CTAs shared, or that have a
+// prefix, from their partial results, in order; a warp per row:
+//   M = max m_s,  O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) lq_s,
+//   lse = ln 2 (M + log2 sum 2^(m_s - M) l_s).
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const PagedFwdParams p, int rows_per_block) {
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
+    const long long total_rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
+    grid_wait();
+    grid_release();
+    if (row >= total_rows) return;
+    const int units = p.c.H_kv * p.row_blocks;
+    const int r = static_cast<int>(row % p.rows);
+    const long long head = row / p.rows;  // b * H_kv + key/value head
+    const int b = static_cast<int>(head / p.c.H_kv);
+    const int u = static_cast<int>(head % p.c.H_kv) * p.row_blocks + r / rows_per_block;
+    const int n = r % rows_per_block;
+    const Spread sp = spread_of(p.c, b);
+    const int tiles = tiles_of(sp.len);
+    const int run = run_of(sp.total * units, p.ctas);
+    const int begin = sp.before * units + u * tiles;  // the unit's first tile among all
+    const int c0 = begin / run, c1 = tiles > 0 ? (begin + tiles - 1) / run : c0 - 1;  // its CTAs
+    const bool whole = c0 == c1;
+    if (whole && !p.parts_always) return;  // written by its CTA
+    const int own = c1 - c0 + 1, parts = own + p.splits;
+    auto slot = [&](int i) -> long long {  // of part i < own
+        if (whole) return 2ll * p.ctas + static_cast<long long>(b) * units + u;
+        // a CTA whose run starts inside or with the unit has it as its first
+        const int cta = c0 + i;
+        return 2ll * cta + (i == 0 && begin != c0 * run ? 1 : 0);
+    };
+    auto stats = [&](int i) -> float4 {
+        if (i < own) return p.part_ml[slot(i) * rows_per_block + n];
+        return *reinterpret_cast<const float4*>(p.ml_part + (static_cast<size_t>(i - own) * total_rows + row) * 4);
+    };
+    float M = -INFINITY;
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, stats(i).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const float ref = M == -INFINITY ? 0.0f : M;
+    constexpr int kPer = D / 32;
+    float acc[kPer] = {}, L = 0.0f, LQ = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float4 ml = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        if (i0 + lane < parts) ml = stats(i0 + lane);
+        const float w = ex2(ml.x - ref);
+        float l = w * ml.y, q = w * ml.z;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, off);
+            q += __shfl_xor_sync(0xffffffffu, q, off);
+        }
+        L += l;
+        LQ += q;
+        const int here = min(32, parts - i0);
+#pragma unroll 4
+        for (int k = 0; k < here; ++k) {
+            const float f = __shfl_sync(0xffffffffu, w, k);
+            const int i = i0 + k;
+            const float* src = (i < own ? p.unit_o + (slot(i) * rows_per_block + n) * D
+                                        : p.o_part + (static_cast<size_t>(i - own) * total_rows + row) * D) + lane * kPer;
+            if (f == 0.0f) continue;
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) acc[x] += f * src[x];
+        }
+    }
+    const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * kPer);
+#pragma unroll
+    for (int x = 0; x < kPer; x += 2) dst[x / 2] = pack_16x2<F16>(acc[x] * inv, acc[x + 1] * inv);
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = L == 0.0f ? -INFINITY : (ref + log2f(L)) * 0.69314718055994531f;
+}
+
+template <int D, bool F16, bool kCausal, int NR>
+cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,
+                           cudaStream_t stream) {
+    using C = Cfg<D, F16, NR>;
+    auto kern = fa_paged_kernel<D, F16, kCausal, NR>;
+    static SmemAllowed allowed;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes), allowed);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), kDecThreads, C::kSmemBytes, stream, q, k, v, p);
+    if (e != cudaSuccess) return e;
+    const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
+    return launch_dependent(fa_paged_join_kernel<D, F16>, dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
+                            kJoinThreads, 0, stream, p, NR);
+}
+
+template <int D, bool F16>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,
+                   cudaStream_t stream) {
+    if (paged_rows_per_block(p.rows) == 16)
+        return p.causal ? launch_variant<D, F16, true, 16>(q, k, v, p, stream)
+                        : launch_variant<D, F16, false, 16>(q, k, v, p, stream);
+    return p.causal ? launch_variant<D, F16, true, 32>(q, k, v, p, stream)
+                    : launch_variant<D, F16, false, 32>(q, k, v, p, stream);
+}
+
+}  // namespace paged
+}  // namespace fa

@@ -34,7 +34,8 @@ typedef enum {
     FA_ERR_ALIGNMENT = 3,    /* a tensor base address is not 16-byte aligned */
     FA_ERR_CUDA = 4,         /* a CUDA runtime or driver call failed (see fa_last_error_message) */
     FA_ERR_TIMEOUT = 5,      /* a kernel gave up waiting on an internal barrier (device status) */
-    FA_ERR_CAPACITY = 6      /* rows appended to a full 4-bit cache were dropped (device status) */
+    FA_ERR_CAPACITY = 6,     /* rows appended to a full cache were dropped (device status) */
+    FA_ERR_RANGE = 7         /* a page number or a position outside its range (device status) */
 } fa_status_t;
 
 /* Element type of q, k, v and o (the low 8 bits of every `dtype` argument). */
@@ -580,10 +581,118 @@ int fa_packed_bwd_validate(const fa_rows_t* q, const fa_rows_t* k, const fa_rows
                            int64_t T_k, int64_t H, int64_t H_kv, int64_t d, float scale, int dtype,
                            const void* workspace, size_t workspace_bytes);
 
+/* ------------------------------------------------------------------------
+ * The paged 16-bit key/value cache.
+ *
+ * Keys and values of sequences of different lengths in pages of a common pool,
+ * so that memory is handed out a page at a time and sequences may share pages
+ * (a prompt's).  fa_paged_append rotates rows by their positions and stores
+ * them, fa_paged_fwd attends over a sequence's pages, behind a prefix that all
+ * sequences share, if there is one.  The attention is the pages' (online softmax
+ * over key partitions, "FlashAttention dissected", sections "Algorithmic core in
+ * pseudocode" and "Interaction with the KV cache during inference"); the layout
+ * and the rotation have no counterpart there.
+ *
+ * Slot s of sequence b is row s % page_size of page block_table[b][s / page_size].
+ * The library never allocates: every array is the caller's, on the current device.
+ */
+typedef struct {
+    void* k_pages;              /* [num_pages, H_kv, page_size, d], 16-byte aligned, of the calls' dtype */
+    void* v_pages;              /* as k_pages */
+    const int32_t* block_table; /* [B, max_pages]; numbers behind a sequence's last slot are not looked at */
+    int32_t* lengths;           /* [B]: slots in use, 0 .. max_pages * page_size (other values are clamped) */
+    int64_t num_pages;
+    int64_t page_size;          /* 16, 32, 64 or 128 */
+    int64_t B, max_pages, H_kv;
+    int64_t d;                  /* 64 or 128 */
+} fa_paged_cache_t;
+
+/* fa_paged_append: pairs of neighbouring channels are rotated (else channel j with j + rot / 2). */
+#define FA_FLAG_INTERLEAVED 0x200
+
+/*
+ * fa_paged_append — store new rows of every sequence behind its last slot, keys
+ * rotated by their positions, and rotate the queries beside them.
+ *
+ *   k, v       : views of T rows and H_kv heads;  cu: int32 [B + 1] on the
+ *                device, rows cu[b] .. cu[b + 1] - 1 are sequence b's (not
+ *                decreasing, within 0 .. T), or NULL: T / B rows each.
+ *   q, q_out   : views of T rows and H heads, or both NULL; q_out may be q.
+ *   k_out      : view of T rows and H_kv heads that gets the rotated keys too
+ *                (for fa_packed_fwd over a prompt), or NULL; may be k.
+ *   table      : fp32 [table_rows, rot], 16-byte aligned: row p holds the cosines of
+ *                position p's rot / 2 angles, then their sines; or NULL: nothing
+ *                is rotated (q_out and k_out are copies).  rot: a multiple of 16 up to d, the
+ *                channels that are rotated; the others are copied.
+ *   positions  : int32 [T], the rows' positions, or NULL: first_position + the slot.
+ *   lengths_out: int32 [B], receives the lengths with the new rows; may be the
+ *                cache's own (advanced in place), which are left alone otherwise.
+ *   dtype      : FA_DTYPE_BF16 or FA_DTYPE_F16, optionally FA_FLAG_INTERLEAVED.
+ * Pair (x, y) becomes (x cos - y sin, x sin + y cos), in 32 bits, rounded once.
+ * Key and value rows past max_pages * page_size slots are dropped and
+ * fa_device_status reports FA_ERR_CAPACITY; those whose page number is outside the
+ * pool are dropped, and positions outside the table are rotated as its first
+ * or last row, and it reports FA_ERR_RANGE.  Rows of no sequence, and pages
+ * but for the new rows, are left as they were.  Where two slots written are the
+ * same row of the pool either may stay.  One kernel, and a second one when lengths
+ * advance in place and a sequence has more than a few rows.
+ */
+int fa_paged_append(const fa_paged_cache_t* cache, const fa_rows_t* k, const fa_rows_t* v, const int32_t* cu,
+                    int64_t T, const fa_rows_t* q, const fa_rows_t* q_out, int64_t H, const fa_rows_t* k_out,
+                    const float* table, int64_t table_rows, int64_t rot, const int32_t* positions,
+                    int64_t first_position, int32_t* lengths_out, int dtype, void* stream);
+
+/*
+ * fa_paged_fwd — attention of q [B, H, N_q, d] over the sequences' slots:
+ *
+ *     O = softmax(scale q K^T) V,  lse = log sum exp(scale q K^T)
+ *
+ * over key/value head h / (H / H_kv) of the prefix's prefix_length slots, read once
+ * for all sequences, followed by the sequence's own lengths[b].
+ *   o            : [B, H, N_q, d] of `dtype`;  lse: fp32 [B, H, N_q] or NULL.
+ *   prefix_pages : int32 [ceil(prefix_length / page_size)] on the device, pages of
+ *                  the same pool; NULL exactly where prefix_length is 0.
+ *   dtype        : FA_DTYPE_BF16 or FA_DTYPE_F16, optionally FA_FLAG_CAUSAL:
+ *                  row i sees the prefix and the own slots
+ *                  j < lengths[b] - (N_q - 1 - i).
+ *   N_q * H / H_kv <= 128 (decode steps and drafts): else FA_ERR_UNSUPPORTED.
+ *   workspace    : fa_paged_fwd_workspace_size(...) bytes, 16-byte aligned;
+ *                  nothing in it needs to be zeroed.  Calls (and replays of
+ *                  captured ones) that may run at once need one each.
+ * A row that sees no slot gets O = 0 and lse = -inf.  A page number outside the pool reads as
+ * zeros.  What slots at or behind the length hold does not matter; an infinity
+ * or a NaN in a value row that a draft's mask hides may reach that draft's rows.
+ * Lengths, block table and prefix pages are read on the device, so a captured call
+ * follows them.  Scores, sums and lse are held in 32 bits; the weights are rounded
+ * to `dtype` for their product with V and divided by the sum of the rounded ones (the
+ * prefix's, of its tiles' largest ones).  Results do not depend on the order
+ * in which blocks run.  Two kernels, three with a prefix.
+ */
+int fa_paged_fwd(const fa_paged_cache_t* cache, const void* q, void* o, float* lse, int64_t H, int64_t N_q,
+                 const int32_t* prefix_pages, int64_t prefix_length, float scale, int dtype, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fa_paged_fwd on the current device, for a cache of B
+ * sequences of up to `capacity` (max_pages * page_size) slots (the SM count is
+ * the one CUDA query; 1024 SMs when no device answers); 0 for invalid sizes. */
+size_t fa_paged_fwd_workspace_size(int64_t B, int64_t H, int64_t H_kv, int64_t N_q, int64_t capacity, int64_t d,
+                                   int64_t prefix_length);
+
+/* The host-side argument checks of the two calls, alone; no CUDA call but
+ * fa_paged_fwd_workspace_size's query. */
+int fa_paged_append_validate(const fa_paged_cache_t* cache, const fa_rows_t* k, const fa_rows_t* v, const int32_t* cu,
+                             int64_t T, const fa_rows_t* q, const fa_rows_t* q_out, int64_t H,
+                             const fa_rows_t* k_out, const float* table, int64_t table_rows, int64_t rot,
+                             const int32_t* positions, int64_t first_position, const int32_t* lengths_out, int dtype);
+int fa_paged_fwd_validate(const fa_paged_cache_t* cache, const void* q, const void* o, const float* lse, int64_t H,
+                          int64_t N_q, const int32_t* prefix_pages, int64_t prefix_length, float scale, int dtype,
+                          const void* workspace, size_t workspace_bytes);
+
 /*
  * fa_device_status — synchronise `stream`, then read and clear the device
- * error word the kernels set when a bounded wait gives up or a 4-bit cache
- * overflows.  Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_CAPACITY, or FA_ERR_CUDA
+ * error word the kernels set when a bounded wait gives up, a cache overflows or
+ * a number is out of its range.  Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_CAPACITY,
+ * FA_ERR_RANGE (in this order, where several are set), or FA_ERR_CUDA
  * if the synchronisation itself failed.
  * A launch that timed out leaves its outputs incomplete (the CTAs of that
  * launch stop early); later launches run normally whether or not the word
