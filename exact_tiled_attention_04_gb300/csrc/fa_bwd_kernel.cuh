@@ -72,6 +72,7 @@
 #include <cstdint>
 
 #include "fa_bwd_internal.h"
+#include "fa_kv4.h"
 #include "fa_packed.cuh"
 #include "fa_packed.h"
 #include "fa_ptx.cuh"
@@ -895,11 +896,9 @@ cudaError_t launch_packed_bwd_variant(const CUtensorMap& dq, const PackedBwdPara
                                       cudaStream_t stream) {
     using C = BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>;
     auto kern = fa_bwd_kernel<D, F16, kCausal, true, PackedBwdParams>;
-    cudaFuncAttributes attr;  // see launch_bwd_variant
-    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != static_cast<int>(C::kLaunchRegs)) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes));
+    static SmemAllowed allowed;
+    const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
+                                          static_cast<int>(C::kLaunchRegs), allowed);
     if (e != cudaSuccess) return e;
     kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(dq, dq, dq, dq, dq, dq, dq, p);
     return cudaGetLastError();

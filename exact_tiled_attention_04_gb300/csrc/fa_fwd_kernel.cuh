@@ -60,17 +60,15 @@
 #include <cstdint>
 
 #include "fa_internal.h"
-#include "fa_packed.cuh"
-#include "fa_packed.h"
 #include "fa_paged.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
 
-// What a launch's query blocks are (kMode): blocks of a [B, H, N, d] tensor,
-// of packed sequences (PackedFwdParams), or the rows that several sequences
-// have for one key/value head, over the pages of a prefix (PrefixFwdParams).
-constexpr int kModeBatch = 0, kModePacked = 1, kModePrefix = 2;
+// What a launch's query blocks are (kMode): blocks of a [B, H, N, d] tensor, or
+// the rows that several sequences have for one key/value head, over the pages of
+// a prefix (PrefixFwdParams).
+constexpr int kModeBatch = 0, kModePrefix = 1;
 
 constexpr int kTileM = 128;  // query rows per softmax warpgroup = TMEM lanes
 constexpr int kTileN = 128;  // keys per K/V tile
@@ -191,9 +189,7 @@ struct FwdCfg {
     static constexpr int kOffTurnFlags = kOffAbort + 4;  // [2][4] u32: turns each softmax warp has received
     static constexpr int kSmemUsed = kOffTurnFlags + 32;
     static constexpr size_t kSmemBytes = static_cast<size_t>(kSmemUsed) + 1024;  // alignment slack
-    static constexpr int kOffBlock = kSmemUsed;  // packed launches: the CTA's SeqBlock and head
-    static constexpr size_t kSmemBytesPacked = kSmemBytes + 32;
-    static_assert(kSmemBytesPacked <= 232448, "shared memory budget exceeded");
+    static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
     // In-cluster merge of split partials: the unnormalised O (256 rows x D
     // fp32) and (m, l, lq) per row, written over the K and V rings once every
     // product of the CTA has completed.
@@ -733,76 +729,6 @@ __device__ __forceinline__ void cluster_merge(const FwdParams& p, uint8_t* smem,
     cluster_sync_all();
 }
 
-// Producer warp of a packed launch.  As in a batch, but a tile's rows past its
-// sequence's end are the next sequence's.  Their scores are masked and their
-// queries not stored; a value row, however, would enter the product with weight
-// 0, and 0 x infinity is not 0.  So the sequence's last value tile, the last
-// tile that this CTA loads, lands on a barrier of its own, and the warp zeroes
-// the rows that are not the sequence's before it hands the tile on.
-template <int D, bool F16>
-__device__ __forceinline__ void produce_packed(const CUtensorMap& map_q, const CUtensorMap& map_k,
-                                               const CUtensorMap& map_v, const PackedFwdParams& p, uint8_t* smem,
-                                               uint32_t sbase, int lane, const SeqBlock& blk, int row0, int head,
-                                               int kvh, int T, volatile uint32_t* abort_flag) {
-    using C = FwdCfg<false, D, F16>;
-    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(i); };
-    const int end = blk.nk - (T - 1) * kTileN;  // keys of the last tile
-    const bool tail = end < kTileN;
-    int nk = 0, nv = 0;  // K and V tiles whose loads were issued
-    if (lane == 0) {
-        const uint64_t keep = policy_evict_last();
-        const uint64_t once = policy_evict_first();
-        mbar_arrive_expect_tx(bar(C::kBarQFull), 2u * C::kTileBytes);
-        for (int w = 0; w < 2; ++w)
-            for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_3d(sbase + C::kOffQ + w * C::kTileBytes + a * C::kAtomBytes, &map_q, bar(C::kBarQFull),
-                            a * C::kAtomElems, blk.q0 + row0 + w * p.tile_step, head + w * p.head_step, once);
-        for (int j = 0; j < T; ++j) {
-            const int ks = j % C::kKStages;
-            if (!wait_phase(bar(C::kBarKEmpty + ks), ((j / C::kKStages) & 1) ^ 1, abort_flag, p, 1)) break;
-            mbar_arrive_expect_tx(bar(C::kBarKFull + ks), C::kTileBytes);
-            for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_3d(sbase + C::kOffK + ks * C::kTileBytes + a * C::kAtomBytes, &map_k, bar(C::kBarKFull + ks),
-                            a * C::kAtomElems, blk.k0 + j * kTileN, kvh, keep);
-            nk = j + 1;
-            const int vs = j % C::kVStages;
-            if (!wait_phase(bar(C::kBarVEmpty + vs), ((j / C::kVStages) & 1) ^ 1, abort_flag, p, 2)) break;
-            const uint32_t vbar = tail && j + 1 == T ? bar(C::kBarVRaw) : bar(C::kBarVFull + vs);
-            mbar_arrive_expect_tx(vbar, C::kTileBytes);
-            for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_3d(sbase + C::kOffV + vs * C::kTileBytes + a * C::kAtomBytes, &map_v, vbar,
-                            a * C::kAtomElems, blk.k0 + j * kTileN, kvh, keep);
-            nv = j + 1;
-        }
-    }
-    __syncwarp();
-    if (tail && __shfl_sync(0xffffffffu, nv, 0) == T) {
-        const int vs = (T - 1) % C::kVStages;
-        // (not left before the tile has landed: nothing may write to shared memory behind the CTA's end)
-        if (__all_sync(0xffffffffu, wait_phase(bar(C::kBarVRaw), 0, abort_flag, p, 3, false))) {
-            for (int a = 0; a < C::kAtoms; ++a) {
-                uint4* rows = reinterpret_cast<uint4*>(smem + C::kOffV + vs * C::kTileBytes + a * C::kAtomBytes);
-                for (int i = end * 8 + lane; i < kTileN * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::kBarVFull + vs));
-        }
-    }
-    // every load has landed (see the batch's producer)
-    if (lane == 0) {
-        wait_phase(bar(C::kBarQFull), 0, abort_flag, p, 3, false);
-        for (int s = 0; s < C::kKStages && s < nk; ++s) {
-            const int last = s + ((nk - 1 - s) / C::kKStages) * C::kKStages;
-            wait_phase(bar(C::kBarKFull + s), (last / C::kKStages) & 1, abort_flag, p, 3, false);
-        }
-        for (int s = 0; s < C::kVStages && s < nv; ++s) {
-            const int last = s + ((nv - 1 - s) / C::kVStages) * C::kVStages;
-            wait_phase(bar(C::kBarVFull + s), (last / C::kVStages) & 1, abort_flag, p, 3, false);
-        }
-    }
-}
-
 // Producer warp of a prefix launch: query rows of several sequences, keys and
 // values page by page (a box per lane).  Value rows behind the prefix's end, in
 // its last page or in pages that are not loaded, are zeroed as above.
@@ -900,9 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (a tail launch starts at query block p.item_offset; unmasked launches only)
     const unsigned int cta = blockIdx.x / static_cast<unsigned>(p.splits) + static_cast<unsigned>(p.item_offset);
     int qb, bh;
-    if constexpr (kMode == kModePacked) {
-        qb = bh = 0;  // found on the device, below
-    } else if constexpr (kMode == kModePrefix) {
+    if constexpr (kMode == kModePrefix) {
         qb = static_cast<int>(cta % static_cast<unsigned>(p.blocks));  // of the sequences
         bh = static_cast<int>(cta / static_cast<unsigned>(p.blocks));  // the key/value head
     } else if (kCausal) {
@@ -925,11 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // packed launches hold no query row in tile 1: its issuer and softmax
     // warpgroup sit out, and K/V stages are released by tile 0 alone
     constexpr bool one_tile = kOneTile;
-    int row0 = qb * 2 * kTileM;
-    if constexpr (kMode == kModePrefix) {
-        kvh = bh;
-        row0 = 0;
-    }
+    const int row0 = kMode == kModePrefix ? 0 : qb * 2 * kTileM;
+    if constexpr (kMode == kModePrefix) kvh = bh;
     // prefix launches: the first sequence of tile 0
     [[maybe_unused]] int seq0 = 0;
     if constexpr (kMode == kModePrefix) seq0 = qb * (kOneTile ? 1 : 2) * p.seqs;
@@ -944,9 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int t_begin = static_cast<int>(split) * p.tiles_per_split;
     // <= 0: this partition sees no key (causal mask); only its epilogue runs
-    int T = min(p.tiles_per_split, n_tiles_block - t_begin);
-    bool has_work = !kCausal || T > 0;  // without the mask every partition has a tile
-    [[maybe_unused]] SeqBlock blk;       // packed launches: the sequence
+    const int T = min(p.tiles_per_split, n_tiles_block - t_begin);
+    const bool has_work = !kCausal || T > 0;  // without the mask every partition has a tile
 
     auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(i); };
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
@@ -1004,43 +924,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
-    if constexpr (kMode == kModePacked) {
-        if (warp == kTransposeWarp) {
-            int unit;
-            blk = find_block<false>(p.seqs, kTileM + p.tile_step, p.units, blockIdx.x, unit);
-            int* out = reinterpret_cast<int*>(smem + C::kOffBlock);
-            if (lane == 0) {
-                out[0] = blk.q0;
-                out[1] = blk.nq;
-                out[2] = blk.k0;
-                out[3] = blk.nk;
-                out[4] = blk.r;
-                out[5] = unit * (1 + p.head_step);
-            }
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    bool skip = *abort_flag != 0u;
-    if constexpr (kMode == kModePacked) {
-        const int* in = reinterpret_cast<const int*>(smem + C::kOffBlock);
-        blk.q0 = in[0];
-        blk.nq = in[1];
-        blk.k0 = in[2];
-        blk.nk = in[3];
-        blk.r = in[4];
-        bh = in[5];  // the head (of tile 0)
-        kvh = bh / p.group;
-        skip = skip || blk.r < 0;  // the grid is as large as any lengths need
-        row0 = blk.r * (kTileM + p.tile_step);
-        // keys that the block's last row sees
-        int seen = blk.nk;
-        if (kCausal) seen = min(blk.nk, min(row0 + kTileM + p.tile_step, blk.nq) + blk.nk - blk.nq);
-        T = seen <= 0 ? 0 : (seen + kTileN - 1) / kTileN;
-        has_work = T > 0;
-    }
+    const bool skip = *abort_flag != 0u;
 
     if (skip) {
         // nothing issued: go straight to the teardown
@@ -1057,8 +945,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!TF32 && pack) zero_unloaded_q<C::kTileBytes, C::kAtoms, C::kAtomBytes>(smem + C::kOffQ, pack_rows, lane);
         if constexpr (kMode == kModePrefix) {
             produce_prefix<D, F16, kOneTile>(map_q, map_k, map_v, p, smem, sbase, lane, seq0, kvh, t_begin, T, abort_flag);
-        } else if constexpr (kMode == kModePacked) {
-            produce_packed<D, F16>(map_q, map_k, map_v, p, smem, sbase, lane, blk, row0, bh, kvh, T, abort_flag);
         } else if constexpr (TF32) {
             produce_tf32<D>(map_q, map_k, map_v, p, smem, sbase, lane, row0, bh, kvh, t_begin, T, abort_flag);
         } else if (lane == 0) {
@@ -1253,11 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             out_row = r < pack_rows ? (static_cast<long long>(bh) * p.group + r / p.Nq) * p.Nq + qi : -1;
         }
         int row_limit = p.Nkv;
-        if constexpr (kMode == kModePacked) {
-            const int i = row0 + w * p.tile_step + t;  // (a sequence's rows fit an int, and so does 255 more)
-            out_row = i < blk.nq ? blk.q0 + i : -1;
-            row_limit = kCausal ? max(-1, min(blk.nk, i + 1 + blk.nk - blk.nq)) : blk.nk;
-        } else if constexpr (kMode == kModePrefix) {
+        if constexpr (kMode == kModePrefix) {
             const int b = seq0 + w * p.seqs + t / p.rows;
             out_row = t < p.rows * p.seqs && b < p.B ? (static_cast<long long>(b) * p.H_kv + kvh) * p.rows + t % p.rows : -1;
         } else if (kCausal) {
@@ -1561,31 +1443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p.lse != nullptr && out_row >= 0) {
                 const float lse2 = (l > 0.0f) ? (m_ref + log2f(l)) : -INFINITY;
-                if constexpr (kMode == kModePacked)
-                    p.lse[static_cast<size_t>(bh + w * p.head_step) * p.seqs.Tq + out_row] = lse2 * 0.69314718055994531f;
-                else
-                    p.lse[out_row] = lse2 * 0.69314718055994531f;
+                p.lse[out_row] = lse2 * 0.69314718055994531f;
             }
-            if constexpr (kMode == kModePacked) {
-                // the warp's rows of the sequence, 16 bytes a lane (a tensor store would write the next sequence's)
-                __syncwarp();
-                constexpr int kChunks = D / 8, kRows = 32 / kChunks;
-                uint16_t* out = static_cast<uint16_t*>(p.out) +
-                                static_cast<size_t>(blk.q0 + row0 + w * p.tile_step + wi * 32) * p.o_row +
-                                static_cast<size_t>(bh + w * p.head_step) * p.o_head + (lane % kChunks) * 8;
-                const int have = blk.nq - (row0 + w * p.tile_step + wi * 32);
-                const uint8_t* src = stage + (lane % kChunks) / 8 * C::kAtomBytes;
-#pragma unroll 4
-                for (int r = lane / kChunks; r < min(32, have); r += kRows) {
-                    const int rr = wi * 32 + r;
-                    *reinterpret_cast<uint4*>(out + static_cast<size_t>(r) * p.o_row) =
-                        *reinterpret_cast<const uint4*>(src + rr * 128 + (((lane % 8) ^ (rr & 7)) << 4));
-                }
-            } else {
-                fence_proxy_async_smem();
-            }
+            fence_proxy_async_smem();
         }
-      if constexpr (kMode != kModePacked) {
         // Every thread of the warpgroup arrives exactly once, whatever happened.
         mbar_arrive(bar(C::kBarEpi + w));
         if (t == 0) {
@@ -1610,7 +1471,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-      }
         // back to the launch allocation for the in-cluster merge (see warpgroup 2)
         if (!kOneTile && p.cluster) regs_decrease<kLaunchRegs>();
     }
@@ -1640,33 +1500,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;");
 }
 
-// Packed launches: `grid` CTAs, enough for any lengths.
-template <int D, bool F16, bool kCausal>
-cudaError_t launch_packed_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                                  const PackedFwdParams& p, unsigned int grid, cudaStream_t stream) {
-    using C = FwdCfg<false, D, F16>;
-    auto kern = fa_fwd_kernel<false, D, F16, kCausal, false, kModePacked, PackedFwdParams>;
-    cudaFuncAttributes attr;  // see launch_fwd_variant
-    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytesPacked));
-    if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, C::kSmemBytesPacked, stream>>>(q, k, v, q, p);
-    return cudaGetLastError();
-}
-
 // Prefix launches.
 template <int D, bool F16, bool kOneTile>
 cudaError_t launch_prefix_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                   const PrefixFwdParams& p, cudaStream_t stream) {
     using C = FwdCfg<false, D, F16>;
     auto kern = fa_fwd_kernel<false, D, F16, false, kOneTile, kModePrefix, PrefixFwdParams>;
-    cudaFuncAttributes attr;  // see launch_fwd_variant
-    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != static_cast<int>(kLaunchRegs)) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes));
+    static SmemAllowed allowed;
+    const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
+                                          static_cast<int>(kLaunchRegs), allowed);
     if (e != cudaSuccess) return e;
     // (launched without overlap: the kernel behind it relies on this one having begun after all before it)
     kern<<<static_cast<unsigned>(p.H_kv * p.blocks * p.splits), kThreads, C::kSmemBytes, stream>>>(q, k, v, q, p);

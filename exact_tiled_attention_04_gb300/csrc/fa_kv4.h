@@ -48,6 +48,22 @@ inline cudaError_t allow_smem(const void* kernel, int smem, SmemAllowed& done) {
     if (e == cudaSuccess && cached) done.ctx_id[dev].store(host::current_context_id(), std::memory_order_relaxed);
     return e;
 }
+// The same for a kernel whose warps move registers among them (setmaxnreg): it
+// has to have been compiled for exactly `regs` a thread, as an increase without
+// the registers behind it would never return.
+inline cudaError_t allow_smem_regs(const void* kernel, int smem, int regs, SmemAllowed& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long ctx = host::current_context_id();
+    if (dev < host::kMaxCachedDevices && ctx != 0 && done.ctx_id[dev].load(std::memory_order_relaxed) == ctx)
+        return cudaSuccess;
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != regs) return cudaErrorInvalidConfiguration;
+    return allow_smem(kernel, smem, done);
+}
 template <class Kernel, class... Args>
 cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchAttribute attr[1];

@@ -1,0 +1,709 @@
+// Forward kernel over packed sequences, sm_103a: the products, the softmax and
+// their overlap are those of the forward kernel (fa_fwd_kernel.cuh: one CTA =
+// two tiles of 128 query rows against one key/value head, two softmax
+// warpgroups, an issuing warp for each).  What differs is the work around them.
+//
+// Packed batches have many short sequences, and a CTA that does one block of
+// rows pays 9 us beside the block's key tiles (time stamps: 0.9 from the CTA
+// before it on the SM, 2.2 to find its block, 2.4 until Q and K have landed,
+// 1.7 to write O, 1.5 to tear down), as much as five tiles take.  So a CTA goes through
+// many blocks without a pause.  The grid has a CTA for every block; a running
+// CTA takes the next one's place before that one starts (cluster launch
+// control), so blocks still begin in the grid's order, heaviest first, on the
+// SM that is free first.
+//   warps 0-7  softmax of tiles 0 and 1, as there; O goes to global memory
+//              from registers, so that the query tiles are free for the next block
+//   warp  8    issuer of tile 0, owner of tensor memory
+//   warp  9    TMA producer, in the next block's tiles while this one ends
+//   warp 10    issuer of tile 1
+//   warp 11    asks for the next block, finds its sequence (find_block), and
+//              zeroes what a sequence's last value tile has of the next one
+// All ring and score barriers count tiles over the CTA's whole life.
+//
+// Rows past a sequence's end are the next sequence's.  Their scores are masked
+// and their queries not stored; a value row, however, enters the product with
+// weight 0, and 0 x infinity is not 0.  So a sequence's last value tile lands on a
+// barrier of its own, and warp 11 hands it on with those rows zeroed.
+//
+// Every wait is bounded as in the forward kernel.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "fa_fwd_kernel.cuh"
+#include "fa_packed.cuh"
+#include "fa_packed.h"
+
+namespace fa {
+namespace packed {
+
+template <int D, bool F16>
+struct Cfg : FwdCfg<false, D, F16> {
+    using Base = FwdCfg<false, D, F16>;
+    // barriers
+    static constexpr int kBarQFull = 0;
+    static constexpr int kBarQEmpty = 1;                             // both issuers' last scores of a block
+    static constexpr int kBarKFull = 2;
+    static constexpr int kBarKEmpty = kBarKFull + Base::kKStages;
+    static constexpr int kBarVFull = kBarKEmpty + Base::kKStages;
+    static constexpr int kBarVEmpty = kBarVFull + Base::kVStages;
+    static constexpr int kBarVRaw = kBarVEmpty + Base::kVStages;     // a sequence's last value tile
+    static constexpr int kBarSFull = kBarVRaw + 1;                   // [2] (not kStageDone)
+    static constexpr int kBarSFree = kBarSFull + 2;                  // [2] kEarlyS: S_w read (4 warps)
+    static constexpr int kBarPFull = kBarSFree + 2;                  // [2 tiles][2 halves]
+    static constexpr int kBarOFull = kBarPFull + 4;                  // [2]
+    static constexpr int kBarOFree = kBarOFull + 2;                  // [2] O_w read (4 warps)
+    static constexpr int kBarTurn = kBarOFree + 2;                   // [2]
+    static constexpr int kBarDrain = kBarTurn + 2;                   // [2]
+    static constexpr int kBarNext = kBarDrain + 2;                   // answer to the request for a block
+    static constexpr int kBarBlockFull = kBarNext + 1;               // [2] a block's description
+    static constexpr int kBarBlockEmpty = kBarBlockFull + 2;         // [2] every reader is done with the block
+    static constexpr int kBarLoaded = kBarBlockEmpty + 2;            // the loads of a block are about to end
+    static constexpr int kNumBars = kBarLoaded + 1;
+    // Key tiles left to load when the next block is asked for.  Asking takes 1
+    // us and finding the sequence 2, a tile 1.8; asked for at a block's start,
+    // the last blocks lay with CTAs that had a long one before them (one
+    // sequence of 8192, causal, H = 32/8, d = 128: 555 us, against %s).
+    static constexpr int kAskAhead = 2;
+    static constexpr int kBlockReaders = 8 + 3;                      // softmax warps, issuers, producer
+    static constexpr int kOffAnswer = (Base::kOffBar + kNumBars * 8 + 15) / 16 * 16;  // 16 bytes
+    static constexpr int kOffBlocks = kOffAnswer + 16;               // int [2][8]
+    static constexpr int kOffTmemSlot = kOffBlocks + 64;
+    static constexpr int kOffAbort = kOffTmemSlot + 4;
+    static constexpr int kOffTurnFlags = kOffAbort + 4;              // [2][4] u32
+    static constexpr size_t kSmemBytes = static_cast<size_t>(kOffTurnFlags + 32) + 1024;  // alignment slack
+    static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
+};
+
+// A block as its readers see it.
+struct Block {
+    int q0, nq, k0, nk, row0, head;  // head of tile 0; row0: first row within the sequence; nq < 0: no more blocks
+    int T;                           // key tiles that its last row sees
+};
+
+__device__ __forceinline__ Block block_of(const int4* in) {
+    const int4 x = in[0], y = in[1];
+    return {x.x, x.y, x.z, x.w, y.x, y.y, y.z};
+}
+
+// Ask for the CTA that would start next: its index, or the answer that there is
+// none, arrives at `answer` (16 bytes) as transaction bytes on `bar`.
+__device__ __forceinline__ void request_next(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(bar)
+                 : "memory");
+}
+// The answer: true and the CTA's blockIdx.x, which will not start.
+__device__ __forceinline__ bool read_next(uint32_t answer, unsigned int& index) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    index = x;
+    return got != 0u;
+}
+
+// Rows of 16-byte chunks out of a warp whose lane r holds row r: four lanes
+// exchange their rows' four chunks (64 bytes), so that a store instruction writes 64
+// contiguous bytes of eight rows instead of 16 of thirty-two.
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+    auto swap = [&](uint4& a, uint4& b, int o) {  // lanes with the bit take b's place for their partner's a
+        const bool up = (lane & o) != 0;
+        uint4 send = up ? a : b;
+        send.x = __shfl_xor_sync(0xffffffffu, send.x, o);
+        send.y = __shfl_xor_sync(0xffffffffu, send.y, o);
+        send.z = __shfl_xor_sync(0xffffffffu, send.z, o);
+        send.w = __shfl_xor_sync(0xffffffffu, send.w, o);
+        if (up) a = send;
+        else b = send;
+    };
+    swap(x[0], x[1], 1);
+    swap(x[2], x[3], 1);
+    swap(x[0], x[2], 2);
+    swap(x[1], x[3], 2);
+}
+
+// Epilogue of a block, by a softmax warpgroup: this thread's row of O / lq, four
+// lanes writing 64 bytes of their four rows in turn (`out`: the first of the
+// four rows, this lane's 16 bytes; `have` of them are the sequence's).  Not inlined: it runs
+// once per block, and as a call it leaves the softmax loop's registers as they
+// are (inlined, 312 to 388 bytes were spilled there at d = 128).
+template <int D, bool F16>
+__device__ __noinline__ void store_rows(uint16_t* out, long long row_stride, int have, bool any, uint32_t tO, float inv_l,
+                                        uint32_t o_free) {
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        if (any) {
+            tmem_ld32(tO + 32u * q, o);
+            tmem_ld_wait(o);
+        } else {  // no visible key: O = 0 (and lse = -inf)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (q == D / 32 - 1 && any) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+        }
+        uint4 x[4];
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+            x[cc].x = pack_16x2<F16>(u2f(o[8 * cc + 0]) * inv_l, u2f(o[8 * cc + 1]) * inv_l);
+            x[cc].y = pack_16x2<F16>(u2f(o[8 * cc + 2]) * inv_l, u2f(o[8 * cc + 3]) * inv_l);
+            x[cc].z = pack_16x2<F16>(u2f(o[8 * cc + 4]) * inv_l, u2f(o[8 * cc + 5]) * inv_l);
+            x[cc].w = pack_16x2<F16>(u2f(o[8 * cc + 6]) * inv_l, u2f(o[8 * cc + 7]) * inv_l);
+        }
+        transpose4(x, lane);
+        uint16_t* row = out + q * 32;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (r < have) *reinterpret_cast<uint4*>(row) = x[r];
+            row += row_stride;
+        }
+    }
+}
+
+template <int D, bool F16, bool kCausal>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v, const PackedFwdParams p) {
+    using C = Cfg<D, F16>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw_u32 & 1023u)) & 1023u;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw_u32 + pad;
+
+    const int warp = static_cast<int>(threadIdx.x) / 32;
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(i); };
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
+
+    if (threadIdx.x == 0) {
+        const unsigned int abort_gen = *reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen);
+        mbar_init(bar(C::kBarQFull), 1);
+        mbar_init(bar(C::kBarQEmpty), 2);
+        for (int s = 0; s < C::kKStages; ++s) {
+            mbar_init(bar(C::kBarKFull + s), 1);
+            mbar_init(bar(C::kBarKEmpty + s), 2);  // both issuers' commits
+        }
+        for (int s = 0; s < C::kVStages; ++s) {
+            mbar_init(bar(C::kBarVFull + s), 1);
+            mbar_init(bar(C::kBarVEmpty + s), 2);
+        }
+        mbar_init(bar(C::kBarVRaw), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(bar(C::kBarSFull + w), 1);
+            mbar_init(bar(C::kBarSFree + w), 4);  // one arrival per softmax warp
+            mbar_init(bar(C::kBarPFull + 2 * w + 0), 4);
+            mbar_init(bar(C::kBarPFull + 2 * w + 1), 4);
+            mbar_init(bar(C::kBarOFull + w), 1);
+            mbar_init(bar(C::kBarOFree + w), 4);
+            mbar_init(bar(C::kBarTurn + w), 4);
+            mbar_init(bar(C::kBarDrain + w), 1);
+            mbar_init(bar(C::kBarBlockFull + w), 1);
+            mbar_init(bar(C::kBarBlockEmpty + w), C::kBlockReaders);
+        }
+        mbar_init(bar(C::kBarNext), 1);
+        mbar_init(bar(C::kBarLoaded), 1);
+        volatile uint32_t* tf = reinterpret_cast<volatile uint32_t*>(smem + C::kOffTurnFlags);
+        for (int i = 0; i < 8; ++i) tf[i] = i < 4 ? 1u : 0u;
+        *abort_flag = (abort_gen == p.gen) ? 1u : 0u;
+        mbar_init_fence();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool skip = *abort_flag != 0u;
+
+    // Block n of the CTA, for one of its readers; false when there is none (or the CTA gives up).
+    auto block_info = [&](int n) { return reinterpret_cast<const int4*>(smem + C::kOffBlocks + (n & 1) * 32); };
+    auto read_block = [&](int n, Block& b) -> bool {
+        if (!wait_phase(bar(C::kBarBlockFull + (n & 1)), (n >> 1) & 1, abort_flag, p, 80)) return false;
+        b = block_of(block_info(n));
+        return b.nq >= 0;
+    };
+    auto done_block = [&](int n) { mbar_arrive(bar(C::kBarBlockEmpty + (n & 1))); };
+
+    if (skip) {
+        // nothing issued: go straight to the teardown
+    } else if (warp >= 8) {
+        regs_decrease<C::kOtherRegs>();
+        if (warp == kTransposeWarp) {
+            // ------------------------------------------------- blocks, tails
+            unsigned int index = blockIdx.x;
+            bool more = true, ok = true;
+            int n = 0, tails = 0, asked = 0;
+            int tail_stage = -1, tail_rows = 0;  // of the block published last
+            int G = 0;                           // key tiles of the blocks published
+            while (ok) {
+                Block b{};
+                b.nq = -1;
+                if (n > 0) {
+                    ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarLoaded), (n - 1) & 1, abort_flag, p, 87));
+                    if (!ok) break;
+                }
+                while (more) {
+                    if (n > 0 || asked > 0) {  // (the first block is the CTA's own)
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(C::kBarNext), 16);
+                            request_next(sbase + C::kOffAnswer, bar(C::kBarNext));
+                        }
+                        ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarNext), (asked - 1) & 1, abort_flag, p, 81, false));
+                        if (!ok) break;
+                        more = read_next(sbase + C::kOffAnswer, index);
+                        fence_proxy_async_smem();  // read before the next answer may be written
+                        __syncwarp();
+                        if (!more) break;
+                    }
+                    ++asked;
+                    int unit;
+                    const SeqBlock f = find_block<false>(p.seqs, kTileM + p.tile_step, p.units, index, unit);
+                    if (f.r >= 0) {
+                        b = {f.q0, f.nq, f.k0, f.nk, f.r * (kTileM + p.tile_step), unit * (1 + p.head_step), 0};
+                        int seen = f.nk;
+                        if (kCausal) seen = min(f.nk, min(b.row0 + kTileM + p.tile_step, f.nq) + f.nk - f.nq);
+                        b.T = seen <= 0 ? 0 : (seen + kTileN - 1) / kTileN;
+                        break;
+                    }
+                    // (the grid is as large as any lengths need)
+                }
+                if (!ok) break;
+                ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarBlockEmpty + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag, p, 82));
+                if (!ok) break;
+                if (lane == 0) {
+                    int4* out = reinterpret_cast<int4*>(smem + C::kOffBlocks + (n & 1) * 32);
+                    out[0] = make_int4(b.q0, b.nq, b.k0, b.nk);
+                    out[1] = make_int4(b.row0, b.head, b.T, 0);
+                    mbar_arrive(bar(C::kBarBlockFull + (n & 1)));
+                }
+                __syncwarp();
+                // the last value tile of the block before, where its sequence ends in it
+                if (tail_stage >= 0) {
+                    ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarVRaw), tails & 1, abort_flag, p, 83));
+                    if (!ok) break;
+                    ++tails;
+                    for (int a = 0; a < C::kAtoms; ++a) {
+                        uint4* rows = reinterpret_cast<uint4*>(smem + C::kOffV + tail_stage * C::kTileBytes + a * C::kAtomBytes);
+                        for (int i = tail_rows * 8 + lane; i < kTileN * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::kBarVFull + tail_stage));
+                }
+                if (b.nq < 0) break;
+                tail_stage = -1;
+                G += b.T;
+                if (b.T > 0 && b.nk - (b.T - 1) * kTileN < kTileN) {
+                    tail_stage = (G - 1) % C::kVStages;
+                    tail_rows = b.nk - (b.T - 1) * kTileN;
+                }
+                ++n;
+            }
+        } else if (warp == kLoadWarp) {
+            // ------------------------------------------------- TMA producer
+            if (lane == 0) {
+                const uint64_t keep = policy_evict_last();
+                const uint64_t once = policy_evict_first();
+                int G = 0, m = 0, tails = 0;  // tiles, blocks with tiles, and sequences' last tiles so far
+                int nk = 0, nv = 0;           // K and V tiles whose loads were issued
+                int last_tail = -C::kVStages;  // V tile that went to the barrier of its own
+                bool ok = true;
+                Block b;
+                for (int n = 0; ok && read_block(n, b); ++n) {
+                    const int kvh = b.head / p.group;
+                    const bool tail = b.nk - (b.T - 1) * kTileN < kTileN;
+                    if (b.T <= C::kAskAhead) mbar_arrive(bar(C::kBarLoaded));
+                    for (int j = 0; j < b.T; ++j, ++G) {
+                        if (j > 0 && j == b.T - C::kAskAhead) mbar_arrive(bar(C::kBarLoaded));
+                        const int ks = G % C::kKStages;
+                        ok = wait_phase(bar(C::kBarKEmpty + ks), ((G / C::kKStages) & 1) ^ 1, abort_flag, p, 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(bar(C::kBarKFull + ks), C::kTileBytes);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_3d(sbase + C::kOffK + ks * C::kTileBytes + a * C::kAtomBytes, &map_k,
+                                        bar(C::kBarKFull + ks), a * C::kAtomElems, b.k0 + j * kTileN, kvh, keep);
+                        nk = G + 1;
+                        if (j == 0) {
+                            ok = wait_phase(bar(C::kBarQEmpty), (m & 1) ^ 1, abort_flag, p, 84);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(bar(C::kBarQFull), 2u * C::kTileBytes);
+                            for (int w = 0; w < 2; ++w)
+                                for (int a = 0; a < C::kAtoms; ++a)
+                                    tma_load_3d(sbase + C::kOffQ + w * C::kTileBytes + a * C::kAtomBytes, &map_q,
+                                                bar(C::kBarQFull), a * C::kAtomElems, b.q0 + b.row0 + w * p.tile_step,
+                                                b.head + w * p.head_step, once);
+                            ++m;
+                        }
+                        const int vs = G % C::kVStages;
+                        ok = wait_phase(bar(C::kBarVEmpty + vs), ((G / C::kVStages) & 1) ^ 1, abort_flag, p, 2);
+                        if (!ok) break;
+                        uint32_t vbar = bar(C::kBarVFull + vs);
+                        if (tail && j + 1 == b.T) {
+                            // the tail before has been handed on (long ago where its stage was loaded again since)
+                            if (G - last_tail < C::kVStages)
+                                ok = wait_phase(bar(C::kBarVFull + last_tail % C::kVStages), (last_tail / C::kVStages) & 1,
+                                                abort_flag, p, 86);
+                            if (!ok) break;
+                            vbar = bar(C::kBarVRaw);
+                            last_tail = G;
+                            ++tails;
+                        }
+                        mbar_arrive_expect_tx(vbar, C::kTileBytes);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_3d(sbase + C::kOffV + vs * C::kTileBytes + a * C::kAtomBytes, &map_v, vbar,
+                                        a * C::kAtomElems, b.k0 + j * kTileN, kvh, keep);
+                        nv = G + 1;
+                    }
+                    done_block(n);
+                }
+                // Drain: every load has landed before the CTA may exit.
+                if (m > 0) wait_phase(bar(C::kBarQFull), (m - 1) & 1, abort_flag, p, 3, false);
+                for (int s = 0; s < C::kKStages && s < nk; ++s) {
+                    const int last = s + ((nk - 1 - s) / C::kKStages) * C::kKStages;
+                    wait_phase(bar(C::kBarKFull + s), (last / C::kKStages) & 1, abort_flag, p, 3, false);
+                }
+                if (tails > 0) wait_phase(bar(C::kBarVRaw), (tails - 1) & 1, abort_flag, p, 3, false);
+                for (int s = 0; s < C::kVStages && s < nv; ++s) {
+                    const int last = s + ((nv - 1 - s) / C::kVStages) * C::kVStages;
+                    if (last == last_tail) continue;  // (its other barrier is warp 11's to complete)
+                    wait_phase(bar(C::kBarVFull + s), (last / C::kVStages) & 1, abort_flag, p, 3, false);
+                }
+            }
+        } else if (lane == 0) {
+            // ------------------------------------------ tensor-core issuers
+            const int w = (warp == kMmaWarp) ? 0 : 1;
+            const uint32_t dS = tmem + 128u * static_cast<uint32_t>(w);
+            const uint32_t dO = tmem + C::kColO + static_cast<uint32_t>(D * w);
+            const uint32_t dP = C::kEarlyS ? tmem + C::kColP + 64u * static_cast<uint32_t>(w) : dS;
+            const uint32_t sQ = sbase + C::kOffQ + w * C::kTileBytes;
+            constexpr bool kDescAdd = D == 128;  // see the forward kernel
+            const uint64_t dQ0 = smem_desc_sw128(sQ, 16, 1024);
+            auto issue_qk = [&](int ks) {
+                const uint32_t sK = sbase + C::kOffK + ks * C::kTileBytes;
+                const uint64_t dK0 = smem_desc_sw128(sK, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < C::kQkSteps; ++kk) {
+                    const uint32_t off = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
+                    const uint64_t da = kDescAdd ? dQ0 + (off >> 4) : smem_desc_sw128(sQ + off, 16, 1024);
+                    const uint64_t db = kDescAdd ? dK0 + (off >> 4) : smem_desc_sw128(sK + off, 16, 1024);
+                    mma_ss<false>(dS, da, db, C::kIdescQK, kk > 0 ? 1u : 0u);
+                }
+            };
+            auto issue_pv = [&](int vs, bool accumulate, int k0, int k1) {
+                const uint32_t sV = sbase + C::kOffV + vs * C::kTileBytes;
+#pragma unroll
+                for (int kk = k0; kk < k1; ++kk) {
+                    const uint64_t db = kDescAdd ? smem_desc_sw128(sV, C::kAtomBytes, 1024) + ((kk * C::kUmmaK * 128) >> 4)
+                                                 : smem_desc_sw128(sV + kk * C::kUmmaK * 128, C::kAtomBytes, 1024);
+                    mma_ts<false>(dO, dP + kk * 8, db, C::kIdescPV, (accumulate || kk > 0) ? 1u : 0u);
+                }
+            };
+            // scores of tile G; `last`: the block's last, behind which its queries are free
+            auto scores = [&](int G, bool last) -> bool {
+                const int ks = G % C::kKStages;
+                if (!wait_phase(bar(C::kBarKFull + ks), (G / C::kKStages) & 1, abort_flag, p, 7)) return false;
+                tc_fence_after();
+                issue_qk(ks);
+                if (!C::kStageDone) tc_commit(bar(C::kBarSFull + w));
+                tc_commit(bar(C::kBarKEmpty + ks));
+                if (last) tc_commit(bar(C::kBarQEmpty));
+                return true;
+            };
+            int G = 0, m = 0;  // tiles and blocks with tiles so far
+            bool ok = true;
+            Block b;
+            for (int n = 0; ok && read_block(n, b); ++n) {
+                const int T = b.T;
+                if (T > 0) {
+                    ok = wait_phase(bar(C::kBarQFull), m & 1, abort_flag, p, 4);
+                    // (kEarlyS) the block before has been read out of S
+                    if (ok && C::kEarlyS && G > 0) ok = wait_phase(bar(C::kBarSFree + w), (G - 1) & 1, abort_flag, p, 14);
+                    if (ok) ok = scores(G, T == 1);
+                }
+                for (int j = 0; ok && j < T; ++j) {
+                    const int g = G + j, vs = g % C::kVStages;
+                    if (C::kEarlyS && j + 1 < T) {
+                        // S(j+1) as soon as the softmax has read S(j)
+                        ok = wait_phase(bar(C::kBarSFree + w), g & 1, abort_flag, p, 14) && scores(g + 1, j + 2 == T);
+                        if (!ok) break;
+                    }
+                    ok = wait_phase(bar(C::kBarVFull + vs), (g / C::kVStages) & 1, abort_flag, p, 5);
+                    if (!ok) break;
+                    // O of the block before has been read
+                    if (j == 0 && m > 0) ok = wait_phase(bar(C::kBarOFree + w), (m - 1) & 1, abort_flag, p, 85);
+                    if (ok) ok = wait_phase(bar(C::kBarPFull + 2 * w), g & 1, abort_flag, p, 6);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(vs, j > 0, 0, C::kPvSteps / 2);
+                    ok = wait_phase(bar(C::kBarPFull + 2 * w + 1), g & 1, abort_flag, p, 6);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(vs, true, C::kPvSteps / 2, C::kPvSteps);
+                    tc_commit(bar(C::kBarVEmpty + vs));
+                    if (j + 1 == T) {
+                        tc_commit(bar(C::kBarOFull + w));
+                    } else if (!C::kEarlyS) {
+                        ok = scores(g + 1, j + 2 == T);
+                    }
+                }
+                G += T;
+                if (T > 0) ++m;
+                done_block(n);
+            }
+            // every tensor-core operation has completed before tensor memory is released
+            tc_commit(bar(C::kBarDrain + w));
+            wait_phase(bar(C::kBarDrain + w), 0, abort_flag, p, 9, false);
+        }
+    } else {
+        // ------------------------------------------------ softmax warpgroups
+        // (the forward kernel's loop; its comments there)
+        regs_increase<C::kSoftmaxRegs>();
+        const int w = warp / 4;
+        const int wi = warp % 4;
+        const int t = wi * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(wi * 32) << 16;
+        const uint32_t tS = tmem + lane_off + 128u * static_cast<uint32_t>(w);
+        const uint32_t tO = tmem + lane_off + C::kColO + static_cast<uint32_t>(D * w);
+        const uint32_t tP = C::kEarlyS ? tmem + lane_off + C::kColP + 64u * static_cast<uint32_t>(w) : tS;
+        const float c = p.scale_log2;
+        constexpr bool kFlagTurns = !kCausal;
+        volatile uint32_t* const turn_mine = reinterpret_cast<volatile uint32_t*>(smem + C::kOffTurnFlags) + 4 * w + wi;
+        volatile uint32_t* const turn_other =
+            reinterpret_cast<volatile uint32_t*>(smem + C::kOffTurnFlags) + 4 * (1 - w) + wi;
+        int G = 0, m = 0;  // tiles and blocks with tiles so far; G counts on inside a block
+        // hand the turn to the other warpgroup after this one's tile G
+        auto pass_turn = [&]() {
+            if (kFlagTurns) *turn_other = static_cast<uint32_t>(G + 1 + w);
+            else mbar_arrive(bar(C::kBarTurn + (1 - w)));
+        };
+        if (!kFlagTurns && C::kTakeTurns && w == 1 && lane == 0) mbar_arrive(bar(C::kBarTurn + 0));
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            int row_limit, T;
+            {
+                Block b;
+                if (!__all_sync(0xffffffffu, read_block(n, b))) break;
+                const int i = b.row0 + w * p.tile_step + t;  // this thread's row of the sequence
+                row_limit = kCausal ? max(-1, min(b.nk, i + 1 + b.nk - b.nq)) : b.nk;
+                T = b.T;
+            }
+            float m_ref = -INFINITY, l = 0.0f, lq = 0.0f;
+            for (int j = 0; j < T; ++j, ++G) {
+                bool got = C::kStageDone ? wait_phase(bar(C::kBarKEmpty + G % C::kKStages), (G / C::kKStages) & 1,
+                                                      abort_flag, p, 10)
+                                         : wait_phase(bar(C::kBarSFull + w), G & 1, abort_flag, p, 10);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                if (C::kTakeTurns) {
+                    got = kFlagTurns ? wait_flag(turn_mine, static_cast<uint32_t>(G + 1), abort_flag, p, 13)
+                                     : wait_phase(bar(C::kBarTurn + w), G & 1, abort_flag, p, 13);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                }
+                tc_fence_after();
+
+                uint32_t s[4][32];
+                float qmax[4];
+                if constexpr (C::kHwMax) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32_max(tS + 32u * q, s[q], qmax[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_wait_red(s[q], qmax[q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32u * q, s[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
+                }
+                auto unmasked_max = [&]() -> float {
+                    if constexpr (C::kHwMax) return fmaxf(fmax3(qmax[0], qmax[1], qmax[2]), qmax[3]);
+                    else return row_extreme<true>(s);
+                };
+                if constexpr (C::kEarlyS) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::kBarSFree + w));
+                }
+                // kEarlyS: P_w and O_w hold the tile before's product until it completes
+                auto wait_prev_product = [&]() -> bool {
+                    if (!C::kEarlyS || j == 0) return true;
+                    const bool done = wait_phase(bar(C::kBarVEmpty + (G - 1) % C::kVStages), ((G - 1) / C::kVStages) & 1,
+                                                 abort_flag, p, 15);
+                    return __all_sync(0xffffffffu, done);
+                };
+
+                const int valid = row_limit - j * kTileN;  // keys of this tile that the row sees
+                const bool masked = kCausal ? __any_sync(0xffffffffu, valid < kTileN) : (valid < kTileN);
+                if (masked) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (q * 32 + e >= valid) s[q][e] = s[0][0];
+                }
+
+                if constexpr (D == 64 || !kCausal) {
+                    if (!masked && j > 0) {
+                        const float shift_s = (m_ref == -INFINITY) ? 0.0f : m_ref;
+                        const uint64_t c2s = f2_pack(c, c);
+                        const uint64_t ns2s = f2_pack(-shift_s, -shift_s);
+                        uint32_t pw0[32];
+                        uint64_t acc_s[4] = {0, 0, 0, 0};
+                        exp_half_regs<F16>(s, c2s, ns2s, 0, pw0, acc_s);
+                        const float mx_s = (c >= 0.0f) ? unmasked_max() : row_extreme<false>(s);
+                        const bool need_s = mx_s * c > m_ref + kRescaleThreshold;
+                        if (!__any_sync(0xffffffffu, need_s)) {
+                            if (!wait_prev_product()) {
+                                ok = false;
+                                break;
+                            }
+                            tmem_st32(tP, pw0);
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(C::kBarPFull + 2 * w + 0));
+                            if (C::kTakeTurns && C::kTurnAfterHalf == 0 && lane == 0) pass_turn();
+                            exp_half<false, F16, false>(s, c2s, ns2s, valid, tP, 1, acc_s);
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(C::kBarPFull + 2 * w + 1));
+                            if (C::kTakeTurns && C::kTurnAfterHalf == 1 && lane == 0) pass_turn();
+                            const float tsum = sum8(acc_s);
+                            const float pmax = ex2(fmaf(mx_s, c, -shift_s));
+                            const float pmax_r = widen_lo16<F16>(pack_16x2<F16>(pmax, 0.0f));
+                            l += tsum;
+                            lq += tsum + (pmax_r - pmax);
+                            continue;
+                        }
+                    }
+                }
+
+                const float mx = (c >= 0.0f) ? (masked ? row_extreme<true>(s) : unmasked_max()) : row_extreme<false>(s);
+                const float m_tile = (!kCausal || valid > 0) ? mx * c : -INFINITY;
+                const float m_new = fmaxf(m_ref, m_tile);
+                const bool need = m_new > m_ref + kRescaleThreshold;  // always true on the first tile
+                const float alpha = need ? ex2(m_ref - m_new) : 1.0f;
+                if (need) {
+                    l *= alpha;
+                    lq *= alpha;
+                    m_ref = m_new;
+                }
+                const float shift = (m_ref == -INFINITY) ? 0.0f : m_ref;
+                if (j > 0 && __any_sync(0xffffffffu, need)) {
+                    if (!wait_prev_product()) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32u * q, o);
+                        tmem_ld_wait(o);
+                        const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float x0, x1;
+                            f2_unpack(f2_mul(f2_pack(u2f(o[e]), u2f(o[e + 1])), a2), x0, x1);
+                            o[e] = f2u(x0);
+                            o[e + 1] = f2u(x1);
+                        }
+                        tmem_st32(tO + 32u * q, o);
+                    }
+                }
+                const uint64_t c2 = f2_pack(c, c);
+                const uint64_t ns2 = f2_pack(-shift, -shift);
+                uint64_t acc[4] = {0, 0, 0, 0};
+                if (!wait_prev_product()) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (masked) exp_half<false, F16, true>(s, c2, ns2, valid, tP, h, acc);
+                    else exp_half<false, F16, false>(s, c2, ns2, valid, tP, h, acc);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::kBarPFull + 2 * w + h));
+                    if (C::kTakeTurns && h == C::kTurnAfterHalf && lane == 0) pass_turn();
+                }
+                const float tsum = sum8(acc);
+                const float pmax = ex2(fmaf(mx, c, -shift));
+                const float pmax_r = widen_lo16<F16>(pack_16x2<F16>(pmax, 0.0f));
+                l += tsum;
+                lq += tsum + ((!kCausal || valid > 0) ? pmax_r - pmax : 0.0f);
+            }
+            if (!ok) break;
+
+            if (T > 0) {
+                ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarOFull + w), m & 1, abort_flag, p, 11));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            {
+                const Block b = block_of(block_info(n));
+                const int head = b.head + w * p.head_step;
+                const int row0 = b.row0 + w * p.tile_step;  // the tile's first row of the sequence
+                if (p.lse != nullptr && row0 + t < b.nq)
+                    p.lse[static_cast<size_t>(head) * p.seqs.Tq + b.q0 + row0 + t] =
+                        (l > 0.0f ? m_ref + log2f(l) : -INFINITY) * 0.69314718055994531f;
+                store_rows<D, F16>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(b.q0 + row0 + (t & ~3)) * p.o_row +
+                                       static_cast<size_t>(head) * p.o_head + (lane & 3) * 8,
+                                   p.o_row, b.nq - (row0 + (t & ~3)), T > 0, tO, lq > 0.0f ? 1.0f / lq : 0.0f,
+                                   bar(C::kBarOFree + w));
+            }
+            if (T > 0) ++m;
+            __syncwarp();
+            if (lane == 0) done_block(n);
+        }
+    }
+
+    // --------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// `grid`: CTAs enough for any lengths.
+template <int D, bool F16, bool kCausal>
+cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PackedFwdParams& p,
+                           unsigned int grid, cudaStream_t stream) {
+    using C = Cfg<D, F16>;
+    auto kern = fa_packed_fwd_kernel<D, F16, kCausal>;
+    static SmemAllowed allowed;
+    const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
+                                          static_cast<int>(kLaunchRegs), allowed);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kThreads, C::kSmemBytes, stream>>>(q, k, v, p);
+    return cudaGetLastError();
+}
+
+}  // namespace packed
+}  // namespace fa

@@ -75,7 +75,8 @@ struct Cfg {
     static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kOffPlan = kOffAbort + 4;        // int [8]: the CTA's run
-    static constexpr int kSmemUsed = kOffPlan + 32;
+    static constexpr int kOffQuery = kOffPlan + 32;       // uint8 [128]: query index of each of a head's rows
+    static constexpr int kSmemUsed = kOffQuery + 128;
     static constexpr size_t kSmemBytes = static_cast<size_t>(kSmemUsed) + 1024;  // alignment slack
     static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
     static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "operand tiles must be 1024-byte aligned");
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
         mbar_init_fence();
     }
+    if (kCausal && threadIdx.x < 128) smem[C::kOffQuery + threadIdx.x] = static_cast<uint8_t>(threadIdx.x % p.Nq);
     if (warp == kDecMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
@@ -378,10 +380,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 l[n] = 0.0f;
                 lq[n] = 0.0f;
             }
-            // is key `key` visible to row n (rows past the last see every key)
+            // is key `key` visible to row n
             auto visible = [&](int n, int key) -> bool {
                 if (key >= k.len) return false;
-                if (kCausal && n < rows) return key <= (row0 + n) % p.Nq + k.len - p.Nq;
+                // (rows past the last are not stored)
+                if (kCausal) return key <= smem[C::kOffQuery + row0 + n] + k.len - p.Nq;
                 return true;
             };
             const int first = k.t, last = k.last();
@@ -403,14 +406,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
                 // x = t - m: the exponent of each weight against the current reference
                 float x[NR];
-                bool need = j == first || !ok;
+                bool need = !ok;
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
                     x[n] = fmaf(u2f(s[n]), c, -m[n]);
                     if (masked && !visible(n, key)) x[n] = -INFINITY;
                     need |= x[n] > kRescaleThreshold;
                 }
-                if (named_barrier_or(kDecNamedBar, 128, need)) {
+                // (a unit's first tile always sets the references: no vote)
+                if (j == first || named_barrier_or(kDecNamedBar, 128, need)) {
                     if (named_barrier_or(kDecNamedBar, 128, !ok)) {  // every thread leaves together
                         ok = false;
                         break;
@@ -554,6 +558,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 8;
 
 // The second kernel: rows whose keys several CTAs shared, or that have a
 // prefix, from their partial results, in order; a warp per row:
@@ -610,16 +615,30 @@ __global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const Paged
         }
         L += l;
         LQ += q;
+        // eight parts' loads at a time; those past the last repeat it with weight 0
         const int here = min(32, parts - i0);
-#pragma unroll 4
-        for (int k = 0; k < here; ++k) {
-            const float f = __shfl_sync(0xffffffffu, w, k);
-            const int i = i0 + k;
-            const float* src = (i < own ? p.unit_o + (slot(i) * rows_per_block + n) * D
-                                        : p.o_part + (static_cast<size_t>(i - own) * total_rows + row) * D) + lane * kPer;
-            if (f == 0.0f) continue;
+        for (int k0 = 0; k0 < here; k0 += kJoinAhead) {
+            float o[kJoinAhead][kPer];
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) acc[x] += f * src[x];
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const int i = i0 + min(k0 + k, here - 1);
+                const float* src = (i < own ? p.unit_o + (slot(i) * rows_per_block + n) * D
+                                            : p.o_part + (static_cast<size_t>(i - own) * total_rows + row) * D) + lane * kPer;
+                if constexpr (kPer == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(src);
+                    o[k][0] = y.x, o[k][1] = y.y, o[k][2] = y.z, o[k][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(src);
+                    o[k][0] = y.x, o[k][1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+                if (k0 + k >= here || f == 0.0f) continue;  // (0 times what a part without keys holds)
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) acc[x] += f * o[k][x];
+            }
         }
     }
     const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
