@@ -11,8 +11,8 @@
 // CTA takes the next one's place before that one starts (cluster launch
 // control), so blocks still begin in the grid's order, heaviest first, on the
 // SM that is free first.
-//   warps 0-7  softmax of tiles 0 and 1, as there; O goes to global memory
-//              from registers, so that the query tiles are free for the next block
+//   warps 0-7  softmax of tiles 0 and 1, as there; O leaves by 4 KB of shared
+//              memory a warp, so that the query tiles are free for the next block
 //   warp  8    issuer of tile 0, owner of tensor memory
 //   warp  9    TMA producer, in the next block's tiles while this one ends
 //   warp 10    issuer of tile 1
@@ -41,14 +41,21 @@ namespace packed {
 template <int D, bool F16>
 struct Cfg : FwdCfg<false, D, F16> {
     using Base = FwdCfg<false, D, F16>;
+    // A K stage less than there (d = 128), whose place the rows of O take on
+    // their way out: 4 KB a warp, 32 rows of 64 channels.
+    static constexpr int kKStages = D == 128 ? 2 : 4;
+    static constexpr int kVStages = Base::kVStages;
+    static constexpr int kOffV = Base::kOffK + kKStages * Base::kTileBytes;
+    static constexpr int kOffRows = kOffV + kVStages * Base::kTileBytes;
+    static constexpr int kOffBar = kOffRows + 8 * 4096;
     // barriers
     static constexpr int kBarQFull = 0;
     static constexpr int kBarQEmpty = 1;                             // both issuers' last scores of a block
     static constexpr int kBarKFull = 2;
-    static constexpr int kBarKEmpty = kBarKFull + Base::kKStages;
-    static constexpr int kBarVFull = kBarKEmpty + Base::kKStages;
-    static constexpr int kBarVEmpty = kBarVFull + Base::kVStages;
-    static constexpr int kBarVRaw = kBarVEmpty + Base::kVStages;     // a sequence's last value tile
+    static constexpr int kBarKEmpty = kBarKFull + kKStages;
+    static constexpr int kBarVFull = kBarKEmpty + kKStages;
+    static constexpr int kBarVEmpty = kBarVFull + kVStages;
+    static constexpr int kBarVRaw = kBarVEmpty + kVStages;     // a sequence's last value tile
     static constexpr int kBarSFull = kBarVRaw + 1;                   // [2] (not kStageDone)
     static constexpr int kBarSFree = kBarSFull + 2;                  // [2] kEarlyS: S_w read (4 warps)
     static constexpr int kBarPFull = kBarSFree + 2;                  // [2 tiles][2 halves]
@@ -67,7 +74,7 @@ struct Cfg : FwdCfg<false, D, F16> {
     // sequence of 8192, causal, H = 32/8, d = 128: 555 us, against %s).
     static constexpr int kAskAhead = 2;
     static constexpr int kBlockReaders = 8 + 3;                      // softmax warps, issuers, producer
-    static constexpr int kOffAnswer = (Base::kOffBar + kNumBars * 8 + 15) / 16 * 16;  // 16 bytes
+    static constexpr int kOffAnswer = (kOffBar + kNumBars * 8 + 15) / 16 * 16;  // 16 bytes
     static constexpr int kOffBlocks = kOffAnswer + 16;               // int [2][8]
     static constexpr int kOffTmemSlot = kOffBlocks + 64;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
@@ -112,66 +119,55 @@ __device__ __forceinline__ bool read_next(uint32_t answer, unsigned int& index) 
     return got != 0u;
 }
 
-// Rows of 16-byte chunks out of a warp whose lane r holds row r: four lanes
-// exchange their rows' four chunks (64 bytes), so that a store instruction writes 64
-// contiguous bytes of eight rows instead of 16 of thirty-two.
-__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
-    auto swap = [&](uint4& a, uint4& b, int o) {  // lanes with the bit take b's place for their partner's a
-        const bool up = (lane & o) != 0;
-        uint4 send = up ? a : b;
-        send.x = __shfl_xor_sync(0xffffffffu, send.x, o);
-        send.y = __shfl_xor_sync(0xffffffffu, send.y, o);
-        send.z = __shfl_xor_sync(0xffffffffu, send.z, o);
-        send.w = __shfl_xor_sync(0xffffffffu, send.w, o);
-        if (up) a = send;
-        else b = send;
-    };
-    swap(x[0], x[1], 1);
-    swap(x[2], x[3], 1);
-    swap(x[0], x[2], 2);
-    swap(x[1], x[3], 2);
-}
-
-// Epilogue of a block, by a softmax warpgroup: this thread's row of O / lq, four
-// lanes writing 64 bytes of their four rows in turn (`out`: the first of the
-// four rows, this lane's 16 bytes; `have` of them are the sequence's).  Not inlined: it runs
-// once per block, and as a call it leaves the softmax loop's registers as they
-// are (inlined, 312 to 388 bytes were spilled there at d = 128).
+// Epilogue of a block, by one softmax warp: its 32 rows of O / lq (lane r has row
+// r) by way of `stage` (4 KB of its own) as whole lines, the rows past `have`
+// left out.  Not inlined: it runs once per block, and as a call it leaves the
+// softmax loop's registers as they are (inlined, 312 to 388 bytes were spilled
+// there at d = 128).  (Four lanes exchanging their rows' pieces by shuffles
+// instead took 2.1 us, this %s.)
 template <int D, bool F16>
 __device__ __noinline__ void store_rows(uint16_t* out, long long row_stride, int have, bool any, uint32_t tO, float inv_l,
-                                        uint32_t o_free) {
+                                        uint8_t* stage, uint32_t o_free) {
     const int lane = static_cast<int>(threadIdx.x) % 32;
 #pragma unroll
-    for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
+    for (int h = 0; h < D / 64; ++h) {
+        uint32_t o[2][32];
         if (any) {
-            tmem_ld32(tO + 32u * q, o);
-            tmem_ld_wait(o);
+            tmem_ld32(tO + 64u * h, o[0]);
+            tmem_ld32(tO + 64u * h + 32u, o[1]);
+            tmem_ld_wait(o[0]);
+            tmem_ld_wait(o[1]);
         } else {  // no visible key: O = 0 (and lse = -inf)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
+            for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0u;
         }
-        if (q == D / 32 - 1 && any) {
+        if (h == D / 64 - 1 && any) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
         }
-        uint4 x[4];
+        if (h > 0) __syncwarp();  // the rows before have been read
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-            x[cc].x = pack_16x2<F16>(u2f(o[8 * cc + 0]) * inv_l, u2f(o[8 * cc + 1]) * inv_l);
-            x[cc].y = pack_16x2<F16>(u2f(o[8 * cc + 2]) * inv_l, u2f(o[8 * cc + 3]) * inv_l);
-            x[cc].z = pack_16x2<F16>(u2f(o[8 * cc + 4]) * inv_l, u2f(o[8 * cc + 5]) * inv_l);
-            x[cc].w = pack_16x2<F16>(u2f(o[8 * cc + 6]) * inv_l, u2f(o[8 * cc + 7]) * inv_l);
+        for (int c = 0; c < 8; ++c) {
+            const uint32_t(&x)[32] = o[c / 4];
+            const int e = (c % 4) * 8;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(pack_16x2<F16>(u2f(x[e]) * inv_l, u2f(x[e + 1]) * inv_l),
+                           pack_16x2<F16>(u2f(x[e + 2]) * inv_l, u2f(x[e + 3]) * inv_l),
+                           pack_16x2<F16>(u2f(x[e + 4]) * inv_l, u2f(x[e + 5]) * inv_l),
+                           pack_16x2<F16>(u2f(x[e + 6]) * inv_l, u2f(x[e + 7]) * inv_l));
         }
-        transpose4(x, lane);
-        uint16_t* row = out + q * 32;
+        __syncwarp();
+        uint16_t* row = out + (lane / 8) * row_stride + 64 * h + (lane % 8) * 8;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (r < have) *reinterpret_cast<uint4*>(row) = x[r];
-            row += row_stride;
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + lane / 8;
+            if (r < have)
+                *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane ^ r) & 7) << 4));
+            row += 4 * row_stride;
         }
     }
+    __syncwarp();  // (the next block's rows go to the same place)
 }
 
 template <int D, bool F16, bool kCausal>
@@ -671,10 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p.lse != nullptr && row0 + t < b.nq)
                     p.lse[static_cast<size_t>(head) * p.seqs.Tq + b.q0 + row0 + t] =
                         (l > 0.0f ? m_ref + log2f(l) : -INFINITY) * 0.69314718055994531f;
-                store_rows<D, F16>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(b.q0 + row0 + (t & ~3)) * p.o_row +
-                                       static_cast<size_t>(head) * p.o_head + (lane & 3) * 8,
-                                   p.o_row, b.nq - (row0 + (t & ~3)), T > 0, tO, lq > 0.0f ? 1.0f / lq : 0.0f,
-                                   bar(C::kBarOFree + w));
+                store_rows<D, F16>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(b.q0 + row0 + wi * 32) * p.o_row +
+                                       static_cast<size_t>(head) * p.o_head,
+                                   p.o_row, b.nq - (row0 + wi * 32), T > 0, tO, lq > 0.0f ? 1.0f / lq : 0.0f,
+                                   smem + C::kOffRows + warp * 4096, bar(C::kBarOFree + w));
             }
             if (T > 0) ++m;
             __syncwarp();
