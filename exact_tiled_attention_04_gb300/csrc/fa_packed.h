@@ -30,6 +30,7 @@ struct PackedFwdParams : FwdParams {
     PackedSeqs seqs;
     int units;                 // heads, or pairs of heads
     int tile_step, head_step;
+    int negate;                // 1: the scale is negative (scale_log2 holds its magnitude, never 0)
     long long o_row, o_head;   // strides of the output in elements
 };
 cudaError_t launch_packed_fwd_bf16(int d, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,

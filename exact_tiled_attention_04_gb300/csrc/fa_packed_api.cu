@@ -180,7 +180,9 @@ int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
     p.splits = 1;
     p.n_q_blocks = 1;
     p.causal = p.seqs.causal;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    // masked scores are -inf, so a scale of 0 becomes one that makes every other score 0
+    p.scale_log2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f);
+    p.negate = scale < 0.0f ? 1 : 0;
     // Groups of an even number of heads: the CTA's two tiles are the same rows of two heads, which see the same keys
     // (a block of 256 rows runs its first tile through keys only the second sees) and leave fewer rows empty.
     const bool pairs = p.group % 2 == 0;

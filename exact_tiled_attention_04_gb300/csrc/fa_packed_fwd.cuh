@@ -83,6 +83,9 @@ struct Cfg : FwdCfg<false, D, F16> {
     static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
 };
 
+// Instruction descriptor: the product of -A and B.
+constexpr uint32_t kNegateA = 1u << 13;
+
 // A block as its readers see it.
 struct Block {
     int q0, nq, k0, nk, row0, head;  // head of tile 0; row0: first row within the sequence; nq < 0: no more blocks
@@ -397,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t sQ = sbase + C::kOffQ + w * C::kTileBytes;
             constexpr bool kDescAdd = D == 128;  // see the forward kernel
             const uint64_t dQ0 = smem_desc_sw128(sQ, 16, 1024);
+            const uint32_t idesc_qk = C::kIdescQK | (p.negate ? kNegateA : 0u);
             auto issue_qk = [&](int ks) {
                 const uint32_t sK = sbase + C::kOffK + ks * C::kTileBytes;
                 const uint64_t dK0 = smem_desc_sw128(sK, 16, 1024);
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t off = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
                     const uint64_t da = kDescAdd ? dQ0 + (off >> 4) : smem_desc_sw128(sQ + off, 16, 1024);
                     const uint64_t db = kDescAdd ? dK0 + (off >> 4) : smem_desc_sw128(sK + off, 16, 1024);
-                    mma_ss<false>(dS, da, db, C::kIdescQK, kk > 0 ? 1u : 0u);
+                    mma_ss<false>(dS, da, db, idesc_qk, kk > 0 ? 1u : 0u);
                 }
             };
             auto issue_pv = [&](int vs, bool accumulate, int k0, int k1) {
@@ -475,7 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------ softmax warpgroups
-        // (the forward kernel's loop; its comments there)
+        // The forward kernel's loop (its comments there) in less code: a short
+        // sequence's tiles are full, masked, first and last ones in turn, and
+        // with a path of its own for each the instruction cache did not hold
+        // them (16 sequences of 512, causal, d = 128: 3.5 warps in a scheduler's
+        // ten waited for instructions).  Masked scores are -inf, so that their weights
+        // come out as 0 by the same path; a negative scale is taken into the
+        // product (kNegateA), so that the reference is a maximum; and the maximum
+        // comes with the scores, so that nothing is gained by exponentials ahead of it.
         regs_increase<C::kSoftmaxRegs>();
         const int w = warp / 4;
         const int wi = warp % 4;
@@ -521,86 +532,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
 
+                // the scores and each 32-key quarter's maximum (reducing load)
                 uint32_t s[4][32];
                 float qmax[4];
-                if constexpr (C::kHwMax) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32_max(tS + 32u * q, s[q], qmax[q]);
+                for (int q = 0; q < 4; ++q) tmem_ld32_max(tS + 32u * q, s[q], qmax[q]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_wait_red(s[q], qmax[q]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32u * q, s[q]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
-                }
-                auto unmasked_max = [&]() -> float {
-                    if constexpr (C::kHwMax) return fmaxf(fmax3(qmax[0], qmax[1], qmax[2]), qmax[3]);
-                    else return row_extreme<true>(s);
-                };
+                for (int q = 0; q < 4; ++q) tmem_ld_wait_red(s[q], qmax[q]);
                 if constexpr (C::kEarlyS) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::kBarSFree + w));
                 }
-                // kEarlyS: P_w and O_w hold the tile before's product until it completes
-                auto wait_prev_product = [&]() -> bool {
-                    if (!C::kEarlyS || j == 0) return true;
-                    const bool done = wait_phase(bar(C::kBarVEmpty + (G - 1) % C::kVStages), ((G - 1) / C::kVStages) & 1,
-                                                 abort_flag, p, 15);
-                    return __all_sync(0xffffffffu, done);
-                };
-
+                float mx = fmaxf(fmax3(qmax[0], qmax[1], qmax[2]), qmax[3]);
                 const int valid = row_limit - j * kTileN;  // keys of this tile that the row sees
-                const bool masked = kCausal ? __any_sync(0xffffffffu, valid < kTileN) : (valid < kTileN);
-                if (masked) {
+                if (kCausal ? __any_sync(0xffffffffu, valid < kTileN) : (valid < kTileN)) {
+                    // the others' weights are 2^-inf
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (q * 32 + e >= valid) s[q][e] = s[0][0];
+                            if (q * 32 + e >= valid) s[q][e] = 0xff800000u;
+                    mx = row_extreme<true>(s);
                 }
 
-                if constexpr (D == 64 || !kCausal) {
-                    if (!masked && j > 0) {
-                        const float shift_s = (m_ref == -INFINITY) ? 0.0f : m_ref;
-                        const uint64_t c2s = f2_pack(c, c);
-                        const uint64_t ns2s = f2_pack(-shift_s, -shift_s);
-                        uint32_t pw0[32];
-                        uint64_t acc_s[4] = {0, 0, 0, 0};
-                        exp_half_regs<F16>(s, c2s, ns2s, 0, pw0, acc_s);
-                        const float mx_s = (c >= 0.0f) ? unmasked_max() : row_extreme<false>(s);
-                        const bool need_s = mx_s * c > m_ref + kRescaleThreshold;
-                        if (!__any_sync(0xffffffffu, need_s)) {
-                            if (!wait_prev_product()) {
-                                ok = false;
-                                break;
-                            }
-                            tmem_st32(tP, pw0);
-                            tmem_st_wait();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(C::kBarPFull + 2 * w + 0));
-                            if (C::kTakeTurns && C::kTurnAfterHalf == 0 && lane == 0) pass_turn();
-                            exp_half<false, F16, false>(s, c2s, ns2s, valid, tP, 1, acc_s);
-                            tmem_st_wait();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(C::kBarPFull + 2 * w + 1));
-                            if (C::kTakeTurns && C::kTurnAfterHalf == 1 && lane == 0) pass_turn();
-                            const float tsum = sum8(acc_s);
-                            const float pmax = ex2(fmaf(mx_s, c, -shift_s));
-                            const float pmax_r = widen_lo16<F16>(pack_16x2<F16>(pmax, 0.0f));
-                            l += tsum;
-                            lq += tsum + (pmax_r - pmax);
-                            continue;
-                        }
-                    }
-                }
-
-                const float mx = (c >= 0.0f) ? (masked ? row_extreme<true>(s) : unmasked_max()) : row_extreme<false>(s);
-                const float m_tile = (!kCausal || valid > 0) ? mx * c : -INFINITY;
-                const float m_new = fmaxf(m_ref, m_tile);
+                // lazy reference, as in the forward kernel
+                const float m_new = fmaxf(m_ref, mx * c);
                 const bool need = m_new > m_ref + kRescaleThreshold;  // always true on the first tile
                 const float alpha = need ? ex2(m_ref - m_new) : 1.0f;
                 if (need) {
@@ -609,12 +566,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_ref = m_new;
                 }
                 const float shift = (m_ref == -INFINITY) ? 0.0f : m_ref;
+                // kEarlyS: P_w and O_w hold the tile before's product until it completes
+                if (C::kEarlyS && j > 0) {
+                    ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarVEmpty + (G - 1) % C::kVStages),
+                                                            ((G - 1) / C::kVStages) & 1, abort_flag, p, 15));
+                    if (!ok) break;
+                }
                 if (j > 0 && __any_sync(0xffffffffu, need)) {
-                    if (!wait_prev_product()) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t o[32];
                         tmem_ld32(tO + 32u * q, o);
@@ -633,14 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t c2 = f2_pack(c, c);
                 const uint64_t ns2 = f2_pack(-shift, -shift);
                 uint64_t acc[4] = {0, 0, 0, 0};
-                if (!wait_prev_product()) {
-                    ok = false;
-                    break;
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (masked) exp_half<false, F16, true>(s, c2, ns2, valid, tP, h, acc);
-                    else exp_half<false, F16, false>(s, c2, ns2, valid, tP, h, acc);
+                    exp_half<false, F16, false>(s, c2, ns2, 0, tP, h, acc);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -651,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float pmax = ex2(fmaf(mx, c, -shift));
                 const float pmax_r = widen_lo16<F16>(pack_16x2<F16>(pmax, 0.0f));
                 l += tsum;
-                lq += tsum + ((!kCausal || valid > 0) ? pmax_r - pmax : 0.0f);
+                lq += tsum + (pmax_r - pmax);
             }
             if (!ok) break;
 

@@ -140,3 +140,10 @@ def test_backward_keys_of_other_lengths(lens, lens_k, causal, d, dtype):
 def test_backward_many_sequences(B, causal):
     lens = [(7 * i * i + 3 * i) % 200 for i in range(B)]
     check_backward(*batch(8, lens, 2, 1, 64, "bf16"), causal)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.0])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_scales(scale, d, causal):
+    check_backward(*batch(9, [200, 1, 130], 4, 2, d, "bf16"), causal, scale)
