@@ -566,6 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_ref = m_new;
                 }
                 const float shift = (m_ref == -INFINITY) ? 0.0f : m_ref;
+                const uint64_t c2 = f2_pack(c, c);
+                const uint64_t ns2 = f2_pack(-shift, -shift);
+                uint64_t acc[4] = {0, 0, 0, 0};
+                // (kEarlyS: the first half's exponentials run ahead of the wait below)
+                uint32_t pw[32];
+                if constexpr (C::kEarlyS) exp_half_regs<F16>(s, c2, ns2, 0, pw, acc);
                 // kEarlyS: P_w and O_w hold the tile before's product until it completes
                 if (C::kEarlyS && j > 0) {
                     ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarVEmpty + (G - 1) % C::kVStages),
@@ -589,12 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st32(tO + 32u * q, o);
                     }
                 }
-                const uint64_t c2 = f2_pack(c, c);
-                const uint64_t ns2 = f2_pack(-shift, -shift);
-                uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    exp_half<false, F16, false>(s, c2, ns2, 0, tP, h, acc);
+                    if (C::kEarlyS && h == 0) tmem_st32(tP, pw);
+                    else exp_half<false, F16, false>(s, c2, ns2, 0, tP, h, acc);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
