@@ -61,8 +61,7 @@ struct Cfg : FwdCfg<false, D, F16> {
     static constexpr int kBarPFull = kBarSFree + 2;                  // [2 tiles][2 halves]
     static constexpr int kBarOFull = kBarPFull + 4;                  // [2]
     static constexpr int kBarOFree = kBarOFull + 2;                  // [2] O_w read (4 warps)
-    static constexpr int kBarTurn = kBarOFree + 2;                   // [2]
-    static constexpr int kBarDrain = kBarTurn + 2;                   // [2]
+    static constexpr int kBarDrain = kBarOFree + 2;                  // [2]
     static constexpr int kBarNext = kBarDrain + 2;                   // answer to the request for a block
     static constexpr int kBarBlockFull = kBarNext + 1;               // [2] a block's description
     static constexpr int kBarBlockEmpty = kBarBlockFull + 2;         // [2] every reader is done with the block
@@ -210,7 +209,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(C::kBarPFull + 2 * w + 1), 4);
             mbar_init(bar(C::kBarOFull + w), 1);
             mbar_init(bar(C::kBarOFree + w), 4);
-            mbar_init(bar(C::kBarTurn + w), 4);
             mbar_init(bar(C::kBarDrain + w), 1);
             mbar_init(bar(C::kBarBlockFull + w), 1);
             mbar_init(bar(C::kBarBlockEmpty + w), C::kBlockReaders);
@@ -496,17 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + lane_off + C::kColO + static_cast<uint32_t>(D * w);
         const uint32_t tP = C::kEarlyS ? tmem + lane_off + C::kColP + 64u * static_cast<uint32_t>(w) : tS;
         const float c = p.scale_log2;
-        constexpr bool kFlagTurns = !kCausal;
         volatile uint32_t* const turn_mine = reinterpret_cast<volatile uint32_t*>(smem + C::kOffTurnFlags) + 4 * w + wi;
         volatile uint32_t* const turn_other =
             reinterpret_cast<volatile uint32_t*>(smem + C::kOffTurnFlags) + 4 * (1 - w) + wi;
         int G = 0, m = 0;  // tiles and blocks with tiles so far; G counts on inside a block
-        // hand the turn to the other warpgroup after this one's tile G
-        auto pass_turn = [&]() {
-            if (kFlagTurns) *turn_other = static_cast<uint32_t>(G + 1 + w);
-            else mbar_arrive(bar(C::kBarTurn + (1 - w)));
-        };
-        if (!kFlagTurns && C::kTakeTurns && w == 1 && lane == 0) mbar_arrive(bar(C::kBarTurn + 0));
+        // hand the turn to the other warpgroup after this one's tile G, warp to
+        // warp through shared counters, with the mask too (by barriers 16384
+        // causal keys and shorter sequences beside them took 2073 us, so 2014)
+        auto pass_turn = [&]() { *turn_other = static_cast<uint32_t>(G + 1 + w); };
         bool ok = true;
         for (int n = 0; ok; ++n) {
             int row_limit, T;
@@ -525,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 if (C::kTakeTurns) {
-                    got = kFlagTurns ? wait_flag(turn_mine, static_cast<uint32_t>(G + 1), abort_flag, p, 13)
-                                     : wait_phase(bar(C::kBarTurn + w), G & 1, abort_flag, p, 13);
+                    got = wait_flag(turn_mine, static_cast<uint32_t>(G + 1), abort_flag, p, 13);
                     ok = __all_sync(0xffffffffu, got);
                     if (!ok) break;
                 }

@@ -12,7 +12,10 @@
 // per CTA (one CTA an SM): none idles because a sequence is short, and a long
 // one is shared by many.  A CTA goes through the units of its run without a
 // pause: the loading warp is up to a ring ahead, in the next unit's keys while
-// the softmax still ends this one, and Q, S^T and O^T have two buffers each.
+// the softmax still ends this one, Q, S^T and O^T have two buffers each, and two
+// softmax warpgroups take the units in turn, as the ends of one (its last
+// product, the sums over 128 threads, its rows' way out) take as long as three of
+// its tiles (64 sequences of up to 512 slots behind a prefix: %s).
 // Of a unit cut between CTAs each leaves a partial result, at most two a CTA,
 // which a second kernel adds up in order, so results do not depend on timing.
 //
@@ -44,6 +47,11 @@ struct Cfg {
     static constexpr int kQkSteps = D / kUmmaK;
     static constexpr int kPvSteps = 128 / kUmmaK;
     static constexpr int kStages = D == 128 ? 3 : 6;  // K+V stages
+    // Softmax warpgroups: two take the run's units in turn (at 32 rows their
+    // registers would not fit).
+    static constexpr int kGroups = NR == 16 ? 2 : 1;
+    static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1;
+    static constexpr int kThreads = (kLoadWarp + 1) * 32;
     static constexpr uint32_t kFmt = F16 ? 0u : 1u;
     static constexpr uint32_t kIdescQK = instr_desc(kFmt, false, false, 128, NR);
     static constexpr uint32_t kIdescPV = instr_desc(kFmt, true, false, 128, NR);
@@ -58,15 +66,16 @@ struct Cfg {
     static constexpr int kOffK = kOffV + kStages * kTileBytes;  // [kStages]
     static constexpr int kOffQ = kOffK + kStages * kTileBytes;  // [2] x kAtoms x NR rows
     static constexpr int kOffP = kOffQ + 2 * kQBytes;           // [2] x 2 atoms x NR rows
-    static constexpr int kOffRed = kOffP + 2 * 2 * kRowAtomBytes;  // float [3][4 warps][NR]
-    static constexpr int kOffBar = kOffRed + 3 * 4 * NR * 4;
+    static constexpr int kRedFloats = 3 * 4 * NR;
+    static constexpr int kOffRed = kOffP + 2 * 2 * kRowAtomBytes;  // float [kGroups][3][4 warps][NR]
+    static constexpr int kOffBar = kOffRed + kGroups * kRedFloats * 4;
     // barriers
     static constexpr int kBarQFull = 0;                   // [2] a unit's Q landed
     static constexpr int kBarQEmpty = kBarQFull + 2;      // [2] its last scores are computed
     static constexpr int kBarFull = kBarQEmpty + 2;       // [kStages] K and V of a tile landed
     static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] both consumed
-    static constexpr int kBarS = kBarEmpty + kStages;     // [2] S^T buffer ready
-    static constexpr int kBarP = kBarS + 2;               // [2] P^T buffer written (4 warps)
+    static constexpr int kBarS = kBarEmpty + kStages;     // [kGroups][2] S^T buffer ready, by the group's own count of tiles
+    static constexpr int kBarP = kBarS + 2 * kGroups;     // [2] P^T buffer written (4 warps)
     static constexpr int kBarPFree = kBarP + 2;           // [2] the product reading it is done
     static constexpr int kBarO = kBarPFree + 2;           // [2] every product of a unit is done
     static constexpr int kBarOFree = kBarO + 2;           // [2] its O^T was read (4 warps)
@@ -165,7 +174,7 @@ __device__ __forceinline__ Cursor first_of(const PagedCache& c, int units, int c
 
 // One CTA per run.  map_q: [B * H_kv, R, d] (d first), boxes of NR rows.
 template <int D, bool F16, bool kCausal, int NR>
-__global__ void __launch_bounds__(kDecThreads, 1)
+__global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
     fa_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const PagedFwdParams p) {
     using C = Cfg<D, F16, NR>;
@@ -187,7 +196,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(C::kBarQFull + b), 1);
             mbar_init(bar(C::kBarQEmpty + b), 1);
-            mbar_init(bar(C::kBarS + b), 1);
+            for (int g = 0; g < C::kGroups; ++g) mbar_init(bar(C::kBarS + 2 * g + b), 1);
             mbar_init(bar(C::kBarP + b), 4);
             mbar_init(bar(C::kBarPFree + b), 1);
             mbar_init(bar(C::kBarO + b), 1);
@@ -202,11 +211,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         mbar_init_fence();
     }
     if (kCausal && threadIdx.x < 128) smem[C::kOffQuery + threadIdx.x] = static_cast<uint8_t>(threadIdx.x % p.Nq);
-    if (warp == kDecMmaWarp) {
+    if (warp == C::kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
     }
-    if (warp == kDecLoadWarp) {
+    if (warp == C::kLoadWarp) {
         if (lane == 0) {
             tma_prefetch_desc(&map_q);
             tma_prefetch_desc(&map_k);
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     if (skip) {
         // nothing (the device error word already reports the failure)
-    } else if (warp == kDecLoadWarp) {
+    } else if (warp == C::kLoadWarp) {
         // ---------------------------------------------------------- producer
         const uint64_t once = policy_evict_first();  // every byte here is read once
         const int pages = 128 / p.c.page;            // of a tile
@@ -292,7 +301,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 wait_phase(bar(C::kBarQFull + b), (last >> 1) & 1, abort_flag, p, 61, false);
             }
         }
-    } else if (warp == kDecMmaWarp) {
+    } else if (warp == C::kMmaWarp) {
         // ------------------------------------------------------------ issuer
         if (lane == 0 && start.valid()) {
             const int total = start.end - start.pos;
@@ -300,6 +309,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             // the next unit, maybe, while this one's are issued: a cursor each
             Cursor ks = start, kv = start;
             int seg_s = 0, seg_v = 0, js = ks.t, jv = kv.t;
+            int scored[C::kGroups] = {};  // tiles of each softmax group so far
             bool ok = true;
             auto issue_s = [&](int it) {
                 if (js == ks.t) ok = wait_phase(bar(C::kBarQFull + (seg_s & 1)), (seg_s >> 1) & 1, abort_flag, p, 62);
@@ -315,7 +325,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     mma_ss<false>(tmem + C::kColS + NR * (it & 1), smem_desc_sw128(sK + koff, 16, 1024),
                                   smem_desc_sw128(sQ + qoff, 16, 1024), C::kIdescQK, kk > 0 ? 1u : 0u);
                 }
-                tc_commit(bar(C::kBarS + (it & 1)));
+                if (C::kGroups == 2 && (seg_s & 1)) tc_commit(bar(C::kBarS + 2 + (scored[C::kGroups - 1]++ & 1)));
+                else tc_commit(bar(C::kBarS + (scored[0]++ & 1)));
                 if (++js == ks.last()) {
                     tc_commit(bar(C::kBarQEmpty + (seg_s & 1)));
                     ks.next(p.c, units);
@@ -357,19 +368,25 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             wait_phase(bar(C::kBarDrain), 0, abort_flag, p, 65, false);
         }
     } else {
-        // ------------------------------------------------ softmax warpgroup
-        const int t = static_cast<int>(threadIdx.x);  // key t of each tile; lane t of O^T
-        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+        // ----------------------------------------------- softmax warpgroups
+        const int group = warp / 4, gwarp = warp % 4;  // of the units seg, every kGroups-th one
+        const int t = static_cast<int>(threadIdx.x) % 128;  // key t of each tile; lane t of O^T
+        const uint32_t lane_base = static_cast<uint32_t>(gwarp * 32) << 16;
+        const uint32_t named = kDecNamedBar + static_cast<uint32_t>(group);
         const uint32_t tS = tmem + lane_base + C::kColS;
         const float c = p.scale_log2;
-        float* red = reinterpret_cast<float*>(smem + C::kOffRed);  // [3][4 warps][NR]
+        float* red = reinterpret_cast<float*>(smem + C::kOffRed) + group * C::kRedFloats;  // [3][4 warps][NR]
         constexpr int kLanesPerRow = 32 / NR;                      // after warp_reduce_rows
         // key t's 16-bit slot in row n of a P^T buffer (see the decode kernel)
         const int pch = (t % 64) / 8;
         uint8_t* pkey = smem + C::kOffP + (t / 64) * C::kRowAtomBytes + (t % 8) * 2;
         bool ok = true;
-        int it = 0, seg = 0;
+        int it = 0, mine = 0, seg = 0;  // tiles, those of this group, units
         for (Cursor k = start; ok && k.valid(); k.next(p.c, units), ++seg) {
+            if (C::kGroups == 2 && (seg & 1) != group) {
+                it += k.last() - k.t;
+                continue;
+            }
             const int row0 = (k.u % p.row_blocks) * NR;
             const int rows = min(p.rows - row0, NR);
             const uint32_t tO = tmem + lane_base + C::kColO + NR * (seg & 1);
@@ -388,13 +405,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 return true;
             };
             const int first = k.t, last = k.last();
-            for (int j = first; j < last; ++j, ++it) {
+            for (int j = first; j < last; ++j, ++it, ++mine) {
                 const int b = it & 1, s_ = it % C::kStages;
                 const int key0 = j * 128;
                 const int key = key0 + t;
                 const bool masked = key0 + 128 > k.len || (kCausal && key0 + 127 > k.len - p.Nq);
                 uint32_t s[NR];
-                if (ok) ok = wait_phase(bar(C::kBarS + b), (it >> 1) & 1, abort_flag, p, 66);
+                if (ok) ok = wait_phase(bar(C::kBarS + 2 * group + (mine & 1)), (mine >> 1) & 1, abort_flag, p, 66);
                 ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-wide
                 if (ok) {
                     tc_fence_after();
@@ -414,8 +431,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     need |= x[n] > kRescaleThreshold;
                 }
                 // (a unit's first tile always sets the references: no vote)
-                if (j == first || named_barrier_or(kDecNamedBar, 128, need)) {
-                    if (named_barrier_or(kDecNamedBar, 128, !ok)) {  // every thread leaves together
+                if (j == first || named_barrier_or(named, 128, need)) {
+                    if (named_barrier_or(named, 128, !ok)) {  // every thread leaves together
                         ok = false;
                         break;
                     }
@@ -424,8 +441,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
                     for (int n = 0; n < NR; ++n) v[n] = (masked && !visible(n, key)) ? -INFINITY : u2f(s[n]) * c;
                     const float r = warp_reduce_rows<NR, true>(v, lane);
-                    if (lane % kLanesPerRow == 0) red[warp * NR + lane / kLanesPerRow] = r;
-                    named_barrier_sync(kDecNamedBar, 128);
+                    if (lane % kLanesPerRow == 0) red[gwarp * NR + lane / kLanesPerRow] = r;
+                    named_barrier_sync(named, 128);
                     float alpha[NR];
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
@@ -490,7 +507,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             // --------------------------------------------- the unit's result
             if (ok) ok = wait_phase(bar(C::kBarO + (seg & 1)), (seg >> 1) & 1, abort_flag, p, 69);
             ok = __all_sync(0xffffffffu, ok);
-            if (named_barrier_or(kDecNamedBar, 128, !ok)) {
+            if (named_barrier_or(named, 128, !ok)) {
                 ok = false;
                 break;
             }
@@ -505,10 +522,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const float rl = warp_reduce_rows<NR, false>(l, lane);
             const float rq = warp_reduce_rows<NR, false>(lq, lane);
             if (lane % kLanesPerRow == 0) {
-                red[4 * NR + warp * NR + lane / kLanesPerRow] = rl;
-                red[8 * NR + warp * NR + lane / kLanesPerRow] = rq;
+                red[4 * NR + gwarp * NR + lane / kLanesPerRow] = rl;
+                red[8 * NR + gwarp * NR + lane / kLanesPerRow] = rq;
             }
-            named_barrier_sync(kDecNamedBar, 128);
+            named_barrier_sync(named, 128);
             const bool whole = first == 0 && last == k.tiles();
             const long long unit = static_cast<long long>(k.b) * units + k.u;
             if (whole && !p.parts_always) {
@@ -550,7 +567,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // --------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
-    if (warp == kDecMmaWarp) {
+    if (warp == C::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
@@ -656,7 +673,7 @@ cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUt
     static SmemAllowed allowed;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes), allowed);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), kDecThreads, C::kSmemBytes, stream, q, k, v, p);
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), C::kThreads, C::kSmemBytes, stream, q, k, v, p);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
     return launch_dependent(fa_paged_join_kernel<D, F16>, dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
