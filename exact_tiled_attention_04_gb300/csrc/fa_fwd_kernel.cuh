@@ -60,15 +60,9 @@
 #include <cstdint>
 
 #include "fa_internal.h"
-#include "fa_paged.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
-
-// What a launch's query blocks are (kMode): blocks of a [B, H, N, d] tensor, or
-// the rows that several sequences have for one key/value head, over the pages of
-// a prefix (PrefixFwdParams).
-constexpr int kModeBatch = 0, kModePrefix = 1;
 
 constexpr int kTileM = 128;  // query rows per softmax warpgroup = TMEM lanes
 constexpr int kTileN = 128;  // keys per K/V tile
@@ -729,86 +723,13 @@ __device__ __forceinline__ void cluster_merge(const FwdParams& p, uint8_t* smem,
     cluster_sync_all();
 }
 
-// Producer warp of a prefix launch: query rows of several sequences, keys and
-// values page by page (a box per lane).  Value rows behind the prefix's end, in
-// its last page or in pages that are not loaded, are zeroed as above.
-template <int D, bool F16, bool kOneTile>
-__device__ __forceinline__ void produce_prefix(const CUtensorMap& map_q, const CUtensorMap& map_k,
-                                               const CUtensorMap& map_v, const PrefixFwdParams& p, uint8_t* smem,
-                                               uint32_t sbase, int lane, int seq0, int kvh, int t_begin, int T,
-                                               volatile uint32_t* abort_flag) {
-    using C = FwdCfg<false, D, F16>;
-    auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBar + 8u * static_cast<uint32_t>(i); };
-    constexpr int kTiles = kOneTile ? 1 : 2;
-    const uint64_t keep = policy_evict_last();
-    const int end = p.Nkv - (t_begin + T - 1) * kTileN;  // keys of the last tile
-    const bool tail = end < kTileN;
-    const int per_tile = kTileN / p.page, mine = lane / C::kAtoms, atom = lane % C::kAtoms;
-    if (lane == 0) {
-        mbar_arrive_expect_tx(bar(C::kBarQFull), static_cast<uint32_t>(kTiles * C::kAtoms * p.rows * p.seqs * 128));
-        for (int w = 0; w < kTiles; ++w)
-            for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_4d(sbase + C::kOffQ + w * C::kTileBytes + a * C::kAtomBytes, &map_q, bar(C::kBarQFull),
-                            a * C::kAtomElems, 0, kvh, seq0 + w * p.seqs, keep);
-    }
-    int nk = 0, nv = 0;  // K and V tiles whose loads were issued
-    for (int j = 0; j < T; ++j) {
-        const int page0 = (t_begin + j) * per_tile, have = min(per_tile, p.n_pages - page0);
-        const int id = mine < have ? p.pages[page0 + mine] : 0;
-        const uint32_t bytes = static_cast<uint32_t>(have * p.page * C::kAtoms * 128);
-        const int ks = j % C::kKStages, vs = j % C::kVStages;
-        if (!__all_sync(0xffffffffu, wait_phase(bar(C::kBarKEmpty + ks), ((j / C::kKStages) & 1) ^ 1, abort_flag, p, 1)))
-            break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarKFull + ks), bytes);
-        __syncwarp();
-        if (mine < have)
-            tma_load_4d(sbase + C::kOffK + ks * C::kTileBytes + atom * C::kAtomBytes + mine * p.page * 128, &map_k,
-                        bar(C::kBarKFull + ks), atom * C::kAtomElems, 0, kvh, id, keep);
-        nk = j + 1;
-        if (!__all_sync(0xffffffffu, wait_phase(bar(C::kBarVEmpty + vs), ((j / C::kVStages) & 1) ^ 1, abort_flag, p, 2)))
-            break;
-        const uint32_t vbar = tail && j + 1 == T ? bar(C::kBarVRaw) : bar(C::kBarVFull + vs);
-        if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
-        __syncwarp();
-        if (mine < have)
-            tma_load_4d(sbase + C::kOffV + vs * C::kTileBytes + atom * C::kAtomBytes + mine * p.page * 128, &map_v, vbar,
-                        atom * C::kAtomElems, 0, kvh, id, keep);
-        nv = j + 1;
-    }
-    __syncwarp();
-    if (tail && nv == T) {
-        const int vs = (T - 1) % C::kVStages;
-        if (__all_sync(0xffffffffu, wait_phase(bar(C::kBarVRaw), 0, abort_flag, p, 3, false))) {
-            for (int a = 0; a < C::kAtoms; ++a) {
-                uint4* rows = reinterpret_cast<uint4*>(smem + C::kOffV + vs * C::kTileBytes + a * C::kAtomBytes);
-                for (int i = end * 8 + lane; i < kTileN * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::kBarVFull + vs));
-        }
-    }
-    if (lane == 0) {
-        wait_phase(bar(C::kBarQFull), 0, abort_flag, p, 3, false);
-        for (int s = 0; s < C::kKStages && s < nk; ++s) {
-            const int last = s + ((nk - 1 - s) / C::kKStages) * C::kKStages;
-            wait_phase(bar(C::kBarKFull + s), (last / C::kKStages) & 1, abort_flag, p, 3, false);
-        }
-        for (int s = 0; s < C::kVStages && s < nv; ++s) {
-            const int last = s + ((nv - 1 - s) / C::kVStages) * C::kVStages;
-            wait_phase(bar(C::kBarVFull + s), (last / C::kVStages) & 1, abort_flag, p, 3, false);
-        }
-    }
-}
-
 // kOneTile: a packed launch (p.pack = 1), where query tile 1 holds no row;
 // a template parameter so that unpacked launches carry none of its checks.
-template <bool TF32, int D, bool F16 = false, bool kCausal = false, bool kOneTile = false, int kMode = kModeBatch,
-          class Params = FwdParams>
+template <bool TF32, int D, bool F16 = false, bool kCausal = false, bool kOneTile = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
-                  const Params p) {
+                  const FwdParams p) {
     using C = FwdCfg<TF32, D, F16>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -821,15 +742,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // blockIdx.x = cta * splits + split; cta = bh * n_q_blocks + qb, or
     // (causal) the heavy-first order of lpt_item over (bh, block)
     // grouped heads packed into query tile 0 (p.pack; always set when kOneTile)
-    const bool pack = kMode == kModeBatch && (kOneTile || p.pack != 0);
+    const bool pack = kOneTile || p.pack != 0;
     const unsigned int split = blockIdx.x % static_cast<unsigned>(p.splits);
     // (a tail launch starts at query block p.item_offset; unmasked launches only)
     const unsigned int cta = blockIdx.x / static_cast<unsigned>(p.splits) + static_cast<unsigned>(p.item_offset);
     int qb, bh;
-    if constexpr (kMode == kModePrefix) {
-        qb = static_cast<int>(cta % static_cast<unsigned>(p.blocks));  // of the sequences
-        bh = static_cast<int>(cta / static_cast<unsigned>(p.blocks));  // the key/value head
-    } else if (kCausal) {
+    if (kCausal) {
         // later query blocks see more keys: heaviest first, by groups of heads
         // (packed launches have one block per key/value head)
         const int units = static_cast<int>(gridDim.x / static_cast<unsigned>(p.splits)) / p.n_q_blocks;
@@ -843,17 +761,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // key/value head of this query head (grouped-query attention: H / H_kv
     // query heads share one key/value head)
     // packed: bh is the key/value head itself; otherwise its query head's
-    int kvh = pack ? bh : (bh / p.H) * p.H_kv + (bh % p.H) / p.group;
+    const int kvh = pack ? bh : (bh / p.H) * p.H_kv + (bh % p.H) / p.group;
     // rows of query tile 0 that hold query rows in a packed launch
     const int pack_rows = pack ? p.Nq * p.group : 0;
     // packed launches hold no query row in tile 1: its issuer and softmax
     // warpgroup sit out, and K/V stages are released by tile 0 alone
     constexpr bool one_tile = kOneTile;
-    const int row0 = kMode == kModePrefix ? 0 : qb * 2 * kTileM;
-    if constexpr (kMode == kModePrefix) kvh = bh;
-    // prefix launches: the first sequence of tile 0
-    [[maybe_unused]] int seq0 = 0;
-    if constexpr (kMode == kModePrefix) seq0 = qb * (kOneTile ? 1 : 2) * p.seqs;
+    const int row0 = qb * 2 * kTileM;
     // key tiles this query block can see: all, or under the causal mask
     // those up to the last key its last row sees
     int n_tiles_block = p.n_kv_tiles;
@@ -943,9 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (the split last wave) may place its CTAs as this grid's leave the SMs
         if (lane == 0) asm volatile("griddepcontrol.launch_dependents;");
         if (!TF32 && pack) zero_unloaded_q<C::kTileBytes, C::kAtoms, C::kAtomBytes>(smem + C::kOffQ, pack_rows, lane);
-        if constexpr (kMode == kModePrefix) {
-            produce_prefix<D, F16, kOneTile>(map_q, map_k, map_v, p, smem, sbase, lane, seq0, kvh, t_begin, T, abort_flag);
-        } else if constexpr (TF32) {
+        if constexpr (TF32) {
             produce_tf32<D>(map_q, map_k, map_v, p, smem, sbase, lane, row0, bh, kvh, t_begin, T, abort_flag);
         } else if (lane == 0) {
             const uint64_t keep = policy_evict_last();   // K/V: read by every query block of the head
@@ -1139,10 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             out_row = r < pack_rows ? (static_cast<long long>(bh) * p.group + r / p.Nq) * p.Nq + qi : -1;
         }
         int row_limit = p.Nkv;
-        if constexpr (kMode == kModePrefix) {
-            const int b = seq0 + w * p.seqs + t / p.rows;
-            out_row = t < p.rows * p.seqs && b < p.B ? (static_cast<long long>(b) * p.H_kv + kvh) * p.rows + t % p.rows : -1;
-        } else if (kCausal) {
+        if (kCausal) {
             const long long lim = qi + p.causal_offset + 1;
             row_limit = static_cast<int>(max(-1ll, min(static_cast<long long>(p.Nkv), lim)));
         }
@@ -1387,7 +1296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, got);
         }
         uint8_t* stage = smem + C::kOffQ + w * C::kTileBytes;  // Q_w is free after its last S MMA
-        const bool split_mode = kMode == kModePrefix || p.splits > 1;
+        const bool split_mode = p.splits > 1;
         if (ok && split_mode && active) {
             tc_fence_after();
             if (has_work) {
@@ -1498,27 +1407,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // CTA completes only after the grid before it in the stream, so that
     // work after this launch still sees both (returns at once otherwise)
     if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;");
-}
-
-// Prefix launches.
-template <int D, bool F16, bool kOneTile>
-cudaError_t launch_prefix_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                                  const PrefixFwdParams& p, cudaStream_t stream) {
-    using C = FwdCfg<false, D, F16>;
-    auto kern = fa_fwd_kernel<false, D, F16, false, kOneTile, kModePrefix, PrefixFwdParams>;
-    static SmemAllowed allowed;
-    const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
-                                          static_cast<int>(kLaunchRegs), allowed);
-    if (e != cudaSuccess) return e;
-    // (launched without overlap: the kernel behind it relies on this one having begun after all before it)
-    kern<<<static_cast<unsigned>(p.H_kv * p.blocks * p.splits), kThreads, C::kSmemBytes, stream>>>(q, k, v, q, p);
-    return cudaGetLastError();
-}
-template <int D, bool F16>
-cudaError_t launch_prefix(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PrefixFwdParams& p,
-                          cudaStream_t stream) {
-    return p.B <= p.seqs ? launch_prefix_variant<D, F16, true>(q, k, v, p, stream)
-                         : launch_prefix_variant<D, F16, false>(q, k, v, p, stream);
 }
 
 template <bool TF32, int D, bool F16, bool kCausal, bool kOneTile>

@@ -25,6 +25,10 @@
 // weight 0, and 0 x infinity is not 0.  So a sequence's last value tile lands on a
 // barrier of its own, and warp 11 hands it on with those rows zeroed.
 //
+// The same kernel (kPrefix) goes over the pages of a prefix that a batch of
+// sequences shares: a block's rows are those of several sequences, its keys a
+// partition of the prefix, its result a partial one (PrefixFwdParams).
+//
 // Every wait is bounded as in the forward kernel.
 #pragma once
 
@@ -34,6 +38,7 @@
 #include "fa_fwd_kernel.cuh"
 #include "fa_packed.cuh"
 #include "fa_packed.h"
+#include "fa_paged.h"
 
 namespace fa {
 namespace packed {
@@ -72,7 +77,6 @@ struct Cfg : FwdCfg<false, D, F16> {
     // the last blocks lay with CTAs that had a long one before them (one
     // sequence of 8192, causal, H = 32/8, d = 128: 555 us, against %s).
     static constexpr int kAskAhead = 2;
-    static constexpr int kBlockReaders = 8 + 3;                      // softmax warps, issuers, producer
     static constexpr int kOffAnswer = (kOffBar + kNumBars * 8 + 15) / 16 * 16;  // 16 bytes
     static constexpr int kOffBlocks = kOffAnswer + 16;               // int [2][8]
     static constexpr int kOffTmemSlot = kOffBlocks + 64;
@@ -85,7 +89,8 @@ struct Cfg : FwdCfg<false, D, F16> {
 // Instruction descriptor: the product of -A and B.
 constexpr uint32_t kNegateA = 1u << 13;
 
-// A block as its readers see it.
+// A block as its readers see it (kPrefix: q0 the first sequence, nq 0, k0 the
+// first key tile, nk the prefix's keys, row0 the partition, head the key/value head).
 struct Block {
     int q0, nq, k0, nk, row0, head;  // head of tile 0; row0: first row within the sequence; nq < 0: no more blocks
     int T;                           // key tiles that its last row sees
@@ -172,10 +177,43 @@ __device__ __noinline__ void store_rows(uint16_t* out, long long row_stride, int
     __syncwarp();  // (the next block's rows go to the same place)
 }
 
-template <int D, bool F16, bool kCausal>
+// Epilogue of a prefix's block: the warp's 32 rows of O as they are, lane r's row
+// to row `out_row` of the partition's slab (-1: not a query row) by way of
+// `stage`, and their statistics.
+template <int D>
+__device__ __noinline__ void store_part(float* o_part, float4* ml_part, long long out_row, uint32_t tO, float4 ml,
+                                        uint8_t* stage, uint32_t o_free) {
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    if (out_row >= 0) ml_part[out_row] = ml;
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32u * q, o);
+        tmem_ld_wait(o);
+        if (q == D / 32 - 1) tc_fence_before();
+        __syncwarp();  // the rows before have been read (and, the last time, all loads are done)
+        if (q == D / 32 - 1 && lane == 0) mbar_arrive(o_free);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + lane / 8;
+            const long long row = __shfl_sync(0xffffffffu, out_row, r);
+            if (row >= 0)
+                *reinterpret_cast<uint4*>(o_part + row * D + 32 * q + (lane % 8) * 4) =
+                    *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane ^ r) & 7) << 4));
+        }
+    }
+    __syncwarp();
+}
+
+template <int D, bool F16, bool kCausal, bool kPrefix, class Params>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v, const PackedFwdParams p) {
+                         const __grid_constant__ CUtensorMap map_v, const Params p) {
     using C = Cfg<D, F16>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -189,17 +227,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::kOffAbort);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
 
+    int tiles = 2;  // of a block; with one, the second issuer and warpgroup sit out
+    if constexpr (kPrefix) tiles = 1 + p.pair;
+
     if (threadIdx.x == 0) {
         const unsigned int abort_gen = *reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen);
         mbar_init(bar(C::kBarQFull), 1);
-        mbar_init(bar(C::kBarQEmpty), 2);
+        mbar_init(bar(C::kBarQEmpty), tiles);
         for (int s = 0; s < C::kKStages; ++s) {
             mbar_init(bar(C::kBarKFull + s), 1);
-            mbar_init(bar(C::kBarKEmpty + s), 2);  // both issuers' commits
+            mbar_init(bar(C::kBarKEmpty + s), tiles);  // the issuers' commits
         }
         for (int s = 0; s < C::kVStages; ++s) {
             mbar_init(bar(C::kBarVFull + s), 1);
-            mbar_init(bar(C::kBarVEmpty + s), 2);
+            mbar_init(bar(C::kBarVEmpty + s), tiles);
         }
         mbar_init(bar(C::kBarVRaw), 1);
         for (int w = 0; w < 2; ++w) {
@@ -211,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(C::kBarOFree + w), 4);
             mbar_init(bar(C::kBarDrain + w), 1);
             mbar_init(bar(C::kBarBlockFull + w), 1);
-            mbar_init(bar(C::kBarBlockEmpty + w), C::kBlockReaders);
+            mbar_init(bar(C::kBarBlockEmpty + w), 5 * tiles + 1);  // softmax warps, issuers, producer
         }
         mbar_init(bar(C::kBarNext), 1);
         mbar_init(bar(C::kBarLoaded), 1);
@@ -243,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return b.nq >= 0;
     };
     auto done_block = [&](int n) { mbar_arrive(bar(C::kBarBlockEmpty + (n & 1))); };
+
+    if (kPrefix) grid_release();  // the kernel behind may be set up
 
     if (skip) {
         // nothing issued: go straight to the teardown
@@ -276,16 +319,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!more) break;
                     }
                     ++asked;
-                    int unit;
-                    const SeqBlock f = find_block<false>(p.seqs, kTileM + p.tile_step, p.units, index, unit);
-                    if (f.r >= 0) {
-                        b = {f.q0, f.nq, f.k0, f.nk, f.r * (kTileM + p.tile_step), unit * (1 + p.head_step), 0};
-                        int seen = f.nk;
-                        if (kCausal) seen = min(f.nk, min(b.row0 + kTileM + p.tile_step, f.nq) + f.nk - f.nq);
-                        b.T = seen <= 0 ? 0 : (seen + kTileN - 1) / kTileN;
+                    if constexpr (kPrefix) {
+                        const int i = static_cast<int>(index), split = i % p.splits, rest = i / p.splits;
+                        const int t0 = split * p.tiles_per_split;
+                        b = {rest % p.blocks * tiles * p.seqs, 0, t0, p.Nkv, split, rest / p.blocks,
+                             min(p.tiles_per_split, p.n_kv_tiles - t0)};
                         break;
+                    } else {
+                        int unit;
+                        const SeqBlock f = find_block<false>(p.seqs, kTileM + p.tile_step, p.units, index, unit);
+                        if (f.r >= 0) {
+                            b = {f.q0, f.nq, f.k0, f.nk, f.r * (kTileM + p.tile_step), unit * (1 + p.head_step), 0};
+                            int seen = f.nk;
+                            if (kCausal) seen = min(f.nk, min(b.row0 + kTileM + p.tile_step, f.nq) + f.nk - f.nq);
+                            b.T = seen <= 0 ? 0 : (seen + kTileN - 1) / kTileN;
+                            break;
+                        }
+                        // (the grid is as large as any lengths need)
                     }
-                    // (the grid is as large as any lengths need)
                 }
                 if (!ok) break;
                 ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarBlockEmpty + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag, p, 82));
@@ -313,15 +364,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (b.nq < 0) break;
                 tail_stage = -1;
                 G += b.T;
-                if (b.T > 0 && b.nk - (b.T - 1) * kTileN < kTileN) {
+                const int end = b.nk - ((kPrefix ? b.k0 : 0) + b.T - 1) * kTileN;  // keys of the last tile
+                if (b.T > 0 && end < kTileN) {
                     tail_stage = (G - 1) % C::kVStages;
-                    tail_rows = b.nk - (b.T - 1) * kTileN;
+                    tail_rows = end;
                 }
                 ++n;
             }
         } else if (warp == kLoadWarp) {
             // ------------------------------------------------- TMA producer
-            if (lane == 0) {
+            // (a prefix's boxes are dealt to the lanes, a page of 64 channels each)
+            if (lane == 0 || kPrefix) {
                 const uint64_t keep = policy_evict_last();
                 const uint64_t once = policy_evict_first();
                 int G = 0, m = 0, tails = 0;  // tiles, blocks with tiles, and sequences' last tiles so far
@@ -329,52 +382,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int last_tail = -C::kVStages;  // V tile that went to the barrier of its own
                 bool ok = true;
                 Block b;
-                for (int n = 0; ok && read_block(n, b); ++n) {
-                    const int kvh = b.head / p.group;
-                    const bool tail = b.nk - (b.T - 1) * kTileN < kTileN;
-                    if (b.T <= C::kAskAhead) mbar_arrive(bar(C::kBarLoaded));
+                // every lane's wait, or the one lane's
+                auto all = [&](bool got) -> bool { return kPrefix ? __all_sync(0xffffffffu, got) : got; };
+                for (int n = 0; ok && all(read_block(n, b)); ++n) {
+                    const bool tail = b.nk - ((kPrefix ? b.k0 : 0) + b.T - 1) * kTileN < kTileN;
+                    // tile j's rows of K or V
+                    [[maybe_unused]] int id = 0, pages = 0;  // (a prefix: this lane's page of the tile, and how many it has)
+                    auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t full, int j) {
+                        if constexpr (kPrefix) {
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(full, static_cast<uint32_t>(pages * p.page * C::kAtoms * 128));
+                            __syncwarp();
+                            const int mine = lane / C::kAtoms, a = lane % C::kAtoms;
+                            if (mine < pages)
+                                tma_load_4d(dst + a * C::kAtomBytes + mine * p.page * 128, map, full, a * C::kAtomElems, 0,
+                                            b.head, id, keep);
+                            __syncwarp();
+                        } else {
+                            mbar_arrive_expect_tx(full, C::kTileBytes);
+                            for (int a = 0; a < C::kAtoms; ++a)
+                                tma_load_3d(dst + a * C::kAtomBytes, map, full, a * C::kAtomElems, b.k0 + j * kTileN,
+                                            b.head / p.group, keep);
+                        }
+                    };
+                    if (lane == 0 && b.T <= C::kAskAhead) mbar_arrive(bar(C::kBarLoaded));
                     for (int j = 0; j < b.T; ++j, ++G) {
-                        if (j > 0 && j == b.T - C::kAskAhead) mbar_arrive(bar(C::kBarLoaded));
+                        if (lane == 0 && j > 0 && j == b.T - C::kAskAhead) mbar_arrive(bar(C::kBarLoaded));
+                        if constexpr (kPrefix) {
+                            const int page0 = (b.k0 + j) * (kTileN / p.page);
+                            pages = min(kTileN / p.page, p.n_pages - page0);
+                            id = lane / C::kAtoms < pages ? p.pages[page0 + lane / C::kAtoms] : 0;
+                        }
                         const int ks = G % C::kKStages;
-                        ok = wait_phase(bar(C::kBarKEmpty + ks), ((G / C::kKStages) & 1) ^ 1, abort_flag, p, 1);
+                        ok = all(wait_phase(bar(C::kBarKEmpty + ks), ((G / C::kKStages) & 1) ^ 1, abort_flag, p, 1));
                         if (!ok) break;
-                        mbar_arrive_expect_tx(bar(C::kBarKFull + ks), C::kTileBytes);
-                        for (int a = 0; a < C::kAtoms; ++a)
-                            tma_load_3d(sbase + C::kOffK + ks * C::kTileBytes + a * C::kAtomBytes, &map_k,
-                                        bar(C::kBarKFull + ks), a * C::kAtomElems, b.k0 + j * kTileN, kvh, keep);
+                        load(sbase + C::kOffK + ks * C::kTileBytes, &map_k, bar(C::kBarKFull + ks), j);
                         nk = G + 1;
                         if (j == 0) {
-                            ok = wait_phase(bar(C::kBarQEmpty), (m & 1) ^ 1, abort_flag, p, 84);
+                            ok = all(wait_phase(bar(C::kBarQEmpty), (m & 1) ^ 1, abort_flag, p, 84));
                             if (!ok) break;
-                            mbar_arrive_expect_tx(bar(C::kBarQFull), 2u * C::kTileBytes);
-                            for (int w = 0; w < 2; ++w)
-                                for (int a = 0; a < C::kAtoms; ++a)
-                                    tma_load_3d(sbase + C::kOffQ + w * C::kTileBytes + a * C::kAtomBytes, &map_q,
-                                                bar(C::kBarQFull), a * C::kAtomElems, b.q0 + b.row0 + w * p.tile_step,
-                                                b.head + w * p.head_step, once);
+                            if constexpr (kPrefix) {
+                                if (lane == 0) {
+                                    mbar_arrive_expect_tx(bar(C::kBarQFull),
+                                                          static_cast<uint32_t>(tiles * C::kAtoms * p.rows * p.seqs * 128));
+                                    for (int w = 0; w < tiles; ++w)
+                                        for (int a = 0; a < C::kAtoms; ++a)
+                                            tma_load_4d(sbase + C::kOffQ + w * C::kTileBytes + a * C::kAtomBytes, &map_q,
+                                                        bar(C::kBarQFull), a * C::kAtomElems, 0, b.head, b.q0 + w * p.seqs, keep);
+                                }
+                                __syncwarp();
+                            } else {
+                                mbar_arrive_expect_tx(bar(C::kBarQFull), 2u * C::kTileBytes);
+                                for (int w = 0; w < 2; ++w)
+                                    for (int a = 0; a < C::kAtoms; ++a)
+                                        tma_load_3d(sbase + C::kOffQ + w * C::kTileBytes + a * C::kAtomBytes, &map_q,
+                                                    bar(C::kBarQFull), a * C::kAtomElems, b.q0 + b.row0 + w * p.tile_step,
+                                                    b.head + w * p.head_step, once);
+                            }
                             ++m;
                         }
                         const int vs = G % C::kVStages;
-                        ok = wait_phase(bar(C::kBarVEmpty + vs), ((G / C::kVStages) & 1) ^ 1, abort_flag, p, 2);
+                        ok = all(wait_phase(bar(C::kBarVEmpty + vs), ((G / C::kVStages) & 1) ^ 1, abort_flag, p, 2));
                         if (!ok) break;
                         uint32_t vbar = bar(C::kBarVFull + vs);
                         if (tail && j + 1 == b.T) {
                             // the tail before has been handed on (long ago where its stage was loaded again since)
                             if (G - last_tail < C::kVStages)
-                                ok = wait_phase(bar(C::kBarVFull + last_tail % C::kVStages), (last_tail / C::kVStages) & 1,
-                                                abort_flag, p, 86);
+                                ok = all(wait_phase(bar(C::kBarVFull + last_tail % C::kVStages),
+                                                    (last_tail / C::kVStages) & 1, abort_flag, p, 86));
                             if (!ok) break;
                             vbar = bar(C::kBarVRaw);
                             last_tail = G;
                             ++tails;
                         }
-                        mbar_arrive_expect_tx(vbar, C::kTileBytes);
-                        for (int a = 0; a < C::kAtoms; ++a)
-                            tma_load_3d(sbase + C::kOffV + vs * C::kTileBytes + a * C::kAtomBytes, &map_v, vbar,
-                                        a * C::kAtomElems, b.k0 + j * kTileN, kvh, keep);
+                        load(sbase + C::kOffV + vs * C::kTileBytes, &map_v, vbar, j);
                         nv = G + 1;
                     }
-                    done_block(n);
+                    if (lane == 0) done_block(n);
                 }
                 // Drain: every load has landed before the CTA may exit.
                 if (m > 0) wait_phase(bar(C::kBarQFull), (m - 1) & 1, abort_flag, p, 3, false);
@@ -389,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_phase(bar(C::kBarVFull + s), (last / C::kVStages) & 1, abort_flag, p, 3, false);
                 }
             }
-        } else if (lane == 0) {
+        } else if (lane == 0 && (warp == kMmaWarp || tiles == 2)) {
             // ------------------------------------------ tensor-core issuers
             const int w = (warp == kMmaWarp) ? 0 : 1;
             const uint32_t dS = tmem + 128u * static_cast<uint32_t>(w);
@@ -475,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(bar(C::kBarDrain + w));
             wait_phase(bar(C::kBarDrain + w), 0, abort_flag, p, 9, false);
         }
-    } else {
+    } else if (warp < 4 * tiles) {
         // ------------------------------------------------ softmax warpgroups
         // The forward kernel's loop (its comments there) in less code: a short
         // sequence's tiles are full, masked, first and last ones in turn, and
@@ -508,8 +592,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             {
                 Block b;
                 if (!__all_sync(0xffffffffu, read_block(n, b))) break;
-                const int i = b.row0 + w * p.tile_step + t;  // this thread's row of the sequence
-                row_limit = kCausal ? max(-1, min(b.nk, i + 1 + b.nk - b.nq)) : b.nk;
+                if constexpr (kPrefix) {
+                    row_limit = b.nk - b.k0 * kTileN;  // keys from the partition's first tile on
+                } else {
+                    const int i = b.row0 + w * p.tile_step + t;  // this thread's row of the sequence
+                    row_limit = kCausal ? max(-1, min(b.nk, i + 1 + b.nk - b.nq)) : b.nk;
+                }
                 T = b.T;
             }
             float m_ref = -INFINITY, l = 0.0f, lq = 0.0f;
@@ -519,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          : wait_phase(bar(C::kBarSFull + w), G & 1, abort_flag, p, 10);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
-                if (C::kTakeTurns) {
+                if (C::kTakeTurns && tiles == 2) {
                     got = wait_flag(turn_mine, static_cast<uint32_t>(G + 1), abort_flag, p, 13);
                     ok = __all_sync(0xffffffffu, got);
                     if (!ok) break;
@@ -597,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::kBarPFull + 2 * w + h));
-                    if (C::kTakeTurns && h == C::kTurnAfterHalf && lane == 0) pass_turn();
+                    if (C::kTakeTurns && tiles == 2 && h == C::kTurnAfterHalf && lane == 0) pass_turn();
                 }
                 const float tsum = sum8(acc);
                 const float pmax = ex2(fmaf(mx, c, -shift));
@@ -612,7 +700,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
             }
-            {
+            if constexpr (kPrefix) {
+                const Block b = block_of(block_info(n));
+                const int seq = b.q0 + w * p.seqs + t / p.rows;
+                const long long row = t < p.rows * p.seqs && seq < p.B
+                                          ? (static_cast<long long>(seq) * p.H_kv + b.head) * p.rows + t % p.rows : -1;
+                const long long slab = b.row0 * p.part_rows;
+                store_part<D>(p.o_part + slab * D, reinterpret_cast<float4*>(p.ml_part) + slab, row, tO,
+                              make_float4(m_ref, l, lq, 0.0f), smem + C::kOffRows + warp * 4096, bar(C::kBarOFree + w));
+            } else {
                 const Block b = block_of(block_info(n));
                 const int head = b.head + w * p.head_step;
                 const int row0 = b.row0 + w * p.tile_step;  // the tile's first row of the sequence
@@ -644,12 +740,27 @@ template <int D, bool F16, bool kCausal>
 cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PackedFwdParams& p,
                            unsigned int grid, cudaStream_t stream) {
     using C = Cfg<D, F16>;
-    auto kern = fa_packed_fwd_kernel<D, F16, kCausal>;
+    auto kern = fa_packed_fwd_kernel<D, F16, kCausal, false, PackedFwdParams>;
     static SmemAllowed allowed;
     const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
                                           static_cast<int>(kLaunchRegs), allowed);
     if (e != cudaSuccess) return e;
     kern<<<grid, kThreads, C::kSmemBytes, stream>>>(q, k, v, p);
+    return cudaGetLastError();
+}
+
+// A prefix.  Launched without overlap: the kernel behind it relies on this one
+// having begun after all before it.
+template <int D, bool F16>
+cudaError_t launch_prefix(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PrefixFwdParams& p,
+                          cudaStream_t stream) {
+    using C = Cfg<D, F16>;
+    auto kern = fa_packed_fwd_kernel<D, F16, false, true, PrefixFwdParams>;
+    static SmemAllowed allowed;
+    const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
+                                          static_cast<int>(kLaunchRegs), allowed);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(p.H_kv * p.blocks * p.splits), kThreads, C::kSmemBytes, stream>>>(q, k, v, p);
     return cudaGetLastError();
 }
 

@@ -65,16 +65,18 @@ cudaError_t launch_paged_fwd_bf16(const CUtensorMap& q, const CUtensorMap& k, co
 cudaError_t launch_paged_fwd_f16(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,
                                  cudaStream_t stream);
 
-// The prefix that all sequences share, by the forward kernel.  A tile of 128
-// query rows holds the `rows` rows that `seqs` sequences (as many as fit) have
-// for one key/value head; a CTA has two tiles (or, where one holds all
-// sequences, one) and a partition of the keys, and leaves a partial result.
-// The key/value tiles come from pages as in the kernel above.
+// The prefix that all sequences share, by the packed forward kernel
+// (fa_packed_fwd.cuh).  A tile of 128 query rows holds the `rows` rows that `seqs`
+// sequences (as many as fit) have for one key/value head; a block has two tiles (or,
+// where one holds all sequences, one) and a partition of the keys, and leaves a
+// partial result.  The key/value tiles come from pages as in the kernel above.
 struct PrefixFwdParams : FwdParams {
     const int32_t* pages;  // numbers of the prefix's pages
     int page, n_pages;
     int B, rows, seqs;
-    int blocks;            // CTAs along the sequences, per key/value head
+    int blocks;            // blocks along the sequences, per key/value head
+    int pair;              // 1: two tiles
+    int negate;            // as in PackedFwdParams
 };
 // q: [B, H_kv, rows, d] with boxes of `rows` rows x 1 x `seqs` sequences.
 cudaError_t launch_prefix_fwd_bf16(int d, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,

@@ -391,13 +391,13 @@ int fa_paged_fwd(const fa_paged_cache_t* cache, const void* q, void* o, float* l
         f.part_rows = c.B * H * N_q;
         f.Nkv = static_cast<int>(prefix_length);
         f.n_kv_tiles = static_cast<int>((prefix_length + 127) / 128);
-        f.n_q_blocks = 1;
         f.H = p.H;
         f.H_kv = p.H_kv;
         f.group = p.group;
         f.splits = plan.prefix_splits;
         f.tiles_per_split = plan.prefix_tiles;
-        f.scale_log2 = p.scale_log2;
+        f.scale_log2 = std::fmax(std::fabs(p.scale_log2), 1.17549435e-38f);  // as fa_packed_fwd's
+        f.negate = scale < 0.0f ? 1 : 0;
         f.pages = prefix_pages;
         f.page = p.c.page;
         f.n_pages = static_cast<int>((prefix_length + c.page_size - 1) / c.page_size);
@@ -405,6 +405,7 @@ int fa_paged_fwd(const fa_paged_cache_t* cache, const void* q, void* o, float* l
         f.rows = plan.rows;
         f.seqs = plan.prefix_seqs;
         f.blocks = plan.prefix_blocks;
+        f.pair = c.B > plan.prefix_seqs ? 1 : 0;
         const int64_t qdims[4] = {c.d, plan.rows, c.H_kv, c.B};
         const int64_t qstrides[4] = {1, c.d, plan.rows * c.d, H * N_q * c.d};
         const uint32_t qbox[4] = {64, static_cast<uint32_t>(plan.rows), 1, static_cast<uint32_t>(plan.prefix_seqs)};

@@ -1,5 +1,6 @@
 // Attention over the paged key/value cache, fp16: instantiations of
-// its kernels and of the forward kernel over a prefix.
+// its kernels and of the packed forward kernel over a prefix.
+#include "fa_packed_fwd.cuh"
 #include "fa_paged_kernel.cuh"
 
 namespace fa {
@@ -11,7 +12,8 @@ cudaError_t launch_paged_fwd_f16(const CUtensorMap& q, const CUtensorMap& k, con
 
 cudaError_t launch_prefix_fwd_f16(int d, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                    const PrefixFwdParams& p, cudaStream_t stream) {
-    return d == 64 ? launch_prefix<64, true>(q, k, v, p, stream) : launch_prefix<128, true>(q, k, v, p, stream);
+    return d == 64 ? packed::launch_prefix<64, true>(q, k, v, p, stream)
+                   : packed::launch_prefix<128, true>(q, k, v, p, stream);
 }
 
 }  // namespace fa
