@@ -59,7 +59,7 @@ struct PagedFwdParams : FwdParams {
     // the prefix's partial results, `splits` slabs of [B * H_kv * rows] rows
     // (FwdParams::o_part, ml_part; splits = 0: no prefix)
 };
-constexpr int paged_rows_per_block(int64_t rows) { return rows <= 16 ? 16 : 32; }
+constexpr int paged_rows_per_block(int64_t rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 cudaError_t launch_paged_fwd_bf16(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,
                                   cudaStream_t stream);
 cudaError_t launch_paged_fwd_f16(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,

@@ -416,7 +416,7 @@ int fa_paged_fwd(const fa_paged_cache_t* cache, const void* q, void* o, float* l
     p.gen = next_generation();
     const int64_t qdims[3] = {c.d, plan.rows, c.B * c.H_kv};
     const int64_t qstrides[3] = {1, c.d, plan.rows * c.d};
-    const uint32_t qbox[3] = {64, static_cast<uint32_t>(plan.rows_per_block), 1};
+    const uint32_t qbox[3] = {64, plan.rows_per_block < 16 ? 16u : static_cast<uint32_t>(plan.rows_per_block), 1};
     if ((st = encode_strided(&mq, q, dtype, 3, qdims, qstrides, qbox)) != FA_OK) return st;
     const cudaError_t e = f16 ? fa::launch_paged_fwd_f16(mq, mk, mv, p, s) : fa::launch_paged_fwd_bf16(mq, mk, mv, p, s);
     return e == cudaSuccess ? FA_OK : cuda_failed("paged attention launch", e);

@@ -35,8 +35,10 @@
 namespace fa {
 namespace paged {
 
-template <int D, bool F16, int NR>
+// NV: query rows of a block, 4, 8, 16 or 32; the products' N is at least 16.
+template <int D, bool F16, int NV>
 struct Cfg {
+    static constexpr int NR = NV < 16 ? 16 : NV;
     static constexpr int kAtomElems = 64;
     static constexpr int kAtoms = D / kAtomElems;
     static constexpr int kAtomBytes = 128 * 128;            // 128 keys x 128 bytes
@@ -66,8 +68,9 @@ struct Cfg {
     static constexpr int kOffK = kOffV + kStages * kTileBytes;  // [kStages]
     static constexpr int kOffQ = kOffK + kStages * kTileBytes;  // [2] x kAtoms x NR rows
     static constexpr int kOffP = kOffQ + 2 * kQBytes;           // [2] x 2 atoms x NR rows
-    static constexpr int kRedFloats = 3 * 4 * NR;
-    static constexpr int kOffRed = kOffP + 2 * 2 * kRowAtomBytes;  // float [kGroups][3][4 warps][NR]
+    // of a group, floats: row maxima, sums l and lq of each warp [3][4][NV]; references [NV]
+    static constexpr int kRedFloats = 13 * NV;
+    static constexpr int kOffRed = kOffP + 2 * 2 * kRowAtomBytes;  // [kGroups]
     static constexpr int kOffBar = kOffRed + kGroups * kRedFloats * 4;
     // barriers
     static constexpr int kBarQFull = 0;                   // [2] a unit's Q landed
@@ -172,12 +175,54 @@ __device__ __forceinline__ Cursor first_of(const PagedCache& c, int units, int c
     return k;
 }
 
+// NV consecutive TMEM columns of this warp's 32 lanes (one per thread), the wait
+// for them, and back.
+template <int NV>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[NV]) {
+    if constexpr (NV >= 16) {
+        tmem_ld_cols<NV>(taddr, r);
+        tmem_ld_cols_wait<NV>(r);
+    } else if constexpr (NV == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                     :
+                     : "memory");
+    } else {
+        static_assert(NV == 4, "4, 8, 16 or 32 columns");
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])
+                     :
+                     : "memory");
+    }
+}
+template <int NV>
+__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[NV]) {
+    if constexpr (NV >= 16) {
+        tmem_st_cols<NV>(taddr, r);
+    } else if constexpr (NV == 8) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3])
+                     : "memory");
+    }
+}
+
 // One CTA per run.  map_q: [B * H_kv, R, d] (d first), boxes of NR rows.
-template <int D, bool F16, bool kCausal, int NR>
-__global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
+template <int D, bool F16, bool kCausal, int NV>
+__global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
     fa_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const PagedFwdParams p) {
-    using C = Cfg<D, F16, NR>;
+    using C = Cfg<D, F16, NV>;
+    constexpr int NR = C::NR;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_u32 & 1023u)) & 1023u;
@@ -209,6 +254,11 @@ __global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
         mbar_init(bar(C::kBarDrain), 1);
         *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
         mbar_init_fence();
+    }
+    if constexpr (NV < NR) {  // rows that only the products have
+        for (int i = static_cast<int>(threadIdx.x); i < 4 * C::kRowAtomBytes / 16; i += C::kThreads)
+            reinterpret_cast<uint4*>(smem + C::kOffP)[i] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
     }
     if (kCausal && threadIdx.x < 128) smem[C::kOffQuery + threadIdx.x] = static_cast<uint8_t>(threadIdx.x % p.Nq);
     if (warp == C::kMmaWarp) {
@@ -375,8 +425,10 @@ __global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
         const uint32_t named = kDecNamedBar + static_cast<uint32_t>(group);
         const uint32_t tS = tmem + lane_base + C::kColS;
         const float c = p.scale_log2;
-        float* red = reinterpret_cast<float*>(smem + C::kOffRed) + group * C::kRedFloats;  // [3][4 warps][NR]
-        constexpr int kLanesPerRow = 32 / NR;                      // after warp_reduce_rows
+        float* red = reinterpret_cast<float*>(smem + C::kOffRed) + group * C::kRedFloats;
+        float* ref = red + 12 * NV;            // the references, for the unit's result
+        float* inv = red;                      // 1 / lq then, where the maxima were
+        constexpr int kLanesPerRow = 32 / NV;  // after warp_reduce_rows
         // key t's 16-bit slot in row n of a P^T buffer (see the decode kernel)
         const int pch = (t % 64) / 8;
         uint8_t* pkey = smem + C::kOffP + (t / 64) * C::kRowAtomBytes + (t % 8) * 2;
@@ -387,49 +439,48 @@ __global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
                 it += k.last() - k.t;
                 continue;
             }
-            const int row0 = (k.u % p.row_blocks) * NR;
-            const int rows = min(p.rows - row0, NR);
+            const int row0 = (k.u % p.row_blocks) * NV;
+            const int rows = min(p.rows - row0, NV);
             const uint32_t tO = tmem + lane_base + C::kColO + NR * (seg & 1);
-            float m[NR], l[NR], lq[NR];  // reference maxima (base 2, scaled), sums
+            float m[NV], l[NV], lq[NV];  // reference maxima (base 2, scaled), sums
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
+            for (int n = 0; n < NV; ++n) {
                 m[n] = -INFINITY;
                 l[n] = 0.0f;
                 lq[n] = 0.0f;
             }
-            // is key `key` visible to row n
-            auto visible = [&](int n, int key) -> bool {
-                if (key >= k.len) return false;
-                // (rows past the last are not stored)
-                if (kCausal) return key <= smem[C::kOffQuery + row0 + n] + k.len - p.Nq;
-                return true;
-            };
             const int first = k.t, last = k.last();
             for (int j = first; j < last; ++j, ++it, ++mine) {
                 const int b = it & 1, s_ = it % C::kStages;
-                const int key0 = j * 128;
-                const int key = key0 + t;
-                const bool masked = key0 + 128 > k.len || (kCausal && key0 + 127 > k.len - p.Nq);
-                uint32_t s[NR];
+                const int key = j * 128 + t;
+                uint32_t s[NV];
                 if (ok) ok = wait_phase(bar(C::kBarS + 2 * group + (mine & 1)), (mine >> 1) & 1, abort_flag, p, 66);
                 ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-wide
                 if (ok) {
                     tc_fence_after();
-                    tmem_ld_cols<NR>(tS + NR * b, s);
-                    tmem_ld_cols_wait<NR>(s);
+                    ld_cols<NV>(tS + NR * b, s);
                 } else {
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) s[n] = 0u;
+                    for (int n = 0; n < NV; ++n) s[n] = 0u;
                 }
-                // x = t - m: the exponent of each weight against the current reference
-                float x[NR];
+                // scores in base 2; of keys that a row does not see -inf (rows past the last are not stored)
+                float x[NV];
+#pragma unroll
+                for (int n = 0; n < NV; ++n) x[n] = u2f(s[n]) * c;
+                if (j * 128 + 128 > k.len || (kCausal && j * 128 + 127 > k.len - p.Nq)) {
+                    if (kCausal) {
+                        const int late = key - k.len + p.Nq;  // rows of query indexes below it do not see the key
+#pragma unroll
+                        for (int n = 0; n < NV; ++n)
+                            if (key >= k.len || late > static_cast<int>(smem[C::kOffQuery + row0 + n])) x[n] = -INFINITY;
+                    } else if (key >= k.len) {
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) x[n] = -INFINITY;
+                    }
+                }
                 bool need = !ok;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    x[n] = fmaf(u2f(s[n]), c, -m[n]);
-                    if (masked && !visible(n, key)) x[n] = -INFINITY;
-                    need |= x[n] > kRescaleThreshold;
-                }
+                for (int n = 0; n < NV; ++n) need |= x[n] - m[n] > kRescaleThreshold;
                 // (a unit's first tile always sets the references: no vote)
                 if (j == first || named_barrier_or(named, 128, need)) {
                     if (named_barrier_or(named, 128, !ok)) {  // every thread leaves together
@@ -437,35 +488,34 @@ __global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
                         break;
                     }
                     // the tile's row maxima over its 128 keys
-                    float v[NR];
+                    float v[NV];
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) v[n] = (masked && !visible(n, key)) ? -INFINITY : u2f(s[n]) * c;
-                    const float r = warp_reduce_rows<NR, true>(v, lane);
-                    if (lane % kLanesPerRow == 0) red[gwarp * NR + lane / kLanesPerRow] = r;
+                    for (int n = 0; n < NV; ++n) v[n] = x[n];
+                    const float r = warp_reduce_rows<NV, true>(v, lane);
+                    if (lane % kLanesPerRow == 0) red[gwarp * NV + lane / kLanesPerRow] = r;
                     named_barrier_sync(named, 128);
-                    float alpha[NR];
+                    float alpha[NV];
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        const float tmax = fmaxf(fmaxf(red[n], red[NR + n]), fmaxf(red[2 * NR + n], red[3 * NR + n]));
+                    for (int n = 0; n < NV; ++n) {
+                        const float tmax = fmaxf(fmaxf(red[n], red[NV + n]), fmaxf(red[2 * NV + n], red[3 * NV + n]));
                         float mn = fmaxf(m[n], tmax);
                         if (mn == -INFINITY) mn = 0.0f;  // no visible key yet: any finite reference
                         alpha[n] = ex2(m[n] - mn);      // 0 while m was -inf
                         l[n] *= alpha[n];
                         lq[n] *= alpha[n];
                         m[n] = mn;
-                        x[n] = (masked && !visible(n, key)) ? -INFINITY : fmaf(u2f(s[n]), c, -mn);
+                        if (t == 0) ref[n] = mn;
                     }
                     if (j > first) {  // O^T holds tiles < j: rescale it once the last product into it is done
                         ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarPFree + (b ^ 1)), ((it - 1) >> 1) & 1,
                                                                 abort_flag, p, 67));
                         if (ok) {
                             tc_fence_after();
-                            uint32_t o[NR];
-                            tmem_ld_cols<NR>(tO, o);
-                            tmem_ld_cols_wait<NR>(o);
+                            uint32_t o[NV];
+                            ld_cols<NV>(tO, o);
 #pragma unroll
-                            for (int n = 0; n < NR; ++n) o[n] = f2u(u2f(o[n]) * alpha[n]);
-                            tmem_st_cols<NR>(tO, o);
+                            for (int n = 0; n < NV; ++n) o[n] = f2u(u2f(o[n]) * alpha[n]);
+                            st_cols<NV>(tO, o);
                             tmem_st_wait();
                         }
                     }
@@ -475,6 +525,7 @@ __global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok && key >= k.len) {  // value rows behind the sequence's end, and of pages not loaded
                     ok = wait_phase(bar(C::kBarFull + s_), (it / C::kStages) & 1, abort_flag, p, 72);
+#pragma unroll 1
                     for (int a = 0; ok && a < C::kAtoms; ++a) {
                         uint4* row = reinterpret_cast<uint4*>(smem + C::kOffV + s_ * C::kTileBytes + a * C::kAtomBytes + t * 128);
 #pragma unroll
@@ -485,8 +536,8 @@ __global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
                 if (ok) {
                     uint8_t* pbuf = pkey + b * 2 * C::kRowAtomBytes;
 #pragma unroll
-                    for (int n = 0; n < NR; n += 2) {
-                        const float p0 = ex2(x[n]), p1 = ex2(x[n + 1]);
+                    for (int n = 0; n < NV; n += 2) {
+                        const float p0 = ex2(x[n] - m[n]), p1 = ex2(x[n + 1] - m[n + 1]);
                         l[n] += p0;
                         l[n + 1] += p1;
                         const uint32_t w2 = pack_16x2<F16>(p0, p1);
@@ -505,59 +556,56 @@ __global__ void __launch_bounds__((Cfg<D, F16, NR>::kThreads), 1)
             }
 
             // --------------------------------------------- the unit's result
+            // l and lq over the 128 keys of the warpgroup, while the last product runs
+            const float rl = warp_reduce_rows<NV, false>(l, lane);
+            const float rq = warp_reduce_rows<NV, false>(lq, lane);
+            if (lane % kLanesPerRow == 0) {
+                red[4 * NV + gwarp * NV + lane / kLanesPerRow] = rl;
+                red[8 * NV + gwarp * NV + lane / kLanesPerRow] = rq;
+            }
+            const bool whole = first == 0 && last == k.tiles();
+            const bool final = whole && !p.parts_always;
+            const long long unit = static_cast<long long>(k.b) * units + k.u;
+            // first row of the output, or of the partial result's slot
+            const long long at = final ? (static_cast<long long>(k.b) * p.c.H_kv + k.u / p.row_blocks) * p.rows + row0
+                                       : (whole ? 2ll * p.ctas + unit : 2ll * blockIdx.x + (seg == 0 ? 0 : 1)) * NV;
+            named_barrier_sync(named, 128);
+            if (t < rows) {
+                const float* a = red + 4 * NV + t;
+                const float* q = red + 8 * NV + t;
+                const float L = (a[0] + a[NV]) + (a[2 * NV] + a[3 * NV]);
+                const float LQ = (q[0] + q[NV]) + (q[2 * NV] + q[3 * NV]);
+                if (final) {
+                    inv[t] = LQ == 0.0f ? 0.0f : 1.0f / LQ;
+                    if (p.lse != nullptr) p.lse[at + t] = L == 0.0f ? -INFINITY : (ref[t] + log2f(L)) * 0.69314718055994531f;
+                } else {
+                    // a row that sees no key here gets weight 0 (m = -inf)
+                    p.part_ml[at + t] = make_float4(L == 0.0f ? -INFINITY : ref[t], L, LQ, 0.0f);
+                }
+            }
             if (ok) ok = wait_phase(bar(C::kBarO + (seg & 1)), (seg >> 1) & 1, abort_flag, p, 69);
             ok = __all_sync(0xffffffffu, ok);
-            if (named_barrier_or(named, 128, !ok)) {
+            if (named_barrier_or(named, 128, !ok)) {  // (and `inv` is written)
                 ok = false;
                 break;
             }
             tc_fence_after();
-            uint32_t o[NR];
-            tmem_ld_cols<NR>(tO, o);
-            tmem_ld_cols_wait<NR>(o);
+            uint32_t o[NV];
+            ld_cols<NV>(tO, o);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarOFree + (seg & 1)));
-            // l and lq over the 128 keys of the warpgroup
-            const float rl = warp_reduce_rows<NR, false>(l, lane);
-            const float rq = warp_reduce_rows<NR, false>(lq, lane);
-            if (lane % kLanesPerRow == 0) {
-                red[4 * NR + gwarp * NR + lane / kLanesPerRow] = rl;
-                red[8 * NR + gwarp * NR + lane / kLanesPerRow] = rq;
-            }
-            named_barrier_sync(named, 128);
-            const bool whole = first == 0 && last == k.tiles();
-            const long long unit = static_cast<long long>(k.b) * units + k.u;
-            if (whole && !p.parts_always) {
-                uint16_t* out = static_cast<uint16_t*>(p.out);
-                const long long at = (static_cast<long long>(k.b) * p.c.H_kv + k.u / p.row_blocks) * p.rows + row0;
+            if (t < D) {
+                if (final) {
+                    uint16_t* out = static_cast<uint16_t*>(p.out) + at * D + t;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    if (n >= rows) break;
-                    const float* a = red + 4 * NR + n;
-                    const float* q = red + 8 * NR + n;
-                    const float LQ = (q[0] + q[NR]) + (q[2 * NR] + q[3 * NR]);
-                    const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
-                    if (t < D) out[(at + n) * D + t] = static_cast<uint16_t>(pack_16x2<F16>(u2f(o[n]) * inv, 0.0f) & 0xFFFFu);
-                    if (t == n && p.lse != nullptr) {
-                        const float L = (a[0] + a[NR]) + (a[2 * NR] + a[3 * NR]);
-                        p.lse[at + n] = L == 0.0f ? -INFINITY : (m[n] + log2f(L)) * 0.69314718055994531f;
-                    }
-                }
-            } else {
-                // a partial result; a row that sees no key here gets weight 0 (m = -inf)
-                const long long slot = whole ? 2ll * p.ctas + unit : 2ll * blockIdx.x + (seg == 0 ? 0 : 1);
+                    for (int n = 0; n < NV; ++n)
+                        if (n < rows) out[n * D] = static_cast<uint16_t>(pack_16x2<F16>(u2f(o[n]) * inv[n], 0.0f) & 0xFFFFu);
+                } else {
+                    float* out = p.unit_o + at * D + t;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    if (n >= rows) break;
-                    const float* a = red + 4 * NR + n;
-                    const float* q = red + 8 * NR + n;
-                    if (t < D) p.unit_o[(slot * NR + n) * D + t] = u2f(o[n]);
-                    if (t == n) {
-                        const float L = (a[0] + a[NR]) + (a[2 * NR] + a[3 * NR]);
-                        p.part_ml[slot * NR + n] = make_float4(L == 0.0f ? -INFINITY : m[n], L,
-                                                               (q[0] + q[NR]) + (q[2 * NR] + q[3 * NR]), 0.0f);
-                    }
+                    for (int n = 0; n < NV; ++n)
+                        if (n < rows) out[n * D] = u2f(o[n]);
                 }
             }
             // `red` is written again after the next unit's votes, which all threads reach
@@ -665,11 +713,11 @@ __global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const Paged
     if (lane == 0 && p.lse != nullptr) p.lse[row] = L == 0.0f ? -INFINITY : (ref + log2f(L)) * 0.69314718055994531f;
 }
 
-template <int D, bool F16, bool kCausal, int NR>
+template <int D, bool F16, bool kCausal, int NV>
 cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,
                            cudaStream_t stream) {
-    using C = Cfg<D, F16, NR>;
-    auto kern = fa_paged_kernel<D, F16, kCausal, NR>;
+    using C = Cfg<D, F16, NV>;
+    auto kern = fa_paged_kernel<D, F16, kCausal, NV>;
     static SmemAllowed allowed;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes), allowed);
     if (e != cudaSuccess) return e;
@@ -677,17 +725,24 @@ cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUt
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
     return launch_dependent(fa_paged_join_kernel<D, F16>, dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
-                            kJoinThreads, 0, stream, p, NR);
+                            kJoinThreads, 0, stream, p, NV);
+}
+
+template <int D, bool F16, bool kCausal>
+cudaError_t launch_rows(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,
+                        cudaStream_t stream) {
+    switch (paged_rows_per_block(p.rows)) {
+        case 4: return launch_variant<D, F16, kCausal, 4>(q, k, v, p, stream);
+        case 8: return launch_variant<D, F16, kCausal, 8>(q, k, v, p, stream);
+        case 16: return launch_variant<D, F16, kCausal, 16>(q, k, v, p, stream);
+        default: return launch_variant<D, F16, kCausal, 32>(q, k, v, p, stream);
+    }
 }
 
 template <int D, bool F16>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedFwdParams& p,
                    cudaStream_t stream) {
-    if (paged_rows_per_block(p.rows) == 16)
-        return p.causal ? launch_variant<D, F16, true, 16>(q, k, v, p, stream)
-                        : launch_variant<D, F16, false, 16>(q, k, v, p, stream);
-    return p.causal ? launch_variant<D, F16, true, 32>(q, k, v, p, stream)
-                    : launch_variant<D, F16, false, 32>(q, k, v, p, stream);
+    return p.causal ? launch_rows<D, F16, true>(q, k, v, p, stream) : launch_rows<D, F16, false>(q, k, v, p, stream);
 }
 
 }  // namespace paged
