@@ -623,20 +623,77 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
 }
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinAhead = 8;
+constexpr int kJoinAhead = 16;  // partial rows whose loads are in flight
+
+// A row's partial results added up in order, as consecutive tiles of the online
+// softmax are:  M = max m_s,  O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) lq_s,
+// lse = ln 2 (M + log2 sum 2^(m_s - M) l_s).  By one warp, D / 32 channels a lane.
+template <int D>
+struct Joined {
+    static constexpr int kPer = D / 32;
+    float M = -INFINITY, L = 0.0f, LQ = 0.0f, acc[kPer] = {};
+
+    // `parts` of them: part i's statistics and row by stats(i) and row(i).
+    template <class Stats, class Row>
+    __device__ __forceinline__ void add(int parts, Stats stats, Row row) {
+        const int lane = static_cast<int>(threadIdx.x) % 32;
+        for (int i0 = 0; i0 < parts; i0 += kJoinAhead) {
+            const int here = min(kJoinAhead, parts - i0);
+            float4 ml = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+            if (lane < here) ml = stats(i0 + lane);
+            float o[kJoinAhead][kPer];
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {  // (those past the last repeat it)
+                const float* src = row(i0 + min(k, here - 1)) + lane * kPer;
+                if constexpr (kPer == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(src);
+                    o[k][0] = y.x, o[k][1] = y.y, o[k][2] = y.z, o[k][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(src);
+                    o[k][0] = y.x, o[k][1] = y.y;
+                }
+            }
+            float most = ml.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+            most = fmaxf(most, M);
+            const float ref = most == -INFINITY ? 0.0f : most;
+            const float old = ex2(M - ref), w = ex2(ml.x - ref);
+            float l = w * ml.y, q = w * ml.z;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, off);
+                q += __shfl_xor_sync(0xffffffffu, q, off);
+            }
+            M = most;
+            L = L * old + l;
+            LQ = LQ * old + q;
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) acc[x] *= old;
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const float f = __shfl_sync(0xffffffffu, w, k);
+                if (k < here && f != 0.0f) {  // (0 times what a part without keys holds)
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x) acc[x] += f * o[k][x];
+                }
+            }
+        }
+    }
+};
 
 // The second kernel: rows whose keys several CTAs shared, or that have a
-// prefix, from their partial results, in order; a warp per row:
-//   M = max m_s,  O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) lq_s,
-//   lse = ln 2 (M + log2 sum 2^(m_s - M) l_s).
+// prefix, a warp each.  The lengths are read ahead of the wait: the kernel
+// before let this one be set up behind its own wait for whatever wrote them.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const PagedFwdParams p, int rows_per_block) {
     const int lane = static_cast<int>(threadIdx.x) % 32;
     const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
     const long long total_rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
-    grid_wait();
-    grid_release();
-    if (row >= total_rows) return;
+    if (row >= total_rows) {
+        grid_wait();
+        return;
+    }
     const int units = p.c.H_kv * p.row_blocks;
     const int r = static_cast<int>(row % p.rows);
     const long long head = row / p.rows;  // b * H_kv + key/value head
@@ -649,68 +706,27 @@ __global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const Paged
     const int begin = sp.before * units + u * tiles;  // the unit's first tile among all
     const int c0 = begin / run, c1 = tiles > 0 ? (begin + tiles - 1) / run : c0 - 1;  // its CTAs
     const bool whole = c0 == c1;
+    grid_wait();
+    grid_release();
     if (whole && !p.parts_always) return;  // written by its CTA
-    const int own = c1 - c0 + 1, parts = own + p.splits;
-    auto slot = [&](int i) -> long long {  // of part i < own
+    Joined<D> j;
+    j.add(p.splits, [&](int i) { return *reinterpret_cast<const float4*>(p.ml_part + (i * total_rows + row) * 4); },
+          [&](int i) { return p.o_part + (i * total_rows + row) * D; });
+    auto slot = [&](int i) -> long long {
         if (whole) return 2ll * p.ctas + static_cast<long long>(b) * units + u;
         // a CTA whose run starts inside or with the unit has it as its first
         const int cta = c0 + i;
         return 2ll * cta + (i == 0 && begin != c0 * run ? 1 : 0);
     };
-    auto stats = [&](int i) -> float4 {
-        if (i < own) return p.part_ml[slot(i) * rows_per_block + n];
-        return *reinterpret_cast<const float4*>(p.ml_part + (static_cast<size_t>(i - own) * total_rows + row) * 4);
-    };
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, stats(i).x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float ref = M == -INFINITY ? 0.0f : M;
-    constexpr int kPer = D / 32;
-    float acc[kPer] = {}, L = 0.0f, LQ = 0.0f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float4 ml = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-        if (i0 + lane < parts) ml = stats(i0 + lane);
-        const float w = ex2(ml.x - ref);
-        float l = w * ml.y, q = w * ml.z;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            l += __shfl_xor_sync(0xffffffffu, l, off);
-            q += __shfl_xor_sync(0xffffffffu, q, off);
-        }
-        L += l;
-        LQ += q;
-        // eight parts' loads at a time; those past the last repeat it with weight 0
-        const int here = min(32, parts - i0);
-        for (int k0 = 0; k0 < here; k0 += kJoinAhead) {
-            float o[kJoinAhead][kPer];
-#pragma unroll
-            for (int k = 0; k < kJoinAhead; ++k) {
-                const int i = i0 + min(k0 + k, here - 1);
-                const float* src = (i < own ? p.unit_o + (slot(i) * rows_per_block + n) * D
-                                            : p.o_part + (static_cast<size_t>(i - own) * total_rows + row) * D) + lane * kPer;
-                if constexpr (kPer == 4) {
-                    const float4 y = *reinterpret_cast<const float4*>(src);
-                    o[k][0] = y.x, o[k][1] = y.y, o[k][2] = y.z, o[k][3] = y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2*>(src);
-                    o[k][0] = y.x, o[k][1] = y.y;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kJoinAhead; ++k) {
-                const float f = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-                if (k0 + k >= here || f == 0.0f) continue;  // (0 times what a part without keys holds)
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) acc[x] += f * o[k][x];
-            }
-        }
-    }
-    const float inv = LQ == 0.0f ? 0.0f : 1.0f / LQ;
+    j.add(c1 - c0 + 1, [&](int i) { return p.part_ml[slot(i) * rows_per_block + n]; },
+          [&](int i) { return p.unit_o + (slot(i) * rows_per_block + n) * D; });
+    const float inv = j.LQ == 0.0f ? 0.0f : 1.0f / j.LQ;
+    constexpr int kPer = Joined<D>::kPer;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * kPer);
 #pragma unroll
-    for (int x = 0; x < kPer; x += 2) dst[x / 2] = pack_16x2<F16>(acc[x] * inv, acc[x + 1] * inv);
-    if (lane == 0 && p.lse != nullptr) p.lse[row] = L == 0.0f ? -INFINITY : (ref + log2f(L)) * 0.69314718055994531f;
+    for (int x = 0; x < kPer; x += 2) dst[x / 2] = pack_16x2<F16>(j.acc[x] * inv, j.acc[x + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[row] = j.L == 0.0f ? -INFINITY : (j.M + log2f(j.L)) * 0.69314718055994531f;
 }
 
 template <int D, bool F16, bool kCausal, int NV>
