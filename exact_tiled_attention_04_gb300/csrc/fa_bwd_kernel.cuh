@@ -367,6 +367,10 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         tmem_alloc(smem_u32(tmem_slot), kBwdTmemCols);
         tmem_relinquish();
     }
+    // Packed: set up beside the kernel before, whose results are read behind this
+    // wait.  (The dQ conversion is not let in early: its waiting blocks cost the last
+    // wave's CTAs 2 %.)
+    if constexpr (kPacked) grid_wait();
     [[maybe_unused]] int* const block_info = reinterpret_cast<int*>(ctrl + C::kNumBars * 8 + 8);
     if constexpr (kPacked) {
         if (warp == kBwdReduceWarp) {
@@ -900,8 +904,7 @@ cudaError_t launch_packed_bwd_variant(const CUtensorMap& dq, const PackedBwdPara
     const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
                                           static_cast<int>(C::kLaunchRegs), allowed);
     if (e != cudaSuccess) return e;
-    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(dq, dq, dq, dq, dq, dq, dq, p);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(grid), C::kThreads, C::kSmemBytes, stream, dq, dq, dq, dq, dq, dq, dq, p);
 }
 
 template <int D, bool F16, bool kCausal>

@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "fa_kv4.h"
 #include "fa_packed.cuh"
 #include "fa_packed.h"
 #include "fa_ptx.cuh"
@@ -59,6 +60,8 @@ __device__ __forceinline__ void write_map(CUtensorMap* out, const CUtensorMap& w
 template <int D, bool F16>
 __global__ void __launch_bounds__(kAuxThreads) fa_packed_prep_kernel(const PackedAuxParams p,
                                                                      const __grid_constant__ PackedMaps m) {
+    grid_wait();
+    grid_release();
     if (static_cast<int>(blockIdx.x) >= p.tiles) {  // a block per sequence behind the tiles, in head 0's row of the grid
         __shared__ __align__(128) uint8_t copy[kPackedMaps][128];
         const int s = static_cast<int>(blockIdx.x) - p.tiles, i = static_cast<int>(threadIdx.x) / 32;
@@ -111,6 +114,8 @@ __global__ void __launch_bounds__(kAuxThreads) fa_packed_prep_kernel(const Packe
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kAuxThreads) fa_packed_dq_kernel(const PackedAuxParams p) {
+    grid_wait();
+    grid_release();
     constexpr int kLanes = D / 8, kStep = kAuxThreads / kLanes;
     const int tile = static_cast<int>(blockIdx.x), head = static_cast<int>(blockIdx.y);
     int q0, first, rows;
@@ -134,16 +139,14 @@ cudaError_t launch_packed_prep(const PackedAuxParams& p, const PackedMaps& m, in
     const dim3 grid(static_cast<unsigned>(p.tiles + p.seqs.B), static_cast<unsigned>(p.H));
     auto kern = d == 64 ? (f16 ? fa_packed_prep_kernel<64, true> : fa_packed_prep_kernel<64, false>)
                         : (f16 ? fa_packed_prep_kernel<128, true> : fa_packed_prep_kernel<128, false>);
-    kern<<<grid, kAuxThreads, 0, stream>>>(p, m);
-    return cudaGetLastError();
+    return launch_dependent(kern, grid, kAuxThreads, 0, stream, p, m);
 }
 
 cudaError_t launch_packed_dq(const PackedAuxParams& p, int d, bool f16, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.H));
     auto kern = d == 64 ? (f16 ? fa_packed_dq_kernel<64, true> : fa_packed_dq_kernel<64, false>)
                         : (f16 ? fa_packed_dq_kernel<128, true> : fa_packed_dq_kernel<128, false>);
-    kern<<<grid, kAuxThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(kern, grid, kAuxThreads, 0, stream, p);
 }
 
 }  // namespace fa

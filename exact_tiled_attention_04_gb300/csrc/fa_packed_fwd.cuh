@@ -270,6 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
+    // set up beside the kernel before; what it wrote is read behind this wait
+    grid_wait();
+    grid_release();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -284,8 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return b.nq >= 0;
     };
     auto done_block = [&](int n) { mbar_arrive(bar(C::kBarBlockEmpty + (n & 1))); };
-
-    if (kPrefix) grid_release();  // the kernel behind may be set up
 
     if (skip) {
         // nothing issued: go straight to the teardown
@@ -745,12 +746,11 @@ cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUt
     const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
                                           static_cast<int>(kLaunchRegs), allowed);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, C::kSmemBytes, stream>>>(q, k, v, p);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(grid), kThreads, C::kSmemBytes, stream, q, k, v, p);
 }
 
-// A prefix.  Launched without overlap: the kernel behind it relies on this one
-// having begun after all before it.
+// A prefix.  (The kernel behind it relies on this one to let it be set up only
+// behind its own wait.)
 template <int D, bool F16>
 cudaError_t launch_prefix(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PrefixFwdParams& p,
                           cudaStream_t stream) {
@@ -760,8 +760,8 @@ cudaError_t launch_prefix(const CUtensorMap& q, const CUtensorMap& k, const CUte
     const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
                                           static_cast<int>(kLaunchRegs), allowed);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(p.H_kv * p.blocks * p.splits), kThreads, C::kSmemBytes, stream>>>(q, k, v, p);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(static_cast<unsigned>(p.H_kv * p.blocks * p.splits)), kThreads, C::kSmemBytes, stream, q,
+                            k, v, p);
 }
 
 }  // namespace packed

@@ -272,8 +272,9 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
             tma_prefetch_desc(&map_v);
         }
         // Lengths, pages and q may come from the kernel before.  Behind a
-        // prefix's kernel, which reads them too and so began after whatever
-        // wrote them, this one waits at its end, for the second kernel's sake.
+        // prefix's kernel, which reads them too and lets this one be set up
+        // behind its own wait for whatever wrote them, this one waits at its end
+        // instead, for the second kernel's sake.
         if (!p.parts_always) grid_wait();
         grid_release();
         const Cursor k = first_of(p.c, units, p.ctas);

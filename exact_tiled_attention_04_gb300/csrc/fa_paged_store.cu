@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kAppendWarps = 8;  // of a block, unless it has a whole sequence
 constexpr int kMostWarps = 16;
-constexpr int kBatch = 4;        // rows per lane whose loads are in flight
+constexpr int kBatch = 2;        // rows per lane whose loads are in flight
 
 // Sequence of row t by the offsets cu[0 .. B], or -1.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, long long t) {
@@ -54,6 +54,31 @@ __global__ void __launch_bounds__(kMostWarps * 32) paged_append_kernel(const Pag
     const long long w = static_cast<long long>(blockIdx.x) * warps + warp;
     const long long t = w / p.parts;
     const int part = static_cast<int>(w % p.parts);
+    const int H = p.q.data != nullptr ? p.H : 0, H_kv = p.c.H_kv;
+    const int rows = H + 2 * H_kv;  // the token's query heads, key heads, value heads
+    const int per_row = p.c.d / 16, u = lane % per_row;
+    const int rows_per_warp = 32 / per_row, step = p.parts * rows_per_warp;
+    const int pairs = p.rot / 16;
+    // this lane's two pieces of a row: the sides of eight pairs, or of rows that are not turned any two
+    const bool turn = u < pairs;
+    const int e0 = !turn ? p.rot + 16 * (u - pairs) : kInterleaved ? 16 * u : 8 * u;
+    const int e1 = !turn || kInterleaved ? e0 + 8 : e0 + p.rot / 2;
+    uint4 x[kBatch], y[kBatch];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = r0 + k * step;
+            if (r >= rows) break;
+            const bool value = r >= H + H_kv;
+            const RowsView& from = r < H ? p.q : value ? p.v : p.k;
+            const uint16_t* src = from.data + t * from.row + (r < H ? r : value ? r - H - H_kv : r - H) * from.head;
+            x[k] = *reinterpret_cast<const uint4*>(src + (value ? 16 * u : e0));
+            y[k] = *reinterpret_cast<const uint4*>(src + (value ? 16 * u + 8 : e1));
+        }
+    };
+    // the first rows are on their way while sequence, slot, page and angles are looked up, one behind the other
+    const int first = part * rows_per_warp + lane / per_row;
+    if (t < p.T) load(first);
     int b = -1;
     if (t < p.T) b = p.cu != nullptr ? sequence_of(p.cu, p.c.B, t) : static_cast<int>(t / p.n);
     if (b >= 0) {
@@ -71,12 +96,6 @@ __global__ void __launch_bounds__(kMostWarps * 32) paged_append_kernel(const Pag
         } else {
             error = kDevErrCapacity;
         }
-        // this lane's two pieces of a row: the sides of eight pairs, or of rows that are not turned any two
-        const int per_row = p.c.d / 16, u = lane % per_row;
-        const int pairs = p.rot / 16;
-        const bool turn = u < pairs;
-        const int e0 = !turn ? p.rot + 16 * (u - pairs) : kInterleaved ? 16 * u : 8 * u;
-        const int e1 = !turn || kInterleaved ? e0 + 8 : e0 + p.rot / 2;
         float cs[8], sn[8];
         if (turn) {
             long long pos = p.positions != nullptr ? p.positions[t] : p.first_position + slot;
@@ -91,22 +110,9 @@ __global__ void __launch_bounds__(kMostWarps * 32) paged_append_kernel(const Pag
             sn[0] = d.x, sn[1] = d.y, sn[2] = d.z, sn[3] = d.w, sn[4] = e.x, sn[5] = e.y, sn[6] = e.z, sn[7] = e.w;
         }
         if (error != 0 && part == 0 && lane == 0) atomicOr(&p.status->word, error);
-        const int H = p.q.data != nullptr ? p.H : 0, H_kv = p.c.H_kv;
-        const int rows = H + 2 * H_kv;  // the token's query heads, key heads, value heads
-        const int rows_per_warp = 32 / per_row, step = p.parts * rows_per_warp;
         const size_t head_size = static_cast<size_t>(p.c.page) * p.c.d;
-        for (int r0 = part * rows_per_warp + lane / per_row; r0 < rows; r0 += kBatch * step) {
-            uint4 x[kBatch], y[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int r = r0 + k * step;
-                if (r >= rows) break;
-                const bool value = r >= H + H_kv;
-                const RowsView& from = r < H ? p.q : value ? p.v : p.k;
-                const uint16_t* src = from.data + t * from.row + (r < H ? r : value ? r - H - H_kv : r - H) * from.head;
-                x[k] = *reinterpret_cast<const uint4*>(src + (value ? 16 * u : e0));
-                y[k] = *reinterpret_cast<const uint4*>(src + (value ? 16 * u + 8 : e1));
-            }
+        for (int r0 = first; r0 < rows; r0 += kBatch * step) {
+            if (r0 != first) load(r0);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int r = r0 + k * step;
