@@ -306,8 +306,7 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
     int n_q_tiles = p.n_q_tiles, n_kv = p.Nkv, causal_offset = p.causal_offset;
     // first tile of a query head's statistics and first row of its accumulator
     [[maybe_unused]] int pad_tile = 0;
-    const CUtensorMap *pm_q = &map_q, *pm_k = &map_k, *pm_v = &map_v, *pm_do = &map_do, *pm_dk = &map_dk,
-                      *pm_dv = &map_dv;
+    const CUtensorMap *pm_q = &map_q, *pm_k = &map_k, *pm_v = &map_v, *pm_do = &map_do;
     // Query tiles that see a key of this block: all, or under the causal mask
     // those holding a row i >= kb*128 - causal_offset (query i sees key j iff
     // j <= i + causal_offset).  The last query row sees every key, so at
@@ -405,8 +404,6 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         pm_k = maps + kMapK;
         pm_v = maps + kMapV;
         pm_do = maps + kMapDout;
-        pm_dk = maps + kMapDk;
-        pm_dv = maps + kMapDv;
         plan();
     }
     const bool has_work = T > 0;
@@ -875,10 +872,17 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         if (t == 0) {
             const bool all_in = bwd_wait(bar(C::kBarEpi + w), 0, abort_flag, p, 45);
             if (all_in && !*abort_flag) {
-                const CUtensorMap* map = (w == 0) ? pm_dv : pm_dk;
-                if constexpr (kPacked) acquire_map(map);
+                const CUtensorMap* map = (w == 0) ? &map_dv : &map_dk;
+                int row = kb * 128, head = unit;
+                if constexpr (kPacked) {  // (read again rather than held over the loop)
+                    const volatile int* info = block_info;
+                    map = p.maps + info[0] * kPackedMaps + (w == 0 ? kMapDv : kMapDk);
+                    row = info[1] * 128;
+                    head = info[5];
+                    acquire_map(map);
+                }
                 for (int a = 0; a < C::kAtoms; ++a)
-                    tma_store_3d(map, smem_u32(stage + a * C::kAtomBytes), a * C::kAtomElems, kb * 128, unit);
+                    tma_store_3d(map, smem_u32(stage + a * C::kAtomBytes), a * C::kAtomElems, row, head);
                 tma_store_commit();
                 tma_store_wait_read();
             }
