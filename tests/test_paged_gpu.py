@@ -266,3 +266,231 @@ def test_shared_prefix(prefix, B, H, H_kv, N_q, d, dtype, page):
     lengths = [(53 * b) % 300 for b in range(B)]
     c, pages = cache_of(g, lengths, H_kv, d, page, dtype, prefix=prefix)
     check(g, c, lengths, H, N_q, causal=N_q > 1, prefix_pages=pages, prefix=prefix)
+
+
+@pytest.mark.parametrize("N_q,length", [(4, 2), (4, 4), (4, 5), (8, 1), (3, 0), (4, 127), (4, 130), (2, 640)])
+@pytest.mark.parametrize("prefix", [0, 33])
+@pytest.mark.parametrize("d", [64, 128])
+def test_causal_drafts(N_q, length, prefix, d):
+    """Drafts longer than what they follow: rows that see nothing (or the prefix alone)."""
+    g = rng(14)
+    lengths = [length, 300]
+    c, pages = cache_of(g, lengths, 2, d, 16, prefix=prefix)
+    check(g, c, lengths, 4, N_q, causal=True, prefix_pages=pages, prefix=prefix)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.0])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_scales(scale, prefix):
+    g = rng(15)
+    lengths = [300, 17]
+    c, pages = cache_of(g, lengths, 2, 64, 32, prefix=prefix)
+    check(g, c, lengths, 6, 1, scale=scale, prefix_pages=pages, prefix=prefix)
+
+
+@pytest.mark.parametrize("G", [4, 8, 16, 32])  # rows of a block
+@pytest.mark.parametrize("prefix", [0, 1500])
+def test_growing_scores(G, prefix):
+    """Every tile's scores are far above the one's before it: the reference moves each time."""
+    g = rng(16)
+    lengths = [2000, 900]
+    c, pages = cache_of(g, lengths, 1, 64, 64, prefix=prefix)
+    q = torch.ones(2, G, 1, 64, device="cuda").bfloat16() * torch.linspace(0.2, 1, G, device="cuda").bfloat16()[None, :, None, None]
+    for numbers, n, base in [(pages, prefix, 0)] * (prefix > 0) + [(c.block_table[b], n, prefix) for b, n in enumerate(lengths)]:
+        for s in range(0, n, 64):
+            c.k_pages[int(numbers[s // 64]), :, :n - s] = (base + s) / 512
+    check(g, c, lengths, G, 1, prefix_pages=pages, prefix=prefix, q=q)
+
+
+def test_lengths_outside_the_cache_are_clamped():
+    g = rng(17)
+    c, _ = cache_of(g, [64, 64, 64], 2, 64, 16, poison=False)
+    q = torch.randn(3, 4, 1, 64, generator=g, device="cuda").bfloat16()
+    want = fa.paged_attention(q, c)
+    c.lengths.copy_(int32([64, 1 << 30, -5]))
+    out, lse = fa.paged_attention(q, c)
+    assert torch.equal(out[:2], want[0][:2]) and torch.equal(lse[:2], want[1][:2])
+    assert (out[2] == 0).all() and (lse[2] == -math.inf).all()
+
+
+@pytest.mark.parametrize("prefix", [0, 64])
+def test_pages_outside_the_pool_read_as_zeros(prefix):
+    g = rng(18)
+    c, pages = cache_of(g, [100, 40], 2, 128, 16, poison=False, prefix=prefix)
+    c.block_table[0, 2], c.block_table[1, 0] = c.num_pages + 5, -3
+    if prefix:
+        pages[1] = 1 << 30
+    q = torch.randn(2, 4, 1, 128, generator=g, device="cuda").bfloat16()
+    got = fa.paged_attention(q, c, prefix_pages=pages, prefix_length=prefix)
+    # the same with a page of zeros
+    zero = torch.zeros(1, *c.k_pages.shape[1:], device="cuda").bfloat16()
+    k, v = torch.cat((c.k_pages, zero)), torch.cat((c.v_pages, zero))
+    bad = (c.block_table < 0) | (c.block_table >= c.num_pages)
+    c2 = fa.PagedKVCache(k, v, torch.where(bad, c.num_pages, c.block_table).int(), c.lengths)
+    if prefix:
+        pages = torch.where(pages >= c.num_pages, c.num_pages, pages).int()
+    want = fa.paged_attention(q, c2, prefix_pages=pages, prefix_length=prefix)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_one_page_in_many_sequences():
+    """A prompt's pages in several block tables, and the same page twice in one."""
+    g = rng(19)
+    c, _ = cache_of(g, [160, 96], 2, 64, 32)
+    c.block_table[1, :2] = c.block_table[0, 3]
+    check(g, c, [160, 96], 4, 1)
+
+
+def test_pools_pass_32_bits():
+    """Pages behind 2^32 elements of the pool, written and attended to."""
+    g = rng(20)
+    H_kv, page, d = 8, 128, 128
+    num = 2 ** 32 // (H_kv * page * d) + 40
+    k = torch.zeros(num, H_kv, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    table = torch.arange(num - 8, num, device="cuda").int().flip(0).reshape(2, 4).contiguous()
+    c = fa.PagedKVCache(k, v, table, int32([0, 0]))
+    lens = [500, 130]
+    check_append(g, c, lens, 16, fa.rotary_table(512, d))
+    check(g, c, lens, 16, 1)
+    check(g, c, lens, 16, 1, prefix_pages=table[0, :2].contiguous(), prefix=200)
+    assert not k[:num - 8].any()
+
+
+def test_long_cache():
+    """One sequence over many CTAs, every SM's run a part of it."""
+    g = rng(21)
+    lengths = [150000]
+    c, _ = cache_of(g, lengths, 1, 64, 128)
+    check(g, c, lengths, 4, 1)
+
+
+# ------------------------------------------------- streams, captured calls, calls at once
+@pytest.mark.parametrize("prefix", [0, 700])
+def test_repeats_and_another_stream(prefix):
+    g = rng(22)
+    c, pages = cache_of(g, [300, 5, 7000, 0], 2, 128, 64, prefix=prefix)
+    q = torch.randn(4, 8, 2, 128, generator=g, device="cuda").bfloat16()
+    want = fa.paged_attention(q, c, causal=True, prefix_pages=pages, prefix_length=prefix)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (None, s):
+        got = fa.paged_attention(q, c, causal=True, prefix_pages=pages, prefix_length=prefix, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_results_do_not_depend_on_the_workspace():
+    g = rng(23)
+    c, pages = cache_of(g, [300, 5, 7000, 0], 2, 128, 64, prefix=300)
+    q = torch.randn(4, 8, 1, 128, generator=g, device="cuda").bfloat16()
+    want = None
+    for fill in (0, 255):
+        ws = torch.full((c.workspace_size(8, 1, 300),), fill, dtype=torch.uint8, device="cuda")
+        got = fa.paged_attention(q, c, prefix_pages=pages, prefix_length=300, workspace=ws)
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_at_once():
+    jobs = []
+    for i, (lengths, prefix) in enumerate((([5000, 1, 400], 0), ([100] * 30, 1000), ([20000], 0), ([64, 3000], 77))):
+        g = rng(30 + i)
+        c, pages = cache_of(g, lengths, 2, 128, 16, prefix=prefix)
+        q = torch.randn(len(lengths), 8, 1, 128, generator=g, device="cuda").bfloat16()
+        jobs.append((q, c, pages, prefix, fa.paged_attention(q, c, prefix_pages=pages, prefix_length=prefix)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(20):
+        got = []
+        for s, (q, c, pages, prefix, _) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                got.append(fa.paged_attention(q, c, prefix_pages=pages, prefix_length=prefix))
+        torch.cuda.synchronize()
+        for a, (_, _, _, _, want) in zip(got, jobs):
+            assert all(torch.equal(x, y) for x, y in zip(a, want))
+
+
+# ---------------------------------------------------------- a serving loop
+@pytest.mark.parametrize("prefix", [0, 100])
+@pytest.mark.parametrize("d,dtype,page", [(64, "f16", 16), (128, "bf16", 64)])
+def test_prompts_then_captured_steps(prefix, d, dtype, page):
+    """Prompts of different lengths rotated, stored and attended to, then decode steps in a captured graph that advances
+    the lengths, against 64-bit attention over the rotated rows that the cache holds."""
+    g = rng(40)
+    H, H_kv, steps = 8, 2, 5
+    lens = [130, 1, 77]
+    c, pages = cache_of(g, [0, 0, 0], H_kv, d, page, dtype, room=max(lens) + steps, prefix=prefix)
+    table = fa.rotary_table(prefix + max(lens) + steps, d)
+    T, cu = sum(lens), int32(R.offsets(lens))
+    q, k, v = (rows(g, T, h, d, dtype=dtype) for h in (H, H_kv, H_kv))
+    k_rot = torch.empty_like(k)
+    q_rot = fa.paged_append(c, k, v, cu=cu, q=q, table=table, first_position=prefix, k_out=k_rot)
+    assert c.lengths.tolist() == lens
+    pos = torch.cat([torch.arange(n, device="cuda") for n in lens]) + prefix
+    within(q_rot, *rotated(q, table, pos, False))
+    within(k_rot, *rotated(k, table, pos, False))
+    for b, n in enumerate(lens):  # the cache holds the rows that the prompt attends over
+        at = R.offsets(lens)[b]
+        assert torch.equal(gather(c.k_pages, c.block_table[b], n), k_rot[at:at + n])
+        assert torch.equal(gather(c.v_pages, c.block_table[b], n), v[at:at + n])
+    out, lse = fa.packed_attention(q_rot, k_rot, v, cu, causal=True)
+    want_o, want_l, tol_o, tol_l = R.forward(q_rot, k_rot, v, R.offsets(lens), R.offsets(lens), 1 / math.sqrt(d), True)
+    within(out, want_o, tol_o)
+    within(lse, want_l, tol_l)
+
+    new = [[rows(g, 3, h, d, dtype=dtype) for h in (H, H_kv, H_kv)] for _ in range(steps)]
+    q1, k1, v1 = (torch.zeros_like(x) for x in new[0])
+    ws = torch.empty(c.workspace_size(H, 1, prefix), dtype=torch.uint8, device="cuda")
+
+    def step():
+        q1_rot = fa.paged_append(c, k1, v1, q=q1, table=table, first_position=prefix)
+        return q1_rot, *fa.paged_attention(q1_rot.view(3, H, 1, d), c, prefix_pages=pages, prefix_length=prefix, workspace=ws)
+
+    held = c.lengths.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q1_rot, out, lse = step()
+    c.lengths.copy_(held)
+    for i in range(steps):
+        for x, y in zip((q1, k1, v1), new[i]):
+            x.copy_(y)
+        graph.replay()
+        lengths = [n + i + 1 for n in lens]
+        assert c.lengths.tolist() == lengths
+        within(q1_rot, *rotated(q1, table, torch.tensor(lengths, device="cuda") - 1 + prefix, False))
+        want_o, want_l, tol_o, tol_l = reference(q1_rot.view(3, H, 1, d), c, lengths, 1 / math.sqrt(d), False, pages, prefix)
+        within(out, want_o, tol_o)
+        within(lse, want_l, tol_l)
+
+
+def test_a_prefix_is_as_if_each_sequence_held_it():
+    g = rng(41)
+    prefix, lengths, page = 200, [50, 130, 1], 32
+    c, pages = cache_of(g, lengths, 2, 64, page, prefix=prefix)
+    q = torch.randn(3, 8, 1, 64, generator=g, device="cuda").bfloat16()
+    out, lse = fa.paged_attention(q, c, prefix_pages=pages, prefix_length=prefix)
+    # copies of prefix and own slots, page after page
+    k, v = [], []
+    for b, n in enumerate(lengths):
+        for to, x in ((k, c.k_pages), (v, c.v_pages)):
+            to.append(torch.cat((gather(x, pages, prefix), gather(x, c.block_table[b], n))).float())
+    most = max(len(x) for x in k)
+    cap = -(-most // page)
+    kp, vp = (torch.zeros(3 * cap, 2, page, 64, device="cuda").bfloat16() for _ in range(2))
+    table = torch.arange(3 * cap, device="cuda").int().view(3, cap)
+    for b in range(3):
+        for pool, x in ((kp, k[b]), (vp, v[b])):
+            full = torch.zeros(cap * page, 2, 64, device="cuda")
+            full[:len(x)] = x
+            pool[b * cap:(b + 1) * cap] = full.view(cap, page, 2, 64).transpose(1, 2).bfloat16()
+    one = fa.PagedKVCache(kp, vp, table, int32([len(x) for x in k]))
+    o2, l2 = fa.paged_attention(q, one)
+    _, _, tol, tol_l = reference(q, c, lengths, 1 / 8, False, pages, prefix)
+    within(o2, out.double(), 2 * tol)
+    within(l2, lse.double(), 2 * tol_l)
