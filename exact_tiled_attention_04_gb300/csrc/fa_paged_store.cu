@@ -41,8 +41,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, long long t
 __device__ __forceinline__ int held(const PagedCache& c, int b) { return min(max(c.lengths[b], 0), c.capacity); }
 
 __device__ __forceinline__ int advanced(const PagedAppendParams& p, int b) {
-    const long long n = p.cu != nullptr ? max(p.cu[b + 1] - p.cu[b], 0) : p.n;
-    return static_cast<int>(min(static_cast<long long>(held(p.c, b)) + n, static_cast<long long>(p.c.capacity)));
+    const long long n = p.cu != nullptr ? static_cast<long long>(p.cu[b + 1]) - p.cu[b] : p.n;
+    return static_cast<int>(min(held(p.c, b) + max(n, 0ll), static_cast<long long>(p.c.capacity)));
 }
 
 template <bool F16, bool kInterleaved>
@@ -82,8 +82,7 @@ __global__ void __launch_bounds__(kMostWarps * 32) paged_append_kernel(const Pag
     int b = -1;
     if (t < p.T) b = p.cu != nullptr ? sequence_of(p.cu, p.c.B, t) : static_cast<int>(t / p.n);
     if (b >= 0) {
-        const int i = static_cast<int>(p.cu != nullptr ? t - p.cu[b] : t % p.n);
-        const long long slot = static_cast<long long>(held(p.c, b)) + i;
+        const long long slot = held(p.c, b) + (p.cu != nullptr ? t - p.cu[b] : t % p.n);  // (64 bits: whatever cu holds)
         // where the row goes in the cache
         long long at = -1;  // its element in a head's pages
         unsigned int error = 0;

@@ -616,7 +616,9 @@ typedef struct {
  *
  *   k, v       : views of T rows and H_kv heads;  cu: int32 [B + 1] on the
  *                device, rows cu[b] .. cu[b + 1] - 1 are sequence b's (not
- *                decreasing, within 0 .. T), or NULL: T / B rows each.
+ *                decreasing, within 0 .. T; with other values no row outside
+ *                the tensors and the pool is read or written, but what is stored
+ *                and the lengths are not defined), or NULL: T / B rows each.
  *   q, q_out   : views of T rows and H heads, or both NULL; q_out may be q.
  *   k_out      : view of T rows and H_kv heads that gets the rotated keys too
  *                (for fa_packed_fwd over a prompt), or NULL; may be k.

@@ -165,6 +165,33 @@ def test_append_types_and_pages(page, d, dtype):
     check_append(g, c, lens, 6, fa.rotary_table(900, d), with_k=True)
 
 
+@pytest.mark.parametrize("cu", [[-2 ** 31, 5, 20, 41], [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 41], [30, 10, 50, 2 ** 31 - 1], [41, 0, 0, 0]])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_offsets_that_are_none(cu, in_place):
+    """Offsets out of range or order: other pages and rows are not touched, lengths stay within the capacity, and the
+    next call is as ever."""
+    g = rng(22)
+    c, _ = cache_of(g, [15, 3, 100], 2, 64, 16, room=60, poison=False)
+    mine = [int(x) for x in c.block_table.flatten() if x >= 0]
+    other = [i for i in range(c.num_pages) if i not in mine]
+    was = [x[other].clone() for x in (c.k_pages, c.v_pages)]
+    held = c.lengths.clone()
+    table = fa.rotary_table(200, 64)
+    guard = torch.full((2, 141, 2, 64), 5.0, device="cuda").bfloat16()
+    x = rows(g, 41, 2, 64)
+    out = torch.empty_like(c.lengths)
+    fa.paged_append(c, x, x, cu=int32(cu), q=x, q_out=guard[0, 50:91], k_out=guard[1, 50:91], table=table,
+                    lengths_out=None if in_place else out)
+    got = c.lengths if in_place else out
+    assert fa.fa_device_status(None) in (fa.FA_OK, fa.FA_ERR_CAPACITY, fa.FA_ERR_RANGE)
+    assert (got >= held).all() and (got <= c.capacity).all()
+    assert (guard[:, :50] == 5).all() and (guard[:, 91:] == 5).all()
+    for a, b in zip(was, (c.k_pages, c.v_pages)):
+        assert torch.equal(a, b[other])
+    c.lengths.copy_(held)
+    check_append(g, c, [3, 0, 38], 2, table)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("d,rot", [(64, 64), (64, 16), (128, 128), (128, 48), (128, 112)])
 def test_append_rotations(d, rot, interleaved):
