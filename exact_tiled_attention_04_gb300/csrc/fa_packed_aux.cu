@@ -4,6 +4,9 @@
 //         row of the fp32 dQ accumulator; and the tensor maps of each sequence's
 //         rows;
 //   dq:   dQ = scale * accumulator in the input dtype.
+// What bounds them: memory.  For 16384 rows of 32 heads, d = 128: prep 82 us for 537
+// MB (6.5 TB/s: o and dO read, the accumulator's zeros written), dq 56 us for 403
+// MB (7.2 TB/s, part of the accumulator being in L2 still).
 // A block has one tile of 128 rows of one head; rows of 16-byte chunks, d / 8
 // lanes a row, so that a warp reads whole lines whatever the strides.
 #include <cmath>

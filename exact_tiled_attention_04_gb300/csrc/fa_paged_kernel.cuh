@@ -15,9 +15,15 @@
 // the softmax still ends this one, Q, S^T and O^T have two buffers each, and two
 // softmax warpgroups take the units in turn, as the ends of one (its last
 // product, the sums over 128 threads, its rows' way out) take as long as three of
-// its tiles (64 sequences of up to 512 slots behind a prefix: %s).
+// its tiles (64 sequences of up to 512 slots behind a prefix of 8192: 52.5 us
+// against 60.7 with one).
 // Of a unit cut between CTAs each leaves a partial result, at most two a CTA,
 // which a second kernel adds up in order, so results do not depend on timing.
+//
+// Measured: 32 sequences of up to 16384 slots (H = 32 over 8, d = 128, bf16, pages
+// of 64) 167 us, 6.6 TB/s of keys and values; four of up to 1000 (8 over 2, d =
+// 64) 7.5 us, the depth of the two kernels: set-up, the run's place, the first
+// tile, the unit's end, the second kernel.
 //
 // Pages.  A tile of 128 keys is 128 / page boxes of a tensor map over
 // [pages, H_kv, page, d], one or more per lane of the loading warp.  Pages behind the
