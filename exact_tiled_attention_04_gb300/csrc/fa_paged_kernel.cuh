@@ -641,16 +641,16 @@ struct Joined {
     float M = -INFINITY, L = 0.0f, LQ = 0.0f, acc[kPer] = {};
 
     // `parts` of them: part i's statistics and row by stats(i) and row(i).
-    template <class Stats, class Row>
-    __device__ __forceinline__ void add(int parts, Stats stats, Row row) {
+    template <int kAhead, class Stats, class Row>
+    __device__ __forceinline__ void add_by(int parts, Stats stats, Row row) {
         const int lane = static_cast<int>(threadIdx.x) % 32;
-        for (int i0 = 0; i0 < parts; i0 += kJoinAhead) {
-            const int here = min(kJoinAhead, parts - i0);
+        for (int i0 = 0; i0 < parts; i0 += kAhead) {
+            const int here = min(kAhead, parts - i0);
             float4 ml = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
             if (lane < here) ml = stats(i0 + lane);
-            float o[kJoinAhead][kPer];
+            float o[kAhead][kPer];
 #pragma unroll
-            for (int k = 0; k < kJoinAhead; ++k) {  // (those past the last repeat it)
+            for (int k = 0; k < kAhead; ++k) {  // (those past the last repeat it)
                 const float* src = row(i0 + min(k, here - 1)) + lane * kPer;
                 if constexpr (kPer == 4) {
                     const float4 y = *reinterpret_cast<const float4*>(src);
@@ -678,7 +678,7 @@ struct Joined {
 #pragma unroll
             for (int x = 0; x < kPer; ++x) acc[x] *= old;
 #pragma unroll
-            for (int k = 0; k < kJoinAhead; ++k) {
+            for (int k = 0; k < kAhead; ++k) {
                 const float f = __shfl_sync(0xffffffffu, w, k);
                 if (k < here && f != 0.0f) {  // (0 times what a part without keys holds)
 #pragma unroll
@@ -686,6 +686,11 @@ struct Joined {
                 }
             }
         }
+    }
+    template <class Stats, class Row>
+    __device__ __forceinline__ void add(int parts, Stats stats, Row row) {
+        if (parts <= 4) add_by<4>(parts, stats, row);
+        else add_by<kJoinAhead>(parts, stats, row);
     }
 };
 
