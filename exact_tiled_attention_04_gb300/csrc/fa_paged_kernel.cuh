@@ -536,7 +536,7 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
                     for (int a = 0; ok && a < C::kAtoms; ++a) {
                         uint4* row = reinterpret_cast<uint4*>(smem + C::kOffV + s_ * C::kTileBytes + a * C::kAtomBytes + t * 128);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int i = 0; i < 8; ++i) row[i ^ (t & 7)] = make_uint4(0u, 0u, 0u, 0u);  // (all banks at a time)
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);
