@@ -54,7 +54,7 @@ struct Cfg {
     static constexpr int kUmmaK = 16;
     static constexpr int kQkSteps = D / kUmmaK;
     static constexpr int kPvSteps = 128 / kUmmaK;
-    static constexpr int kStages = D == 128 ? 3 : 6;  // K+V stages
+    static constexpr int kStages = D == 128 ? 3 : 6;  // of K, and of V
     // Softmax warpgroups: two take the run's units in turn (at 32 rows their
     // registers would not fit).
     static constexpr int kGroups = NR == 16 ? 2 : 1;
@@ -81,9 +81,9 @@ struct Cfg {
     // barriers
     static constexpr int kBarQFull = 0;                   // [2] a unit's Q landed
     static constexpr int kBarQEmpty = kBarQFull + 2;      // [2] its last scores are computed
-    static constexpr int kBarFull = kBarQEmpty + 2;       // [kStages] K and V of a tile landed
-    static constexpr int kBarEmpty = kBarFull + kStages;  // [kStages] both consumed
-    static constexpr int kBarS = kBarEmpty + kStages;     // [kGroups][2] S^T buffer ready, by the group's own count of tiles
+    static constexpr int kBarFull = kBarQEmpty + 2;           // [K, V][kStages] a tile landed
+    static constexpr int kBarEmpty = kBarFull + 2 * kStages;  // [K, V][kStages] its product is done
+    static constexpr int kBarS = kBarEmpty + 2 * kStages;     // [kGroups][2] S^T buffer ready, by the group's own count of tiles
     static constexpr int kBarP = kBarS + 2 * kGroups;     // [2] P^T buffer written (4 warps)
     static constexpr int kBarPFree = kBarP + 2;           // [2] the product reading it is done
     static constexpr int kBarO = kBarPFree + 2;           // [2] every product of a unit is done
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
             mbar_init(bar(C::kBarO + b), 1);
             mbar_init(bar(C::kBarOFree + b), 4);
         }
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < 2 * C::kStages; ++s) {
             mbar_init(bar(C::kBarFull + s), 1);
             mbar_init(bar(C::kBarEmpty + s), 1);
         }
@@ -308,14 +308,10 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
         // ---------------------------------------------------------- producer
         const uint64_t once = policy_evict_first();  // every byte here is read once
         const int pages = 128 / p.c.page;            // of a tile
-        // this lane's boxes of a tile: a part (K or V, 64 channels) of page `mine` and of every 32 / (2 kAtoms)-th one behind it
-        constexpr int kParts = 2 * C::kAtoms;
-        const int part = lane % kParts, mine = lane / kParts;
-        const bool value = part >= C::kAtoms;
-        const int atom = part % C::kAtoms;
-        const CUtensorMap* map = value ? &map_v : &map_k;
-        const uint32_t dst0 = sbase + (value ? C::kOffV : C::kOffK) + atom * C::kAtomBytes;
-        int it = 0, seg = 0;
+        // this lane's box of K's or V's tile: 64 channels of page `mine` (8 pages at most, 2 boxes each)
+        const int mine = lane / C::kAtoms, atom = lane % C::kAtoms;
+        const uint32_t box = static_cast<uint32_t>(atom * C::kAtomBytes + mine * p.c.page * 128);
+        int it = 0, keys = 0, seg = 0;  // tiles, their K loads issued, units
         bool ok = true;
         for (Cursor k = start; ok && k.valid(); k.next(p.c, units), ++seg) {
             const int kvh = k.u / p.row_blocks, rb = k.u % p.row_blocks;
@@ -332,26 +328,32 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
             for (int j = k.t; j < k.last(); ++j, ++it) {
                 const int s = it % C::kStages;
                 const int have = min(pages, (k.len - j * 128 + p.c.page - 1) / p.c.page);  // pages of the tile in use
-                int id = mine < have ? table[j * pages + mine] : 0;
-                ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarEmpty + s), ((it / C::kStages) & 1) ^ 1, abort_flag, p, 60));
-                if (!ok) break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar(C::kBarFull + s),
-                                          static_cast<uint32_t>(have * p.c.page) * (kParts * 128u));
-                __syncwarp();
-                for (int g = mine; g < have; g += 32 / kParts) {
-                    if (g != mine) id = table[j * pages + g];
-                    tma_load_4d(dst0 + s * C::kTileBytes + g * p.c.page * 128, map, bar(C::kBarFull + s),
-                                atom * C::kAtomElems, 0, kvh, id, once);
+                const int id = mine < have ? table[j * pages + mine] : 0;
+                // (K's stage is free when the scores are computed, a product before V's)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    if (ok) ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarEmpty + v * C::kStages + s),
+                                                                    ((it / C::kStages) & 1) ^ 1, abort_flag, p, 60));
+                    if (!ok) break;
+                    const uint32_t full = bar(C::kBarFull + v * C::kStages + s);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(have * p.c.page) * (C::kAtoms * 128u));
+                    __syncwarp();
+                    if (mine < have)
+                        tma_load_4d(sbase + (v ? C::kOffV : C::kOffK) + s * C::kTileBytes + box, v ? &map_v : &map_k, full,
+                                    atom * C::kAtomElems, 0, kvh, id, once);
+                    __syncwarp();
+                    if (v == 0) ++keys;
                 }
-                __syncwarp();
+                if (!ok) break;
             }
         }
         // every issued load has landed before the CTA may exit
         if (lane == 0) {
-            for (int s = 0; s < C::kStages && s < it; ++s) {
-                const int last = s + ((it - 1 - s) / C::kStages) * C::kStages;
-                wait_phase(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, p, 61, false);
+            for (int s = 0; s < C::kStages; ++s) {
+                if (s < keys) wait_phase(bar(C::kBarFull + s), ((keys - 1 - s) / C::kStages) & 1, abort_flag, p, 61, false);
+                if (s < it)
+                    wait_phase(bar(C::kBarFull + C::kStages + s), ((it - 1 - s) / C::kStages) & 1, abort_flag, p, 61, false);
             }
             for (int b = 0; b < 2 && b < seg; ++b) {
                 const int last = b + ((seg - 1 - b) / 2) * 2;
@@ -368,19 +370,32 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
             int seg_s = 0, seg_v = 0, js = ks.t, jv = kv.t;
             int scored[C::kGroups] = {};  // tiles of each softmax group so far
             bool ok = true;
+            // Operand descriptors: of a stage or a buffer by adding its offset / 16 (one
+            // thread's instructions are what a tile costs here, 1.2 us of them if
+            // each descriptor is put together anew)
+            const uint64_t dK0 = smem_desc_sw128(sbase + C::kOffK, 16, 1024);
+            const uint64_t dQ0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+            const uint64_t dV0 = smem_desc_sw128(sbase + C::kOffV, C::kAtomBytes, 1024);
+            const uint64_t dP0 = smem_desc_sw128(sbase + C::kOffP, 16, 1024);
+            uint32_t stage_s = 0, stage_v = 0, phase_s = 0, phase_v = 0;  // of the rings
             auto issue_s = [&](int it) {
                 if (js == ks.t) ok = wait_phase(bar(C::kBarQFull + (seg_s & 1)), (seg_s >> 1) & 1, abort_flag, p, 62);
-                if (ok) ok = wait_phase(bar(C::kBarFull + it % C::kStages), (it / C::kStages) & 1, abort_flag, p, 63);
+                if (ok) ok = wait_phase(bar(C::kBarFull + stage_s), phase_s, abort_flag, p, 63);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t sK = sbase + C::kOffK + (it % C::kStages) * C::kTileBytes;
-                const uint32_t sQ = sbase + C::kOffQ + (seg_s & 1) * C::kQBytes;
+                const uint64_t dK = dK0 + stage_s * (C::kTileBytes >> 4);
+                const uint64_t dQ = dQ0 + (seg_s & 1) * (C::kQBytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < C::kQkSteps; ++kk) {
                     const uint32_t koff = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
                     const uint32_t qoff = (kk * 32) / 128 * C::kRowAtomBytes + (kk * 32) % 128;
-                    mma_ss<false>(tmem + C::kColS + NR * (it & 1), smem_desc_sw128(sK + koff, 16, 1024),
-                                  smem_desc_sw128(sQ + qoff, 16, 1024), C::kIdescQK, kk > 0 ? 1u : 0u);
+                    mma_ss<false>(tmem + C::kColS + NR * (it & 1), dK + (koff >> 4), dQ + (qoff >> 4), C::kIdescQK,
+                                  kk > 0 ? 1u : 0u);
+                }
+                tc_commit(bar(C::kBarEmpty + stage_s));  // K is no longer read
+                if (++stage_s == C::kStages) {
+                    stage_s = 0;
+                    phase_s ^= 1;
                 }
                 if (C::kGroups == 2 && (seg_s & 1)) tc_commit(bar(C::kBarS + 2 + (scored[C::kGroups - 1]++ & 1)));
                 else tc_commit(bar(C::kBarS + (scored[0]++ & 1)));
@@ -398,21 +413,25 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
                 if (first && seg_v >= 2)  // O^T of the unit before the last one has been read
                     ok = wait_phase(bar(C::kBarOFree + (seg_v & 1)), ((seg_v >> 1) & 1) ^ 1, abort_flag, p, 71);
                 if (ok) ok = wait_phase(bar(C::kBarP + b), (it >> 1) & 1, abort_flag, p, 64);
+                if (ok) ok = wait_phase(bar(C::kBarFull + C::kStages + stage_v), phase_v, abort_flag, p, 73);
                 if (!ok) break;
                 tc_fence_after();
                 // O^T += V^T P^T: A = V read MN-major (d contiguous, its two
                 // 64-element blocks 16 KB apart), B = P^T K-major
-                const uint32_t sV = sbase + C::kOffV + (it % C::kStages) * C::kTileBytes;
-                const uint32_t sP = sbase + C::kOffP + b * 2 * C::kRowAtomBytes;
+                const uint64_t dV = dV0 + stage_v * (C::kTileBytes >> 4);
+                const uint64_t dP = dP0 + b * (2 * C::kRowAtomBytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < C::kPvSteps; ++kk) {
                     const uint32_t poff = (kk * 32) / 128 * C::kRowAtomBytes + (kk * 32) % 128;
-                    mma_ss<false>(tmem + C::kColO + NR * (seg_v & 1),
-                                  smem_desc_sw128(sV + kk * C::kUmmaK * 128, C::kAtomBytes, 1024),
-                                  smem_desc_sw128(sP + poff, 16, 1024), C::kIdescPV, (!first || kk > 0) ? 1u : 0u);
+                    mma_ss<false>(tmem + C::kColO + NR * (seg_v & 1), dV + (kk * C::kUmmaK * 128 >> 4), dP + (poff >> 4),
+                                  C::kIdescPV, (!first || kk > 0) ? 1u : 0u);
                 }
                 tc_commit(bar(C::kBarPFree + b));
-                tc_commit(bar(C::kBarEmpty + it % C::kStages));  // K and V are no longer read
+                tc_commit(bar(C::kBarEmpty + C::kStages + stage_v));  // V is no longer read
+                if (++stage_v == C::kStages) {
+                    stage_v = 0;
+                    phase_v ^= 1;
+                }
                 if (++jv == kv.last()) {
                     tc_commit(bar(C::kBarO + (seg_v & 1)));
                     kv.next(p.c, units);
@@ -531,7 +550,7 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
                 if (ok && it >= 2) ok = wait_phase(bar(C::kBarPFree + b), ((it - 2) >> 1) & 1, abort_flag, p, 68);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok && key >= k.len) {  // value rows behind the sequence's end, and of pages not loaded
-                    ok = wait_phase(bar(C::kBarFull + s_), (it / C::kStages) & 1, abort_flag, p, 72);
+                    ok = wait_phase(bar(C::kBarFull + C::kStages + s_), (it / C::kStages) & 1, abort_flag, p, 72);
 #pragma unroll 1
                     for (int a = 0; ok && a < C::kAtoms; ++a) {
                         uint4* row = reinterpret_cast<uint4*>(smem + C::kOffV + s_ * C::kTileBytes + a * C::kAtomBytes + t * 128);
