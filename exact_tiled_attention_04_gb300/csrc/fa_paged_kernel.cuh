@@ -58,8 +58,9 @@ struct Cfg {
     // Softmax warpgroups: two take the run's units in turn (at 32 rows their
     // registers would not fit).
     static constexpr int kGroups = NR == 16 ? 2 : 1;
-    static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1;
-    static constexpr int kThreads = (kLoadWarp + 1) * 32;
+    // Issuers of the scores (and owner of tensor memory) and of the products with V.
+    static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1, kPvWarp = kMmaWarp + 2;
+    static constexpr int kThreads = (kPvWarp + 1) * 32;
     static constexpr uint32_t kFmt = F16 ? 0u : 1u;
     static constexpr uint32_t kIdescQK = instr_desc(kFmt, false, false, 128, NR);
     static constexpr uint32_t kIdescPV = instr_desc(kFmt, true, false, 128, NR);
@@ -88,7 +89,7 @@ struct Cfg {
     static constexpr int kBarPFree = kBarP + 2;           // [2] the product reading it is done
     static constexpr int kBarO = kBarPFree + 2;           // [2] every product of a unit is done
     static constexpr int kBarOFree = kBarO + 2;           // [2] its O^T was read (4 warps)
-    static constexpr int kBarDrain = kBarOFree + 2;
+    static constexpr int kBarDrain = kBarOFree + 2;       // both issuers' last products are done
     static constexpr int kNumBars = kBarDrain + 1;
     static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
             mbar_init(bar(C::kBarFull + s), 1);
             mbar_init(bar(C::kBarEmpty + s), 1);
         }
-        mbar_init(bar(C::kBarDrain), 1);
+        mbar_init(bar(C::kBarDrain), 2);
         *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
         mbar_init_fence();
     }
@@ -361,30 +362,27 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
             }
         }
     } else if (warp == C::kMmaWarp) {
-        // ------------------------------------------------------------ issuer
+        // ------------------------------------------------------------ scores
+        // (Descriptors of a stage or a buffer by adding its offset / 16: one thread's
+        // instructions are what a tile costs here.)
         if (lane == 0 && start.valid()) {
-            const int total = start.end - start.pos;
-            // S^T of the run's tiles goes two ahead of their products with V, so in
-            // the next unit, maybe, while this one's are issued: a cursor each
-            Cursor ks = start, kv = start;
-            int seg_s = 0, seg_v = 0, js = ks.t, jv = kv.t;
-            int scored[C::kGroups] = {};  // tiles of each softmax group so far
-            bool ok = true;
-            // Operand descriptors: of a stage or a buffer by adding its offset / 16 (one
-            // thread's instructions are what a tile costs here, 1.2 us of them if
-            // each descriptor is put together anew)
             const uint64_t dK0 = smem_desc_sw128(sbase + C::kOffK, 16, 1024);
             const uint64_t dQ0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
-            const uint64_t dV0 = smem_desc_sw128(sbase + C::kOffV, C::kAtomBytes, 1024);
-            const uint64_t dP0 = smem_desc_sw128(sbase + C::kOffP, 16, 1024);
-            uint32_t stage_s = 0, stage_v = 0, phase_s = 0, phase_v = 0;  // of the rings
-            auto issue_s = [&](int it) {
-                if (js == ks.t) ok = wait_phase(bar(C::kBarQFull + (seg_s & 1)), (seg_s >> 1) & 1, abort_flag, p, 62);
-                if (ok) ok = wait_phase(bar(C::kBarFull + stage_s), phase_s, abort_flag, p, 63);
-                if (!ok) return;
+            const int total = start.end - start.pos;
+            uint32_t stage = 0, phase = 0;
+            int seg = 0, scored[C::kGroups] = {};  // units; tiles of each softmax group
+            Cursor k = start;
+            int j = k.t;
+            for (int it = 0; it < total; ++it) {
+                bool ok = true;
+                if (j == k.t) ok = wait_phase(bar(C::kBarQFull + (seg & 1)), (seg >> 1) & 1, abort_flag, p, 62);
+                if (ok) ok = wait_phase(bar(C::kBarFull + stage), phase, abort_flag, p, 63);
+                // the scores before in this buffer were read before their P^T was published
+                if (ok && it >= 2) ok = wait_phase(bar(C::kBarP + (it & 1)), ((it >> 1) & 1) ^ 1, abort_flag, p, 64);
+                if (!ok) break;
                 tc_fence_after();
-                const uint64_t dK = dK0 + stage_s * (C::kTileBytes >> 4);
-                const uint64_t dQ = dQ0 + (seg_s & 1) * (C::kQBytes >> 4);
+                const uint64_t dK = dK0 + stage * (C::kTileBytes >> 4);
+                const uint64_t dQ = dQ0 + (seg & 1) * (C::kQBytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < C::kQkSteps; ++kk) {
                     const uint32_t koff = (kk * 32) / 128 * C::kAtomBytes + (kk * 32) % 128;
@@ -392,53 +390,65 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
                     mma_ss<false>(tmem + C::kColS + NR * (it & 1), dK + (koff >> 4), dQ + (qoff >> 4), C::kIdescQK,
                                   kk > 0 ? 1u : 0u);
                 }
-                tc_commit(bar(C::kBarEmpty + stage_s));  // K is no longer read
-                if (++stage_s == C::kStages) {
-                    stage_s = 0;
-                    phase_s ^= 1;
-                }
-                if (C::kGroups == 2 && (seg_s & 1)) tc_commit(bar(C::kBarS + 2 + (scored[C::kGroups - 1]++ & 1)));
+                if (C::kGroups == 2 && (seg & 1)) tc_commit(bar(C::kBarS + 2 + (scored[C::kGroups - 1]++ & 1)));
                 else tc_commit(bar(C::kBarS + (scored[0]++ & 1)));
-                if (++js == ks.last()) {
-                    tc_commit(bar(C::kBarQEmpty + (seg_s & 1)));
-                    ks.next(p.c, units);
-                    js = ks.t;
-                    ++seg_s;
+                tc_commit(bar(C::kBarEmpty + stage));  // K is no longer read
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
-            };
-            for (int it = 0; ok && it < 2 && it < total; ++it) issue_s(it);
-            for (int it = 0; ok && it < total; ++it) {
+                if (++j == k.last()) {
+                    tc_commit(bar(C::kBarQEmpty + (seg & 1)));
+                    k.next(p.c, units);
+                    j = k.t;
+                    ++seg;
+                }
+            }
+            tc_commit(bar(C::kBarDrain));
+            wait_phase(bar(C::kBarDrain), 0, abort_flag, p, 65, false);
+        }
+    } else if (warp == C::kPvWarp) {
+        // ------------------------------------------------ products with V
+        if (lane == 0 && start.valid()) {
+            const uint64_t dV0 = smem_desc_sw128(sbase + C::kOffV, C::kAtomBytes, 1024);
+            const uint64_t dP0 = smem_desc_sw128(sbase + C::kOffP, 16, 1024);
+            const int total = start.end - start.pos;
+            uint32_t stage = 0, phase = 0;
+            int seg = 0;
+            Cursor k = start;
+            int j = k.t;
+            for (int it = 0; it < total; ++it) {
                 const int b = it & 1;
-                const bool first = jv == kv.t;
-                if (first && seg_v >= 2)  // O^T of the unit before the last one has been read
-                    ok = wait_phase(bar(C::kBarOFree + (seg_v & 1)), ((seg_v >> 1) & 1) ^ 1, abort_flag, p, 71);
-                if (ok) ok = wait_phase(bar(C::kBarP + b), (it >> 1) & 1, abort_flag, p, 64);
-                if (ok) ok = wait_phase(bar(C::kBarFull + C::kStages + stage_v), phase_v, abort_flag, p, 73);
+                const bool first = j == k.t;
+                bool ok = true;
+                if (first && seg >= 2)  // O^T of the unit before the last one has been read
+                    ok = wait_phase(bar(C::kBarOFree + (seg & 1)), ((seg >> 1) & 1) ^ 1, abort_flag, p, 71);
+                if (ok) ok = wait_phase(bar(C::kBarFull + C::kStages + stage), phase, abort_flag, p, 73);
+                if (ok) ok = wait_phase(bar(C::kBarP + b), (it >> 1) & 1, abort_flag, p, 74);
                 if (!ok) break;
                 tc_fence_after();
                 // O^T += V^T P^T: A = V read MN-major (d contiguous, its two
                 // 64-element blocks 16 KB apart), B = P^T K-major
-                const uint64_t dV = dV0 + stage_v * (C::kTileBytes >> 4);
+                const uint64_t dV = dV0 + stage * (C::kTileBytes >> 4);
                 const uint64_t dP = dP0 + b * (2 * C::kRowAtomBytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < C::kPvSteps; ++kk) {
                     const uint32_t poff = (kk * 32) / 128 * C::kRowAtomBytes + (kk * 32) % 128;
-                    mma_ss<false>(tmem + C::kColO + NR * (seg_v & 1), dV + (kk * C::kUmmaK * 128 >> 4), dP + (poff >> 4),
+                    mma_ss<false>(tmem + C::kColO + NR * (seg & 1), dV + (kk * C::kUmmaK * 128 >> 4), dP + (poff >> 4),
                                   C::kIdescPV, (!first || kk > 0) ? 1u : 0u);
                 }
                 tc_commit(bar(C::kBarPFree + b));
-                tc_commit(bar(C::kBarEmpty + C::kStages + stage_v));  // V is no longer read
-                if (++stage_v == C::kStages) {
-                    stage_v = 0;
-                    phase_v ^= 1;
+                tc_commit(bar(C::kBarEmpty + C::kStages + stage));  // V is no longer read
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
-                if (++jv == kv.last()) {
-                    tc_commit(bar(C::kBarO + (seg_v & 1)));
-                    kv.next(p.c, units);
-                    jv = kv.t;
-                    ++seg_v;
+                if (++j == k.last()) {
+                    tc_commit(bar(C::kBarO + (seg & 1)));
+                    k.next(p.c, units);
+                    j = k.t;
+                    ++seg;
                 }
-                if (it + 2 < total) issue_s(it + 2);  // buffer b: its S^T was read before this P^T was published
             }
             tc_commit(bar(C::kBarDrain));
             wait_phase(bar(C::kBarDrain), 0, abort_flag, p, 65, false);
