@@ -16,17 +16,21 @@
 // softmax warpgroups take the units in turn, as the ends of one (its last
 // product, the sums over 128 threads, its rows' way out) take as long as three of
 // its tiles (64 sequences of up to 512 slots behind a prefix of 8192: 52.5 us
-// against 60.7 with one).
+// against 60.7 with one).  A warp issues the scores and another the products with
+// V: one thread's instructions for both, 1.2 us a tile, were more than the tile's
+// 64 KB take (1.45 us on all SMs, less on some): 64 sequences of 256 slots 16.5 us
+// against 17.7.  K's stage of the ring is free a product before V's.
 // Of a unit cut between CTAs each leaves a partial result, at most two a CTA,
 // which a second kernel adds up in order, so results do not depend on timing.
 //
 // Measured: 32 sequences of up to 16384 slots (H = 32 over 8, d = 128, bf16, pages
-// of 64) 167 us, 6.6 TB/s of keys and values; four of up to 1000 (8 over 2, d =
-// 64) 7.5 us, the depth of the two kernels: set-up, the run's place, the first
-// tile, the unit's end, the second kernel.
+// of 64) 164 to 165 us, 6.7 TB/s of keys and values; 64 of 128, 512, 1024 and 4096
+// slots 11.5, 25.8, 46.8 and 159 us, about 7 us and their bytes; four of up to 1000
+// (8 over 2, d = 64) 7.2 to 7.5 us, the depth of the two kernels: set-up, the run's place, the
+// first tile, the unit's end, the second kernel.
 //
 // Pages.  A tile of 128 keys is 128 / page boxes of a tensor map over
-// [pages, H_kv, page, d], one or more per lane of the loading warp.  Pages behind the
+// [pages, H_kv, page, d] each for K and V, one per lane of the loading warp.  Pages behind the
 // last one in use are not loaded and a number outside the pool reads as
 // zeros.  Value rows behind a sequence's end hold anything; their weight is 0, but 0 x
 // infinity is not, so the softmax threads zero them in shared memory.
