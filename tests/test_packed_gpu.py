@@ -142,6 +142,41 @@ def test_backward_many_sequences(B, causal):
     check_backward(*batch(8, lens, 2, 1, 64, "bf16"), causal)
 
 
+@pytest.mark.parametrize("H,H_kv", [(1, 1), (4, 2)])  # blocks of 256 rows of a head, of 128 of two
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,first", [(64, 0), (65, 0), (65, 300), (700, 0)])
+def test_sequences_in_order(B, first, causal, H, H_kv):
+    """Batches of more sequences than are ordered by their work: empty ones, long ones among short ones, rows of no
+    sequence before and behind them, keys of other lengths."""
+    lens = [(0, 1, 700, 7, 128, 3, 129, 0, 31, 257)[(i * i + i // 7) % 10 if i % 13 == 0 else i % 2 + 3 * (i % 3 == 0)]
+            for i in range(B)]
+    lens_k = [n + (0, 5, 130)[i % 3] if i % 11 else 0 for i, n in enumerate(lens)]
+    g = rng(30)
+    Tq, Tk = sum(lens) + first + 40, sum(lens_k) + first + 40
+    q, k, v = rows(g, Tq, H, 64), rows(g, Tk, H_kv, 64), rows(g, Tk, H_kv, 64)
+    cu_q, cu_k = R.offsets(lens, first), R.offsets(lens_k, first)
+    dx = [torch.full(x.shape, 5.0, device="cuda").bfloat16() for x in (q, k, v)]
+    check_backward(q, k, v, cu_q, cu_k, causal, dq=dx[0], dk=dx[1], dv=dx[2])
+    for x, cu in zip(dx, (cu_q, cu_k, cu_k)):
+        assert (x[:first] == 5).all() and (x[cu[-1]:] == 5).all()
+
+
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_many_offsets_that_are_none(seed):
+    g = rng(31 + seed)
+    q, k, v, good, _ = batch(32, [100, 100, 200], 2, 2, 64, "bf16")
+    cu = torch.randint(-500, 1000, (100,), generator=g, device="cuda").int()
+    if seed == 1:
+        cu = torch.randint(-2 ** 31, 2 ** 31 - 1, (100,), generator=g, device="cuda").int()
+    if seed == 2:
+        cu = cu.sort(descending=True)[0]
+    guard = torch.full((3, 500, 2, 64), 5.0, device="cuda").bfloat16()
+    out, lse = fa.packed_attention(q, k, v, cu, causal=True, out=guard[0, 50:450])
+    fa.packed_attention_backward(q, k, v, out, lse, q, cu, causal=True, dq=guard[1, 50:450], dk=guard[2, 50:450])
+    assert (guard[:, :50] == 5).all() and (guard[:, 450:] == 5).all()
+    check_backward(q, k, v, good, good, True)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [False, True])
