@@ -4,8 +4,8 @@
 // The lengths are on the device, and a grid that follows them would need a
 // kernel or a copy ahead of every call.  Instead each CTA finds its own block,
 // with one warp, while the others set the CTA up.  Blocks are numbered by their
-// work, heaviest first, so that a long sequence's last blocks do not begin at
-// the end of the launch: with a mask block r of a sequence sees about r blocks
+// work, heaviest first (in batches of up to kMostByWork sequences), so that a long
+// sequence's last blocks do not begin at the end of the launch: with a mask block r of a sequence sees about r blocks
 // of keys more than its first one, so blocks with the same `level` (first
 // level of the sequence + r) cost about the same, and the number of blocks at
 // or above a level is a sum over the sequences.  A binary search over the

@@ -18,6 +18,7 @@ struct PagedCache {
     int32_t* lengths;        // [B]
     int num_pages, page, B, max_pages, H_kv, d;
     int capacity;            // max_pages * page
+    int unwaited;            // 1: read behind another kernel's wait for what wrote it (attention behind a prefix)
 };
 
 struct RowsView {

@@ -371,6 +371,7 @@ int fa_paged_fwd(const fa_paged_cache_t* cache, const void* q, void* o, float* l
     p.row_blocks = plan.row_blocks;
     p.ctas = plan.ctas;
     p.parts_always = prefix_length > 0 ? 1 : 0;
+    p.c.unwaited = p.parts_always;
     p.part_ml = reinterpret_cast<float4*>(ws + plan.part_ml);
     p.unit_o = reinterpret_cast<float*>(ws + plan.unit_o);
     p.ml_part = reinterpret_cast<float*>(ws + plan.prefix_ml);

@@ -105,7 +105,15 @@ struct Cfg {
     static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "operand tiles must be 1024-byte aligned");
 };
 
-__device__ __forceinline__ int length_of(const PagedCache& c, int b) { return min(max(c.lengths[b], 0), c.capacity); }
+// A word that a kernel before wrote.  Where no wait of this kernel's own lies
+// between (c.unwaited: behind a prefix's kernel; the second kernel), from L2, as the
+// SM's L1 may hold what was there before; else by way of L1, which saves the page
+// numbers' way (2 % of a step over long sequences).
+__device__ __forceinline__ int word_of(const int32_t* at, bool unwaited) { return unwaited ? __ldcg(at) : *at; }
+__device__ __forceinline__ int length_of(const PagedCache& c, int b, bool unwaited) {
+    return min(max(word_of(c.lengths + b, unwaited), 0), c.capacity);
+}
+__device__ __forceinline__ int length_of(const PagedCache& c, int b) { return length_of(c, b, c.unwaited != 0); }
 __device__ __forceinline__ int tiles_of(int len) { return (len + 127) / 128; }
 
 // Tiles of a run, all CTAs' alike (the tiles of all units number less than 2^31).
@@ -116,11 +124,11 @@ struct Spread {
     int before, total;  // in tiles of one unit each
     int len;            // of sequence b
 };
-__device__ __forceinline__ Spread spread_of(const PagedCache& c, int b) {
+__device__ __forceinline__ Spread spread_of(const PagedCache& c, int b, bool unwaited) {
     const int lane = static_cast<int>(threadIdx.x) % 32;
     int before = 0, total = 0, len = 0;
     for (int s = lane; s < c.B; s += 32) {
-        const int l = length_of(c, s), n = tiles_of(l);
+        const int l = length_of(c, s, unwaited), n = tiles_of(l);
         total += n;
         if (s < b) before += n;
         if (s == b) len = l;
@@ -153,7 +161,7 @@ struct Cursor {
 // The run of CTA blockIdx.x, by one warp.
 __device__ __forceinline__ Cursor first_of(const PagedCache& c, int units, int ctas) {
     const int lane = static_cast<int>(threadIdx.x) % 32;
-    const Spread all = spread_of(c, 0);
+    const Spread all = spread_of(c, 0, c.unwaited != 0);
     Cursor k{};
     const int total = all.total * units, run = run_of(total, ctas);
     const long long pos = static_cast<long long>(blockIdx.x) * run;
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
             for (int j = k.t; j < k.last(); ++j, ++it) {
                 const int s = it % C::kStages;
                 const int have = min(pages, (k.len - j * 128 + p.c.page - 1) / p.c.page);  // pages of the tile in use
-                const int id = mine < have ? table[j * pages + mine] : 0;
+                const int id = mine < have ? word_of(table + j * pages + mine, p.c.unwaited != 0) : 0;
                 // (K's stage is free when the scores are computed, a product before V's)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
@@ -727,14 +735,53 @@ struct Joined {
     }
 };
 
+// spread_of for a warp of a block whose first row is of sequence b0, the lengths
+// read by all warps together: in larger batches than kJoinAlone each warp's own
+// pass over them would take longer than its rows (2048 sequences of 256 slots 355 us,
+// by each warp 405; 128 27.3, 26.6).
+constexpr int kJoinAlone = 256;
+__device__ __forceinline__ Spread spread_by_block(const PagedCache& c, int b0, int b) {
+    __shared__ int parts[2][kJoinThreads / 32];
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    int before = 0, total = 0;
+    for (int s = static_cast<int>(threadIdx.x); s < c.B; s += kJoinThreads) {
+        const int n = tiles_of(length_of(c, s, true));
+        total += n;
+        if (s < b0) before += n;
+    }
+    total = static_cast<int>(__reduce_add_sync(0xffffffffu, total));
+    before = static_cast<int>(__reduce_add_sync(0xffffffffu, before));
+    if (lane == 0) {
+        parts[0][threadIdx.x / 32] = before;
+        parts[1][threadIdx.x / 32] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) {
+        before += parts[0][i];
+        total += parts[1][i];
+    }
+    // (a block has 8 rows, so at most 7 sequences begin behind its first one's)
+    const int s = b0 + lane;
+    before += static_cast<int>(__reduce_add_sync(0xffffffffu, s < b ? tiles_of(length_of(c, s, true)) : 0));
+    return {before, total, length_of(c, b, true)};
+}
+
 // The second kernel: rows whose keys several CTAs shared, or that have a
 // prefix, a warp each.  The lengths are read ahead of the wait: the kernel
 // before let this one be set up behind its own wait for whatever wrote them.
-template <int D, bool F16>
+// kMany: more than kJoinAlone sequences.
+template <int D, bool F16, bool kMany>
 __global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const PagedFwdParams p, int rows_per_block) {
     const int lane = static_cast<int>(threadIdx.x) % 32;
     const long long row = static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
     const long long total_rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
+    [[maybe_unused]] const long long per_sequence = static_cast<long long>(p.c.H_kv) * p.rows;
+    Spread sp;
+    if constexpr (kMany)
+        sp = spread_by_block(p.c, static_cast<int>(static_cast<long long>(blockIdx.x) * (kJoinThreads / 32) / per_sequence),
+                             static_cast<int>(min(row, total_rows - 1) / per_sequence));
     if (row >= total_rows) {
         grid_wait();
         return;
@@ -745,7 +792,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const Paged
     const int b = static_cast<int>(head / p.c.H_kv);
     const int u = static_cast<int>(head % p.c.H_kv) * p.row_blocks + r / rows_per_block;
     const int n = r % rows_per_block;
-    const Spread sp = spread_of(p.c, b);
+    if constexpr (!kMany) sp = spread_of(p.c, b, true);
     const int tiles = tiles_of(sp.len);
     const int run = run_of(sp.total * units, p.ctas);
     const int begin = sp.before * units + u * tiles;  // the unit's first tile among all
@@ -785,8 +832,9 @@ cudaError_t launch_variant(const CUtensorMap& q, const CUtensorMap& k, const CUt
     e = launch_dependent(kern, dim3(static_cast<unsigned>(p.ctas)), C::kThreads, C::kSmemBytes, stream, q, k, v, p);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(p.c.B) * p.c.H_kv * p.rows;
-    return launch_dependent(fa_paged_join_kernel<D, F16>, dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
-                            kJoinThreads, 0, stream, p, NV);
+    auto join = p.c.B > kJoinAlone ? fa_paged_join_kernel<D, F16, true> : fa_paged_join_kernel<D, F16, false>;
+    return launch_dependent(join, dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))), kJoinThreads, 0,
+                            stream, p, NV);
 }
 
 template <int D, bool F16, bool kCausal>

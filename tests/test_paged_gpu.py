@@ -285,6 +285,17 @@ def test_many_sequences(B):
     check(g, c, lengths, 8, 1)
 
 
+@pytest.mark.parametrize("H,H_kv,N_q,prefix", [(1, 1, 1, 0), (8, 2, 1, 0), (6, 2, 3, 0), (2, 1, 1, 100)])
+@pytest.mark.parametrize("B", [256, 257, 600])
+def test_more_sequences_than_a_warp_reads_alone(B, H, H_kv, N_q, prefix):
+    """Blocks of the second kernel whose rows are of one sequence, of several, of eight; long sequences among short and
+    empty ones."""
+    g = rng(23)
+    lengths = [(37 * b * b) % 200 if b % 3 else 3000 * (b % 60 == 0) for b in range(B)]
+    c, pages = cache_of(g, lengths, H_kv, 64, 64, prefix=prefix)
+    check(g, c, lengths, H, N_q, causal=N_q > 1, prefix_pages=pages, prefix=prefix)
+
+
 @pytest.mark.parametrize("prefix", [1, 100, 128, 1000, 5000])
 @pytest.mark.parametrize("B,H,H_kv,N_q", [(1, 1, 1, 1), (3, 8, 2, 1), (40, 8, 2, 1), (9, 16, 1, 1), (5, 8, 1, 16), (70, 4, 2, 2)])
 @pytest.mark.parametrize("d,dtype,page", [(64, "f16", 16), (128, "bf16", 64)])
