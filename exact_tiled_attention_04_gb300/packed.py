@@ -13,6 +13,30 @@ from . import kv4 as _k
 _rows_t = _b.fa_rows_t
 
 
+def _call_with_workspace(where: str, function, device, stream, size: int, *args):
+    """`kv4._call` with a workspace of `size` bytes that belongs to the call: from
+    the stream's memory, and free for what is queued behind it (without a tensor
+    around it, which takes longer to make than the kernels' launches)."""
+    torch_c = _k.torch._C
+    if torch_c._cuda_getDevice() != device.index:
+        with _k.torch.cuda.device(device):
+            return _call_with_workspace(where, function, device, stream, size, *args)
+    current = torch_c._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    memory = torch_c._cuda_cudaCachingAllocator_raw_alloc(max(size, 16), current)
+    try:
+        status = function(*args, memory, size, current or None)
+    finally:
+        torch_c._cuda_cudaCachingAllocator_raw_delete(memory)
+    if status != _b.FA_OK:
+        raise _b.FAError(status, where)
+
+
+def _new(rows: int, heads: int, d: int, dtype, device, stream):
+    """An output [rows, heads, d] and its C view."""
+    t = _k._empty((rows, heads, d), dtype, device, stream)
+    return t, _rows_t(t.data_ptr() or None, heads * d, d)
+
+
 def _view(t, what: str, shape, dtype, device):
     """The C view of a [rows, heads, d] tensor whose rows may lie apart."""
     if t.dtype is not dtype:
@@ -80,12 +104,14 @@ def packed_attention(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
     _, T_q, _, H, _, d = sizes
     torch = _k.torch
     if out is None:
-        out = _k._empty((T_q, H, d), q.dtype, device, stream)
+        out, view = _new(T_q, H, d, q.dtype, device, stream)
+    else:
+        view = _view(out, "out", q.shape, q.dtype, device)
     if lse is not None:
         _k._check(lse, "lse", torch.float32, (H, T_q), device)
     elif with_lse:
         lse = _k._empty((H, T_q), torch.float32, device, stream)
-    _k._call("fa_packed_fwd", _b.load().fa_packed_fwd, device, stream, *views, _view(out, "out", q.shape, q.dtype, device),
+    _k._call("fa_packed_fwd", _b.load().fa_packed_fwd, device, stream, *views, view,
              lse.data_ptr() or None if lse is not None else None, cu_q.data_ptr(), cu_k.data_ptr(), *sizes,
              _k._scale(scale, d), code | _b.FA_FLAG_CAUSAL if causal else code)
     return out, lse
@@ -100,21 +126,23 @@ def packed_attention_backward(q, k, v, o, lse, dout, cu_q, cu_k=None, scale: flo
     if cu_k is None:
         cu_k = cu_q
     device, code, sizes, (vq, vk, vv) = _inputs(q, k, v, cu_q, cu_k)
-    B, T_q, _, H, _, d = sizes
+    B, T_q, T_k, H, H_kv, d = sizes
     dtype, torch = q.dtype, _k.torch
     _k._check(lse, "lse", torch.float32, (H, T_q), device)
-    dq, dk, dv = (_k._empty(x.shape, dtype, device, stream) if dx is None else dx
-                  for x, dx in ((q, dq), (k, dk), (v, dv)))
+    outputs = []
+    for x, what, rows, heads in ((dq, "dq", T_q, H), (dk, "dk", T_k, H_kv), (dv, "dv", T_k, H_kv)):
+        outputs.append(_new(rows, heads, d, dtype, device, stream) if x is None
+                       else (x, _view(x, what, (rows, heads, d), dtype, device)))
+    (dq, vdq), (dk, vdk), (dv, vdv) = outputs
+    args = (vq, vk, vv, _view(o, "o", q.shape, dtype, device), _view(dout, "dout", q.shape, dtype, device),
+            lse.data_ptr() or None, vdq, vdk, vdv, cu_q.data_ptr(), cu_k.data_ptr(), *sizes, _k._scale(scale, d),
+            code | _b.FA_FLAG_CAUSAL if causal else code)
+    function = _b.load().fa_packed_bwd
     if workspace is None:
-        size = _b.fa_packed_bwd_workspace_size(B, T_q, H, d)
-        workspace = _k._empty(max(size, 16), torch.uint8, device, stream, returned=False)
+        _call_with_workspace("fa_packed_bwd", function, device, stream, _b.fa_packed_bwd_workspace_size(B, T_q, H, d), *args)
     else:
-        size = workspace.numel() * workspace.element_size()
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    _k._call("fa_packed_bwd", _b.load().fa_packed_bwd, device, stream, vq, vk, vv,
-             _view(o, "o", q.shape, dtype, device), _view(dout, "dout", q.shape, dtype, device), lse.data_ptr() or None,
-             _view(dq, "dq", q.shape, dtype, device), _view(dk, "dk", k.shape, dtype, device),
-             _view(dv, "dv", k.shape, dtype, device), cu_q.data_ptr(), cu_k.data_ptr(), *sizes, _k._scale(scale, d),
-             code | _b.FA_FLAG_CAUSAL if causal else code, workspace.data_ptr(), size)
+        _k._call("fa_packed_bwd", function, device, stream, *args, workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size())
     return dq, dk, dv

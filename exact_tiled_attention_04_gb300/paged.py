@@ -11,7 +11,7 @@ import ctypes
 
 from . import binding as _b
 from . import kv4 as _k
-from .packed import _offsets, _view
+from .packed import _call_with_workspace, _new, _offsets, _view
 
 
 def rotary_table(rows: int, rot: int, base: float = 10000.0, device="cuda"):
@@ -113,8 +113,9 @@ def paged_append(cache: PagedKVCache, k, v, cu=None, q=None, table=None, positio
         shape = (T, H, cache.d)
         vq = _view(q, "q", shape, dtype, device)
         if q_out is None:
-            q_out = _k._empty(shape, dtype, device, stream)
-        vq_out = _view(q_out, "q_out", shape, dtype, device)
+            q_out, vq_out = _new(T, H, cache.d, dtype, device, stream)
+        else:
+            vq_out = _view(q_out, "q_out", shape, dtype, device)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     vk_out = _view(k_out, "k_out", kv, dtype, device) if k_out is not None else None
@@ -167,15 +168,15 @@ def paged_attention(q, cache: PagedKVCache, scale: float | None = None, causal: 
         _k._check(lse, "lse", torch.float32, (B, H, N_q), device)
     elif with_lse:
         lse = _k._empty((B, H, N_q), torch.float32, device, stream)
+    args = (cache._ref, q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None, H, N_q,
+            prefix_pages.data_ptr() if prefix_pages is not None else None, prefix_length, _k._scale(scale, d),
+            cache._code | _b.FA_FLAG_CAUSAL if causal else cache._code)
+    function = _b.load().fa_paged_fwd
     if workspace is None:
-        size = max(cache.workspace_size(H, N_q, prefix_length), 16)
-        workspace = _k._empty(size, torch.uint8, device, stream, returned=False)
+        _call_with_workspace("fa_paged_fwd", function, device, stream, cache.workspace_size(H, N_q, prefix_length), *args)
     else:
-        size = workspace.numel() * workspace.element_size()
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    _k._call("fa_paged_fwd", _b.load().fa_paged_fwd, device, stream, cache._ref, q.data_ptr(), out.data_ptr(),
-             lse.data_ptr() if lse is not None else None, H, N_q,
-             prefix_pages.data_ptr() if prefix_pages is not None else None, prefix_length, _k._scale(scale, d),
-             cache._code | _b.FA_FLAG_CAUSAL if causal else cache._code, workspace.data_ptr(), size)
+        _k._call("fa_paged_fwd", function, device, stream, *args, workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size())
     return out, lse
