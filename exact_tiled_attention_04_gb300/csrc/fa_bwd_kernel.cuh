@@ -159,7 +159,7 @@ struct BwdCfg {
     static constexpr int kBarStagedDO = kBarStaged + kStages;  // [kStages] read-out layout: [d/2, d), in the dO tile (4)
     static constexpr int kNumBars = kBarStagedDO + kStages;
     // barriers, TMEM slot and abort flag
-    static constexpr int kCtrlBytes = kNumBars * 8 + 8 + 32;  // (32: the SeqBlock of a packed launch)
+    static constexpr int kCtrlBytes = kNumBars * 8 + 8 + 56;  // (56: a packed launch's block, and barriers of its own)
     // The control block lives in whichever alignment gap holds it: below the
     // 1024-aligned base when the slack there is large enough, else after the
     // tiles, so the launch needs only the tiles plus 1 KB.
@@ -261,11 +261,17 @@ __device__ __forceinline__ void bwd_tmem_ld_wait16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// Orders what another kernel wrote to a tensor map in global memory ahead of
-// this thread's tensor copies by it.
-__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
-    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map))
-                 : "memory");
+// Rows first .. 127 of a tile of D / 64 atoms zeroed, by one warp, ahead of the
+// tensor core's reads.
+template <int kAtoms>
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int first) {
+#pragma unroll 1
+    for (int a = 0; a < kAtoms; ++a) {
+        uint4* rows = reinterpret_cast<uint4*>(tile + a * 128 * 128);
+        for (int i = first * 8 + static_cast<int>(threadIdx.x) % 32; i < 128 * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 // kPacked: the key block is one of packed sequences (PackedBwdParams), found from
@@ -310,7 +316,6 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
     int n_q_tiles = p.n_q_tiles, n_kv = p.Nkv, causal_offset = p.causal_offset;
     // first tile of a query head's statistics and first row of its accumulator
     [[maybe_unused]] int pad_tile = 0;
-    const CUtensorMap *pm_q = &map_q, *pm_k = &map_k, *pm_v = &map_v, *pm_do = &map_do;
     // Query tiles that see a key of this block: all, or under the causal mask
     // those holding a row i >= kb*128 - causal_offset (query i sees key j iff
     // j <= i + causal_offset).  The last query row sees every key, so at
@@ -353,17 +358,17 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         mbar_init(bar(C::kBarDrain), 1);
         mbar_init(bar(C::kBarEpi + 0), 128);
         mbar_init(bar(C::kBarEpi + 1), 128);
+        if constexpr (kPacked)
+            for (int i = 0; i < 3; ++i) mbar_init(ctrl_u32 + C::kNumBars * 8 + 40 + 8 * i, 1);
         // A CTA starting after another CTA of this launch timed out does no work.
         *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
         mbar_init_fence();
     }
     if (warp == kBwdLoadWarp && lane == 0) {
-        if constexpr (!kPacked) {
-            tma_prefetch_desc(&map_q);
-            tma_prefetch_desc(&map_k);
-            tma_prefetch_desc(&map_v);
-            tma_prefetch_desc(&map_do);
-        }
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+        tma_prefetch_desc(&map_do);
         tma_prefetch_desc(&map_dq);
     }
     if (warp == kBwdMmaWarp) {
@@ -380,12 +385,13 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
             int head;
             const SeqBlock blk = find_block<true>(p.seqs, 128, p.H_kv, blockIdx.x, head);
             if (lane == 0) {
-                block_info[0] = blk.s;
-                block_info[1] = blk.r;
+                block_info[0] = blk.r;
+                block_info[1] = blk.q0;
                 block_info[2] = blk.nq;
-                block_info[3] = blk.nk;
-                block_info[4] = blk.base;
-                block_info[5] = head;
+                block_info[3] = blk.k0;
+                block_info[4] = blk.nk;
+                block_info[5] = blk.base;
+                block_info[6] = head;
             }
         }
     }
@@ -395,19 +401,14 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
     const uint32_t tmem = *tmem_slot;
     bool skip = *abort_flag != 0u;
     if constexpr (kPacked) {
-        kb = block_info[1];
+        kb = block_info[0];
         skip = skip || kb < 0;  // the grid is as large as any lengths need
         n_q_tiles = (block_info[2] + 127) / 128;
-        n_kv = block_info[3];
+        n_kv = block_info[4];
         causal_offset = n_kv - block_info[2];
-        pad_tile = block_info[4] / 128;
+        pad_tile = block_info[5] / 128;
         b = 0;
-        unit = kvh = block_info[5];
-        const CUtensorMap* maps = p.maps + (kb < 0 ? 0 : block_info[0]) * kPackedMaps;
-        pm_q = maps + kMapQ;
-        pm_k = maps + kMapK;
-        pm_v = maps + kMapV;
-        pm_do = maps + kMapDout;
+        unit = kvh = block_info[6];
         plan();
     }
     const bool has_work = T > 0;
@@ -466,22 +467,103 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         regs_decrease<C::kOtherRegs>();
       if (!has_work) {
         // no query row sees this key block: the epilogue stores zeros
+      } else if (kPacked && warp == kBwdLoadWarp) {
+        // -------------------------------------- TMA producer, packed sequences
+        // The rows behind a sequence's end in its last tile are the next one's.
+        // Their weight is 0, but 0 x infinity is not, so such a tile lands on a
+        // barrier of its own, and this warp zeroes those rows and hands it on.
+        if constexpr (kPacked) {
+            const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+            const uint32_t raw_kv = ctrl_u32 + C::kNumBars * 8 + 40, raw_q = raw_kv + 8, raw_do = raw_kv + 16;
+            const int q0 = block_info[1], k0 = block_info[3];
+            const int keys = n_kv - kb * 128, last_rows = block_info[2] - (n_q_tiles - 1) * 128;
+            const uint32_t to_kv = keys < 128 ? raw_kv : bar(C::kBarKV);
+            // (a raw load is waited for whether the CTA gives up or not: it lands before the CTA exits)
+            auto landed = [&](uint32_t raw, uint32_t phase) { bwd_wait(raw, phase, abort_flag, p, 33, false); __syncwarp(); };
+            // (one lane's wait for a stage: 32 that ask take 4 % at d = 64)
+            auto waited = [&](uint32_t stage_bar, uint32_t phase) -> bool {
+                const bool got = lane != 0 || bwd_wait(stage_bar, phase, abort_flag, p, 31);
+                return __all_sync(0xffffffffu, got);
+            };
+            if (lane == 0) {
+                mbar_arrive_expect_tx(to_kv, 2u * C::kTileBytes);
+                for (int a = 0; a < C::kAtoms; ++a) {
+                    tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, &map_k, to_kv, a * C::kAtomElems, k0 + kb * 128, unit, once);
+                    tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, &map_v, to_kv, a * C::kAtomElems, k0 + kb * 128, unit, once);
+                }
+            }
+            int issued_q = 0, issued_do = 0;
+            uint32_t tails = 0;
+            for (int it = 0; it < T; ++it) {
+                const int s = it % C::kStages;
+                const uint32_t ph = ((it / C::kStages) & 1) ^ 1;
+                const int qt = qt_begin + it % nqt;
+                const int bh = kvh * p.group + it / nqt;
+                const bool tail = qt == n_q_tiles - 1 && last_rows < 128;
+                const uint32_t to_q = tail ? raw_q : bar(C::kBarFull + s), to_do = tail ? raw_do : bar(C::kBarFullDO + s);
+                bool go = waited(bar(C::kBarEmpty + s), ph);
+                if (go) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(to_q, C::kTileBytes + kBwdStatBytes);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q, to_q,
+                                        a * C::kAtomElems, q0 + qt * 128, bh, keep);
+                        bulk_load(sbase + C::kOffStats + s * kBwdStatBytes,
+                                  p.stats + (static_cast<size_t>(bh) * (p.Nq_pad / 128) + static_cast<size_t>(pad_tile + qt)) *
+                                                kStatFloatsPerTile,
+                                  kBwdStatBytes, to_q, keep);
+                    }
+                    issued_q = it + 1;
+                    go = waited(bar(C::kBarEmptyDO + s), ph);
+                }
+                if (go) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(to_do, C::kTileBytes);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, &map_do, to_do,
+                                        a * C::kAtomElems, q0 + qt * 128, bh, keep);
+                    }
+                    issued_do = it + 1;
+                }
+                if (it == 0 && keys < 128) {  // (behind the first tile's loads)
+                    landed(raw_kv, 0);
+                    zero_tail<C::kAtoms>(smem + C::kOffK, keys);
+                    zero_tail<C::kAtoms>(smem + C::kOffV, keys);
+                    if (lane == 0) mbar_arrive(bar(C::kBarKV));
+                }
+                if (tail && issued_q == it + 1) {
+                    landed(raw_q, tails & 1);
+                    zero_tail<C::kAtoms>(smem + C::kOffQ + s * C::kTileBytes, last_rows);
+                    if (lane == 0) mbar_arrive(bar(C::kBarFull + s));
+                }
+                if (tail && issued_do == it + 1) {
+                    landed(raw_do, tails & 1);
+                    zero_tail<C::kAtoms>(smem + C::kOffDO + s * C::kTileBytes, last_rows);
+                    if (lane == 0) mbar_arrive(bar(C::kBarFullDO + s));
+                }
+                if (tail) ++tails;
+                if (!go) break;
+            }
+            // Drain: every issued load has landed before the CTA may exit.
+            if (lane == 0) {
+                bwd_wait(bar(C::kBarKV), 0, abort_flag, p, 32, false);
+                for (int s = 0; s < C::kStages; ++s) {
+                    if (s < issued_q) bwd_wait(bar(C::kBarFull + s), ((issued_q - 1 - s) / C::kStages) & 1, abort_flag, p, 32, false);
+                    if (s < issued_do)
+                        bwd_wait(bar(C::kBarFullDO + s), ((issued_do - 1 - s) / C::kStages) & 1, abort_flag, p, 32, false);
+                }
+            }
+        }
       } else if (warp == kBwdLoadWarp) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
             const uint64_t keep = policy_evict_last();   // Q, dO, stats: read by every key block of the head
             const uint64_t once = policy_evict_first();  // K, V: read once
-            if constexpr (kPacked) {
-                acquire_map(pm_k);
-                acquire_map(pm_v);
-                acquire_map(pm_q);
-                acquire_map(pm_do);
-            }
             mbar_arrive_expect_tx(bar(C::kBarKV), 2u * C::kTileBytes);
             for (int a = 0; a < C::kAtoms; ++a) {
-                tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, pm_k, bar(C::kBarKV), a * C::kAtomElems,
+                tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, &map_k, bar(C::kBarKV), a * C::kAtomElems,
                             kb * 128, unit, once);
-                tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, pm_v, bar(C::kBarKV), a * C::kAtomElems,
+                tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, &map_v, bar(C::kBarKV), a * C::kAtomElems,
                             kb * 128, unit, once);
             }
             int issued_q = 0, issued_do = 0;
@@ -494,7 +576,7 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
                 if (!bwd_wait(bar(C::kBarEmpty + s), ph, abort_flag, p, 31)) break;
                 mbar_arrive_expect_tx(bar(C::kBarFull + s), C::kTileBytes + kBwdStatBytes);
                 for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, pm_q,
+                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q,
                                 bar(C::kBarFull + s), a * C::kAtomElems, qt * 128, bh, keep);
                 bulk_load(sbase + C::kOffStats + s * kBwdStatBytes,
                           p.stats + (static_cast<size_t>(bh) * (p.Nq_pad / 128) + static_cast<size_t>(pad_tile + qt)) *
@@ -504,7 +586,7 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
                 if (!bwd_wait(bar(C::kBarEmptyDO + s), ph, abort_flag, p, 31)) break;
                 mbar_arrive_expect_tx(bar(C::kBarFullDO + s), C::kTileBytes);
                 for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, pm_do,
+                    tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, &map_do,
                                 bar(C::kBarFullDO + s), a * C::kAtomElems, qt * 128, bh, keep);
                 issued_do = it + 1;
             }
@@ -871,19 +953,37 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
             }
             fence_proxy_async_smem();
         }
+        int whole = 1;
+        if constexpr (kPacked) {  // a sequence's last keys: row by row, as the rows behind them are the next one's
+            const volatile int* info = block_info;  // (read again rather than held over the loop)
+            const int keys = info[4] - info[0] * 128;
+            if (keys < 128) {
+                whole = 0;
+                __syncwarp();
+                const long long row_stride = w == 0 ? p.dv_row : p.dk_row;
+                uint16_t* out = (w == 0 ? p.dv : p.dk) + static_cast<long long>(info[3] + info[0] * 128) * row_stride +
+                                info[6] * (w == 0 ? p.dv_head : p.dk_head);
+                if (ok && !*abort_flag) {
+#pragma unroll 1
+                    for (int r = t - lane + lane / 8; r < min(keys, t - lane + 32); r += 4)
+#pragma unroll
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            *reinterpret_cast<uint4*>(out + r * row_stride + a * C::kAtomElems + lane % 8 * 8) =
+                                *reinterpret_cast<const uint4*>(stage + a * C::kAtomBytes + r * 128 + (((lane ^ r) & 7) << 4));
+                }
+            }
+        }
         // Every thread of the warpgroup arrives exactly once, whatever happened.
         mbar_arrive(bar(C::kBarEpi + w));
-        if (t == 0) {
+        if (t == 0 && whole) {
             const bool all_in = bwd_wait(bar(C::kBarEpi + w), 0, abort_flag, p, 45);
             if (all_in && !*abort_flag) {
                 const CUtensorMap* map = (w == 0) ? &map_dv : &map_dk;
                 int row = kb * 128, head = unit;
-                if constexpr (kPacked) {  // (read again rather than held over the loop)
+                if constexpr (kPacked) {
                     const volatile int* info = block_info;
-                    map = p.maps + info[0] * kPackedMaps + (w == 0 ? kMapDv : kMapDk);
-                    row = info[1] * 128;
-                    head = info[5];
-                    acquire_map(map);
+                    row = info[3] + info[0] * 128;
+                    head = info[6];
                 }
                 for (int a = 0; a < C::kAtoms; ++a)
                     tma_store_3d(map, smem_u32(stage + a * C::kAtomBytes), a * C::kAtomElems, row, head);
@@ -904,15 +1004,14 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
 
 // Packed sequences: `grid` CTAs, enough for any lengths.  p.Nq_pad is 128 p.tiles.
 template <int D, bool F16, bool kCausal>
-cudaError_t launch_packed_bwd_variant(const CUtensorMap& dq, const PackedBwdParams& p, unsigned int grid,
-                                      cudaStream_t stream) {
+cudaError_t launch_packed_bwd_variant(const PackedMaps& m, const PackedBwdParams& p, unsigned int grid, cudaStream_t stream) {
     using C = BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>;
     auto kern = fa_bwd_kernel<D, F16, kCausal, true, PackedBwdParams>;
     static SmemAllowed allowed;
     const cudaError_t e = allow_smem_regs(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmemBytes),
                                           static_cast<int>(C::kLaunchRegs), allowed);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(grid), C::kThreads, C::kSmemBytes, stream, dq, dq, dq, dq, dq, dq, dq, p);
+    return launch_dependent(kern, dim3(grid), C::kThreads, C::kSmemBytes, stream, m.q, m.k, m.v, m.dout, m.dk, m.dv, m.dq, p);
 }
 
 template <int D, bool F16, bool kCausal>

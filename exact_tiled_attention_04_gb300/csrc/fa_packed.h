@@ -41,15 +41,11 @@ cudaError_t launch_packed_fwd_f16(int d, const CUtensorMap& q, const CUtensorMap
 // Backward: prep, main and dQ conversion as for a batch (fa_bwd_internal.h),
 // with two differences.  The statistics and the dQ accumulator have whole
 // blocks of 128 rows for every sequence (padded_row, fa_packed.cuh).  And a tile
-// of 128 rows that reaches behind its sequence must not read the next one's rows
-// (an infinity there, times a weight of 0, is a NaN) nor write them, so the prep
-// kernel writes tensor maps of each sequence's rows alone: loads are filled
-// with zeros behind its end and stores stop there.
-enum { kMapQ, kMapK, kMapV, kMapDout, kMapDk, kMapDv, kPackedMaps };
-struct PackedMaps {
-    CUtensorMap map[kPackedMaps];  // of the whole tensors
-    char* base[kPackedMaps];
-    long long row_bytes[kPackedMaps];
+// of 128 rows that reaches behind its sequence must not use the next one's rows
+// (an infinity there, times a weight of 0, is a NaN) nor write them: the main
+// kernel zeroes them in shared memory and stores such a block's rows one by one.
+struct PackedMaps {  // of the whole tensors; dq: over the accumulator
+    CUtensorMap q, k, v, dout, dk, dv, dq;
 };
 struct PackedAuxParams {
     PackedSeqs seqs;
@@ -64,19 +60,16 @@ struct PackedAuxParams {
     uint16_t* dq;
     long long dq_row, dq_head;
     float scale;
-    CUtensorMap* maps;     // [B, kPackedMaps], 128-byte aligned
 };
 struct PackedBwdParams : BwdParams {
     PackedSeqs seqs;
     int tiles;
-    const CUtensorMap* maps;
+    uint16_t *dk, *dv;
+    long long dk_row, dk_head, dv_row, dv_head;
 };
-cudaError_t launch_packed_prep(const PackedAuxParams& p, const PackedMaps& m, int d, bool f16, cudaStream_t stream);
+cudaError_t launch_packed_prep(const PackedAuxParams& p, int d, bool f16, cudaStream_t stream);
 cudaError_t launch_packed_dq(const PackedAuxParams& p, int d, bool f16, cudaStream_t stream);
-// dq: over the accumulator.
-cudaError_t launch_packed_bwd_bf16(int d, const CUtensorMap& dq, const PackedBwdParams& p, unsigned int grid,
-                                   cudaStream_t stream);
-cudaError_t launch_packed_bwd_f16(int d, const CUtensorMap& dq, const PackedBwdParams& p, unsigned int grid,
-                                  cudaStream_t stream);
+cudaError_t launch_packed_bwd_bf16(int d, const PackedMaps& m, const PackedBwdParams& p, unsigned int grid, cudaStream_t stream);
+cudaError_t launch_packed_bwd_f16(int d, const PackedMaps& m, const PackedBwdParams& p, unsigned int grid, cudaStream_t stream);
 
 }  // namespace fa

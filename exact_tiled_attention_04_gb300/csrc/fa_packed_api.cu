@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 #include "fa.h"
 #include "fa_host.h"
@@ -70,15 +71,14 @@ int check_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const 
 
 int64_t pad_tiles(const Sizes& z) { return z.Tq / 128 + z.B; }
 
-// Workspace: 128 bytes to align by, the tensor maps, the row statistics, the dQ accumulator.
+// Workspace: 128 bytes to align by, the row statistics, the dQ accumulator.
 struct Layout {
-    size_t maps, stats, acc, total;
+    size_t stats, acc, total;
 };
 Layout layout(const Sizes& z) {
     Layout l;
     const size_t tiles = static_cast<size_t>(z.H) * static_cast<size_t>(pad_tiles(z));
-    l.maps = 0;
-    l.stats = static_cast<size_t>(z.B) * fa::kPackedMaps * sizeof(CUtensorMap);
+    l.stats = 0;
     l.acc = l.stats + tiles * fa::kStatFloatsPerTile * sizeof(float);
     l.total = l.acc + tiles * 128 * static_cast<size_t>(z.d) * sizeof(float) + 128;
     return l;
@@ -244,20 +244,19 @@ int fa_packed_bwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
     a.dq_row = w.dq.row;
     a.dq_head = w.dq.head;
     a.scale = scale;
-    a.maps = reinterpret_cast<CUtensorMap*>(ws + l.maps);
-    fa::PackedMaps m{};
-    const View* views[fa::kPackedMaps] = {&w.q, &w.k, &w.v, &w.dout, &w.dk, &w.dv};
-    for (int i = 0; i < fa::kPackedMaps; ++i) {
-        if (views[i]->rows == 0) continue;  // no sequence has rows of it: its maps are not written
-        if ((st = map_of(&m.map[i], *views[i], dtype)) != FA_OK) return st;
-        m.base[i] = views[i]->data;
-        m.row_bytes[i] = views[i]->row * 2;
-    }
-    CUtensorMap mdq;
-    if ((st = encode_map(&mdq, a.dq_acc, FA_DTYPE_F32, H, int64_t{128} * a.tiles, d)) != FA_OK) return st;
-    cudaError_t e = fa::launch_packed_prep(a, m, static_cast<int>(d), f16, s);
+    cudaError_t e = cudaSuccess;
+    if (T_q > 0) e = fa::launch_packed_prep(a, static_cast<int>(d), f16, s);
     if (e != cudaSuccess) return cuda_failed("packed backward prep launch", e);
     if (T_k > 0) {
+        fa::PackedMaps m{};
+        if ((st = encode_map(&m.dq, a.dq_acc, FA_DTYPE_F32, H, int64_t{128} * a.tiles, d)) != FA_OK) return st;
+        const std::pair<CUtensorMap*, const View*> maps[6] = {{&m.k, &w.k},   {&m.v, &w.v}, {&m.dk, &w.dk},
+                                                              {&m.dv, &w.dv}, {&m.q, &w.q}, {&m.dout, &w.dout}};
+        for (const auto& x : maps) {
+            if (x.second->rows > 0) st = map_of(x.first, *x.second, dtype);
+            else *x.first = m.k;  // (no queries: not used)
+            if (st != FA_OK) return st;
+        }
         fa::PackedBwdParams p{};
         p.status = device_status_words(&st);
         if (st != FA_OK) return st;
@@ -273,10 +272,15 @@ int fa_packed_bwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
         p.scale = scale;
         p.seqs = a.seqs;
         p.tiles = a.tiles;
-        p.maps = a.maps;
+        p.dk = reinterpret_cast<uint16_t*>(w.dk.data);
+        p.dv = reinterpret_cast<uint16_t*>(w.dv.data);
+        p.dk_row = w.dk.row;
+        p.dk_head = w.dk.head;
+        p.dv_row = w.dv.row;
+        p.dv_head = w.dv.head;
         const unsigned int grid = static_cast<unsigned int>((T_k / 128 + B) * H_kv);
-        e = f16 ? fa::launch_packed_bwd_f16(static_cast<int>(d), mdq, p, grid, s)
-                : fa::launch_packed_bwd_bf16(static_cast<int>(d), mdq, p, grid, s);
+        e = f16 ? fa::launch_packed_bwd_f16(static_cast<int>(d), m, p, grid, s)
+                : fa::launch_packed_bwd_bf16(static_cast<int>(d), m, p, grid, s);
         if (e != cudaSuccess) return cuda_failed("packed backward launch", e);
     }
     if (T_q > 0) {

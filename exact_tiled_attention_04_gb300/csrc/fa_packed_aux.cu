@@ -1,8 +1,7 @@
 // Backward pass over packed sequences: the two memory-bound kernels around the
 // main one (fa_bwd_kernel.cuh).
 //   prep: per query row D = dO . O, the negated base-2 log-sum-exp and a zeroed
-//         row of the fp32 dQ accumulator; and the tensor maps of each sequence's
-//         rows;
+//         row of the fp32 dQ accumulator;
 //   dq:   dQ = scale * accumulator in the input dtype.
 // What bounds them: memory.  For 16384 rows of 32 heads, d = 128: prep 82 us for 537
 // MB (6.5 TB/s: o and dO read, the accumulator's zeros written), dq 56 us for 403
@@ -38,46 +37,10 @@ __device__ __forceinline__ bool find_tile(const PackedSeqs& p, int tile, int& q0
     return first >= 0 && rows > 0;
 }
 
-// Map of rows first .. first + rows - 1 of a tensor, by one warp: a copy of the
-// whole tensor's with another address and another number of rows.
-__device__ __forceinline__ void write_map(CUtensorMap* out, const CUtensorMap& whole, uint8_t* copy, uint64_t address,
-                                          uint32_t rows) {
-    const int lane = static_cast<int>(threadIdx.x) % 32;
-    reinterpret_cast<uint32_t*>(copy)[lane] = reinterpret_cast<const uint32_t*>(&whole)[lane];
-    __syncwarp();
-    const uint32_t at = smem_u32(copy);
-    if (lane == 0) {
-        asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(at), "l"(address)
-                     : "memory");
-        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(at), "r"(rows)
-                     : "memory");
-    }
-    __syncwarp();
-    asm volatile(
-        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
-            reinterpret_cast<uint64_t>(out)),
-        "r"(at)
-        : "memory");
-}
-
 template <int D, bool F16>
-__global__ void __launch_bounds__(kAuxThreads) fa_packed_prep_kernel(const PackedAuxParams p,
-                                                                     const __grid_constant__ PackedMaps m) {
+__global__ void __launch_bounds__(kAuxThreads) fa_packed_prep_kernel(const PackedAuxParams p) {
     grid_wait();
     grid_release();
-    if (static_cast<int>(blockIdx.x) >= p.tiles) {  // a block per sequence behind the tiles, in head 0's row of the grid
-        __shared__ __align__(128) uint8_t copy[kPackedMaps][128];
-        const int s = static_cast<int>(blockIdx.x) - p.tiles, i = static_cast<int>(threadIdx.x) / 32;
-        if (blockIdx.y != 0 || i >= kPackedMaps) return;
-        int q0, nq, k0, nk;
-        seq_rows(p.seqs, s, q0, nq, k0, nk);
-        const bool of_q = i == kMapQ || i == kMapDout;
-        const int first = of_q ? q0 : k0, rows = of_q ? nq : nk;
-        if (rows > 0)  // (no copy goes by the map of an empty sequence)
-            write_map(p.maps + static_cast<size_t>(s) * kPackedMaps + i, m.map[i], copy[i],
-                      reinterpret_cast<uint64_t>(m.base[i] + first * m.row_bytes[i]), static_cast<uint32_t>(rows));
-        return;
-    }
     constexpr int kLanes = D / 8;                  // lanes of a row
     constexpr int kStep = kAuxThreads / kLanes;    // rows at a time
     const int tile = static_cast<int>(blockIdx.x), head = static_cast<int>(blockIdx.y);
@@ -138,11 +101,11 @@ __global__ void __launch_bounds__(kAuxThreads) fa_packed_dq_kernel(const PackedA
 
 }  // namespace
 
-cudaError_t launch_packed_prep(const PackedAuxParams& p, const PackedMaps& m, int d, bool f16, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(p.tiles + p.seqs.B), static_cast<unsigned>(p.H));
+cudaError_t launch_packed_prep(const PackedAuxParams& p, int d, bool f16, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.H));
     auto kern = d == 64 ? (f16 ? fa_packed_prep_kernel<64, true> : fa_packed_prep_kernel<64, false>)
                         : (f16 ? fa_packed_prep_kernel<128, true> : fa_packed_prep_kernel<128, false>);
-    return launch_dependent(kern, grid, kAuxThreads, 0, stream, p, m);
+    return launch_dependent(kern, grid, kAuxThreads, 0, stream, p);
 }
 
 cudaError_t launch_packed_dq(const PackedAuxParams& p, int d, bool f16, cudaStream_t stream) {

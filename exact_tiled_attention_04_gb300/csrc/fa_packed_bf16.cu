@@ -14,13 +14,13 @@ cudaError_t launch_packed_fwd_bf16(int d, const CUtensorMap& q, const CUtensorMa
                          : packed::launch_variant<128, false, false>(q, k, v, p, grid, stream);
 }
 
-cudaError_t launch_packed_bwd_bf16(int d, const CUtensorMap& dq, const PackedBwdParams& p, unsigned int grid,
+cudaError_t launch_packed_bwd_bf16(int d, const PackedMaps& m, const PackedBwdParams& p, unsigned int grid,
                                  cudaStream_t stream) {
     if (d == 64)
-        return p.seqs.causal ? launch_packed_bwd_variant<64, false, true>(dq, p, grid, stream)
-                             : launch_packed_bwd_variant<64, false, false>(dq, p, grid, stream);
-    return p.seqs.causal ? launch_packed_bwd_variant<128, false, true>(dq, p, grid, stream)
-                         : launch_packed_bwd_variant<128, false, false>(dq, p, grid, stream);
+        return p.seqs.causal ? launch_packed_bwd_variant<64, false, true>(m, p, grid, stream)
+                             : launch_packed_bwd_variant<64, false, false>(m, p, grid, stream);
+    return p.seqs.causal ? launch_packed_bwd_variant<128, false, true>(m, p, grid, stream)
+                         : launch_packed_bwd_variant<128, false, false>(m, p, grid, stream);
 }
 
 }  // namespace fa
