@@ -82,6 +82,7 @@ namespace fa {
 constexpr int kBwdMmaWarp = 8;
 constexpr int kBwdLoadWarp = 9;
 constexpr int kBwdReduceWarp = 10;
+constexpr int kBwdTailWarp = 11;   // packed sequences
 constexpr int kBwdReadWarp0 = 12;  // read-out layout: first warp of the dQ read-out warpgroup
 constexpr uint32_t kBwdTmemCols = 512;
 constexpr uint64_t kBwdWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
@@ -159,7 +160,10 @@ struct BwdCfg {
     static constexpr int kBarStagedDO = kBarStaged + kStages;  // [kStages] read-out layout: [d/2, d), in the dO tile (4)
     static constexpr int kNumBars = kBarStagedDO + kStages;
     // barriers, TMEM slot and abort flag
-    static constexpr int kCtrlBytes = kNumBars * 8 + 8 + 56;  // (56: a packed launch's block, and barriers of its own)
+    // a packed launch: 32 bytes of its block, and barriers of the loads that reach
+    // behind a sequence (keys and values, [kStages] of Q, [kStages] of dO)
+    static constexpr int kOffRaw = kNumBars * 8 + 8 + 32;
+    static constexpr int kCtrlBytes = kOffRaw + (1 + 2 * kStages) * 8;
     // The control block lives in whichever alignment gap holds it: below the
     // 1024-aligned base when the slack there is large enough, else after the
     // tiles, so the launch needs only the tiles plus 1 KB.
@@ -274,6 +278,19 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int first) {
     __syncwarp();
 }
 
+// The staged rows below `rows` of this warp's 32 (of 128) to global memory, whole
+// lines at a time.  Not inlined: once per block, and the loop's registers stay as they are.
+template <int kAtoms>
+__device__ __noinline__ void store_tail(uint16_t* out, long long row_stride, int rows, const uint8_t* stage) {
+    const int lane = static_cast<int>(threadIdx.x) % 32, first = static_cast<int>(threadIdx.x) % 128 - lane;
+#pragma unroll 1
+    for (int r = first + lane / 8; r < min(rows, first + 32); r += 4)
+#pragma unroll
+        for (int a = 0; a < kAtoms; ++a)
+            *reinterpret_cast<uint4*>(out + r * row_stride + a * 64 + lane % 8 * 8) =
+                *reinterpret_cast<const uint4*>(stage + a * 128 * 128 + r * 128 + (((lane ^ r) & 7) << 4));
+}
+
 // kPacked: the key block is one of packed sequences (PackedBwdParams), found from
 // the offsets; its products are the batch's, and so are its times but for d = 128
 // without the mask (1 x 8192, H = 32/8: 2650 us against 2550).  Eight documents of
@@ -359,7 +376,7 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         mbar_init(bar(C::kBarEpi + 0), 128);
         mbar_init(bar(C::kBarEpi + 1), 128);
         if constexpr (kPacked)
-            for (int i = 0; i < 3; ++i) mbar_init(ctrl_u32 + C::kNumBars * 8 + 40 + 8 * i, 1);
+            for (int i = 0; i < 1 + 2 * C::kStages; ++i) mbar_init(ctrl_u32 + C::kOffRaw + 8 * i, 1);
         // A CTA starting after another CTA of this launch timed out does no work.
         *abort_flag = (*reinterpret_cast<volatile unsigned int*>(&p.status->abort_gen) == p.gen) ? 1u : 0u;
         mbar_init_fence();
@@ -412,6 +429,10 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         plan();
     }
     const bool has_work = T > 0;
+    // Packed: the rows behind a sequence's end in its last tiles are the next one's.
+    // Their weight is 0, but 0 x infinity is not, so such a tile lands on a barrier of its
+    // own, and warp 11 zeroes those rows and hands it on.
+    [[maybe_unused]] auto raw_bar = [&](int i) -> uint32_t { return ctrl_u32 + C::kOffRaw + 8u * static_cast<uint32_t>(i); };
 
     if (skip) {
         // nothing issued: go straight to the teardown
@@ -467,106 +488,30 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
         regs_decrease<C::kOtherRegs>();
       if (!has_work) {
         // no query row sees this key block: the epilogue stores zeros
-      } else if (kPacked && warp == kBwdLoadWarp) {
-        // -------------------------------------- TMA producer, packed sequences
-        // The rows behind a sequence's end in its last tile are the next one's.
-        // Their weight is 0, but 0 x infinity is not, so such a tile lands on a
-        // barrier of its own, and this warp zeroes those rows and hands it on.
-        if constexpr (kPacked) {
-            const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-            const uint32_t raw_kv = ctrl_u32 + C::kNumBars * 8 + 40, raw_q = raw_kv + 8, raw_do = raw_kv + 16;
-            const int q0 = block_info[1], k0 = block_info[3];
-            const int keys = n_kv - kb * 128, last_rows = block_info[2] - (n_q_tiles - 1) * 128;
-            const uint32_t to_kv = keys < 128 ? raw_kv : bar(C::kBarKV);
-            // (a raw load is waited for whether the CTA gives up or not: it lands before the CTA exits)
-            auto landed = [&](uint32_t raw, uint32_t phase) { bwd_wait(raw, phase, abort_flag, p, 33, false); __syncwarp(); };
-            // (one lane's wait for a stage: 32 that ask take 4 % at d = 64)
-            auto waited = [&](uint32_t stage_bar, uint32_t phase) -> bool {
-                const bool got = lane != 0 || bwd_wait(stage_bar, phase, abort_flag, p, 31);
-                return __all_sync(0xffffffffu, got);
-            };
-            if (lane == 0) {
-                mbar_arrive_expect_tx(to_kv, 2u * C::kTileBytes);
-                for (int a = 0; a < C::kAtoms; ++a) {
-                    tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, &map_k, to_kv, a * C::kAtomElems, k0 + kb * 128, unit, once);
-                    tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, &map_v, to_kv, a * C::kAtomElems, k0 + kb * 128, unit, once);
-                }
-            }
-            int issued_q = 0, issued_do = 0;
-            uint32_t tails = 0;
-            for (int it = 0; it < T; ++it) {
-                const int s = it % C::kStages;
-                const uint32_t ph = ((it / C::kStages) & 1) ^ 1;
-                const int qt = qt_begin + it % nqt;
-                const int bh = kvh * p.group + it / nqt;
-                const bool tail = qt == n_q_tiles - 1 && last_rows < 128;
-                const uint32_t to_q = tail ? raw_q : bar(C::kBarFull + s), to_do = tail ? raw_do : bar(C::kBarFullDO + s);
-                bool go = waited(bar(C::kBarEmpty + s), ph);
-                if (go) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(to_q, C::kTileBytes + kBwdStatBytes);
-                        for (int a = 0; a < C::kAtoms; ++a)
-                            tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q, to_q,
-                                        a * C::kAtomElems, q0 + qt * 128, bh, keep);
-                        bulk_load(sbase + C::kOffStats + s * kBwdStatBytes,
-                                  p.stats + (static_cast<size_t>(bh) * (p.Nq_pad / 128) + static_cast<size_t>(pad_tile + qt)) *
-                                                kStatFloatsPerTile,
-                                  kBwdStatBytes, to_q, keep);
-                    }
-                    issued_q = it + 1;
-                    go = waited(bar(C::kBarEmptyDO + s), ph);
-                }
-                if (go) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(to_do, C::kTileBytes);
-                        for (int a = 0; a < C::kAtoms; ++a)
-                            tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, &map_do, to_do,
-                                        a * C::kAtomElems, q0 + qt * 128, bh, keep);
-                    }
-                    issued_do = it + 1;
-                }
-                if (it == 0 && keys < 128) {  // (behind the first tile's loads)
-                    landed(raw_kv, 0);
-                    zero_tail<C::kAtoms>(smem + C::kOffK, keys);
-                    zero_tail<C::kAtoms>(smem + C::kOffV, keys);
-                    if (lane == 0) mbar_arrive(bar(C::kBarKV));
-                }
-                if (tail && issued_q == it + 1) {
-                    landed(raw_q, tails & 1);
-                    zero_tail<C::kAtoms>(smem + C::kOffQ + s * C::kTileBytes, last_rows);
-                    if (lane == 0) mbar_arrive(bar(C::kBarFull + s));
-                }
-                if (tail && issued_do == it + 1) {
-                    landed(raw_do, tails & 1);
-                    zero_tail<C::kAtoms>(smem + C::kOffDO + s * C::kTileBytes, last_rows);
-                    if (lane == 0) mbar_arrive(bar(C::kBarFullDO + s));
-                }
-                if (tail) ++tails;
-                if (!go) break;
-            }
-            // Drain: every issued load has landed before the CTA may exit.
-            if (lane == 0) {
-                bwd_wait(bar(C::kBarKV), 0, abort_flag, p, 32, false);
-                for (int s = 0; s < C::kStages; ++s) {
-                    if (s < issued_q) bwd_wait(bar(C::kBarFull + s), ((issued_q - 1 - s) / C::kStages) & 1, abort_flag, p, 32, false);
-                    if (s < issued_do)
-                        bwd_wait(bar(C::kBarFullDO + s), ((issued_do - 1 - s) / C::kStages) & 1, abort_flag, p, 32, false);
-                }
-            }
-        }
       } else if (warp == kBwdLoadWarp) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
             const uint64_t keep = policy_evict_last();   // Q, dO, stats: read by every key block of the head
             const uint64_t once = policy_evict_first();  // K, V: read once
-            mbar_arrive_expect_tx(bar(C::kBarKV), 2u * C::kTileBytes);
+            // packed: first rows; rows of the key block and of the last query tile
+            [[maybe_unused]] int q0 = 0, k0 = 0, keys = 128, last_rows = 128;
+            if constexpr (kPacked) {
+                q0 = block_info[1];
+                k0 = block_info[3];
+                keys = n_kv - kb * 128;
+                last_rows = block_info[2] - (n_q_tiles - 1) * 128;
+            }
+            // (packed) tile `it` reaches behind the sequence
+            [[maybe_unused]] auto tail = [&](int it) { return last_rows < 128 && it % nqt == nqt - 1; };
+            uint32_t to = bar(C::kBarKV);
+            if (kPacked && keys < 128) to = raw_bar(0);
+            mbar_arrive_expect_tx(to, 2u * C::kTileBytes);
             for (int a = 0; a < C::kAtoms; ++a) {
-                tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, &map_k, bar(C::kBarKV), a * C::kAtomElems,
-                            kb * 128, unit, once);
-                tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, &map_v, bar(C::kBarKV), a * C::kAtomElems,
-                            kb * 128, unit, once);
+                tma_load_3d(sbase + C::kOffK + a * C::kAtomBytes, &map_k, to, a * C::kAtomElems, k0 + kb * 128, unit, once);
+                tma_load_3d(sbase + C::kOffV + a * C::kAtomBytes, &map_v, to, a * C::kAtomElems, k0 + kb * 128, unit, once);
             }
             int issued_q = 0, issued_do = 0;
+            [[maybe_unused]] uint32_t raws_q = 0, raws_do = 0;  // (packed) bit s: an odd number of such loads into stage s
             for (int it = 0; it < T; ++it) {
                 const int s = it % C::kStages;
                 const uint32_t ph = ((it / C::kStages) & 1) ^ 1;
@@ -574,33 +519,78 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
                 const int qt = qt_begin + it % nqt;
                 const int bh = b * p.H + kvh * p.group + g;
                 if (!bwd_wait(bar(C::kBarEmpty + s), ph, abort_flag, p, 31)) break;
-                mbar_arrive_expect_tx(bar(C::kBarFull + s), C::kTileBytes + kBwdStatBytes);
+                to = bar(C::kBarFull + s);
+                if (kPacked && tail(it)) {
+                    to = raw_bar(1 + s);
+                    raws_q ^= 1u << s;
+                }
+                mbar_arrive_expect_tx(to, C::kTileBytes + kBwdStatBytes);
                 for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q,
-                                bar(C::kBarFull + s), a * C::kAtomElems, qt * 128, bh, keep);
+                    tma_load_3d(sbase + C::kOffQ + s * C::kTileBytes + a * C::kAtomBytes, &map_q, to, a * C::kAtomElems,
+                                q0 + qt * 128, bh, keep);
                 bulk_load(sbase + C::kOffStats + s * kBwdStatBytes,
                           p.stats + (static_cast<size_t>(bh) * (p.Nq_pad / 128) + static_cast<size_t>(pad_tile + qt)) *
                                         kStatFloatsPerTile,
-                          kBwdStatBytes, bar(C::kBarFull + s), keep);
+                          kBwdStatBytes, to, keep);
                 issued_q = it + 1;
                 if (!bwd_wait(bar(C::kBarEmptyDO + s), ph, abort_flag, p, 31)) break;
-                mbar_arrive_expect_tx(bar(C::kBarFullDO + s), C::kTileBytes);
+                to = bar(C::kBarFullDO + s);
+                if (kPacked && tail(it)) {
+                    to = raw_bar(1 + C::kStages + s);
+                    raws_do ^= 1u << s;
+                }
+                mbar_arrive_expect_tx(to, C::kTileBytes);
                 for (int a = 0; a < C::kAtoms; ++a)
-                    tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, &map_do,
-                                bar(C::kBarFullDO + s), a * C::kAtomElems, qt * 128, bh, keep);
+                    tma_load_3d(sbase + C::kOffDO + s * C::kTileBytes + a * C::kAtomBytes, &map_do, to, a * C::kAtomElems,
+                                q0 + qt * 128, bh, keep);
                 issued_do = it + 1;
             }
             // Drain: every issued load has landed before the CTA may exit.
-            bwd_wait(bar(C::kBarKV), 0, abort_flag, p, 32, false);
+            bwd_wait(kPacked && keys < 128 ? raw_bar(0) : bar(C::kBarKV), 0, abort_flag, p, 32, false);
             for (int s = 0; s < C::kStages; ++s) {
                 if (s < issued_q) {
                     const int last = s + ((issued_q - 1 - s) / C::kStages) * C::kStages;
-                    bwd_wait(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, p, 32, false);
+                    if (kPacked && tail(last)) bwd_wait(raw_bar(1 + s), ((raws_q >> s) & 1) ^ 1, abort_flag, p, 32, false);
+                    else bwd_wait(bar(C::kBarFull + s), (last / C::kStages) & 1, abort_flag, p, 32, false);
                 }
                 if (s < issued_do) {
                     const int last = s + ((issued_do - 1 - s) / C::kStages) * C::kStages;
-                    bwd_wait(bar(C::kBarFullDO + s), (last / C::kStages) & 1, abort_flag, p, 32, false);
+                    if (kPacked && tail(last))
+                        bwd_wait(raw_bar(1 + C::kStages + s), ((raws_do >> s) & 1) ^ 1, abort_flag, p, 32, false);
+                    else
+                        bwd_wait(bar(C::kBarFullDO + s), (last / C::kStages) & 1, abort_flag, p, 32, false);
                 }
+            }
+        }
+      } else if (kPacked && warp == kBwdTailWarp) {
+        // ------------------------------------------- rows behind the sequence
+        if constexpr (kPacked) {
+            auto landed = [&](uint32_t raw, uint32_t phase) -> bool {  // (one lane asks)
+                const bool got = lane != 0 || bwd_wait(raw, phase, abort_flag, p, 33);
+                return __all_sync(0xffffffffu, got);
+            };
+            const int keys = n_kv - kb * 128, last_rows = block_info[2] - (n_q_tiles - 1) * 128;
+            bool ok = true;
+            if (keys < 128) {
+                ok = landed(raw_bar(0), 0);
+                if (ok) {
+                    zero_tail<C::kAtoms>(smem + C::kOffK, keys);
+                    zero_tail<C::kAtoms>(smem + C::kOffV, keys);
+                    if (lane == 0) mbar_arrive(bar(C::kBarKV));
+                }
+            }
+            uint32_t phases = 0;  // bit s: of stage s
+            for (int it = nqt - 1; ok && last_rows < 128 && it < T; it += nqt) {
+                const int s = it % C::kStages;
+                ok = landed(raw_bar(1 + s), (phases >> s) & 1);
+                if (!ok) break;
+                zero_tail<C::kAtoms>(smem + C::kOffQ + s * C::kTileBytes, last_rows);
+                if (lane == 0) mbar_arrive(bar(C::kBarFull + s));
+                ok = landed(raw_bar(1 + C::kStages + s), (phases >> s) & 1);
+                if (!ok) break;
+                zero_tail<C::kAtoms>(smem + C::kOffDO + s * C::kTileBytes, last_rows);
+                if (lane == 0) mbar_arrive(bar(C::kBarFullDO + s));
+                phases ^= 1u << s;
             }
         }
       } else if (warp == kBwdReduceWarp) {
@@ -961,16 +951,10 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
                 whole = 0;
                 __syncwarp();
                 const long long row_stride = w == 0 ? p.dv_row : p.dk_row;
-                uint16_t* out = (w == 0 ? p.dv : p.dk) + static_cast<long long>(info[3] + info[0] * 128) * row_stride +
-                                info[6] * (w == 0 ? p.dv_head : p.dk_head);
-                if (ok && !*abort_flag) {
-#pragma unroll 1
-                    for (int r = t - lane + lane / 8; r < min(keys, t - lane + 32); r += 4)
-#pragma unroll
-                        for (int a = 0; a < C::kAtoms; ++a)
-                            *reinterpret_cast<uint4*>(out + r * row_stride + a * C::kAtomElems + lane % 8 * 8) =
-                                *reinterpret_cast<const uint4*>(stage + a * C::kAtomBytes + r * 128 + (((lane ^ r) & 7) << 4));
-                }
+                if (ok && !*abort_flag)
+                    store_tail<C::kAtoms>((w == 0 ? p.dv : p.dk) + static_cast<long long>(info[3] + info[0] * 128) * row_stride +
+                                              info[6] * (w == 0 ? p.dv_head : p.dk_head),
+                                          row_stride, keys, stage);
             }
         }
         // Every thread of the warpgroup arrives exactly once, whatever happened.
