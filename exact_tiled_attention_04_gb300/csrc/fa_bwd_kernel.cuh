@@ -293,9 +293,9 @@ __device__ __noinline__ void store_tail(uint16_t* out, long long row_stride, int
 
 // kPacked: the key block is one of packed sequences (PackedBwdParams), found from
 // the offsets; its products are the batch's, and so are its times but for d = 128
-// without the mask (1 x 8192, H = 32/8: 2650 us against 2550).  Eight documents of
-// 475 to 4096 rows (16384, H = 32/8, d = 128, causal) 957 us of 1100 with the kernels around it,
-// 850 TFLOP/s in all; 8192 and 8000 rows of 16 heads, d = 64, 1755 us.
+// without the mask (1 x 8192, H = 32/8: 2700 us against 2550).  Eight documents of
+// 475 to 4096 rows (16384, H = 32/8, d = 128, causal) 980 us of 1122 with the kernels around it,
+// 832 TFLOP/s in all; 8192 and 8000 rows of 16 heads, d = 64, 1773 us.
 template <int D, bool F16, bool kCausal, bool kPacked = false, class Params = BwdParams>
 __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>::kThreads), 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
