@@ -36,6 +36,7 @@
 // infinity is not, so the softmax threads zero them in shared memory.
 #pragma once
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -547,7 +548,9 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
                     for (int n = 0; n < NV; ++n) {
                         const float tmax = fmaxf(fmaxf(red[n], red[NV + n]), fmaxf(red[2 * NV + n], red[3 * NV + n]));
                         float mn = fmaxf(m[n], tmax);
-                        if (mn == -INFINITY) mn = 0.0f;  // no visible key yet: any finite reference
+                        // no weight yet (no visible key, or scores of -inf alone): the least finite
+                        // reference, below any score that follows (0 would hide scores far below 0)
+                        if (mn == -INFINITY) mn = -FLT_MAX;
                         alpha[n] = ex2(m[n] - mn);      // 0 while m was -inf
                         l[n] *= alpha[n];
                         lq[n] *= alpha[n];

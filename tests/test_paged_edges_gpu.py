@@ -1,0 +1,64 @@
+"""Attention over the paged cache on the GPU: scores of -inf."""
+import math
+
+import pytest
+
+import exact_tiled_attention_04_gb300 as fa
+
+from .gpu_util import ensure_library
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from .test_packed_gpu import int32, rng, within  # noqa: E402
+from .test_paged_gpu import cache_of, reference  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return ensure_library()
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    assert fa.fa_device_status(None) == fa.FA_OK
+
+
+@pytest.mark.parametrize("G,N_q", [(1, 1), (8, 1), (4, 4), (32, 1)])
+@pytest.mark.parametrize("d,dtype", [(64, "f16"), (128, "bf16")])
+def test_first_keys_without_weight(G, N_q, d, dtype):
+    """The first 128 keys' scores are -inf and the others' about -100: the result is attention over the others."""
+    g = rng(61)
+    lengths = [300, 1000, 30000]
+    c, _ = cache_of(g, lengths, 2, d, 64, dtype, poison=False)
+    q = torch.randn(3, 2 * G, N_q, d, generator=g, device="cuda").to(c.dtype)
+    q[..., 0] = 8.0
+    c.k_pages[..., 0] = -12.5 * math.sqrt(d)
+    for b in range(3):
+        c.k_pages[c.block_table[b, :2].long(), ..., 0] = -math.inf
+    out, lse = fa.paged_attention(q, c)
+    rest = fa.PagedKVCache(c.k_pages, c.v_pages, c.block_table[:, 2:].contiguous(), c.lengths - 128)
+    want_o, want_l, tol_o, tol_l = reference(q, rest, [n - 128 for n in lengths], 1 / math.sqrt(d), False)
+    within(lse, want_l, tol_l, "lse")
+    within(out, want_o, tol_o, "out")
+
+
+def test_runs_without_weight():
+    """One long sequence whose keys' scores are -inf but for the last ten's: most of its runs leave nothing."""
+    g = rng(62)
+    c, _ = cache_of(g, [40000], 1, 64, 64, "f16", poison=False)
+    q = torch.randn(1, 4, 1, 64, generator=g, device="cuda").half()
+    q[..., 0] = 8.0
+    page = int(c.block_table[0, 39999 // 64])  # slots 39936 .. 39999
+    c.k_pages[..., 0] = -math.inf
+    c.k_pages[page, 0, 54:, 0] = -100.0
+    out, lse = fa.paged_attention(q, c)
+    k, v = (torch.zeros(1, 1, 16, 64, device="cuda").half() for _ in range(2))
+    k[0, 0, :10], v[0, 0, :10] = c.k_pages[page, 0, 54:], c.v_pages[page, 0, 54:]
+    rest = fa.PagedKVCache(k, v, int32([[0]]), int32([10]))
+    want_o, want_l, tol_o, tol_l = reference(q, rest, [10], 1 / 8, False)
+    within(lse, want_l, tol_l, "lse")
+    within(out, want_o, tol_o, "out")
