@@ -40,16 +40,35 @@ inline int make_view(const fa_rows_t* r, int64_t rows, int64_t heads, int64_t d,
     return FA_OK;
 }
 
-// Views with no element in common: their spans do not meet, or both have rows
-// equally far apart and their heads take different parts of a row's distance.
-inline bool disjoint(const View& a, const View& b) {
-    if (a.rows == 0 || b.rows == 0) return true;
-    if (!overlaps(a.data, a.span(), b.data, b.span())) return true;
-    if (!a.by_row || !b.by_row || a.row != b.row) return false;
-    const int64_t period = a.row * 2, wa = ((a.heads - 1) * a.head + a.d) * 2, wb = ((b.heads - 1) * b.head + b.d) * 2;
+// Elements at the addresses a + [0, wa) and b + [0, wb), each repeated every
+// `period` bytes, have none in common.
+inline bool apart(const View& a, int64_t wa, const View& b, int64_t wb, int64_t period) {
     int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.data) - reinterpret_cast<uintptr_t>(a.data)) % period;
     if (off < 0) off += period;
     return off >= wa && off + wb <= period;
+}
+
+// The distance in bytes that all of a view's strides are multiples of, where
+// the smaller one is that (a stride that is not used counts as one), else 0.
+inline int64_t step_of(const View& v) {
+    if (v.rows <= 1 && v.heads <= 1) return 0;
+    const int64_t row = v.rows <= 1 ? v.head : v.row, head = v.heads <= 1 ? v.row : v.head;
+    const int64_t small = row < head ? row : head;
+    return row % small == 0 && head % small == 0 ? small * 2 : 0;
+}
+
+// Views with no element in common: their spans do not meet; or both have rows
+// equally far apart and their heads take different parts of a row's distance
+// ([rows, heads of q, of k, of v]); or their rows of d elements take different
+// parts of a distance that all their strides are multiples of ([rows, heads, 3, d]).
+inline bool disjoint(const View& a, const View& b) {
+    if (a.rows == 0 || b.rows == 0) return true;
+    if (!overlaps(a.data, a.span(), b.data, b.span())) return true;
+    if (a.by_row && b.by_row && a.row == b.row &&
+        apart(a, ((a.heads - 1) * a.head + a.d) * 2, b, ((b.heads - 1) * b.head + b.d) * 2, a.row * 2))
+        return true;
+    const int64_t step = step_of(a);
+    return step > 0 && step == step_of(b) && apart(a, a.d * 2, b, b.d * 2, step);
 }
 
 // A view and n bytes at p with any byte between them.

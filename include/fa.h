@@ -558,7 +558,7 @@ int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
  * Rows of dq, dk and dv that belong to no sequence are left as they were; keys
  * that no query sees get zeros.  Non-finite rows of o, dout, q, k or v stay in
  * their sequence, as above.  dq, dk, dv and the workspace overlap no input and
- * not each other (slices of one tensor are fine).  dQ is summed over the key
+ * not each other (slices of one tensor are fine: of its heads, or parts beside each head).  dQ is summed over the key
  * blocks in fp32 in an order that may change from call to call, as in fa_bwd;
  * dk and dv repeat bit for bit.  Three kernels.
  */
