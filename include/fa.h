@@ -540,7 +540,11 @@ typedef struct {
  * belong to no sequence are left as they were, and whatever the rows of other
  * sequences or of none hold (infinities, NaN) does not enter a sequence's
  * results.  Within a sequence, an infinity or a NaN in a value row may reach
- * queries up to 127 rows before it that do not see it.  o overlaps no input.
+ * queries that do not see it, as masked keys are multiplied with weight 0: those
+ * whose last visible key is fewer than 128 rows before it, where H / H_kv is odd
+ * fewer than 256, and 127 more where n_k - n_q is no multiple of 128 (keys go by
+ * whole tiles of 128, up to the last that a block of 128 or 256 queries sees).
+ * o overlaps no input.
  * Results do not depend on the order in which blocks run.  One kernel; no workspace.
  */
 int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, const fa_rows_t* o, float* lse,
@@ -557,7 +561,8 @@ int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
  *               captured ones) that may run at once need one each.
  * Rows of dq, dk and dv that belong to no sequence are left as they were; keys
  * that no query sees get zeros.  Non-finite rows of o, dout, q, k or v stay in
- * their sequence, as above.  dq, dk, dv and the workspace overlap no input and
+ * their sequence (in it they may reach gradients of rows that the mask hides from
+ * them).  dq, dk, dv and the workspace overlap no input and
  * not each other (slices of one tensor are fine: of its heads, or parts beside each head).  dQ is summed over the key
  * blocks in fp32 in an order that may change from call to call, as in fa_bwd;
  * dk and dv repeat bit for bit.  Three kernels.

@@ -1,5 +1,5 @@
 """Attention over packed sequences on the GPU: slices of one tensor in every
-order of rows, heads and parts."""
+order of rows, heads and parts; how far a value row that is not finite reaches."""
 import math
 
 import pytest
@@ -64,3 +64,25 @@ def test_rows_rotated_in_place_beside_each_other(order):
     c.lengths.copy_(held)
     fa.paged_append(c, k, v, cu=int32([0, 40, 41]), table=table, k_out=k)
     assert torch.equal(k, k_rot) and torch.equal(v, v0)
+
+
+@pytest.mark.parametrize("H,H_kv", [(4, 2), (3, 3), (3, 1)])  # blocks of 128 rows of two heads, of 256 of one
+@pytest.mark.parametrize("n_q,n_k", [(700, 700), (700, 701), (600, 728), (700, 760), (256, 257)])
+@pytest.mark.parametrize("d,dtype", [(64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_how_far_a_value_row_reaches(H, H_kv, n_q, n_k, d, dtype, value):
+    """Queries that see the row are not finite; those that do not, from the distance on that the header gives, and the
+    other sequence's are as without it, bit for bit."""
+    q, k, v, cu_q, cu_k = batch(60, [40, n_q], H, H_kv, d, dtype, [40, n_k])
+    want, want_l = fa.packed_attention(q, k, v, int32(cu_q), int32(cu_k), causal=True)
+    last = torch.arange(n_q, device="cuda") + n_k - n_q  # the last key that each query sees
+    reach = 128 + 128 * (H // H_kv % 2) + 127 * ((n_k - n_q) % 128 != 0)
+    for key in [*range(0, n_k, 37), 255, n_k - 1] + [383] * (n_k > 383):
+        w = v.clone()
+        w[cu_k[1] + key] = value
+        out, lse = fa.packed_attention(q, k, w, int32(cu_q), int32(cu_k), causal=True)
+        assert torch.equal(lse, want_l) and torch.equal(out[:40], want[:40])
+        out = out[40:]
+        assert not torch.isfinite(out[last >= key]).any()
+        far = last <= key - reach
+        assert torch.equal(out[far], want[40:][far])
