@@ -24,7 +24,7 @@ namespace fa {
 struct SeqBlock {
     int q0, nq, k0, nk;  // the sequence's first query row, queries, first key row, keys
     int s;               // sequence
-    int r;               // its block, -1: `index` is past the last one
+    int r;               // its block, -1: none, -2: nor has any `index` behind it
     int base;            // its first row in arrays that give every sequence whole blocks of 128 rows (padded_row)
 };
 
@@ -76,11 +76,12 @@ __device__ __forceinline__ SeqBlock find_in_order(const PackedSeqs& p, int rows,
     const int T = kKeys ? p.Tk : p.Tq;
     const int32_t* cu = kKeys ? p.cu_k : p.cu_q;
     auto place_of = [&](int s) { return min(max(cu[s], 0), T) / rows + s; };
-    const int places = T / rows + p.B;
+    const int places = min(max(cu[p.B], 0), T) / rows + p.B;
     SeqBlock out;
-    out.r = -1;
+    out.r = -2;
     unit = 0;
     if (static_cast<unsigned long long>(places) * static_cast<unsigned>(units) <= index) return out;
+    out.r = -1;
     int place;
     lpt_item(index, units, places, unit, place);
     int lo = 0, hi = p.B;
@@ -132,7 +133,7 @@ __device__ __forceinline__ SeqBlock find_block(const PackedSeqs& p, int rows, in
         return __reduce_add_sync(0xffffffffu, n);
     };
     SeqBlock out;
-    out.r = -1;
+    out.r = -2;
     unit = 0;
     const int total = above(0);
     if (total == 0 || static_cast<unsigned long long>(total) * static_cast<unsigned>(units) <= index) return out;

@@ -86,3 +86,38 @@ def test_how_far_a_value_row_reaches(H, H_kv, n_q, n_k, d, dtype, value):
         assert not torch.isfinite(out[last >= key]).any()
         far = last <= key - reach
         assert torch.equal(out[far], want[40:][far])
+
+
+@pytest.mark.parametrize("H,H_kv,d", [(4, 2, 64), (3, 1, 128)])
+@pytest.mark.parametrize("lens", [[130, 0, 300, 1], [14] * 70, [0, 0], [0] * 80], ids=str)
+@pytest.mark.parametrize("causal", [False, True])
+def test_few_rows_in_use(lens, causal, H, H_kv, d):
+    """Tensors with room for far more rows than the sequences have: results bit for bit those of tensors without it, and
+    the other rows untouched; forward and backward, as a captured call whose offsets shrink has them."""
+    g = rng(65)
+    room, n = 20000, sum(lens)
+    q, k, v, dout = (rows(g, room, h, d) for h in (H, H_kv, H_kv, H))
+    cu = int32([0] + [room * (i + 1) // len(lens) for i in range(len(lens))])
+    out, grads = torch.zeros_like(q), [torch.zeros_like(x) for x in (q, k, v)]
+    lse = torch.zeros(H, room, device="cuda")
+
+    def call():
+        fa.packed_attention(q, k, v, cu, causal=causal, out=out, lse=lse)
+        fa.packed_attention_backward(q, k, v, out, lse, dout, cu, causal=causal, dq=grads[0], dk=grads[1], dv=grads[2])
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    cu.copy_(int32(R.offsets(lens)))
+    for x in (out, lse, *grads):
+        x.fill_(7.0)
+    graph.replay()
+    for x in (out, lse.T, *grads):
+        assert (x[n:] == 7).all()
+    small = [x[:n].contiguous() for x in (q, k, v, dout)]
+    want, want_l = fa.packed_attention(*small[:3], int32(R.offsets(lens)), causal=causal)
+    assert torch.equal(out[:n], want) and torch.equal(lse[:, :n], want_l)
+    dq, dk, dv = fa.packed_attention_backward(*small[:3], want, want_l, small[3], int32(R.offsets(lens)), causal=causal)
+    assert torch.equal(grads[1][:n], dk) and torch.equal(grads[2][:n], dv)
+    assert torch.allclose(grads[0][:n].float(), dq.float(), rtol=2.0 ** -7, atol=1e-5)
