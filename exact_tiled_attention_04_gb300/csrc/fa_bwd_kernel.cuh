@@ -194,10 +194,10 @@ struct BwdCfg {
 // false when the CTA is aborting (if `honor_abort`) or when this wait gave up
 // after kBwdWaitLimitNs, in which case it raises the CTA's abort flag, sets
 // the sticky device error bits (waiting role in bits 8-15) and marks this
-// launch's generation as aborted.
+// launch's generation as aborted.  `limits`: how many times kBwdWaitLimitNs.
 __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                          const BwdParams& bp, unsigned int where,
-                                         bool honor_abort = true) {
+                                         bool honor_abort = true, unsigned int limits = 1) {
     if (mbar_test(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     uint32_t spins = 0;
@@ -205,7 +205,7 @@ __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile
         if (mbar_test(bar, parity)) return true;
         if ((++spins & 31u) == 0u) {
             if (honor_abort && *abort_flag) return false;
-            if (global_timer_ns() - t0 > kBwdWaitLimitNs) {
+            if (global_timer_ns() - t0 > kBwdWaitLimitNs * limits) {
                 *abort_flag = 1u;
                 atomicOr(&bp.status->word, kDevErrTimeout | (where << 8));
                 atomicExch(&bp.status->abort_gen, bp.gen);
@@ -565,8 +565,8 @@ __global__ void __launch_bounds__((BwdCfg<D, F16, bwd_read_layout<D, kCausal>()>
       } else if (kPacked && warp == kBwdTailWarp) {
         // ------------------------------------------- rows behind the sequence
         if constexpr (kPacked) {
-            auto landed = [&](uint32_t raw, uint32_t phase) -> bool {  // (one lane asks)
-                const bool got = lane != 0 || bwd_wait(raw, phase, abort_flag, p, 33);
+            auto landed = [&](uint32_t raw, uint32_t phase) -> bool {  // (one lane asks, for as long as a sequence takes)
+                const bool got = lane != 0 || bwd_wait(raw, phase, abort_flag, p, 33, true, kSweepLimits);
                 return __all_sync(0xffffffffu, got);
             };
             const int keys = n_kv - kb * 128, last_rows = block_info[2] - (n_q_tiles - 1) * 128;

@@ -236,10 +236,12 @@ __device__ __forceinline__ bool wait_flag(volatile uint32_t* flag, uint32_t targ
 // which case it raises the CTA's abort flag, sets the sticky device error
 // bits (with the waiting role in bits 8-15) and marks this launch's
 // generation as aborted, so CTAs of the same launch that start later skip
-// their work.  Later launches are not affected.
+// their work.  Later launches are not affected.  `limits`: how many times
+// kWaitLimitNs (kSweepLimits).
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity,
                                            volatile uint32_t* abort_flag, const FwdParams& fp,
-                                           unsigned int where, bool honor_abort = true) {
+                                           unsigned int where, bool honor_abort = true,
+                                           unsigned int limits = 1) {
     DevStatus* const status = fp.status;
     const unsigned int gen = fp.gen;
     if (mbar_test(bar, parity)) return true;
@@ -249,7 +251,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity,
         if (mbar_test(bar, parity)) return true;
         if ((++spins & 31u) == 0u) {
             if (honor_abort && *abort_flag) return false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
+            if (global_timer_ns() - t0 > kWaitLimitNs * limits) {
                 *abort_flag = 1u;
                 atomicOr(&status->word, kDevErrTimeout | (where << 8));
                 atomicExch(&status->abort_gen, gen);

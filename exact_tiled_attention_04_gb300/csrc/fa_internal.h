@@ -68,6 +68,12 @@ constexpr unsigned int kDevErrTimeout = 1u;
 constexpr unsigned int kDevErrCapacity = 2u;  // rows appended to a full cache
 constexpr unsigned int kDevErrRange = 4u;     // a page number or a position outside its range
 
+// Limit, in those of the other waits (a second), of a wait that lasts as long as a
+// sweep over all tiles of a sequence: 2^24 tiles of 128 rows at 2.6 us are 44 s, where
+// a second ended such waits at some 400000 tiles.  (It ends with the others' too,
+// by the abort flag.)
+constexpr unsigned int kSweepLimits = 64;
+
 // A one-CTA kernel that waits, with the forward kernel's bounded wait, on a
 // barrier phase nothing completes; it must give up and report a timeout.
 cudaError_t launch_selftest_wait(const FwdParams& p, cudaStream_t stream);

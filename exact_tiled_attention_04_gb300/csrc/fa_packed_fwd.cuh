@@ -38,7 +38,8 @@
 // 1 x 8192 774 us (750, as there the last wave's key range is split over idle SMs,
 // which takes the lengths on the host).
 //
-// Every wait is bounded as in the forward kernel.
+// Every wait is bounded as in the forward kernel, those for a whole block (warp 11's
+// for its loads, the others' for the next one, behind places without one) by kSweepLimits.
 #pragma once
 
 #include <cmath>
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Block n of the CTA, for one of its readers; false when there is none (or the CTA gives up).
     auto block_info = [&](int n) { return reinterpret_cast<const int4*>(smem + C::kOffBlocks + (n & 1) * 32); };
     auto read_block = [&](int n, Block& b) -> bool {
-        if (!wait_phase(bar(C::kBarBlockFull + (n & 1)), (n >> 1) & 1, abort_flag, p, 80)) return false;
+        if (!wait_phase(bar(C::kBarBlockFull + (n & 1)), (n >> 1) & 1, abort_flag, p, 80, true, kSweepLimits)) return false;
         b = block_of(block_info(n));
         return b.nq >= 0;
     };
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Block b{};
                 b.nq = -1;
                 if (n > 0) {
-                    ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarLoaded), (n - 1) & 1, abort_flag, p, 87));
+                    ok = __all_sync(0xffffffffu, wait_phase(bar(C::kBarLoaded), (n - 1) & 1, abort_flag, p, 87, true, kSweepLimits));
                     if (!ok) break;
                 }
                 while (more) {

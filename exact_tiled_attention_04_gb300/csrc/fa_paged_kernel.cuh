@@ -503,7 +503,8 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
                 const int b = it & 1, s_ = it % C::kStages;
                 const int key = j * 128 + t;
                 uint32_t s[NV];
-                if (ok) ok = wait_phase(bar(C::kBarS + 2 * group + (mine & 1)), (mine >> 1) & 1, abort_flag, p, 66);
+                if (ok) ok = wait_phase(bar(C::kBarS + 2 * group + (mine & 1)), (mine >> 1) & 1, abort_flag, p, 66,
+                                        true, kSweepLimits);  // (behind the other group's unit)
                 ok = __all_sync(0xffffffffu, ok);  // the TMEM loads below are warp-wide
                 if (ok) {
                     tc_fence_after();

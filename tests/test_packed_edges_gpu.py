@@ -1,5 +1,6 @@
 """Attention over packed sequences on the GPU: slices of one tensor in every
-order of rows, heads and parts; how far a value row that is not finite reaches."""
+order of rows, heads and parts; how far a value row that is not finite reaches;
+tensors with room for more rows than are in use; the longest sequences."""
 import math
 
 import pytest
@@ -121,3 +122,43 @@ def test_few_rows_in_use(lens, causal, H, H_kv, d):
     dq, dk, dv = fa.packed_attention_backward(*small[:3], want, want_l, small[3], int32(R.offsets(lens)), causal=causal)
     assert torch.equal(grads[1][:n], dk) and torch.equal(grads[2][:n], dv)
     assert torch.allclose(grads[0][:n].float(), dq.float(), rtol=2.0 ** -7, atol=1e-5)
+
+
+def test_forward_sweep_of_more_than_a_second():
+    """One query over 2^27 + 1 keys of score 0, whose values take turns in sign: the last one over their number, exactly
+    (powers of two; of values of one sign the sum would stop at 2^26 of them, below its last bits)."""
+    n = 2 ** 27 + 1
+    k = torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    row = (2.0 ** (torch.arange(64, device="cuda") % 3) * (1 - 2 * (torch.arange(64, device="cuda") % 2))).bfloat16()
+    v = row.repeat(n, 1)[:, None]
+    v[1::2] *= -1
+    q = rows(rng(66), 3, 1, 64)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    out, lse = fa.packed_attention(q, k, v, int32([0, 1, 3]), int32([0, n, n]))
+    end.record()
+    assert fa.fa_device_status(None) == fa.FA_OK
+    assert torch.equal(out[0, 0], row * 2.0 ** -27) and abs(lse[0, 0].item() - math.log(n)) <= 2.0 ** -21 * math.log(n)
+    assert not out[1:].any() and (lse[0, 1:] == -math.inf).all()
+    assert start.elapsed_time(end) > 1000  # a wait for the block lasted longer than the limit of the others
+
+
+def test_backward_sweep_of_more_than_a_second():
+    """Gradients of 80 million queries, all of them zeros with zero gradients but the last, over 100 keys."""
+    n, keys = 80_000_001, 100
+    x = torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    x[-1] = rows(rng(67), 1, 64)
+    k, v = rows(rng(68), keys, 1, 64), rows(rng(69), keys, 1, 64)
+    lse = torch.full((1, n), math.log(keys), device="cuda")
+    cu_q, cu_k = int32([0, n]), int32([0, keys])
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    dq, dk, dv = fa.packed_attention_backward(x, k, v, x, lse, x, cu_q, cu_k)
+    end.record()
+    assert fa.fa_device_status(None) == fa.FA_OK
+    last = x[-1:].clone()
+    want = R.backward(last, k, v, last, lse[:, -1:], last, [0, 1], [0, keys], 1 / 8, False)
+    for name, got in (("dq", dq[-1:]), ("dk", dk), ("dv", dv)):
+        within(got, *want[name], name)
+    assert not dq[:-1].any()
+    assert start.elapsed_time(end) > 1000
