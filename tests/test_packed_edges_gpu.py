@@ -162,3 +162,26 @@ def test_backward_sweep_of_more_than_a_second():
         within(got, *want[name], name)
     assert not dq[:-1].any()
     assert start.elapsed_time(end) > 1000
+
+
+@pytest.mark.parametrize("n", [2 ** 18, 2 ** 20, 2 ** 22])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_long_sums(n, dtype):
+    """Sums of n terms of one sign: forward over n keys of like weight, dV of n queries of like weight.  One accumulation in
+    fp32 that loses up to a step for every 16 terms (n 2^-27), beside the roundings of the weights and of the result."""
+    g = rng(70)
+    x = (torch.rand(n, 1, 64, generator=g, device="cuda") + 0.5).to(dtype)
+    zero, q = torch.zeros_like(x), rows(g, 2, 1, 64).to(dtype)
+    out, lse = fa.packed_attention(q, zero, x, int32([0, 2]), int32([0, n]))
+    half = R.HALF[dtype]
+    mean = x.double().mean(0)
+    assert ((out.double() - mean).abs() <= (2 * half + R.sums(n)) * mean).all()
+    assert ((lse.double() - math.log(n)).abs() <= R.sums(n) + 2.0 ** -22 * math.log(n)).all()
+    # every query has the weight 1/4 for each of four keys
+    k = torch.zeros(4, 1, 64, dtype=dtype, device="cuda")
+    lse = torch.full((1, n), math.log(4.0), device="cuda")
+    _, dk, dv = fa.packed_attention_backward(zero, k, k, zero, lse, x, int32([0, n]), int32([0, 4]))
+    want = x.double().sum(0) / 4
+    if dtype == torch.bfloat16:  # (fp16 ends at 65504)
+        assert ((dv.double() - want).abs() <= (2 * half + 2.0 ** -20 + R.sums(n)) * want).all()
+    assert not dk.any()
