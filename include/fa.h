@@ -564,7 +564,11 @@ int fa_packed_fwd(const fa_rows_t* q, const fa_rows_t* k, const fa_rows_t* v, co
  * query heads that share a key/value head.
  *   workspace : fa_packed_bwd_workspace_size(...) bytes, 16-byte aligned;
  *               nothing in it needs to be zeroed.  Calls (and replays of
- *               captured ones) that may run at once need one each.
+ *               captured ones) that may run at once need one each.  Its size,
+ *               H (T_q / 128 + B) (512 d + 1024) + 128 bytes, grows with the
+ *               sequences beside the rows: an fp32 row of dQ for each query row,
+ *               and up to 127 more for each sequence (24000 rows of 16 heads, d = 128,
+ *               in 8 sequences 0.21 GB, in 1000 1.26, in 4000 4.46).
  * Rows of dq, dk and dv that belong to no sequence are left as they were; keys
  * that no query sees get zeros.  Non-finite rows of o, dout, q, k or v stay in
  * their sequence (in it they may reach gradients of rows that the mask hides from

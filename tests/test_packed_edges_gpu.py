@@ -185,3 +185,32 @@ def test_long_sums(n, dtype):
     if dtype == torch.bfloat16:  # (fp16 ends at 65504)
         assert ((dv.double() - want).abs() <= (2 * half + 2.0 ** -20 + R.sums(n)) * want).all()
     assert not dk.any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [5, 70])
+@pytest.mark.parametrize("causal", [False, True])
+def test_gradients_do_not_depend_on_the_workspace(causal, B, d):
+    """Whatever the workspace held, with empty sequences and rows of none; nothing behind it is written."""
+    g = rng(62)
+    lens = [(0, 130, 1, 257, 40)[i % 5] if B == 5 else i * i % 60 for i in range(B)]
+    T = 19 + sum(lens) + 300
+    q, k, v, dout = (rows(g, T, h, d) for h in (4, 2, 2, 4))
+    cu = R.offsets(lens, 19)
+    out, lse = torch.zeros_like(q), torch.zeros(4, T, device="cuda")
+    fa.packed_attention(q, k, v, int32(cu), causal=causal, out=out, lse=lse)
+    want = R.backward(q, k, v, out, lse, dout, cu, cu, 1 / math.sqrt(d), causal)
+    need = fa.fa_packed_bwd_workspace_size(B, T, 4, d)
+    first = None
+    for fill in (0, 255):  # zeros, NaN
+        ws = torch.full((need + 256,), fill, dtype=torch.uint8, device="cuda")
+        ws[need:] = 77
+        grads = [torch.full_like(x, 7) for x in (q, k, v)]
+        got = fa.packed_attention_backward(q, k, v, out, lse, dout, int32(cu), causal=causal, workspace=ws[:need],
+                                           dq=grads[0], dk=grads[1], dv=grads[2])
+        for name, x in zip(("dq", "dk", "dv"), got):
+            within(x[19:cu[-1]], *(t[19:cu[-1]] for t in want[name]), name)
+            assert (x[:19] == 7).all() and (x[cu[-1]:] == 7).all()
+        assert (ws[need:] == 77).all()
+        first = first or got
+        assert torch.equal(got[1], first[1]) and torch.equal(got[2], first[2])

@@ -84,3 +84,9 @@ def test_views_that_are_taken_share_nothing():
             taken += 1
             assert not elements(dq, T, H) & elements(dk, T, H_kv), (T, H, H_kv, row, head, row2, head2, dq.data - dk.data)
     assert taken > 500
+
+
+@pytest.mark.parametrize("B,T_q,H,d", [(1, 0, 1, 64), (3, 100, 4, 64), (8, 24000, 16, 128), (4000, 24000, 16, 128), (70, 127, 3, 64)])
+def test_size_of_the_gradients_workspace(B, T_q, H, d):
+    """What the header says it takes."""
+    assert fab.fa_packed_bwd_workspace_size(B, T_q, H, d) == H * (T_q // 128 + B) * (512 * d + 1024) + 128
