@@ -653,8 +653,9 @@ typedef struct {
  * pool are dropped, and positions outside the table are rotated as its first
  * or last row, and it reports FA_ERR_RANGE.  Rows of no sequence, and pages
  * but for the new rows, are left as they were.  Where two slots written are the
- * same row of the pool either may stay.  One kernel, and a second one when lengths
- * advance in place and a sequence has more than a few rows.
+ * same row of the pool either may stay.  One kernel where lengths_out is not the
+ * cache's, or where cu is NULL and each sequence has one row (in large batches, or of
+ * few heads, a few); else, with cu or without rows too, a second one advances the lengths.
  */
 int fa_paged_append(const fa_paged_cache_t* cache, const fa_rows_t* k, const fa_rows_t* v, const int32_t* cu,
                     int64_t T, const fa_rows_t* q, const fa_rows_t* q_out, int64_t H, const fa_rows_t* k_out,

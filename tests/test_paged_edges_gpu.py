@@ -1,4 +1,4 @@
-"""Attention over the paged cache on the GPU: scores of -inf."""
+"""The paged cache on the GPU: scores of -inf, and how many kernels each call launches."""
 import math
 
 import pytest
@@ -10,7 +10,7 @@ from .gpu_util import ensure_library
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
-from .test_packed_gpu import int32, rng, within  # noqa: E402
+from .test_packed_gpu import int32, rng, rows, within  # noqa: E402
 from .test_paged_gpu import cache_of, reference  # noqa: E402
 
 
@@ -62,3 +62,39 @@ def test_runs_without_weight():
     want_o, want_l, tol_o, tol_l = reference(q, rest, [10], 1 / 8, False)
     within(lse, want_l, tol_l, "lse")
     within(out, want_o, tol_o, "out")
+
+
+def kernels(call):
+    """Kernels that a call launches: nodes of the graph it is captured into."""
+    import ctypes
+    call()  # (what is set up once)
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    n = ctypes.c_size_t()
+    cuda = ctypes.CDLL("libcuda.so.1")
+    assert cuda.cuGraphGetNodes(ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+    return n.value
+
+
+def test_kernels_of_each_call():
+    g = rng(71)
+    c, pages = cache_of(g, [15, 300, 7], 2, 64, 16, room=100, prefix=40, poison=False)
+    table, apart = fa.rotary_table(1000, 64), torch.empty_like(c.lengths)
+
+    def append(T, **kw):
+        x = rows(g, T, 2, 64)
+        q = rows(g, T, 8, 64)
+        return kernels(lambda: fa.paged_append(c, x, x, q=q, table=table, **kw))
+
+    assert append(3) == 1 and append(3, lengths_out=apart) == 1  # a row each
+    assert append(3, cu=int32([0, 1, 2, 3])) == 2 and append(3, cu=int32([0, 1, 2, 3]), lengths_out=apart) == 1
+    assert append(60) == 2 and append(60, lengths_out=apart) == 1
+    assert append(0) == 2 and append(0, lengths_out=apart) == 1
+    q = rows(g, 3, 4, 64).view(3, 4, 1, 64)
+    assert kernels(lambda: fa.paged_attention(q, c)) == 2
+    assert kernels(lambda: fa.paged_attention(q, c, prefix_pages=pages, prefix_length=40)) == 3
+    x, cu = rows(g, 50, 2, 64), int32([0, 20, 50])
+    out, lse = fa.packed_attention(x, x, x, cu)
+    assert kernels(lambda: fa.packed_attention(x, x, x, cu)) == 1
+    assert kernels(lambda: fa.packed_attention_backward(x, x, x, out, lse, x, cu)) == 3
