@@ -40,7 +40,7 @@ struct PagedAppendParams {
     int parts;   // warps that share a token's rows
 };
 // interleaved: pairs of neighbouring channels.
-cudaError_t launch_paged_append(const PagedAppendParams& p, bool f16, bool interleaved, cudaStream_t stream);
+cudaError_t launch_paged_append(const PagedAppendParams& p, int sms, bool f16, bool interleaved, cudaStream_t stream);
 
 // Attention over the cache.  Rows: the R = N_q * group query rows of a
 // key/value head, row r = g * N_q + i (query head g of the group, query i), in

@@ -318,8 +318,8 @@ int fa_paged_append(const fa_paged_cache_t* cache, const fa_rows_t* k, const fa_
     p.T = T;
     p.n = cu == nullptr ? static_cast<int>(T / cache->B) : 0;
     p.H = static_cast<int>(H);
-    const cudaError_t e = fa::launch_paged_append(p, (dtype & 0xFF) == FA_DTYPE_F16, (dtype & FA_FLAG_INTERLEAVED) != 0,
-                                                  static_cast<cudaStream_t>(stream));
+    const cudaError_t e = fa::launch_paged_append(p, sm_count(), (dtype & 0xFF) == FA_DTYPE_F16,
+                                                  (dtype & FA_FLAG_INTERLEAVED) != 0, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : cuda_failed("paged append launch", e);
 }
 

@@ -182,13 +182,13 @@ __global__ void __launch_bounds__(256) paged_advance_kernel(const PagedAppendPar
 
 }  // namespace
 
-cudaError_t launch_paged_append(const PagedAppendParams& params, bool f16, bool interleaved, cudaStream_t stream) {
+cudaError_t launch_paged_append(const PagedAppendParams& params, int sms, bool f16, bool interleaved, cudaStream_t stream) {
     PagedAppendParams p = params;
     const int per_warp = 32 / (p.c.d / 16), rows = (p.q.data != nullptr ? p.H : 0) + 2 * p.c.H_kv;
     const int most = (rows + per_warp - 1) / per_warp;  // warps a token can use
-    // As many warps as fill the device about once share the tokens: 152 SMs of 64 warps (one token of each of 32
+    // As many warps as fill the device about once share the tokens, 64 an SM (one token of each of 32
     // sequences, H = 32/8, d = 128: 3.1 us, by one warp a token 5.5).
-    long long parts = (152 * 64) / (p.T > 0 ? p.T : 1);
+    long long parts = sms * 64ll / (p.T > 0 ? p.T : 1);
     parts = parts < 1 ? 1 : parts > most ? most : parts;
     if (parts > kMostWarps) parts = kMostWarps;
     p.parts = static_cast<int>(parts);
