@@ -25,7 +25,10 @@
 //
 // Measured: 32 sequences of up to 16384 slots (H = 32 over 8, d = 128, bf16, pages
 // of 64) 164 to 165 us, 6.7 TB/s of keys and values; 64 of 128, 512, 1024 and 4096
-// slots 11.5, 25.8, 46.8 and 159 us, about 7 us and their bytes; four of up to 1000
+// slots 11.5, 25.8, 46.8 and 159 us, about 7 us and their bytes (32 of 16384 in pages of
+// 128, 64, 32 and 16: 307, 310, 316 and 336 us; d = 64 163, 165, 173 and 207); of more than 32
+// rows a head each block of 32 is a unit that reads the head's keys and values again (16 of 4096
+// slots, 32, 64, 96 and 128 rows 52, 92, 130 and 168 us; d = 64 38, 67, 95 and 121); four of up to 1000
 // (8 over 2, d = 64) 7.2 to 7.5 us, the depth of the two kernels: set-up, the run's place, the
 // first tile, the unit's end, the second kernel.
 //
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__((Cfg<D, F16, NV>::kThreads), 1)
         // nothing (the device error word already reports the failure)
     } else if (warp == C::kLoadWarp) {
         // ---------------------------------------------------------- producer
-        const uint64_t once = policy_evict_first();  // every byte here is read once
+        const uint64_t once = policy_evict_first();  // a unit reads every byte once (see Measured for row blocks)
         const int pages = 128 / p.c.page;            // of a tile
         // this lane's box of K's or V's tile: 64 channels of page `mine` (8 pages at most, 2 boxes each)
         const int mine = lane / C::kAtoms, atom = lane % C::kAtoms;

@@ -142,10 +142,11 @@ def paged_append(cache: PagedKVCache, k, v, cu=None, q=None, table=None, positio
 def paged_attention(q, cache: PagedKVCache, scale: float | None = None, causal: bool = False, prefix_pages=None,
                     prefix_length: int = 0, out=None, lse=None, with_lse: bool = True, workspace=None, stream=None):
     """O = softmax(scale * Q K^T) V for q [B, H, N_q, d] over the sequences' slots;
-    H a multiple of H_kv, N_q * H / H_kv <= 128.
+    H a multiple of H_kv, N_q * H / H_kv <= 128.  (`paged_append` returns queries as
+    [rows, heads, d]: with N_q above 1 they are transposed in between.)
 
     prefix_pages (int32, of the same pool) and prefix_length: slots that come
-    before every sequence's own, read once for all of them.  causal: query i
+    before every sequence's own, read once for up to 256 rows a key/value head.  causal: query i
     sees the prefix and the own slots j < length - (N_q - 1 - i).  Returns
     (out, lse) as `attention` does.  `workspace` (uint8, cache.workspace_size(...)
     bytes) is allocated when not given."""

@@ -667,15 +667,17 @@ int fa_paged_append(const fa_paged_cache_t* cache, const fa_rows_t* k, const fa_
  *
  *     O = softmax(scale q K^T) V,  lse = log sum exp(scale q K^T)
  *
- * over key/value head h / (H / H_kv) of the prefix's prefix_length slots, read once
- * for all sequences, followed by the sequence's own lengths[b].
+ * over key/value head h / (H / H_kv) of the prefix's prefix_length slots, which all
+ * sequences share (read once for two tiles of up to 128 rows of whole sequences, so
+ * for a batch of up to 256 rows a key/value head), followed by the sequence's own lengths[b].
  *   o            : [B, H, N_q, d] of `dtype`;  lse: fp32 [B, H, N_q] or NULL.
  *   prefix_pages : int32 [ceil(prefix_length / page_size)] on the device, pages of
  *                  the same pool; NULL exactly where prefix_length is 0.
  *   dtype        : FA_DTYPE_BF16 or FA_DTYPE_F16, optionally FA_FLAG_CAUSAL:
  *                  row i sees the prefix and the own slots
  *                  j < lengths[b] - (N_q - 1 - i).
- *   N_q * H / H_kv <= 128 (decode steps and drafts): else FA_ERR_UNSUPPORTED.
+ *   N_q * H / H_kv <= 128 (decode steps and drafts): else FA_ERR_UNSUPPORTED.  Above 32
+ *                  the own slots' keys and values are read once for every 32.
  *   workspace    : fa_paged_fwd_workspace_size(...) bytes, 16-byte aligned;
  *                  nothing in it needs to be zeroed.  Calls (and replays of
  *                  captured ones) that may run at once need one each.
