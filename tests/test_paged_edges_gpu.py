@@ -98,3 +98,18 @@ def test_kernels_of_each_call():
     out, lse = fa.packed_attention(x, x, x, cu)
     assert kernels(lambda: fa.packed_attention(x, x, x, cu)) == 1
     assert kernels(lambda: fa.packed_attention_backward(x, x, x, out, lse, x, cu)) == 3
+
+
+def test_drafts_stored_then_attended():
+    """Three drafted tokens of each sequence rotated and stored, the queries transposed, causal attention behind a prefix."""
+    g = rng(72)
+    B, N, H, H_kv, d, prefix = 3, 3, 8, 2, 64, 40
+    held = [15, 300, 0]
+    c, pages = cache_of(g, held, H_kv, d, 16, room=N, prefix=prefix, poison=False)
+    q, k, v = (rows(g, B * N, h, d) for h in (H, H_kv, H_kv))
+    got = fa.paged_append(c, k, v, q=q, table=fa.rotary_table(400, d), first_position=prefix)
+    q4 = got.view(B, N, H, d).transpose(1, 2).contiguous()
+    out, lse = fa.paged_attention(q4, c, causal=True, prefix_pages=pages, prefix_length=prefix)
+    want_o, want_l, tol_o, tol_l = reference(q4, c, [n + N for n in held], 1 / 8, True, pages, prefix)
+    within(lse, want_l, tol_l, "lse")
+    within(out, want_o, tol_o, "out")
