@@ -32,7 +32,8 @@
 // What bounds it: the tensor cores and, beside them, the exponentials, as in the
 // forward kernel; below some 1000 rows a sequence the ends of the blocks.
 // Measured (bf16, causal, H = 32 over 8, d = 128): sequences of 16384, 8191, 4096
-// and 1000 rows 2.00 ms, 1450 TFLOP/s; 16 of 17 to 2048 rows 143 us, 870 TFLOP/s;
+// and 1000 rows 2.00 to 2.04 ms, 1450 to 1420 TFLOP/s (2.09 to 2.11 ms, 1380 to 1370, in
+// longer runs, on several boxes); 16 of 17 to 2048 rows 143 us, 870 TFLOP/s;
 // 64 of 128 rows 43 us at d = 64 (67 with a CTA per block).  Uniform lengths, against
 // the batch's kernel: 1 x 8192 400 us (444), 16 x 512 62 us (98); without the mask
 // 1 x 8192 774 us (750, as there the last wave's key range is split over idle SMs,
