@@ -64,10 +64,9 @@ __device__ __forceinline__ void seq_levels(const PackedSeqs& p, int rows, int nq
 // first_row / rows + s on (as in padded_row, no sum is needed), and the last
 // sequence that begins at or before a place is found by a 32-way search; some
 // places have no block.  Measured (24000 rows, H = 16/4, d = 128, causal, us by order
-// and by work), forward: 100 sequences of 240 rows 109, 124; 300 of 80 115, 238;
-// 1000 of 24 316, 1632; 4000 of 6 1170, 20760; 48 of 20 to 4000 rows 170, 171.
-// Backward: 1000 of 24 733, 1023; 64 of 20 to 4000 519, 469 (both ways 3 to 7 % more since
-// the kernel zeroes the rows behind a sequence itself).
+// and by work), forward: 100 sequences of 240 rows 99, 110; 300 of 80 106, 220;
+// 1000 of 24 304, 1621; 4000 of 6 1165, 20540; 48 of 20 to 4000 rows (37325 in all) 296, 298.
+// Backward: 1000 of 24 770, 1060; 48 of 20 to 4000 1127, 1069.
 constexpr int kMostByWork = 64;
 
 template <bool kKeys>
